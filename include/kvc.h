@@ -26,7 +26,9 @@
  *     multiple of 16 bytes.  Query head h reads KV head h / (n_heads_q / n_heads_kv)
  *     (grouped-query attention, [KVCL] "01 · Conceito"; [KVC] "O gargalo de memória...").
  *   - Element types: KVC_F32 (fp32 storage and arithmetic) or KVC_BF16 (bf16 storage, fp32
- *     arithmetic).  Queries and new keys/values use the cache's type; outputs are fp32.
+ *     arithmetic).  Queries and new keys/values use the cache's type; outputs are fp32, except
+ *     where an entry point says that they have the cache's type (the draft-tree and latent
+ *     attention, whose outputs feed the next projection directly).
  */
 #ifndef KVC_H_
 #define KVC_H_
@@ -552,6 +554,138 @@ kvc_status kvc_h2o_prefill_select_gqa(const void *q, int32_t n_heads_q, const kv
                                       int32_t seq_len, int32_t L_local, int32_t K_hh,
                                       float scale, int32_t *idx_out, float *score_out,
                                       float *s_full, void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* Trees of drafted tokens.  A drafting model proposes n_draft tokens per sequence at once; token
+ * i sees the whole cache and, of the drafted tokens, those whose bit is set in its mask word
+ * (itself and its ancestors).  The drafted keys and values stay OUT of the cache until they
+ * are accepted: a ring, an evicted slot or a page never loses a token to a draft that is then
+ * rejected.  No counterpart on the pages (they decode one token at a time); the attention is
+ * that of kvc_decode_attn for every drafted token.
+ * k, v: device [batch][n_draft][n_heads_kv][d_head], cache dtype, contiguous, 16-byte aligned
+ * (for a latent cache k is [batch][n_draft][d_latent + d_rope] and v is not read).  k == NULL:
+ * the query tokens see the cache only (their keys were appended already).
+ * mask: device uint64[batch][n_draft]; bit j of word i set: token i sees token j.  Bits at or
+ * above the sequence's token count are ignored.  NULL: a chain, token i sees tokens 0..i.
+ * count (nullable): device int32[batch], drafted tokens of each sequence, 0..n_draft (a value
+ * outside records KVC_DEV_BAD_LENGTH and is clamped).  Outputs of tokens at or beyond it are
+ * left as they were, and their keys and values are not used (nor need they be finite).  NULL:
+ * n_draft each. */
+typedef struct {
+    const void *k;
+    const void *v;
+    const uint64_t *mask;
+    const int32_t *count;
+    int32_t n_draft;        /* query tokens per sequence, 1..64                              */
+    int32_t reserved;
+} kvc_draft;
+
+/* Attention of a tree of drafted tokens over a cache: for every sequence b, drafted token i <
+ * count[b] and query head h,
+ *   out[b,i,h] = sum_j softmax_j(scale * q[b,i,h].k_j) v_j
+ * over the valid slots of KV head h / (n_heads_q / n_heads_kv) -- slots 0..len[b*H+h]-1, or
+ * 0..n_valid-1 when len is NULL -- and the drafted tokens that token i sees.  A length outside
+ * [0, cap] records KVC_DEV_BAD_LENGTH and is clamped.  What slots at or beyond the length hold
+ * is never used, whatever it is; a drafted token's non-finite value reaches only the rows that
+ * see it.  A row that sees nothing gets out = 0 and lse = -inf.
+ * q: [batch][n_draft][n_heads_q][d_head] cache dtype, contiguous; out: the same shape and type;
+ * lse (nullable): fp32 [batch][n_draft][n_heads_q].  Any group size up to 64.
+ * bf16 caches run on the tensor cores (fp32 accumulation and softmax statistics; the
+ * probabilities are rounded to bf16 for the product with the values), fp32 caches in fp32.
+ * Two launches (the second joins the partial results of rows whose slots were split over
+ * thread blocks).  Results do not depend on timing.  Workspace:
+ * kvc_decode_attn_tree_workspace_bytes(), 256-byte aligned; it need not be cleared, and calls
+ * that share one must not overlap on the GPU. */
+size_t kvc_decode_attn_tree_workspace_bytes(int32_t batch, int32_t n_heads_q,
+                                            int32_t n_heads_kv, int32_t d_head, int32_t n_draft,
+                                            int32_t dtype);
+kvc_status kvc_decode_attn_tree(const void *q, int32_t n_heads_q, const kvc_cache *cache,
+                                const int32_t *len, int32_t n_valid, const kvc_draft *draft,
+                                float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/* kvc_decode_attn_tree over a paged cache: the slots are the len[b] tokens of each sequence's
+ * page table (a table entry outside the pool records KVC_DEV_BAD_BLOCK and reads block 0).
+ * Block sizes that are multiples of 8 and divide the tensor-core tile (128 slots; 64 with
+ * d_head 256), or are multiples of it, run on the tensor cores with bf16 pools; others run on
+ * the CUDA cores. */
+kvc_status kvc_decode_attn_tree_paged(const void *q, int32_t n_heads_q,
+                                      const kvc_block_pool *pool, const kvc_page_table *pt,
+                                      const kvc_draft *draft, float scale, void *out, float *lse,
+                                      void *ws, size_t ws_bytes, void *stream);
+
+/* Keep an accepted path: append the drafted tokens path[b*n_draft + 0 .. n_accept[b]-1] of every
+ * sequence, in that order, at the tail of the cache (KVC_APPEND_TAIL's slots):
+ *   slot len[b*H+h] + i of (b, h) <- drafted token path[b*n_draft + i];  len += n_accept[b].
+ * path: device int32[batch][n_draft]; n_accept: device int32[batch].  Copies are bit exact.
+ * All or nothing: an n_accept outside [0, n_draft] (KVC_DEV_BAD_LENGTH) or a path entry outside
+ * [0, count[b]) (KVC_DEV_BAD_INDEX) appends nothing to that sequence; a row whose length is
+ * outside [0, cap] (KVC_DEV_BAD_LENGTH) or which has no room (KVC_DEV_TAIL_FULL) is left as it
+ * was.  draft->mask is not used. */
+kvc_status kvc_tree_accept(const kvc_cache *cache, int32_t *len, const kvc_draft *draft,
+                           const int32_t *path, const int32_t *n_accept, void *stream);
+
+/* kvc_tree_accept for a paged cache.  Blocks are popped for the tokens that open one, in sequence
+ * order from the top of the free stack (so the ids do not depend on timing), with score 0;
+ * n_blocks and len follow.  accepted: device int32[batch], the tokens appended (n_accept[b], or
+ * 0 where the sequence was refused: besides the cases above KVC_DEV_BAD_LENGTH for lengths that
+ * disagree with n_blocks or a table without room, KVC_DEV_POOL_EMPTY when the stack has too few
+ * ids left for it, KVC_DEV_BAD_BLOCK for an id outside the pool). */
+kvc_status kvc_tree_accept_paged(const kvc_block_pool *pool, const kvc_page_table *pt,
+                                 const kvc_free_pool *free_pool, const kvc_draft *draft,
+                                 const int32_t *path, const int32_t *n_accept, int32_t *accepted,
+                                 void *stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* Latent caches: one row per token for all heads, from which every head's key and value follow by
+ * two matrices (low-rank joint compression of keys and values; no counterpart on the pages).
+ * Row (b, s): c[b*stride_b + s*stride_slot + 0 .. d_latent-1] is the latent vector, the d_rope
+ * elements after it the position-rotated key part that the heads share.
+ *   expanded form: k[b,h,s] = [ W_k[h] c_lat | c_rope ],  v[b,h,s] = W_v[h] c_lat
+ *   absorbed form: q'[h] = [ W_k[h]^T q_nope[h] | q_rope[h] ],  logit = scale * q'[h].c,
+ *                  o'[h] = sum_j p_j c_lat_j,  the head's output W_v[h] o'[h]
+ * (the same attention: the matrices are applied to the query and to the output instead of to
+ * every cached row).
+ * d_latent is 128, 256 or 512; d_rope a multiple of 8 in 0..64; pointers 16-byte aligned and
+ * strides multiples of 16 bytes, stride_slot >= d_latent + d_rope. */
+typedef struct {
+    void *c;
+    int32_t dtype;          /* kvc_dtype */
+    int32_t batch;
+    int32_t cap;            /* slots per sequence */
+    int32_t d_latent;
+    int32_t d_rope;
+    int32_t reserved;
+    int64_t stride_b;       /* elements */
+    int64_t stride_slot;
+} kvc_latent_cache;
+
+/* Absorbed latent attention of one token or a tree of drafted tokens per sequence: kvc_decode_attn_tree
+ * with one KV head for all n_heads_q (at most 256) query heads, keys of d_latent + d_rope elements and
+ * the first d_latent of each row as its value.  len: device int32[batch], or NULL with n_valid.
+ * q: [batch][n_draft][n_heads_q][d_latent + d_rope]; out: [batch][n_draft][n_heads_q][d_latent]
+ * (cache dtype); lse (nullable): fp32 [batch][n_draft][n_heads_q].  Plain decoding passes the
+ * new token as a draft of one (or appends its row first and passes draft->k == NULL). */
+size_t kvc_decode_attn_latent_workspace_bytes(int32_t batch, int32_t n_heads_q, int32_t d_latent,
+                                              int32_t d_rope, int32_t n_draft, int32_t dtype);
+kvc_status kvc_decode_attn_latent(const void *q, int32_t n_heads_q, const kvc_latent_cache *cache,
+                                  const int32_t *len, int32_t n_valid, const kvc_draft *draft,
+                                  float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                                  void *stream);
+
+/* kvc_tree_accept for a latent cache (len: device int32[batch]; draft->k holds the rows). */
+kvc_status kvc_latent_accept(const kvc_latent_cache *cache, int32_t *len, const kvc_draft *draft,
+                             const int32_t *path, const int32_t *n_accept, void *stream);
+
+/* Expanded form: the keys and values of slots 0 .. len[b]-1 (len: device int32[batch], or NULL with
+ * n_valid) for every head, into an ordinary cache that every selection and decode of this
+ * library reads.  w_k: [n_heads][dst->d_head - d_rope][d_latent], w_v:
+ * [n_heads][dst->d_head][d_latent], cache dtype, contiguous, n_heads = dst->n_heads_kv;
+ * d_rope < dst->d_head.  dst slots at or beyond the length are left as they were.  fp32
+ * accumulation, rounded once to the cache's type; the d_rope part is copied. */
+kvc_status kvc_latent_expand(const kvc_latent_cache *cache, const int32_t *len, int32_t n_valid,
+                             const void *w_k, const void *w_v, const kvc_cache *dst,
+                             void *stream);
 
 #ifdef __cplusplus
 }

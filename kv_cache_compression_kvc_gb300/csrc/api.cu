@@ -1179,4 +1179,342 @@ kvc_status kvc_h2o_prefill_select_gqa(const void *q, int32_t n_heads_q, const kv
     return ok();
 }
 
+
+// ------------------------------------------------------------------------------------------
+// Trees of drafted tokens, latent caches.
+static kvc_status check_draft(const kvc_draft *d, const char *name, bool need_v, bool need_k)
+{
+    if (d == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null draft descriptor", name);
+    if (d->n_draft < 1 || d->n_draft > 64)
+        return fail(KVC_ERR_SHAPE, "%s: n_draft %d (supported: 1..64)", name, d->n_draft);
+    if (need_k && d->k == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "%s: null drafted rows", name);
+    if (need_v && (d->k == nullptr) != (d->v == nullptr))
+        return fail(KVC_ERR_INVALID_ARG, "%s: drafted keys without values or the reverse", name);
+    if (!aligned16(d->k) || (need_v && !aligned16(d->v)))
+        return fail(KVC_ERR_ALIGN, "%s: drafted rows must be 16-byte aligned", name);
+    if ((reinterpret_cast<uintptr_t>(d->mask) & 7u) || (reinterpret_cast<uintptr_t>(d->count) & 3u))
+        return fail(KVC_ERR_ALIGN, "%s: mask and count alignment", name);
+    return KVC_OK;
+}
+
+static kvc_status check_latent(const kvc_latent_cache *c, const char *name)
+{
+    if (c == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null latent cache descriptor", name);
+    if (c->c == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null latent rows", name);
+    if (c->dtype != KVC_F32 && c->dtype != KVC_BF16)
+        return fail(KVC_ERR_INVALID_ARG, "%s: dtype %d", name, c->dtype);
+    if (c->batch <= 0 || c->cap < 0)
+        return fail(KVC_ERR_SHAPE, "%s: batch %d cap %d", name, c->batch, c->cap);
+    if (c->d_latent != 128 && c->d_latent != 256 && c->d_latent != 512)
+        return fail(KVC_ERR_SHAPE, "%s: d_latent %d (supported: 128, 256, 512)", name, c->d_latent);
+    if (c->d_rope < 0 || c->d_rope > 64 || c->d_rope % 8)
+        return fail(KVC_ERR_SHAPE, "%s: d_rope %d (supported: multiples of 8 in 0..64)", name,
+                    c->d_rope);
+    if (c->stride_slot < c->d_latent + c->d_rope || c->stride_b < 0)
+        return fail(KVC_ERR_SHAPE, "%s: strides", name);
+    const int64_t eb = elem_bytes(c->dtype);
+    if (!aligned16(c->c) || (c->stride_slot * eb) % 16 || (c->stride_b * eb) % 16)
+        return fail(KVC_ERR_ALIGN, "%s: pointers and strides must be 16-byte aligned", name);
+    return KVC_OK;
+}
+
+// Workspace of either kernel that a call may take.
+static size_t tree_ws_bytes(int G, int DK, int DV, int T, int dtype, bool latent, int n_sm)
+{
+    size_t n = kvc::tree_plan(G, DK, DV, T, latent, false, n_sm).bytes;
+    if (dtype == KVC_BF16) n = std::max(n, kvc::tree_plan(G, DK, DV, T, latent, true, n_sm).bytes);
+    return n;
+}
+
+// Checks shared by the three attention entry points, then the launches.  p: inputs filled in.
+static kvc_status tree_run(kvc::TreeParams &p, int dtype, bool tc_ok, const kvc_draft *d, float scale,
+                           void *ws, size_t ws_bytes, void *stream, const char *name)
+{
+    if (p.q == nullptr || p.out == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null q/out", name);
+    if (!aligned16(p.q) || !aligned16(p.out))
+        return fail(KVC_ERR_ALIGN, "%s: q and out must be 16-byte aligned", name);
+    if ((reinterpret_cast<uintptr_t>(p.lse) & 3u) || (reinterpret_cast<uintptr_t>(p.len) & 3u))
+        return fail(KVC_ERR_ALIGN, "%s: lse and len alignment", name);
+    if (!std::isfinite(scale)) return fail(KVC_ERR_INVALID_ARG, "%s: scale", name);
+    if (p.len == nullptr && (p.n_valid < 0 || p.n_valid > p.cap))
+        return fail(KVC_ERR_CAPACITY, "%s: n_valid %d outside [0, cap %d]", name, p.n_valid, p.cap);
+    if ((long long)p.B * p.Hkv > 0x7fffffffLL)
+        return fail(KVC_ERR_SHAPE, "%s: batch * heads too large", name);
+    int32_t *code = nullptr;
+    int n_sm = 0;
+    kvc_status st = device_info(&code, &n_sm);
+    if (st != KVC_OK) return st;
+    p.P = p.B * p.Hkv;
+    p.kd = d->k;
+    p.vd = p.latent ? d->k : d->v;
+    p.mask = d->mask;
+    p.count = d->count;
+    p.T = d->n_draft;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.dev_code = code;
+    const size_t need = tree_ws_bytes(p.G, p.DK, p.DV, p.T, dtype, p.latent != 0, n_sm);
+    if (ws == nullptr || ws_bytes < need)
+        return fail(KVC_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", name, need, ws_bytes);
+    if (!aligned256(ws)) return fail(KVC_ERR_WORKSPACE, "%s: workspace alignment", name);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto plan = [&](bool tc) {
+        const kvc::TreePlan pl = kvc::tree_plan(p.G, p.DK, p.DV, p.T, p.latent != 0, tc, n_sm);
+        p.RN = pl.RN; p.RP = pl.RP; p.RT = pl.RT; p.groups = pl.groups;
+        char *base = static_cast<char *>(ws);
+        p.ws_info = reinterpret_cast<int4 *>(base + pl.off_info);
+        p.ws_ml = reinterpret_cast<float *>(base + pl.off_ml);
+        p.ws_o = reinterpret_cast<float *>(base + pl.off_o);
+    };
+    bool used = false;
+    cudaError_t e = cudaSuccess;
+    if (tc_ok && dtype == KVC_BF16) {
+        plan(true);
+        e = kvc::launch_tree_attn_tc(p, s, &used);
+    }
+    if (e == cudaSuccess && !used) {
+        plan(false);
+        e = kvc::launch_tree_attn(p, dtype, s);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    e = kvc::launch_tree_merge(p, dtype, s);
+    if (e != cudaSuccess) return cuda_fail(e, "tree merge launch");
+    return ok();
+}
+
+static kvc_status tree_heads(int32_t n_heads_q, int32_t n_heads_kv, const char *name, int *G)
+{
+    if (n_heads_q <= 0 || n_heads_q % n_heads_kv)
+        return fail(KVC_ERR_SHAPE, "%s: n_heads_q %d not a multiple of n_heads_kv %d", name,
+                    n_heads_q, n_heads_kv);
+    *G = n_heads_q / n_heads_kv;
+    if (*G > 64) return fail(KVC_ERR_SHAPE, "%s: group size %d (supported: 1..64)", name, *G);
+    return KVC_OK;
+}
+
+size_t kvc_decode_attn_tree_workspace_bytes(int32_t batch, int32_t n_heads_q,
+                                            int32_t n_heads_kv, int32_t d_head, int32_t n_draft,
+                                            int32_t dtype)
+{
+    if (batch <= 0 || n_heads_kv <= 0 || n_heads_q <= 0 || n_heads_q % n_heads_kv ||
+        n_heads_q / n_heads_kv > 64 || (d_head != 64 && d_head != 128 && d_head != 256) ||
+        n_draft < 1 || n_draft > 64 || (dtype != KVC_F32 && dtype != KVC_BF16))
+        return 0;
+    return tree_ws_bytes(n_heads_q / n_heads_kv, d_head, d_head, n_draft, dtype, false,
+                         sm_count_or_default());
+}
+
+static void tree_fill(kvc::TreeParams &p, const kvc_cache &c, const void *q, int n_heads_q, int G,
+                      void *out, float *lse)
+{
+    p.q = q; p.out = out; p.lse = lse;
+    p.k = c.k; p.v = c.v;
+    p.sb = c.stride_b; p.sh = c.stride_h; p.ss = c.stride_slot;
+    p.B = c.batch; p.Hq = n_heads_q; p.Hkv = c.n_heads_kv; p.G = G; p.cap = c.cap;
+    p.DK = p.DV = c.d_head;
+}
+
+kvc_status kvc_decode_attn_tree(const void *q, int32_t n_heads_q, const kvc_cache *cache,
+                                const int32_t *len, int32_t n_valid, const kvc_draft *draft,
+                                float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                                void *stream)
+{
+    const char *name = "kvc_decode_attn_tree";
+    kvc_status st = check_cache(cache, name, true);
+    if (st != KVC_OK) return st;
+    st = check_draft(draft, name, true, false);
+    if (st != KVC_OK) return st;
+    int G = 0;
+    st = tree_heads(n_heads_q, cache->n_heads_kv, name, &G);
+    if (st != KVC_OK) return st;
+    kvc::TreeParams p{};
+    tree_fill(p, *cache, q, n_heads_q, G, out, lse);
+    p.len = len; p.len_per_pair = 1; p.n_valid = n_valid;
+    return tree_run(p, cache->dtype, cache->cap > 0, draft, scale, ws, ws_bytes, stream, name);
+}
+
+kvc_status kvc_decode_attn_tree_paged(const void *q, int32_t n_heads_q,
+                                      const kvc_block_pool *pool, const kvc_page_table *pt,
+                                      const kvc_draft *draft, float scale, void *out, float *lse,
+                                      void *ws, size_t ws_bytes, void *stream)
+{
+    const char *name = "kvc_decode_attn_tree_paged";
+    kvc_cache view;
+    kvc_status st = check_paged(pool, pt, name, &view);
+    if (st != KVC_OK) return st;
+    st = check_draft(draft, name, true, false);
+    if (st != KVC_OK) return st;
+    int G = 0;
+    st = tree_heads(n_heads_q, pool->n_heads_kv, name, &G);
+    if (st != KVC_OK) return st;
+    kvc::TreeParams p{};
+    tree_fill(p, view, q, n_heads_q, G, out, lse);
+    p.len = pt->len;
+    p.table = pt->table; p.max_blocks = pt->max_blocks; p.bs = pool->block_size;
+    p.n_pool = pool->n_blocks;
+    return tree_run(p, pool->dtype, kvc::tree_tc_pages(pool->block_size, pool->d_head), draft, scale,
+                    ws, ws_bytes, stream, name);
+}
+
+size_t kvc_decode_attn_latent_workspace_bytes(int32_t batch, int32_t n_heads_q, int32_t d_latent,
+                                              int32_t d_rope, int32_t n_draft, int32_t dtype)
+{
+    if (batch <= 0 || n_heads_q <= 0 || n_heads_q > 256 ||
+        (d_latent != 128 && d_latent != 256 && d_latent != 512) || d_rope < 0 || d_rope > 64 ||
+        d_rope % 8 || n_draft < 1 || n_draft > 64 || (dtype != KVC_F32 && dtype != KVC_BF16))
+        return 0;
+    return tree_ws_bytes(n_heads_q, d_latent + d_rope, d_latent, n_draft, dtype, true,
+                         sm_count_or_default());
+}
+
+kvc_status kvc_decode_attn_latent(const void *q, int32_t n_heads_q, const kvc_latent_cache *cache,
+                                  const int32_t *len, int32_t n_valid, const kvc_draft *draft,
+                                  float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                                  void *stream)
+{
+    const char *name = "kvc_decode_attn_latent";
+    kvc_status st = check_latent(cache, name);
+    if (st != KVC_OK) return st;
+    st = check_draft(draft, name, false, false);
+    if (st != KVC_OK) return st;
+    if (n_heads_q <= 0 || n_heads_q > 256)
+        return fail(KVC_ERR_SHAPE, "%s: n_heads_q %d (supported: 1..256)", name, n_heads_q);
+    kvc::TreeParams p{};
+    p.q = q; p.out = out; p.lse = lse;
+    p.k = cache->c; p.v = cache->c;
+    p.sb = cache->stride_b; p.ss = cache->stride_slot;
+    p.B = cache->batch; p.Hq = n_heads_q; p.Hkv = 1; p.G = n_heads_q; p.cap = cache->cap;
+    p.DK = cache->d_latent + cache->d_rope;
+    p.DV = cache->d_latent;
+    p.latent = 1;
+    p.len = len; p.n_valid = n_valid;
+    return tree_run(p, cache->dtype, cache->cap > 0, draft, scale, ws, ws_bytes, stream, name);
+}
+
+static kvc_status accept_run(kvc::AcceptParams &p, const kvc_draft *draft, const int32_t *path,
+                             const int32_t *n_accept, bool paged, void *stream, const char *name)
+{
+    if (path == nullptr || n_accept == nullptr || p.len == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "%s: null path, n_accept or len", name);
+    if ((long long)p.B * p.H > 0x7fffffffLL)
+        return fail(KVC_ERR_SHAPE, "%s: batch * heads too large", name);
+    kvc_status st = device_info(&p.dev_code, nullptr);
+    if (st != KVC_OK) return st;
+    p.kd = draft->k;
+    p.vd = draft->v;
+    p.count = draft->count;
+    p.T = draft->n_draft;
+    p.path = path;
+    p.n_accept = n_accept;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = paged ? kvc::launch_tree_accept_paged(p, s) : kvc::launch_tree_accept(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "accept launch");
+    return ok();
+}
+
+kvc_status kvc_tree_accept(const kvc_cache *cache, int32_t *len, const kvc_draft *draft,
+                           const int32_t *path, const int32_t *n_accept, void *stream)
+{
+    const char *name = "kvc_tree_accept";
+    kvc_status st = check_cache(cache, name, true);
+    if (st != KVC_OK) return st;
+    st = check_draft(draft, name, true, true);
+    if (st != KVC_OK) return st;
+    kvc::AcceptParams p{};
+    p.k = cache->k; p.v = cache->v;
+    p.sb = cache->stride_b; p.sh = cache->stride_h; p.ss = cache->stride_slot;
+    p.B = cache->batch; p.H = cache->n_heads_kv; p.cap = cache->cap;
+    p.eb = elem_bytes(cache->dtype);
+    p.row_bytes = cache->d_head * p.eb;
+    p.len = len;
+    return accept_run(p, draft, path, n_accept, false, stream, name);
+}
+
+kvc_status kvc_latent_accept(const kvc_latent_cache *cache, int32_t *len, const kvc_draft *draft,
+                             const int32_t *path, const int32_t *n_accept, void *stream)
+{
+    const char *name = "kvc_latent_accept";
+    kvc_status st = check_latent(cache, name);
+    if (st != KVC_OK) return st;
+    st = check_draft(draft, name, false, true);
+    if (st != KVC_OK) return st;
+    kvc::AcceptParams p{};
+    p.k = cache->c;
+    p.sb = cache->stride_b; p.ss = cache->stride_slot;
+    p.B = cache->batch; p.H = 1; p.cap = cache->cap;
+    p.eb = elem_bytes(cache->dtype);
+    p.row_bytes = (cache->d_latent + cache->d_rope) * p.eb;
+    p.len = len;
+    return accept_run(p, draft, path, n_accept, false, stream, name);
+}
+
+kvc_status kvc_tree_accept_paged(const kvc_block_pool *pool, const kvc_page_table *pt,
+                                 const kvc_free_pool *free_pool, const kvc_draft *draft,
+                                 const int32_t *path, const int32_t *n_accept, int32_t *accepted,
+                                 void *stream)
+{
+    const char *name = "kvc_tree_accept_paged";
+    kvc_cache view;
+    kvc_status st = check_paged(pool, pt, name, &view);
+    if (st != KVC_OK) return st;
+    st = check_free_pool(free_pool, name);
+    if (st != KVC_OK) return st;
+    st = check_draft(draft, name, true, true);
+    if (st != KVC_OK) return st;
+    if (accepted == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null accepted", name);
+    kvc::AcceptParams p{};
+    p.k = pool->k; p.v = pool->v;
+    p.B = pt->batch; p.H = pool->n_heads_kv;
+    p.eb = elem_bytes(pool->dtype);
+    p.row_bytes = pool->d_head * p.eb;
+    p.len = pt->len;
+    p.table = pt->table; p.n_blocks = pt->n_blocks; p.score = pt->score;
+    p.max_blocks = pt->max_blocks; p.bs = pool->block_size; p.n_pool = pool->n_blocks;
+    p.free_ids = free_pool->ids; p.free_top = free_pool->top; p.free_cap = free_pool->capacity;
+    p.accepted = accepted;
+    return accept_run(p, draft, path, n_accept, true, stream, name);
+}
+
+kvc_status kvc_latent_expand(const kvc_latent_cache *cache, const int32_t *len, int32_t n_valid,
+                             const void *w_k, const void *w_v, const kvc_cache *dst, void *stream)
+{
+    const char *name = "kvc_latent_expand";
+    kvc_status st = check_latent(cache, name);
+    if (st != KVC_OK) return st;
+    st = check_cache(dst, name, true);
+    if (st != KVC_OK) return st;
+    if (dst->dtype != cache->dtype || dst->batch != cache->batch)
+        return fail(KVC_ERR_SHAPE, "%s: dst dtype %d batch %d, latent cache %d %d", name, dst->dtype,
+                    dst->batch, cache->dtype, cache->batch);
+    if (cache->d_rope >= dst->d_head)
+        return fail(KVC_ERR_SHAPE, "%s: d_rope %d leaves no key of d_head %d", name, cache->d_rope,
+                    dst->d_head);
+    if (w_k == nullptr || w_v == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null weights", name);
+    if (!aligned16(w_k) || !aligned16(w_v))
+        return fail(KVC_ERR_ALIGN, "%s: weights must be 16-byte aligned", name);
+    if (len == nullptr && (n_valid < 0 || n_valid > cache->cap || n_valid > dst->cap))
+        return fail(KVC_ERR_CAPACITY, "%s: n_valid %d outside [0, cap %d and %d]", name, n_valid,
+                    cache->cap, dst->cap);
+    if (dst->batch > 65535)
+        return fail(KVC_ERR_SHAPE, "%s: batch %d > 65535", name, dst->batch);
+    if ((long long)dst->n_heads_kv * (2 * dst->d_head / 64 + 1) > 65535)
+        return fail(KVC_ERR_SHAPE, "%s: %d heads", name, dst->n_heads_kv);
+    int32_t *code = nullptr;
+    st = device_info(&code, nullptr);
+    if (st != KVC_OK) return st;
+    kvc::ExpandParams p{};
+    p.c = cache->c; p.c_sb = cache->stride_b; p.c_ss = cache->stride_slot;
+    p.B = cache->batch; p.H = dst->n_heads_kv; p.R = cache->d_latent; p.E = cache->d_rope;
+    p.D = dst->d_head; p.cap = cache->cap;
+    p.len = len; p.n_valid = n_valid;
+    p.wk = w_k; p.wv = w_v;
+    p.k = dst->k; p.v = dst->v;
+    p.sb = dst->stride_b; p.sh = dst->stride_h; p.ss = dst->stride_slot;
+    p.dst_cap = dst->cap;
+    p.dev_code = code;
+    const cudaError_t e = kvc::launch_latent_expand(p, cache->dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "latent expand launch");
+    return ok();
+}
+
 }  // extern "C"

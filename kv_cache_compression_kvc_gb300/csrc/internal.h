@@ -281,4 +281,84 @@ cudaError_t launch_gather_scores(const float *s_full, int64_t s_stride, const in
                                  int64_t idx_stride, int rows, int n_keep, float *out,
                                  cudaStream_t stream);
 
+// ------------------------------------------------------------------------------------------
+// Attention of a tree of drafted tokens over a cache (contiguous, paged or latent); see
+// tree_attn.cuh for the schedule.
+struct TreeParams {
+    const void *q;               // [B][T][Hq][DK]
+    const void *k, *v;           // slot rows (strides in elements; v == k for a latent cache)
+    int64_t sb, sh, ss;
+    int32_t B, Hq, Hkv, G, P, cap;
+    int32_t DK, DV;              // key and value widths (latent: d_latent + d_rope, d_latent)
+    int32_t latent;
+    const int32_t *len;          // nullable; per pair or per sequence
+    int32_t len_per_pair, n_valid;
+    const int32_t *table;        // paged: [B][max_blocks]; pool [Hkv][n_pool][bs][D]
+    int32_t max_blocks, bs, n_pool;
+    const void *kd, *vd;         // drafted rows: token t of pair (b, h) at ((b*T + t)*Hkv + h)*DK
+    const uint64_t *mask;        // nullable (chain)
+    const int32_t *count;        // nullable (T each)
+    int32_t T;
+    float scale_log2;            // scale * log2(e)
+    void *out;                   // [B][T][Hq][DV], cache type
+    float *lse;                  // nullable
+    // schedule (plan): row tiles of RP rows padded to RN, `groups` ranges of tiles
+    int32_t RN, RP, RT, groups;
+    float *ws_o;                 // [groups*RT*2][RN][DV]
+    float *ws_ml;                // [groups*RT*2][RN][2] (max in log2 units, sum)
+    int4 *ws_info;               // [groups]
+    int32_t *dev_code;
+};
+struct TreePlan {
+    bool tc;                     // tensor-core kernel
+    int32_t RN, RP, RT, groups;
+    size_t off_info, off_ml, off_o, bytes;
+};
+// Row tile of the tensor-core kernel: RN rows (its matrix size), RP of them used.
+void tree_tc_rows(int G, int DV, int T, bool latent, int32_t *RN, int32_t *RP);
+TreePlan tree_plan(int G, int DK, int DV, int T, bool latent, bool tc, int n_sm);
+bool tree_tc_pages(int bs, int D);           // block sizes the tensor-core kernel takes
+cudaError_t launch_tree_attn(const TreeParams &p, int dtype, cudaStream_t stream);
+// Sets *used = false, launching nothing, when the tensor maps cannot be made.
+cudaError_t launch_tree_attn_tc(const TreeParams &p, cudaStream_t stream, bool *used);
+cudaError_t launch_tree_merge(const TreeParams &p, int dtype, cudaStream_t stream);
+
+// Accepted paths.
+struct AcceptParams {
+    void *k, *v;                 // v null for a latent cache
+    int64_t sb, sh, ss;          // elements
+    int32_t B, H, cap;
+    int32_t row_bytes;           // bytes of one row
+    int32_t eb;
+    int32_t *len;                // [B*H], or [B] paged
+    const void *kd, *vd;
+    const int32_t *count, *path, *n_accept;
+    int32_t T;
+    // paged
+    int32_t *table, *n_blocks;
+    float *score;
+    int32_t max_blocks, bs, n_pool;
+    int32_t *free_ids, *free_top;
+    int32_t free_cap;
+    int32_t *accepted;
+    int32_t *dev_code;
+};
+cudaError_t launch_tree_accept(const AcceptParams &p, cudaStream_t stream);
+cudaError_t launch_tree_accept_paged(const AcceptParams &p, cudaStream_t stream);
+
+// Latent rows to per-head keys and values.
+struct ExpandParams {
+    const void *c;
+    int64_t c_sb, c_ss;
+    int32_t B, H, R, E, D, cap;  // cap: slots of the latent cache
+    const int32_t *len;
+    int32_t n_valid;
+    const void *wk, *wv;
+    void *k, *v;
+    int64_t sb, sh, ss;
+    int32_t dst_cap;
+    int32_t *dev_code;
+};
+cudaError_t launch_latent_expand(const ExpandParams &p, int dtype, cudaStream_t stream);
+
 }  // namespace kvc

@@ -76,6 +76,19 @@ class kvc_duo(ctypes.Structure):
                 ("retrieval_heads", ctypes.c_void_p), ("t", ctypes.c_void_p)]
 
 
+class kvc_draft(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("count", ctypes.c_void_p), ("n_draft", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class kvc_latent_cache(ctypes.Structure):
+    _fields_ = [("c", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("cap", ctypes.c_int32), ("d_latent", ctypes.c_int32),
+                ("d_rope", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("stride_b", ctypes.c_int64), ("stride_slot", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -90,6 +103,8 @@ _POOL_P = ctypes.POINTER(kvc_block_pool)
 _PT_P = ctypes.POINTER(kvc_page_table)
 _FREE_P = ctypes.POINTER(kvc_free_pool)
 _DUO_P = ctypes.POINTER(kvc_duo)
+_DRAFT_P = ctypes.POINTER(kvc_draft)
+_LATENT_P = ctypes.POINTER(kvc_latent_cache)
 
 # name -> (restype, argtypes); every symbol declared in include/kvc.h
 SIGNATURES = {
@@ -136,6 +151,18 @@ SIGNATURES = {
     "kvc_h2o_prefill_gqa_workspace_bytes": (_SZ, [_I32] * 5),
     "kvc_h2o_prefill_select_gqa": (_I32, [_P, _I32, _CACHE_P, _I32, _I32, _I32, _F32, _P, _P, _P,
                                           _P, _SZ, _P]),
+    "kvc_decode_attn_tree_workspace_bytes": (_SZ, [_I32] * 6),
+    "kvc_decode_attn_tree": (_I32, [_P, _I32, _CACHE_P, _P, _I32, _DRAFT_P, _F32, _P, _P, _P,
+                                    _SZ, _P]),
+    "kvc_decode_attn_tree_paged": (_I32, [_P, _I32, _POOL_P, _PT_P, _DRAFT_P, _F32, _P, _P, _P,
+                                          _SZ, _P]),
+    "kvc_tree_accept": (_I32, [_CACHE_P, _P, _DRAFT_P, _P, _P, _P]),
+    "kvc_tree_accept_paged": (_I32, [_POOL_P, _PT_P, _FREE_P, _DRAFT_P, _P, _P, _P, _P]),
+    "kvc_decode_attn_latent_workspace_bytes": (_SZ, [_I32] * 6),
+    "kvc_decode_attn_latent": (_I32, [_P, _I32, _LATENT_P, _P, _I32, _DRAFT_P, _F32, _P, _P, _P,
+                                      _SZ, _P]),
+    "kvc_latent_accept": (_I32, [_LATENT_P, _P, _DRAFT_P, _P, _P, _P]),
+    "kvc_latent_expand": (_I32, [_LATENT_P, _P, _I32, _P, _P, _CACHE_P, _P]),
     "kvc_h2o_prefill_select": (_I32, [_P, _CACHE_P, _I32, _I32, _I32, _F32, _P, _P, _P, _P,
                                       _SZ, _P]),
 }
@@ -673,3 +700,259 @@ def kvc_h2o_prefill_select_gqa(q: torch.Tensor, k_prompt: torch.Tensor, *, seq_l
         _ptr(q), Hq, ctypes.byref(c), seq_len, L_local, K_hh, float(scale), _ptr(idx_out),
         _ptr(score_out), _ptr(s_full), wp, wb, _stream(stream)))
     return idx_out, score_out
+
+
+# ------------------------------------------------------------------------------------------
+# Trees of drafted tokens, latent caches.
+def _need(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> None:
+    """The library reads `t` as a contiguous array of this type and shape: check it first."""
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous() or
+                          t.device != device):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}, "
+                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _on_current(device: torch.device, view, what: str) -> None:
+    """The kernels run on the current CUDA device: the tensors, and those of the cache, live there."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {device}: the current CUDA device is needed")
+    kept = getattr(view, "_keep", None)
+    kept = kept[0] if isinstance(kept, tuple) else kept
+    if kept is not None and kept.device != device:
+        raise ValueError(f"{what} is on {device}, the cache on {kept.device}")
+
+
+def _torch_dtype(code: int) -> torch.dtype:
+    return torch.bfloat16 if code == KVC_BF16 else torch.float32
+
+
+def make_draft(k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, *,
+               mask: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None,
+               n_draft: Optional[int] = None) -> kvc_draft:
+    """Describe the drafted tokens of a batch (see kvc.h).  k, v [B, n_draft, n_heads_kv, d_head];
+    for a latent cache k [B, n_draft, d_latent + d_rope] alone.  mask int64 [B, n_draft] (the
+    bits of a uint64), count int32 [B].  Without k the query tokens see the cache only: give
+    n_draft."""
+    d = kvc_draft()
+    if k is not None:
+        if k.dim() not in (3, 4) or not k.is_contiguous():
+            raise ValueError("drafted rows are contiguous [B, n_draft, n_heads_kv, d_head] or "
+                             "[B, n_draft, d_latent + d_rope]")
+        if v is not None and (v.shape != k.shape or v.dtype != k.dtype or
+                              not v.is_contiguous() or v.device != k.device):
+            raise ValueError("drafted values must match the drafted keys")
+        if (v is None) != (k.dim() == 3):
+            raise ValueError("drafted keys need values, drafted latent rows have none")
+        if n_draft is not None and n_draft != k.shape[1]:
+            raise ValueError(f"n_draft {n_draft}, but {k.shape[1]} drafted rows")
+        d.n_draft = k.shape[1]
+        _need(mask, "mask", torch.int64, k.shape[:2], k.device)
+        _need(count, "count", torch.int32, k.shape[:1], k.device)
+    elif v is not None or n_draft is None:
+        raise ValueError("a draft needs its keys, or n_draft alone")
+    else:
+        if mask is not None:
+            raise ValueError("a mask needs drafted keys")
+        if count is not None and (count.dtype != torch.int32 or count.dim() != 1 or
+                                  not count.is_contiguous()):
+            raise ValueError("count must be a contiguous int32 tensor [B]")
+        d.n_draft = n_draft
+    d.k, d.v = (None if x is None else x.data_ptr() for x in (k, v))
+    d.mask, d.count = (None if x is None else x.data_ptr() for x in (mask, count))
+    d._keep = (k, v, mask, count)   # the descriptor holds their addresses: keep them alive
+    d._rows = None if k is None else (k.shape, k.dtype, k.device)
+    return d
+
+
+def latent_cache_view(c: torch.Tensor, d_latent: int) -> kvc_latent_cache:
+    """Describe latent rows [batch, cap, d_latent + d_rope] (a row contiguous)."""
+    if c.dim() != 3 or c.stride(2) != 1 or not 0 < d_latent <= c.shape[2]:
+        raise ValueError("latent rows are [batch, cap, d_latent + d_rope], a row contiguous")
+    x = kvc_latent_cache()
+    x.c = c.data_ptr()
+    x.dtype = _dtype_code(c.dtype)
+    x.batch, x.cap = c.shape[0], c.shape[1]
+    x.d_latent, x.d_rope = d_latent, c.shape[2] - d_latent
+    x.stride_b, x.stride_slot = c.stride(0), c.stride(1)
+    x._keep = c                     # the descriptor holds its address: keep it alive
+    return x
+
+
+def kvc_decode_attn_tree_workspace_bytes(batch, n_heads_q, n_heads_kv, d_head, n_draft,
+                                         dtype) -> int:
+    return int(load().kvc_decode_attn_tree_workspace_bytes(batch, n_heads_q, n_heads_kv, d_head,
+                                                           n_draft, dtype))
+
+
+def kvc_decode_attn_latent_workspace_bytes(batch, n_heads_q, d_latent, d_rope, n_draft,
+                                           dtype) -> int:
+    return int(load().kvc_decode_attn_latent_workspace_bytes(batch, n_heads_q, d_latent, d_rope,
+                                                             n_draft, dtype))
+
+
+def tree_workspace(batch, n_heads_q, n_heads_kv, d_head, n_draft, dtype: torch.dtype,
+                   device) -> torch.Tensor:
+    """A workspace for kvc_decode_attn_tree and kvc_decode_attn_tree_paged (need not be cleared)."""
+    n = kvc_decode_attn_tree_workspace_bytes(batch, n_heads_q, n_heads_kv, d_head, n_draft,
+                                             _dtype_code(dtype))
+    return torch.empty(n + 256, dtype=torch.uint8, device=device)
+
+
+def latent_workspace(batch, n_heads_q, d_latent, d_rope, n_draft, dtype: torch.dtype,
+                     device) -> torch.Tensor:
+    """A workspace for kvc_decode_attn_latent (need not be cleared)."""
+    n = kvc_decode_attn_latent_workspace_bytes(batch, n_heads_q, d_latent, d_rope, n_draft,
+                                               _dtype_code(dtype))
+    return torch.empty(n + 256, dtype=torch.uint8, device=device)
+
+
+def _attn_args(q, view, width, out_width, code, batch, draft, rows_shape, out, lse):
+    """Checks shared by the draft-tree and latent attention; returns out."""
+    dt = _torch_dtype(code)
+    if q.dim() != 4 or q.dtype != dt or not q.is_contiguous() or q.shape[0] != batch or \
+            q.shape[1] != draft.n_draft or q.shape[3] != width:
+        raise ValueError(f"q must be a contiguous {dt} tensor [{batch}, {draft.n_draft}, "
+                         f"n_heads_q, {width}], got {q.dtype} {list(q.shape)}")
+    dev = q.device
+    _on_current(dev, view, "q")
+    if draft._rows is not None and draft._rows != (rows_shape, dt, dev):
+        raise ValueError(f"drafted rows must be {dt} {list(rows_shape)} on {dev}, got "
+                         f"{draft._rows[1]} {list(draft._rows[0])} on {draft._rows[2]}")
+    _need(draft._keep[3], "count", torch.int32, (batch,), dev)
+    if out is None:
+        out = torch.empty(q.shape[:3] + (out_width,), dtype=dt, device=dev)
+    else:
+        _need(out, "out", dt, q.shape[:3] + (out_width,), dev)
+    _need(lse, "lse", torch.float32, q.shape[:3], dev)
+    return out
+
+
+def kvc_decode_attn_tree(q: torch.Tensor, cache: kvc_cache, draft: kvc_draft, *, scale: float,
+                         len: Optional[torch.Tensor] = None, n_valid: Optional[int] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """q [B, T, Hq, D] -> out [B, T, Hq, D] (the cache's type): every drafted token over the cached
+    slots and the drafted tokens it sees.  len int32 [B, Hkv] (or [B * Hkv])."""
+    c = cache
+    out = _attn_args(q, c, c.d_head, c.d_head, c.dtype, c.batch, draft,
+                     (c.batch, draft.n_draft, c.n_heads_kv, c.d_head), out, lse)
+    if len is not None and len.dim() == 2:
+        _need(len, "len", torch.int32, (c.batch, c.n_heads_kv), q.device)
+    else:
+        _need(len, "len", torch.int32, (c.batch * c.n_heads_kv,), q.device)
+    if ws is None:
+        ws = tree_workspace(c.batch, q.shape[2], c.n_heads_kv, c.d_head, draft.n_draft, q.dtype,
+                            q.device)
+    wp, wb = _ws_ptr(ws)
+    _check(load().kvc_decode_attn_tree(
+        q.data_ptr(), q.shape[2], c, _ptr(len), -1 if n_valid is None else n_valid, draft, scale,
+        out.data_ptr(), _ptr(lse), wp, wb, _stream(stream)))
+    return out
+
+
+def kvc_decode_attn_tree_paged(q: torch.Tensor, pool: kvc_block_pool, pt: kvc_page_table,
+                               draft: kvc_draft, *, scale: float,
+                               out: Optional[torch.Tensor] = None,
+                               lse: Optional[torch.Tensor] = None,
+                               ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """q [B, T, Hq, D] -> out [B, T, Hq, D] over each sequence's page table and its drafts."""
+    out = _attn_args(q, pool, pool.d_head, pool.d_head, pool.dtype, pt.batch, draft,
+                     (pt.batch, draft.n_draft, pool.n_heads_kv, pool.d_head), out, lse)
+    if ws is None:
+        ws = tree_workspace(pt.batch, q.shape[2], pool.n_heads_kv, pool.d_head, draft.n_draft,
+                            q.dtype, q.device)
+    wp, wb = _ws_ptr(ws)
+    _check(load().kvc_decode_attn_tree_paged(
+        q.data_ptr(), q.shape[2], pool, pt, draft, scale, out.data_ptr(), _ptr(lse), wp, wb,
+        _stream(stream)))
+    return out
+
+
+def kvc_decode_attn_latent(q: torch.Tensor, cache: kvc_latent_cache, draft: kvc_draft, *,
+                           scale: float, len: Optional[torch.Tensor] = None,
+                           n_valid: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                           lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """Absorbed latent attention: q [B, T, Hq, d_latent + d_rope] -> out [B, T, Hq, d_latent].
+    len int32 [B]."""
+    c = cache
+    width = c.d_latent + c.d_rope
+    out = _attn_args(q, c, width, c.d_latent, c.dtype, c.batch, draft,
+                     (c.batch, draft.n_draft, width), out, lse)
+    _need(len, "len", torch.int32, (c.batch,), q.device)
+    if ws is None:
+        ws = latent_workspace(c.batch, q.shape[2], c.d_latent, c.d_rope, draft.n_draft, q.dtype,
+                              q.device)
+    wp, wb = _ws_ptr(ws)
+    _check(load().kvc_decode_attn_latent(
+        q.data_ptr(), q.shape[2], c, _ptr(len), -1 if n_valid is None else n_valid, draft, scale,
+        out.data_ptr(), _ptr(lse), wp, wb, _stream(stream)))
+    return out
+
+
+def _accept_args(draft, view, rows_shape, code, path, n_accept):
+    if draft._rows is None:
+        raise ValueError("accepting needs the drafted rows")
+    shape, dtype, dev = draft._rows
+    if shape != rows_shape or dtype != _torch_dtype(code):
+        raise ValueError(f"drafted rows must be {_torch_dtype(code)} {list(rows_shape)}, got "
+                         f"{dtype} {list(shape)}")
+    _on_current(dev, view, "the draft")
+    _need(path, "path", torch.int32, shape[:2], dev)
+    _need(n_accept, "n_accept", torch.int32, shape[:1], dev)
+    return dev
+
+
+def kvc_tree_accept(cache: kvc_cache, len: torch.Tensor, draft: kvc_draft, path: torch.Tensor,
+                    n_accept: torch.Tensor, stream=None) -> None:
+    """Append drafted tokens path[b, :n_accept[b]] at the tail of every (sequence, head); len
+    int32 [B, Hkv] (or [B * Hkv]) advances.  path int32 [B, n_draft], n_accept int32 [B]."""
+    c = cache
+    dev = _accept_args(draft, c, (c.batch, draft.n_draft, c.n_heads_kv, c.d_head), c.dtype, path,
+                       n_accept)
+    shape = (c.batch, c.n_heads_kv) if len.dim() == 2 else (c.batch * c.n_heads_kv,)
+    _need(len, "len", torch.int32, shape, dev)
+    _check(load().kvc_tree_accept(c, len.data_ptr(), draft, path.data_ptr(), n_accept.data_ptr(),
+                                  _stream(stream)))
+
+
+def kvc_latent_accept(cache: kvc_latent_cache, len: torch.Tensor, draft: kvc_draft,
+                      path: torch.Tensor, n_accept: torch.Tensor, stream=None) -> None:
+    """kvc_tree_accept for a latent cache; len int32 [B]."""
+    c = cache
+    dev = _accept_args(draft, c, (c.batch, draft.n_draft, c.d_latent + c.d_rope), c.dtype, path,
+                       n_accept)
+    _need(len, "len", torch.int32, (c.batch,), dev)
+    _check(load().kvc_latent_accept(c, len.data_ptr(), draft, path.data_ptr(),
+                                    n_accept.data_ptr(), _stream(stream)))
+
+
+def kvc_tree_accept_paged(pool: kvc_block_pool, pt: kvc_page_table, free_pool: kvc_free_pool,
+                          draft: kvc_draft, path: torch.Tensor, n_accept: torch.Tensor, *,
+                          accepted: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """kvc_tree_accept for a paged cache; returns accepted int32 [B] (0: refused)."""
+    dev = _accept_args(draft, pool, (pt.batch, draft.n_draft, pool.n_heads_kv, pool.d_head), pool.dtype,
+                       path, n_accept)
+    if accepted is None:
+        accepted = torch.empty(pt.batch, dtype=torch.int32, device=dev)
+    else:
+        _need(accepted, "accepted", torch.int32, (pt.batch,), dev)
+    _check(load().kvc_tree_accept_paged(pool, pt, free_pool, draft, path.data_ptr(),
+                                        n_accept.data_ptr(), accepted.data_ptr(),
+                                        _stream(stream)))
+    return accepted
+
+
+def kvc_latent_expand(cache: kvc_latent_cache, w_k: torch.Tensor, w_v: torch.Tensor,
+                      dst: kvc_cache, *, len: Optional[torch.Tensor] = None,
+                      n_valid: Optional[int] = None, stream=None) -> None:
+    """Keys and values of every head from latent rows into an ordinary cache.  w_k
+    [H, d_head - d_rope, d_latent], w_v [H, d_head, d_latent]; len int32 [B]."""
+    c, H, D = cache, dst.n_heads_kv, dst.d_head
+    dev = w_k.device
+    _on_current(dev, cache, "w_k")
+    _need(w_k, "w_k", _torch_dtype(c.dtype), (H, D - c.d_rope, c.d_latent), dev)
+    _need(w_v, "w_v", _torch_dtype(c.dtype), (H, D, c.d_latent), dev)
+    _need(len, "len", torch.int32, (c.batch,), dev)
+    _check(load().kvc_latent_expand(c, _ptr(len), -1 if n_valid is None else n_valid,
+                                    w_k.data_ptr(), w_v.data_ptr(), dst, _stream(stream)))
