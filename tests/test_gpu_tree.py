@@ -427,8 +427,11 @@ def test_accept_refusals_leave_rows_as_they_were():
     assert run(ten, bad, [3, 3, 2])[1] == [[13, 13], [10, 10], [12, 12]]
     assert run(ten, bad, [3, 2, 2])[:2] == (0, [[13, 13], [12, 12], [12, 12]])   # not on the path
     assert run(ten, good, [5, -1, 4])[:2] == (5, [[10, 10], [10, 10], [14, 14]])
-    assert run([[17, 16], [20, 0], [21, -1]], good, [4, 1, 1]) == \
-        (1, [[17, 20], [20, 1], [21, -1]], [[0, 4], [0, 1], [0, 0]])
+    assert run([[17, 16], [20, 0], [1, 2]], good, [4, 1, 1]) == \
+        (1, [[17, 20], [20, 1], [2, 3]], [[0, 4], [0, 1], [1, 1]])
+    # two kinds of refusal at once: whichever block records first (the codes keep the first)
+    st, ln, rows = run([[17, 16], [20, 0], [21, -1]], good, [4, 1, 1])
+    assert st in (1, 5) and ln == [[17, 20], [20, 1], [21, -1]] and rows == [[0, 4], [0, 1], [0, 0]]
     count = torch.tensor([4, 2, 0], dtype=torch.int32, device=dev)
     assert run(ten, good, [4, 3, 0], count)[:2] == (3, [[14, 14], [10, 10], [10, 10]])
 
