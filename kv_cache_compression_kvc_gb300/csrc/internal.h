@@ -360,5 +360,8 @@ struct ExpandParams {
     int32_t *dev_code;
 };
 cudaError_t launch_latent_expand(const ExpandParams &p, int dtype, cudaStream_t stream);
+// bf16 on the tensor cores; sets *used = false, launching nothing, when the tensor maps cannot be
+// made.
+cudaError_t launch_latent_expand_tc(const ExpandParams &p, cudaStream_t stream, bool *used);
 
 }  // namespace kvc

@@ -1,4 +1,5 @@
-// latent_expand.cu -- the expanded form of a latent cache on the CUDA cores (fp32 arithmetic):
+// latent_expand.cu -- the expanded form of a latent cache on the CUDA cores (fp32 caches, fp32
+// arithmetic):
 //   K[b,h,s,i] = sum_r W_k[h,i,r] c[b,s,r] (i < D - E),  K[b,h,s,D-E+e] = c[b,s,R+e],
 //   V[b,h,s,i] = sum_r W_v[h,i,r] c[b,s,r].
 // A block computes 64 slots x 64 outputs of one head (256 threads, 4 x 4 each) from 32-deep
@@ -89,6 +90,11 @@ cudaError_t launch_latent_expand(const ExpandParams &p, int dtype, cudaStream_t 
 {
     const int most = p.len != nullptr ? (p.cap < p.dst_cap ? p.cap : p.dst_cap) : p.n_valid;
     if (most <= 0) return cudaSuccess;
+    if (dtype == 1) {
+        bool used = false;
+        const cudaError_t e = launch_latent_expand_tc(p, stream, &used);
+        if (e != cudaSuccess || used) return e;
+    }
     const int kt = (p.D - p.E + kTO - 1) / kTO, vt = p.D / kTO;
     const dim3 grid((unsigned)((most + kTS - 1) / kTS), (unsigned)(p.H * (kt + vt)), (unsigned)p.B);
     if (dtype == 1)

@@ -9,14 +9,27 @@
 namespace kvc {
 namespace tc {
 
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
-                                       int c3, uint32_t bar)
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                       int c3, int c4, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
         : "memory");
+}
+// Brings a box into L2.
+__device__ __forceinline__ void prefetch_5d(const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+                 : "memory");
+}
+// The first use of a tensor map otherwise stalls its copy for about 2 us.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 __device__ __forceinline__ void fence_before()
 {
@@ -49,6 +62,16 @@ constexpr uint32_t idesc(int M, int N, bool a_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// One lane of a converged warp.  Products and TMA copies are issued by a whole warp that picks a
+// lane for each group: their operands are then warp-uniform to the compiler.  Issued from a branch
+// on the thread index, a product costs 179 clocks of issue whatever its shape (64 x 64 x 16 and
+// 128 x 256 x 16 alike) and a copy about 400; this way a 128 x 128 x 16 product costs its 65.
+__device__ __forceinline__ bool elect()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
 {
@@ -91,22 +114,31 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float *v)
           "=r"(r[31])
         : "r"(taddr));
 }
+// 16 columns.
+__device__ __forceinline__ void ld16(uint32_t taddr, float *v)
+{
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void wait_ld()
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void st32(uint32_t taddr, const float *v)
+__device__ __forceinline__ void st16(uint32_t taddr, const float *v)
 {
     const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-        "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
-            taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void wait_st()
@@ -124,6 +156,18 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t a, uint32_t
 {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
+}
+// Whether the phase with this parity has completed (no waiting).
+__device__ __forceinline__ bool test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // Barrier `id` over n threads.
 __device__ __forceinline__ void bar_sync(int id, int n)
@@ -145,22 +189,22 @@ __device__ __forceinline__ bool bar_any(int id, int n, bool x)
 // ---- host ---------------------------------------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 encoder();   // nullptr when the driver has none
 
-// bf16 map of four dimensions (strides of the upper three in bytes), 128-byte swizzle, 64-element
-// rows: box {64, b1, b2, 1}.
-inline bool encode_4d(CUtensorMap *m, const void *ptr, const uint64_t (&dims)[4],
-                      const uint64_t (&strides)[3], uint32_t b1, uint32_t b2)
+// bf16 map of five dimensions (strides of the upper four in bytes), 128-byte swizzle, box {64, b1,
+// b2, b3, 1}: copies of 64-element pieces.
+inline bool encode_5d(CUtensorMap *m, const void *ptr, const uint64_t (&dims)[5],
+                      const uint64_t (&strides)[4], uint32_t b1, uint32_t b2, uint32_t b3)
 {
     const auto enc = encoder();
     if (enc == nullptr) return false;
-    cuuint64_t d[4], s[3];
-    for (int i = 0; i < 4; ++i) {
-        if (dims[i] == 0 || dims[i] > 0x80000000ull) return false;
+    cuuint64_t d[5], s[4];
+    for (int i = 0; i < 5; ++i) {
+        if (dims[i] == 0 || dims[i] > 0x7fffffffull) return false;
         d[i] = dims[i];
     }
-    for (int i = 0; i < 3; ++i) s[i] = strides[i];
-    cuuint32_t box[4] = {64, b1, b2, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), d, s, box, estr,
+    for (int i = 0; i < 4; ++i) s[i] = strides[i];
+    cuuint32_t box[5] = {64, b1, b2, b3, 1};
+    cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(ptr), d, s, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -34,6 +34,12 @@ struct Elem<float> {
         f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
     }
     static __device__ __forceinline__ float narrow(float x) { return x; }
+    template <int W>
+    static __device__ __forceinline__ void store(float *p, const float *x)
+    {
+        if constexpr (W == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        else *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+    }
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -44,6 +50,15 @@ struct Elem<__nv_bfloat16> {
         f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
     }
     static __device__ __forceinline__ __nv_bfloat16 narrow(float x) { return __float2bfloat16(x); }
+    template <int W>
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *x)
+    {
+        __nv_bfloat162 y[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) y[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        if constexpr (W == 4) *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(y);
+        else *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<uint32_t *>(y);
+    }
 };
 
 __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) <= 3.402823466e38f; }
@@ -79,16 +94,15 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
     float *sV = sA + kRows;                  // [64][DV]
     if (LATENT) sV = sK;
     const int VS = LATENT ? KS : DV;
-    __shared__ long long s_scan[kThreads / 32 + 4];
     __shared__ unsigned long long s_nf;      // drafted tokens with non-finite values
 
     const int tid = threadIdx.x;
     const int rt = blockIdx.x % p.RT, g = blockIdx.x / p.RT;
     pdl_trigger();
     pdl_wait();
-    const TreeRange range = tree_range<kThreads>(p, g, kTile, s_scan);
+    const TreeRange range = tree_range(p, g, kTile);
     int4 note = make_int4(-1, 0, 0, 0);
-    TreeWalk walk(range);
+    TreeWalk walk(p, range);
     TreeSeg s;
 
     constexpr int NC = out_cols<DV>();       // column groups
@@ -307,59 +321,60 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
     if (rt == 0 && tid == 0) p.ws_info[g] = note;
 }
 
-// Joins the partial states of split pairs.  Block (g, rt, row) takes the pair whose first part
-// group g holds (if any), row `row` of row tile rt; its four warps take every fourth part, each
-// lane DV / 32 columns, and meet in shared memory.  What bounds it: latency (one read of each
-// part, eight in flight per warp).
-constexpr int kMergeWarps = 4;
-template <typename T, int DV>
+// Joins the partial states of split pairs.  Blocks (group g * row tile, row chunk) take the pair
+// whose first part group g holds (if any): WPR of a block's eight warps per row, each every
+// WPR-th part, DV / 32 columns a lane.  Bound by latency (a chain of three L2 reads), so a warp has
+// several parts in flight and the grid is one wave: one warp per row where there are many rows
+// (1216 blocks on the SnapKV cache instead of 9728 of a row each: 13 us to 4), eight where
+// there are few rows of many parts.
+constexpr int kMergeWarps = 8;
+template <typename T, int DV, int WPR>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const TreeParams p)
 {
     constexpr int CPL = DV / 32;             // columns per lane
     static_assert(CPL == 2 || CPL % 4 == 0, "vector columns");
     constexpr int W = CPL == 2 ? 2 : 4;      // floats per load
     constexpr int NV = CPL / W;
-    __shared__ float s_o[kMergeWarps][DV];
-    __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+    constexpr int ROWS = kMergeWarps / WPR;  // rows per block
+    __shared__ float s_o[WPR > 1 ? kMergeWarps : 1][WPR > 1 ? DV : 1];
+    __shared__ float s_l[kMergeWarps];
     pdl_trigger();
     pdl_wait();
     const int rt = blockIdx.x % p.RT, g = blockIdx.x / p.RT;
     const int4 note = p.ws_info[g];
     if (note.x < 0) return;
     const int pair = note.x, b = pair / p.Hkv, kh = pair - b * p.Hkv;
-    const int r = blockIdx.y;
-    const int rows = min(p.RP, tree_count(p, b) * p.G - rt * p.RP);
-    if (r >= rows) return;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nseg = note.y - g + 1;
+    const int r = blockIdx.y * ROWS + w / WPR, part0 = w % WPR;
+    const int rows = min(p.RP, tree_count(p, b) * p.G - rt * p.RP);
+    const bool live = r < rows;
+    if (WPR == 1 && !live) return;
+    const int nseg = live ? note.y - g + 1 : 0;
     auto slot_of = [&](int i) -> size_t {
         return ((size_t)((g + i) * p.RT + rt) * 2 + (i == 0 ? note.z : 0)) * p.RN + r;
     };
     float M = kNegBig;
-    for (int i = w * 32 + lane; i < nseg; i += kMergeWarps * 32)
-        M = fmaxf(M, __ldcg(p.ws_ml + slot_of(i) * 2));
+    for (int i = lane; i < nseg; i += 32) M = fmaxf(M, __ldcg(p.ws_ml + slot_of(i) * 2));
     M = warp_max(M);
-    if (lane == 0) s_m[w] = M;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) M = fmaxf(M, s_m[i]);
     float o[CPL], L = 0.f;
 #pragma unroll
     for (int c = 0; c < CPL; ++c) o[c] = 0.f;
     constexpr int UNR = CPL >= 16 ? 4 : 8;
-    for (int i0 = w; i0 < nseg; i0 += kMergeWarps * UNR) {
+#pragma unroll 1
+    for (int i0 = part0; i0 < nseg; i0 += WPR * UNR) {
         float x[UNR][CPL], ml[UNR][2];
 #pragma unroll
         for (int u = 0; u < UNR; ++u) {
-            const int i = i0 + u * kMergeWarps;
+            const int i = i0 + u * WPR;
             ml[u][0] = kNegBig;
             ml[u][1] = 0.f;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) x[u][c] = 0.f;
             if (i < nseg) {
                 const size_t st = slot_of(i);
-                ml[u][0] = __ldcg(p.ws_ml + st * 2);
-                ml[u][1] = __ldcg(p.ws_ml + st * 2 + 1);
+                const float2 y2 = __ldcg(reinterpret_cast<const float2 *>(p.ws_ml + st * 2));
+                ml[u][0] = y2.x;
+                ml[u][1] = y2.y;
 #pragma unroll
                 for (int n = 0; n < NV; ++n) {
                     const float *src = p.ws_o + st * DV + (n * 32 + lane) * W;
@@ -383,26 +398,38 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
             for (int k = 0; k < CPL; ++k) o[k] = fmaf(c, x[u][k], o[k]);
         }
     }
+    if constexpr (WPR > 1) {                 // the row's warps meet, in order
 #pragma unroll
-    for (int n = 0; n < NV; ++n)
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int e = 0; e < W; ++e) s_o[w][(n * 32 + lane) * W + e] = o[n * W + e];
-    if (lane == 0) s_l[w] = L;
-    __syncthreads();
-    const int row_g = rt * p.RP + r;
-    const size_t row = ((size_t)b * p.T + row_g / p.G) * p.Hq + kh * p.G + row_g % p.G;
-    L = 0.f;
+            for (int e = 0; e < W; ++e) s_o[w][(n * 32 + lane) * W + e] = o[n * W + e];
+        if (lane == 0) s_l[w] = L;
+        __syncthreads();
+        if (part0 != 0 || !live) return;
+        L = 0.f;
 #pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) L += s_l[i];
-    const float inv = 1.f / L;
-    for (int d = threadIdx.x; d < DV; d += kMergeWarps * 32) {
-        float x = 0.f;
+        for (int c = 0; c < CPL; ++c) o[c] = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < WPR; ++i) {
+            L += s_l[w + i];
 #pragma unroll
-        for (int i = 0; i < kMergeWarps; ++i) x += s_o[i][d];
-        x = L == 0.f ? 0.f : x * inv;
-        static_cast<T *>(p.out)[row * DV + d] = Elem<T>::narrow(x);
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int e = 0; e < W; ++e) o[n * W + e] += s_o[w + i][(n * 32 + lane) * W + e];
+        }
     }
-    if (threadIdx.x == 0 && p.lse != nullptr)
+    const int row_g = rt * p.RP + r, t = row_g / p.G;
+    const size_t row = ((size_t)b * p.T + t) * p.Hq + kh * p.G + (row_g - t * p.G);
+    const float inv = 1.f / L;
+    T *dst = static_cast<T *>(p.out) + row * DV;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        float y[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) y[e] = L == 0.f ? 0.f : o[n * W + e] * inv;
+        Elem<T>::template store<W>(dst + (n * 32 + lane) * W, y);
+    }
+    if (lane == 0 && p.lse != nullptr)
         p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
@@ -444,10 +471,14 @@ cudaError_t launch_dims(const TreeParams &p, cudaStream_t stream)
 template <typename T, int DV>
 cudaError_t merge_typed(const TreeParams &p, cudaStream_t stream)
 {
-    const int rows = std::min(p.RP, p.T * p.G);
-    return launch_pdl(tree_merge_kernel<T, DV>,
-                      dim3((unsigned)(p.groups * p.RT), (unsigned)rows), dim3(kMergeWarps * 32), 0,
-                      stream, p);
+    const int rows = std::min(p.RP, p.T * p.G), gx = p.groups * p.RT;
+    // eight warps a row while that makes at most four blocks an SM
+    if ((long long)gx * rows <= 4 * 152)
+        return launch_pdl(tree_merge_kernel<T, DV, 8>, dim3((unsigned)gx, (unsigned)rows),
+                          dim3(kMergeWarps * 32), 0, stream, p);
+    return launch_pdl(tree_merge_kernel<T, DV, 1>,
+                      dim3((unsigned)gx, (unsigned)((rows + kMergeWarps - 1) / kMergeWarps)),
+                      dim3(kMergeWarps * 32), 0, stream, p);
 }
 template <typename T>
 cudaError_t merge_dims(const TreeParams &p, cudaStream_t stream)
@@ -466,7 +497,7 @@ void tree_tc_rows(int G, int DV, int T, bool latent, int32_t *RN, int32_t *RP)
 {
     (void)DV;
     if (latent) {
-        *RN = *RP = 64;
+        *RN = *RP = T * G <= 32 ? 32 : 64;
     } else {
         *RN = T * G <= 64 ? 64 : 128;
         *RP = *RN / G * G;

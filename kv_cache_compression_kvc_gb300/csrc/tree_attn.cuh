@@ -8,9 +8,9 @@
 // walks range g for row tile rt, so the RT blocks that read the same slots run side by side
 // and all but the first find them in L2.
 //
-// The lengths live on the device, so every block finds its own range: the block scans the
-// pairs' tile counts (one read of the lengths), which makes the ranges equal however ragged the
-// batch is, without a host round trip.
+// The lengths live on the device, so every warp finds its block's range by itself: it scans the
+// pairs' tile counts (one read of the lengths, no block barrier), which makes the ranges equal
+// however ragged the batch is, without a host round trip.
 //
 // A pair that lies inside one range is finished by its block.  A pair that crosses ranges leaves
 // one partial state (max, sum, unnormalised output) per range: workspace slot 2*block for the
@@ -47,33 +47,41 @@ __device__ __forceinline__ int tree_tiles(const TreeParams &p, int len, int cnt,
     return n > 0 ? n : 1;
 }
 
+// Range g holds tiles [g*q + min(g, r), ...): q tiles, one more in the first r ranges.
 struct TreeRange {
     int pair, off;               // first pair of the range and the tile inside it
+    int len, cnt;                // that pair's slots and drafted tokens
     int n;                       // tiles in the range
-    long long t0, T;             // the range's first tile, all tiles
-    int Ce;                      // ranges in use: min(groups, T)
+    long long t0;                // the range's first tile
+    long long q;
+    int r;
+    __device__ __forceinline__ int group_of(long long t) const
+    {
+        const long long big = r * (q + 1);
+        return (int)(t < big ? t / (q + 1) : r + (t - big) / q);
+    }
 };
 
-// Called by all NT threads of a block; scratch: NT / 32 + 4 long longs of shared memory.
-template <int NT>
-__device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int TS,
-                                                long long *scratch)
+// Called by a converged warp; every warp of a block gets the same range.
+__device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int TS)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = (p.P + NT - 1) / NT;
-    const int q0 = threadIdx.x * per, q1 = min(p.P, q0 + per);
-    const bool check = g == 0 && blockIdx.x == 0;
+    const int lane = threadIdx.x & 31;
+    const int per = (p.P + 31) >> 5;
+    const int q0 = min(p.P, lane * per), q1 = min(p.P, q0 + per);
+    const bool check = blockIdx.x == 0 && threadIdx.x < 32;
     long long sum = 0;
+    int b = q0 / p.Hkv, kh = q0 - b * p.Hkv;
     for (int q = q0; q < q1; ++q) {
-        const int b = q / p.Hkv;
-        sum += tree_tiles(p, tree_len(p, q), tree_count(p, b), TS);
-        if (check) {
-            if (p.len != nullptr) {
-                const int n = p.len[p.len_per_pair ? q : b];
-                if (n < 0 || n > p.cap) record_code(p.dev_code, kDevBadLengthCode);
-            }
-            if (p.count != nullptr && (p.count[b] < 0 || p.count[b] > p.T))
-                record_code(p.dev_code, kDevBadLengthCode);
+        int n = p.n_valid, c = p.T;
+        if (p.len != nullptr) n = p.len[p.len_per_pair ? q : b];
+        if (p.count != nullptr) c = p.count[b];
+        if (check && (n < 0 || n > p.cap || c < 0 || c > p.T)) record_code(p.dev_code, kDevBadLengthCode);
+        n = n < 0 ? 0 : (n > p.cap ? p.cap : n);
+        c = c < 0 ? 0 : (c > p.T ? p.T : c);
+        sum += tree_tiles(p, n, c, TS);
+        if (++kh == p.Hkv) {
+            kh = 0;
+            ++b;
         }
     }
     long long incl = sum;
@@ -82,35 +90,38 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int 
         const long long y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    long long before = incl - sum, T = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before += scratch[w];
-        T += scratch[w];
-    }
+    const long long T = __shfl_sync(0xffffffffu, incl, 31);
     TreeRange r;
-    r.T = T;
-    r.Ce = T < p.groups ? (int)T : p.groups;
-    r.t0 = g < r.Ce ? (long long)g * T / r.Ce : 0;
-    const long long t1 = g < r.Ce ? (long long)(g + 1) * T / r.Ce : 0;
-    r.n = (int)(t1 - r.t0);
-    long long *res = scratch + NT / 32;
-    if (r.n > 0 && before <= r.t0 && r.t0 < before + sum) {
+    if (T <= 0x7fffffff) {                       // (64-bit division is a long subroutine)
+        const unsigned c = (unsigned)p.groups, t = (unsigned)T;
+        r.q = t / c;
+        r.r = (int)(t - (unsigned)r.q * c);
+    } else {
+        r.q = T / p.groups;
+        r.r = (int)(T % p.groups);
+    }
+    r.t0 = g * r.q + min(g, r.r);
+    r.n = (int)(r.q + (g < r.r ? 1 : 0));
+    const long long before = incl - sum;
+    const bool here = r.n > 0 && before <= r.t0 && r.t0 < incl;
+    int q = q0, off = 0, len = 0, cnt = 0;
+    if (here) {
         long long t = before;
-        for (int q = q0; q < q1; ++q) {
-            const int nt = tree_tiles(p, tree_len(p, q), tree_count(p, q / p.Hkv), TS);
-            if (r.t0 < t + nt) {
-                res[0] = q;
-                res[1] = r.t0 - t;
-                break;
-            }
+        for (;; ++q) {
+            len = tree_len(p, q);
+            cnt = tree_count(p, q / p.Hkv);
+            const int nt = tree_tiles(p, len, cnt, TS);
+            if (r.t0 < t + nt || q == q1 - 1) break;
             t += nt;
         }
+        off = (int)(r.t0 - t);
     }
-    __syncthreads();
-    r.pair = r.n > 0 ? (int)res[0] : 0;
-    r.off = r.n > 0 ? (int)res[1] : 0;
+    const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    if (src < 0) r.n = 0;
+    r.pair = __shfl_sync(0xffffffffu, q, src & 31);
+    r.off = __shfl_sync(0xffffffffu, off, src & 31);
+    r.len = __shfl_sync(0xffffffffu, len, src & 31);
+    r.cnt = __shfl_sync(0xffffffffu, cnt, src & 31);
     return r;
 }
 
@@ -138,34 +149,39 @@ struct TreeSeg {
 
 // Walks the pairs of a range in order.
 struct TreeWalk {
-    int pair, off, left;
+    int pair, b, kh, off, left, len, cnt;
     bool first;
-    __device__ __forceinline__ explicit TreeWalk(const TreeRange &r)
-        : pair(r.pair), off(r.off), left(r.n), first(true)
+    __device__ __forceinline__ TreeWalk(const TreeParams &p, const TreeRange &r)
+        : pair(r.pair), b(r.pair / p.Hkv), kh(r.pair - r.pair / p.Hkv * p.Hkv), off(r.off), left(r.n),
+          len(r.len), cnt(r.cnt), first(true)
     {
     }
     __device__ __forceinline__ bool next(const TreeParams &p, int rt, int TS, TreeSeg &s)
     {
         while (left > 0 && pair < p.P) {
-            s.pair = pair;
-            s.b = pair / p.Hkv;
-            s.kh = pair - s.b * p.Hkv;
-            s.len = tree_len(p, pair);
-            s.cnt = tree_count(p, s.b);
-            s.nt = tree_tiles(p, s.len, s.cnt, TS);
-            if (s.nt == 0) {
-                ++pair;
-                off = 0;
-                continue;
+            if (!first) {
+                len = tree_len(p, pair);
+                cnt = tree_count(p, b);
             }
+            s.pair = pair;
+            s.b = b;
+            s.kh = kh;
+            s.len = len;
+            s.cnt = cnt;
+            s.nt = tree_tiles(p, len, cnt, TS);
             s.lo = off;
             s.hi = min(s.nt, off + left);
-            left -= s.hi - s.lo;
-            s.rows = min(p.RP, s.cnt * p.G - rt * p.RP);
+            s.rows = min(p.RP, cnt * p.G - rt * p.RP);
             s.first = first;
-            first = false;
             ++pair;
+            if (++kh == p.Hkv) {
+                kh = 0;
+                ++b;
+            }
             off = 0;
+            if (s.nt == 0) continue;
+            left -= s.hi - s.lo;
+            first = false;
             return true;
         }
         return false;
@@ -179,7 +195,7 @@ __device__ __forceinline__ void tree_note_split(const TreeParams &p, const TreeR
 {
     if (s.lo != 0 || s.hi == s.nt) return;
     const long long last = r.t0 + r.n - s.hi + s.nt - 1;     // the pair's last tile
-    note = make_int4(s.pair, (int)(((last + 1) * r.Ce - 1) / r.T), s.first ? 0 : 1, 0);
+    note = make_int4(s.pair, r.group_of(last), s.first ? 0 : 1, 0);
 }
 
 __device__ __forceinline__ uint64_t tree_mask_word(const TreeParams &p, int b, int t, int cnt)

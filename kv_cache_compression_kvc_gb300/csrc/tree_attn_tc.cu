@@ -20,10 +20,10 @@
 //   The running maximum is lazy: a tile whose logits stay below max + 8 (log2 units) keeps the old
 //   reference, so P stays below 2^8 and O is rescaled only when the maximum really rises.
 //
-// Roles (192 threads): warp 0 issues TMA loads into a ring of units (128 dims x TS slots), warp 1
+// Roles: warp 0 issues TMA loads into a ring of units (128 dims x TS slots), warp 1
 // owns tensor memory and issues the products, one tile ahead for S so that the softmax of a tile
-// overlaps the next tile's Q K^T, warps 2-5 (one per 32 lanes) run the softmax, rescale and write
-// the outputs.  Hand-over by mbarriers; every wait is bounded (see common.cuh): when one gives up
+// overlaps the next tile's Q K^T, the others (sets of four, one warp per 32 lanes and
+// 32 of a tile's slots each) run the softmax, rescale and write the outputs.  Hand-over by mbarriers; every wait is bounded (see common.cuh): when one gives up
 // the block records KVC_DEV_TIMEOUT, stops issuing and walks to its end, waits for its loads and
 // products in flight and frees its tensor memory.
 //
@@ -58,8 +58,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
 
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kSoftmax = 128;                // softmax threads
 constexpr int kBar = 1;                      // their named barrier
 constexpr float kSlack = 8.f;                // lazy maximum, log2 units
 constexpr int kSmemMax = 227 * 1024;
@@ -67,8 +65,12 @@ constexpr int kSmemMax = 227 * 1024;
 // DKP: key width padded to 64; DV: value width; RN: rows of a row tile.
 template <int DKP, int DV, bool LATENT, int RN>
 struct Plan {
+    static constexpr int SM = RN < 64 ? 64 : RN;             // M of S (rows past RN: not used)
     static constexpr int UD = DV < 128 ? 64 : 128;           // dims per ring unit
     static constexpr int TS = LATENT || DV == 256 ? 64 : 128;   // slots per tile
+    static constexpr int SETS = TS / 32;                     // softmax sets of four warps
+    static constexpr int SOFTMAX = 128 * SETS;               // softmax threads
+    static constexpr int THREADS = 64 + SOFTMAX;
     static constexpr int SUB = TS * 128;                     // [TS slots][64 dims]
     static constexpr int SUBS = UD / 64;
     static constexpr int UNIT = SUBS * SUB;
@@ -79,8 +81,8 @@ struct Plan {
     static constexpr int QSUBS = DKP / 64;
     static constexpr int Q_BYTES = QSUBS * RN * 128;
     static constexpr int P_BYTES = TS / 64 * RN * 128;
-    static constexpr int ROPE = LATENT ? SUB : 0;
-    static constexpr int SMALL = 1024 + RN * 4;              // barriers, flags, factors
+    static constexpr int ROPE = LATENT ? 2 * SUB : 0;        // two tiles' rope parts
+    static constexpr int SMALL = 640 + (1 + SETS) * RN * 4;         // barriers, flags, row values
     static constexpr int FIT = (kSmemMax - 1024 - Q_BYTES - P_BYTES - ROPE - SMALL) / UNIT;
     static constexpr int NU = FIT > 16 ? 16 : FIT;           // ring units
     // S of tile t + 1 is issued before the values of tile t are used
@@ -92,16 +94,21 @@ struct Plan {
     static_assert(USED <= 512, "tensor memory");
 };
 
+// Rows are seen as [sub][64]: dimensions {64, slot, sub, head, sequence} for the caches and the
+// drafted rows, {64, head, token, sub} for tree queries and {64, row, sub} for latent ones, so one
+// copy brings all 64-element pieces of a unit.  r*: the rope parts of a latent cache's rows
+// (q, cache, drafts), widths below 64 filled with zeros.
 struct Maps {
-    CUtensorMap q, k, v, kd, vd;
+    CUtensorMap q, k, v, kd, vd, rq, rk, rd;
 };
 
 template <int DKP, int DV, bool LATENT, int RN>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Plan<DKP, DV, LATENT, RN>::THREADS, 1)
 tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
 {
     using PL = Plan<DKP, DV, LATENT, RN>;
     constexpr int TS = PL::TS, NU = PL::NU, KU = PL::KU, PER = PL::PER, MB = PL::MB, UD = PL::UD;
+    constexpr int kSets = PL::SETS, kSoftmax = PL::SOFTMAX;
     constexpr int SUB = PL::SUB, SUBS = PL::SUBS, UNIT = PL::UNIT;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -111,34 +118,35 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     const uint32_t ring = sR + PL::ROPE;
     const uint32_t bars = ring + NU * UNIT;
     const uint32_t b_full = bars, b_empty = b_full + 8 * NU;
-    const uint32_t b_rope_full = b_empty + 8 * NU, b_rope_empty = b_rope_full + 8;
-    const uint32_t b_q_full = b_rope_empty + 8, b_q_empty = b_q_full + 8;
+    const uint32_t b_rope_full = b_empty + 8 * NU, b_rope_empty = b_rope_full + 16;
+    const uint32_t b_q_full = b_rope_empty + 16, b_q_empty = b_q_full + 8;
     const uint32_t b_s_full = b_q_empty + 8, b_s_empty = b_s_full + 16;
     const uint32_t b_p_full = b_s_empty + 16, b_pv = b_p_full + 8, b_done = b_pv + 8;
     const uint32_t tmem_slot = b_done + 8;
     unsigned char *small = smem_raw + (bars - raw) + 512;
-    long long *s_scan = reinterpret_cast<long long *>(small);             // 10
-    unsigned long long *s_nf2 = reinterpret_cast<unsigned long long *>(small + 96);
-    volatile int *s_abort = reinterpret_cast<volatile int *>(small + 112);
+    unsigned long long *s_nf2 = reinterpret_cast<unsigned long long *>(small);
+    volatile int *s_abort = reinterpret_cast<volatile int *>(small + 16);
     float *s_fac = reinterpret_cast<float *>(small + 128);                // RN
-    static_assert(8 * (2 * 16 + 12) + 8 <= 512, "barrier area");
+    float *s_row = s_fac + RN;                                            // [kSets][RN]
+    static_assert(8 * (2 * 16 + 13) + 8 <= 512, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rt = blockIdx.x % p.RT, g = blockIdx.x / p.RT;
+    if (warp == 2 && lane < 8) tc::prefetch_map(&maps.q + lane);
     if (threadIdx.x == 0) {
         for (int i = 0; i < NU; ++i) {
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 1);
         }
-        mbar_init(b_rope_full, 1);
-        mbar_init(b_rope_empty, 1);
         mbar_init(b_q_full, 1);
         mbar_init(b_q_empty, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(b_rope_full + 8 * i, 1);
+            mbar_init(b_rope_empty + 8 * i, 1);
             mbar_init(b_s_full + 8 * i, 1);
-            mbar_init(b_s_empty + 8 * i, 4);
+            mbar_init(b_s_empty + 8 * i, 4 * kSets);
         }
-        mbar_init(b_p_full, 4);
+        mbar_init(b_p_full, 4 * kSets);
         mbar_init(b_pv, 1);
         mbar_init(b_done, 1);
         *s_abort = 0;
@@ -154,8 +162,9 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
 
     pdl_trigger();
     pdl_wait();
-    const TreeRange range = tree_range<kThreads>(p, g, TS, s_scan);
+    const TreeRange range = tree_range(p, g, TS);
 
+    const bool rope = LATENT && p.DK > DV;                   // the keys have a rope part
     auto wait = [&](uint32_t bar, uint32_t parity) {
         if (!mbar_wait_abortable(bar, parity, kMbarSpinLimit, s_abort)) {
             *s_abort = 1;
@@ -171,31 +180,40 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     unsigned n_units = 0, n_tiles = 0, n_segs = 0;           // the producer's counts (for the drain)
     if (warp == 0) {
         // ================================ loads ===================================================
-        TreeWalk walk(range);
+        TreeWalk walk(p, range);
         TreeSeg s;
-        const uint32_t q_bytes = (uint32_t)PL::QSUBS * (LATENT ? RN : p.RP) * 128;
-        const int bx = p.table != nullptr ? min(p.bs, TS) : TS;      // rows of a cache box
+        const bool paged = p.table != nullptr;
+        const int bx = paged ? min(p.bs, TS) : TS;           // slots of a cache copy
+        uint32_t slot = 0, ph = 1;                           // ring position
         while (walk.next(p, rt, TS, s)) {
             if (s.rows <= 0) continue;
-            if (lane == 0) {
-                if (n_segs > 0) wait(b_q_empty, (n_segs - 1) & 1);
-                if (!*s_abort) {
-                    mbar_arrive_expect_tx(b_q_full, q_bytes);
-                    const int y = LATENT ? s.b * p.T * p.Hq + rt * p.RP : s.kh * p.G;
-                    const int z = LATENT ? 0 : s.b * p.T + rt * (p.RP / p.G);
+            if (n_segs > 0) wait(b_q_empty, (n_segs - 1) & 1);
+            if (!*s_abort && tc::elect()) {
+                if constexpr (LATENT) {
+                    const int y = s.b * p.T * p.Hq + rt * RN;
+                    mbar_arrive_expect_tx(b_q_full, (uint32_t)(KU * SUBS + (rope ? 1 : 0)) * RN * 128);
+                    tc::tma_5d(sQ, &maps.q, 0, y, 0, 0, 0, b_q_full);
+                    if (rope) tc::tma_5d(sQ + KU * SUBS * RN * 128, &maps.rq, 0, y, 0, 0, 0, b_q_full);
+                } else {
+                    const int t0 = s.b * p.T + rt * (p.RP / p.G);
+                    mbar_arrive_expect_tx(b_q_full, (uint32_t)PL::QSUBS * p.RP * 128);
+#pragma unroll
                     for (int i = 0; i < PL::QSUBS; ++i)
-                        tc::tma_4d(sQ + i * RN * 128, &maps.q, i * 64, y, z, 0, b_q_full);
+                        tc::tma_5d(sQ + i * RN * 128, &maps.q, 0, s.kh * p.G, t0, i, 0, b_q_full);
                 }
             }
+            __syncwarp();
             ++n_segs;
             for (int tile = s.lo; tile < s.hi; ++tile, ++n_tiles) {
                 const bool draft = s.is_draft(p, tile);
                 const int valid = s.valid(p, tile, TS);
+                const int y = draft ? 0 : tile * TS;
                 // page of this lane (paged caches): row of its first slot in the pool
                 int page_row = 0, pages = 1;
-                if (p.table != nullptr && !draft && valid > 0) {
+                const bool by_page = paged && !draft;
+                if (by_page) {
                     pages = p.bs < TS ? (valid + p.bs - 1) / p.bs : 1;
-                    if (lane < pages) {
+                    if (lane < pages && valid > 0) {
                         const int lb = tile * TS / p.bs + lane;
                         int blk = __ldg(p.table + (size_t)s.b * p.max_blocks + lb);
                         if (blk < 0 || blk >= p.n_pool) {
@@ -206,147 +224,211 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                                    (p.bs > TS ? tile * TS % p.bs : 0);
                     }
                 }
-                const int rows = draft ? 64 : bx * pages;
-                if (LATENT && lane == 0) {
-                    if (n_tiles > 0) wait(b_rope_empty, (n_tiles - 1) & 1);
-                    if (valid == 0) mbar_arrive(b_rope_full);
-                    else if (!*s_abort) {
-                        mbar_arrive_expect_tx(b_rope_full, (uint32_t)rows * 128);
-                        if (draft) tc::tma_4d(sR, &maps.kd, DV, 0, 0, s.b, b_rope_full);
-                        else tc::tma_4d(sR, &maps.k, DV, tile * TS, 0, s.b, b_rope_full);
-                    }
-                }
-                for (int u = 0; u < PER; ++u, ++n_units) {
-                    const uint32_t slot = n_units % NU;
-                    const uint32_t bar = b_full + 8 * slot, dst = ring + slot * UNIT;
-                    if (lane == 0) {
-                        if (n_units >= NU) wait(b_empty + 8 * slot, (n_units / NU - 1) & 1);
-                        if (valid == 0) mbar_arrive(bar);
-                        else if (!*s_abort) mbar_arrive_expect_tx(bar, (uint32_t)rows * 128 * SUBS);
-                    }
-                    __syncwarp();
-                    if (valid == 0 || *s_abort) continue;
-                    const bool isv = u >= KU;
-                    const int x = (isv ? u - KU : u) * UD;
-                    if (draft || p.table == nullptr) {
-                        if (lane == 0) {
-#pragma unroll
-                            for (int i = 0; i < SUBS; ++i) {
-                                if (draft)
-                                    tc::tma_4d(dst + i * SUB, isv ? &maps.vd : &maps.kd, x + i * 64,
-                                               s.kh, 0, s.b, bar);
-                                else
-                                    tc::tma_4d(dst + i * SUB, isv ? &maps.v : &maps.k, x + i * 64,
-                                               tile * TS, s.kh, s.b, bar);
-                            }
+                const bool go = !*s_abort;
+                const uint32_t bytes = (draft ? TS : bx * pages) * 128u;   // of a 64-wide piece
+                if (rope) {
+                    const uint32_t r = n_tiles & 1;
+                    if (n_tiles >= 2) wait(b_rope_empty + 8 * r, ((n_tiles >> 1) - 1) & 1);
+                    if (go && tc::elect()) {
+                        if (valid == 0) mbar_arrive(b_rope_full + 8 * r);
+                        else {
+                            mbar_arrive_expect_tx(b_rope_full + 8 * r, bytes);
+                            tc::tma_5d(sR + r * SUB, draft ? &maps.rd : &maps.rk, 0, y, 0, 0, s.b,
+                                       b_rope_full + 8 * r);
                         }
-                    } else if (lane < pages) {
-#pragma unroll
-                        for (int i = 0; i < SUBS; ++i)
-                            tc::tma_4d(dst + i * SUB + lane * bx * 128, isv ? &maps.v : &maps.k,
-                                       x + i * 64, page_row, 0, 0, bar);
                     }
                     __syncwarp();
+                }
+#pragma unroll 1
+                for (int u = 0; u < PER; ++u, ++n_units) {
+                    const uint32_t bar = b_full + 8 * slot, dst = ring + slot * UNIT;
+                    const bool isv = u >= KU;
+                    const int sub = (isv ? u - KU : u) * SUBS;
+                    if (n_units >= NU) wait(b_empty + 8 * slot, ph);
+                    if (go && tc::elect()) {
+                        if (valid == 0) mbar_arrive(bar);
+                        else mbar_arrive_expect_tx(bar, bytes * SUBS);
+                        if (valid > 0 && !by_page)
+                            tc::tma_5d(dst, draft ? (isv ? &maps.vd : &maps.kd) : (isv ? &maps.v : &maps.k),
+                                       0, y, sub, s.kh, s.b, bar);
+                    }
+                    __syncwarp();
+                    if (by_page && go && valid > 0) {
+                        for (int i = 0; i < pages; ++i) {
+                            const int row = __shfl_sync(0xffffffffu, page_row, i);
+                            if (tc::elect()) {
+#pragma unroll
+                                for (int c = 0; c < SUBS; ++c)
+                                    tc::tma_5d(dst + c * SUB + i * bx * 128, isv ? &maps.v : &maps.k, 0,
+                                               row, sub + c, 0, 0, bar);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (++slot == NU) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
                 }
             }
         }
     } else if (warp == 1) {
         // ================================ products ================================================
-        if (lane == 0) {
-            constexpr uint32_t id_s = tc::idesc(RN, TS, false);
-            constexpr uint32_t id_o = tc::idesc(UD, RN, true);
-            TreeWalk walk(range);
-            TreeSeg s, nx;
-            auto next_seg = [&](TreeSeg &x) {
-                while (walk.next(p, rt, TS, x))
-                    if (x.rows > 0) return true;
-                return false;
-            };
-            unsigned seg_no = 0;                             // segments whose S has begun
-            auto scores = [&](const TreeSeg &x, int tile, unsigned n) {
-                const uint32_t buf = n & 1;
-                if (n >= 2) wait(b_s_empty + 8 * buf, ((n >> 1) - 1) & 1);
-                if (tile == x.lo) {
-                    wait(b_q_full, seg_no & 1);
-                    ++seg_no;
-                }
-                const uint32_t d = tS + buf * TS;
-                if constexpr (LATENT) {
-                    wait(b_rope_full, n & 1);
-                    tc::fence_after();
+        constexpr uint32_t id_s = tc::idesc(PL::SM, TS, false);
+        constexpr uint32_t id_o = tc::idesc(UD, RN, true);
+        TreeWalk walk(p, range);
+        TreeSeg s, nx;
+        auto next_seg = [&](TreeSeg &x) {
+            while (walk.next(p, rt, TS, x))
+                if (x.rows > 0) return true;
+            return false;
+        };
+        unsigned seg_no = 0;                                 // segments whose S has begun
+        uint32_t k_slot = 0, k_ph = 0, v_slot = LATENT ? 0 : KU, v_ph = 0;   // ring positions
+        auto step = [&](uint32_t &slot, uint32_t &ph, uint32_t by) {
+            slot += by;
+            if (slot >= NU) {
+                slot -= NU;
+                ph ^= 1;
+            }
+        };
+        auto scores = [&](const TreeSeg &x, int tile, unsigned n) {
+            const uint32_t buf = n & 1;
+            if (n >= 2) wait(b_s_empty + 8 * buf, ((n >> 1) - 1) & 1);
+            if (tile == x.lo) {
+                wait(b_q_full, seg_no & 1);
+                ++seg_no;
+            }
+            // every unit has arrived, then one block of products: each wait, fence and pick of a
+            // lane between products costs the tensor cores about 300 clocks
+            uint32_t src[KU], bar[KU];
+            if (rope) wait(b_rope_full + 8 * buf, (n >> 1) & 1);
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                wait(b_full + 8 * k_slot, k_ph);
+                src[u] = ring + k_slot * UNIT;
+                bar[u] = b_empty + 8 * k_slot;
+                step(k_slot, k_ph, 1);
+            }
+            tc::fence_after();
+            const uint32_t d = tS + buf * TS;
+            if (tc::elect()) {
+                if (rope) {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         tc::mma(d, tc::desc_k(sQ + KU * SUBS * RN * 128 + kk * 32),
-                                tc::desc_k(sR + kk * 32), id_s, kk > 0);
-                    tc::commit(b_rope_empty);
+                                tc::desc_k(sR + buf * SUB + kk * 32), id_s, kk > 0);
+                    tc::commit(b_rope_empty + 8 * buf);
                 }
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
-                    const unsigned un = n * PER + u;
-                    const uint32_t slot = un % NU, src = ring + slot * UNIT;
-                    wait(b_full + 8 * slot, (un / NU) & 1);
-                    tc::fence_after();
 #pragma unroll
                     for (int i = 0; i < SUBS; ++i)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             tc::mma(d, tc::desc_k(sQ + (u * SUBS + i) * RN * 128 + kk * 32),
-                                    tc::desc_k(src + i * SUB + kk * 32), id_s,
-                                    LATENT || u > 0 || i > 0 || kk > 0);
-                    if (!LATENT) tc::commit(b_empty + 8 * slot);
+                                    tc::desc_k(src[u] + i * SUB + kk * 32), id_s,
+                                    rope || u > 0 || i > 0 || kk > 0);
+                    if (!LATENT) tc::commit(bar[u]);
                 }
                 tc::commit(b_s_full + 8 * buf);
                 if (tile == x.hi - 1) tc::commit(b_q_empty);
-            };
-            unsigned n = 0;
-            bool have = next_seg(s);
-            int tile = have ? s.lo : 0;
-            if (have) scores(s, tile, 0);
-            while (have) {
-                const bool more_here = tile + 1 < s.hi;
-                if (more_here) scores(s, tile + 1, n + 1);
-                // O^T += V^T P^T
-                const int steps = steps_of(s, tile);
-                wait(b_p_full, n & 1);
-                tc::fence_after();
+            }
+            __syncwarp();
+            if (!LATENT) step(k_slot, k_ph, KU);             // past the values
+        };
+        unsigned n = 0;
+        bool have = next_seg(s);
+        int tile = have ? s.lo : 0;
+        if (have) scores(s, tile, 0);
+        while (have) {
+            const bool more_here = tile + 1 < s.hi;
+            // the next tile's S goes first, so that its softmax overlaps these values' product;
+            // with a ring of two tiles only if it has arrived, since waiting for it here would
+            // hold up the product that frees the ring
+            bool ahead = more_here;
+            if (NU < 3 * PER && more_here) {
+                uint32_t last = k_slot + KU - 1, ph = k_ph;
+                if (last >= NU) {
+                    last -= NU;
+                    ph ^= 1;
+                }
+                ahead = __shfl_sync(0xffffffffu, (int)tc::test(b_full + 8 * last, ph), 0) != 0;
+            }
+            if (ahead) scores(s, tile + 1, n + 1);
+            // O^T += V^T P^T
+            const int steps = steps_of(s, tile);
+            uint32_t src[MB], bar[MB];
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                if (!LATENT) wait(b_full + 8 * v_slot, v_ph);
+                src[m] = ring + v_slot * UNIT;
+                bar[m] = b_empty + 8 * v_slot;
+                step(v_slot, v_ph, 1);
+            }
+            wait(b_p_full, n & 1);
+            tc::fence_after();
+            if (tc::elect()) {
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
-                    const unsigned un = n * PER + (LATENT ? 0 : KU) + m;
-                    const uint32_t slot = un % NU, src = ring + slot * UNIT;
-                    wait(b_full + 8 * slot, (un / NU) & 1);
-                    tc::fence_after();
-                    for (int ks = 0; ks < steps; ++ks)
-                        tc::mma(tO + m * RN, tc::desc(src + ks * 2048, SUB, 1024),
-                                tc::desc_k(sP + (ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
-                                tile > s.lo || ks > 0);
-                    tc::commit(b_empty + 8 * slot);
+#pragma unroll
+                    for (int ks = 0; ks < TS / 16; ++ks)
+                        if (ks < steps)
+                            tc::mma(tO + m * RN, tc::desc(src[m] + ks * 2048, SUB, 1024),
+                                    tc::desc_k(sP + (ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
+                                    tile > s.lo || ks > 0);
+                    tc::commit(bar[m]);
                 }
                 tc::commit(b_pv);
-                ++n;
-                ++tile;
-                if (!more_here) {
-                    have = next_seg(nx);
-                    if (have) {
-                        s = nx;
-                        tile = s.lo;
-                        scores(s, tile, n);
-                    }
+            }
+            __syncwarp();
+            if (!LATENT) step(v_slot, v_ph, KU);             // past the next tile's keys
+            if (more_here && !ahead) scores(s, tile + 1, n + 1);
+            ++n;
+            ++tile;
+            if (!more_here) {
+                have = next_seg(nx);
+                if (have) {
+                    s = nx;
+                    tile = s.lo;
+                    scores(s, tile, n);
                 }
             }
         }
     } else {
         // ================================ softmax, outputs ========================================
+        // Set i takes slots 32 i .. 32 i + 31 of a tile: a row has a thread in each set, which keep
+        // the same maximum and their own part of the sum.
+        constexpr int HC = 32;
+        const int set = (warp - 2) / 4;
         const int q4 = warp & 3;                             // lanes 32 q4 .. of tensor memory
-        const int tw = q4 * 32 + lane;                       // 0..127
+        const int ln = q4 * 32 + lane;                       // 0..127
+        const int tw = set * 128 + ln;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         // the row of S (M = RN) and the dimension of O^T (M = UD) this thread's lane holds
-        const int row = RN == 128 ? tw : (lane < 16 ? q4 * 16 + lane : RN);
-        const int dim = UD == 128 ? tw : (lane < 16 ? q4 * 16 + lane : UD);
+        const int row = RN == 128 ? ln : (lane < 16 ? q4 * 16 + lane : 64);
+        const int dim = UD == 128 ? ln : (lane < 16 ? q4 * 16 + lane : UD);
         const int row_lo = RN == 128 ? q4 * 32 : q4 * 16;    // first row of this warp
-        TreeWalk walk(range);
+        const int c0 = set * HC;                             // first slot
+        // what a row of token t gets in dimension d from the drafted tokens whose values are not
+        // finite (bits of nf): those that it sees, as they are
+        auto stray = [&](unsigned long long nf, int t, int d, const TreeSeg &x) -> float {
+            float y = 0.f;
+            unsigned long long hit = nf & tree_mask_word(p, x.b, t, x.cnt);
+            while (hit) {
+                const int i = __ffsll((long long)hit) - 1;
+                hit &= hit - 1;
+                const float z = __bfloat162float(static_cast<const __nv_bfloat16 *>(
+                    p.vd)[(((size_t)x.b * p.T + i) * p.Hkv + x.kh) * p.DK + d]);
+                if (!(fabsf(z) <= 3.402823466e38f)) y += z;
+            }
+            return y;
+        };
+        TreeWalk walk(p, range);
         TreeSeg s;
         int4 note = make_int4(-1, 0, 0, 0);
         unsigned n = 0, seg_no = 0;
+        uint32_t v_unit = LATENT ? 0 : KU;                   // this tile's first value unit
         while (walk.next(p, rt, TS, s)) {
             tree_note_split(p, range, g, s, note);
             if (s.rows <= 0) continue;
@@ -355,87 +437,104 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             const int r0 = rt * p.RP;
             float m = kNegBig, l = 0.f;
             bool drafts = false;
+            const uint64_t word = mine ? tree_mask_word(p, s.b, (r0 + row) / p.G, s.cnt) : 0ull;
             // drafted tokens with non-finite values: alternate words, since a thread may set up
             // the next pair's while another still reads this one's
             unsigned long long *s_nf = s_nf2 + (seg_no++ & 1);
-            for (int tile = s.lo; tile < s.hi; ++tile, ++n) {
+            for (int tile = s.lo; tile < s.hi; ++tile, ++n, v_unit += PER) {
                 const bool draft = s.is_draft(p, tile);
                 const int valid = s.valid(p, tile, TS);
                 const uint32_t buf = n & 1;
-                float x[TS];
-                float mx = -INFINITY;
+                float x[HC];
+                float mx = -INFINITY, scale = p.scale_log2;
                 wait(b_s_full + 8 * buf, (n >> 1) & 1);
                 tc::fence_after();
                 if (any) {
 #pragma unroll
-                    for (int c = 0; c < TS; c += 32) tc::ld32(tS + buf * TS + lanes + c, x + c);
+                    for (int c = 0; c < HC; c += 32) tc::ld32(tS + buf * TS + lanes + c0 + c, x + c);
                     tc::wait_ld();
                 }
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_s_empty + 8 * buf);
                 if (any) {
+                    if (draft || valid < TS) {               // masked: scaled here, once
+                        uint32_t see;                        // slots c0 .. c0 + 31
+                        if (draft) see = set == 0 ? (uint32_t)word : set == 1 ? (uint32_t)(word >> 32) : 0u;
+                        else see = valid - c0 >= 32 ? ~0u : valid > c0 ? (1u << (valid - c0)) - 1u : 0u;
 #pragma unroll
-                    for (int c = 0; c < TS; ++c) x[c] *= p.scale_log2;
-                    if (draft) {
-                        const uint64_t see =
-                            mine ? tree_mask_word(p, s.b, (r0 + row) / p.G, s.cnt) : 0ull;
-#pragma unroll
-                        for (int c = 0; c < TS; ++c)
-                            if (c >= 64 || !((see >> (c & 63)) & 1ull)) x[c] = -INFINITY;
-                    } else if (valid < TS) {
-#pragma unroll
-                        for (int c = 0; c < TS; ++c)
-                            if (c >= valid) x[c] = -INFINITY;
+                        for (int c = 0; c < HC; ++c)
+                            x[c] = (see >> c) & 1u ? x[c] * scale : -INFINITY;
+                        scale = 1.f;
                     }
-                    float a0 = x[0], a1 = x[1], a2 = x[2], a3 = x[3];
+                    // the largest scaled logit: of the smallest value when the scale is negative
+                    float a[4] = {x[0], x[1], x[2], x[3]};
+                    if (scale >= 0.f) {
 #pragma unroll
-                    for (int c = 4; c < TS; c += 4) {
-                        a0 = fmaxf(a0, x[c]);
-                        a1 = fmaxf(a1, x[c + 1]);
-                        a2 = fmaxf(a2, x[c + 2]);
-                        a3 = fmaxf(a3, x[c + 3]);
+                        for (int c = 4; c < HC; ++c) a[c & 3] = fmaxf(a[c & 3], x[c]);
+                        mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * scale;
+                    } else {
+#pragma unroll
+                        for (int c = 4; c < HC; ++c) a[c & 3] = fminf(a[c & 3], x[c]);
+                        mx = fminf(fminf(a[0], a[1]), fminf(a[2], a[3])) * scale;
                     }
-                    mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3));
                 }
                 if (draft && tw == 0) *s_nf = 0ull;          // ordered by the barrier below
                 if (tc::bar_any(kBar, kSoftmax, mine && mx > m + kSlack)) {
-                    const float m_new = fmaxf(m, mx);
+                    // the maximum rises: agree on it, then bring l and O to it
+                    if (row < RN) s_row[set * RN + row] = mx;
+                    tc::bar_sync(kBar, kSoftmax);
+                    float m_new = m;
+                    if (row < RN) {
+#pragma unroll
+                        for (int i = 0; i < kSets; ++i) m_new = fmaxf(m_new, s_row[i * RN + row]);
+                    }
                     const float f = ex2(m - m_new);
                     m = m_new;
                     l *= f;
                     if (tile > s.lo) {
-                        if (row < RN) s_fac[row] = f;
+                        if (set == 0 && row < RN) s_fac[row] = f;
                         wait(b_pv, (n - 1) & 1);
                         tc::fence_after();
                         tc::bar_sync(kBar, kSoftmax);
 #pragma unroll 1
-                        for (int c = 0; c < MB * RN; c += 32) {
+                        for (int c = set * 16; c < MB * RN; c += 16 * kSets) {
                             if ((c & (RN - 1)) >= s.rows) continue;
-                            float o[32];
-                            tc::ld32(tO + lanes + c, o);
+                            float o[16];
+                            tc::ld16(tO + lanes + c, o);
                             tc::wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] *= s_fac[(c & (RN - 1)) + j];
-                            tc::st32(tO + lanes + c, o);
+                            for (int j = 0; j < 16; ++j) o[j] *= s_fac[(c & (RN - 1)) + j];
+                            tc::st16(tO + lanes + c, o);
                         }
                         tc::wait_st();
                     }
                 }
                 if (any) {
+                    const float2 sc = make_float2(scale, scale), mm = make_float2(-m, -m);
+                    float2 z0 = make_float2(0.f, 0.f), z1 = z0;
 #pragma unroll
-                    for (int c = 0; c < TS; ++c) {
-                        x[c] = ex2(x[c] - m);
-                        l += x[c];
+                    for (int c = 0; c < HC; c += 4) {
+                        float2 y0 = __ffma2_rn(make_float2(x[c], x[c + 1]), sc, mm);
+                        float2 y1 = __ffma2_rn(make_float2(x[c + 2], x[c + 3]), sc, mm);
+                        x[c] = y0.x = ex2(y0.x);
+                        x[c + 1] = y0.y = ex2(y0.y);
+                        x[c + 2] = y1.x = ex2(y1.x);
+                        x[c + 3] = y1.y = ex2(y1.y);
+                        z0 = __fadd2_rn(z0, y0);
+                        z1 = __fadd2_rn(z1, y1);
                     }
+                    z0 = __fadd2_rn(z0, z1);
+                    l += z0.x + z0.y;
                 }
                 if (n > 0) wait(b_pv, (n - 1) & 1);          // P of the previous tile is used up
                 if (any && row < RN) {
 #pragma unroll
-                    for (int c = 0; c < TS / 8; ++c) {       // 16-byte chunks of the row
+                    for (int c = 0; c < HC / 8; ++c) {       // 16-byte chunks of the row
                         const float *y = x + 8 * c;
-                        tc::st_shared_16(sP + (c >> 3) * RN * 128 + row * 128 +
-                                             (((c & 7) ^ (row & 7)) << 4),
+                        const int k = c0 / 8 + c;
+                        tc::st_shared_16(sP + (k >> 3) * RN * 128 + row * 128 +
+                                             (((k & 7) ^ (row & 7)) << 4),
                                          tc::pack_bf16(y[0], y[1]), tc::pack_bf16(y[2], y[3]),
                                          tc::pack_bf16(y[4], y[5]), tc::pack_bf16(y[6], y[7]));
                     }
@@ -444,20 +543,19 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 const int depth = steps_of(s, tile) * 16;
                 if (valid < depth || draft) {
                     for (int u = 0; u < MB; ++u) {
-                        const unsigned un = n * PER + (LATENT ? 0 : KU) + u;
+                        const unsigned un = v_unit + u;
                         const uint32_t slot = un % NU;
                         wait(b_full + 8 * slot, (un / NU) & 1);
                         unsigned char *base = smem_raw + (ring + slot * UNIT - raw);
-                        for (int i = tw; i < SUBS * (depth - valid) * 8; i += kSoftmax) {
-                            const int sub = i / ((depth - valid) * 8), k = i % ((depth - valid) * 8);
-                            *reinterpret_cast<uint4 *>(base + sub * SUB + valid * 128 + k * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
+                        // a warp takes a row: eight lanes per 64 dims
+                        const int sub = lane >> 3;
+                        uint4 *at = reinterpret_cast<uint4 *>(base + sub * SUB + (lane & 7) * 16);
+                        for (int r = valid + warp - 2; r < depth; r += kSoftmax / 32)
+                            if (sub < SUBS) at[r * 8] = make_uint4(0, 0, 0, 0);
                         if (draft) {
-                            for (int i = tw; i < SUBS * valid * 8; i += kSoftmax) {
-                                const int sub = i / (valid * 8), k = i % (valid * 8);
-                                uint4 *at = reinterpret_cast<uint4 *>(base + sub * SUB + k * 16);
-                                uint4 w = *at;
+                            for (int r = warp - 2; r < valid; r += kSoftmax / 32) {
+                                if (sub >= SUBS) continue;
+                                uint4 w = at[r * 8];
                                 uint32_t bad = 0;
                                 auto fix = [&](uint32_t y) {
                                     if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u, bad = 1;
@@ -466,8 +564,8 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                                 };
                                 w.x = fix(w.x); w.y = fix(w.y); w.z = fix(w.z); w.w = fix(w.w);
                                 if (bad) {
-                                    *at = w;
-                                    atomicOr(s_nf, 1ull << (k >> 3));
+                                    at[r * 8] = w;
+                                    atomicOr(s_nf, 1ull << r);
                                 }
                             }
                         }
@@ -482,59 +580,69 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             // this part's outputs: O^T / l, or the partial state
             const bool whole = s.whole();
             const size_t part = (size_t)blockIdx.x * 2 + (s.first ? 0 : 1);
-            if (mine) {
-                const int t = (r0 + row) / p.G, h = s.kh * p.G + (r0 + row) % p.G;
-                if (!whole) {
-                    p.ws_ml[(part * RN + row) * 2] = m;
-                    p.ws_ml[(part * RN + row) * 2 + 1] = l;
-                } else if (p.lse != nullptr) {
-                    p.lse[((size_t)s.b * p.T + t) * p.Hq + h] =
-                        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-                }
-            }
             wait(b_pv, (n - 1) & 1);                         // every warp is past its last rescaling
             tc::fence_after();
-            if (row < RN) s_fac[row] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+            if (set > 0 && row < RN) s_row[set * RN + row] = l;
+            tc::bar_sync(kBar, kSoftmax);
+            if (set == 0 && row < RN) {
+#pragma unroll
+                for (int i = 1; i < kSets; ++i) l += s_row[i * RN + row];
+                s_fac[row] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                if (mine) {
+                    const int t = (r0 + row) / p.G, h = s.kh * p.G + (r0 + row) % p.G;
+                    if (!whole) {
+                        p.ws_ml[(part * RN + row) * 2] = m;
+                        p.ws_ml[(part * RN + row) * 2 + 1] = l;
+                    } else if (p.lse != nullptr) {
+                        p.lse[((size_t)s.b * p.T + t) * p.Hq + h] =
+                            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    }
+                }
+            }
             tc::bar_sync(kBar, kSoftmax);
             const unsigned long long nf = drafts ? *s_nf : 0ull;
 #pragma unroll 1
-            for (int c = 0; c < MB * RN; c += 32) {
+            for (int c = set * 16; c < MB * RN; c += 16 * kSets) {
                 const int ra = c & (RN - 1);                 // first row of these columns
                 if (ra >= s.rows) continue;
                 const int d = c / RN * UD + dim;
-                float o[32];
-                tc::ld32(tO + lanes + c, o);
+                const int here = min(16, s.rows - ra);
+                float o[16];
+                __syncwarp();
+                tc::ld16(tO + lanes + c, o);
                 tc::wait_ld();
                 if (dim >= UD) continue;
-                int t = (r0 + ra) / p.G, hg = (r0 + ra) % p.G;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (ra + j < s.rows) {
-                        float y = o[j] * s_fac[ra + j];
-                        if (nf) {
-                            unsigned long long hit = nf & tree_mask_word(p, s.b, t, s.cnt);
-                            while (hit) {
-                                const int i = __ffsll((long long)hit) - 1;
-                                hit &= hit - 1;
-                                const float z = __bfloat162float(
-                                    static_cast<const __nv_bfloat16 *>(
-                                        p.vd)[(((size_t)s.b * p.T + i) * p.Hkv + s.kh) * p.DK + d]);
-                                if (!(fabsf(z) <= 3.402823466e38f)) y += z;
-                            }
-                        }
-                        if (whole) {
-                            const size_t at = ((size_t)s.b * p.T + t) * p.Hq + s.kh * p.G + hg;
-                            static_cast<__nv_bfloat16 *>(p.out)[at * DV + d] = __float2bfloat16(y);
-                        } else {
-                            p.ws_o[(part * RN + ra + j) * DV + d] = y;
-                        }
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(s_fac + ra + j);
+                    o[j] *= f.x; o[j + 1] *= f.y; o[j + 2] *= f.z; o[j + 3] *= f.w;
+                }
+                int t = (r0 + ra) / p.G, hg = (r0 + ra) - t * p.G;
+                if (nf) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < here) o[j] += stray(nf, (r0 + ra + j) / p.G, d, s);
+                }
+                if (whole) {
+                    __nv_bfloat16 *dst =
+                        static_cast<__nv_bfloat16 *>(p.out) +
+                        (((size_t)s.b * p.T + t) * p.Hq + s.kh * p.G + hg) * DV + d;
+                    const int wrap = (p.Hq - p.G + 1) * DV;  // to the next token's first head
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (j < here) *dst = __float2bfloat16(o[j]);
+                        ++hg;
+                        dst += hg == p.G ? wrap : DV;
+                        hg = hg == p.G ? 0 : hg;
                     }
-                    if (++hg == p.G) {
-                        hg = 0;
-                        ++t;
-                    }
+                } else {
+                    float *dst = p.ws_o + (part * RN + ra) * DV + d;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < here) dst[j * DV] = o[j];
                 }
             }
+            __syncwarp();
             tc::fence_before();
         }
         if (rt == 0 && tw == 0) p.ws_info[g] = note;
@@ -551,10 +659,12 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             };
             for (unsigned i = n_units > NU ? n_units - NU : 0; i < n_units; ++i)
                 drain(b_full + 8 * (i % NU), (i / NU) & 1);
-            if (LATENT && n_tiles > 0) drain(b_rope_full, (n_tiles - 1) & 1);
+            for (unsigned i = n_tiles > 2 ? n_tiles - 2 : 0; rope && i < n_tiles; ++i)
+                drain(b_rope_full + 8 * (i & 1), (i >> 1) & 1);
             if (n_segs > 0) drain(b_q_full, (n_segs - 1) & 1);
-        } else if (threadIdx.x == 32) {
-            tc::commit(b_done);
+        } else if (warp == 1) {
+            if (tc::elect()) tc::commit(b_done);
+            __syncwarp();
             mbar_wait_ok(b_done, 0, kMbarSpinLimit);
         }
         __syncthreads();
@@ -578,7 +688,7 @@ cudaError_t launch_typed(const TreeParams &p, const Maps &maps, cudaStream_t str
         configured[dev] = true;
     }
     return launch_pdl(tree_tc_kernel<DKP, DV, LATENT, RN>, dim3((unsigned)(p.groups * p.RT)),
-                      dim3(kThreads), PL::SMEM, stream, maps, p);
+                      dim3(PL::THREADS), PL::SMEM, stream, maps, p);
 }
 
 int tile_slots(int D) { return D == 256 ? 64 : 128; }
@@ -595,42 +705,60 @@ cudaError_t launch_tree_attn_tc(const TreeParams &p, cudaStream_t stream, bool *
 {
     *used = false;
     Maps maps;
-    const uint64_t dk = (uint64_t)p.DK, row = dk * 2;
-    const uint64_t B = p.B, T = p.T, Hq = p.Hq, Hkv = p.Hkv;
+    const uint64_t row = (uint64_t)p.DK * 2;
+    const uint64_t B = p.B, T = p.T, Hq = p.Hq, Hkv = p.Hkv, subs = p.DV / 64;
     const int TS = p.latent ? 64 : tile_slots(p.DV);
-    if (B * T * Hq > 0x7fffffffull) return cudaSuccess;
-    bool ok = p.latent ? tc::encode_4d(&maps.q, p.q, {dk, B * T * Hq, 1, 1},
-                                       {row, row * B * T * Hq, row * B * T * Hq}, p.RN, 1)
-                       : tc::encode_4d(&maps.q, p.q, {dk, Hq, B * T, 1},
-                                       {row, row * Hq, row * Hq * B * T}, p.G, p.RP / p.G);
+    const int units = p.DV < 128 ? 1 : 2;                    // 64-wide pieces of a ring unit
+    const uint64_t ss = (uint64_t)p.ss * 2, sb = (uint64_t)p.sb * 2;
     auto cache = [&](CUtensorMap *m, const void *ptr) {
         if (p.table != nullptr) {
             const uint64_t rows = Hkv * (uint64_t)p.n_pool * p.bs;
-            if (rows > 0x7fffffffull) return false;
-            return tc::encode_4d(m, ptr, {dk, rows, 1, 1}, {row, row * rows, row * rows},
-                                 p.bs < TS ? p.bs : TS, 1);
+            return tc::encode_5d(m, ptr, {64, rows, subs, 1, 1}, {row, 128, row * rows, row * rows},
+                                 p.bs < TS ? p.bs : TS, 1, 1);
         }
         const uint64_t sh = p.latent ? row : (uint64_t)p.sh * 2;
-        return tc::encode_4d(m, ptr, {dk, (uint64_t)p.cap, Hkv, B},
-                             {(uint64_t)p.ss * 2, sh, (uint64_t)p.sb * 2}, TS, 1);
+        return tc::encode_5d(m, ptr, {64, (uint64_t)p.cap, subs, Hkv, B}, {ss, 128, sh, sb}, TS, units, 1);
     };
     auto drafted = [&](CUtensorMap *m, const void *ptr) {
-        return tc::encode_4d(m, ptr, {dk, Hkv, T, B}, {row, row * Hkv, row * Hkv * T}, 1, 64);
+        return tc::encode_5d(m, ptr, {64, T, subs, Hkv, B}, {row * Hkv, 128, row, row * Hkv * T}, TS,
+                             units, 1);
     };
-    ok = ok && cache(&maps.k, p.k);
-    maps.v = maps.kd = maps.vd = maps.k;
-    if (ok && !p.latent) ok = cache(&maps.v, p.v);
-    if (ok && p.kd != nullptr) {
-        ok = drafted(&maps.kd, p.kd);
-        if (ok && !p.latent) ok = drafted(&maps.vd, p.vd);
+    bool ok = cache(&maps.k, p.k);
+    if (ok && p.latent) {
+        const uint64_t rows = B * T * Hq, all = row * rows, E = p.DK - p.DV;
+        ok = tc::encode_5d(&maps.q, p.q, {64, rows, subs, 1, 1}, {row, 128, all, all}, p.RN, (uint32_t)subs, 1);
+        const auto part = [&](const void *ptr) { return static_cast<const char *>(ptr) + p.DV * 2; };
+        if (ok && E > 0)
+            ok = tc::encode_5d(&maps.rq, part(p.q), {E, rows, 1, 1, 1}, {row, all, all, all}, p.RN, 1, 1) &&
+                 tc::encode_5d(&maps.rk, part(p.k), {E, (uint64_t)p.cap, 1, 1, B}, {ss, row, row, sb}, TS, 1, 1);
+        else if (ok)
+            maps.rq = maps.q, maps.rk = maps.k;
+        maps.kd = maps.vd = maps.v = maps.rd = maps.k;
+        if (ok && p.kd != nullptr) {
+            ok = drafted(&maps.kd, p.kd);
+            if (ok && E > 0)
+                ok = tc::encode_5d(&maps.rd, part(p.kd), {E, T, 1, 1, B}, {row, row, row, row * T}, TS, 1, 1);
+        }
+    } else if (ok) {
+        ok = tc::encode_5d(&maps.q, p.q, {64, Hq, B * T, subs, 1}, {row, row * Hq, 128, row * Hq * B * T},
+                           p.G, p.RP / p.G, 1) &&
+             cache(&maps.v, p.v);
+        maps.kd = maps.vd = maps.rq = maps.rk = maps.rd = maps.k;
+        if (ok && p.kd != nullptr) ok = drafted(&maps.kd, p.kd) && drafted(&maps.vd, p.vd);
     }
     if (!ok) return cudaSuccess;
     *used = true;
     if (p.latent) {
         switch (p.DV) {
-        case 128: return launch_typed<192, 128, true, 64>(p, maps, stream);
-        case 256: return launch_typed<320, 256, true, 64>(p, maps, stream);
-        default: return launch_typed<576, 512, true, 64>(p, maps, stream);
+        case 128:
+            return p.RN == 32 ? launch_typed<192, 128, true, 32>(p, maps, stream)
+                              : launch_typed<192, 128, true, 64>(p, maps, stream);
+        case 256:
+            return p.RN == 32 ? launch_typed<320, 256, true, 32>(p, maps, stream)
+                              : launch_typed<320, 256, true, 64>(p, maps, stream);
+        default:
+            return p.RN == 32 ? launch_typed<576, 512, true, 32>(p, maps, stream)
+                              : launch_typed<576, 512, true, 64>(p, maps, stream);
         }
     }
     const bool wide = p.RN == 128;

@@ -722,6 +722,16 @@ def _on_current(device: torch.device, view, what: str) -> None:
         raise ValueError(f"{what} is on {device}, the cache on {kept.device}")
 
 
+def _raw_stream(device: torch.device, stream) -> int:
+    """The cudaStream_t of `stream`, or of the device's current stream (without making the Stream
+    object that costs more than the launch)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _data(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _torch_dtype(code: int) -> torch.dtype:
     return torch.bfloat16 if code == KVC_BF16 else torch.float32
 
@@ -844,9 +854,9 @@ def kvc_decode_attn_tree(q: torch.Tensor, cache: kvc_cache, draft: kvc_draft, *,
         ws = tree_workspace(c.batch, q.shape[2], c.n_heads_kv, c.d_head, draft.n_draft, q.dtype,
                             q.device)
     wp, wb = _ws_ptr(ws)
-    _check(load().kvc_decode_attn_tree(
-        q.data_ptr(), q.shape[2], c, _ptr(len), -1 if n_valid is None else n_valid, draft, scale,
-        out.data_ptr(), _ptr(lse), wp, wb, _stream(stream)))
+    _check((_lib or load()).kvc_decode_attn_tree(
+        q.data_ptr(), q.shape[2], c, _data(len), -1 if n_valid is None else n_valid, draft, scale,
+        out.data_ptr(), _data(lse), wp, wb, _raw_stream(q.device, stream)))
     return out
 
 
@@ -862,9 +872,9 @@ def kvc_decode_attn_tree_paged(q: torch.Tensor, pool: kvc_block_pool, pt: kvc_pa
         ws = tree_workspace(pt.batch, q.shape[2], pool.n_heads_kv, pool.d_head, draft.n_draft,
                             q.dtype, q.device)
     wp, wb = _ws_ptr(ws)
-    _check(load().kvc_decode_attn_tree_paged(
-        q.data_ptr(), q.shape[2], pool, pt, draft, scale, out.data_ptr(), _ptr(lse), wp, wb,
-        _stream(stream)))
+    _check((_lib or load()).kvc_decode_attn_tree_paged(
+        q.data_ptr(), q.shape[2], pool, pt, draft, scale, out.data_ptr(), _data(lse), wp, wb,
+        _raw_stream(q.device, stream)))
     return out
 
 
@@ -884,9 +894,9 @@ def kvc_decode_attn_latent(q: torch.Tensor, cache: kvc_latent_cache, draft: kvc_
         ws = latent_workspace(c.batch, q.shape[2], c.d_latent, c.d_rope, draft.n_draft, q.dtype,
                               q.device)
     wp, wb = _ws_ptr(ws)
-    _check(load().kvc_decode_attn_latent(
-        q.data_ptr(), q.shape[2], c, _ptr(len), -1 if n_valid is None else n_valid, draft, scale,
-        out.data_ptr(), _ptr(lse), wp, wb, _stream(stream)))
+    _check((_lib or load()).kvc_decode_attn_latent(
+        q.data_ptr(), q.shape[2], c, _data(len), -1 if n_valid is None else n_valid, draft, scale,
+        out.data_ptr(), _data(lse), wp, wb, _raw_stream(q.device, stream)))
     return out
 
 
@@ -912,8 +922,8 @@ def kvc_tree_accept(cache: kvc_cache, len: torch.Tensor, draft: kvc_draft, path:
                        n_accept)
     shape = (c.batch, c.n_heads_kv) if len.dim() == 2 else (c.batch * c.n_heads_kv,)
     _need(len, "len", torch.int32, shape, dev)
-    _check(load().kvc_tree_accept(c, len.data_ptr(), draft, path.data_ptr(), n_accept.data_ptr(),
-                                  _stream(stream)))
+    _check((_lib or load()).kvc_tree_accept(c, len.data_ptr(), draft, path.data_ptr(), n_accept.data_ptr(),
+                                  _raw_stream(dev, stream)))
 
 
 def kvc_latent_accept(cache: kvc_latent_cache, len: torch.Tensor, draft: kvc_draft,
@@ -923,8 +933,8 @@ def kvc_latent_accept(cache: kvc_latent_cache, len: torch.Tensor, draft: kvc_dra
     dev = _accept_args(draft, c, (c.batch, draft.n_draft, c.d_latent + c.d_rope), c.dtype, path,
                        n_accept)
     _need(len, "len", torch.int32, (c.batch,), dev)
-    _check(load().kvc_latent_accept(c, len.data_ptr(), draft, path.data_ptr(),
-                                    n_accept.data_ptr(), _stream(stream)))
+    _check((_lib or load()).kvc_latent_accept(c, len.data_ptr(), draft, path.data_ptr(),
+                                    n_accept.data_ptr(), _raw_stream(dev, stream)))
 
 
 def kvc_tree_accept_paged(pool: kvc_block_pool, pt: kvc_page_table, free_pool: kvc_free_pool,
@@ -937,9 +947,9 @@ def kvc_tree_accept_paged(pool: kvc_block_pool, pt: kvc_page_table, free_pool: k
         accepted = torch.empty(pt.batch, dtype=torch.int32, device=dev)
     else:
         _need(accepted, "accepted", torch.int32, (pt.batch,), dev)
-    _check(load().kvc_tree_accept_paged(pool, pt, free_pool, draft, path.data_ptr(),
+    _check((_lib or load()).kvc_tree_accept_paged(pool, pt, free_pool, draft, path.data_ptr(),
                                         n_accept.data_ptr(), accepted.data_ptr(),
-                                        _stream(stream)))
+                                        _raw_stream(dev, stream)))
     return accepted
 
 
@@ -954,5 +964,5 @@ def kvc_latent_expand(cache: kvc_latent_cache, w_k: torch.Tensor, w_v: torch.Ten
     _need(w_k, "w_k", _torch_dtype(c.dtype), (H, D - c.d_rope, c.d_latent), dev)
     _need(w_v, "w_v", _torch_dtype(c.dtype), (H, D, c.d_latent), dev)
     _need(len, "len", torch.int32, (c.batch,), dev)
-    _check(load().kvc_latent_expand(c, _ptr(len), -1 if n_valid is None else n_valid,
-                                    w_k.data_ptr(), w_v.data_ptr(), dst, _stream(stream)))
+    _check((_lib or load()).kvc_latent_expand(c, _data(len), -1 if n_valid is None else n_valid,
+                                    w_k.data_ptr(), w_v.data_ptr(), dst, _raw_stream(dev, stream)))
