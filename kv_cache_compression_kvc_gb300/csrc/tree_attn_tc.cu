@@ -85,6 +85,9 @@ struct Plan {
     static constexpr int SMALL = 640 + (1 + SETS) * RN * 4;         // barriers, flags, row values
     static constexpr int FIT = (kSmemMax - 1024 - Q_BYTES - P_BYTES - ROPE - SMALL) / UNIT;
     static constexpr int NU = FIT > 16 ? 16 : FIT;           // ring units
+    // A latent tile's copies complete on one barrier (its units are keys and values at once), ring
+    // of NTB; other caches' units have a barrier each.
+    static constexpr int NTB = LATENT ? (NU + KU - 1) / KU + 1 : NU;
     // S of tile t + 1 is issued before the values of tile t are used
     static_assert(NU >= 2 * KU, "ring too small");
     static constexpr int SMEM = 1024 + Q_BYTES + P_BYTES + ROPE + NU * UNIT + SMALL;
@@ -117,8 +120,9 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     const uint32_t sR = sP + PL::P_BYTES;                    // rope part of the keys
     const uint32_t ring = sR + PL::ROPE;
     const uint32_t bars = ring + NU * UNIT;
-    const uint32_t b_full = bars, b_empty = b_full + 8 * NU;
-    const uint32_t b_rope_full = b_empty + 8 * NU, b_rope_empty = b_rope_full + 16;
+    constexpr int NTB = PL::NTB;
+    const uint32_t b_full = bars, b_empty = b_full + 8 * NTB;
+    const uint32_t b_rope_empty = b_empty + 8 * NU;
     const uint32_t b_q_full = b_rope_empty + 16, b_q_empty = b_q_full + 8;
     const uint32_t b_s_full = b_q_empty + 8, b_s_empty = b_s_full + 16;
     const uint32_t b_p_full = b_s_empty + 16, b_pv = b_p_full + 8, b_done = b_pv + 8;
@@ -128,20 +132,17 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     volatile int *s_abort = reinterpret_cast<volatile int *>(small + 16);
     float *s_fac = reinterpret_cast<float *>(small + 128);                // RN
     float *s_row = s_fac + RN;                                            // [kSets][RN]
-    static_assert(8 * (2 * 16 + 13) + 8 <= 512, "barrier area");
+    static_assert(8 * (NTB + NU + 11) + 8 <= 512, "barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rt = blockIdx.x % p.RT, g = blockIdx.x / p.RT;
     if (warp == 2 && lane < 8) tc::prefetch_map(&maps.q + lane);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NU; ++i) {
-            mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 1);
-        }
+        for (int i = 0; i < NTB; ++i) mbar_init(b_full + 8 * i, 1);
+        for (int i = 0; i < NU; ++i) mbar_init(b_empty + 8 * i, 1);
         mbar_init(b_q_full, 1);
         mbar_init(b_q_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(b_rope_full + 8 * i, 1);
             mbar_init(b_rope_empty + 8 * i, 1);
             mbar_init(b_s_full + 8 * i, 1);
             mbar_init(b_s_empty + 8 * i, 4 * kSets);
@@ -184,7 +185,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         TreeSeg s;
         const bool paged = p.table != nullptr;
         const int bx = paged ? min(p.bs, TS) : TS;           // slots of a cache copy
-        uint32_t slot = 0, ph = 1;                           // ring position
+        uint32_t slot = 0, ph = 1, t_slot = 0;               // ring positions
         while (walk.next(p, rt, TS, s)) {
             if (s.rows <= 0) continue;
             if (n_segs > 0) wait(b_q_empty, (n_segs - 1) & 1);
@@ -226,28 +227,33 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 }
                 const bool go = !*s_abort;
                 const uint32_t bytes = (draft ? TS : bx * pages) * 128u;   // of a 64-wide piece
-                if (rope) {
+                uint32_t bar = b_full + 8 * t_slot;          // latent: one barrier for the tile
+                if constexpr (LATENT) {
                     const uint32_t r = n_tiles & 1;
-                    if (n_tiles >= 2) wait(b_rope_empty + 8 * r, ((n_tiles >> 1) - 1) & 1);
+                    if (rope && n_tiles >= 2) wait(b_rope_empty + 8 * r, ((n_tiles >> 1) - 1) & 1);
                     if (go && tc::elect()) {
-                        if (valid == 0) mbar_arrive(b_rope_full + 8 * r);
+                        if (valid == 0) mbar_arrive(bar);
                         else {
-                            mbar_arrive_expect_tx(b_rope_full + 8 * r, bytes);
-                            tc::tma_5d(sR + r * SUB, draft ? &maps.rd : &maps.rk, 0, y, 0, 0, s.b,
-                                       b_rope_full + 8 * r);
+                            mbar_arrive_expect_tx(bar, bytes * (KU * SUBS + (rope ? 1 : 0)));
+                            if (rope)
+                                tc::tma_5d(sR + r * SUB, draft ? &maps.rd : &maps.rk, 0, y, 0, 0, s.b, bar);
                         }
                     }
                     __syncwarp();
+                    if (++t_slot == NTB) t_slot = 0;
                 }
 #pragma unroll 1
                 for (int u = 0; u < PER; ++u, ++n_units) {
-                    const uint32_t bar = b_full + 8 * slot, dst = ring + slot * UNIT;
+                    const uint32_t dst = ring + slot * UNIT;
+                    if (!LATENT) bar = b_full + 8 * slot;
                     const bool isv = u >= KU;
                     const int sub = (isv ? u - KU : u) * SUBS;
                     if (n_units >= NU) wait(b_empty + 8 * slot, ph);
                     if (go && tc::elect()) {
-                        if (valid == 0) mbar_arrive(bar);
-                        else mbar_arrive_expect_tx(bar, bytes * SUBS);
+                        if (!LATENT) {
+                            if (valid == 0) mbar_arrive(bar);
+                            else mbar_arrive_expect_tx(bar, bytes * SUBS);
+                        }
                         if (valid > 0 && !by_page)
                             tc::tma_5d(dst, draft ? (isv ? &maps.vd : &maps.kd) : (isv ? &maps.v : &maps.k),
                                        0, y, sub, s.kh, s.b, bar);
@@ -285,6 +291,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         };
         unsigned seg_no = 0;                                 // segments whose S has begun
         uint32_t k_slot = 0, k_ph = 0, v_slot = LATENT ? 0 : KU, v_ph = 0;   // ring positions
+        uint32_t t_slot = 0, t_ph = 0;                       // latent: tile barriers
         auto step = [&](uint32_t &slot, uint32_t &ph, uint32_t by) {
             slot += by;
             if (slot >= NU) {
@@ -302,10 +309,16 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             // every unit has arrived, then one block of products: each wait, fence and pick of a
             // lane between products costs the tensor cores about 300 clocks
             uint32_t src[KU], bar[KU];
-            if (rope) wait(b_rope_full + 8 * buf, (n >> 1) & 1);
+            if constexpr (LATENT) {
+                wait(b_full + 8 * t_slot, t_ph);
+                if (++t_slot == NTB) {
+                    t_slot = 0;
+                    t_ph ^= 1;
+                }
+            }
 #pragma unroll
             for (int u = 0; u < KU; ++u) {
-                wait(b_full + 8 * k_slot, k_ph);
+                if (!LATENT) wait(b_full + 8 * k_slot, k_ph);
                 src[u] = ring + k_slot * UNIT;
                 bar[u] = b_empty + 8 * k_slot;
                 step(k_slot, k_ph, 1);
@@ -348,8 +361,8 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             // hold up the product that frees the ring
             bool ahead = more_here;
             if (NU < 3 * PER && more_here) {
-                uint32_t last = k_slot + KU - 1, ph = k_ph;
-                if (last >= NU) {
+                uint32_t last = LATENT ? t_slot : k_slot + KU - 1, ph = LATENT ? t_ph : k_ph;
+                if (!LATENT && last >= NU) {
                     last -= NU;
                     ph ^= 1;
                 }
@@ -545,7 +558,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     for (int u = 0; u < MB; ++u) {
                         const unsigned un = v_unit + u;
                         const uint32_t slot = un % NU;
-                        wait(b_full + 8 * slot, (un / NU) & 1);
+                        if (!LATENT) wait(b_full + 8 * slot, (un / NU) & 1);   // (S implies a latent tile)
                         unsigned char *base = smem_raw + (ring + slot * UNIT - raw);
                         // a warp takes a row: eight lanes per 64 dims
                         const int sub = lane >> 3;
@@ -657,10 +670,9 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             auto drain = [&](uint32_t bar, uint32_t parity) {
                 mbar_wait_ok(bar, parity, kMbarSpinLimit >> 4);
             };
-            for (unsigned i = n_units > NU ? n_units - NU : 0; i < n_units; ++i)
-                drain(b_full + 8 * (i % NU), (i / NU) & 1);
-            for (unsigned i = n_tiles > 2 ? n_tiles - 2 : 0; rope && i < n_tiles; ++i)
-                drain(b_rope_full + 8 * (i & 1), (i >> 1) & 1);
+            const unsigned loads = LATENT ? n_tiles : n_units;
+            for (unsigned i = loads > NTB ? loads - NTB : 0; i < loads; ++i)
+                drain(b_full + 8 * (i % NTB), (i / NTB) & 1);
             if (n_segs > 0) drain(b_q_full, (n_segs - 1) & 1);
         } else if (warp == 1) {
             if (tc::elect()) tc::commit(b_done);
