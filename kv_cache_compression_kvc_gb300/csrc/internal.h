@@ -300,6 +300,7 @@ struct TreeParams {
     const int32_t *count;        // nullable (T each)
     int32_t T;
     float scale_log2;            // scale * log2(e)
+    float inv_G;                 // 1 / G
     void *out;                   // [B][T][Hq][DV], cache type
     float *lse;                  // nullable
     // schedule (plan): row tiles of RP rows padded to RN, `groups` ranges of tiles

@@ -10,13 +10,21 @@
 // (up to 256 rows) a stage: the latent rows are read once per block, the matrices (a few MB)
 // from L2.  A head's K and V rows form one accumulator of up to 256 columns (K then V, K's width
 // rounded up to 16; d_head 256: K and V one after the other), double-buffered in tensor memory, so
-// the writes of one head overlap the products of the next.  Work: (slot tile, head) units in one
-// sequence, split evenly over the blocks; tiles are counted from the lengths on the device.
+// the writes of one head overlap the products of the next.
 //
-// Roles (192 threads): warp 0 copies (TMA), warp 1 issues the products, warps 2-5 take a slot per
-// thread from tensor memory, round once and write 32 bytes at a time (whole sectors: a row's
-// pieces are contiguous), the shared rope part from registers.  Every wait is bounded, as in
-// tree_attn_tc.cu.
+// Work: (slot tile, head) units in one sequence, split evenly over the blocks; tiles are counted
+// from the lengths on the device.  Clusters of two or four blocks that share the matrices' stages
+// by multicast were measured and dropped (52.9 and 59.9 us against 53.0 alone: L2 is not what
+// bounds it).
+//
+// Roles (352 threads): warp 0 copies (TMA), warp 1 issues the products, warps 2-9 (two sets, one
+// for either accumulator) take a slot per thread from tensor memory, round once, and pass 32
+// columns at a time through shared memory so that a store instruction writes contiguous pieces of
+// 8 slots (32-byte pieces of 32 slots straight from registers: 57 us against 35 for the
+// products alone); the shared rope part goes from the latent rows to the keys in the same
+// stores.  Warp 10 waits for the stages on behalf of warp 1 and passes them on through named
+// barriers: a satisfied mbarrier wait between two stages costs the issuing warp about 200 clocks,
+// in which the tensor cores run dry.  Every wait is bounded, as in tree_attn_tc.cu.
 #include "tc_ops.cuh"
 #include "internal.h"
 
@@ -24,7 +32,9 @@ namespace kvc {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 352;
+constexpr int kStaging = 8 * 2048;           // a writing warp's [32 slots][32 columns]
+constexpr int kBarStage = 1;                 // named barriers: a stage has arrived
 constexpr int kTile = 128;                   // slots
 constexpr int kSub = kTile * 128;            // bytes of [128 slots][64]
 constexpr int kSmemMax = 227 * 1024;
@@ -39,16 +49,8 @@ struct ExpandPlan {
     int32_t jobs;                // per head: 1 (K and V together) or 2
     int32_t nk, nk16;            // K rows, rounded up to 16
     int32_t stage, stages;       // bytes of a stage, stages
-    int32_t wide;                // destination rows 32-byte aligned
     int32_t smem;
 };
-
-__device__ __forceinline__ void store_32(void *p, const uint32_t *r)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 
 // Slots of sequence b to expand.
 __device__ __forceinline__ int expand_len(const ExpandParams &p, int b)
@@ -146,7 +148,8 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
     const uint32_t sA = (raw + 1023u) & ~1023u;
     const int subs = p.R / 64;
     const uint32_t sW = sA + subs * kSub;
-    const uint32_t bars = sW + pl.stages * pl.stage;
+    const uint32_t sE = sW + pl.stages * pl.stage;
+    const uint32_t bars = sE + kStaging;
     const uint32_t b_full = bars, b_empty = b_full + 8 * kMaxStages;
     const uint32_t b_a_full = b_empty + 8 * kMaxStages, b_a_empty = b_a_full + 8;
     const uint32_t b_acc_full = b_a_empty + 8, b_acc_empty = b_acc_full + 16;
@@ -226,7 +229,7 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
             }
         }
     } else if (warp == 1) {
-        uint32_t slot = 0, ph = 0;
+        uint32_t slot = 0;
         unsigned n = 0;                          // accumulators so far
         while (walk.next(p, lo, hi)) {
             wait(b_a_full, n_a & 1);
@@ -239,7 +242,7 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
                 const uint32_t buf = n & 1, d = tmem + buf * 256;
                 if (n >= 2) wait(b_acc_empty + 8 * buf, ((n >> 1) - 1) & 1);
                 for (int k = 0; k < subs; ++k) {
-                    wait(b_full + 8 * slot, ph);
+                    tc::bar_sync(kBarStage + slot, 64);
                     tc::fence_after();
                     if (tc::elect()) {
                         const uint32_t a = sA + k * kSub, w = sW + slot * pl.stage;
@@ -253,80 +256,95 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
                         }
                     }
                     __syncwarp();
-                    if (++slot == (uint32_t)pl.stages) {
-                        slot = 0;
-                        ph ^= 1;
-                    }
+                    if (++slot == (uint32_t)pl.stages) slot = 0;
                 }
                 if (++job == pl.jobs) job = 0;
             }
         }
-    } else {
-        const int q4 = warp & 3;
-        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
-        unsigned n = 0;
-        const int E16 = p.E / 8;                 // 16-byte pieces of the rope part
-        while (walk.next(p, lo, hi)) {
-            const int s = walk.tile * kTile + q4 * 32 + lane;
-            const bool mine = s < walk.n;
-            uint4 rope[8];
-            {
-                const __nv_bfloat16 *src =
-                    static_cast<const __nv_bfloat16 *>(p.c) + walk.b * p.c_sb + (int64_t)s * p.c_ss + p.R;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    rope[i] = mine && i < E16 ? __ldg(reinterpret_cast<const uint4 *>(src) + i)
-                                              : make_uint4(0, 0, 0, 0);
+    } else if (warp == 10) {
+        // a slot's barrier cannot be reached twice: it is loaded again only after warp 1 used it
+        uint32_t slot = 0, ph = 0;
+        while (walk.next(p, lo, hi))
+            for (int i = (hi - lo) * subs; i > 0; --i) {
+                wait(b_full + 8 * slot, ph);
+                __syncwarp();
+                tc::bar_arrive(kBarStage + slot, 64);
+                if (++slot == (uint32_t)pl.stages) {
+                    slot = 0;
+                    ph ^= 1;
+                }
             }
+    } else {
+        const int q4 = warp & 3, set = (warp - 2) >> 2;
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        const uint32_t mem = sE + (warp - 2) * 2048;
+        const int row4 = lane >> 2, piece = lane & 3;        // store phase: rows 8 i + row4, 8 columns
+        unsigned n = 0;
+        while (walk.next(p, lo, hi)) {
+            const int s0 = walk.tile * kTile + q4 * 32;
+            const int live = walk.n - s0;                    // slots of this warp to write
+            const __nv_bfloat16 *rope = static_cast<const __nv_bfloat16 *>(p.c) + walk.b * p.c_sb +
+                                        (int64_t)s0 * p.c_ss + p.R - pl.nk;   // indexed by K column
             int h = lo / pl.jobs, job = lo - h * pl.jobs;
             for (int j = lo; j < hi; ++j, ++n) {
                 const bool dok = pl.jobs == 1 || job == 0, dov = pl.jobs == 1 || job == 1;
-                const uint32_t buf = n & 1;
-                const int kcols = dok ? pl.nk16 : 0, cols = kcols + (dov ? p.D : 0);
-                const int64_t at = walk.b * p.sb + h * p.sh + (int64_t)s * p.ss;
-                __nv_bfloat16 *kr = static_cast<__nv_bfloat16 *>(p.k) + at;
-                __nv_bfloat16 *vr = static_cast<__nv_bfloat16 *>(p.v) + at - kcols;   // indexed by column
+                const int64_t at = walk.b * p.sb + h * p.sh + (int64_t)s0 * p.ss;
+                if (++job == pl.jobs) {
+                    job = 0;
+                    ++h;
+                }
+                const uint32_t buf = n & 1, acc = tmem + buf * 256 + lanes;
+                if ((int)buf != set) continue;
+                const int kcols = dok ? pl.nk16 : 0;
                 wait(b_acc_full + 8 * buf, (n >> 1) & 1);
                 tc::fence_after();
 #pragma unroll 1
-                for (int c = 0; c < cols; c += 32) {
-                    float x[32];
+                for (int c = dok ? 0 : p.D; c < (dov ? 2 * p.D : p.D); c += 32) {
+                    const bool isv = c >= p.D;
+                    const int col0 = isv ? c - p.D : c;
+                    const int width = isv ? p.D : pl.nk;     // columns that are products
+                    __syncwarp();                            // the last piece is stored
+                    if (col0 < width) {                      // (else all rope)
+                        float x[32];
+                        tc::ld32(acc + (isv ? kcols : 0) + col0, x);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tc::st_shared_16(mem + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4),
+                                             tc::pack_bf16(x[8 * i], x[8 * i + 1]),
+                                             tc::pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                             tc::pack_bf16(x[8 * i + 4], x[8 * i + 5]),
+                                             tc::pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+                    }
                     __syncwarp();
-                    tc::ld32(tmem + buf * 256 + lanes + c, x);
-                    tc::wait_ld();
-                    if (!mine) continue;
+                    const int col = col0 + 8 * piece;
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(isv ? p.v : p.k) + at + col;
+                    uint4 w[4];
+                    if (col < width) {
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {            // 16 columns: all K or all V
-                        const int col = c + 16 * g;
-                        if (col >= cols) break;
-                        uint32_t w[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) w[i] = tc::pack_bf16(x[16 * g + 2 * i], x[16 * g + 2 * i + 1]);
-                        const bool isk = col < kcols;
-                        __nv_bfloat16 *dst = (isk ? kr : vr) + col;
-                        const bool all = !isk || col + 16 <= pl.nk;
-                        if (pl.wide && all) {
-                            store_32(dst, w);
-                        } else {
-                            *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                            if (all)
-                                *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * i + row4;
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                                         : "r"(mem + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4)));
                         }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = 8 * i + row4;
+                            if (r < live)
+                                w[i] = __ldg(reinterpret_cast<const uint4 *>(rope + (int64_t)r * p.c_ss + col));
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + row4;
+                        if (r < live) *reinterpret_cast<uint4 *>(dst + (int64_t)r * p.ss) = w[i];
                     }
                 }
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_acc_empty + 8 * buf);
-                if (dok && mine) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(kr + pl.nk);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (i < E16) dst[i] = rope[i];
-                }
-                if (++job == pl.jobs) {
-                    job = 0;
-                    ++h;
-                }
             }
         }
     }
@@ -360,12 +378,10 @@ cudaError_t launch_latent_expand_tc(const ExpandParams &p, cudaStream_t stream, 
     const int rows = pl.jobs == 1 ? pl.nk16 + p.D : 256;
     const int subs = p.R / 64;
     pl.stage = rows * 128;
-    const int room = kSmemMax - 1024 - subs * kSub - 512;
+    const int room = kSmemMax - 1024 - subs * kSub - kStaging - 512;
     pl.stages = room / pl.stage;
     if (pl.stages > kMaxStages) pl.stages = kMaxStages;
-    pl.smem = 1024 + subs * kSub + pl.stages * pl.stage + 512;
-    auto al32 = [](const void *x) { return (reinterpret_cast<uintptr_t>(x) & 31u) == 0; };
-    pl.wide = al32(p.k) && al32(p.v) && p.ss % 16 == 0 && p.sh % 16 == 0 && p.sb % 16 == 0;
+    pl.smem = 1024 + subs * kSub + pl.stages * pl.stage + kStaging + 512;
     ExpandMaps maps;
     const uint64_t R = p.R, B = p.B, H = p.H, S = subs;
     const uint64_t ss = (uint64_t)p.c_ss * 2, sb = (uint64_t)p.c_sb * 2, row = R * 2;
@@ -390,12 +406,11 @@ cudaError_t launch_latent_expand_tc(const ExpandParams &p, cudaStream_t stream, 
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    // no more blocks than (tile, job) units there can be
-    const long long most = (long long)p.B * ((p.cap < p.dst_cap ? p.cap : p.dst_cap) + kTile - 1) / kTile *
+    // no more blocks than units there can be
+    const long long most = (long long)p.B * (((p.cap < p.dst_cap ? p.cap : p.dst_cap) + kTile - 1) / kTile) *
                            p.H * pl.jobs;
-    const int grid = most < sms[dev] ? (most > 0 ? (int)most : 1) : sms[dev];
-    return launch_pdl(latent_expand_tc_kernel, dim3((unsigned)grid), dim3(kThreads), (size_t)pl.smem, stream,
-                      maps, p, pl);
+    const unsigned grid = (unsigned)(most < sms[dev] ? (most > 0 ? most : 1) : sms[dev]);
+    return launch_pdl(latent_expand_tc_kernel, dim3(grid), dim3(kThreads), (size_t)pl.smem, stream, maps, p, pl);
 }
 
 }  // namespace kvc

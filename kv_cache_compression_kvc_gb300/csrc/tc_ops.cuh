@@ -18,14 +18,6 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
         : "memory");
 }
-// Brings a box into L2.
-__device__ __forceinline__ void prefetch_5d(const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
-                 : "memory");
-}
 // The first use of a tensor map otherwise stalls its copy for about 2 us.
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
@@ -173,6 +165,10 @@ __device__ __forceinline__ bool test(uint32_t bar, uint32_t parity)
 __device__ __forceinline__ void bar_sync(int id, int n)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int n)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 __device__ __forceinline__ bool bar_any(int id, int n, bool x)
 {

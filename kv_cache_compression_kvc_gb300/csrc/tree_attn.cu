@@ -343,15 +343,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     const int rt = blockIdx.x % p.RT, g = blockIdx.x / p.RT;
     const int4 note = p.ws_info[g];
     if (note.x < 0) return;
-    const int pair = note.x, b = pair / p.Hkv, kh = pair - b * p.Hkv;
+    const int b = note.x, kh = note.y;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = blockIdx.y * ROWS + w / WPR, part0 = w % WPR;
-    const int rows = min(p.RP, tree_count(p, b) * p.G - rt * p.RP);
+    const int rows = min(p.RP, (note.w >> 1) * p.G - rt * p.RP);
     const bool live = r < rows;
     if (WPR == 1 && !live) return;
-    const int nseg = live ? note.y - g + 1 : 0;
+    const int nseg = live ? note.z - g + 1 : 0;
     auto slot_of = [&](int i) -> size_t {
-        return ((size_t)((g + i) * p.RT + rt) * 2 + (i == 0 ? note.z : 0)) * p.RN + r;
+        return ((size_t)((g + i) * p.RT + rt) * 2 + (i == 0 ? note.w & 1 : 0)) * p.RN + r;
     };
     float M = kNegBig;
     for (int i = lane; i < nseg; i += 32) M = fmaxf(M, __ldcg(p.ws_ml + slot_of(i) * 2));

@@ -66,23 +66,22 @@ struct TreeRange {
 __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int TS)
 {
     const int lane = threadIdx.x & 31;
-    const int per = (p.P + 31) >> 5;
-    const int q0 = min(p.P, lane * per), q1 = min(p.P, q0 + per);
+    // items: pairs, or whole sequences (Hkv equal pairs) where the heads share a length
+    const int items = p.len_per_pair ? p.P : p.B, heads = p.len_per_pair ? 1 : p.Hkv;
+    const int per = (items + 31) >> 5;
+    const int q0 = min(items, lane * per), q1 = min(items, q0 + per);
     const bool check = blockIdx.x == 0 && threadIdx.x < 32;
+    auto count_of = [&](int q) {
+        return p.count == nullptr ? p.T : p.count[p.len_per_pair ? q / p.Hkv : q];
+    };
     long long sum = 0;
-    int b = q0 / p.Hkv, kh = q0 - b * p.Hkv;
+#pragma unroll 4
     for (int q = q0; q < q1; ++q) {
-        int n = p.n_valid, c = p.T;
-        if (p.len != nullptr) n = p.len[p.len_per_pair ? q : b];
-        if (p.count != nullptr) c = p.count[b];
+        int n = p.len != nullptr ? p.len[q] : p.n_valid, c = count_of(q);
         if (check && (n < 0 || n > p.cap || c < 0 || c > p.T)) record_code(p.dev_code, kDevBadLengthCode);
         n = n < 0 ? 0 : (n > p.cap ? p.cap : n);
         c = c < 0 ? 0 : (c > p.T ? p.T : c);
-        sum += tree_tiles(p, n, c, TS);
-        if (++kh == p.Hkv) {
-            kh = 0;
-            ++b;
-        }
+        sum += (long long)tree_tiles(p, n, c, TS) * heads;
     }
     long long incl = sum;
 #pragma unroll
@@ -107,14 +106,23 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int 
     int q = q0, off = 0, len = 0, cnt = 0;
     if (here) {
         long long t = before;
+        int nt = 0;
         for (;; ++q) {
-            len = tree_len(p, q);
-            cnt = tree_count(p, q / p.Hkv);
-            const int nt = tree_tiles(p, len, cnt, TS);
-            if (r.t0 < t + nt || q == q1 - 1) break;
-            t += nt;
+            len = p.len != nullptr ? p.len[q] : p.n_valid;
+            len = len < 0 ? 0 : (len > p.cap ? p.cap : len);
+            cnt = count_of(q);
+            cnt = cnt < 0 ? 0 : (cnt > p.T ? p.T : cnt);
+            nt = tree_tiles(p, len, cnt, TS);
+            const long long end = t + (long long)nt * heads;
+            if (r.t0 < end || q == q1 - 1) break;
+            t = end;
         }
         off = (int)(r.t0 - t);
+        if (heads > 1) {
+            const int kh = nt > 0 ? off / nt : 0;
+            off -= kh * nt;
+            q = q * heads + kh;
+        }
     }
     const int src = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
     if (src < 0) r.n = 0;
@@ -189,13 +197,14 @@ struct TreeWalk {
 };
 
 // Where the merge finds a split pair: written by the block that holds its first part.
-//   info[g] = {pair or -1, last group, workspace slot (0 or 1) of the first part, 0}
+//   info[g] = {sequence or -1, KV head, last group, drafted tokens * 2 + workspace slot (0 or 1) of
+//   the first part}
 __device__ __forceinline__ void tree_note_split(const TreeParams &p, const TreeRange &r, int g,
                                                 const TreeSeg &s, int4 &note)
 {
     if (s.lo != 0 || s.hi == s.nt) return;
     const long long last = r.t0 + r.n - s.hi + s.nt - 1;     // the pair's last tile
-    note = make_int4(s.pair, r.group_of(last), s.first ? 0 : 1, 0);
+    note = make_int4(s.b, s.kh, r.group_of(last), s.cnt * 2 + (s.first ? 0 : 1));
 }
 
 __device__ __forceinline__ uint64_t tree_mask_word(const TreeParams &p, int b, int t, int cnt)

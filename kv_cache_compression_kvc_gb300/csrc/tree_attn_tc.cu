@@ -351,7 +351,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             if (!LATENT) step(k_slot, k_ph, KU);             // past the values
         };
         unsigned n = 0;
-        bool have = next_seg(s);
+        bool have = next_seg(s), have_nx = have && next_seg(nx);
         int tile = have ? s.lo : 0;
         if (have) scores(s, tile, 0);
         while (have) {
@@ -400,11 +400,12 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             ++n;
             ++tile;
             if (!more_here) {
-                have = next_seg(nx);
+                have = have_nx;
                 if (have) {
                     s = nx;
                     tile = s.lo;
                     scores(s, tile, n);
+                    have_nx = next_seg(nx);
                 }
             }
         }
@@ -442,15 +443,21 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         int4 note = make_int4(-1, 0, 0, 0);
         unsigned n = 0, seg_no = 0;
         uint32_t v_unit = LATENT ? 0 : KU;                   // this tile's first value unit
-        while (walk.next(p, rt, TS, s)) {
+        const int r0 = rt * p.RP;
+        const int tok = (r0 + row) / p.G, hg_row = (r0 + row) - tok * p.G;   // of this thread's row
+        auto token_of = [&](int r) { return (int)(((float)r + 0.5f) * p.inv_G); };
+        TreeSeg nx;
+        bool more = walk.next(p, rt, TS, nx);
+        while (more) {
+            s = nx;
+            more = walk.next(p, rt, TS, nx);                 // its lengths arrive meanwhile
             tree_note_split(p, range, g, s, note);
             if (s.rows <= 0) continue;
             const bool mine = row < s.rows;
             const bool any = row_lo < s.rows;                // warp-uniform
-            const int r0 = rt * p.RP;
             float m = kNegBig, l = 0.f;
             bool drafts = false;
-            const uint64_t word = mine ? tree_mask_word(p, s.b, (r0 + row) / p.G, s.cnt) : 0ull;
+            const uint64_t word = mine && s.hi == s.nt ? tree_mask_word(p, s.b, tok, s.cnt) : 0ull;
             // drafted tokens with non-finite values: alternate words, since a thread may set up
             // the next pair's while another still reads this one's
             unsigned long long *s_nf = s_nf2 + (seg_no++ & 1);
@@ -602,12 +609,12 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 for (int i = 1; i < kSets; ++i) l += s_row[i * RN + row];
                 s_fac[row] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 if (mine) {
-                    const int t = (r0 + row) / p.G, h = s.kh * p.G + (r0 + row) % p.G;
+                    const int h = s.kh * p.G + hg_row;
                     if (!whole) {
                         p.ws_ml[(part * RN + row) * 2] = m;
                         p.ws_ml[(part * RN + row) * 2 + 1] = l;
                     } else if (p.lse != nullptr) {
-                        p.lse[((size_t)s.b * p.T + t) * p.Hq + h] =
+                        p.lse[((size_t)s.b * p.T + tok) * p.Hq + h] =
                             l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
                     }
                 }
@@ -630,11 +637,12 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     const float4 f = *reinterpret_cast<const float4 *>(s_fac + ra + j);
                     o[j] *= f.x; o[j + 1] *= f.y; o[j + 2] *= f.z; o[j + 3] *= f.w;
                 }
-                int t = (r0 + ra) / p.G, hg = (r0 + ra) - t * p.G;
+                const int t = token_of(r0 + ra);
+                int hg = (r0 + ra) - t * p.G;
                 if (nf) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        if (j < here) o[j] += stray(nf, (r0 + ra + j) / p.G, d, s);
+                        if (j < here) o[j] += stray(nf, token_of(r0 + ra + j), d, s);
                 }
                 if (whole) {
                     __nv_bfloat16 *dst =

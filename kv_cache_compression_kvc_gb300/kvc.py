@@ -714,7 +714,7 @@ def _need(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> None:
 
 def _on_current(device: torch.device, view, what: str) -> None:
     """The kernels run on the current CUDA device: the tensors, and those of the cache, live there."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise ValueError(f"{what} is on {device}: the current CUDA device is needed")
     kept = getattr(view, "_keep", None)
     kept = kept[0] if isinstance(kept, tuple) else kept
@@ -819,21 +819,26 @@ def latent_workspace(batch, n_heads_q, d_latent, d_rope, n_draft, dtype: torch.d
 def _attn_args(q, view, width, out_width, code, batch, draft, rows_shape, out, lse):
     """Checks shared by the draft-tree and latent attention; returns out."""
     dt = _torch_dtype(code)
-    if q.dim() != 4 or q.dtype != dt or not q.is_contiguous() or q.shape[0] != batch or \
-            q.shape[1] != draft.n_draft or q.shape[3] != width:
+    shape = q.shape
+    if q.dim() != 4 or q.dtype != dt or not q.is_contiguous() or \
+            shape != (batch, draft.n_draft, shape[2], width):
         raise ValueError(f"q must be a contiguous {dt} tensor [{batch}, {draft.n_draft}, "
-                         f"n_heads_q, {width}], got {q.dtype} {list(q.shape)}")
+                         f"n_heads_q, {width}], got {q.dtype} {list(shape)}")
     dev = q.device
     _on_current(dev, view, "q")
-    if draft._rows is not None and draft._rows != (rows_shape, dt, dev):
+    rows = draft._rows
+    if rows is not None and rows != (rows_shape, dt, dev):
         raise ValueError(f"drafted rows must be {dt} {list(rows_shape)} on {dev}, got "
-                         f"{draft._rows[1]} {list(draft._rows[0])} on {draft._rows[2]}")
-    _need(draft._keep[3], "count", torch.int32, (batch,), dev)
+                         f"{rows[1]} {list(rows[0])} on {rows[2]}")
+    if draft._keep[3] is not None:
+        _need(draft._keep[3], "count", torch.int32, (batch,), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, shape[:3], dev)
     if out is None:
-        out = torch.empty(q.shape[:3] + (out_width,), dtype=dt, device=dev)
-    else:
-        _need(out, "out", dt, q.shape[:3] + (out_width,), dev)
-    _need(lse, "lse", torch.float32, q.shape[:3], dev)
+        if out_width == width:
+            return torch.empty_like(q)
+        return torch.empty((batch, shape[1], shape[2], out_width), dtype=dt, device=dev)
+    _need(out, "out", dt, shape[:3] + (out_width,), dev)
     return out
 
 
@@ -846,10 +851,9 @@ def kvc_decode_attn_tree(q: torch.Tensor, cache: kvc_cache, draft: kvc_draft, *,
     c = cache
     out = _attn_args(q, c, c.d_head, c.d_head, c.dtype, c.batch, draft,
                      (c.batch, draft.n_draft, c.n_heads_kv, c.d_head), out, lse)
-    if len is not None and len.dim() == 2:
-        _need(len, "len", torch.int32, (c.batch, c.n_heads_kv), q.device)
-    else:
-        _need(len, "len", torch.int32, (c.batch * c.n_heads_kv,), q.device)
+    if len is not None:
+        _need(len, "len", torch.int32, (c.batch, c.n_heads_kv) if len.dim() == 2 else
+              (c.batch * c.n_heads_kv,), q.device)
     if ws is None:
         ws = tree_workspace(c.batch, q.shape[2], c.n_heads_kv, c.d_head, draft.n_draft, q.dtype,
                             q.device)
