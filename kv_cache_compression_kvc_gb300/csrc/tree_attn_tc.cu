@@ -15,6 +15,11 @@
 //   none for S), and the value rows are used as they lie in memory (V^T is the MN-major A
 //   operand).  P goes through shared memory as the K-major B operand, rounded to bf16: the weights
 //   are off by at most 2^-8 each, as is the bf16 output.
+//   With 128 rows of an ordinary cache of up to 128 dims (PT below) O is kept by row instead and P
+//   goes through tensor memory as the A operand (O += P V): that leaves shared memory for a third
+//   tile in flight, a row's O is in its own thread's lane, and two P buffers let the softmax of two
+//   tiles run side by side.  512 rows a pair, 8 x 8192 slots, 128 dims: 282 us, without it 300.
+//   With 256 dims (64-slot tiles, short budgets) it was the slower one, 36 us for 31.
 //   A latent cache's tile is loaded once and serves as K (all of it) and V (its first d_latent
 //   columns).
 //   The running maximum is lazy: a tile whose logits stay below max + 8 (log2 units) keeps the old
@@ -68,7 +73,8 @@ struct Plan {
     static constexpr int SM = RN < 64 ? 64 : RN;             // M of S (rows past RN: not used)
     static constexpr int UD = DV < 128 ? 64 : 128;           // dims per ring unit
     static constexpr int TS = LATENT || DV == 256 ? 64 : 128;   // slots per tile
-    static constexpr int SETS = TS / 32;                     // softmax sets of four warps
+    static constexpr bool PT = RN == 128 && DV <= 128 && !LATENT;   // P in tensor memory, O by row
+    static constexpr int SETS = PT ? 2 : TS / 32;            // softmax sets of four warps
     static constexpr int SOFTMAX = 128 * SETS;               // softmax threads
     static constexpr int THREADS = 64 + SOFTMAX;
     static constexpr int SUB = TS * 128;                     // [TS slots][64 dims]
@@ -80,9 +86,9 @@ struct Plan {
     static constexpr int MB = DV / UD;                       // blocks of O^T
     static constexpr int QSUBS = DKP / 64;
     static constexpr int Q_BYTES = QSUBS * RN * 128;
-    static constexpr int P_BYTES = TS / 64 * RN * 128;
+    static constexpr int P_BYTES = PT ? 0 : TS / 64 * RN * 128;
     static constexpr int ROPE = LATENT ? 2 * SUB : 0;        // two tiles' rope parts
-    static constexpr int SMALL = 640 + (1 + SETS) * RN * 4;         // barriers, flags, row values
+    static constexpr int SMALL = 640 + (PT ? 2 : 1 + SETS) * RN * 4;         // barriers, flags, row values
     static constexpr int FIT = (kSmemMax - 1024 - Q_BYTES - P_BYTES - ROPE - SMALL) / UNIT;
     static constexpr int NU = FIT > 16 ? 16 : FIT;           // ring units
     // A latent tile's copies complete on one barrier (its units are keys and values at once), ring
@@ -91,8 +97,8 @@ struct Plan {
     // S of tile t + 1 is issued before the values of tile t are used
     static_assert(NU >= 2 * KU, "ring too small");
     static constexpr int SMEM = 1024 + Q_BYTES + P_BYTES + ROPE + NU * UNIT + SMALL;
-    static constexpr int O_COLS = MB * RN;
-    static constexpr int USED = O_COLS + 2 * TS;
+    static constexpr int O_COLS = PT ? DV : MB * RN;
+    static constexpr int USED = O_COLS + 2 * TS + (PT ? TS : 0);
     static constexpr uint32_t COLS = USED > 256 ? 512 : 256;
     static_assert(USED <= 512, "tensor memory");
 };
@@ -104,6 +110,59 @@ struct Plan {
 struct Maps {
     CUtensorMap q, k, v, kd, vd, rq, rk, rd;
 };
+
+// The values that are not finite among the drafted tokens that row r of the row tile sees (nf: the
+// tokens that have some), added as they are to what this thread wrote of dimension d of the row: such
+// a value leaves nothing else of it.  Hardly ever called, so kept out of the loop that writes.
+template <int RN, int DV>
+__device__ __forceinline__ void add_stray(const TreeParams &p, const TreeSeg &s, size_t part, int r0, int r,
+                                          int d, unsigned long long nf)
+{
+    const int tok = (r0 + r) / p.G, h = s.kh * p.G + (r0 + r) - tok * p.G;
+    const long long stride = (long long)p.Hkv * p.DK;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.vd) + (size_t)s.b * p.T * stride +
+                             (size_t)s.kh * p.DK + d;
+    float y = 0.f;
+    for (unsigned long long hit = nf & tree_mask_word(p, s.b, tok, s.cnt); hit; hit &= hit - 1) {
+        const float z = __bfloat162float(v[(__ffsll((long long)hit) - 1) * stride]);
+        if (!(fabsf(z) <= 3.402823466e38f)) y += z;
+    }
+    if (y == 0.f) return;
+    if (s.whole()) {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + (((size_t)s.b * p.T + tok) * p.Hq + h) * DV + d;
+        *o = __float2bfloat16(__bfloat162float(*o) + y);
+    } else {
+        p.ws_o[(part * RN + r) * DV + d] += y;
+    }
+}
+
+// Zeroes the value rows [valid, depth) of a unit and, in the drafted tokens' tile, every value that
+// is not finite (its row goes into *nf).  Called by `warps` warps, w the caller's number: a warp
+// takes a row, eight lanes per 64 dims.
+template <int SUBS, int SUB>
+__device__ __forceinline__ void clean_unit(unsigned char *base, int w, int warps, int valid, int depth,
+                                           bool draft, unsigned long long *nf)
+{
+    const int lane = threadIdx.x & 31, sub = lane >> 3;
+    if (sub >= SUBS) return;
+    uint4 *at = reinterpret_cast<uint4 *>(base + sub * SUB + (lane & 7) * 16);
+    for (int r = valid + w; r < depth; r += warps) at[r * 8] = make_uint4(0, 0, 0, 0);
+    if (!draft) return;
+    for (int r = w; r < valid; r += warps) {
+        uint4 x = at[r * 8];
+        uint32_t bad = 0;
+        auto fix = [&](uint32_t y) {
+            if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u, bad = 1;
+            if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu, bad = 1;
+            return y;
+        };
+        x.x = fix(x.x); x.y = fix(x.y); x.z = fix(x.z); x.w = fix(x.w);
+        if (bad) {
+            at[r * 8] = x;
+            atomicOr(nf, 1ull << r);
+        }
+    }
+}
 
 template <int DKP, int DV, bool LATENT, int RN>
 __global__ void __launch_bounds__(Plan<DKP, DV, LATENT, RN>::THREADS, 1)
@@ -124,8 +183,8 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     const uint32_t b_full = bars, b_empty = b_full + 8 * NTB;
     const uint32_t b_rope_empty = b_empty + 8 * NU;
     const uint32_t b_q_full = b_rope_empty + 16, b_q_empty = b_q_full + 8;
-    const uint32_t b_s_full = b_q_empty + 8, b_s_empty = b_s_full + 16;
-    const uint32_t b_p_full = b_s_empty + 16, b_pv = b_p_full + 8, b_done = b_pv + 8;
+    const uint32_t b_s_full = b_q_empty + 8;
+    const uint32_t b_p_full = b_s_full + 16, b_pv = b_p_full + 16, b_done = b_pv + 16;
     const uint32_t tmem_slot = b_done + 8;
     unsigned char *small = smem_raw + (bars - raw) + 512;
     unsigned long long *s_nf2 = reinterpret_cast<unsigned long long *>(small);
@@ -145,10 +204,9 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_rope_empty + 8 * i, 1);
             mbar_init(b_s_full + 8 * i, 1);
-            mbar_init(b_s_empty + 8 * i, 4 * kSets);
+            mbar_init(b_p_full + 8 * i, PL::PT ? 4 : 4 * kSets);
+            mbar_init(b_pv + 8 * i, 1);
         }
-        mbar_init(b_p_full, 4 * kSets);
-        mbar_init(b_pv, 1);
         mbar_init(b_done, 1);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -159,7 +217,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     tc::fence_after();
     uint32_t tmem;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot));
-    const uint32_t tO = tmem, tS = tmem + PL::O_COLS;
+    const uint32_t tO = tmem, tS = tmem + PL::O_COLS, tP = tS + 2 * TS;
 
     pdl_trigger();
     pdl_wait();
@@ -281,7 +339,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     } else if (warp == 1) {
         // ================================ products ================================================
         constexpr uint32_t id_s = tc::idesc(PL::SM, TS, false);
-        constexpr uint32_t id_o = tc::idesc(UD, RN, true);
+        constexpr uint32_t id_o = PL::PT ? tc::idesc_b_mn(RN, UD) : tc::idesc(UD, RN, true);
         TreeWalk walk(p, range);
         TreeSeg s, nx;
         auto next_seg = [&](TreeSeg &x) {
@@ -301,7 +359,8 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         };
         auto scores = [&](const TreeSeg &x, int tile, unsigned n) {
             const uint32_t buf = n & 1;
-            if (n >= 2) wait(b_s_empty + 8 * buf, ((n >> 1) - 1) & 1);
+            // (this S buffer has been read: the weights of the tile before last, which were waited
+            // for, came from it)
             if (tile == x.lo) {
                 wait(b_q_full, seg_no & 1);
                 ++seg_no;
@@ -369,7 +428,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 ahead = __shfl_sync(0xffffffffu, (int)tc::test(b_full + 8 * last, ph), 0) != 0;
             }
             if (ahead) scores(s, tile + 1, n + 1);
-            // O^T += V^T P^T
+            // O^T += V^T P^T, or O += P V
             const int steps = steps_of(s, tile);
             uint32_t src[MB], bar[MB];
 #pragma unroll
@@ -379,20 +438,27 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 bar[m] = b_empty + 8 * v_slot;
                 step(v_slot, v_ph, 1);
             }
-            wait(b_p_full, n & 1);
+            if constexpr (PL::PT) wait(b_p_full + 8 * (n & 1), (n >> 1) & 1);
+            else wait(b_p_full, n & 1);
             tc::fence_after();
             if (tc::elect()) {
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
 #pragma unroll
                     for (int ks = 0; ks < TS / 16; ++ks)
-                        if (ks < steps)
-                            tc::mma(tO + m * RN, tc::desc(src[m] + ks * 2048, SUB, 1024),
-                                    tc::desc_k(sP + (ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
-                                    tile > s.lo || ks > 0);
+                        if (ks < steps) {
+                            if constexpr (PL::PT)
+                                tc::mma_ta(tO + m * UD, tP + (n & 1) * (TS / 2) + ks * 8,
+                                           tc::desc(src[m] + ks * 2048, SUB, 1024), id_o,
+                                           tile > s.lo || ks > 0);
+                            else
+                                tc::mma(tO + m * RN, tc::desc(src[m] + ks * 2048, SUB, 1024),
+                                        tc::desc_k(sP + (ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
+                                        tile > s.lo || ks > 0);
+                        }
                     tc::commit(bar[m]);
                 }
-                tc::commit(b_pv);
+                tc::commit(b_pv + (PL::PT ? 8 * (n & 1) : 0));
             }
             __syncwarp();
             if (!LATENT) step(v_slot, v_ph, KU);             // past the next tile's keys
@@ -409,6 +475,233 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 }
             }
         }
+    } else if constexpr (PL::PT) {
+        // ================================ softmax, outputs: P in tensor memory ====================
+        // Set 0 takes the even tiles, set 1 the odd ones; a row is one thread's in either set, and
+        // its row of O in the same lane, so only the two warps of the same 32 rows have to agree.
+        // The rows' running maxima (shared memory) move in tile order: the warp of tile n passes
+        // its partner a token (named barrier) once tile n's are final; a warp whose weights refer
+        // to an older maximum by then computes them again.
+        const int set = (warp - 2) / 4;
+        const int q4 = warp & 3;                             // lanes 32 q4 .. of tensor memory
+        const int row = q4 * 32 + lane;
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        const int token = kBar + 1 + q4;                     // + 4 * set
+        volatile float *v_max = s_fac + RN;
+        if (set == 0) v_max[row] = kNegBig;
+        tc::bar_sync(kBar, kSoftmax);
+        TreeWalk walk(p, range);
+        TreeSeg s, nx;
+        int4 note = make_int4(-1, 0, 0, 0);
+        unsigned n = 0, seg_no = 0;
+        uint32_t v_unit = KU;                                // this tile's first value unit
+        const int r0 = rt * p.RP;
+        const int tok = (r0 + row) / p.G, hg_row = (r0 + row) - tok * p.G;
+        auto next_seg = [&]() {                              // (row tile 0 has rows in every pair)
+            while (walk.next(p, rt, TS, nx))
+                if (nx.rows > 0) return true;
+            return false;
+        };
+        bool more = next_seg();
+        while (more) {
+            s = nx;
+            more = next_seg();
+            tree_note_split(p, range, g, s, note);
+            const bool mine = row < s.rows;
+            const bool any = q4 * 32 < s.rows;               // warp-uniform
+            float l = 0.f, l_ref = kNegBig;                  // sum over this set's tiles, its reference
+            const uint64_t word = mine && s.hi == s.nt ? tree_mask_word(p, s.b, tok, s.cnt) : 0ull;
+            unsigned long long *s_nf = s_nf2 + (seg_no++ & 1);
+            for (int tile = s.lo; tile < s.hi; ++tile, ++n, v_unit += PER) {
+                if ((int)(n & 1) != set) continue;
+                const bool draft = s.is_draft(p, tile);
+                const int valid = s.valid(p, tile, TS);
+                const bool masked = draft || valid < TS;
+                float mx = -INFINITY, m = kNegBig, z = 0.f;
+                uint32_t w[TS / 2];                          // the row's weights, bf16 pairs
+                // 64 logits of the row, masked ones -inf (and then scaled: returns the scale to use)
+                auto logits = [&](int half, float *x) -> float {
+                    tc::ld32(tS + set * TS + lanes + 64 * half, x);
+                    tc::ld32(tS + set * TS + lanes + 64 * half + 32, x + 32);
+                    tc::wait_ld();
+                    if (!masked) return p.scale_log2;
+                    const int v = valid - 64 * half;
+                    const uint64_t see = draft ? (half == 0 ? word : 0ull)
+                                               : v >= 64 ? ~0ull : v <= 0 ? 0ull : (1ull << v) - 1ull;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        x[c] = (see >> c) & 1ull ? x[c] * p.scale_log2 : -INFINITY;
+                    return 1.f;
+                };
+                wait(b_s_full + 8 * set, (n >> 1) & 1);
+                tc::fence_after();
+                if (any) {
+#pragma unroll
+                    for (int half = 0; half < TS / 64; ++half) {
+                        float x[64];
+                        const float scale = logits(half, x);
+                        // the largest scaled logit: of the smallest value when the scale is negative
+                        float a[4] = {x[0], x[1], x[2], x[3]};
+                        if (scale >= 0.f) {
+#pragma unroll
+                            for (int c = 4; c < 64; ++c) a[c & 3] = fmaxf(a[c & 3], x[c]);
+                            mx = fmaxf(mx, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * scale);
+                        } else {
+#pragma unroll
+                            for (int c = 4; c < 64; ++c) a[c & 3] = fminf(a[c & 3], x[c]);
+                            mx = fmaxf(mx, fminf(fminf(a[0], a[1]), fminf(a[2], a[3])) * scale);
+                        }
+                    }
+                    // weights against the maximum as it stands, or this tile's where it rises
+                    m = v_max[row];
+                    if (mx > m + kSlack) m = mx;
+                }
+                float m_cur = kNegBig, m_fin = kNegBig;
+                bool rise = false;
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    if (any) {
+                        z = 0.f;
+#pragma unroll
+                        for (int half = 0; half < TS / 64; ++half) {
+                            float x[64];
+                            const float scale = logits(half, x);
+                            const float2 sc = make_float2(scale, scale), mm = make_float2(-m, -m);
+                            float2 z0 = make_float2(0.f, 0.f), z1 = z0;
+#pragma unroll
+                            for (int c = 0; c < 64; c += 4) {
+                                float2 y0 = __ffma2_rn(make_float2(x[c], x[c + 1]), sc, mm);
+                                float2 y1 = __ffma2_rn(make_float2(x[c + 2], x[c + 3]), sc, mm);
+                                y0.x = ex2(y0.x);
+                                y0.y = ex2(y0.y);
+                                y1.x = ex2(y1.x);
+                                y1.y = ex2(y1.y);
+                                z0 = __fadd2_rn(z0, y0);
+                                z1 = __fadd2_rn(z1, y1);
+                                w[32 * half + c / 2] = tc::pack_bf16(y0.x, y0.y);
+                                w[32 * half + c / 2 + 1] = tc::pack_bf16(y1.x, y1.y);
+                            }
+                            z0 = __fadd2_rn(z0, z1);
+                            z += z0.x + z0.y;
+                        }
+                    }
+                    if (pass == 1) break;
+                    // the maxima up to the tile before are final
+                    if (n > 0) tc::bar_sync(token + 4 * (set ^ 1), 64);
+                    m_cur = v_max[row];
+                    rise = mine && mx > m_cur + kSlack;
+                    m_fin = rise ? m : m_cur;
+                    if (!__any_sync(0xffffffffu, mine && m != m_fin)) break;
+                    m = m_fin;
+                }
+                if (rise) v_max[row] = m_fin;
+                __threadfence_block();
+                __syncwarp();
+                if (more || tile + 1 < s.hi) tc::bar_arrive(token + 4 * set, 64);
+                if (tile > s.lo && __any_sync(0xffffffffu, rise)) {
+                    wait(b_pv + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
+                    tc::fence_after();
+                    const float f = rise ? ex2(m_cur - m_fin) : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < DV; c += 16) {
+                        float o[16];
+                        tc::ld16(tO + lanes + c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] *= f;
+                        tc::st16(tO + lanes + c, o);
+                    }
+                }
+                l = l * ex2(l_ref - m_fin) + z;
+                l_ref = m_fin;
+                if (n >= 2) wait(b_pv + 8 * (n & 1), ((n - 2) >> 1) & 1);   // this P buffer is used up
+                tc::fence_after();
+                if (any) {
+#pragma unroll
+                    for (int half = 0; half < TS / 64; ++half)
+                        tc::st32(tP + set * (TS / 2) + lanes + 32 * half, w + 32 * half);
+                }
+                tc::wait_st();
+                // value rows past the valid ones, and a drafted token's non-finite values
+                const int depth = steps_of(s, tile) * 16;
+                if (valid < depth || draft) {
+                    if (draft) {
+                        if (q4 == 0 && lane == 0) *s_nf = 0ull;
+                        tc::bar_sync(kBar + 9 + set, 128);
+                    }
+                    for (int u = 0; u < MB; ++u) {
+                        const unsigned un = v_unit + u;
+                        const uint32_t slot = un % NU;
+                        wait(b_full + 8 * slot, (un / NU) & 1);
+                        clean_unit<SUBS, SUB>(smem_raw + (ring + slot * UNIT - raw), q4, 4, valid, depth, draft, s_nf);
+                    }
+                }
+                tc::fence_async();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_p_full + 8 * set);
+            }
+            // this part's outputs: O / l, or the partial state
+            const bool whole = s.whole();
+            const size_t part = (size_t)blockIdx.x * 2 + (s.first ? 0 : 1);
+            wait(b_pv + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
+            tc::fence_after();
+            const float m = v_max[row];
+            l *= ex2(l_ref - m);
+            if (set == 1) s_fac[row] = l;
+            tc::bar_sync(kBar, kSoftmax);
+            if (set == 0) {
+                l += s_fac[row];
+                v_max[row] = kNegBig;                        // for the next pair
+                s_fac[row] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                if (mine) {
+                    if (!whole) {
+                        p.ws_ml[(part * RN + row) * 2] = m;
+                        p.ws_ml[(part * RN + row) * 2 + 1] = l;
+                    } else if (p.lse != nullptr) {
+                        p.lse[((size_t)s.b * p.T + tok) * p.Hq + s.kh * p.G + hg_row] =
+                            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                    }
+                }
+            }
+            tc::bar_sync(kBar, kSoftmax);
+            const unsigned long long nf = p.kd != nullptr && s.hi == s.nt ? *s_nf : 0ull;
+            const float f = s_fac[row];
+            if (any) {
+#pragma unroll 1
+                for (int c = set * (DV / 2); c < (set + 1) * (DV / 2); c += 16) {
+                    float o[16];
+                    __syncwarp();
+                    tc::ld16(tO + lanes + c, o);
+                    tc::wait_ld();
+                    if (!mine) continue;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] *= f;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(
+                            static_cast<__nv_bfloat16 *>(p.out) +
+                            (((size_t)s.b * p.T + tok) * p.Hq + s.kh * p.G + hg_row) * DV + c);
+                        dst[0] = make_uint4(tc::pack_bf16(o[0], o[1]), tc::pack_bf16(o[2], o[3]),
+                                            tc::pack_bf16(o[4], o[5]), tc::pack_bf16(o[6], o[7]));
+                        dst[1] = make_uint4(tc::pack_bf16(o[8], o[9]), tc::pack_bf16(o[10], o[11]),
+                                            tc::pack_bf16(o[12], o[13]), tc::pack_bf16(o[14], o[15]));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.ws_o + (part * RN + row) * DV + c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                }
+                if (nf && mine)
+#pragma unroll 1
+                    for (int d = set * (DV / 2); d < (set + 1) * (DV / 2); ++d)
+                        add_stray<RN, DV>(p, s, part, r0, row, d, nf);
+            }
+            __syncwarp();
+            tc::fence_before();
+            tc::bar_sync(kBar, kSoftmax);                    // O is free for the next pair
+        }
+        if (rt == 0 && set == 0 && row == 0) p.ws_info[g] = note;
     } else {
         // ================================ softmax, outputs ========================================
         // Set i takes slots 32 i .. 32 i + 31 of a tile: a row has a thread in each set, which keep
@@ -424,20 +717,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         const int dim = UD == 128 ? ln : (lane < 16 ? q4 * 16 + lane : UD);
         const int row_lo = RN == 128 ? q4 * 32 : q4 * 16;    // first row of this warp
         const int c0 = set * HC;                             // first slot
-        // what a row of token t gets in dimension d from the drafted tokens whose values are not
-        // finite (bits of nf): those that it sees, as they are
-        auto stray = [&](unsigned long long nf, int t, int d, const TreeSeg &x) -> float {
-            float y = 0.f;
-            unsigned long long hit = nf & tree_mask_word(p, x.b, t, x.cnt);
-            while (hit) {
-                const int i = __ffsll((long long)hit) - 1;
-                hit &= hit - 1;
-                const float z = __bfloat162float(static_cast<const __nv_bfloat16 *>(
-                    p.vd)[(((size_t)x.b * p.T + i) * p.Hkv + x.kh) * p.DK + d]);
-                if (!(fabsf(z) <= 3.402823466e38f)) y += z;
-            }
-            return y;
-        };
         TreeWalk walk(p, range);
         TreeSeg s;
         int4 note = make_int4(-1, 0, 0, 0);
@@ -474,9 +753,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     for (int c = 0; c < HC; c += 32) tc::ld32(tS + buf * TS + lanes + c0 + c, x + c);
                     tc::wait_ld();
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(b_s_empty + 8 * buf);
                 if (any) {
                     if (draft || valid < TS) {               // masked: scaled here, once
                         uint32_t see;                        // slots c0 .. c0 + 31
@@ -567,28 +843,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                         const uint32_t slot = un % NU;
                         if (!LATENT) wait(b_full + 8 * slot, (un / NU) & 1);   // (S implies a latent tile)
                         unsigned char *base = smem_raw + (ring + slot * UNIT - raw);
-                        // a warp takes a row: eight lanes per 64 dims
-                        const int sub = lane >> 3;
-                        uint4 *at = reinterpret_cast<uint4 *>(base + sub * SUB + (lane & 7) * 16);
-                        for (int r = valid + warp - 2; r < depth; r += kSoftmax / 32)
-                            if (sub < SUBS) at[r * 8] = make_uint4(0, 0, 0, 0);
-                        if (draft) {
-                            for (int r = warp - 2; r < valid; r += kSoftmax / 32) {
-                                if (sub >= SUBS) continue;
-                                uint4 w = at[r * 8];
-                                uint32_t bad = 0;
-                                auto fix = [&](uint32_t y) {
-                                    if ((y & 0x7f80u) == 0x7f80u) y &= 0xffff0000u, bad = 1;
-                                    if ((y & 0x7f800000u) == 0x7f800000u) y &= 0xffffu, bad = 1;
-                                    return y;
-                                };
-                                w.x = fix(w.x); w.y = fix(w.y); w.z = fix(w.z); w.w = fix(w.w);
-                                if (bad) {
-                                    at[r * 8] = w;
-                                    atomicOr(s_nf, 1ull << r);
-                                }
-                            }
-                        }
+                        clean_unit<SUBS, SUB>(base, warp - 2, kSoftmax / 32, valid, depth, draft, s_nf);
                     }
                     drafts |= draft;
                 }
@@ -639,11 +894,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 }
                 const int t = token_of(r0 + ra);
                 int hg = (r0 + ra) - t * p.G;
-                if (nf) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < here) o[j] += stray(nf, token_of(r0 + ra + j), d, s);
-                }
                 if (whole) {
                     __nv_bfloat16 *dst =
                         static_cast<__nv_bfloat16 *>(p.out) +
@@ -663,6 +913,12 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                         if (j < here) dst[j * DV] = o[j];
                 }
             }
+            if (nf && dim < UD)
+#pragma unroll 1
+                for (int c = set * 16; c < MB * RN; c += kSets * 16)
+#pragma unroll 1
+                    for (int ra = c & (RN - 1); ra < min((c & (RN - 1)) + 16, s.rows); ++ra)
+                        add_stray<RN, DV>(p, s, part, r0, ra, c / RN * UD + dim, nf);
             __syncwarp();
             tc::fence_before();
         }
