@@ -39,16 +39,18 @@ __device__ __forceinline__ void fence_async()
 // Shared-memory matrix descriptor, 128-byte swizzle: 8 lines of 128 bytes form an atom of 1024.
 // K-major operand: atoms of 8 rows, sbo = 1024 between them (lbo unused).  MN-major operand: an
 // atom is 8 steps of K by 64 elements of M; sbo between atoms along K, lbo between atoms along M.
-__device__ __forceinline__ uint64_t desc(uint32_t saddr, uint32_t lbo, uint32_t sbo)
+// The words of a descriptor are kept apart: the upper one is a constant, and a step of `bytes` along
+// the operand adds bytes >> 4 to the lower one (shared memory ends below 2^18, so the sum stays in its
+// 14 bits), which is one instruction between two products.
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ Desc operator+(uint32_t bytes) const { return {lo + (bytes >> 4), hi}; }
+};
+__device__ __forceinline__ Desc desc(uint32_t saddr, uint32_t lbo, uint32_t sbo)
 {
-    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+    return {((saddr >> 4) & 0x3FFFu) | (lbo >> 4) << 16, (sbo >> 4) | 1u << 14 | 2u << 29};
 }
-__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) { return desc(saddr, 16, 1024); }
+__device__ __forceinline__ Desc desc_k(uint32_t saddr) { return desc(saddr, 16, 1024); }
 // Instruction descriptor: bf16 x bf16 -> fp32, M x N; a_mn: A is MN-major.
 constexpr uint32_t idesc(int M, int N, bool a_mn)
 {
@@ -65,22 +67,22 @@ __device__ __forceinline__ bool elect()
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
     return r != 0;
 }
-__device__ __forceinline__ void mma(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc)
+__device__ __forceinline__ void mma(uint32_t tmem_d, Desc a, Desc b, uint32_t id, uint32_t acc)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n"
+        " mov.b64 b, {%3, %4};\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(tmem_d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(id), "r"(acc)
         : "memory");
 }
 // A from tensor memory (K-major: a column holds two elements of a row), B MN-major.
 constexpr uint32_t idesc_b_mn(int M, int N) { return idesc(M, N, false) | (1u << 16); }
-__device__ __forceinline__ void mma_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t id, uint32_t acc)
+__device__ __forceinline__ void mma_ta(uint32_t tmem_d, uint32_t tmem_a, Desc b, uint32_t id, uint32_t acc)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(b), "r"(id), "r"(acc)
+        "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "r"(b.lo), "r"(b.hi), "r"(id), "r"(acc)
         : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar)

@@ -18,7 +18,8 @@
 //   With 128 rows of an ordinary cache of up to 128 dims (PT below) O is kept by row instead and P
 //   goes through tensor memory as the A operand (O += P V): that leaves shared memory for a third
 //   tile in flight, a row's O is in its own thread's lane, and two P buffers let the softmax of two
-//   tiles run side by side.  512 rows a pair, 8 x 8192 slots, 128 dims: 282 us, without it 300.
+//   tiles run side by side.  16 pairs of 131072 slots, 256 rows each, 128 dims: 282 us, without
+//   it 300.
 //   With 256 dims (64-slot tiles, short budgets) it was the slower one, 36 us for 31.
 //   A latent cache's tile is loaded once and serves as K (all of it) and V (its first d_latent
 //   columns).
@@ -230,8 +231,10 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             record_code(p.dev_code, kDevCodeTimeout);
         }
     };
-    // slots of tile i rounded up to the product's depth of 16 (at least one step)
+    // slots of tile i rounded up to the product's depth of 16 (at least one step); all of them with
+    // PT, where the issuing warp's instructions count for more than a last tile's products
     auto steps_of = [&](const TreeSeg &s, int i) {
+        if constexpr (PL::PT) return TS / 16;
         const int v = s.valid(p, i, TS);
         return v > 16 ? (v + 15) / 16 : 1;
     };
@@ -357,121 +360,161 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 ph ^= 1;
             }
         };
-        auto scores = [&](const TreeSeg &x, int tile, unsigned n) {
-            const uint32_t buf = n & 1;
-            // (this S buffer has been read: the weights of the tile before last, which were waited
-            // for, came from it)
-            if (tile == x.lo) {
-                wait(b_q_full, seg_no & 1);
-                ++seg_no;
-            }
-            // every unit has arrived, then one block of products: each wait, fence and pick of a
-            // lane between products costs the tensor cores about 300 clocks
-            uint32_t src[KU], bar[KU];
-            if constexpr (LATENT) {
-                wait(b_full + 8 * t_slot, t_ph);
-                if (++t_slot == NTB) {
-                    t_slot = 0;
-                    t_ph ^= 1;
+        // One loop with one place for either product (each is a long run of unrolled instructions,
+        // which a block has to fetch before it first runs them): n_s tiles have their S issued, n_o
+        // their values' product, at most two apart.  PT, where the tensor cores count: if a tile's
+        // weights and the keys of the tile after the next are there, both products are one run, since
+        // each wait, fence and pick of a lane between products costs about 300 clocks (284 us for 302;
+        // with few rows the same costs 1 us in 30, and with latent rows 100 us for 93).
+        // `due`: the steps of the oldest product of values to come, times 2, plus 1 where O begins;
+        // the next one's in the upper half.
+        bool more = next_seg(s), more_nx = false;
+        int tile = more ? s.lo : 0;
+        unsigned n_s = 0, n_o = 0;
+        uint32_t due = 0;
+        while (more || n_o < n_s) {
+            const bool begins = tile == s.lo;
+            // Waits first look at all their barriers at once: a wait for one that has long completed
+            // takes some 200 clocks, in which the tensor cores run dry.
+            // The next tile's keys (and, where a pair begins, its queries) have arrived:
+            auto keys = [&] {
+                bool in = true;
+                if constexpr (LATENT) {
+                    in = tc::test(b_full + 8 * t_slot, t_ph);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < KU; ++u) {
+                        const bool wrap = k_slot + u >= NU;
+                        in &= tc::test(b_full + 8 * (wrap ? k_slot + u - NU : k_slot + u), wrap ? k_ph ^ 1 : k_ph);
+                    }
                 }
+                if (begins) in &= tc::test(b_q_full, seg_no & 1);
+                return in;
+            };
+            // One tile ahead: its S goes first, so that its softmax overlaps the values' product.
+            // With a ring of two tiles, or where the next pair begins, only if it has arrived, since
+            // waiting for it here would hold up the product that frees the ring.
+            bool score = more && n_s - n_o < 2, there = false;
+            if (score) {
+                there = __all_sync(0xffffffffu, keys());
+                if (n_s > n_o && (NU < 3 * PER || begins)) score = there;
             }
+            const bool values = !score;
+            uint32_t vsrc[MB], vbar[MB];
+            if (values) {
+                const uint32_t p_bar = b_p_full + (PL::PT ? 8 * (n_o & 1) : 0);
+                const uint32_t p_ph = (PL::PT ? n_o >> 1 : n_o) & 1;
+                const uint32_t slot0 = v_slot, ph0 = v_ph;
+                bool in = tc::test(p_bar, p_ph);
 #pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                if (!LATENT) wait(b_full + 8 * k_slot, k_ph);
-                src[u] = ring + k_slot * UNIT;
-                bar[u] = b_empty + 8 * k_slot;
-                step(k_slot, k_ph, 1);
+                for (int m = 0; m < MB; ++m) {
+                    if (!LATENT) in &= tc::test(b_full + 8 * v_slot, v_ph);
+                    vsrc[m] = ring + v_slot * UNIT;
+                    vbar[m] = b_empty + 8 * v_slot;
+                    step(v_slot, v_ph, 1);
+                }
+                if (!LATENT) step(v_slot, v_ph, KU);         // past the next tile's keys
+                if constexpr (PL::PT) there = more && keys();
+                in = __all_sync(0xffffffffu, in);
+                if (!in) {
+                    if constexpr (!LATENT) {
+                        uint32_t slot = slot0, ph = ph0;
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) {
+                            wait(b_full + 8 * slot, ph);
+                            step(slot, ph, 1);
+                        }
+                    }
+                    wait(p_bar, p_ph);
+                    if constexpr (PL::PT) there = more && keys();
+                }
+                if constexpr (PL::PT) score = there = __all_sync(0xffffffffu, there);
             }
-            tc::fence_after();
-            const uint32_t d = tS + buf * TS;
-            if (tc::elect()) {
-                if (rope) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma(d, tc::desc_k(sQ + KU * SUBS * RN * 128 + kk * 32),
-                                tc::desc_k(sR + buf * SUB + kk * 32), id_s, kk > 0);
-                    tc::commit(b_rope_empty + 8 * buf);
+            uint32_t ksrc[KU], kbar[KU];
+            if (score) {
+                // (its S buffer has been read: the weights of the tile before last, which were
+                // waited for, came from it)
+                if (!there && begins) wait(b_q_full, seg_no & 1);
+                if constexpr (LATENT) {
+                    if (!there) wait(b_full + 8 * t_slot, t_ph);
+                    if (++t_slot == NTB) {
+                        t_slot = 0;
+                        t_ph ^= 1;
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
+                    if (!LATENT && !there) wait(b_full + 8 * k_slot, k_ph);
+                    ksrc[u] = ring + k_slot * UNIT;
+                    kbar[u] = b_empty + 8 * k_slot;
+                    step(k_slot, k_ph, 1);
+                }
+                if (!LATENT) step(k_slot, k_ph, KU);         // past the values
+            }
+            tc::fence_after();
+            const uint32_t buf = n_s & 1, d = tS + buf * TS;
+            if (tc::elect()) {
+                if (values) {                                // O^T += V^T P^T, or O += P V
+                    const int steps = PL::PT ? TS / 16 : (int)((due & 0xffffu) >> 1);
+                    const tc::Desc dp = tc::desc_k(sP);
 #pragma unroll
-                    for (int i = 0; i < SUBS; ++i)
+                    for (int m = 0; m < MB; ++m) {
+                        const tc::Desc dv = tc::desc(vsrc[m], SUB, 1024);
+#pragma unroll
+                        for (int ks = 0; ks < TS / 16; ++ks)
+                            if (ks < steps) {
+                                if constexpr (PL::PT)
+                                    tc::mma_ta(tO + m * UD, tP + (n_o & 1) * (TS / 2) + ks * 8, dv + ks * 2048,
+                                               id_o, !(due & 1u) || ks > 0);
+                                else
+                                    tc::mma(tO + m * RN, dv + ks * 2048,
+                                            dp + ((ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
+                                            !(due & 1u) || ks > 0);
+                            }
+                        tc::commit(vbar[m]);
+                    }
+                    tc::commit(b_pv + (PL::PT ? 8 * (n_o & 1) : 0));
+                }
+                if (score) {
+                    const tc::Desc dq = tc::desc_k(sQ);
+                    if (rope) {
+                        const tc::Desc dr = tc::desc_k(sR + buf * SUB);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            tc::mma(d, tc::desc_k(sQ + (u * SUBS + i) * RN * 128 + kk * 32),
-                                    tc::desc_k(src[u] + i * SUB + kk * 32), id_s,
-                                    rope || u > 0 || i > 0 || kk > 0);
-                    if (!LATENT) tc::commit(bar[u]);
+                            tc::mma(d, dq + (KU * SUBS * RN * 128 + kk * 32), dr + kk * 32, id_s, kk > 0);
+                        tc::commit(b_rope_empty + 8 * buf);
+                    }
+#pragma unroll
+                    for (int u = 0; u < KU; ++u) {
+                        const tc::Desc dk = tc::desc_k(ksrc[u]);
+#pragma unroll
+                        for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc::mma(d, dq + ((u * SUBS + i) * RN * 128 + kk * 32), dk + (i * SUB + kk * 32),
+                                        id_s, rope || u > 0 || i > 0 || kk > 0);
+                        if (!LATENT) tc::commit(kbar[u]);
+                    }
+                    tc::commit(b_s_full + 8 * buf);
+                    if (tile == s.hi - 1) tc::commit(b_q_empty);
                 }
-                tc::commit(b_s_full + 8 * buf);
-                if (tile == x.hi - 1) tc::commit(b_q_empty);
             }
             __syncwarp();
-            if (!LATENT) step(k_slot, k_ph, KU);             // past the values
-        };
-        unsigned n = 0;
-        bool have = next_seg(s), have_nx = have && next_seg(nx);
-        int tile = have ? s.lo : 0;
-        if (have) scores(s, tile, 0);
-        while (have) {
-            const bool more_here = tile + 1 < s.hi;
-            // the next tile's S goes first, so that its softmax overlaps these values' product;
-            // with a ring of two tiles only if it has arrived, since waiting for it here would
-            // hold up the product that frees the ring
-            bool ahead = more_here;
-            if (NU < 3 * PER && more_here) {
-                uint32_t last = LATENT ? t_slot : k_slot + KU - 1, ph = LATENT ? t_ph : k_ph;
-                if (!LATENT && last >= NU) {
-                    last -= NU;
-                    ph ^= 1;
+            if (values) {
+                due >>= 16;
+                ++n_o;
+            }
+            if (score) {
+                due |= ((uint32_t)steps_of(s, tile) * 2u + (begins ? 1u : 0u)) << (n_s > n_o ? 16 : 0);
+                ++n_s;
+                if (begins) {
+                    ++seg_no;
+                    more_nx = next_seg(nx);                  // (its lengths arrive meanwhile)
                 }
-                ahead = __shfl_sync(0xffffffffu, (int)tc::test(b_full + 8 * last, ph), 0) != 0;
-            }
-            if (ahead) scores(s, tile + 1, n + 1);
-            // O^T += V^T P^T, or O += P V
-            const int steps = steps_of(s, tile);
-            uint32_t src[MB], bar[MB];
-#pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                if (!LATENT) wait(b_full + 8 * v_slot, v_ph);
-                src[m] = ring + v_slot * UNIT;
-                bar[m] = b_empty + 8 * v_slot;
-                step(v_slot, v_ph, 1);
-            }
-            if constexpr (PL::PT) wait(b_p_full + 8 * (n & 1), (n >> 1) & 1);
-            else wait(b_p_full, n & 1);
-            tc::fence_after();
-            if (tc::elect()) {
-#pragma unroll
-                for (int m = 0; m < MB; ++m) {
-#pragma unroll
-                    for (int ks = 0; ks < TS / 16; ++ks)
-                        if (ks < steps) {
-                            if constexpr (PL::PT)
-                                tc::mma_ta(tO + m * UD, tP + (n & 1) * (TS / 2) + ks * 8,
-                                           tc::desc(src[m] + ks * 2048, SUB, 1024), id_o,
-                                           tile > s.lo || ks > 0);
-                            else
-                                tc::mma(tO + m * RN, tc::desc(src[m] + ks * 2048, SUB, 1024),
-                                        tc::desc_k(sP + (ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
-                                        tile > s.lo || ks > 0);
-                        }
-                    tc::commit(bar[m]);
-                }
-                tc::commit(b_pv + (PL::PT ? 8 * (n & 1) : 0));
-            }
-            __syncwarp();
-            if (!LATENT) step(v_slot, v_ph, KU);             // past the next tile's keys
-            if (more_here && !ahead) scores(s, tile + 1, n + 1);
-            ++n;
-            ++tile;
-            if (!more_here) {
-                have = have_nx;
-                if (have) {
+                if (++tile == s.hi) {
+                    more = more_nx;
                     s = nx;
                     tile = s.lo;
-                    scores(s, tile, n);
-                    have_nx = next_seg(nx);
                 }
             }
         }
