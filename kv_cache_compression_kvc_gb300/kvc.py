@@ -704,36 +704,46 @@ def kvc_h2o_prefill_select_gqa(q: torch.Tensor, k_prompt: torch.Tensor, *, seq_l
 
 # ------------------------------------------------------------------------------------------
 # Trees of drafted tokens, latent caches.
-def _need(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> None:
+# The checks below run before every launch of a few microseconds: they read each property once, and
+# compare devices by their index (-1 for a CPU tensor) and types by identity.
+_DTYPES = {KVC_BF16: torch.bfloat16, KVC_F32: torch.float32}
+
+
+def _bad(t: torch.Tensor, what: str, dtype, shape, index) -> None:
+    raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}, "
+                     f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _need(t: Optional[torch.Tensor], what: str, dtype, shape, index: int) -> None:
     """The library reads `t` as a contiguous array of this type and shape: check it first."""
-    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous() or
-                          t.device != device):
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor {list(shape)} on {device}, "
-                         f"got {t.dtype} {list(t.shape)} on {t.device}")
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or
+                          t.get_device() != index):
+        _bad(t, what, dtype, shape, index)
 
 
-def _on_current(device: torch.device, view, what: str) -> None:
+def _on_current(index: int, view, what: str) -> None:
     """The kernels run on the current CUDA device: the tensors, and those of the cache, live there."""
-    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"{what} is on {device}: the current CUDA device is needed")
+    if index < 0 or index != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} is on {'the CPU' if index < 0 else f'cuda:{index}'}: the current "
+                         "CUDA device is needed")
     kept = getattr(view, "_keep", None)
-    kept = kept[0] if isinstance(kept, tuple) else kept
-    if kept is not None and kept.device != device:
-        raise ValueError(f"{what} is on {device}, the cache on {kept.device}")
+    if type(kept) is tuple:
+        kept = kept[0]
+    if kept is not None and kept.get_device() != index:
+        raise ValueError(f"{what} is on cuda:{index}, the cache on {kept.device}")
 
 
-def _raw_stream(device: torch.device, stream) -> int:
+def _raw_stream(index: int, stream) -> int:
     """The cudaStream_t of `stream`, or of the device's current stream (without making the Stream
     object that costs more than the launch)."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _data(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _torch_dtype(code: int) -> torch.dtype:
-    return torch.bfloat16 if code == KVC_BF16 else torch.float32
+def _space(ws: torch.Tensor):
+    """256-byte aligned address inside a workspace tensor and the bytes available after it."""
+    base = ws.data_ptr()
+    aligned = (base + 255) & ~255
+    return aligned, ws.numel() * ws.element_size() - (aligned - base)
 
 
 def make_draft(k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, *,
@@ -756,8 +766,8 @@ def make_draft(k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = Non
         if n_draft is not None and n_draft != k.shape[1]:
             raise ValueError(f"n_draft {n_draft}, but {k.shape[1]} drafted rows")
         d.n_draft = k.shape[1]
-        _need(mask, "mask", torch.int64, k.shape[:2], k.device)
-        _need(count, "count", torch.int32, k.shape[:1], k.device)
+        _need(mask, "mask", torch.int64, k.shape[:2], k.get_device())
+        _need(count, "count", torch.int32, k.shape[:1], k.get_device())
     elif v is not None or n_draft is None:
         raise ValueError("a draft needs its keys, or n_draft alone")
     else:
@@ -770,7 +780,7 @@ def make_draft(k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = Non
     d.k, d.v = (None if x is None else x.data_ptr() for x in (k, v))
     d.mask, d.count = (None if x is None else x.data_ptr() for x in (mask, count))
     d._keep = (k, v, mask, count)   # the descriptor holds their addresses: keep them alive
-    d._rows = None if k is None else (k.shape, k.dtype, k.device)
+    d._rows = None if k is None else (tuple(k.shape), k.dtype, k.get_device())
     return d
 
 
@@ -817,29 +827,29 @@ def latent_workspace(batch, n_heads_q, d_latent, d_rope, n_draft, dtype: torch.d
 
 
 def _attn_args(q, view, width, out_width, code, batch, draft, rows_shape, out, lse):
-    """Checks shared by the draft-tree and latent attention; returns out."""
-    dt = _torch_dtype(code)
+    """Checks shared by the draft-tree and latent attention; returns out and the device's index."""
+    dt = _DTYPES.get(code)
     shape = q.shape
-    if q.dim() != 4 or q.dtype != dt or not q.is_contiguous() or \
-            shape != (batch, draft.n_draft, shape[2], width):
+    if len(shape) != 4 or shape[0] != batch or shape[1] != draft.n_draft or shape[3] != width or \
+            q.dtype is not dt or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous {dt} tensor [{batch}, {draft.n_draft}, "
                          f"n_heads_q, {width}], got {q.dtype} {list(shape)}")
-    dev = q.device
-    _on_current(dev, view, "q")
+    index = q.get_device()
+    _on_current(index, view, "q")
     rows = draft._rows
-    if rows is not None and rows != (rows_shape, dt, dev):
-        raise ValueError(f"drafted rows must be {dt} {list(rows_shape)} on {dev}, got "
-                         f"{rows[1]} {list(rows[0])} on {rows[2]}")
-    if draft._keep[3] is not None:
-        _need(draft._keep[3], "count", torch.int32, (batch,), dev)
+    if rows is None:
+        _need(draft._keep[3], "count", torch.int32, (batch,), index)
+    elif rows != (rows_shape, dt, index):        # (mask and count match the rows)
+        raise ValueError(f"drafted rows must be {dt} {list(rows_shape)} on cuda:{index}, got "
+                         f"{rows[1]} {list(rows[0])} on device {rows[2]}")
     if lse is not None:
-        _need(lse, "lse", torch.float32, shape[:3], dev)
+        _need(lse, "lse", torch.float32, shape[:3], index)
     if out is None:
         if out_width == width:
-            return torch.empty_like(q)
-        return torch.empty((batch, shape[1], shape[2], out_width), dtype=dt, device=dev)
-    _need(out, "out", dt, shape[:3] + (out_width,), dev)
-    return out
+            return torch.empty_like(q), index
+        return torch.empty((batch, shape[1], shape[2], out_width), dtype=dt, device=q.device), index
+    _need(out, "out", dt, shape[:3] + (out_width,), index)
+    return out, index
 
 
 def kvc_decode_attn_tree(q: torch.Tensor, cache: kvc_cache, draft: kvc_draft, *, scale: float,
@@ -849,18 +859,19 @@ def kvc_decode_attn_tree(q: torch.Tensor, cache: kvc_cache, draft: kvc_draft, *,
     """q [B, T, Hq, D] -> out [B, T, Hq, D] (the cache's type): every drafted token over the cached
     slots and the drafted tokens it sees.  len int32 [B, Hkv] (or [B * Hkv])."""
     c = cache
-    out = _attn_args(q, c, c.d_head, c.d_head, c.dtype, c.batch, draft,
-                     (c.batch, draft.n_draft, c.n_heads_kv, c.d_head), out, lse)
+    B, Hkv, D = c.batch, c.n_heads_kv, c.d_head
+    out, index = _attn_args(q, c, D, D, c.dtype, B, draft, (B, draft.n_draft, Hkv, D), out, lse)
     if len is not None:
-        _need(len, "len", torch.int32, (c.batch, c.n_heads_kv) if len.dim() == 2 else
-              (c.batch * c.n_heads_kv,), q.device)
+        _need(len, "len", torch.int32, (B, Hkv) if len.dim() == 2 else (B * Hkv,), index)
     if ws is None:
-        ws = tree_workspace(c.batch, q.shape[2], c.n_heads_kv, c.d_head, draft.n_draft, q.dtype,
-                            q.device)
-    wp, wb = _ws_ptr(ws)
-    _check((_lib or load()).kvc_decode_attn_tree(
-        q.data_ptr(), q.shape[2], c, _data(len), -1 if n_valid is None else n_valid, draft, scale,
-        out.data_ptr(), _data(lse), wp, wb, _raw_stream(q.device, stream)))
+        ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
+    wp, wb = _space(ws)
+    status = (_lib or load()).kvc_decode_attn_tree(
+        q.data_ptr(), q.shape[2], c, None if len is None else len.data_ptr(),
+        -1 if n_valid is None else n_valid, draft, scale, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), wp, wb, _raw_stream(index, stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -870,15 +881,16 @@ def kvc_decode_attn_tree_paged(q: torch.Tensor, pool: kvc_block_pool, pt: kvc_pa
                                lse: Optional[torch.Tensor] = None,
                                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """q [B, T, Hq, D] -> out [B, T, Hq, D] over each sequence's page table and its drafts."""
-    out = _attn_args(q, pool, pool.d_head, pool.d_head, pool.dtype, pt.batch, draft,
-                     (pt.batch, draft.n_draft, pool.n_heads_kv, pool.d_head), out, lse)
+    B, Hkv, D = pt.batch, pool.n_heads_kv, pool.d_head
+    out, index = _attn_args(q, pool, D, D, pool.dtype, B, draft, (B, draft.n_draft, Hkv, D), out, lse)
     if ws is None:
-        ws = tree_workspace(pt.batch, q.shape[2], pool.n_heads_kv, pool.d_head, draft.n_draft,
-                            q.dtype, q.device)
-    wp, wb = _ws_ptr(ws)
-    _check((_lib or load()).kvc_decode_attn_tree_paged(
-        q.data_ptr(), q.shape[2], pool, pt, draft, scale, out.data_ptr(), _data(lse), wp, wb,
-        _raw_stream(q.device, stream)))
+        ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
+    wp, wb = _space(ws)
+    status = (_lib or load()).kvc_decode_attn_tree_paged(
+        q.data_ptr(), q.shape[2], pool, pt, draft, scale, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), wp, wb, _raw_stream(index, stream))
+    if status:
+        _check(status)
     return out
 
 
@@ -890,31 +902,33 @@ def kvc_decode_attn_latent(q: torch.Tensor, cache: kvc_latent_cache, draft: kvc_
     """Absorbed latent attention: q [B, T, Hq, d_latent + d_rope] -> out [B, T, Hq, d_latent].
     len int32 [B]."""
     c = cache
-    width = c.d_latent + c.d_rope
-    out = _attn_args(q, c, width, c.d_latent, c.dtype, c.batch, draft,
-                     (c.batch, draft.n_draft, width), out, lse)
-    _need(len, "len", torch.int32, (c.batch,), q.device)
+    B, R = c.batch, c.d_latent
+    width = R + c.d_rope
+    out, index = _attn_args(q, c, width, R, c.dtype, B, draft, (B, draft.n_draft, width), out, lse)
+    _need(len, "len", torch.int32, (B,), index)
     if ws is None:
-        ws = latent_workspace(c.batch, q.shape[2], c.d_latent, c.d_rope, draft.n_draft, q.dtype,
-                              q.device)
-    wp, wb = _ws_ptr(ws)
-    _check((_lib or load()).kvc_decode_attn_latent(
-        q.data_ptr(), q.shape[2], c, _data(len), -1 if n_valid is None else n_valid, draft, scale,
-        out.data_ptr(), _data(lse), wp, wb, _raw_stream(q.device, stream)))
+        ws = latent_workspace(B, q.shape[2], R, width - R, draft.n_draft, q.dtype, q.device)
+    wp, wb = _space(ws)
+    status = (_lib or load()).kvc_decode_attn_latent(
+        q.data_ptr(), q.shape[2], c, None if len is None else len.data_ptr(),
+        -1 if n_valid is None else n_valid, draft, scale, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), wp, wb, _raw_stream(index, stream))
+    if status:
+        _check(status)
     return out
 
 
 def _accept_args(draft, view, rows_shape, code, path, n_accept):
     if draft._rows is None:
         raise ValueError("accepting needs the drafted rows")
-    shape, dtype, dev = draft._rows
-    if shape != rows_shape or dtype != _torch_dtype(code):
-        raise ValueError(f"drafted rows must be {_torch_dtype(code)} {list(rows_shape)}, got "
+    shape, dtype, index = draft._rows
+    if shape != rows_shape or dtype is not _DTYPES.get(code):
+        raise ValueError(f"drafted rows must be {_DTYPES.get(code)} {list(rows_shape)}, got "
                          f"{dtype} {list(shape)}")
-    _on_current(dev, view, "the draft")
-    _need(path, "path", torch.int32, shape[:2], dev)
-    _need(n_accept, "n_accept", torch.int32, shape[:1], dev)
-    return dev
+    _on_current(index, view, "the draft")
+    _need(path, "path", torch.int32, shape[:2], index)
+    _need(n_accept, "n_accept", torch.int32, shape[:1], index)
+    return index
 
 
 def kvc_tree_accept(cache: kvc_cache, len: torch.Tensor, draft: kvc_draft, path: torch.Tensor,
@@ -922,38 +936,39 @@ def kvc_tree_accept(cache: kvc_cache, len: torch.Tensor, draft: kvc_draft, path:
     """Append drafted tokens path[b, :n_accept[b]] at the tail of every (sequence, head); len
     int32 [B, Hkv] (or [B * Hkv]) advances.  path int32 [B, n_draft], n_accept int32 [B]."""
     c = cache
-    dev = _accept_args(draft, c, (c.batch, draft.n_draft, c.n_heads_kv, c.d_head), c.dtype, path,
-                       n_accept)
-    shape = (c.batch, c.n_heads_kv) if len.dim() == 2 else (c.batch * c.n_heads_kv,)
-    _need(len, "len", torch.int32, shape, dev)
-    _check((_lib or load()).kvc_tree_accept(c, len.data_ptr(), draft, path.data_ptr(), n_accept.data_ptr(),
-                                  _raw_stream(dev, stream)))
+    B, Hkv = c.batch, c.n_heads_kv
+    index = _accept_args(draft, c, (B, draft.n_draft, Hkv, c.d_head), c.dtype, path, n_accept)
+    _need(len, "len", torch.int32, (B, Hkv) if len.dim() == 2 else (B * Hkv,), index)
+    status = (_lib or load()).kvc_tree_accept(c, len.data_ptr(), draft, path.data_ptr(),
+                                              n_accept.data_ptr(), _raw_stream(index, stream))
+    if status:
+        _check(status)
 
 
 def kvc_latent_accept(cache: kvc_latent_cache, len: torch.Tensor, draft: kvc_draft,
                       path: torch.Tensor, n_accept: torch.Tensor, stream=None) -> None:
     """kvc_tree_accept for a latent cache; len int32 [B]."""
     c = cache
-    dev = _accept_args(draft, c, (c.batch, draft.n_draft, c.d_latent + c.d_rope), c.dtype, path,
-                       n_accept)
-    _need(len, "len", torch.int32, (c.batch,), dev)
+    index = _accept_args(draft, c, (c.batch, draft.n_draft, c.d_latent + c.d_rope), c.dtype, path,
+                         n_accept)
+    _need(len, "len", torch.int32, (c.batch,), index)
     _check((_lib or load()).kvc_latent_accept(c, len.data_ptr(), draft, path.data_ptr(),
-                                    n_accept.data_ptr(), _raw_stream(dev, stream)))
+                                    n_accept.data_ptr(), _raw_stream(index, stream)))
 
 
 def kvc_tree_accept_paged(pool: kvc_block_pool, pt: kvc_page_table, free_pool: kvc_free_pool,
                           draft: kvc_draft, path: torch.Tensor, n_accept: torch.Tensor, *,
                           accepted: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """kvc_tree_accept for a paged cache; returns accepted int32 [B] (0: refused)."""
-    dev = _accept_args(draft, pool, (pt.batch, draft.n_draft, pool.n_heads_kv, pool.d_head), pool.dtype,
-                       path, n_accept)
+    index = _accept_args(draft, pool, (pt.batch, draft.n_draft, pool.n_heads_kv, pool.d_head),
+                         pool.dtype, path, n_accept)
     if accepted is None:
-        accepted = torch.empty(pt.batch, dtype=torch.int32, device=dev)
+        accepted = torch.empty(pt.batch, dtype=torch.int32, device=path.device)
     else:
-        _need(accepted, "accepted", torch.int32, (pt.batch,), dev)
+        _need(accepted, "accepted", torch.int32, (pt.batch,), index)
     _check((_lib or load()).kvc_tree_accept_paged(pool, pt, free_pool, draft, path.data_ptr(),
                                         n_accept.data_ptr(), accepted.data_ptr(),
-                                        _raw_stream(dev, stream)))
+                                        _raw_stream(index, stream)))
     return accepted
 
 
@@ -963,10 +978,10 @@ def kvc_latent_expand(cache: kvc_latent_cache, w_k: torch.Tensor, w_v: torch.Ten
     """Keys and values of every head from latent rows into an ordinary cache.  w_k
     [H, d_head - d_rope, d_latent], w_v [H, d_head, d_latent]; len int32 [B]."""
     c, H, D = cache, dst.n_heads_kv, dst.d_head
-    dev = w_k.device
-    _on_current(dev, cache, "w_k")
-    _need(w_k, "w_k", _torch_dtype(c.dtype), (H, D - c.d_rope, c.d_latent), dev)
-    _need(w_v, "w_v", _torch_dtype(c.dtype), (H, D, c.d_latent), dev)
-    _need(len, "len", torch.int32, (c.batch,), dev)
-    _check((_lib or load()).kvc_latent_expand(c, _data(len), -1 if n_valid is None else n_valid,
-                                    w_k.data_ptr(), w_v.data_ptr(), dst, _raw_stream(dev, stream)))
+    index = w_k.get_device()
+    _on_current(index, cache, "w_k")
+    _need(w_k, "w_k", _DTYPES.get(c.dtype), (H, D - c.d_rope, c.d_latent), index)
+    _need(w_v, "w_v", _DTYPES.get(c.dtype), (H, D, c.d_latent), index)
+    _need(len, "len", torch.int32, (c.batch,), index)
+    _check((_lib or load()).kvc_latent_expand(c, None if len is None else len.data_ptr(), -1 if n_valid is None else n_valid,
+                                    w_k.data_ptr(), w_v.data_ptr(), dst, _raw_stream(index, stream)))
