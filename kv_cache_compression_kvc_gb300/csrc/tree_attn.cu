@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
     pdl_trigger();
     pdl_wait();
     const TreeRange range = tree_range(p, g, kTile);
-    int4 note = make_int4(-1, 0, 0, 0);
+    TreeNote note;
     TreeWalk walk(p, range);
     TreeSeg s;
 
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
     const int ty = tid / 16, tx = tid % 16;  // logits: rows 2ty, 2ty+1; slots tx + 16 i
 
     while (walk.next(p, rt, kTile, s)) {
-        tree_note_split(p, range, g, s, note);
+        note.see(range, s);
         if (s.rows <= 0) continue;
         __syncthreads();                     // the previous pair's shared memory is done with
         const int r0 = rt * p.RP;
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
             }
         }
     }
-    if (rt == 0 && tid == 0) p.ws_info[g] = note;
+    if (rt == 0 && tid == 0) p.ws_info[g] = note.get(range);
 }
 
 // Joins the partial states of split pairs.  Blocks (group g * row tile, row chunk) take the pair

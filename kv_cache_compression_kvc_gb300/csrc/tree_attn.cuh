@@ -199,13 +199,23 @@ struct TreeWalk {
 // Where the merge finds a split pair: written by the block that holds its first part.
 //   info[g] = {sequence or -1, KV head, last group, drafted tokens * 2 + workspace slot (0 or 1) of
 //   the first part}
-__device__ __forceinline__ void tree_note_split(const TreeParams &p, const TreeRange &r, int g,
-                                                const TreeSeg &s, int4 &note)
-{
-    if (s.lo != 0 || s.hi == s.nt) return;
-    const long long last = r.t0 + r.n - s.hi + s.nt - 1;     // the pair's last tile
-    note = make_int4(s.b, s.kh, r.group_of(last), s.cnt * 2 + (s.first ? 0 : 1));
-}
+// (The division that finds the last group is left for the end: in 64 bits it costs some 500 clocks.)
+struct TreeNote {
+    int b = -1, kh = 0, how = 0;
+    long long last = 0;                          // the pair's last tile
+    __device__ __forceinline__ void see(const TreeRange &r, const TreeSeg &s)
+    {
+        if (s.lo != 0 || s.hi == s.nt) return;
+        b = s.b;
+        kh = s.kh;
+        how = s.cnt * 2 + (s.first ? 0 : 1);
+        last = r.t0 + r.n - s.hi + s.nt - 1;
+    }
+    __device__ __forceinline__ int4 get(const TreeRange &r) const
+    {
+        return make_int4(b, kh, b < 0 ? 0 : r.group_of(last), how);
+    }
+};
 
 __device__ __forceinline__ uint64_t tree_mask_word(const TreeParams &p, int b, int t, int cnt)
 {

@@ -247,9 +247,15 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         const bool paged = p.table != nullptr;
         const int bx = paged ? min(p.bs, TS) : TS;           // slots of a cache copy
         uint32_t slot = 0, ph = 1, t_slot = 0;               // ring positions
-        while (walk.next(p, rt, TS, s)) {
-            if (s.rows <= 0) continue;
-            if (n_segs > 0) wait(b_q_empty, (n_segs - 1) & 1);
+        // A pair's queries replace the last pair's once its last S is complete.  Their load is held
+        // back until then while the pair's tiles go on filling the ring: waiting for the queries'
+        // place first left HBM idle at each change of pair (a block that changed pairs took 27 us
+        // where the others took 22).
+        bool queries = false;                                // this pair's are still to be loaded
+        TreeNote note;
+        auto load_q = [&] {
+            queries = false;
+            ++n_segs;
             if (!*s_abort && tc::elect()) {
                 if constexpr (LATENT) {
                     const int y = s.b * p.T * p.Hq + rt * RN;
@@ -265,7 +271,23 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 }
             }
             __syncwarp();
-            ++n_segs;
+        };
+        auto seen = [&](uint32_t bar, uint32_t parity) {
+            return __shfl_sync(0xffffffffu, (int)tc::test(bar, parity), 0) != 0;
+        };
+        // the place of a ring unit, loading the queries meanwhile if theirs comes first
+        auto wait_unit = [&](uint32_t bar, uint32_t parity) {
+            for (uint32_t it = 0; queries && it < kMbarSpinLimit; ++it) {
+                if (seen(b_q_empty, (n_segs - 1) & 1)) load_q();
+                else if (seen(bar, parity) || __shfl_sync(0xffffffffu, *s_abort, 0)) return;
+            }
+            wait(bar, parity);
+        };
+        while (walk.next(p, rt, TS, s)) {
+            if (s.rows <= 0) continue;
+            queries = true;
+            if (n_segs == 0) load_q();
+            note.see(range, s);
             for (int tile = s.lo; tile < s.hi; ++tile, ++n_tiles) {
                 const bool draft = s.is_draft(p, tile);
                 const int valid = s.valid(p, tile, TS);
@@ -291,7 +313,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 uint32_t bar = b_full + 8 * t_slot;          // latent: one barrier for the tile
                 if constexpr (LATENT) {
                     const uint32_t r = n_tiles & 1;
-                    if (rope && n_tiles >= 2) wait(b_rope_empty + 8 * r, ((n_tiles >> 1) - 1) & 1);
+                    if (rope && n_tiles >= 2) wait_unit(b_rope_empty + 8 * r, ((n_tiles >> 1) - 1) & 1);
                     if (go && tc::elect()) {
                         if (valid == 0) mbar_arrive(bar);
                         else {
@@ -309,7 +331,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     if (!LATENT) bar = b_full + 8 * slot;
                     const bool isv = u >= KU;
                     const int sub = (isv ? u - KU : u) * SUBS;
-                    if (n_units >= NU) wait(b_empty + 8 * slot, ph);
+                    if (n_units >= NU) wait_unit(b_empty + 8 * slot, ph);
                     if (go && tc::elect()) {
                         if (!LATENT) {
                             if (valid == 0) mbar_arrive(bar);
@@ -338,7 +360,12 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     }
                 }
             }
+            if (queries) {
+                wait(b_q_empty, (n_segs - 1) & 1);
+                load_q();
+            }
         }
+        if (rt == 0 && lane == 0) p.ws_info[g] = note.get(range);
     } else if (warp == 1) {
         // ================================ products ================================================
         constexpr uint32_t id_s = tc::idesc(PL::SM, TS, false);
@@ -535,7 +562,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         tc::bar_sync(kBar, kSoftmax);
         TreeWalk walk(p, range);
         TreeSeg s, nx;
-        int4 note = make_int4(-1, 0, 0, 0);
         unsigned n = 0, seg_no = 0;
         uint32_t v_unit = KU;                                // this tile's first value unit
         const int r0 = rt * p.RP;
@@ -549,7 +575,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         while (more) {
             s = nx;
             more = next_seg();
-            tree_note_split(p, range, g, s, note);
             const bool mine = row < s.rows;
             const bool any = q4 * 32 < s.rows;               // warp-uniform
             float l = 0.f, l_ref = kNegBig;                  // sum over this set's tiles, its reference
@@ -744,7 +769,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             tc::fence_before();
             tc::bar_sync(kBar, kSoftmax);                    // O is free for the next pair
         }
-        if (rt == 0 && set == 0 && row == 0) p.ws_info[g] = note;
     } else {
         // ================================ softmax, outputs ========================================
         // Set i takes slots 32 i .. 32 i + 31 of a tile: a row has a thread in each set, which keep
@@ -762,7 +786,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         const int c0 = set * HC;                             // first slot
         TreeWalk walk(p, range);
         TreeSeg s;
-        int4 note = make_int4(-1, 0, 0, 0);
         unsigned n = 0, seg_no = 0;
         uint32_t v_unit = LATENT ? 0 : KU;                   // this tile's first value unit
         const int r0 = rt * p.RP;
@@ -773,7 +796,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         while (more) {
             s = nx;
             more = walk.next(p, rt, TS, nx);                 // its lengths arrive meanwhile
-            tree_note_split(p, range, g, s, note);
             if (s.rows <= 0) continue;
             const bool mine = row < s.rows;
             const bool any = row_lo < s.rows;                // warp-uniform
@@ -965,7 +987,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             __syncwarp();
             tc::fence_before();
         }
-        if (rt == 0 && tw == 0) p.ws_info[g] = note;
     }
 
     tc::fence_before();
