@@ -77,7 +77,7 @@ struct Plan {
     static constexpr bool PT = RN == 128 && DV <= 128 && !LATENT;   // P in tensor memory, O by row
     static constexpr int SETS = PT ? 2 : TS / 32;            // softmax sets of four warps
     static constexpr int SOFTMAX = 128 * SETS;               // softmax threads
-    static constexpr int THREADS = 64 + SOFTMAX;
+    static constexpr int THREADS = 96 + SOFTMAX;             // and a loading, two issuing warps
     static constexpr int SUB = TS * 128;                     // [TS slots][64 dims]
     static constexpr int SUBS = UD / 64;
     static constexpr int UNIT = SUBS * SUB;
@@ -196,7 +196,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rt = blockIdx.x % p.RT, g = blockIdx.x / p.RT;
-    if (warp == 2 && lane < 8) tc::prefetch_map(&maps.q + lane);
+    if (warp == 3 && lane < 8) tc::prefetch_map(&maps.q + lane);
     if (threadIdx.x == 0) {
         for (int i = 0; i < NTB; ++i) mbar_init(b_full + 8 * i, 1);
         for (int i = 0; i < NU; ++i) mbar_init(b_empty + 8 * i, 1);
@@ -208,7 +208,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             mbar_init(b_p_full + 8 * i, PL::PT ? 4 : 4 * kSets);
             mbar_init(b_pv + 8 * i, 1);
         }
-        mbar_init(b_done, 1);
+        mbar_init(b_done, 2);
         *s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -366,182 +366,134 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             }
         }
         if (rt == 0 && lane == 0) p.ws_info[g] = note.get(range);
-    } else if (warp == 1) {
+    } else if (warp < 3) {
         // ================================ products ================================================
-        constexpr uint32_t id_s = tc::idesc(PL::SM, TS, false);
-        constexpr uint32_t id_o = PL::PT ? tc::idesc_b_mn(RN, UD) : tc::idesc(UD, RN, true);
+        // Warp 1 issues S = Q K^T, warp 2 the values' products; what orders them are the barriers
+        // between each and the softmax.  (One warp for both left the tensor cores waiting for it: a
+        // step takes an issuing warp some 600 clocks besides the products themselves.)
         TreeWalk walk(p, range);
         TreeSeg s, nx;
-        auto next_seg = [&](TreeSeg &x) {
-            while (walk.next(p, rt, TS, x))
-                if (x.rows > 0) return true;
+        auto next_seg = [&] {
+            while (walk.next(p, rt, TS, nx))
+                if (nx.rows > 0) return true;
             return false;
         };
-        unsigned seg_no = 0;                                 // segments whose S has begun
-        uint32_t k_slot = 0, k_ph = 0, v_slot = LATENT ? 0 : KU, v_ph = 0;   // ring positions
-        uint32_t t_slot = 0, t_ph = 0;                       // latent: tile barriers
-        auto step = [&](uint32_t &slot, uint32_t &ph, uint32_t by) {
+        // A step first looks at all its barriers at once, since a wait for one that has long completed
+        // takes some 200 clocks.
+        auto all = [&](bool in) { return __all_sync(0xffffffffu, in) != 0; };
+        auto step = [&](uint32_t &slot, uint32_t &ph, uint32_t by, uint32_t size) {
             slot += by;
-            if (slot >= NU) {
-                slot -= NU;
+            if (slot >= size) {
+                slot -= size;
                 ph ^= 1;
             }
         };
-        // One loop with one place for either product (each is a long run of unrolled instructions,
-        // which a block has to fetch before it first runs them): n_s tiles have their S issued, n_o
-        // their values' product, at most two apart.  PT, where the tensor cores count: if a tile's
-        // weights and the keys of the tile after the next are there, both products are one run, since
-        // each wait, fence and pick of a lane between products costs about 300 clocks (284 us for 302;
-        // with few rows the same costs 1 us in 30, and with latent rows 100 us for 93).
-        // `due`: the steps of the oldest product of values to come, times 2, plus 1 where O begins;
-        // the next one's in the upper half.
-        bool more = next_seg(s), more_nx = false;
-        int tile = more ? s.lo : 0;
-        unsigned n_s = 0, n_o = 0;
-        uint32_t due = 0;
-        while (more || n_o < n_s) {
-            const bool begins = tile == s.lo;
-            // Waits first look at all their barriers at once: a wait for one that has long completed
-            // takes some 200 clocks, in which the tensor cores run dry.
-            // The next tile's keys (and, where a pair begins, its queries) have arrived:
-            auto keys = [&] {
-                bool in = true;
+        unsigned n = 0;
+        uint32_t slot = LATENT || warp == 1 ? 0 : KU, ph = 0;         // ring position
+        uint32_t t_slot = 0, t_ph = 0;                                // latent: tile barriers
+        uint32_t src[KU], bar[KU];                                    // (a tile has KU value units too)
+        // This tile's units have arrived; `more` and `more_ph`: one further barrier.
+        auto take = [&](uint32_t more, uint32_t more_ph) {
+            bool in = tc::test(more, more_ph);
+            uint32_t at = slot, at_ph = ph;
+            if constexpr (LATENT) in &= tc::test(b_full + 8 * t_slot, t_ph);
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                if (!LATENT) in &= tc::test(b_full + 8 * at, at_ph);
+                src[u] = ring + at * UNIT;
+                bar[u] = b_empty + 8 * at;
+                step(at, at_ph, 1, NU);
+            }
+            if (!all(in)) {
                 if constexpr (LATENT) {
-                    in = tc::test(b_full + 8 * t_slot, t_ph);
+                    wait(b_full + 8 * t_slot, t_ph);
                 } else {
-#pragma unroll
+                    uint32_t w = slot, w_ph = ph;
+#pragma unroll 1
                     for (int u = 0; u < KU; ++u) {
-                        const bool wrap = k_slot + u >= NU;
-                        in &= tc::test(b_full + 8 * (wrap ? k_slot + u - NU : k_slot + u), wrap ? k_ph ^ 1 : k_ph);
+                        wait(b_full + 8 * w, w_ph);
+                        step(w, w_ph, 1, NU);
                     }
                 }
-                if (begins) in &= tc::test(b_q_full, seg_no & 1);
-                return in;
-            };
-            // One tile ahead: its S goes first, so that its softmax overlaps the values' product.
-            // With a ring of two tiles, or where the next pair begins, only if it has arrived, since
-            // waiting for it here would hold up the product that frees the ring.
-            bool score = more && n_s - n_o < 2, there = false;
-            if (score) {
-                there = __all_sync(0xffffffffu, keys());
-                if (n_s > n_o && (NU < 3 * PER || begins)) score = there;
+                wait(more, more_ph);
+                __syncwarp();
             }
-            const bool values = !score;
-            uint32_t vsrc[MB], vbar[MB];
-            if (values) {
-                const uint32_t p_bar = b_p_full + (PL::PT ? 8 * (n_o & 1) : 0);
-                const uint32_t p_ph = (PL::PT ? n_o >> 1 : n_o) & 1;
-                const uint32_t slot0 = v_slot, ph0 = v_ph;
-                bool in = tc::test(p_bar, p_ph);
-#pragma unroll
-                for (int m = 0; m < MB; ++m) {
-                    if (!LATENT) in &= tc::test(b_full + 8 * v_slot, v_ph);
-                    vsrc[m] = ring + v_slot * UNIT;
-                    vbar[m] = b_empty + 8 * v_slot;
-                    step(v_slot, v_ph, 1);
-                }
-                if (!LATENT) step(v_slot, v_ph, KU);         // past the next tile's keys
-                if constexpr (PL::PT) there = more && keys();
-                in = __all_sync(0xffffffffu, in);
-                if (!in) {
-                    if constexpr (!LATENT) {
-                        uint32_t slot = slot0, ph = ph0;
-#pragma unroll
-                        for (int m = 0; m < MB; ++m) {
-                            wait(b_full + 8 * slot, ph);
-                            step(slot, ph, 1);
-                        }
-                    }
-                    wait(p_bar, p_ph);
-                    if constexpr (PL::PT) there = more && keys();
-                }
-                if constexpr (PL::PT) score = there = __all_sync(0xffffffffu, there);
-            }
-            uint32_t ksrc[KU], kbar[KU];
-            if (score) {
-                // (its S buffer has been read: the weights of the tile before last, which were
-                // waited for, came from it)
-                if (!there && begins) wait(b_q_full, seg_no & 1);
-                if constexpr (LATENT) {
-                    if (!there) wait(b_full + 8 * t_slot, t_ph);
-                    if (++t_slot == NTB) {
-                        t_slot = 0;
-                        t_ph ^= 1;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < KU; ++u) {
-                    if (!LATENT && !there) wait(b_full + 8 * k_slot, k_ph);
-                    ksrc[u] = ring + k_slot * UNIT;
-                    kbar[u] = b_empty + 8 * k_slot;
-                    step(k_slot, k_ph, 1);
-                }
-                if (!LATENT) step(k_slot, k_ph, KU);         // past the values
-            }
+            slot = at;
+            ph = at_ph;
+            if constexpr (LATENT) step(t_slot, t_ph, 1, NTB);
+            else step(slot, ph, KU, NU);                              // past the other kind's units
             tc::fence_after();
-            const uint32_t buf = n_s & 1, d = tS + buf * TS;
-            if (tc::elect()) {
-                if (values) {                                // O^T += V^T P^T, or O += P V
-                    const int steps = PL::PT ? TS / 16 : (int)((due & 0xffffu) >> 1);
-                    const tc::Desc dp = tc::desc_k(sP);
-#pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        const tc::Desc dv = tc::desc(vsrc[m], SUB, 1024);
-#pragma unroll
-                        for (int ks = 0; ks < TS / 16; ++ks)
-                            if (ks < steps) {
-                                if constexpr (PL::PT)
-                                    tc::mma_ta(tO + m * UD, tP + (n_o & 1) * (TS / 2) + ks * 8, dv + ks * 2048,
-                                               id_o, !(due & 1u) || ks > 0);
-                                else
-                                    tc::mma(tO + m * RN, dv + ks * 2048,
-                                            dp + ((ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
-                                            !(due & 1u) || ks > 0);
-                            }
-                        tc::commit(vbar[m]);
-                    }
-                    tc::commit(b_pv + (PL::PT ? 8 * (n_o & 1) : 0));
-                }
-                if (score) {
-                    const tc::Desc dq = tc::desc_k(sQ);
-                    if (rope) {
-                        const tc::Desc dr = tc::desc_k(sR + buf * SUB);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc::mma(d, dq + (KU * SUBS * RN * 128 + kk * 32), dr + kk * 32, id_s, kk > 0);
-                        tc::commit(b_rope_empty + 8 * buf);
-                    }
-#pragma unroll
-                    for (int u = 0; u < KU; ++u) {
-                        const tc::Desc dk = tc::desc_k(ksrc[u]);
-#pragma unroll
-                        for (int i = 0; i < SUBS; ++i)
+        };
+        bool any = next_seg();
+        if (warp == 1) {
+            constexpr uint32_t id_s = tc::idesc(PL::SM, TS, false);
+            const tc::Desc dq = tc::desc_k(sQ);
+            unsigned seg_no = 0;
+            while (any) {
+                s = nx;
+                wait(b_q_full, seg_no & 1);
+                ++seg_no;
+                for (int tile = s.lo; tile < s.hi; ++tile, ++n) {
+                    const uint32_t buf = n & 1, d = tS + buf * TS;
+                    // the S buffer has been read: the weights of the tile before last came from it
+                    if (n >= 2) take(b_p_full + 8 * buf, ((n >> 1) - 1) & 1);
+                    else take(b_q_full, (seg_no - 1) & 1);
+                    if (tc::elect()) {
+                        if (rope) {
+                            const tc::Desc dr = tc::desc_k(sR + buf * SUB);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc::mma(d, dq + ((u * SUBS + i) * RN * 128 + kk * 32), dk + (i * SUB + kk * 32),
-                                        id_s, rope || u > 0 || i > 0 || kk > 0);
-                        if (!LATENT) tc::commit(kbar[u]);
+                                tc::mma(d, dq + (KU * SUBS * RN * 128 + kk * 32), dr + kk * 32, id_s, kk > 0);
+                            tc::commit(b_rope_empty + 8 * buf);
+                        }
+#pragma unroll
+                        for (int u = 0; u < KU; ++u) {
+                            const tc::Desc dk = tc::desc_k(src[u]);
+#pragma unroll
+                            for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc::mma(d, dq + ((u * SUBS + i) * RN * 128 + kk * 32),
+                                            dk + (i * SUB + kk * 32), id_s, rope || u > 0 || i > 0 || kk > 0);
+                            if (!LATENT) tc::commit(bar[u]);
+                        }
+                        tc::commit(b_s_full + 8 * buf);
+                        if (tile == s.hi - 1) tc::commit(b_q_empty);
                     }
-                    tc::commit(b_s_full + 8 * buf);
-                    if (tile == s.hi - 1) tc::commit(b_q_empty);
+                    __syncwarp();
+                    if (tile == s.lo) any = next_seg();               // (its lengths arrive meanwhile)
                 }
             }
-            __syncwarp();
-            if (values) {
-                due >>= 16;
-                ++n_o;
-            }
-            if (score) {
-                due |= ((uint32_t)steps_of(s, tile) * 2u + (begins ? 1u : 0u)) << (n_s > n_o ? 16 : 0);
-                ++n_s;
-                if (begins) {
-                    ++seg_no;
-                    more_nx = next_seg(nx);                  // (its lengths arrive meanwhile)
-                }
-                if (++tile == s.hi) {
-                    more = more_nx;
-                    s = nx;
-                    tile = s.lo;
+        } else {
+            // O^T += V^T P^T, or O += P V
+            constexpr uint32_t id_o = PL::PT ? tc::idesc_b_mn(RN, UD) : tc::idesc(UD, RN, true);
+            const tc::Desc dp = tc::desc_k(sP);
+            while (any) {
+                s = nx;
+                for (int tile = s.lo; tile < s.hi; ++tile, ++n) {
+                    const int steps = steps_of(s, tile);
+                    take(b_p_full + 8 * (n & 1), (n >> 1) & 1);
+                    if (tc::elect()) {
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) {
+                            const tc::Desc dv = tc::desc(src[m], SUB, 1024);
+#pragma unroll
+                            for (int ks = 0; ks < TS / 16; ++ks)
+                                if (ks < steps) {
+                                    if constexpr (PL::PT)
+                                        tc::mma_ta(tO + m * UD, tP + (n & 1) * (TS / 2) + ks * 8, dv + ks * 2048,
+                                                   id_o, tile > s.lo || ks > 0);
+                                    else
+                                        tc::mma(tO + m * RN, dv + ks * 2048,
+                                                dp + ((ks >> 2) * RN * 128 + (ks & 3) * 32), id_o,
+                                                tile > s.lo || ks > 0);
+                                }
+                            tc::commit(bar[m]);
+                        }
+                        tc::commit(b_pv + (PL::PT ? 8 * (n & 1) : 0));
+                    }
+                    __syncwarp();
+                    if (tile == s.lo) any = next_seg();
                 }
             }
         }
@@ -552,7 +504,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         // The rows' running maxima (shared memory) move in tile order: the warp of tile n passes
         // its partner a token (named barrier) once tile n's are final; a warp whose weights refer
         // to an older maximum by then computes them again.
-        const int set = (warp - 2) / 4;
+        const int set = (warp - 3) / 4;
         const int q4 = warp & 3;                             // lanes 32 q4 .. of tensor memory
         const int row = q4 * 32 + lane;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
@@ -774,7 +726,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         // Set i takes slots 32 i .. 32 i + 31 of a tile: a row has a thread in each set, which keep
         // the same maximum and their own part of the sum.
         constexpr int HC = 32;
-        const int set = (warp - 2) / 4;
+        const int set = (warp - 3) / 4;
         const int q4 = warp & 3;                             // lanes 32 q4 .. of tensor memory
         const int ln = q4 * 32 + lane;                       // 0..127
         const int tw = set * 128 + ln;
@@ -908,14 +860,14 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                         const uint32_t slot = un % NU;
                         if (!LATENT) wait(b_full + 8 * slot, (un / NU) & 1);   // (S implies a latent tile)
                         unsigned char *base = smem_raw + (ring + slot * UNIT - raw);
-                        clean_unit<SUBS, SUB>(base, warp - 2, kSoftmax / 32, valid, depth, draft, s_nf);
+                        clean_unit<SUBS, SUB>(base, warp - 3, kSoftmax / 32, valid, depth, draft, s_nf);
                     }
                     drafts |= draft;
                 }
                 tc::fence_async();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(b_p_full);
+                if (lane == 0) mbar_arrive(b_p_full + 8 * buf);
             }
             // this part's outputs: O^T / l, or the partial state
             const bool whole = s.whole();
@@ -1002,7 +954,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             for (unsigned i = loads > NTB ? loads - NTB : 0; i < loads; ++i)
                 drain(b_full + 8 * (i % NTB), (i / NTB) & 1);
             if (n_segs > 0) drain(b_q_full, (n_segs - 1) & 1);
-        } else if (warp == 1) {
+        } else if (warp == 1 || warp == 2) {                 // each its own products
             if (tc::elect()) tc::commit(b_done);
             __syncwarp();
             mbar_wait_ok(b_done, 0, kMbarSpinLimit);
