@@ -37,6 +37,7 @@
 // the product (0 * inf would not be 0); so are a drafted token's non-finite values, which are then
 // added to the rows that do see the token when the output is written.
 #include <mutex>
+#include <type_traits>
 
 #include "tc_ops.cuh"
 #include "tree_attn.cuh"
@@ -378,9 +379,6 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 if (nx.rows > 0) return true;
             return false;
         };
-        // A step first looks at all its barriers at once, since a wait for one that has long completed
-        // takes some 200 clocks.
-        auto all = [&](bool in) { return __all_sync(0xffffffffu, in) != 0; };
         auto step = [&](uint32_t &slot, uint32_t &ph, uint32_t by, uint32_t size) {
             slot += by;
             if (slot >= size) {
@@ -392,27 +390,28 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         uint32_t slot = LATENT || warp == 1 ? 0 : KU, ph = 0;         // ring position
         uint32_t t_slot = 0, t_ph = 0;                                // latent: tile barriers
         uint32_t src[KU], bar[KU];                                    // (a tile has KU value units too)
-        // This tile's units have arrived; `more` and `more_ph`: one further barrier.
-        auto take = [&](uint32_t more, uint32_t more_ph) {
+        // The next COUNT units have arrived, and one more barrier has completed.  Looks at all of them
+        // at once first, since a wait for one that has long completed takes some 200 clocks.  A latent
+        // tile has one barrier, which its values need not look at: the weights came after its S.
+        auto take = [&](auto COUNT, uint32_t more, uint32_t more_ph) {
             bool in = tc::test(more, more_ph);
             uint32_t at = slot, at_ph = ph;
-            if constexpr (LATENT) in &= tc::test(b_full + 8 * t_slot, t_ph);
+            if (LATENT && warp == 1) in &= tc::test(b_full + 8 * t_slot, t_ph);
 #pragma unroll
-            for (int u = 0; u < KU; ++u) {
+            for (int u = 0; u < COUNT; ++u) {
                 if (!LATENT) in &= tc::test(b_full + 8 * at, at_ph);
                 src[u] = ring + at * UNIT;
                 bar[u] = b_empty + 8 * at;
                 step(at, at_ph, 1, NU);
             }
-            if (!all(in)) {
+            if (!__all_sync(0xffffffffu, in)) {
                 if constexpr (LATENT) {
-                    wait(b_full + 8 * t_slot, t_ph);
+                    if (warp == 1) wait(b_full + 8 * t_slot, t_ph);
                 } else {
-                    uint32_t w = slot, w_ph = ph;
 #pragma unroll 1
-                    for (int u = 0; u < KU; ++u) {
-                        wait(b_full + 8 * w, w_ph);
-                        step(w, w_ph, 1, NU);
+                    for (int u = 0; u < COUNT; ++u) {
+                        wait(b_full + 8 * slot, ph);
+                        step(slot, ph, 1, NU);
                     }
                 }
                 wait(more, more_ph);
@@ -420,8 +419,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             }
             slot = at;
             ph = at_ph;
-            if constexpr (LATENT) step(t_slot, t_ph, 1, NTB);
-            else step(slot, ph, KU, NU);                              // past the other kind's units
+            if (LATENT && warp == 1) step(t_slot, t_ph, 1, NTB);
             tc::fence_after();
         };
         bool any = next_seg();
@@ -435,32 +433,43 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 ++seg_no;
                 for (int tile = s.lo; tile < s.hi; ++tile, ++n) {
                     const uint32_t buf = n & 1, d = tS + buf * TS;
-                    // the S buffer has been read: the weights of the tile before last came from it
-                    if (n >= 2) take(b_p_full + 8 * buf, ((n >> 1) - 1) & 1);
-                    else take(b_q_full, (seg_no - 1) & 1);
-                    if (tc::elect()) {
-                        if (rope) {
-                            const tc::Desc dr = tc::desc_k(sR + buf * SUB);
+                    // As each unit arrives, or a latent tile's together (a row tile of 128 heads 84 us,
+                    // by units 87).  The S buffer has been read: the weights of the tile before last
+                    // came from it.
+                    constexpr int AT_ONCE = LATENT ? KU : 1;
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc::mma(d, dq + (KU * SUBS * RN * 128 + kk * 32), dr + kk * 32, id_s, kk > 0);
-                            tc::commit(b_rope_empty + 8 * buf);
-                        }
-#pragma unroll
-                        for (int u = 0; u < KU; ++u) {
-                            const tc::Desc dk = tc::desc_k(src[u]);
-#pragma unroll
-                            for (int i = 0; i < SUBS; ++i)
+                    for (int u0 = 0; u0 < KU; u0 += AT_ONCE) {
+                        using Count = std::integral_constant<int, AT_ONCE>;
+                        if (n >= 2) take(Count{}, b_p_full + 8 * buf, ((n >> 1) - 1) & 1);
+                        else take(Count{}, b_q_full, (seg_no - 1) & 1);
+                        if (tc::elect()) {
+                            if (rope && u0 == 0) {
+                                const tc::Desc dr = tc::desc_k(sR + buf * SUB);
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    tc::mma(d, dq + ((u * SUBS + i) * RN * 128 + kk * 32),
-                                            dk + (i * SUB + kk * 32), id_s, rope || u > 0 || i > 0 || kk > 0);
-                            if (!LATENT) tc::commit(bar[u]);
+                                    tc::mma(d, dq + (KU * SUBS * RN * 128 + kk * 32), dr + kk * 32, id_s, kk > 0);
+                                tc::commit(b_rope_empty + 8 * buf);
+                            }
+#pragma unroll
+                            for (int u = u0; u < u0 + AT_ONCE; ++u) {
+                                const tc::Desc dk = tc::desc_k(src[u - u0]);
+#pragma unroll
+                                for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        tc::mma(d, dq + ((u * SUBS + i) * RN * 128 + kk * 32),
+                                                dk + (i * SUB + kk * 32), id_s,
+                                                rope || u > 0 || i > 0 || kk > 0);
+                                if (!LATENT) tc::commit(bar[u - u0]);
+                            }
+                            if (u0 + AT_ONCE == KU) {
+                                tc::commit(b_s_full + 8 * buf);
+                                if (tile == s.hi - 1) tc::commit(b_q_empty);
+                            }
                         }
-                        tc::commit(b_s_full + 8 * buf);
-                        if (tile == s.hi - 1) tc::commit(b_q_empty);
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!LATENT) step(slot, ph, KU, NU);                  // past the values
                     if (tile == s.lo) any = next_seg();               // (its lengths arrive meanwhile)
                 }
             }
@@ -472,7 +481,8 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 s = nx;
                 for (int tile = s.lo; tile < s.hi; ++tile, ++n) {
                     const int steps = steps_of(s, tile);
-                    take(b_p_full + 8 * (n & 1), (n >> 1) & 1);
+                    take(std::integral_constant<int, KU>{}, b_p_full + 8 * (n & 1), (n >> 1) & 1);
+                    if (!LATENT) step(slot, ph, KU, NU);              // past the next tile's keys
                     if (tc::elect()) {
 #pragma unroll
                         for (int m = 0; m < MB; ++m) {
