@@ -78,7 +78,8 @@ struct Plan {
     static constexpr bool PT = RN == 128 && DV <= 128 && !LATENT;   // P in tensor memory, O by row
     static constexpr int SETS = PT ? 2 : TS / 32;            // softmax sets of four warps
     static constexpr int SOFTMAX = 128 * SETS;               // softmax threads
-    static constexpr int THREADS = 96 + SOFTMAX;             // and a loading, two issuing warps
+    static constexpr int CONTROL = LATENT ? 4 : 3;           // loading and issuing warps come first
+    static constexpr int THREADS = 32 * CONTROL + SOFTMAX;
     static constexpr int SUB = TS * 128;                     // [TS slots][64 dims]
     static constexpr int SUBS = UD / 64;
     static constexpr int UNIT = SUBS * SUB;
@@ -197,7 +198,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rt = blockIdx.x % p.RT, g = blockIdx.x / p.RT;
-    if (warp == 3 && lane < 8) tc::prefetch_map(&maps.q + lane);
+    if (warp == 2 && lane < 8) tc::prefetch_map(&maps.q + lane);
     if (threadIdx.x == 0) {
         for (int i = 0; i < NTB; ++i) mbar_init(b_full + 8 * i, 1);
         for (int i = 0; i < NU; ++i) mbar_init(b_empty + 8 * i, 1);
@@ -240,14 +241,26 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         return v > 16 ? (v + 15) / 16 : 1;
     };
 
-    unsigned n_units = 0, n_tiles = 0, n_segs = 0;           // the producer's counts (for the drain)
-    if (warp == 0) {
+    // Warp 0 loads, and the second half of a latent tile's units warp 3 (a unit takes a warp some 400
+    // clocks: 128 heads 84 -> 80 us; the keys and values of other caches from two warps came out slower,
+    // 260 us for 254 and 60 for 57).
+    constexpr int FIRST = LATENT ? (PER + 1) / 2 : PER;      // warp 0's
+    const int u_lo = warp == 0 ? 0 : FIRST, u_hi = warp == 0 ? FIRST : PER;
+    unsigned n_tiles = 0, n_segs = 0;                        // their counts (for the drain)
+    if (warp == 0 || (LATENT && warp == 3)) {
         // ================================ loads ===================================================
         TreeWalk walk(p, range);
         TreeSeg s;
         const bool paged = p.table != nullptr;
         const int bx = paged ? min(p.bs, TS) : TS;           // slots of a cache copy
-        uint32_t slot = 0, ph = 1, t_slot = 0;               // ring positions
+        uint32_t slot = u_lo, ph = 1, t_slot = 0;            // ring positions
+        auto step = [&](uint32_t by) {
+            slot += by;
+            if (slot >= NU) {
+                slot -= NU;
+                ph ^= 1;
+            }
+        };
         // A pair's queries replace the last pair's once its last S is complete.  Their load is held
         // back until then while the pair's tiles go on filling the ring: waiting for the queries'
         // place first left HBM idle at each change of pair (a block that changed pairs took 27 us
@@ -286,8 +299,8 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         };
         while (walk.next(p, rt, TS, s)) {
             if (s.rows <= 0) continue;
-            queries = true;
-            if (n_segs == 0) load_q();
+            queries = warp == 0;
+            if (queries && n_segs == 0) load_q();
             note.see(range, s);
             for (int tile = s.lo; tile < s.hi; ++tile, ++n_tiles) {
                 const bool draft = s.is_draft(p, tile);
@@ -314,25 +327,27 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 uint32_t bar = b_full + 8 * t_slot;          // latent: one barrier for the tile
                 if constexpr (LATENT) {
                     const uint32_t r = n_tiles & 1;
-                    if (rope && n_tiles >= 2) wait_unit(b_rope_empty + 8 * r, ((n_tiles >> 1) - 1) & 1);
-                    if (go && tc::elect()) {
-                        if (valid == 0) mbar_arrive(bar);
-                        else {
-                            mbar_arrive_expect_tx(bar, bytes * (KU * SUBS + (rope ? 1 : 0)));
-                            if (rope)
-                                tc::tma_5d(sR + r * SUB, draft ? &maps.rd : &maps.rk, 0, y, 0, 0, s.b, bar);
+                    if (warp == 0) {
+                        if (rope && n_tiles >= 2) wait_unit(b_rope_empty + 8 * r, ((n_tiles >> 1) - 1) & 1);
+                        if (go && tc::elect()) {
+                            if (valid == 0) mbar_arrive(bar);
+                            else {
+                                mbar_arrive_expect_tx(bar, bytes * (KU * SUBS + (rope ? 1 : 0)));
+                                if (rope)
+                                    tc::tma_5d(sR + r * SUB, draft ? &maps.rd : &maps.rk, 0, y, 0, 0, s.b, bar);
+                            }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     if (++t_slot == NTB) t_slot = 0;
                 }
 #pragma unroll 1
-                for (int u = 0; u < PER; ++u, ++n_units) {
+                for (int u = u_lo; u < u_hi; ++u) {
                     const uint32_t dst = ring + slot * UNIT;
                     if (!LATENT) bar = b_full + 8 * slot;
                     const bool isv = u >= KU;
                     const int sub = (isv ? u - KU : u) * SUBS;
-                    if (n_units >= NU) wait_unit(b_empty + 8 * slot, ph);
+                    if (n_tiles * PER + u >= NU) wait_unit(b_empty + 8 * slot, ph);
                     if (go && tc::elect()) {
                         if (!LATENT) {
                             if (valid == 0) mbar_arrive(bar);
@@ -355,18 +370,16 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                             __syncwarp();
                         }
                     }
-                    if (++slot == NU) {
-                        slot = 0;
-                        ph ^= 1;
-                    }
+                    step(1);
                 }
+                step(PER - (u_hi - u_lo));
             }
             if (queries) {
                 wait(b_q_empty, (n_segs - 1) & 1);
                 load_q();
             }
         }
-        if (rt == 0 && lane == 0) p.ws_info[g] = note.get(range);
+        if (warp == 0 && rt == 0 && lane == 0) p.ws_info[g] = note.get(range);
     } else if (warp < 3) {
         // ================================ products ================================================
         // Warp 1 issues S = Q K^T, warp 2 the values' products; what orders them are the barriers
@@ -514,7 +527,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         // The rows' running maxima (shared memory) move in tile order: the warp of tile n passes
         // its partner a token (named barrier) once tile n's are final; a warp whose weights refer
         // to an older maximum by then computes them again.
-        const int set = (warp - 3) / 4;
+        const int set = (warp - PL::CONTROL) / 4;
         const int q4 = warp & 3;                             // lanes 32 q4 .. of tensor memory
         const int row = q4 * 32 + lane;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
@@ -736,7 +749,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         // Set i takes slots 32 i .. 32 i + 31 of a tile: a row has a thread in each set, which keep
         // the same maximum and their own part of the sum.
         constexpr int HC = 32;
-        const int set = (warp - 3) / 4;
+        const int set = (warp - PL::CONTROL) / 4;
         const int q4 = warp & 3;                             // lanes 32 q4 .. of tensor memory
         const int ln = q4 * 32 + lane;                       // 0..127
         const int tw = set * 128 + ln;
@@ -870,7 +883,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                         const uint32_t slot = un % NU;
                         if (!LATENT) wait(b_full + 8 * slot, (un / NU) & 1);   // (S implies a latent tile)
                         unsigned char *base = smem_raw + (ring + slot * UNIT - raw);
-                        clean_unit<SUBS, SUB>(base, warp - 3, kSoftmax / 32, valid, depth, draft, s_nf);
+                        clean_unit<SUBS, SUB>(base, warp - PL::CONTROL, kSoftmax / 32, valid, depth, draft, s_nf);
                     }
                     drafts |= draft;
                 }
@@ -956,13 +969,18 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
     // after a wait ran out: the loads in flight have landed and the products issued have completed
     // before the block frees tensor memory and exits
     if (*s_abort) {
-        if (threadIdx.x == 0) {
+        if (threadIdx.x == 0 || (LATENT && threadIdx.x == 96)) {   // each its own loads
             auto drain = [&](uint32_t bar, uint32_t parity) {
                 mbar_wait_ok(bar, parity, kMbarSpinLimit >> 4);
             };
-            const unsigned loads = LATENT ? n_tiles : n_units;
-            for (unsigned i = loads > NTB ? loads - NTB : 0; i < loads; ++i)
-                drain(b_full + 8 * (i % NTB), (i / NTB) & 1);
+            if constexpr (LATENT) {
+                for (unsigned i = n_tiles > NTB ? n_tiles - NTB : 0; i < n_tiles; ++i)
+                    drain(b_full + 8 * (i % NTB), (i / NTB) & 1);
+            } else {
+                const unsigned units = n_tiles * PER;
+                for (unsigned i = units > NU ? units - NU : 0; i < units; ++i)
+                    if ((int)(i % PER) >= u_lo && (int)(i % PER) < u_hi) drain(b_full + 8 * (i % NU), (i / NU) & 1);
+            }
             if (n_segs > 0) drain(b_q_full, (n_segs - 1) & 1);
         } else if (warp == 1 || warp == 2) {                 // each its own products
             if (tc::elect()) tc::commit(b_done);
