@@ -1262,6 +1262,8 @@ static kvc_status tree_run(kvc::TreeParams &p, int dtype, bool tc_ok, const kvc_
     auto plan = [&](bool tc) {
         const kvc::TreePlan pl = kvc::tree_plan(p.G, p.DK, p.DV, p.T, p.latent != 0, tc, n_sm);
         p.RN = pl.RN; p.RP = pl.RP; p.RT = pl.RT; p.groups = pl.groups;
+        p.whole = kvc::tree_whole(p, tc);
+        if (p.whole) p.groups = std::min(p.groups, p.P);
         char *base = static_cast<char *>(ws);
         p.ws_info = reinterpret_cast<int4 *>(base + pl.off_info);
         p.ws_ml = reinterpret_cast<float *>(base + pl.off_ml);
@@ -1278,8 +1280,10 @@ static kvc_status tree_run(kvc::TreeParams &p, int dtype, bool tc_ok, const kvc_
         e = kvc::launch_tree_attn(p, dtype, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
-    e = kvc::launch_tree_merge(p, dtype, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tree merge launch");
+    if (!p.whole) {
+        e = kvc::launch_tree_merge(p, dtype, s);
+        if (e != cudaSuccess) return cuda_fail(e, "tree merge launch");
+    }
     return ok();
 }
 

@@ -305,6 +305,7 @@ struct TreeParams {
     float *lse;                  // nullable
     // schedule (plan): row tiles of RP rows padded to RN, `groups` ranges of tiles
     int32_t RN, RP, RT, groups;
+    int32_t whole;               // ranges of whole pairs: none is split
     float *ws_o;                 // [groups*RT*2][RN][DV]
     float *ws_ml;                // [groups*RT*2][RN][2] (max in log2 units, sum)
     int4 *ws_info;               // [groups]
@@ -318,6 +319,7 @@ struct TreePlan {
 // Row tile of the tensor-core kernel: RN rows (its matrix size), RP of them used.
 void tree_tc_rows(int G, int DV, int T, bool latent, int32_t *RN, int32_t *RP);
 TreePlan tree_plan(int G, int DK, int DV, int T, bool latent, bool tc, int n_sm);
+bool tree_whole(const TreeParams &p, bool tc);   // ranges of whole pairs, no merge
 bool tree_tc_pages(int bs, int D);           // block sizes the tensor-core kernel takes
 cudaError_t launch_tree_attn(const TreeParams &p, int dtype, cudaStream_t stream);
 // Sets *used = false, launching nothing, when the tensor maps cannot be made.

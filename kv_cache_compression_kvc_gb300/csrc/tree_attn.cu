@@ -529,6 +529,16 @@ TreePlan tree_plan(int G, int DK, int DV, int T, bool latent, bool tc, int n_sm)
     return pl;
 }
 
+bool tree_whole(const TreeParams &p, bool tc)
+{
+    if (!tc) return false;
+    const int TS = p.latent || p.DV == 256 ? 64 : 128;
+    const long long slots = p.len == nullptr ? p.n_valid : p.cap;
+    const long long tiles = (slots + TS - 1) / TS + (p.kd != nullptr);
+    const long long spare = ((long long)p.P + p.groups - 1) / p.groups * p.groups - p.P;
+    return tiles <= kWholeTiles && spare * tiles <= (long long)(p.latent ? kWholeWaitLatent : kWholeWait) * p.groups;
+}
+
 cudaError_t launch_tree_attn(const TreeParams &p, int dtype, cudaStream_t stream)
 {
     return dtype == 1 ? launch_dims<__nv_bfloat16>(p, stream) : launch_dims<float>(p, stream);

@@ -16,6 +16,14 @@
 // one partial state (max, sum, unnormalised output) per range: workspace slot 2*block for the
 // first pair of a block's range, 2*block + 1 for its last; tree_merge_kernel, launched next,
 // joins them in range order (no atomics: results do not depend on timing).
+//
+// Short pairs are not split: the ranges are whole pairs then, and the merge is not launched.  The
+// tensor-core kernel does so where the most tiles that a pair can have (by the cache's capacity, which
+// the host knows) are kWholeTiles at most and the fullest range has no more than kWholeWait tiles above
+// the mean.  Measured with 8 rows and 128 dims, split and whole: 128 pairs of 4 tiles 15.5 and 11.1 us,
+// of 12 tiles 25.6 and 20.0; 512 pairs of 4 tiles 39.8 and 34.7.  With more tiles above the mean
+// splitting wins: 8 pairs of 9 tiles 11.1 and 15.0, 192 pairs of 12 tiles 36.0 and 41.3.  Latent tiles
+// take longer: 1 sequence of 3 tiles 9.8 and 9.9, of 4 tiles 10.0 and 11.6.
 #pragma once
 
 #include "common.cuh"
@@ -23,6 +31,7 @@
 
 namespace kvc {
 
+constexpr int kWholeTiles = 12, kWholeWait = 4, kWholeWaitLatent = 3;
 constexpr int kDevBadLengthCode = 5;         // KVC_DEV_BAD_LENGTH
 constexpr int kDevBadBlockCode = 9;          // KVC_DEV_BAD_BLOCK
 
@@ -71,6 +80,26 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int 
     const int per = (items + 31) >> 5;
     const int q0 = min(items, lane * per), q1 = min(items, q0 + per);
     const bool check = blockIdx.x == 0 && threadIdx.x < 32;
+    if (p.whole) {
+        if (check) {
+            for (int q = lane; q < items; q += 32) {
+                const int n = p.len != nullptr ? p.len[q] : p.n_valid;
+                const int c = p.count == nullptr ? p.T : p.count[p.len_per_pair ? q / p.Hkv : q];
+                if (n < 0 || n > p.cap || c < 0 || c > p.T) record_code(p.dev_code, kDevBadLengthCode);
+            }
+            __syncwarp();
+        }
+        TreeRange r{};
+        r.pair = (int)((long long)p.P * g / p.groups);
+        const int end = (int)((long long)p.P * (g + 1) / p.groups);
+        r.len = tree_len(p, r.pair);
+        r.cnt = tree_count(p, r.pair / p.Hkv);
+        for (int q = r.pair + lane; q < end; q += 32)
+            r.n += tree_tiles(p, tree_len(p, q), tree_count(p, q / p.Hkv), TS);
+        r.n = __reduce_add_sync(0xffffffffu, r.n);
+        r.q = 1;
+        return r;
+    }
     auto count_of = [&](int q) {
         return p.count == nullptr ? p.T : p.count[p.len_per_pair ? q / p.Hkv : q];
     };
