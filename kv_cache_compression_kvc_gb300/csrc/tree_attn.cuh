@@ -196,7 +196,7 @@ struct TreeWalk {
     __device__ __forceinline__ bool next(const TreeParams &p, int rt, int TS, TreeSeg &s)
     {
         while (left > 0 && pair < p.P) {
-            if (!first) {
+            if (!first || len < 0) {             // (the range knows its first pair's)
                 len = tree_len(p, pair);
                 cnt = tree_count(p, b);
             }
@@ -216,7 +216,10 @@ struct TreeWalk {
                 ++b;
             }
             off = 0;
-            if (s.nt == 0) continue;
+            if (s.nt == 0) {
+                len = -1;
+                continue;
+            }
             left -= s.hi - s.lo;
             first = false;
             return true;

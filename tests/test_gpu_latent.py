@@ -107,6 +107,29 @@ def test_latent_counts_garbage_strides_and_chain(dtype):
         verify(q, c, R, None, full, None, out, lse, what=f"cache only {n}")
 
 
+@pytest.mark.parametrize("B,H,R,E,T,cap,lens", [
+    (4, 20, 256, 32, 6, 900, [0, 830, 899, 64]), (4, 16, 512, 64, 2, 2000, [2000, 1, 0, 1217]),
+    (170, 16, 512, 64, 1, 130, [0, 1, 64, 65, 130]), (320, 20, 128, 0, 5, 100, [100, 0, 37])])
+def test_latent_garbage_in_split_and_whole_sequences(B, H, R, E, T, cap, lens):
+    """Counts from none to all and garbage wherever nothing may be read, in few sequences that are split
+    and in more short ones than blocks."""
+    dev = cuda_or_skip()
+    kvc = lib()
+    dtype = torch.bfloat16
+    q, c = randn((B, T, H, R + E), 31, dev, dtype), randn((B, cap, R + E), 32, dev, dtype)
+    cd = randn((B, T, R + E), 33, dev, dtype)
+    ln = torch.tensor([lens[b % len(lens)] for b in range(B)], dtype=torch.int32, device=dev)
+    count = torch.tensor([(T, 0, T, 1, T // 2)[b % 5] for b in range(B)], dtype=torch.int32, device=dev)
+    for b in range(B):
+        c[b, int(ln[b]):] = (INF, NAN)[b % 2]
+        cd[b, int(count[b]):] = NAN
+    mask = tree_masks(B, T, 34)
+    mask[0, 0] = 0
+    out, lse = run_latent(kvc, q, c, R, cd, ln, mask.to(dev), count=count)
+    assert kvc.kvc_device_status() == 0
+    verify(q, c, R, cd, ln, mask, out, lse, count=count)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("B,H,R,E,D,cap,lens", [
     (1, 1, 128, 0, 64, 5, [5]), (2, 3, 256, 32, 64, 130, [0, 129]), (2, 8, 512, 64, 128, 300, [300, 1]),

@@ -114,6 +114,66 @@ def test_tree_ragged_counts_masks_and_garbage(dtype, D):
     assert bool((out[0, 2] == 0).all()) and bool((lse[0, 2] == -INF).all())
 
 
+@pytest.mark.parametrize("D,T", [(64, 13), (64, 64), (128, 13), (128, 64), (256, 13), (256, 64)])
+def test_tree_garbage_in_split_pairs(D, T):
+    """The same in a cache whose capacity lets pairs be split, with one and with two row tiles of the
+    tensor cores: parts without drafts, with nothing but drafts, non-finite drafted values in both."""
+    dev = cuda_or_skip()
+    kvc = lib()
+    B, Hkv, G, cap, dtype = 4, 2, 3, 1700, torch.bfloat16
+    q = randn((B, T, Hkv * G, D), 11, dev, dtype)
+    k, v = randn((B, Hkv, cap, D), 12, dev, dtype), randn((B, Hkv, cap, D), 13, dev, dtype)
+    kd, vd = randn((B, T, Hkv, D), 14, dev, dtype), randn((B, T, Hkv, D), 15, dev, dtype)
+    lens = torch.tensor([[0, 1699], [130, 7], [1280, 1281], [5, 128]], dtype=torch.int32, device=dev)
+    count = torch.tensor([T, 0, 6, 1], dtype=torch.int32, device=dev)
+    for b in range(B):
+        for h in range(Hkv):
+            n = int(lens[b, h])
+            k[b, h, n:], v[b, h, n:] = INF, NAN
+        kd[b, int(count[b]):], vd[b, int(count[b]):] = NAN, INF
+    mask = tree_masks(B, T, 19)
+    mask[0, 2] = 0
+    mask[2, 3] = 0
+    vd[0, 5, 1, 9] = -INF                # in a pair of many parts
+    vd[0, 6, 1, D - 1] = NAN
+    vd[2, 4, 1, 3] = INF
+    mask[2, 5] = 1 << 5
+    mask = mask.to(dev)
+    out, lse = run_tree(kvc, q, k, v, kd, vd, lens, mask, count=count)
+    assert kvc.kvc_device_status() == 0
+    verify(q, k, v, kd, vd, lens, mask, out, lse, count=count)
+
+
+@pytest.mark.parametrize("D,G,T", [(64, 2, 3), (128, 4, 40), (128, 1, 5), (256, 2, 3), (256, 5, 33)])
+@pytest.mark.parametrize("drafts", [True, False])
+def test_tree_many_short_pairs(D, G, T, drafts):
+    """More short pairs than blocks, which whole blocks take pair by pair: ragged lengths with empty
+    pairs at either end, sequences without drafted tokens, more than one row tile."""
+    dev = cuda_or_skip()
+    kvc = lib()
+    B, Hkv, cap, dtype = 59, 8, 150, torch.bfloat16
+    q = randn((B, T, Hkv * G, D), 21, dev, dtype)
+    k, v = randn((B, Hkv, cap, D), 22, dev, dtype), randn((B, Hkv, cap, D), 23, dev, dtype)
+    kd, vd = randn((B, T, Hkv, D), 24, dev, dtype), randn((B, T, Hkv, D), 25, dev, dtype)
+    gen = torch.Generator().manual_seed(26)
+    lens = torch.randint(0, cap + 1, (B, Hkv), generator=gen, dtype=torch.int32)
+    lens[0], lens[-1], lens[20] = 0, 0, cap
+    count = torch.randint(0, T + 1, (B,), generator=gen, dtype=torch.int32)
+    count[0], count[1], count[-1] = 0, T, 0
+    lens, count = lens.to(dev), count.to(dev)
+    mask = tree_masks(B, T, 27).to(dev)
+    if not drafts:
+        kd = vd = mask = None
+    out, lse = run_tree(kvc, q, k, v, kd, vd, lens, mask, count=count)
+    assert kvc.kvc_device_status() == 0
+    verify(q, k, v, kd, vd, lens, mask, out, lse, count=count)
+    lens[3, 5], count[7] = cap + 9, -2   # recorded, and clamped
+    out, lse = run_tree(kvc, q, k, v, kd, vd, lens, mask, count=count)
+    assert kvc.kvc_device_status() == 5                     # KVC_DEV_BAD_LENGTH
+    lens[3, 5], count[7] = cap, 0
+    verify(q, k, v, kd, vd, lens, mask, out, lse, count=count)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_tree_chain_cache_only_and_n_valid(dtype):
     """No mask: a chain.  No drafted rows: the cache only.  n_valid instead of lengths, also 0."""
