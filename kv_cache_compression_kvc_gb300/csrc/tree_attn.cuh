@@ -90,13 +90,19 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int 
             __syncwarp();
         }
         TreeRange r{};
-        r.pair = (int)((long long)p.P * g / p.groups);
         const int end = (int)((long long)p.P * (g + 1) / p.groups);
-        r.len = tree_len(p, r.pair);
-        r.cnt = tree_count(p, r.pair / p.Hkv);
-        for (int q = r.pair + lane; q < end; q += 32)
-            r.n += tree_tiles(p, tree_len(p, q), tree_count(p, q / p.Hkv), TS);
+        unsigned at = p.P;                       // the first pair with tiles
+        for (int q = (int)((long long)p.P * g / p.groups) + lane; q < end; q += 32) {
+            const int n = tree_tiles(p, tree_len(p, q), tree_count(p, q / p.Hkv), TS);
+            r.n += n;
+            if (n > 0) at = min(at, (unsigned)q);
+        }
         r.n = __reduce_add_sync(0xffffffffu, r.n);
+        r.pair = (int)__reduce_min_sync(0xffffffffu, at);
+        if (r.n > 0) {
+            r.len = tree_len(p, r.pair);
+            r.cnt = tree_count(p, r.pair / p.Hkv);
+        }
         r.q = 1;
         return r;
     }
@@ -196,7 +202,7 @@ struct TreeWalk {
     __device__ __forceinline__ bool next(const TreeParams &p, int rt, int TS, TreeSeg &s)
     {
         while (left > 0 && pair < p.P) {
-            if (!first || len < 0) {             // (the range knows its first pair's)
+            if (!first) {
                 len = tree_len(p, pair);
                 cnt = tree_count(p, b);
             }
@@ -216,10 +222,7 @@ struct TreeWalk {
                 ++b;
             }
             off = 0;
-            if (s.nt == 0) {
-                len = -1;
-                continue;
-            }
+            if (s.nt == 0) continue;
             left -= s.hi - s.lo;
             first = false;
             return true;
