@@ -1241,6 +1241,11 @@ static kvc_status tree_run(kvc::TreeParams &p, int dtype, bool tc_ok, const kvc_
         return fail(KVC_ERR_CAPACITY, "%s: n_valid %d outside [0, cap %d]", name, p.n_valid, p.cap);
     if ((long long)p.B * p.Hkv > 0x7fffffffLL)
         return fail(KVC_ERR_SHAPE, "%s: batch * heads too large", name);
+    // a block counts its tiles (64 slots at least) in 32 bits: bounded for 128 SMs
+    if ((double)p.B * p.Hkv * (p.cap / 64 + 2) >
+        (double)(1 << 28) *
+            kvc::tree_plan(p.G, p.DK, p.DV, d->n_draft, p.latent != 0, dtype == KVC_BF16, 128).groups)
+        return fail(KVC_ERR_SHAPE, "%s: batch * heads * cap too large", name);
     int32_t *code = nullptr;
     int n_sm = 0;
     kvc_status st = device_info(&code, &n_sm);

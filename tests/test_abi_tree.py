@@ -81,6 +81,18 @@ def test_latent_refusals(kvc, want, cache_kw, draft_kw, call):
     assert st == want and kvc.kvc_last_error()
 
 
+def test_more_tiles_than_a_block_counts_is_refused(kvc):
+    """Broadcast sequences (stride 0) of the largest capacity, for tree and latent attention."""
+    big = {"batch": 1 << 21, "cap": 2 ** 31 - 1, "stride_b": 0, "stride_slot": 576}
+    st = kvc.load().kvc_decode_attn_latent(4096, 16, B_(latent(kvc, **big)), None, 4, B_(draft(kvc)), 1.0,
+                                           4096, None, None, 0, None)
+    assert st == SHAPE and "too large" in kvc.kvc_last_error()
+    big = {"batch": 1 << 21, "cap": 2 ** 31 - 1, "stride_b": 0, "stride_h": 0}
+    st = kvc.load().kvc_decode_attn_tree(4096, 4, B_(cache(kvc, **big)), None, 4, B_(draft(kvc)), 1.0,
+                                         4096, None, None, 0, None)
+    assert st == SHAPE and "too large" in kvc.kvc_last_error()
+
+
 def test_accept_refusals_before_launch(kvc):
     lib = kvc.load()
     c, d, lt = cache(kvc), draft(kvc), latent(kvc)
