@@ -592,8 +592,8 @@ typedef struct {
  * lse (nullable): fp32 [batch][n_draft][n_heads_q].  Any group size up to 64.
  * bf16 caches run on the tensor cores (fp32 accumulation and softmax statistics; the
  * probabilities are rounded to bf16 for the product with the values), fp32 caches in fp32.
- * Two launches (the second joins the partial results of rows whose slots were split over
- * thread blocks).  Results do not depend on timing.  Workspace:
+ * One launch or two (the second joins the partial results of rows whose slots were split over
+ * thread blocks; short rows are not split).  Results do not depend on timing.  Workspace:
  * kvc_decode_attn_tree_workspace_bytes(), 256-byte aligned; it need not be cleared, and calls
  * that share one must not overlap on the GPU. */
 size_t kvc_decode_attn_tree_workspace_bytes(int32_t batch, int32_t n_heads_q,
