@@ -32,6 +32,7 @@
 namespace kvc {
 
 constexpr int kWholeTiles = 12, kWholeWait = 4, kWholeWaitLatent = 3;
+constexpr int kPairEnd = 2;
 constexpr int kDevBadLengthCode = 5;         // KVC_DEV_BAD_LENGTH
 constexpr int kDevBadBlockCode = 9;          // KVC_DEV_BAD_BLOCK
 
@@ -56,12 +57,22 @@ __device__ __forceinline__ int tree_tiles(const TreeParams &p, int len, int cnt,
     return n > 0 ? n : 1;
 }
 
-// Range g holds tiles [g*q + min(g, r), ...): q tiles, one more in the first r ranges.
+// The same with what the end of a pair costs a block (its outputs, then the next pair's first S and
+// softmax with nothing before them), so that ranges with such an end get fewer tiles.
+// Counted as none, one and two tiles: 32 pairs of 5243 slots 29.9, 29.1 and 28.3 us, 8 pairs of up to
+// 13107 slots of 256 dims 29.4, 28.1 and 27.6, 32 latent sequences 45.4, 44.6 and 44.4.
+__device__ __forceinline__ int tree_cost(const TreeParams &p, int len, int cnt, int TS)
+{
+    const int n = tree_tiles(p, len, cnt, TS);
+    return n > 0 ? n + kPairEnd : 0;
+}
+
+// Range g holds the units [g*q + min(g, r), ...): q units, one more in the first r ranges.
 struct TreeRange {
-    int pair, off;               // first pair of the range and the tile inside it
+    int pair, off;               // first pair of the range and the unit inside it
     int len, cnt;                // that pair's slots and drafted tokens
-    int n;                       // tiles in the range
-    long long t0;                // the range's first tile
+    int n;                       // units in the range
+    long long t0;                // the range's first unit
     long long q;
     int r;
     __device__ __forceinline__ int group_of(long long t) const
@@ -93,7 +104,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int 
         const int end = (int)((long long)p.P * (g + 1) / p.groups);
         unsigned at = p.P;                       // the first pair with tiles
         for (int q = (int)((long long)p.P * g / p.groups) + lane; q < end; q += 32) {
-            const int n = tree_tiles(p, tree_len(p, q), tree_count(p, q / p.Hkv), TS);
+            const int n = tree_cost(p, tree_len(p, q), tree_count(p, q / p.Hkv), TS);
             r.n += n;
             if (n > 0) at = min(at, (unsigned)q);
         }
@@ -116,7 +127,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int 
         if (check && (n < 0 || n > p.cap || c < 0 || c > p.T)) record_code(p.dev_code, kDevBadLengthCode);
         n = n < 0 ? 0 : (n > p.cap ? p.cap : n);
         c = c < 0 ? 0 : (c > p.T ? p.T : c);
-        sum += (long long)tree_tiles(p, n, c, TS) * heads;
+        sum += (long long)tree_cost(p, n, c, TS) * heads;
     }
     long long incl = sum;
 #pragma unroll
@@ -147,7 +158,7 @@ __device__ __forceinline__ TreeRange tree_range(const TreeParams &p, int g, int 
             len = len < 0 ? 0 : (len > p.cap ? p.cap : len);
             cnt = count_of(q);
             cnt = cnt < 0 ? 0 : (cnt > p.T ? p.T : cnt);
-            nt = tree_tiles(p, len, cnt, TS);
+            nt = tree_cost(p, len, cnt, TS);
             const long long end = t + (long long)nt * heads;
             if (r.t0 < end || q == q1 - 1) break;
             t = end;
@@ -202,7 +213,7 @@ struct TreeWalk {
     __device__ __forceinline__ bool next(const TreeParams &p, int rt, int TS, TreeSeg &s)
     {
         while (left > 0 && pair < p.P) {
-            if (!first) {
+            if (!first || len < 0) {             // (the range knows its first pair's)
                 len = tree_len(p, pair);
                 cnt = tree_count(p, b);
             }
@@ -212,8 +223,9 @@ struct TreeWalk {
             s.len = len;
             s.cnt = cnt;
             s.nt = tree_tiles(p, len, cnt, TS);
+            const int cost = s.nt > 0 ? min(left, s.nt + kPairEnd - off) : 0;
             s.lo = off;
-            s.hi = min(s.nt, off + left);
+            s.hi = min(s.nt, off + cost);
             s.rows = min(p.RP, cnt * p.G - rt * p.RP);
             s.first = first;
             ++pair;
@@ -222,8 +234,11 @@ struct TreeWalk {
                 ++b;
             }
             off = 0;
-            if (s.nt == 0) continue;
-            left -= s.hi - s.lo;
+            left -= cost;
+            if (s.hi <= s.lo) {                  // (no tiles, or none in this range)
+                len = -1;
+                continue;
+            }
             first = false;
             return true;
         }
@@ -237,7 +252,7 @@ struct TreeWalk {
 // (The division that finds the last group is left for the end: in 64 bits it costs some 500 clocks.)
 struct TreeNote {
     int b = -1, kh = 0, how = 0;
-    long long last = 0;                          // the pair's last tile
+    long long last = 0;                          // the pair's last tile (its unit)
     __device__ __forceinline__ void see(const TreeRange &r, const TreeSeg &s)
     {
         if (s.lo != 0 || s.hi == s.nt) return;

@@ -105,7 +105,7 @@ struct Plan {
     // A latent tile's copies complete on one barrier (its units are keys and values at once), ring
     // of NTB; other caches' units have a barrier each.
     static constexpr int NTB = LATENT ? (NU + KU - 1) / KU + 1 : NU;
-    // S of tile t + 1 is issued before the values of tile t are used
+    // the next tile's keys arrive while a tile's values are still needed
     static_assert(NU >= 2 * KU, "ring too small");
     static constexpr int SMEM = 1024 + Q_BYTES + P_BYTES + ROPE + NU * UNIT + SMALL;
     static constexpr int O_COLS = PT ? DV : MB * RN;
