@@ -726,11 +726,17 @@ def _on_current(index: int, view, what: str) -> None:
     if index < 0 or index != torch._C._cuda_getDevice():
         raise ValueError(f"{what} is on {'the CPU' if index < 0 else f'cuda:{index}'}: the current "
                          "CUDA device is needed")
+    _beside(index, view, what)
+
+
+def _beside(index: int, view, what: str) -> None:
+    """The tensors that a descriptor keeps live on that device too."""
     kept = getattr(view, "_keep", None)
-    if type(kept) is tuple:
-        kept = kept[0]
-    if kept is not None and kept.get_device() != index:
-        raise ValueError(f"{what} is on cuda:{index}, the cache on {kept.device}")
+    if kept is not None:
+        for t in kept if type(kept) is tuple else (kept,):
+            if t is not None and t.get_device() != index:
+                raise ValueError(f"{what} is on cuda:{index}, a tensor of its {type(view).__name__} "
+                                 f"on {t.device}")
 
 
 def _raw_stream(index: int, stream) -> int:
@@ -883,6 +889,7 @@ def kvc_decode_attn_tree_paged(q: torch.Tensor, pool: kvc_block_pool, pt: kvc_pa
     """q [B, T, Hq, D] -> out [B, T, Hq, D] over each sequence's page table and its drafts."""
     B, Hkv, D = pt.batch, pool.n_heads_kv, pool.d_head
     out, index = _attn_args(q, pool, D, D, pool.dtype, B, draft, (B, draft.n_draft, Hkv, D), out, lse)
+    _beside(index, pt, "q")
     if ws is None:
         ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
     wp, wb = _space(ws)
@@ -962,6 +969,8 @@ def kvc_tree_accept_paged(pool: kvc_block_pool, pt: kvc_page_table, free_pool: k
     """kvc_tree_accept for a paged cache; returns accepted int32 [B] (0: refused)."""
     index = _accept_args(draft, pool, (pt.batch, draft.n_draft, pool.n_heads_kv, pool.d_head),
                          pool.dtype, path, n_accept)
+    _beside(index, pt, "the draft")
+    _beside(index, free_pool, "the draft")
     if accepted is None:
         accepted = torch.empty(pt.batch, dtype=torch.int32, device=path.device)
     else:
@@ -980,6 +989,7 @@ def kvc_latent_expand(cache: kvc_latent_cache, w_k: torch.Tensor, w_v: torch.Ten
     c, H, D = cache, dst.n_heads_kv, dst.d_head
     index = w_k.get_device()
     _on_current(index, cache, "w_k")
+    _beside(index, dst, "w_k")
     _need(w_k, "w_k", _DTYPES.get(c.dtype), (H, D - c.d_rope, c.d_latent), index)
     _need(w_v, "w_v", _DTYPES.get(c.dtype), (H, D, c.d_latent), index)
     _need(len, "len", torch.int32, (c.batch,), index)

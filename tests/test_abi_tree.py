@@ -194,3 +194,29 @@ def test_binding_checks_its_tensors(kvc):
                             torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         kvc.kvc_latent_expand(lat, torch.zeros(2, 1, 128), torch.zeros(2, 64, 128), c, n_valid=3)
+
+
+def test_descriptors_of_another_device_are_refused(kvc, monkeypatch):
+    """Any tensor that a descriptor keeps: the first or a later one, in a tuple or alone."""
+    class On:
+        def __init__(self, index):
+            self.device = f"cuda:{index}"
+            self.get_device = lambda: index
+
+    class View:
+        pass
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    v = View()
+    kvc._on_current(0, v, "q")                              # made without tensors: nothing known
+    for kept in ((On(0), On(0)), (On(0), None), On(0)):
+        v._keep = kept
+        kvc._on_current(0, v, "q")
+    for kept in ((On(0), On(1)), (On(1), None), On(1), (On(0), On(0), On(0), On(-1))):
+        v._keep = kept
+        with pytest.raises(ValueError, match="View"):
+            kvc._on_current(0, v, "q")
+    with pytest.raises(ValueError, match="current"):
+        kvc._on_current(1, View(), "q")
+    with pytest.raises(ValueError, match="CPU"):
+        kvc._on_current(-1, View(), "q")
