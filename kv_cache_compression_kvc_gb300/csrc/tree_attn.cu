@@ -196,16 +196,25 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
             if (2 * ty < s.rows) {
                 const float *qa = sQ + 2 * ty * DK, *qb = qa + DK;
                 const float *kk = sK + tx * KS;
+                // sums of 32 dims, then of those: one sum over all of them loses twice as much
+                for (int d0 = 0; d0 < DK; d0 += 32) {
+                    const int d1 = min(DK, d0 + 32);
+                    float part[2][4] = {};
 #pragma unroll 4
-                for (int d = 0; d < DK; d += 4) {
-                    const float4 a = *reinterpret_cast<const float4 *>(qa + d);
-                    const float4 b = *reinterpret_cast<const float4 *>(qb + d);
+                    for (int d = d0; d < d1; d += 4) {
+                        const float4 a = *reinterpret_cast<const float4 *>(qa + d);
+                        const float4 b = *reinterpret_cast<const float4 *>(qb + d);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 x = *reinterpret_cast<const float4 *>(kk + j * 16 * KS + d);
-                        acc[0][j] = fmaf(a.x, x.x, fmaf(a.y, x.y, fmaf(a.z, x.z, fmaf(a.w, x.w, acc[0][j]))));
-                        acc[1][j] = fmaf(b.x, x.x, fmaf(b.y, x.y, fmaf(b.z, x.z, fmaf(b.w, x.w, acc[1][j]))));
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 x = *reinterpret_cast<const float4 *>(kk + j * 16 * KS + d);
+                            part[0][j] = fmaf(a.x, x.x, fmaf(a.y, x.y, fmaf(a.z, x.z, fmaf(a.w, x.w, part[0][j]))));
+                            part[1][j] = fmaf(b.x, x.x, fmaf(b.y, x.y, fmaf(b.z, x.z, fmaf(b.w, x.w, part[1][j]))));
+                        }
                     }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][j] += part[i][j];
                 }
             }
 #pragma unroll
@@ -272,10 +281,10 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
                     for (int i = 0; i < RPT; ++i) {
                         const float4 w =
                             *reinterpret_cast<const float4 *>(sP + (orow + i) * (kTile + 4) + j);
-                        o[i].x = fmaf(w.x, v[0].x, fmaf(w.y, v[1].x, fmaf(w.z, v[2].x, fmaf(w.w, v[3].x, o[i].x))));
-                        o[i].y = fmaf(w.x, v[0].y, fmaf(w.y, v[1].y, fmaf(w.z, v[2].y, fmaf(w.w, v[3].y, o[i].y))));
-                        o[i].z = fmaf(w.x, v[0].z, fmaf(w.y, v[1].z, fmaf(w.z, v[2].z, fmaf(w.w, v[3].z, o[i].z))));
-                        o[i].w = fmaf(w.x, v[0].w, fmaf(w.y, v[1].w, fmaf(w.z, v[2].w, fmaf(w.w, v[3].w, o[i].w))));
+                        o[i].x += fmaf(w.x, v[0].x, fmaf(w.y, v[1].x, fmaf(w.z, v[2].x, w.w * v[3].x)));
+                        o[i].y += fmaf(w.x, v[0].y, fmaf(w.y, v[1].y, fmaf(w.z, v[2].y, w.w * v[3].y)));
+                        o[i].z += fmaf(w.x, v[0].z, fmaf(w.y, v[1].z, fmaf(w.z, v[2].z, w.w * v[3].z)));
+                        o[i].w += fmaf(w.x, v[0].w, fmaf(w.y, v[1].w, fmaf(w.z, v[2].w, w.w * v[3].w)));
                     }
                 }
             }
