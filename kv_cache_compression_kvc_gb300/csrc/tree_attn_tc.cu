@@ -34,11 +34,11 @@
 // KVC_DEV_TIMEOUT, stops issuing and walks to its end, waits for its loads and products in flight
 // and frees its tensor memory.
 //
-// Measured, device time: 32 pairs of 5243 slots, 64 rows, 128 dims 29 us (HBM alone 13; a block has
+// Measured, device time: 32 pairs of 5243 slots, 64 rows, 128 dims 28.6 us (HBM alone 13; a block has
 // nine tiles, so the start, 5 us until its first keys, and the merge, 5 us, count as much as the
-// stream); 512 paged pairs of 817 slots, 8 rows 56 us (33); 16 pairs of 131072 slots, 256 rows 256 us
+// stream); 512 paged pairs of 817 slots, 8 rows 56 us (33); 16 pairs of 131072 slots, 256 rows 259 us
 // (161; 8.5 TB/s from L2 to the SMs); 32 latent sequences of 4608 slots, 32 rows 45 us (26); 8 of
-// 6144 slots, 512 rows in eight row tiles 81 us (28 by the products' operations; shared memory moves
+// 6144 slots, 512 rows in eight row tiles 80 us (28 by the products' operations; shared memory moves
 // 320 KB for a tile of 64 slots by 64 rows, which at 128 B a clock is 56 us alone).
 //
 // Slots past the valid ones hold anything, so their value rows are zeroed in shared memory before
