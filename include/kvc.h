@@ -637,6 +637,15 @@ kvc_status kvc_tree_accept_paged(const kvc_block_pool *pool, const kvc_page_tabl
                                  void *stream);
 
 /* ---------------------------------------------------------------------------------------- */
+/* KVC_TEST_STARVE in a descriptor's `reserved`: a test hook with no counterpart on the pages, for
+ * exercising the bounded waits of the tensor-core kernels without a GPU fault, as
+ * KVC_DECODE_TEST_STARVE does for the decode kernels.  The kernel loads nothing, so its first waits
+ * run out after a short bounded spin; every block still finishes and kvc_device_status() reports
+ * KVC_DEV_TIMEOUT.  The outputs of such a call are undefined, the next call without it is unaffected.
+ * A wait that gives up for a real reason (a lost arrival) ends the same way.  Calls that run on the
+ * CUDA cores have no such waits and ignore it. */
+#define KVC_TEST_STARVE 0x53545256u
+
 /* Latent caches: one row per token for all heads, from which every head's key and value follow by
  * two matrices (low-rank joint compression of keys and values; no counterpart on the pages).
  * Row (b, s): c[b*stride_b + s*stride_slot + 0 .. d_latent-1] is the latent vector, the d_rope
@@ -655,7 +664,7 @@ typedef struct {
     int32_t cap;            /* slots per sequence */
     int32_t d_latent;
     int32_t d_rope;
-    int32_t reserved;
+    int32_t reserved;       /* 0, or KVC_TEST_STARVE for kvc_latent_expand */
     int64_t stride_b;       /* elements */
     int64_t stride_slot;
 } kvc_latent_cache;

@@ -22,7 +22,7 @@ thread_local std::string g_last_error;
 __device__ int32_t g_dev_code;
 
 constexpr int kMaxDevices = 64;
-// polls before a wait gives up under KVC_DECODE_TEST_STARVE (a short, bounded stall)
+// polls before a wait gives up under KVC_DECODE_TEST_STARVE or KVC_TEST_STARVE (a short, bounded stall)
 constexpr uint32_t kTestSpinLimit = 1024;
 std::mutex g_mutex;
 int32_t *g_code_ptr[kMaxDevices] = {};
@@ -1521,6 +1521,10 @@ kvc_status kvc_latent_expand(const kvc_latent_cache *cache, const int32_t *len, 
     p.k = dst->k; p.v = dst->v;
     p.sb = dst->stride_b; p.sh = dst->stride_h; p.ss = dst->stride_slot;
     p.dst_cap = dst->cap;
+    if ((uint32_t)cache->reserved == KVC_TEST_STARVE) {
+        p.starve = 1;
+        p.spin_limit = kTestSpinLimit;
+    }
     p.dev_code = code;
     const cudaError_t e = kvc::launch_latent_expand(p, cache->dtype, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "latent expand launch");

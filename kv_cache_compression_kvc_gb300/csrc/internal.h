@@ -360,6 +360,8 @@ struct ExpandParams {
     void *k, *v;
     int64_t sb, sh, ss;
     int32_t dst_cap;
+    int32_t starve;              // test hook: copy nothing, so the first waits run out
+    uint32_t spin_limit;         // polls before a bounded wait gives up (0: the default)
     int32_t *dev_code;
 };
 cudaError_t launch_latent_expand(const ExpandParams &p, int dtype, cudaStream_t stream);

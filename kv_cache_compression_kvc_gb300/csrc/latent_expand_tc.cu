@@ -17,14 +17,20 @@
 // by multicast were measured and dropped (52.9 and 59.9 us against 53.0 alone: L2 is not what
 // bounds it).
 //
-// Roles (352 threads): warp 0 copies (TMA), warp 1 issues the products, warps 2-9 (two sets, one
+// Roles (320 threads): warp 0 copies (TMA), warp 1 issues the products, warps 2-9 (two sets, one
 // for either accumulator) take a slot per thread from tensor memory, round once, and pass 32
 // columns at a time through shared memory so that a store instruction writes contiguous pieces of
 // 8 slots (32-byte pieces of 32 slots straight from registers: 57 us against 35 for the
 // products alone); the shared rope part goes from the latent rows to the keys in the same
-// stores.  Warp 10 waits for the stages on behalf of warp 1 and passes them on through named
-// barriers: a satisfied mbarrier wait between two stages costs the issuing warp about 200 clocks,
-// in which the tensor cores run dry.  Every wait is bounded, as in tree_attn_tc.cu.
+// stores.  Warp 1 looks at the next stage's barrier before it issues a stage's products and waits
+// only if it had not arrived: a satisfied wait between two stages costs it about 200 clocks, in
+// which the tensor cores run dry.  (A warp of its own that waited and passed the stages on: through
+// a named barrier 1.6 us faster, 52.6, but a wait without a limit; through a counted word 55.8 us.)
+//
+// Every wait is bounded (p.spin_limit polls).  One that gives up records KVC_DEV_TIMEOUT and raises
+// s_abort, which ends the others.  The warp that copies then stops, warp 1 issues no more products,
+// the others walk to their ends, and the block exits once its copies and products in flight are
+// done.  No warp waits for another in any other way, but for the barriers over the whole block.
 #include "tc_ops.cuh"
 #include "internal.h"
 
@@ -32,9 +38,8 @@ namespace kvc {
 
 namespace {
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 320;
 constexpr int kStaging = 8 * 2048;           // a writing warp's [32 slots][32 columns]
-constexpr int kBarStage = 1;                 // named barriers: a stage has arrived
 constexpr int kTile = 128;                   // slots
 constexpr int kSub = kTile * 128;            // bytes of [128 slots][64]
 constexpr int kSmemMax = 227 * 1024;
@@ -182,21 +187,22 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
     pdl_wait();
     const int per_tile = p.H * pl.jobs;
     const ExpandRange range = expand_range(p, per_tile);
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (!mbar_wait_abortable(bar, parity, kMbarSpinLimit, s_abort)) {
-            *s_abort = 1;
-            record_code(p.dev_code, kDevCodeTimeout);
-        }
+    auto wait = [&](uint32_t bar, uint32_t parity) -> bool {             // whether the phase completed
+        if (mbar_wait_abortable(bar, parity, p.spin_limit, s_abort)) return true;
+        *s_abort = 1;
+        record_code(p.dev_code, kDevCodeTimeout);
+        return false;
     };
     ExpandWalk walk(range, per_tile);
     int lo = 0, hi = 0;
     unsigned n_w = 0, n_a = 0;                   // the producer's counts (for the drain)
     if (warp == 0) {
         uint32_t slot = 0, ph = 1;
+        bool go = p.starve == 0;                 // (test hook: no copies, so the first waits run out)
         while (walk.next(p, lo, hi)) {
-            if (n_a > 0) wait(b_a_empty, (n_a - 1) & 1);
-            const bool go = !*s_abort;
-            if (go && tc::elect()) {
+            if (n_a > 0 && go) go = __all_sync(0xffffffffu, wait(b_a_empty, (n_a - 1) & 1));
+            if (!go) break;
+            if (tc::elect()) {
                 mbar_arrive_expect_tx(b_a_full, (uint32_t)subs * kSub);
                 for (int i = 0; i < subs; i += 2)
                     tc::tma_5d(sA + i * kSub, &maps.c, 0, walk.tile * kTile, i, walk.b, 0, b_a_full);
@@ -209,8 +215,9 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
                 const uint32_t bytes = (uint32_t)((dok ? pl.nk : 0) + (dov ? p.D : 0)) * 128u;
                 const uint32_t v_off = dok ? (uint32_t)pl.nk16 * 128u : 0u;
                 for (int k = 0; k < subs; ++k, ++n_w) {
-                    if (n_w >= (unsigned)pl.stages) wait(b_empty + 8 * slot, ph);
-                    if (go && tc::elect()) {
+                    if (n_w >= (unsigned)pl.stages) go = __all_sync(0xffffffffu, wait(b_empty + 8 * slot, ph));
+                    if (!go) break;
+                    if (tc::elect()) {
                         const uint32_t dst = sW + slot * pl.stage, bar = b_full + 8 * slot;
                         mbar_arrive_expect_tx(bar, bytes);
                         if (dok) tc::tma_5d(dst, &maps.wk, 0, h * pl.nk, k, 0, 0, bar);
@@ -222,6 +229,7 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
                         ph ^= 1;
                     }
                 }
+                if (!go) break;
                 if (++job == pl.jobs) {
                     job = 0;
                     ++h;
@@ -229,10 +237,12 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
             }
         }
     } else if (warp == 1) {
-        uint32_t slot = 0;
+        uint32_t slot = 0, ph = 0;
         unsigned n = 0;                          // accumulators so far
+        bool in = false;                         // the next stage was seen to have arrived
+        bool go = true;                          // no wait of this lane has given up
         while (walk.next(p, lo, hi)) {
-            wait(b_a_full, n_a & 1);
+            go &= wait(b_a_full, n_a & 1);
             ++n_a;
             int job = lo - lo / pl.jobs * pl.jobs;
             for (int j = lo; j < hi; ++j, ++n) {
@@ -240,40 +250,32 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
                 const uint32_t id = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(cols >> 3) << 17) |
                                     ((uint32_t)(kTile >> 4) << 24);
                 const uint32_t buf = n & 1, d = tmem + buf * 256;
-                if (n >= 2) wait(b_acc_empty + 8 * buf, ((n >> 1) - 1) & 1);
+                if (n >= 2) go &= wait(b_acc_empty + 8 * buf, ((n >> 1) - 1) & 1);
                 for (int k = 0; k < subs; ++k) {
-                    tc::bar_sync(kBarStage + slot, 64);
+                    if (!__all_sync(0xffffffffu, in)) go &= wait(b_full + 8 * slot, ph);
+                    const uint32_t at = slot;
+                    if (++slot == (uint32_t)pl.stages) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
+                    in = tc::test(b_full + 8 * slot, ph);    // answered while the products are issued
                     tc::fence_after();
-                    if (tc::elect()) {
-                        const uint32_t a = sA + k * kSub, w = sW + slot * pl.stage;
+                    if (tc::elect() && go) {
+                        const uint32_t a = sA + k * kSub, w = sW + at * pl.stage;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             tc::mma(d, tc::desc_k(a + kk * 32), tc::desc_k(w + kk * 32), id, k > 0 || kk > 0);
-                        tc::commit(b_empty + 8 * slot);
+                        tc::commit(b_empty + 8 * at);
                         if (k == subs - 1) {
                             tc::commit(b_acc_full + 8 * buf);
                             if (j == hi - 1) tc::commit(b_a_empty);
                         }
                     }
                     __syncwarp();
-                    if (++slot == (uint32_t)pl.stages) slot = 0;
                 }
                 if (++job == pl.jobs) job = 0;
             }
         }
-    } else if (warp == 10) {
-        // a slot's barrier cannot be reached twice: it is loaded again only after warp 1 used it
-        uint32_t slot = 0, ph = 0;
-        while (walk.next(p, lo, hi))
-            for (int i = (hi - lo) * subs; i > 0; --i) {
-                wait(b_full + 8 * slot, ph);
-                __syncwarp();
-                tc::bar_arrive(kBarStage + slot, 64);
-                if (++slot == (uint32_t)pl.stages) {
-                    slot = 0;
-                    ph ^= 1;
-                }
-            }
     } else {
         const int q4 = warp & 3, set = (warp - 2) >> 2;
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
@@ -368,9 +370,11 @@ latent_expand_tc_kernel(const __grid_constant__ ExpandMaps maps, const ExpandPar
 
 }  // namespace
 
-cudaError_t launch_latent_expand_tc(const ExpandParams &p, cudaStream_t stream, bool *used)
+cudaError_t launch_latent_expand_tc(const ExpandParams &params, cudaStream_t stream, bool *used)
 {
     *used = false;
+    ExpandParams p = params;
+    if (p.spin_limit == 0) p.spin_limit = kMbarSpinLimit;
     ExpandPlan pl{};
     pl.nk = p.D - p.E;
     pl.nk16 = (pl.nk + 15) / 16 * 16;
