@@ -6,9 +6,9 @@
 // four independent copies in flight.
 //
 // Paged caches first need blocks.  tree_accept_pages_kernel, one block for the whole batch, checks
-// every sequence, numbers the blocks they need in sequence order (a block-wide scan) and takes
-// them from the top of the free stack, so that ids do not depend on timing; the copy kernel
-// follows.
+// every sequence (its path, its lengths, its partly filled page), numbers the blocks they need in
+// sequence order (a block-wide scan) and takes them from the top of the free stack, so that ids do
+// not depend on timing; the copy kernel follows.
 #include "common.cuh"
 #include "internal.h"
 
@@ -70,8 +70,7 @@ __device__ __forceinline__ void copy_rows(const AcceptParams &p, int b, int h, i
                 const size_t off = (((size_t)b * p.T + t) * p.H + h) * p.row_bytes +
                                    (size_t)(isv ? c - vpr : c) * 16;
                 x[u] = __ldg(reinterpret_cast<const uint4 *>((isv ? vd : kd) + off));
-                char *base = dst(row, isv);
-                if (base != nullptr) to[u] = base + (size_t)(isv ? c - vpr : c) * 16;
+                to[u] = dst(row, isv) + (size_t)(isv ? c - vpr : c) * 16;
             }
         }
 #pragma unroll
@@ -135,6 +134,13 @@ __global__ void __launch_bounds__(kPageThreads) tree_accept_pages_kernel(const A
                            n > p.max_blocks * p.bs - len)) {
                 code = kDevBadLen;
                 n = -1;
+            }
+            if (n > 0 && len % p.bs != 0) {  // the page that takes the first token is there already
+                const int id = p.table[(size_t)b * p.max_blocks + len / p.bs];
+                if (id < 0 || id >= p.n_pool) {
+                    code = kDevBadBlk;
+                    n = -1;
+                }
             }
             if (n < 0) {
                 record_code(p.dev_code, code);
@@ -202,7 +208,6 @@ __global__ void __launch_bounds__(kPageThreads) tree_accept_pages_kernel(const A
 
 __global__ void __launch_bounds__(kCopyThreads) tree_accept_paged_kernel(const AcceptParams p)
 {
-    __shared__ int s_bad;
     pdl_trigger();
     pdl_wait();
     const int pair = blockIdx.x, b = pair / p.H, h = pair - b * p.H;
@@ -210,19 +215,9 @@ __global__ void __launch_bounds__(kCopyThreads) tree_accept_paged_kernel(const A
     if (n == 0) return;
     const int first = p.len[b] - n;
     const int32_t *tab = p.table + (size_t)b * p.max_blocks;
-    // the last block was there before: its id comes from the caller's table
-    if (threadIdx.x == 0) {
-        const int id = tab[first / p.bs];
-        s_bad = id < 0 || id >= p.n_pool;
-        if (s_bad) record_code(p.dev_code, kDevBadBlk);
-    }
-    __syncthreads();
-    const bool bad = s_bad;
-    const int lb0 = first / p.bs;
     copy_rows(p, b, h, n, [&](int row, bool isv) -> char * {
-        const int slot = first + row, lb = slot / p.bs;
-        if (bad && lb == lb0) return nullptr;
-        const size_t blk = (size_t)tab[lb];
+        const int slot = first + row;
+        const size_t blk = (size_t)tab[slot / p.bs];     // (every id was looked at before)
         char *base = static_cast<char *>(isv ? p.v : p.k);
         return base + (((size_t)h * p.n_pool + blk) * p.bs + slot % p.bs) * p.row_bytes;
     });
