@@ -630,7 +630,9 @@ kvc_status kvc_tree_accept(const kvc_cache *cache, int32_t *len, const kvc_draft
  * n_blocks and len follow.  accepted: device int32[batch], the tokens appended (n_accept[b], or
  * 0 where the sequence was refused: besides the cases above KVC_DEV_BAD_LENGTH for lengths that
  * disagree with n_blocks or a table without room, KVC_DEV_POOL_EMPTY when the stack has too few
- * ids left for it, KVC_DEV_BAD_BLOCK for an id outside the pool). */
+ * ids left for it, KVC_DEV_BAD_BLOCK for an id outside the pool, of its partly filled page or among
+ * those it would pop).  A refused sequence pops nothing: only the bad ids leave the stack, the good
+ * ones among them serve the sequences behind it, in order. */
 kvc_status kvc_tree_accept_paged(const kvc_block_pool *pool, const kvc_page_table *pt,
                                  const kvc_free_pool *free_pool, const kvc_draft *draft,
                                  const int32_t *path, const int32_t *n_accept, int32_t *accepted,

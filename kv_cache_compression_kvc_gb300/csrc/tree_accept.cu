@@ -108,21 +108,20 @@ __global__ void __launch_bounds__(kCopyThreads) tree_accept_kernel(const AcceptP
 __global__ void __launch_bounds__(kPageThreads) tree_accept_pages_kernel(const AcceptParams p)
 {
     __shared__ int s_warp[kPageThreads / 32];
-    __shared__ int s_taken, s_top;
+    __shared__ int s_top;                    // ids left on the stack
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int top0 = 0;                            // (of thread 0)
     if (threadIdx.x == 0) {
-        s_taken = 0;
         int top = *p.free_top;
         if (top < 0 || top > p.free_cap) {
             record_code(p.dev_code, kDevPoolEmpty_);
             top = 0;
         }
-        s_top = top;
+        s_top = top0 = top;
     }
     __syncthreads();
-    const int top = s_top;
     for (int b0 = 0; b0 < p.B; b0 += kPageThreads) {
         const int b = b0 + threadIdx.x;
         int n = 0, need = 0, len = 0, nb = 0, code = 0;
@@ -149,7 +148,8 @@ __global__ void __launch_bounds__(kPageThreads) tree_accept_pages_kernel(const A
             need = n > 0 ? (len + n + p.bs - 1) / p.bs - nb : 0;
         }
         // the blocks taken before this sequence: a scan, or -- when the stack cannot serve
-        // everyone and sequences must be skipped -- one by one in order
+        // everyone or holds an id that is no block, and sequences must be skipped -- one by one
+        // in order
         int incl = need;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -158,42 +158,54 @@ __global__ void __launch_bounds__(kPageThreads) tree_accept_pages_kernel(const A
         }
         if (lane == 31) s_warp[warp] = incl;
         __syncthreads();
-        int before = s_taken + incl - need, all = s_taken;
+        int before = incl - need, all = 0;
         for (int w = 0; w < kPageThreads / 32; ++w) {
             if (w < warp) before += s_warp[w];
             all += s_warp[w];
         }
-        if (all > top) {
-            __syncthreads();
-            for (int i = 0; i < kPageThreads; ++i) {
-                if (threadIdx.x == i) {
-                    before = s_taken;
-                    if (before + need > top) {
+        const int top = s_top;
+        int first = top - before;            // this sequence's ids: first - 1, first - 2, ...
+        bool skip = all > top;
+        if (!skip)
+            for (int i = 0; i < need; ++i) {
+                const int id = p.free_ids[first - 1 - i];
+                skip |= id < 0 || id >= p.n_pool;
+            }
+        if (__syncthreads_or(skip)) {
+            for (int i = 0; i < min(kPageThreads, p.B - b0); ++i) {
+                if (threadIdx.x == i && need > 0) {
+                    first = s_top;
+                    if (need > first) {
                         record_code(p.dev_code, kDevPoolEmpty_);
-                        n = 0;
-                        need = 0;
+                        n = need = 0;
+                    } else {
+                        // a bad id leaves the stack; the good ones with it stay for the sequences
+                        // behind
+                        int keep = first - need;
+                        for (int j = first - need; j < first; ++j) {
+                            const int id = p.free_ids[j];
+                            if (id < 0 || id >= p.n_pool) continue;
+                            if (keep != j) p.free_ids[keep] = id;
+                            ++keep;
+                        }
+                        if (keep < first) {
+                            record_code(p.dev_code, kDevBadBlk);
+                            n = need = 0;
+                            s_top = keep;
+                        } else {
+                            s_top = first - need;
+                        }
                     }
-                    s_taken = before + need;
                 }
                 __syncthreads();
             }
-        } else {
-            __syncthreads();
-            if (threadIdx.x == 0) s_taken = all;
+        } else if (threadIdx.x == 0) {
+            s_top = top - all;
         }
         if (b < p.B) {
-            bool ok = true;
-            for (int i = 0; i < need; ++i) {
-                const int id = p.free_ids[top - 1 - before - i];
-                ok &= id >= 0 && id < p.n_pool;
-            }
-            if (!ok) {
-                record_code(p.dev_code, kDevBadBlk);
-                n = 0;
-            }
             if (n > 0) {
                 for (int i = 0; i < need; ++i) {
-                    p.table[(size_t)b * p.max_blocks + nb + i] = p.free_ids[top - 1 - before - i];
+                    p.table[(size_t)b * p.max_blocks + nb + i] = p.free_ids[first - 1 - i];
                     p.score[(size_t)b * p.max_blocks + nb + i] = 0.f;
                 }
                 p.n_blocks[b] = nb + need;
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kPageThreads) tree_accept_pages_kernel(const A
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0 && s_taken > 0) *p.free_top = top - s_taken;
+    if (threadIdx.x == 0 && s_top != top0) *p.free_top = s_top;
 }
 
 __global__ void __launch_bounds__(kCopyThreads) tree_accept_paged_kernel(const AcceptParams p)

@@ -93,3 +93,57 @@ def test_a_bad_last_page_refuses_its_sequence(bad):
     p = Pages(dev, 4, 40, [5, 6, 4, 3, 7], [[0, bad], [1, 2], [bad], [bad], [3, bad]], [20, 21, 22, 23], 5)
     want, codes = p.check(lib(), [2, 3, 2, 0, 8])
     assert want == [0, 3, 2, 0, 0] and codes == {BAD_BLOCK}
+
+
+def test_bad_ids_leave_the_stack_and_the_others_stay():
+    """A sequence that would take an id outside the pool is refused; the id is dropped, the good ones
+    taken with it serve the sequences behind, in the stack's order."""
+    dev = cuda_or_skip()
+    none = [[] for _ in range(4)]
+    # the first needs two blocks and finds one: the good one stays for the second
+    p = Pages(dev, 4, 40, [0] * 4, none, [20, 21, 22, 77, 24], 4)
+    assert p.check(lib(), [5, 3, 8, 0]) == ([0, 3, 8, 0], {BAD_BLOCK}) and p.ids == [20]
+    # with the last good id kept, the second is served; the third finds an empty stack
+    p = Pages(dev, 4, 40, [0] * 4, none, [20, -5], 4)
+    assert p.check(lib(), [8, 4, 1, 0]) == ([0, 4, 0, 0], {BAD_BLOCK, POOL_EMPTY}) and p.ids == []
+    # nothing but bad ids; a sequence that needs no block is appended all the same
+    p = Pages(dev, 4, 40, [0, 5, 0, 0], [[], [30, 31], [], []], [99, -1, 40], 4)
+    assert p.check(lib(), [5, 3, 4, 4]) == ([0, 3, 0, 0], {BAD_BLOCK, POOL_EMPTY})
+    # too few ids for the first, a bad one for the second, good ones for the others
+    p = Pages(dev, 2, 40, [0] * 4, none, [20, 21, 40], 4)
+    assert p.check(lib(), [8, 3, 2, 1]) == ([0, 0, 2, 1], {BAD_BLOCK, POOL_EMPTY}) and p.ids == []
+
+
+@pytest.mark.parametrize("B,bad,short", [(1, 1, 0), (33, 0, 1), (33, 3, 0), (33, 6, 1), (1300, 0, 0),
+                                         (1300, 9, 0), (1300, 0, 1), (1300, 40, 1)])
+def test_many_sequences_with_bad_ids_and_a_short_stack(B, bad, short):
+    """More sequences than the kernel takes at once, bad ids anywhere on the stack, a stack that cannot
+    serve everyone, bad last pages: as one sequence after another."""
+    dev = cuda_or_skip()
+    gen = torch.Generator().manual_seed(B * 100 + bad * 2 + short)
+
+    def rand(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=gen))
+
+    bs = 3
+    lens = [rand(0, 6) for _ in range(B)]
+    n = [rand(0, 8) for _ in range(B)]
+    held = sum(-(-x // bs) for x in lens)
+    need = sum(-(-(x + m) // bs) - -(-x // bs) for x, m in zip(lens, n))
+    spare = need // 2 if short else need + 5
+    n_pool = held + spare
+    order = torch.randperm(n_pool, generator=gen).tolist()
+    tables = []
+    for x in lens:
+        tables.append([order.pop() for _ in range(-(-x // bs))])
+    ids = order
+    for _ in range(min(bad, len(ids))):
+        ids[rand(0, len(ids) - 1)] = n_pool + rand(0, 1000)
+    if bad > 3:
+        for b in range(0, B, 7):
+            if tables[b]:
+                tables[b][-1] = -rand(1, 1000)
+    p = Pages(dev, bs, n_pool, lens, tables, ids, 6, H=1)
+    want, codes = p.check(lib(), n)
+    assert sum(want) > 0 or B == 1
+    assert bad or short or (want == n and not codes)
