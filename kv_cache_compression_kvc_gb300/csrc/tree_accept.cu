@@ -34,7 +34,10 @@ __device__ __forceinline__ int path_tokens(const AcceptParams &p, int b, int lan
         return -1;
     }
     int cnt = p.count != nullptr ? p.count[b] : p.T;
-    cnt = cnt < 0 ? 0 : (cnt > p.T ? p.T : cnt);
+    if (cnt < 0 || cnt > p.T) {              // recorded and clamped, as the attention does
+        if (lane == 0) record_code(p.dev_code, kDevBadLen);
+        cnt = cnt < 0 ? 0 : p.T;
+    }
     bool bad = false;
     for (int i = lane; i < n; i += lanes) {
         const int t = p.path[(size_t)b * p.T + i];
