@@ -7,6 +7,7 @@ provides device memory and streams.  There is no fallback: if libkvc.so has not 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -208,6 +209,20 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, *given):
+    """Where a call makes those tensors that it was not given: on the stream that its kernels run on.
+    The allocator hands a freed tensor's memory on in the order of the stream that it was made on, so
+    a workspace made on the current stream could be another tensor's while kernels on `stream`
+    still use it, and its zeroes could come after them.  An output made here belongs to `stream` (use
+    on another one: wait for it, and record_stream, as for any tensor)."""
+    if stream is None or (given and all(t is not None for t in given)):
+        return _HERE
+    return torch.cuda.stream(stream)
+
+
 def _dtype_code(dt: torch.dtype) -> int:
     if dt == torch.float32:
         return KVC_F32
@@ -308,10 +323,11 @@ def kvc_decode_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """q [B, Hq, D] -> out [B, Hq, D] fp32 (see kvc.h for valid slots and logits layout)."""
     c = cache if cache is not None else cache_view(k_cache, v_cache)
     B, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(B, Hq, c.n_heads_kv, D, c.cap, q.device)
+    with _on(stream, out, ws):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = decode_workspace(B, Hq, c.n_heads_kv, D, c.cap, q.device)
     wp, wb = _ws_ptr(ws)
     lstride = logits.stride(-2) if logits is not None else 0
     _check(load().kvc_decode_attn(
@@ -330,10 +346,11 @@ def kvc_decode_attn_ex(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     """kvc_decode_attn with flags (KVC_DECODE_KV_SETTLED: see kvc.h for the caller's promise)."""
     c = cache if cache is not None else cache_view(k_cache, v_cache)
     B, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(B, Hq, c.n_heads_kv, D, c.cap, q.device)
+    with _on(stream, out, ws):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = decode_workspace(B, Hq, c.n_heads_kv, D, c.cap, q.device)
     wp, wb = _ws_ptr(ws)
     lstride = logits.stride(-2) if logits is not None else 0
     _check(load().kvc_decode_attn_ex(
@@ -368,10 +385,11 @@ def kvc_decode_attn_alibi(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     """StreamingLLM decode with ALiBi at in-cache positions: q [B, Hq, D] -> out [B, Hq, D]."""
     c = cache if cache is not None else cache_view(k_cache, v_cache)
     B, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(B, Hq, c.n_heads_kv, D, c.cap, q.device)
+    with _on(stream, out, ws):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = decode_workspace(B, Hq, c.n_heads_kv, D, c.cap, q.device)
     wp, wb = _ws_ptr(ws)
     lstride = logits.stride(-2) if logits is not None else 0
     _check(load().kvc_decode_attn_alibi(
@@ -437,11 +455,12 @@ def kvc_decode_attn_paged(q: torch.Tensor, pool: kvc_block_pool, pt: kvc_page_ta
                           stream=None) -> torch.Tensor:
     """q [B, Hq, D] -> out [B, Hq, D] fp32 over each sequence's page table."""
     B, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = decode_workspace(B, Hq, pool.n_heads_kv, D, pt.max_blocks * pool.block_size,
-                              q.device)
+    with _on(stream, out, ws):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = decode_workspace(B, Hq, pool.n_heads_kv, D, pt.max_blocks * pool.block_size,
+                                  q.device)
     wp, wb = _ws_ptr(ws)
     lstride = logits.stride(-2) if logits is not None else 0
     _check(load().kvc_decode_attn_paged(
@@ -457,8 +476,9 @@ def kvc_block_prompt_select(s: torch.Tensor, k_prompt: torch.Tensor, v_prompt: t
     """s [B, Hkv, >= seq_len] per-token prompt scores; k/v_prompt [B, Hkv, cap, D]."""
     c = cache_view(k_prompt, v_prompt)
     if ws is None:
-        ws = _zeroed_workspace(int(load().kvc_block_prompt_select_workspace_bytes(
-            pt.batch, seq_len, pool.block_size, budget_blocks)), s.device)
+        with _on(stream):
+            ws = _zeroed_workspace(int(load().kvc_block_prompt_select_workspace_bytes(
+                pt.batch, seq_len, pool.block_size, budget_blocks)), s.device)
     wp, wb = _ws_ptr(ws)
     _check(load().kvc_block_prompt_select(
         _ptr(s), s.stride(-2), ctypes.byref(c), int(seq_len), ctypes.byref(pool),
@@ -519,12 +539,13 @@ def kvc_decode_attn_duo(q: torch.Tensor, full: kvc_cache, ring: kvc_cache, duo: 
                         stream=None) -> torch.Tensor:
     """q [B, Hq, D] (model head order) -> out [B, Hq, D] fp32."""
     B, Hq, D = q.shape
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = _zeroed_workspace(kvc_decode_attn_duo_workspace_bytes(
-            B, Hq, full.n_heads_kv + ring.n_heads_kv, D, full.cap, duo.desc.n_retrieval),
-            q.device)
+    with _on(stream, out, ws):
+        if out is None:
+            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = _zeroed_workspace(kvc_decode_attn_duo_workspace_bytes(
+                B, Hq, full.n_heads_kv + ring.n_heads_kv, D, full.cap, duo.desc.n_retrieval),
+                q.device)
     wp, wb = _ws_ptr(ws)
     lstride = logits.stride(-2) if logits is not None else 0
     _check(load().kvc_decode_attn_duo(
@@ -544,7 +565,8 @@ def kvc_decode_attn_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     c = cache_view(k_cache, v_cache)
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        with _on(stream):
+            out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
     lstride = logits.stride(-2) if logits is not None else 0
     _check(load().kvc_decode_attn_noalloc(
         _ptr(q), Hq, ctypes.byref(c), _ptr(len), -1 if n_valid is None else int(n_valid),
@@ -596,11 +618,12 @@ def kvc_snapkv_select(q_obs: torch.Tensor, k_prompt: torch.Tensor, *, seq_len: i
     c = cache_view(k_prompt)
     B, Hq = q_obs.shape[0], q_obs.shape[1]
     n_keep = min(budget, seq_len)
-    if idx_out is None:
-        idx_out = torch.empty((B, c.n_heads_kv, n_keep), dtype=torch.int32, device=q_obs.device)
-    if ws is None:
-        ws = _zeroed_workspace(kvc_snapkv_select_workspace_bytes(
-            B, Hq, c.n_heads_kv, c.d_head, seq_len, L_obs), q_obs.device)
+    with _on(stream, idx_out, ws):
+        if idx_out is None:
+            idx_out = torch.empty((B, c.n_heads_kv, n_keep), dtype=torch.int32, device=q_obs.device)
+        if ws is None:
+            ws = _zeroed_workspace(kvc_snapkv_select_workspace_bytes(
+                B, Hq, c.n_heads_kv, c.d_head, seq_len, L_obs), q_obs.device)
     wp, wb = _ws_ptr(ws)
     _check(load().kvc_snapkv_select(
         _ptr(q_obs), ctypes.byref(c), Hq, seq_len, L_obs, pool_k, budget, float(scale),
@@ -650,12 +673,13 @@ def kvc_h2o_prefill_select(q: torch.Tensor, k_prompt: torch.Tensor, *, seq_len: 
     c = cache_view(k_prompt)
     B, H = q.shape[0], q.shape[1]
     n_keep = min(seq_len, K_hh + L_local)
-    if idx_out is None:
-        idx_out = torch.empty((B, H, n_keep), dtype=torch.int32, device=q.device)
-    if score_out is None:
-        score_out = torch.empty((B, H, n_keep), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = _zeroed_workspace(kvc_h2o_prefill_workspace_bytes(B, H, c.d_head, seq_len), q.device)
+    with _on(stream, idx_out, score_out, ws):
+        if idx_out is None:
+            idx_out = torch.empty((B, H, n_keep), dtype=torch.int32, device=q.device)
+        if score_out is None:
+            score_out = torch.empty((B, H, n_keep), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = _zeroed_workspace(kvc_h2o_prefill_workspace_bytes(B, H, c.d_head, seq_len), q.device)
     wp, wb = _ws_ptr(ws)
     _check(load().kvc_h2o_prefill_select(
         _ptr(q), ctypes.byref(c), seq_len, L_local, K_hh, float(scale), _ptr(idx_out),
@@ -689,13 +713,14 @@ def kvc_h2o_prefill_select_gqa(q: torch.Tensor, k_prompt: torch.Tensor, *, seq_l
         raise ValueError(f"s_full must be a contiguous float32 tensor "
                          f"[{c.batch}, {c.n_heads_kv}, {seq_len}]")
     n_keep = min(seq_len, K_hh + L_local)
-    if idx_out is None:
-        idx_out = torch.empty((B, c.n_heads_kv, n_keep), dtype=torch.int32, device=q.device)
-    if score_out is None:
-        score_out = torch.empty((B, c.n_heads_kv, n_keep), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = _zeroed_workspace(kvc_h2o_prefill_gqa_workspace_bytes(
-            B, c.n_heads_kv, c.d_head, seq_len, c.dtype), q.device)
+    with _on(stream, idx_out, score_out, ws):
+        if idx_out is None:
+            idx_out = torch.empty((B, c.n_heads_kv, n_keep), dtype=torch.int32, device=q.device)
+        if score_out is None:
+            score_out = torch.empty((B, c.n_heads_kv, n_keep), dtype=torch.float32, device=q.device)
+        if ws is None:
+            ws = _zeroed_workspace(kvc_h2o_prefill_gqa_workspace_bytes(
+                B, c.n_heads_kv, c.d_head, seq_len, c.dtype), q.device)
     wp, wb = _ws_ptr(ws)
     _check(load().kvc_h2o_prefill_select_gqa(
         _ptr(q), Hq, ctypes.byref(c), seq_len, L_local, K_hh, float(scale), _ptr(idx_out),
@@ -833,7 +858,7 @@ def latent_workspace(batch, n_heads_q, d_latent, d_rope, n_draft, dtype: torch.d
     return torch.empty(n + 256, dtype=torch.uint8, device=device)
 
 
-def _attn_args(q, view, width, out_width, code, batch, draft, rows_shape, out, lse):
+def _attn_args(q, view, width, out_width, code, batch, draft, rows_shape, out, lse, stream):
     """Checks shared by the draft-tree and latent attention; returns out and the device's index."""
     dt = _DTYPES.get(code)
     shape = q.shape
@@ -852,9 +877,10 @@ def _attn_args(q, view, width, out_width, code, batch, draft, rows_shape, out, l
     if lse is not None:
         _need(lse, "lse", torch.float32, shape[:3], index)
     if out is None:
-        if out_width == width:
-            return torch.empty_like(q), index
-        return torch.empty((batch, shape[1], shape[2], out_width), dtype=dt, device=q.device), index
+        with _on(stream):
+            if out_width == width:
+                return torch.empty_like(q), index
+            return torch.empty((batch, shape[1], shape[2], out_width), dtype=dt, device=q.device), index
     _need(out, "out", dt, shape[:3] + (out_width,), index)
     return out, index
 
@@ -867,11 +893,13 @@ def kvc_decode_attn_tree(q: torch.Tensor, cache: kvc_cache, draft: kvc_draft, *,
     slots and the drafted tokens it sees.  len int32 [B, Hkv] (or [B * Hkv])."""
     c = cache
     B, Hkv, D = c.batch, c.n_heads_kv, c.d_head
-    out, index = _attn_args(q, c, D, D, c.dtype, B, draft, (B, draft.n_draft, Hkv, D), out, lse)
+    out, index = _attn_args(q, c, D, D, c.dtype, B, draft, (B, draft.n_draft, Hkv, D), out, lse,
+                            stream)
     if len is not None:
         _need(len, "len", torch.int32, (B, Hkv) if len.dim() == 2 else (B * Hkv,), index)
     if ws is None:
-        ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
+        with _on(stream):
+            ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
     wp, wb = _space(ws)
     status = (_lib or load()).kvc_decode_attn_tree(
         q.data_ptr(), q.shape[2], c, None if len is None else len.data_ptr(),
@@ -889,10 +917,12 @@ def kvc_decode_attn_tree_paged(q: torch.Tensor, pool: kvc_block_pool, pt: kvc_pa
                                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """q [B, T, Hq, D] -> out [B, T, Hq, D] over each sequence's page table and its drafts."""
     B, Hkv, D = pt.batch, pool.n_heads_kv, pool.d_head
-    out, index = _attn_args(q, pool, D, D, pool.dtype, B, draft, (B, draft.n_draft, Hkv, D), out, lse)
+    out, index = _attn_args(q, pool, D, D, pool.dtype, B, draft, (B, draft.n_draft, Hkv, D), out, lse,
+                            stream)
     _beside(index, pt, "q")
     if ws is None:
-        ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
+        with _on(stream):
+            ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
     wp, wb = _space(ws)
     status = (_lib or load()).kvc_decode_attn_tree_paged(
         q.data_ptr(), q.shape[2], pool, pt, draft, scale, out.data_ptr(),
@@ -912,10 +942,12 @@ def kvc_decode_attn_latent(q: torch.Tensor, cache: kvc_latent_cache, draft: kvc_
     c = cache
     B, R = c.batch, c.d_latent
     width = R + c.d_rope
-    out, index = _attn_args(q, c, width, R, c.dtype, B, draft, (B, draft.n_draft, width), out, lse)
+    out, index = _attn_args(q, c, width, R, c.dtype, B, draft, (B, draft.n_draft, width), out, lse,
+                            stream)
     _need(len, "len", torch.int32, (B,), index)
     if ws is None:
-        ws = latent_workspace(B, q.shape[2], R, width - R, draft.n_draft, q.dtype, q.device)
+        with _on(stream):
+            ws = latent_workspace(B, q.shape[2], R, width - R, draft.n_draft, q.dtype, q.device)
     wp, wb = _space(ws)
     status = (_lib or load()).kvc_decode_attn_latent(
         q.data_ptr(), q.shape[2], c, None if len is None else len.data_ptr(),
@@ -973,7 +1005,8 @@ def kvc_tree_accept_paged(pool: kvc_block_pool, pt: kvc_page_table, free_pool: k
     _beside(index, pt, "the draft")
     _beside(index, free_pool, "the draft")
     if accepted is None:
-        accepted = torch.empty(pt.batch, dtype=torch.int32, device=path.device)
+        with _on(stream):
+            accepted = torch.empty(pt.batch, dtype=torch.int32, device=path.device)
     else:
         _need(accepted, "accepted", torch.int32, (pt.batch,), index)
     _check((_lib or load()).kvc_tree_accept_paged(pool, pt, free_pool, draft, path.data_ptr(),
