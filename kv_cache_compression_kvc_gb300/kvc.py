@@ -771,8 +771,12 @@ def _raw_stream(index: int, stream) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _space(ws: torch.Tensor):
-    """256-byte aligned address inside a workspace tensor and the bytes available after it."""
+def _space(ws: torch.Tensor, index: int):
+    """256-byte aligned address inside a workspace tensor and the bytes available after it.  The
+    kernels write there: it lies on their device, and what its shape counts is all its own."""
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on cuda:{index}, got {list(ws.shape)} "
+                         f"on {ws.device}")
     base = ws.data_ptr()
     aligned = (base + 255) & ~255
     return aligned, ws.numel() * ws.element_size() - (aligned - base)
@@ -900,7 +904,7 @@ def kvc_decode_attn_tree(q: torch.Tensor, cache: kvc_cache, draft: kvc_draft, *,
     if ws is None:
         with _on(stream):
             ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
-    wp, wb = _space(ws)
+    wp, wb = _space(ws, index)
     status = (_lib or load()).kvc_decode_attn_tree(
         q.data_ptr(), q.shape[2], c, None if len is None else len.data_ptr(),
         -1 if n_valid is None else n_valid, draft, scale, out.data_ptr(),
@@ -923,7 +927,7 @@ def kvc_decode_attn_tree_paged(q: torch.Tensor, pool: kvc_block_pool, pt: kvc_pa
     if ws is None:
         with _on(stream):
             ws = tree_workspace(B, q.shape[2], Hkv, D, draft.n_draft, q.dtype, q.device)
-    wp, wb = _space(ws)
+    wp, wb = _space(ws, index)
     status = (_lib or load()).kvc_decode_attn_tree_paged(
         q.data_ptr(), q.shape[2], pool, pt, draft, scale, out.data_ptr(),
         None if lse is None else lse.data_ptr(), wp, wb, _raw_stream(index, stream))
@@ -948,7 +952,7 @@ def kvc_decode_attn_latent(q: torch.Tensor, cache: kvc_latent_cache, draft: kvc_
     if ws is None:
         with _on(stream):
             ws = latent_workspace(B, q.shape[2], R, width - R, draft.n_draft, q.dtype, q.device)
-    wp, wb = _space(ws)
+    wp, wb = _space(ws, index)
     status = (_lib or load()).kvc_decode_attn_latent(
         q.data_ptr(), q.shape[2], c, None if len is None else len.data_ptr(),
         -1 if n_valid is None else n_valid, draft, scale, out.data_ptr(),
