@@ -577,7 +577,7 @@ typedef struct {
     const uint64_t *mask;
     const int32_t *count;
     int32_t n_draft;        /* query tokens per sequence, 1..64                              */
-    int32_t reserved;
+    int32_t reserved;       /* 0, or KVC_TEST_STARVE for the attention (see below)           */
 } kvc_draft;
 
 /* Attention of a tree of drafted tokens over a cache: for every sequence b, drafted token i <
@@ -642,7 +642,7 @@ kvc_status kvc_tree_accept_paged(const kvc_block_pool *pool, const kvc_page_tabl
 /* KVC_TEST_STARVE in a descriptor's `reserved`: a test hook with no counterpart on the pages, for
  * exercising the bounded waits of the tensor-core kernels without a GPU fault, as
  * KVC_DECODE_TEST_STARVE does for the decode kernels.  The kernel loads nothing, so its first waits
- * run out after a short bounded spin; every block still finishes and kvc_device_status() reports
+ * give up after a short bounded spin; every block still finishes and kvc_device_status() reports
  * KVC_DEV_TIMEOUT.  The outputs of such a call are undefined, the next call without it is unaffected.
  * A wait that gives up for a real reason (a lost arrival) ends the same way.  Calls that run on the
  * CUDA cores have no such waits and ignore it. */

@@ -1258,6 +1258,7 @@ static kvc_status tree_run(kvc::TreeParams &p, int dtype, bool tc_ok, const kvc_
     p.T = d->n_draft;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.inv_G = 1.f / (float)p.G;
+    p.starve = (uint32_t)d->reserved == KVC_TEST_STARVE;
     p.dev_code = code;
     const size_t need = tree_ws_bytes(p.G, p.DK, p.DV, p.T, dtype, p.latent != 0, n_sm);
     if (ws == nullptr || ws_bytes < need)

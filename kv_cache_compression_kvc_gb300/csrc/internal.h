@@ -309,6 +309,7 @@ struct TreeParams {
     float *ws_o;                 // [groups*RT*2][RN][DV]
     float *ws_ml;                // [groups*RT*2][RN][2] (max in log2 units, sum)
     int4 *ws_info;               // [groups]
+    int32_t starve;              // test hook: load nothing, so the first waits give up
     int32_t *dev_code;
 };
 struct TreePlan {

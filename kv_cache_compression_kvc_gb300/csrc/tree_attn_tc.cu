@@ -30,9 +30,11 @@
 // slots); warp 1 issues S = Q K^T, two S buffers ahead of the softmax, and owns tensor memory; warp 2
 // issues the values' products; the others (sets of four, one warp per 32 lanes and 32 of a tile's
 // slots each, or one tile in two with PT) run the softmax, rescale and write the outputs.  Hand-over
-// by mbarriers; every wait is bounded (see common.cuh): when one gives up the block records
-// KVC_DEV_TIMEOUT, stops issuing and walks to its end, waits for its loads and products in flight
-// and frees its tensor memory.
+// by mbarriers; every wait is bounded (see common.cuh).  When one gives up the block records
+// KVC_DEV_TIMEOUT and loads no further tile.  No wait holds a warp any more then: all of them walk to
+// their ends on whatever memory holds (the products go on; the softmax warps' named barriers do not
+// depend on data, so each passes them as often as the others), and the block waits for its loads
+// and products in flight and frees its tensor memory.
 //
 // Measured, device time: 32 pairs of 5243 slots, 64 rows, 128 dims 28.6 us (HBM alone 13; a block has
 // nine tiles, so the start, 5 us until its first keys, and the merge, 5 us, count as much as the
@@ -219,7 +221,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             mbar_init(b_pv + 8 * i, 1);
         }
         mbar_init(b_done, 2);
-        *s_abort = 0;
+        *s_abort = p.starve;                     // (test hook: as if a wait had given up already)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tc::alloc(tmem_slot, PL::COLS);

@@ -23,7 +23,7 @@ KVC_APPEND_TAIL, KVC_APPEND_RING, KVC_APPEND_FREE_SLOT = 0, 1, 2
 KVC_DECODE_KV_SETTLED = 1
 KVC_DECODE_BALANCE = 2
 KVC_DECODE_TEST_STARVE = 0x80000000
-KVC_TEST_STARVE = 0x53545256        # in the `reserved` field of a kvc_latent_cache (see kvc.h)
+KVC_TEST_STARVE = 0x53545256        # in `reserved` of a kvc_draft or kvc_latent_cache (see kvc.h)
 STATUS_NAMES = {0: "KVC_OK", 1: "KVC_ERR_INVALID_ARG", 2: "KVC_ERR_SHAPE", 3: "KVC_ERR_ALIGN",
                 4: "KVC_ERR_CAPACITY", 5: "KVC_ERR_CUDA", 6: "KVC_ERR_WORKSPACE",
                 7: "KVC_ERR_DEVICE"}
