@@ -26,9 +26,10 @@
  *     multiple of 16 bytes.  Query head h reads KV head h / (n_heads_q / n_heads_kv)
  *     (grouped-query attention, [KVCL] "01 · Conceito"; [KVC] "O gargalo de memória...").
  *   - Element types: KVC_F32 (fp32 storage and arithmetic) or KVC_BF16 (bf16 storage, fp32
- *     arithmetic).  Queries and new keys/values use the cache's type; outputs are fp32, except
- *     where an entry point says that they have the cache's type (the draft-tree and latent
- *     attention, whose outputs feed the next projection directly).
+ *     arithmetic).  Queries and new keys/values use the cache's type; outputs are fp32.  The
+ *     draft-tree and latent attention and the latent expansion differ where their entry points
+ *     say so: their outputs have the cache's type, and that attention rounds the probabilities
+ *     to bf16 for one product.
  */
 #ifndef KVC_H_
 #define KVC_H_
@@ -559,8 +560,10 @@ kvc_status kvc_h2o_prefill_select_gqa(const void *q, int32_t n_heads_q, const kv
 /* Trees of drafted tokens.  A drafting model proposes n_draft tokens per sequence at once; token
  * i sees the whole cache and, of the drafted tokens, those whose bit is set in its mask word
  * (itself and its ancestors).  The drafted keys and values stay OUT of the cache until they
- * are accepted: a ring, an evicted slot or a page never loses a token to a draft that is then
- * rejected.  No counterpart on the pages (they decode one token at a time); the attention is
+ * are accepted: no slot and no page is taken by a draft that is then rejected.  Served are
+ * caches filled from slot 0 (KVC_APPEND_TAIL, compacted or selected prompts), paged caches and latent
+ * caches; not the sink + ring layouts with positions inside the cache, nor DuoAttention's two
+ * caches, and acceptance fills neither ring nor freed slots.  No counterpart on the pages (they decode one token at a time); the attention is
  * that of kvc_decode_attn for every drafted token.
  * k, v: device [batch][n_draft][n_heads_kv][d_head], cache dtype, contiguous, 16-byte aligned
  * (for a latent cache k is [batch][n_draft][d_latent + d_rope] and v is not read).  k == NULL:
@@ -568,7 +571,7 @@ kvc_status kvc_h2o_prefill_select_gqa(const void *q, int32_t n_heads_q, const kv
  * mask: device uint64[batch][n_draft]; bit j of word i set: token i sees token j.  Bits at or
  * above the sequence's token count are ignored.  NULL: a chain, token i sees tokens 0..i.
  * count (nullable): device int32[batch], drafted tokens of each sequence, 0..n_draft (a value
- * outside records KVC_DEV_BAD_LENGTH and is clamped).  Outputs of tokens at or beyond it are
+ * outside records KVC_DEV_BAD_LENGTH and is clamped, by the accept calls too).  Outputs of tokens at or beyond it are
  * left as they were, and their keys and values are not used (nor need they be finite).  NULL:
  * n_draft each. */
 typedef struct {
@@ -591,7 +594,8 @@ typedef struct {
  * q: [batch][n_draft][n_heads_q][d_head] cache dtype, contiguous; out: the same shape and type;
  * lse (nullable): fp32 [batch][n_draft][n_heads_q].  Any group size up to 64.
  * bf16 caches run on the tensor cores (fp32 accumulation and softmax statistics; the
- * probabilities are rounded to bf16 for the product with the values), fp32 caches in fp32.
+ * probabilities are rounded to bf16 for the product with the values, at most 2^-8 of each, where
+ * kvc_decode_attn carries them to 2^-18 and writes fp32), fp32 caches in fp32.
  * One launch or two (the second joins the partial results of rows whose slots were split over
  * thread blocks; short rows are not split).  Results do not depend on timing.  Workspace:
  * kvc_decode_attn_tree_workspace_bytes(), 256-byte aligned; it need not be cleared, and calls
@@ -692,8 +696,9 @@ kvc_status kvc_latent_accept(const kvc_latent_cache *cache, int32_t *len, const 
  * n_valid) for every head, into an ordinary cache that every selection and decode of this
  * library reads.  w_k: [n_heads][dst->d_head - d_rope][d_latent], w_v:
  * [n_heads][dst->d_head][d_latent], cache dtype, contiguous, n_heads = dst->n_heads_kv;
- * d_rope < dst->d_head.  dst slots at or beyond the length are left as they were.  fp32
- * accumulation, rounded once to the cache's type; the d_rope part is copied. */
+ * d_rope < dst->d_head.  A length outside [0, cap] of either cache records KVC_DEV_BAD_LENGTH and is
+ * clamped.  dst slots at or beyond the length are left as they were.  fp32 accumulation, rounded
+ * once to the cache's type; the d_rope part is copied. */
 kvc_status kvc_latent_expand(const kvc_latent_cache *cache, const int32_t *len, int32_t n_valid,
                              const void *w_k, const void *w_v, const kvc_cache *dst,
                              void *stream);

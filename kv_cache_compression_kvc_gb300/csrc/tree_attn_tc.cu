@@ -14,13 +14,17 @@
 //   value of 64 rows takes 256 columns of tensor memory (rows x dims would take all 512 and leave
 //   none for S), and the value rows are used as they lie in memory (V^T is the MN-major A
 //   operand).  P goes through shared memory as the K-major B operand, rounded to bf16: the weights
-//   are off by at most 2^-8 each, as is the bf16 output.
+//   are off by at most 2^-8 each, as is the bf16 output, and errors against 64 bits are 0.0018 to
+//   0.0023 of the outputs' norm where rounding the output alone makes 0.0017.  Carrying the rest of a
+//   weight as a second bf16 term, as the single-token decode does, would double the values' products
+//   and P's room: with 128 rows tensor memory is full as it is, and latent rows are bound by what
+//   shared memory delivers.  The sum l is taken of the unrounded weights, so lse has no part in it.
 //   With 128 rows of an ordinary cache of up to 128 dims (PT below) O is kept by row instead and P
 //   goes through tensor memory as the A operand (O += P V): that leaves shared memory for a third
 //   tile in flight, a row's O is in its own thread's lane, and two P buffers let the softmax of two
-//   tiles run side by side.  16 pairs of 131072 slots, 256 rows each, 128 dims: 282 us, without
-//   it 300.
-//   With 256 dims (64-slot tiles, short budgets) it was the slower one, 36 us for 31.
+//   tiles run side by side.  16 pairs of 131072 slots, 256 rows each, 128 dims: 258 us, without
+//   it 264.  With 256 dims (64-slot tiles, short budgets) it was the slower one, 36 us for 31 when it
+//   was tried.
 //   A latent cache's tile is loaded once and serves as K (all of it) and V (its first d_latent
 //   columns).
 //   The running maximum is lazy: a tile whose logits stay below max + 8 (log2 units) keeps the old
@@ -32,13 +36,13 @@
 // slots each, or one tile in two with PT) run the softmax, rescale and write the outputs.  Hand-over
 // by mbarriers; every wait is bounded (see common.cuh).  When one gives up the block records
 // KVC_DEV_TIMEOUT and loads no further tile.  No wait holds a warp any more then: all of them walk to
-// their ends on whatever memory holds (the products go on; the softmax warps' named barriers do not
-// depend on data, so each passes them as often as the others), and the block waits for its loads
-// and products in flight and frees its tensor memory.
+// their ends on whatever memory holds (the products go on; what the softmax warps do between their
+// named barriers is decided by all of them together, so they stay in step), and the block waits for
+// its loads and products in flight and frees its tensor memory.
 //
 // Measured, device time: 32 pairs of 5243 slots, 64 rows, 128 dims 28.6 us (HBM alone 13; a block has
 // nine tiles, so the start, 5 us until its first keys, and the merge, 5 us, count as much as the
-// stream); 512 paged pairs of 817 slots, 8 rows 56 us (33); 16 pairs of 131072 slots, 256 rows 259 us
+// stream); 512 paged pairs of 817 slots, 8 rows 56 us (33); 16 pairs of 131072 slots, 256 rows 258 us
 // (161; 8.5 TB/s from L2 to the SMs); 32 latent sequences of 4608 slots, 32 rows 45 us (26); 8 of
 // 6144 slots, 512 rows in eight row tiles 80 us (28 by the products' operations; shared memory moves
 // 320 KB for a tile of 64 slots by 64 rows, which at 128 B a clock is 56 us alone).
