@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_kernel(const TreeParams p)
                     make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
         }
         if (tid < kRows) {
-            sM[tid] = kNegBig;
+            sM[tid] = kNoMax;
             sL[tid] = 0.f;
         }
         if (tid == 0) s_nf = 0ull;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
     auto slot_of = [&](int i) -> size_t {
         return ((size_t)((g + i) * p.RT + rt) * 2 + (i == 0 ? note.w & 1 : 0)) * p.RN + r;
     };
-    float M = kNegBig;
+    float M = kNoMax;
     for (int i = lane; i < nseg; i += 32) M = fmaxf(M, __ldcg(p.ws_ml + slot_of(i) * 2));
     M = warp_max(M);
     float o[CPL], L = 0.f;
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Tree
 #pragma unroll
         for (int u = 0; u < UNR; ++u) {
             const int i = i0 + u * WPR;
-            ml[u][0] = kNegBig;
+            ml[u][0] = kNoMax;
             ml[u][1] = 0.f;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) x[u][c] = 0.f;

@@ -547,7 +547,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const int token = kBar + 1 + q4;                     // + 4 * set
         volatile float *v_max = s_fac + RN;
-        if (set == 0) v_max[row] = kNegBig;
+        if (set == 0) v_max[row] = kNoMax;
         tc::bar_sync(kBar, kSoftmax);
         TreeWalk walk(p, range);
         TreeSeg s, nx;
@@ -566,7 +566,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             more = next_seg();
             const bool mine = row < s.rows;
             const bool any = q4 * 32 < s.rows;               // warp-uniform
-            float l = 0.f, l_ref = kNegBig;                  // sum over this set's tiles, its reference
+            float l = 0.f, l_ref = kNoMax;                   // sum over this set's tiles, its reference
             const uint64_t word = mine && s.hi == s.nt ? tree_mask_word(p, s.b, tok, s.cnt) : 0ull;
             unsigned long long *s_nf = s_nf2 + (seg_no++ & 1);
             for (int tile = s.lo; tile < s.hi; ++tile, ++n, v_unit += PER) {
@@ -574,7 +574,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 const bool draft = s.is_draft(p, tile);
                 const int valid = s.valid(p, tile, TS);
                 const bool masked = draft || valid < TS;
-                float mx = -INFINITY, m = kNegBig, z = 0.f;
+                float mx = -INFINITY, m = kNoMax, z = 0.f;
                 uint32_t w[TS / 2];                          // the row's weights, bf16 pairs
                 // 64 logits of the row, masked ones -inf (and then scaled: returns the scale to use)
                 auto logits = [&](int half, float *x) -> float {
@@ -613,7 +613,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     m = v_max[row];
                     if (mx > m + kSlack) m = mx;
                 }
-                float m_cur = kNegBig, m_fin = kNegBig;
+                float m_cur = kNoMax, m_fin = kNoMax;
                 bool rise = false;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
@@ -709,7 +709,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             tc::bar_sync(kBar, kSoftmax);
             if (set == 0) {
                 l += s_fac[row];
-                v_max[row] = kNegBig;                        // for the next pair
+                v_max[row] = kNoMax;                         // for the next pair
                 s_fac[row] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
                 if (mine) {
                     if (!whole) {
@@ -788,7 +788,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             if (s.rows <= 0) continue;
             const bool mine = row < s.rows;
             const bool any = row_lo < s.rows;                // warp-uniform
-            float m = kNegBig, l = 0.f;
+            float m = kNoMax, l = 0.f;
             bool drafts = false;
             const uint64_t word = mine && s.hi == s.nt ? tree_mask_word(p, s.b, tok, s.cnt) : 0ull;
             // drafted tokens with non-finite values: alternate words, since a thread may set up
