@@ -81,6 +81,12 @@ namespace {
 
 constexpr int kBar = 1;                      // their named barrier
 constexpr float kSlack = 8.f;                // lazy maximum, log2 units
+// Weights are exp2(fma(s, scale, -m)).  m is a rounded product and s * scale in the fma is not, so they
+// differ by up to half of m's last place even at the maximum: with m = 2^32 a weight could be 2^128.
+// From here on (half a unit) the products are rounded first, which leaves 0 at the maximum.  That takes
+// the way of the masked tiles, so that other tiles have no further branch (one: 260 -> 272 us for 16
+// pairs of 131072 slots, 256 rows).
+constexpr float kBigMax = 16777216.f;
 constexpr int kSmemMax = 227 * 1024;
 
 // DKP: key width padded to 64; DV: value width; RN: rows of a row tile.
@@ -573,7 +579,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 if ((int)(n & 1) != set) continue;
                 const bool draft = s.is_draft(p, tile);
                 const int valid = s.valid(p, tile, TS);
-                const bool masked = draft || valid < TS;
+                bool scaled = draft || valid < TS;           // logits are masked and scaled as they are read
                 float mx = -INFINITY, m = kNoMax, z = 0.f;
                 uint32_t w[TS / 2];                          // the row's weights, bf16 pairs
                 // 64 logits of the row, masked ones -inf (and then scaled: returns the scale to use)
@@ -581,7 +587,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     tc::ld32(tS + set * TS + lanes + 64 * half, x);
                     tc::ld32(tS + set * TS + lanes + 64 * half + 32, x + 32);
                     tc::wait_ld();
-                    if (!masked) return p.scale_log2;
+                    if (!scaled) return p.scale_log2;
                     const int v = valid - 64 * half;
                     const uint64_t see = draft ? (half == 0 ? word : 0ull)
                                                : v >= 64 ? ~0ull : v <= 0 ? 0ull : (1ull << v) - 1ull;
@@ -617,6 +623,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                 bool rise = false;
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
+                    scaled |= mine && fabsf(m) >= kBigMax;
                     if (any) {
                         z = 0.f;
 #pragma unroll
@@ -789,6 +796,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
             const bool mine = row < s.rows;
             const bool any = row_lo < s.rows;                // warp-uniform
             float m = kNoMax, l = 0.f;
+            bool big = false;                                // some row of the warp has kBigMax
             bool drafts = false;
             const uint64_t word = mine && s.hi == s.nt ? tree_mask_word(p, s.b, tok, s.cnt) : 0ull;
             // drafted tokens with non-finite values: alternate words, since a thread may set up
@@ -808,7 +816,7 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     tc::wait_ld();
                 }
                 if (any) {
-                    if (draft || valid < TS) {               // masked: scaled here, once
+                    if (draft || valid < TS || big) {        // masked: scaled here, once
                         uint32_t see;                        // slots c0 .. c0 + 31
                         if (draft) see = set == 0 ? (uint32_t)word : set == 1 ? (uint32_t)(word >> 32) : 0u;
                         else see = valid - c0 >= 32 ? ~0u : valid > c0 ? (1u << (valid - c0)) - 1u : 0u;
@@ -841,6 +849,12 @@ tree_tc_kernel(const __grid_constant__ Maps maps, const TreeParams p)
                     }
                     const float f = ex2(m - m_new);
                     m = m_new;
+                    big = __any_sync(0xffffffffu, mine && fabsf(m) >= kBigMax);
+                    if (big) {
+#pragma unroll
+                        for (int c = 0; c < HC; ++c) x[c] *= scale;
+                        scale = 1.f;
+                    }
                     l *= f;
                     if (tile > s.lo) {
                         if (set == 0 && row < RN) s_fac[row] = f;

@@ -1,4 +1,5 @@
-"""GPU: logits of any finite size.  Keys of equal components, powers of two, make the logits exact, the largest one shared by every third slot or so and the others far below it: the output is the mean of the
+"""GPU: logits of any finite size.  Keys of equal components, powers of two and 1.375 times those, make the
+logits exact (the second kind not their products with the scale in base-2 units), the largest one shared by every third slot or so and the others far below it: the output is the mean of the
 values there, however large or how far below zero the logits lie."""
 import pytest
 import torch
@@ -45,7 +46,7 @@ LEVELS = [(1, 10), (-1, 10), (1, 26), (-1, 33), (1, 34), (1, 60), (-1, 60), (1, 
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("base", [1.0])
+@pytest.mark.parametrize("base", [1.0, 1.375])
 @pytest.mark.parametrize("sign,level", LEVELS)
 @pytest.mark.parametrize("H,G,D,T,n", [(2, 2, 64, 4, 300), (1, 4, 128, 64, 700), (2, 6, 256, 11, 200),
                                        (1, 1, 128, 1, 20000), (1, 4, 128, 40, 9000)])
@@ -73,7 +74,7 @@ def test_tree(dtype, base, sign, level, H, G, D, T, n):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("base", [1.0])
+@pytest.mark.parametrize("base", [1.0, 1.375])
 @pytest.mark.parametrize("sign,level", LEVELS)
 @pytest.mark.parametrize("Hq,R,E,T,n", [(16, 512, 64, 1, 3000), (32, 256, 64, 4, 400)])
 def test_latent(dtype, base, sign, level, Hq, R, E, T, n):
