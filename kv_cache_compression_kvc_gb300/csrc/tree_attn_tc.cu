@@ -23,7 +23,7 @@
 //   goes through tensor memory as the A operand (O += P V): that leaves shared memory for a third
 //   tile in flight, a row's O is in its own thread's lane, and two P buffers let the softmax of two
 //   tiles run side by side.  16 pairs of 131072 slots, 256 rows each, 128 dims: 258 us, without
-//   it 264.  With 256 dims (64-slot tiles, short budgets) it was the slower one, 36 us for 31 when it
+//   it 265.  With 256 dims (64-slot tiles, short budgets) it was the slower one, 36 us for 31 when it
 //   was tried.
 //   A latent cache's tile is loaded once and serves as K (all of it) and V (its first d_latent
 //   columns).
@@ -40,9 +40,9 @@
 // named barriers is decided by all of them together, so they stay in step), and the block waits for
 // its loads and products in flight and frees its tensor memory.
 //
-// Measured, device time: 32 pairs of 5243 slots, 64 rows, 128 dims 28.6 us (HBM alone 13; a block has
+// Measured, device time: 32 pairs of 5243 slots, 64 rows, 128 dims 29 us (HBM alone 13; a block has
 // nine tiles, so the start, 5 us until its first keys, and the merge, 5 us, count as much as the
-// stream); 512 paged pairs of 817 slots, 8 rows 56 us (33); 16 pairs of 131072 slots, 256 rows 258 us
+// stream); 512 paged pairs of 817 slots, 8 rows 57 us (33); 16 pairs of 131072 slots, 256 rows 258 us
 // (161; 8.5 TB/s from L2 to the SMs); 32 latent sequences of 4608 slots, 32 rows 45 us (26); 8 of
 // 6144 slots, 512 rows in eight row tiles 80 us (28 by the products' operations; shared memory moves
 // 320 KB for a tile of 64 slots by 64 rows, which at 128 B a clock is 56 us alone).
