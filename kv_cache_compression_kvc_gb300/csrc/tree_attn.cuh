@@ -33,9 +33,9 @@ namespace kvc {
 
 constexpr int kWholeTiles = 12, kWholeWait = 4, kWholeWaitLatent = 3;
 constexpr int kPairEnd = 2;
-// A running maximum that has seen nothing: below every finite logit (in log2 units), and finite, so that
-// differences with it are no NaN.
-constexpr float kNoMax = -3.0e38f;
+// A running maximum that has seen nothing: no finite logit (in log2 units) lies below it, and it is
+// finite, so that differences with it are no NaN.
+constexpr float kNoMax = -3.402823466e38f;
 constexpr int kDevBadLengthCode = 5;         // KVC_DEV_BAD_LENGTH
 constexpr int kDevBadBlockCode = 9;          // KVC_DEV_BAD_BLOCK
 

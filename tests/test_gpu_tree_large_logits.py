@@ -1,6 +1,7 @@
 """GPU: logits of any finite size.  Keys of equal components, powers of two and 1.375 times those, make the
-logits exact (the second kind not their products with the scale in base-2 units), the largest one shared by every third slot or so and the others far below it: the output is the mean of the
-values there, however large or how far below zero the logits lie."""
+logits exact (the second kind not their products with the scale in base-2 units), the largest one
+shared by every third slot or so and the others far below it: the output is the mean of the values
+there, however large or how far below zero the logits lie."""
 import pytest
 import torch
 
@@ -71,6 +72,13 @@ def test_tree(dtype, base, sign, level, H, G, D, T, n):
     values = torch.cat([v, vd[:, :1].transpose(1, 2)], 2)
     best = torch.cat([best, torch.ones_like(best[..., :1])], 2)
     check(out.view(B, T, H, G, D), lse.view(B, T, H, G), values, best, sign * base * 2.0 ** level * D, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,G,T,n", [(2, 2, 4, 300), (1, 4, 40, 9000)])
+def test_tree_at_the_lowest(dtype, H, G, T, n):
+    """Logits that are among the lowest finite numbers in base-2 units; the others are -inf."""
+    test_tree(dtype, 1.25, -1, 121, H, G, 64, T, n)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
