@@ -52,7 +52,11 @@ typedef enum {
     KVC_ERR_DEVICE = 7         /* a kernel's own range check fired (see kvc_device_status)   */
 } kvc_status;
 
-typedef enum { KVC_F32 = 0, KVC_BF16 = 1 } kvc_dtype;
+typedef enum {
+    KVC_F32 = 0,
+    KVC_BF16 = 1,
+    KVC_E4M3 = 2                /* pages of kvc_block_pool_q8 only                          */
+} kvc_dtype;
 
 /* Device-side range-check codes recorded by kernels (first one wins until read). */
 enum {
@@ -67,7 +71,8 @@ enum {
     KVC_DEV_SCHEDULE = 8,       /* internal schedule bound violated (results invalid)         */
     KVC_DEV_BAD_BLOCK = 9,      /* page-table or free-stack entry outside the block pool      */
     KVC_DEV_POOL_EMPTY = 10,    /* a sequence needed a new block and the free stack was empty */
-    KVC_DEV_POOL_OVERFLOW = 11  /* a released block did not fit on the free stack             */
+    KVC_DEV_POOL_OVERFLOW = 11, /* a released block did not fit on the free stack             */
+    KVC_DEV_SHARED_PAGE = 12    /* a partly filled page is held by several sequences          */
 };
 
 /* A KV cache (or a prompt's keys/values) in device memory.
@@ -702,6 +707,155 @@ kvc_status kvc_latent_accept(const kvc_latent_cache *cache, int32_t *len, const 
 kvc_status kvc_latent_expand(const kvc_latent_cache *cache, const int32_t *len, int32_t n_valid,
                              const void *w_k, const void *w_v, const kvc_cache *dst,
                              void *stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* Norms of query and key heads and the rotation to their position, in one pass: what makes the rows
+ * that the caches of this library store and the queries that read them.  No counterpart on the
+ * pages (they take keys as position-encoded already, or store them before rotation).  For every
+ * token i, head h and row x of d_head elements, in fp32, rounded once to dtype:
+ *   y = x * rsqrt(mean(x^2) + eps) * w        (w_q for queries, w_k for keys; NULL: y = x)
+ *   of the first d_rot elements, with p = pos[i]:
+ *   y[j], y[j + d_rot/2] = y[j] c - y[j + d_rot/2] s,  y[j + d_rot/2] c + y[j] s,   j < d_rot/2
+ *   c = cos_sin[p][0][j], s = cos_sin[p][1][j]     (the table of kvc_rope_table(n_pos, d_rot))
+ * q: [n_tokens][n_heads_q][d_head], k: [n_tokens][n_heads_kv][d_head], each with its strides in
+ * elements (multiples of 16 bytes), so that both may lie in one projection's output; q_out and k_out
+ * likewise.  An output may be its input (the same pointer and strides); other overlaps are not
+ * allowed.  cos_sin NULL: no rotation (d_rot, pos and n_pos are not looked at); then a weight
+ * is needed.  d_rot: a multiple of 16 in 16..d_head.  A position outside [0, n_pos) records
+ * KVC_DEV_BAD_POSITION and leaves the token's outputs as they were.  n_tokens may be 0. */
+typedef struct {
+    const void *q;              /* device                                                    */
+    const void *k;
+    void *q_out;
+    void *k_out;
+    int32_t dtype;              /* KVC_F32 or KVC_BF16, of the rows and the weights           */
+    int32_t n_tokens;
+    int32_t n_heads_q;
+    int32_t n_heads_kv;         /* of k; any number beside n_heads_q                         */
+    int32_t d_head;             /* 64, 128 or 256                                            */
+    int32_t d_rot;
+    int64_t q_stride_token, q_stride_head, k_stride_token, k_stride_head;
+    int64_t q_out_stride_token, q_out_stride_head, k_out_stride_token, k_out_stride_head;
+} kvc_qk_rows;
+kvc_status kvc_qk_norm_rope(const kvc_qk_rows *rows, const void *w_q, const void *w_k, float eps,
+                            const float *cos_sin, const int32_t *pos, int32_t n_pos,
+                            void *stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* Pages in 8 bits.  No counterpart on the pages.  A pool whose pages hold e4m3 numbers (1 sign, 4
+ * exponent and 3 mantissa bits, no infinities, largest 448) and an fp32 scale for each page and
+ * head, for keys and for values: an element stands for its number times the scale of its page.
+ * pages.dtype is KVC_E4M3, pages.block_size a multiple of 16 up to 1024; k_scale and v_scale:
+ * device fp32[n_heads_kv][n_blocks], positive and at most 2^126.  Page tables and free pools are
+ * those of the other paged caches, and kvc_block_accumulate_evict serves these pages too; the other
+ * calls over kvc_block_pool refuse KVC_E4M3. */
+typedef struct {
+    kvc_block_pool pages;
+    float *k_scale;
+    float *v_scale;
+} kvc_block_pool_q8;
+
+/* Append rows to such pages: n_tokens rows in all, sequence b's being cu[b] .. cu[b+1]-1 (device
+ * int32[batch+1], ascending, within 0..n_tokens), or row b of exactly batch rows when cu is NULL.  A
+ * prompt and a decode step are the same call.
+ * k_new, v_new: [n_tokens][n_heads_kv][d_head], dtype KVC_F32 or KVC_BF16, both with the strides
+ * stride_token and stride_head in elements (multiples of 16 bytes).
+ * A page's scale for a head is the smallest power of two s (2^-120 .. 2^119) with max|x| / s <=
+ * 448 over its rows; stored is x / s rounded to nearest even.  Where new rows raise the scale of a
+ * partly filled page, the numbers there become e4m3(number * s_old / s_new) -- exact but for numbers
+ * that fall below 2^-6, so rows appended one by one and at once give the same page but for those.
+ * A page with another scale (not a power of two) is continued with the larger of the two.  NaN and
+ * infinities are stored as NaN and do not count for the scale.
+ * Pages are popped in sequence order from the top of the free stack (ids do not depend on timing),
+ * with score 0; n_blocks and len follow.  All or nothing for each sequence, as
+ * kvc_tree_accept_paged: lengths that disagree with n_blocks or a table without room
+ * (KVC_DEV_BAD_LENGTH), an id outside the pool of its partly filled page or among those it would pop
+ * (KVC_DEV_BAD_BLOCK; bad ids leave the stack), too few free pages (KVC_DEV_POOL_EMPTY).  Offsets cu
+ * that do not ascend within 0..n_tokens append nothing at all (KVC_DEV_BAD_LENGTH).
+ * appended (nullable): device int32[batch], the rows appended to each sequence.
+ * Two kernels.  Workspace: kvc_paged_append_q8_workspace_bytes(), 256-byte aligned; it need not be
+ * cleared, and calls that share one must not overlap on the GPU. */
+size_t kvc_paged_append_q8_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t block_size);
+kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_table *pt,
+                               const kvc_free_pool *free_pool, const void *k_new,
+                               const void *v_new, int32_t dtype, int32_t n_tokens,
+                               int64_t stride_token, int64_t stride_head, const int32_t *cu,
+                               int32_t *appended, void *ws, size_t ws_bytes, void *stream);
+
+/* kvc_decode_attn_paged over such pages: for every query head h of sequence b
+ *   out[b,h] = sum_j softmax_j(scale * q[b,h].k_j) v_j
+ * over the len[b] tokens of its page table.  q: [batch][n_heads_q][d_head] of dtype KVC_F32 or
+ * KVC_BF16, contiguous; out: the same shape and type.  logits (nullable; fp32, indexed by logical
+ * slot, logits_stride >= max_blocks * block_size) and lse (nullable; fp32 [batch][n_heads_q]) are
+ * what kvc_block_accumulate_evict takes.  A sequence without tokens gets out = 0, lse = -inf.  A
+ * length outside [0, max_blocks * block_size] records KVC_DEV_BAD_LENGTH and is clamped, a table
+ * entry outside the pool KVC_DEV_BAD_BLOCK and reads page 0.  What a page holds behind the length is
+ * never used, whatever it is.
+ * fp32 accumulation and softmax statistics.  With bf16 queries the weights are rounded to fp16 once
+ * (at most 2^-11 of each, eight times finer than the rounding of out); with fp32 queries, queries
+ * and weights enter the products as two fp16 terms (2^-23 of each row's largest element).  Any
+ * group size.  Results do not depend on timing.  One kernel or two.  Workspace:
+ * kvc_decode_attn_paged_q8_workspace_bytes(), 256-byte aligned; it need not be cleared, and calls
+ * that share one must not overlap on the GPU. */
+size_t kvc_decode_attn_paged_q8_workspace_bytes(int32_t batch, int32_t n_heads_q,
+                                                int32_t n_heads_kv, int32_t d_head,
+                                                int32_t dtype);
+kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_heads_q,
+                                    const kvc_block_pool_q8 *pool, const kvc_page_table *pt,
+                                    float scale, void *out, float *logits,
+                                    int64_t logits_stride, float *lse, void *ws,
+                                    size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------- */
+/* Pages held by several sequences (no counterpart on the pages).  Full pages are never written again,
+ * so sequences that begin alike may list the same ones.  shares: device int32[n_blocks], the
+ * sequences that hold a page beyond the first (0 for a page that one sequence holds and for a free
+ * one); zero-filled before the first call, then kept by the two calls below.  A partly filled page
+ * belongs to one sequence.  The calls that append (kvc_paged_append, kvc_paged_append_q8,
+ * kvc_tree_accept_paged, kvc_block_prompt_select) and those that read work on such sequences as
+ * they are.  kvc_block_accumulate_evict knows nothing of shares: give it only sequences whose pages
+ * are their own.
+ * pool: kvc_block_pool of KVC_F32 or KVC_BF16 with k_scale = v_scale = NULL, or the pages of a
+ * kvc_block_pool_q8 with its scales.  pos (nullable): device int32[n_blocks][block_size], the
+ * positions that kvc_paged_append keeps; they go along with their page.  One page table and one
+ * free pool a pool, as everywhere.
+ *
+ * kvc_pages_reorder: every sequence b becomes a copy of what sequence parent[b] was before the call,
+ * or is freed (parent[b] = -1: n_blocks = len = 0); parent[b] = b leaves it alone.  Forking a
+ * prompt, the next step of a beam search and freeing finished sequences are all this call.  parent:
+ * device int32[batch].  Table entries, scores, n_blocks and len follow the parent.  Full pages are
+ * shared; the partly filled page stays with the parent itself where it goes on, else with its first
+ * child, and the other children get a page of their own with a copy of its rows.  Pages that nobody
+ * holds any more are pushed on the free stack in ascending order, and copies take theirs from its
+ * top in sequence order (so ids do not depend on timing, and the stack needs room only for what stays
+ * free).
+ * All or nothing for the whole call, which leaves everything as it was when it records
+ * KVC_DEV_BAD_INDEX (parent outside [-1, batch)), KVC_DEV_BAD_LENGTH (len, n_blocks of any
+ * sequence), KVC_DEV_BAD_BLOCK (an id outside the pool, or a page listed by more sequences than
+ * shares counts), KVC_DEV_SHARED_PAGE, KVC_DEV_POOL_EMPTY (too few free pages, or a top outside
+ * [0, capacity]) or KVC_DEV_POOL_OVERFLOW (more free pages than the stack's capacity).  batch <= 8192.
+ *
+ * kvc_pages_compact: the live pages (those not on the free stack) move to the lowest ids 0 ..
+ * n_live - 1, so that the rest of the pool can be cut off or used otherwise: the k-th live page with
+ * an id >= n_live moves to the k-th free page below n_live, both counted in ascending order; page
+ * tables, scales, shares (nullable) and pos follow, and the free stack then hands out n_live, n_live +
+ * 1, ... in order.  remap: device int32[n_blocks], the new id of every live page and -1 for the free
+ * ones -- for those who keep ids elsewhere (a live page need not be in a table).
+ * A stack with a bad or doubled id, a table entry that is no live page (KVC_DEV_BAD_BLOCK), n_blocks
+ * outside the table (KVC_DEV_BAD_LENGTH) or a top outside the stack (KVC_DEV_POOL_EMPTY): nothing
+ * is moved and remap is not written.
+ *
+ * Each is two kernels.  Workspace of both: kvc_pages_workspace_bytes(), 256-byte aligned; it need not
+ * be cleared, and calls that share one must not overlap on the GPU. */
+size_t kvc_pages_workspace_bytes(int32_t batch, int32_t max_blocks, int32_t n_blocks);
+kvc_status kvc_pages_reorder(const kvc_block_pool *pool, float *k_scale, float *v_scale,
+                             const kvc_page_table *pt, const kvc_free_pool *free_pool,
+                             int32_t *shares, int32_t *pos, const int32_t *parent, void *ws,
+                             size_t ws_bytes, void *stream);
+kvc_status kvc_pages_compact(const kvc_block_pool *pool, float *k_scale, float *v_scale,
+                             const kvc_page_table *pt, const kvc_free_pool *free_pool,
+                             int32_t *shares, int32_t *pos, int32_t *remap, void *ws,
+                             size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

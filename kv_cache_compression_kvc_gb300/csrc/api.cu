@@ -1532,4 +1532,333 @@ kvc_status kvc_latent_expand(const kvc_latent_cache *cache, const int32_t *len, 
     return ok();
 }
 
+// ------------------------------------------------------------------------------------------
+// Norms and rotation, pages in 8 bits, shared pages.
+static kvc_status check_rows(const void *p, int64_t token, int64_t head, int64_t d, int64_t eb,
+                             const char *name, const char *what)
+{
+    if (p == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null %s", name, what);
+    if (token < 0 || head < 0 || (head > 0 && head < d))
+        return fail(KVC_ERR_SHAPE, "%s: strides of %s", name, what);
+    if (!aligned16(p) || token * eb % 16 || head * eb % 16)
+        return fail(KVC_ERR_ALIGN, "%s: %s and its strides must be 16-byte aligned", name, what);
+    return KVC_OK;
+}
+
+kvc_status kvc_qk_norm_rope(const kvc_qk_rows *r, const void *w_q, const void *w_k, float eps,
+                            const float *cos_sin, const int32_t *pos, int32_t n_pos, void *stream)
+{
+    const char *name = "kvc_qk_norm_rope";
+    if (r == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null rows", name);
+    if (r->dtype != KVC_F32 && r->dtype != KVC_BF16)
+        return fail(KVC_ERR_INVALID_ARG, "%s: dtype %d", name, r->dtype);
+    if (r->n_tokens < 0 || r->n_heads_q <= 0 || r->n_heads_kv <= 0)
+        return fail(KVC_ERR_SHAPE, "%s: %d tokens, %d and %d heads", name, r->n_tokens, r->n_heads_q,
+                    r->n_heads_kv);
+    if (r->d_head != 64 && r->d_head != 128 && r->d_head != 256)
+        return fail(KVC_ERR_SHAPE, "%s: d_head %d (supported: 64, 128, 256)", name, r->d_head);
+    if (cos_sin == nullptr && w_q == nullptr && w_k == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "%s: neither weights nor a table", name);
+    if (!(eps >= 0.f) || !std::isfinite(eps))
+        return fail(KVC_ERR_INVALID_ARG, "%s: eps %g", name, (double)eps);
+    const int64_t eb = elem_bytes(r->dtype), d = r->d_head;
+    if (cos_sin != nullptr) {
+        if (r->d_rot < 16 || r->d_rot > r->d_head || r->d_rot % 16)
+            return fail(KVC_ERR_SHAPE, "%s: d_rot %d (a multiple of 16 up to d_head %d)", name, r->d_rot,
+                        r->d_head);
+        if (pos == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: a table needs positions", name);
+        if (n_pos <= 0) return fail(KVC_ERR_SHAPE, "%s: n_pos %d", name, n_pos);
+        if (!aligned16(cos_sin) || (reinterpret_cast<uintptr_t>(pos) & 3u))
+            return fail(KVC_ERR_ALIGN, "%s: cos_sin must be 16-byte, pos 4-byte aligned", name);
+    }
+    if (!aligned16(w_q) || !aligned16(w_k))
+        return fail(KVC_ERR_ALIGN, "%s: weights must be 16-byte aligned", name);
+    if (r->n_tokens == 0) return ok();
+    kvc_status st = check_rows(r->q, r->q_stride_token, r->q_stride_head, d, eb, name, "q");
+    if (st == KVC_OK) st = check_rows(r->k, r->k_stride_token, r->k_stride_head, d, eb, name, "k");
+    if (st == KVC_OK)
+        st = check_rows(r->q_out, r->q_out_stride_token, r->q_out_stride_head, d, eb, name, "q_out");
+    if (st == KVC_OK)
+        st = check_rows(r->k_out, r->k_out_stride_token, r->k_out_stride_head, d, eb, name, "k_out");
+    if (st != KVC_OK) return st;
+    // outputs are written row by row: rows that coincide would race
+    const auto apart = [d](int64_t n_in, int64_t in, int64_t n_out, int64_t out) {
+        return (n_in <= 1 || in >= d) && (n_out <= 1 || out >= (n_in - 1) * in + d);
+    };
+    const auto disjoint = [&](int64_t heads, int64_t token, int64_t head) {
+        return apart(heads, head, r->n_tokens, token) || apart(r->n_tokens, token, heads, head);
+    };
+    if (!disjoint(r->n_heads_q, r->q_out_stride_token, r->q_out_stride_head) ||
+        !disjoint(r->n_heads_kv, r->k_out_stride_token, r->k_out_stride_head))
+        return fail(KVC_ERR_SHAPE, "%s: output rows overlap", name);
+    if ((r->q == r->q_out && (r->q_stride_token != r->q_out_stride_token || r->q_stride_head != r->q_out_stride_head)) ||
+        (r->k == r->k_out && (r->k_stride_token != r->k_out_stride_token || r->k_stride_head != r->k_out_stride_head)))
+        return fail(KVC_ERR_SHAPE, "%s: in place needs the same strides", name);
+    if ((long long)r->n_tokens * ((long long)r->n_heads_q + r->n_heads_kv) > 0x7fffffffLL)
+        return fail(KVC_ERR_SHAPE, "%s: too many rows", name);
+    int32_t *code = nullptr;
+    st = device_info(&code, nullptr);
+    if (st != KVC_OK) return st;
+    kvc::QkNormParams p{};
+    p.q = r->q; p.k = r->k; p.q_out = r->q_out; p.k_out = r->k_out;
+    p.q_st = r->q_stride_token; p.q_sh = r->q_stride_head;
+    p.k_st = r->k_stride_token; p.k_sh = r->k_stride_head;
+    p.qo_st = r->q_out_stride_token; p.qo_sh = r->q_out_stride_head;
+    p.ko_st = r->k_out_stride_token; p.ko_sh = r->k_out_stride_head;
+    p.n_tokens = r->n_tokens; p.Hq = r->n_heads_q; p.Hkv = r->n_heads_kv;
+    p.w_q = w_q; p.w_k = w_k; p.eps = eps;
+    if (cos_sin != nullptr) {
+        p.rot = r->d_rot;
+        p.cos_sin = cos_sin; p.pos = pos; p.n_pos = n_pos;
+    }
+    p.dev_code = code;
+    const cudaError_t e =
+        kvc::launch_qk_norm_rope(p, r->d_head, r->dtype == KVC_BF16, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
+    return ok();
+}
+
+// A pool of any element type, with scales exactly where it holds e4m3 numbers.
+static kvc_status check_pages(const kvc_block_pool *pool, const float *ks, const float *vs,
+                              const kvc_page_table *pt, const char *name)
+{
+    if (pool == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null pool or page-table descriptor", name);
+    const bool q8 = pool->dtype == KVC_E4M3;
+    if ((ks != nullptr) != q8 || (vs != nullptr) != q8)
+        return fail(KVC_ERR_INVALID_ARG, "%s: scales belong to pages of dtype KVC_E4M3, and only to them", name);
+    if (q8 && (pool->block_size % 16 || pool->block_size > 1024))
+        return fail(KVC_ERR_SHAPE, "%s: block_size %d (8-bit pages: a multiple of 16 up to 1024)", name,
+                    pool->block_size);
+    if (q8 && ((reinterpret_cast<uintptr_t>(ks) | reinterpret_cast<uintptr_t>(vs)) & 3u))
+        return fail(KVC_ERR_ALIGN, "%s: scales must be 4-byte aligned", name);
+    // the sizes, as of a pool of 16-bit numbers (whose strides are multiples of 16 bytes where 8-bit ones are)
+    kvc_block_pool like = *pool;
+    if (q8) like.dtype = KVC_BF16;
+    kvc_cache view;
+    return check_paged(&like, pt, name, &view);
+}
+
+static kvc_status check_ws(const void *ws, size_t have, size_t need, const char *name)
+{
+    if (ws == nullptr || have < need)
+        return fail(KVC_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", name, need,
+                    ws == nullptr ? (size_t)0 : have);
+    if (!aligned256(ws)) return fail(KVC_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", name);
+    return KVC_OK;
+}
+
+// Pages that get rows: each holds one new row at least, and all but two of a sequence are filled by it.
+static long long append_jobs(long long batch, long long n_tokens, long long bs)
+{
+    return std::min(n_tokens, n_tokens / bs + 2 * batch);
+}
+
+size_t kvc_paged_append_q8_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t block_size)
+{
+    if (batch <= 0 || n_tokens < 0 || block_size <= 0) return 0;
+    return 256 + align256((size_t)append_jobs(batch, n_tokens, block_size) * sizeof(int4));
+}
+
+kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_table *pt,
+                               const kvc_free_pool *free_pool, const void *k_new, const void *v_new,
+                               int32_t dtype, int32_t n_tokens, int64_t stride_token,
+                               int64_t stride_head, const int32_t *cu, int32_t *appended, void *ws,
+                               size_t ws_bytes, void *stream)
+{
+    const char *name = "kvc_paged_append_q8";
+    if (pool == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null pool or page-table descriptor", name);
+    if (pool->pages.dtype != KVC_E4M3)
+        return fail(KVC_ERR_INVALID_ARG, "%s: pool dtype %d (KVC_E4M3 needed)", name, pool->pages.dtype);
+    kvc_status st = check_pages(&pool->pages, pool->k_scale, pool->v_scale, pt, name);
+    if (st != KVC_OK) return st;
+    st = check_free_pool(free_pool, name);
+    if (st != KVC_OK) return st;
+    if (dtype != KVC_F32 && dtype != KVC_BF16) return fail(KVC_ERR_INVALID_ARG, "%s: dtype %d", name, dtype);
+    if (n_tokens < 0 || (cu == nullptr && n_tokens != pt->batch))
+        return fail(KVC_ERR_SHAPE, "%s: %d rows for %d sequences without offsets", name, n_tokens, pt->batch);
+    const int64_t eb = elem_bytes(dtype), d = pool->pages.d_head;
+    if (n_tokens > 0) {
+        st = check_rows(k_new, stride_token, stride_head, d, eb, name, "k_new");
+        if (st == KVC_OK) st = check_rows(v_new, stride_token, stride_head, d, eb, name, "v_new");
+        if (st != KVC_OK) return st;
+    }
+    if ((reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(appended)) & 3u)
+        return fail(KVC_ERR_ALIGN, "%s: cu and appended must be 4-byte aligned", name);
+    const long long jobs = append_jobs(pt->batch, n_tokens, pool->pages.block_size);
+    if (jobs * 2 * pool->pages.n_heads_kv > 0x7fffffffLL)
+        return fail(KVC_ERR_SHAPE, "%s: too many rows", name);
+    st = check_ws(ws, ws_bytes,
+                  kvc_paged_append_q8_workspace_bytes(pt->batch, n_tokens, pool->pages.block_size), name);
+    if (st != KVC_OK) return st;
+    int32_t *code = nullptr;
+    st = device_info(&code, nullptr);
+    if (st != KVC_OK) return st;
+    kvc::AppendQ8Params p{};
+    p.k = static_cast<uint8_t *>(pool->pages.k); p.v = static_cast<uint8_t *>(pool->pages.v);
+    p.ks = pool->k_scale; p.vs = pool->v_scale;
+    p.n_pool = pool->pages.n_blocks; p.H = pool->pages.n_heads_kv; p.bs = pool->pages.block_size;
+    p.D = pool->pages.d_head; p.B = pt->batch; p.max_blocks = pt->max_blocks;
+    p.table = pt->table; p.n_blocks = pt->n_blocks; p.len = pt->len; p.score = pt->score;
+    p.free_ids = free_pool->ids; p.free_top = free_pool->top; p.free_cap = free_pool->capacity;
+    p.k_new = k_new; p.v_new = v_new; p.new_st = stride_token; p.new_sh = stride_head;
+    p.cu = cu; p.n_tokens = n_tokens; p.appended = appended;
+    p.n_jobs = static_cast<int32_t *>(ws);
+    p.jobs = reinterpret_cast<int4 *>(static_cast<char *>(ws) + 256);
+    p.max_jobs = (int32_t)jobs;
+    p.dev_code = code;
+    const cudaError_t e =
+        kvc::launch_paged_append_q8(p, dtype == KVC_BF16, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit append launch");
+    return ok();
+}
+
+size_t kvc_decode_attn_paged_q8_workspace_bytes(int32_t batch, int32_t n_heads_q, int32_t n_heads_kv,
+                                                int32_t d_head, int32_t dtype)
+{
+    if (batch <= 0 || n_heads_q <= 0 || n_heads_kv <= 0 || n_heads_q % n_heads_kv || d_head <= 0) return 0;
+    return kvc::decode_q8_plan(batch, n_heads_kv, n_heads_q / n_heads_kv, d_head, dtype == KVC_BF16,
+                               sm_count_or_default()).bytes;
+}
+
+kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_heads_q,
+                                    const kvc_block_pool_q8 *pool, const kvc_page_table *pt, float scale,
+                                    void *out, float *logits, int64_t logits_stride, float *lse, void *ws,
+                                    size_t ws_bytes, void *stream)
+{
+    const char *name = "kvc_decode_attn_paged_q8";
+    if (pool == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null pool or page-table descriptor", name);
+    if (pool->pages.dtype != KVC_E4M3)
+        return fail(KVC_ERR_INVALID_ARG, "%s: pool dtype %d (KVC_E4M3 needed)", name, pool->pages.dtype);
+    kvc_status st = check_pages(&pool->pages, pool->k_scale, pool->v_scale, pt, name);
+    if (st != KVC_OK) return st;
+    if (dtype != KVC_F32 && dtype != KVC_BF16) return fail(KVC_ERR_INVALID_ARG, "%s: dtype %d", name, dtype);
+    if (q == nullptr || out == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null q or out", name);
+    if (!aligned16(q) || !aligned16(out) ||
+        ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(lse)) & 3u))
+        return fail(KVC_ERR_ALIGN, "%s: q and out must be 16-byte, logits and lse 4-byte aligned", name);
+    if (!std::isfinite(scale)) return fail(KVC_ERR_INVALID_ARG, "%s: scale is not finite", name);
+    const int Hkv = pool->pages.n_heads_kv;
+    if (n_heads_q <= 0 || n_heads_q % Hkv)
+        return fail(KVC_ERR_SHAPE, "%s: %d query heads over %d KV heads", name, n_heads_q, Hkv);
+    const int cap = pt->max_blocks * pool->pages.block_size;
+    if (logits != nullptr && logits_stride < cap)
+        return fail(KVC_ERR_CAPACITY, "%s: logits_stride %lld < %d", name, (long long)logits_stride, cap);
+    int32_t *code = nullptr;
+    int n_sm = 0;
+    st = device_info(&code, &n_sm);
+    if (st != KVC_OK) return st;
+    const int G = n_heads_q / Hkv;
+    const kvc::DecodeQ8Plan pl =
+        kvc::decode_q8_plan(pt->batch, Hkv, G, pool->pages.d_head, dtype == KVC_BF16, n_sm);
+    if ((long long)pt->batch * Hkv * pl.RT > 0x3fffffffLL || (long long)pt->batch * n_heads_q > 0x7fffffffLL)
+        return fail(KVC_ERR_SHAPE, "%s: batch * heads too large", name);
+    st = check_ws(ws, ws_bytes, pl.bytes, name);
+    if (st != KVC_OK) return st;
+    kvc::DecodeQ8Params p{};
+    p.q = q;
+    p.k = static_cast<const uint8_t *>(pool->pages.k); p.v = static_cast<const uint8_t *>(pool->pages.v);
+    p.ks = pool->k_scale; p.vs = pool->v_scale;
+    p.table = pt->table; p.len = pt->len;
+    p.n_pool = pool->pages.n_blocks; p.bs = pool->pages.block_size; p.max_blocks = pt->max_blocks;
+    p.cap = cap;
+    const uint64_t steps = pool->pages.block_size / 16;
+    p.magic = steps > 1 ? (uint32_t)(((1ull << 32) + steps - 1) / steps) : 0u;
+    p.B = pt->batch; p.Hq = n_heads_q; p.G = G;
+    p.RT = pl.RT; p.RP = pl.RP; p.HR = Hkv * pl.RT;
+    p.scale = scale;
+    p.out = out; p.logits = logits; p.logits_stride = logits_stride; p.lse = lse;
+    p.ranges = pl.ranges; p.by_tile = pl.by_tile; p.n_sm = n_sm;
+    char *w = static_cast<char *>(ws);
+    p.ws_note = reinterpret_cast<int4 *>(w + pl.off_note);
+    p.ws_ml = reinterpret_cast<float *>(w + pl.off_ml);
+    p.ws_o = reinterpret_cast<float *>(w + pl.off_o);
+    p.dev_code = code;
+    const cudaError_t e = kvc::launch_decode_q8(p, pool->pages.d_head, dtype == KVC_BF16,
+                                                static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit decode attention launch");
+    return ok();
+}
+
+// The workspace of the two page calls: counts, freed ids (three lists when compacting), copies, and the
+// reordered tables.
+static size_t pages_layout(int B, int mb, int nb, size_t *ids, size_t *copies, size_t *table, size_t *score)
+{
+    const size_t entries = (size_t)B * mb;
+    *ids = 256;
+    *copies = *ids + align256((size_t)nb * 3 * sizeof(int32_t));
+    *table = *copies + align256((size_t)std::max(B, nb / 2) * sizeof(int4));
+    *score = *table + align256(entries * sizeof(int32_t));
+    return *score + align256(entries * sizeof(float));
+}
+
+size_t kvc_pages_workspace_bytes(int32_t batch, int32_t max_blocks, int32_t n_blocks)
+{
+    if (batch <= 0 || max_blocks <= 0 || n_blocks <= 0) return 0;
+    size_t a, b, c, d;
+    return pages_layout(batch, max_blocks, n_blocks, &a, &b, &c, &d);
+}
+
+static kvc_status pages_call(const kvc_block_pool *pool, float *ks, float *vs, const kvc_page_table *pt,
+                             const kvc_free_pool *free_pool, int32_t *shares, int32_t *pos,
+                             const int32_t *parent, int32_t *remap, void *ws, size_t ws_bytes, bool reorder,
+                             void *stream, const char *name)
+{
+    kvc_status st = check_pages(pool, ks, vs, pt, name);
+    if (st != KVC_OK) return st;
+    st = check_free_pool(free_pool, name);
+    if (st != KVC_OK) return st;
+    if (reorder && (shares == nullptr || parent == nullptr))
+        return fail(KVC_ERR_INVALID_ARG, "%s: null shares or parent", name);
+    if (!reorder && remap == nullptr) return fail(KVC_ERR_INVALID_ARG, "%s: null remap", name);
+    if ((reinterpret_cast<uintptr_t>(shares) | reinterpret_cast<uintptr_t>(pos) |
+         reinterpret_cast<uintptr_t>(parent) | reinterpret_cast<uintptr_t>(remap)) & 3u)
+        return fail(KVC_ERR_ALIGN, "%s: shares, pos, parent and remap must be 4-byte aligned", name);
+    if (reorder && pt->batch > kvc::kPagesMaxBatch)
+        return fail(KVC_ERR_SHAPE, "%s: batch %d > %d", name, pt->batch, kvc::kPagesMaxBatch);
+    st = check_ws(ws, ws_bytes, kvc_pages_workspace_bytes(pt->batch, pt->max_blocks, pool->n_blocks), name);
+    if (st != KVC_OK) return st;
+    int32_t *code = nullptr;
+    int n_sm = 0;
+    st = device_info(&code, &n_sm);
+    if (st != KVC_OK) return st;
+    size_t ids, copies, table, score;
+    pages_layout(pt->batch, pt->max_blocks, pool->n_blocks, &ids, &copies, &table, &score);
+    char *w = static_cast<char *>(ws);
+    kvc::PagesParams p{};
+    p.k = static_cast<char *>(pool->k); p.v = static_cast<char *>(pool->v);
+    p.ks = ks; p.vs = vs;
+    p.n_pool = pool->n_blocks; p.H = pool->n_heads_kv; p.bs = pool->block_size;
+    p.row_bytes = pool->d_head * (pool->dtype == KVC_E4M3 ? 1 : elem_bytes(pool->dtype));
+    p.B = pt->batch; p.max_blocks = pt->max_blocks;
+    p.table = pt->table; p.n_blocks = pt->n_blocks; p.len = pt->len; p.score = pt->score;
+    p.free_ids = free_pool->ids; p.free_top = free_pool->top; p.free_cap = free_pool->capacity;
+    p.shares = shares; p.pos = pos; p.parent = parent; p.remap = remap;
+    p.ws_n = reinterpret_cast<int32_t *>(w);
+    p.ws_ids = reinterpret_cast<int32_t *>(w + ids);
+    p.ws_copies = reinterpret_cast<int4 *>(w + copies);
+    p.ws_table = reinterpret_cast<int32_t *>(w + table);
+    p.ws_score = reinterpret_cast<float *>(w + score);
+    p.dev_code = code;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = reorder ? kvc::launch_pages_reorder(p, n_sm, s) : kvc::launch_pages_compact(p, n_sm, s);
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    return ok();
+}
+
+kvc_status kvc_pages_reorder(const kvc_block_pool *pool, float *k_scale, float *v_scale,
+                             const kvc_page_table *pt, const kvc_free_pool *free_pool, int32_t *shares,
+                             int32_t *pos, const int32_t *parent, void *ws, size_t ws_bytes, void *stream)
+{
+    return pages_call(pool, k_scale, v_scale, pt, free_pool, shares, pos, parent, nullptr, ws, ws_bytes, true,
+                      stream, "kvc_pages_reorder");
+}
+
+kvc_status kvc_pages_compact(const kvc_block_pool *pool, float *k_scale, float *v_scale,
+                             const kvc_page_table *pt, const kvc_free_pool *free_pool, int32_t *shares,
+                             int32_t *pos, int32_t *remap, void *ws, size_t ws_bytes, void *stream)
+{
+    return pages_call(pool, k_scale, v_scale, pt, free_pool, shares, pos, nullptr, remap, ws, ws_bytes, false,
+                      stream, "kvc_pages_compact");
+}
+
 }  // extern "C"

@@ -1,0 +1,412 @@
+// append_q8.cu -- new rows into pages of e4m3 numbers with a scale for each page and head.
+//
+//   s = 2^e, the smallest power of two with max|x| / s <= 448 over the page's rows of a head,
+//   stored x8 = e4m3(x / s), rounded to nearest even: 4 significant bits down to 2^-6 s.
+//
+// Scales are powers of two so that a growing one only moves exponents: rows that a partly filled
+// page held already are brought to the new scale (x8 * s_old / s_new, exact unless it falls below
+// 2^-6 s_new, where the steps are 2^-9 s_new), and a page filled token by token holds what the same
+// rows quantised at once hold, but for such small values.  A page whose scale is no power of two
+// (written by someone else) is read and continued just as well, with a division.
+//
+// append_q8_plan_kernel, one block: checks every sequence, numbers the pages they need in sequence
+// order (block-wide scans) and takes them from the top of the free stack, so that ids do not depend
+// on timing; it writes one job per page that gets rows.  append_q8_rows_kernel, a warp per (job, head,
+// K or V): the rows stay in registers between the maximum and the rounding.  Bound by HBM (2 or 4
+// bytes in, 1 out an element) for prompts, by the latency of the two kernels for single tokens.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kRowWarps = 4;
+constexpr int kDevBadLen_ = 5;               // KVC_DEV_BAD_LENGTH
+constexpr int kDevBadBlk_ = 9;               // KVC_DEV_BAD_BLOCK
+constexpr int kDevPoolEmpty_ = 10;           // KVC_DEV_POOL_EMPTY
+
+// Inclusive scan of two counters over the block (threads in order); s_warp: 2 * 32 words.
+__device__ __forceinline__ int2 block_scan(int2 x, int *s_warp, int2 *all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
+        if (lane >= o) {
+            x.x += a;
+            x.y += b;
+        }
+    }
+    __syncthreads();                         // (s_warp is free)
+    if (lane == 31) {
+        s_warp[warp] = x.x;
+        s_warp[32 + warp] = x.y;
+    }
+    __syncthreads();
+    int2 before = make_int2(0, 0), total = make_int2(0, 0);
+#pragma unroll 4
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        const int a = s_warp[w], b = s_warp[32 + w];
+        if (w < warp) {
+            before.x += a;
+            before.y += b;
+        }
+        total.x += a;
+        total.y += b;
+    }
+    *all = total;
+    return make_int2(x.x + before.x, x.y + before.y);
+}
+
+// The first of n ascending numbers above x.
+__device__ __forceinline__ int find_above(const int *a, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] > x) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) append_q8_plan_kernel(const AppendQ8Params p)
+{
+    __shared__ int s_warp[64];
+    __shared__ int s_need[kPlanThreads];     // pages to pop (then their inclusive scan)
+    __shared__ int s_jobs[kPlanThreads];     // inclusive scan of the pages that get rows
+    __shared__ int s_first[kPlanThreads];    // a sequence's ids are ids[first - 1], ids[first - 2], ...
+    __shared__ int s_n[kPlanThreads];        // rows to append
+    __shared__ int s_len[kPlanThreads], s_row[kPlanThreads];
+    __shared__ int s_top;
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x;
+    bool bad = false;
+    if (p.cu != nullptr)
+        for (int b = tid; b < p.B; b += kPlanThreads) {
+            const int lo = p.cu[b], hi = p.cu[b + 1];
+            bad |= lo < 0 || hi < lo || hi > p.n_tokens;
+        }
+    int top0 = 0;
+    if (tid == 0) {
+        top0 = *p.free_top;
+        if (top0 < 0 || top0 > p.free_cap) {
+            record_code(p.dev_code, kDevPoolEmpty_);
+            top0 = 0;
+        }
+        s_top = top0;
+    }
+    if (__syncthreads_or(bad)) {             // offsets that are none: nothing is appended at all
+        if (tid == 0) {
+            record_code(p.dev_code, kDevBadLen_);
+            *p.n_jobs = 0;
+        }
+        if (p.appended != nullptr)
+            for (int b = tid; b < p.B; b += kPlanThreads) p.appended[b] = 0;
+        return;
+    }
+    int jobs0 = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int n = 0, need = 0, jobs = 0, len = 0, nb = 0, row = 0;
+        if (b < p.B) {
+            row = p.cu != nullptr ? p.cu[b] : b;
+            n = p.cu != nullptr ? p.cu[b + 1] - row : 1;
+            len = p.len[b];
+            nb = p.n_blocks[b];
+            int code = 0;
+            if (len < 0 || len > p.max_blocks * p.bs || nb != (len + p.bs - 1) / p.bs ||
+                n > p.max_blocks * p.bs - len) {
+                code = kDevBadLen_;
+            } else if (n > 0 && len % p.bs != 0) {   // the page that takes the first row is there already
+                const int id = p.table[(size_t)b * p.max_blocks + len / p.bs];
+                if (id < 0 || id >= p.n_pool) code = kDevBadBlk_;
+            }
+            if (code != 0) {
+                record_code(p.dev_code, code);
+                n = 0;
+            }
+            if (n > 0) {
+                need = (len + n + p.bs - 1) / p.bs - nb;
+                jobs = need + (len % p.bs != 0 ? 1 : 0);
+            }
+        }
+        int2 all;
+        int2 incl = block_scan(make_int2(need, jobs), s_warp, &all);
+        const int top = s_top;
+        int first = top - (incl.x - need);
+        bool skip = all.x > top;
+        if (!skip)
+            for (int i = tid; i < all.x; i += kPlanThreads) {
+                const int id = p.free_ids[top - 1 - i];
+                skip |= id < 0 || id >= p.n_pool;
+            }
+        s_need[tid] = need;
+        s_n[tid] = n;
+        if (__syncthreads_or(skip)) {
+            // too few ids, or one that is no page: the sequences one by one in order
+            if (tid == 0) {
+                int t = top;
+                for (int i = 0; i < min(kPlanThreads, p.B - b0); ++i) {
+                    const int want = s_need[i];
+                    s_first[i] = t;
+                    if (want == 0) continue;
+                    if (want > t) {
+                        record_code(p.dev_code, kDevPoolEmpty_);
+                        s_n[i] = 0;
+                        continue;
+                    }
+                    int keep = t - want;     // a bad id leaves the stack, the good ones stay for the others
+                    for (int j = t - want; j < t; ++j) {
+                        const int id = p.free_ids[j];
+                        if (id < 0 || id >= p.n_pool) continue;
+                        if (keep != j) p.free_ids[keep] = id;
+                        ++keep;
+                    }
+                    if (keep < t) {
+                        record_code(p.dev_code, kDevBadBlk_);
+                        s_n[i] = 0;
+                        t = keep;
+                    } else {
+                        t -= want;
+                    }
+                }
+                s_top = t;
+            }
+            __syncthreads();
+            n = s_n[tid];
+            first = s_first[tid];
+            if (n == 0) need = jobs = 0;
+            incl = block_scan(make_int2(need, jobs), s_warp, &all);
+        } else if (tid == 0) {
+            s_top = top - all.x;
+        }
+        __syncthreads();
+        s_need[tid] = incl.x;
+        s_jobs[tid] = incl.y;
+        s_first[tid] = first;
+        s_n[tid] = n;
+        s_len[tid] = len;
+        s_row[tid] = row;
+        __syncthreads();
+        // table entries of the popped pages, then a job for every page that gets rows
+        for (int e = tid; e < all.x; e += kPlanThreads) {
+            const int i = find_above(s_need, kPlanThreads, e);
+            const int j = e - (i > 0 ? s_need[i - 1] : 0);
+            const size_t at = (size_t)(b0 + i) * p.max_blocks + (s_len[i] + p.bs - 1) / p.bs + j;
+            p.table[at] = p.free_ids[s_first[i] - 1 - j];
+            p.score[at] = 0.f;
+        }
+        for (int e = tid; e < all.y; e += kPlanThreads) {
+            const int i = find_above(s_jobs, kPlanThreads, e);
+            const int j = e - (i > 0 ? s_jobs[i - 1] : 0);
+            const int l = s_len[i], lb = l / p.bs + j, held = j == 0 ? l % p.bs : 0;
+            const int at = lb * p.bs + held;                   // the first new row's slot
+            const int id = held > 0 ? p.table[(size_t)(b0 + i) * p.max_blocks + lb]
+                                    : p.free_ids[s_first[i] - 1 - (lb - (l + p.bs - 1) / p.bs)];
+            const int rows = min(p.bs - held, l + s_n[i] - at);
+            p.jobs[jobs0 + e] = make_int4(id, held, s_row[i] + at - l, rows);
+        }
+        jobs0 += all.y;
+        if (b < p.B) {
+            if (n > 0) {
+                p.n_blocks[b] = nb + need;
+                p.len[b] = len + n;
+            }
+            if (p.appended != nullptr) p.appended[b] = n;
+        }
+        __syncthreads();
+    }
+    if (tid == 0) {
+        *p.n_jobs = jobs0;
+        if (s_top != top0) *p.free_top = s_top;
+    }
+}
+
+// 8 elements of a row, and their largest size as a float's bits (NaN counts as nothing).
+template <typename T>
+struct Row8;
+template <>
+struct Row8<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const void *p) { w = ld_stream_16(p); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float *f) const
+    {
+        f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
+        f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
+    }
+};
+template <>
+struct Row8<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void *p)
+    {
+        a = ld_stream_16(p);
+        b = ld_stream_16(static_cast<const char *>(p) + 16);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float *f) const
+    {
+        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+        f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+        f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
+        f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+    }
+};
+
+// The smallest power of two s >= 2^-120 with amax / s <= 448 = 1.75 * 2^8 (2^119 at most: beyond
+// 448 * 2^119 = 2.98e38 values saturate).
+__device__ __forceinline__ float scale_for(float amax)
+{
+    const uint32_t u = __float_as_uint(amax);
+    int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = e < -120 ? -120 : (e > 119 ? 119 : e);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
+{
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+}
+
+// NV: vectors of 8 elements that a lane holds at once.
+template <typename T, int D, int NV>
+__global__ void __launch_bounds__(kRowWarps * 32) append_q8_rows_kernel(const AppendQ8Params p)
+{
+    constexpr int VPR = D / 8;               // vectors per row
+    const int lane = threadIdx.x & 31;
+    const long long task = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    pdl_trigger();
+    pdl_wait();
+    const int job = (int)(task / (2 * p.H)), rest = (int)(task - (long long)job * (2 * p.H));
+    if (job >= *p.n_jobs) return;
+    const int4 j = p.jobs[job];
+    const int h = rest >> 1, held = j.y, n_vec = j.w * VPR;
+    const bool is_v = rest & 1;
+    const T *src = static_cast<const T *>(is_v ? p.v_new : p.k_new) + h * p.new_sh;
+    const int64_t st = p.new_st;
+    const size_t page = (size_t)h * p.n_pool + j.x;
+    uint8_t *dst = (is_v ? p.v : p.k) + page * p.bs * D;
+    float *scale = (is_v ? p.vs : p.ks) + page;
+    const float s_old = held > 0 ? *scale : 0.f;
+
+    Row8<T> x[NV];
+    auto fetch = [&](int v0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = v0 + i * 32 + lane;
+            if (v < n_vec) x[i].load(src + (int64_t)(j.z + v / VPR) * st + v % VPR * 8);
+            else x[i].zero();
+        }
+    };
+    float amax = 0.f;
+    for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
+        fetch(v0);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float f[8];
+            x[i].get(f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+        }
+    }
+    amax = warp_max(amax);
+    const bool inf = amax == INFINITY;       // then the largest finite one counts
+    if (inf) {
+        amax = 0.f;
+        for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
+            fetch(v0);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float f[8];
+                x[i].get(f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (fabsf(f[k]) < INFINITY) amax = fmaxf(amax, fabsf(f[k]));
+            }
+        }
+        amax = warp_max(amax);
+    }
+    const float s = fmaxf(s_old, scale_for(amax));
+    __syncwarp();                            // every lane has read the scale
+    if (lane == 0 && (held == 0 || s != s_old)) *scale = s;
+    if (held > 0 && s != s_old) {            // the rows held before go over to the new scale
+        const float ratio = s_old / s;
+        for (int i = lane; i < held * (D / 16); i += 32) {
+            uint4 w = *reinterpret_cast<uint4 *>(dst + i * 16);
+            uint32_t *q = &w.x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 a = __half22float2(
+                    __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k] & 0xffffu), __NV_E4M3)));
+                const float2 b = __half22float2(
+                    __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q[k] >> 16), __NV_E4M3)));
+                q[k] = pack4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+            }
+            *reinterpret_cast<uint4 *>(dst + i * 16) = w;
+        }
+    }
+    const float inv = 1.f / s;
+    const bool power = (__float_as_uint(s) & 0x7fffffu) == 0u;   // then x * inv is x / s
+    for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
+        if (n_vec > 32 * NV || inf) fetch(v0);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = v0 + i * 32 + lane;
+            float f[8];
+            x[i].get(f);
+            if (inf)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (fabsf(f[k]) == INFINITY) f[k] = __uint_as_float(0x7fc00000u);
+            if (power)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] *= inv;
+            else
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[k] = f[k] / s;
+            if (v < n_vec)
+                *reinterpret_cast<uint2 *>(dst + (size_t)held * D + (size_t)v * 8) =
+                    make_uint2(pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]));
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t rows_typed(const AppendQ8Params &p, cudaStream_t stream)
+{
+    const long long tasks = (long long)p.max_jobs * 2 * p.H;
+    const dim3 grid((unsigned)(tasks > 0 ? (tasks + kRowWarps - 1) / kRowWarps : 1)), block(kRowWarps * 32);
+    // a page of 32 rows of 128 elements is 16 vectors a lane, which is what registers hold in bf16
+    constexpr int NV = sizeof(T) == 2 ? 16 : 8;
+    if (p.cu == nullptr) return launch_pdl(append_q8_rows_kernel<T, D, 1>, grid, block, 0, stream, p);
+    return launch_pdl(append_q8_rows_kernel<T, D, NV>, grid, block, 0, stream, p);
+}
+template <typename T>
+cudaError_t rows_dims(const AppendQ8Params &p, cudaStream_t stream)
+{
+    switch (p.D) {
+    case 64: return rows_typed<T, 64>(p, stream);
+    case 128: return rows_typed<T, 128>(p, stream);
+    default: return rows_typed<T, 256>(p, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append_q8(const AppendQ8Params &p, bool bf16, cudaStream_t stream)
+{
+    const cudaError_t e =
+        launch_pdl(append_q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (e != cudaSuccess) return e;
+    return bf16 ? rows_dims<__nv_bfloat16>(p, stream) : rows_dims<float>(p, stream);
+}
+
+}  // namespace kvc

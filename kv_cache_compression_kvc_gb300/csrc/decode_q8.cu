@@ -1,0 +1,758 @@
+// decode_q8.cu -- attention of one new token per sequence over pages of e4m3 numbers with a scale for
+// each page and head.
+//
+//   x_j = scale * ks(j) * (q . k8_j),   out = sum_j softmax(x)_j vs(j) v8_j,
+//   ks(j), vs(j): the key and value scales of token j's page for this head.
+//
+// What bounds it is the stream of the cache: one byte an element, 4 G operations for the G query heads
+// that share it, far below the ridge.  So everything is arranged around bytes in flight:
+//   A warp works alone.  It owns an equal share of the steps (16 slots of one (sequence, KV head,
+//   row tile)) of the whole batch and keeps kStages steps in flight in its own ring in shared memory
+//   (cp.async, 16 bytes a lane; rows behind the length are filled with zeros, whatever the page
+//   holds there).  No barrier between warps, no wait that could fail to end: a warp waits for its own
+//   copies only.
+//   Both products run on mma.m16n8k16 with the cache as the 16-row operand and the query heads as the 8
+//   columns, so that up to 8 heads waste nothing: S^T = K Q^T, O^T = V^T P^T.  (5th-generation
+//   products want 64 or 128 rows of one operand and, of 8-bit operands, both in 8 bits; the stream
+//   leaves the legacy pipe four fifths idle.)  e4m3 numbers are exact in fp16, so K and V enter
+//   the products as they are stored; a fragment's 16 bytes of one row are 4 steps of the
+//   product's inner dimension, which may be dealt out in any order as long as Q is dealt out alike.
+//   Queries are brought to [2^14, 2^15) by a power of two per row: bf16 then is exact in fp16 down to
+//   2^-31 of the row's largest element.  fp32 queries become two fp16 terms (22 bits), and so do their
+//   weights; with bf16 queries, whose outputs are rounded to 8 bits, weights are rounded once to 11.
+//   Weights carry the value scale: w_j = 2^(x_j + log2 vs(j) - M) with a running maximum M of its
+//   own, so that pages whose values differ by any factor meet on equal terms; the softmax's sum l and its
+//   maximum m are kept beside it.  All sums are fp32.
+//
+// The range of a warp is found on the device (a scan of the lengths), even however ragged the batch
+// is.  A row that crosses ranges leaves partial states (m, l, M, O) in the workspace; decode_q8_merge_kernel
+// joins them in order of the ranges, so results do not depend on timing.
+#include <algorithm>
+#include <type_traits>
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kStep = 16;                    // slots of a step
+constexpr int kEnd = 2;                      // steps that the end of a row tile counts as
+constexpr int kWholeSteps = 8;               // rows of so many steps are not split
+constexpr int kMinUnits = 4;                 // units that a range is worth at least
+constexpr float kSlack = 8.f;                // a maximum rises when it is passed by 2^8
+constexpr float kBoost = 6.f;                // weights are held times 2^6: at most 2^15, exact down to 2^-20
+constexpr float kNone = -3.402823466e38f;    // a maximum of nothing
+constexpr int kDevBadLen_ = 5;
+constexpr int kDevBadBlk_ = 9;
+
+template <int D, int NT, bool SPLIT>
+struct Q8Plan {
+    static constexpr int WARPS = 8;
+    static constexpr int BLOCKS = D <= 128 && NT == 1 && !SPLIT ? 2 : 1;    // per SM (registers)
+    static constexpr int STAGE = 2 * kStep * D + 32;     // keys, values, the two scales, what they are of
+    static constexpr int ROOM = (BLOCKS == 2 ? 112 : 224) * 1024 / WARPS;
+    static constexpr int FIT = ROOM / STAGE;
+    static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+    static constexpr int SMEM = WARPS * STAGES * STAGE;
+};
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two)
+{
+    uint32_t r;
+    asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ void mma_16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t x)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+__device__ __forceinline__ void cp_16(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds_16(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds_8(uint32_t a)
+{
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+
+// Slots of sequence b, clamped to the table, and its steps (one for an empty one, which has rows to write).
+__device__ __forceinline__ int len_of(const DecodeQ8Params &p, int b)
+{
+    const int n = p.len[b];
+    return n < 0 ? 0 : (n > p.cap ? p.cap : n);
+}
+__device__ __forceinline__ int steps_of(int len) { return len > 0 ? (len + kStep - 1) / kStep : 1; }
+
+// A warp's share of the units: every row tile counts its steps and kEnd.  Called by a whole warp.
+struct Range {
+    int b, hr, off, len;         // the first row tile: sequence, head * RT + tile, first unit in it, slots
+    long long t0, left;          // first unit and number of units
+    long long q;                 // units of a range, one more in the first r
+    long long r;
+    __device__ __forceinline__ int range_of(long long t) const
+    {
+        const long long big = r * (q + 1);
+        return (int)(t < big ? t / (q + 1) : r + (t - big) / q);
+    }
+};
+__device__ __forceinline__ Range find_range(const DecodeQ8Params &p, int w, bool check)
+{
+    const int lane = threadIdx.x & 31;
+    const int per = (p.B + 31) >> 5;
+    const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = p.len[b];
+        if (check && (n < 0 || n > p.cap)) record_code(p.dev_code, kDevBadLen_);
+        sum += (long long)(steps_of(n < 0 ? 0 : min(n, p.cap)) + kEnd) * p.HR;
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    const long long T = __shfl_sync(0xffffffffu, incl, 31);
+    Range g;
+    if (p.whole) {               // whole row tiles, equally many a range
+        const long long tiles = (long long)p.B * p.HR, i0 = tiles * w / p.ranges, i1 = tiles * (w + 1) / p.ranges;
+        g.b = (int)(i0 / p.HR);
+        g.hr = (int)(i0 - (long long)g.b * p.HR);
+        g.off = 0;
+        g.len = i0 < i1 ? len_of(p, g.b) : 0;
+        g.t0 = g.q = g.r = g.left = 0;
+        for (long long i = i0; i < i1; ++i) g.left += steps_of(len_of(p, (int)(i / p.HR))) + kEnd;
+        return g;
+    }
+    long long ranges = T / p.min_units;      // each is worth a few steps
+    ranges = ranges < 1 ? 1 : (ranges > p.ranges ? p.ranges : ranges);
+    if (T <= 0x7fffffffLL) {     // (a 64-bit division is a long subroutine)
+        const unsigned t = (unsigned)T, c = (unsigned)ranges;
+        g.q = t / c;
+        g.r = t - t / c * c;
+    } else {
+        g.q = T / ranges;
+        g.r = T - g.q * ranges;
+    }
+    g.b = g.hr = g.off = g.len = 0;
+    g.t0 = w * g.q + (w < g.r ? w : g.r);
+    g.left = w < ranges ? g.q + (w < g.r ? 1 : 0) : 0;
+    const long long before = incl - sum;
+    const bool here = g.left > 0 && before <= g.t0 && g.t0 < incl;
+    int b = b0, hr = 0, off = 0, len = 0;
+    if (here) {
+        long long t = before;
+        long long cost = 0;
+        for (;; ++b) {
+            len = len_of(p, b);
+            cost = steps_of(len) + kEnd;
+            if (g.t0 < t + cost * p.HR || b == b1 - 1) break;
+            t += cost * p.HR;
+        }
+        hr = (int)((g.t0 - t) / cost);
+        off = (int)(g.t0 - t - hr * cost);
+    }
+    const int src = (__ffs(__ballot_sync(0xffffffffu, here)) - 1) & 31;
+    g.b = __shfl_sync(0xffffffffu, b, src);
+    g.hr = __shfl_sync(0xffffffffu, hr, src);
+    g.off = __shfl_sync(0xffffffffu, off, src);
+    g.len = __shfl_sync(0xffffffffu, len, src);
+    return g;
+}
+
+// The steps of a range in order.
+struct Walk {
+    int b, hr, step, len, n;     // the step: row tile (b, hr), its number, the tile's slots and steps
+    long long left;              // units of the range left, this step's among them
+    __device__ __forceinline__ Walk(const DecodeQ8Params &p, const Range &g)
+        : b(g.b), hr(g.hr), step(g.off), len(g.len), n(steps_of(g.len)), left(g.left)
+    {
+        settle(p);
+    }
+    // Moves past a tile's end units to a step, if one is left.
+    __device__ __forceinline__ void settle(const DecodeQ8Params &p)
+    {
+        while (left > 0 && step >= n) {
+            left -= n + kEnd - step;
+            step = 0;
+            if (++hr == p.HR) {
+                hr = 0;
+                if (++b == p.B) {
+                    left = 0;
+                    return;
+                }
+                len = len_of(p, b);
+                n = steps_of(len);
+            }
+        }
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next(const DecodeQ8Params &p)
+    {
+        ++step;
+        --left;
+        settle(p);
+    }
+};
+
+template <int D, int NT, bool SPLIT>
+__global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT, SPLIT>::BLOCKS)
+    decode_q8_kernel(const DecodeQ8Params p)
+{
+    using PL = Q8Plan<D, NT, SPLIT>;
+    using T = typename std::conditional<SPLIT, float, __nv_bfloat16>::type;
+    constexpr int CPR = D / 16;              // 16-byte chunks of a row
+    constexpr int KC = D / 64;               // chunks of a key row that a lane takes
+    constexpr int KS = D / 16;               // steps of the first product's inner dimension
+    constexpr int DT = D / 16;               // 16-dim tiles of the output
+    constexpr int VB = D == 64 ? 8 : 16;     // bytes of a value row that a lane takes at once
+    constexpr int VC = D == 256 ? 2 : 1;     // how often
+    constexpr int S = PL::STAGES;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_addr(smem) + warp * (S * PL::STAGE);
+    // neighbouring ranges on different SMs: a small batch is spread over all of them
+    const int w = warp * gridDim.x + blockIdx.x;
+    pdl_trigger();
+    pdl_wait();
+    const Range range = find_range(p, w, w == 0);
+    bool noted = false;                      // a row tile begins here and ends in a later range
+
+    // ---- copies: one step ahead by step into the ring ----
+    Walk ld(p, range);
+    int page_at = -1, pages = 0;             // the 32 table entries in this warp's lanes: first one's number
+    int ld_b = -1;
+    const int32_t *tab = p.table;
+    auto fetch = [&](int slot) {
+        const uint32_t st = ring + slot * PL::STAGE;
+        if (ld.more()) {
+            const int pos = ld.step * kStep, lb = p.magic != 0 ? (int)__umulhi((unsigned)ld.step, p.magic) : ld.step;
+            if (ld.b != ld_b || lb < page_at || lb >= page_at + 32) {
+                ld_b = ld.b;
+                page_at = lb & ~31;
+                tab = p.table + (size_t)ld.b * p.max_blocks;
+                pages = page_at + lane < p.max_blocks ? __ldg(tab + page_at + lane) : 0;
+            }
+            int id = __shfl_sync(0xffffffffu, pages, lb - page_at);
+            const int valid = min(kStep, ld.len - pos);      // 0 of an empty sequence
+            if (id < 0 || id >= p.n_pool) {
+                if (valid > 0 && lane == 0) record_code(p.dev_code, kDevBadBlk_);
+                id = 0;
+            }
+            const size_t page = (size_t)(ld.hr / p.RT) * p.n_pool + id;
+            const size_t at = (page * p.bs + (pos - lb * p.bs)) * D;
+            const uint8_t *k = p.k + at, *v = p.v + at;
+#pragma unroll
+            for (int i = 0; i < CPR / 2; ++i) {
+                const int x = i * 32 + lane, row = x / CPR, c = x % CPR;
+                const bool ok = row < valid;
+                const int ck = D == 64 ? c : c ^ ((row & 1) << 2);
+                const int cv = D == 64 ? c ^ ((row >> 1 & 1) << 1) : c ^ ((row >> 1 & 3) << 1);
+                cp_16(st + row * D + ck * 16, k + x * 16, ok);
+                cp_16(st + kStep * D + row * D + cv * 16, v + x * 16, ok);
+            }
+            if (lane < 2) cp_4(st + 2 * kStep * D + lane * 4, (lane == 0 ? p.ks : p.vs) + page);
+            if (lane == 0) {
+                const uint32_t m = st + 2 * kStep * D + 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(m), "r"(ld.b), "r"(ld.hr), "r"(ld.step),
+                             "r"(ld.len)
+                             : "memory");
+            }
+            ld.next(p);
+        } else if (lane == 0) {
+            const uint32_t m = st + 2 * kStep * D + 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(m), "r"(-1), "r"(0), "r"(0), "r"(0)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < S - 1; ++i) fetch(i);
+
+    // ---- the row tile being worked on ----
+    uint32_t bq[NT][KS][2], bl[SPLIT ? NT : 1][SPLIT ? KS : 1][2];
+    float fq[NT][2];                         // row 2t, 2t + 1: the query's power of two times scale
+    float o[DT][NT][4];
+    float m[NT][2], mv[NT][2], l[NT][2];
+    int cur_b = -1, cur_hr = -1, cur_len = 0, cur_n = 0, first_step = 0, parts = 0;
+
+    auto begin = [&](int b, int hr) {
+        const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = r0 + nt * 8 + g;
+            const T *q = static_cast<const T *>(p.q) + ((size_t)b * p.Hq + h * p.G + row) * D;
+            float x[KC][16];
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                if (row < p.G) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(q + (t + 4 * c) * 16);
+#pragma unroll
+                    for (int j = 0; j < (SPLIT ? 4 : 2); ++j) {
+                        const uint4 y = __ldg(src + j);
+                        if constexpr (SPLIT) {
+                            x[c][4 * j] = __uint_as_float(y.x); x[c][4 * j + 1] = __uint_as_float(y.y);
+                            x[c][4 * j + 2] = __uint_as_float(y.z); x[c][4 * j + 3] = __uint_as_float(y.w);
+                        } else {
+                            x[c][8 * j] = bf16_lo(y.x); x[c][8 * j + 1] = bf16_hi(y.x);
+                            x[c][8 * j + 2] = bf16_lo(y.y); x[c][8 * j + 3] = bf16_hi(y.y);
+                            x[c][8 * j + 4] = bf16_lo(y.z); x[c][8 * j + 5] = bf16_hi(y.z);
+                            x[c][8 * j + 6] = bf16_lo(y.w); x[c][8 * j + 7] = bf16_hi(y.w);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[c][j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) big = fmaxf(big, fabsf(x[c][j]));
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            int e = (int)(__float_as_uint(big) >> 23) - 127;
+            e = big == 0.f ? 14 : (e < -112 ? -112 : e);
+            const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+            const float down = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float a = x[c][4 * j + 2 * u] * up, d = x[c][4 * j + 2 * u + 1] * up;
+                        const uint32_t hi = pack_h2(a, d);
+                        bq[nt][c * 4 + j][u] = hi;
+                        if constexpr (SPLIT) {
+                            const float2 y = unpack_h2(hi);
+                            bl[nt][c * 4 + j][u] = pack_h2(a - y.x, d - y.y);
+                        }
+                    }
+            fq[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t) * p.scale;
+            fq[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                m[nt][r] = mv[nt][r] = kNone;
+                l[nt][r] = 0.f;
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[d][nt][r] = 0.f;
+        }
+    };
+    // Outputs of the row tile, or its partial state.
+    auto finish = [&](int b, int hr, int lo, int hi, int n) {
+        const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8;
+        const bool whole = lo == 0 && hi == n;
+        const size_t part = (size_t)w * 2 + (parts > 0 ? 1 : 0);
+        if (!p.whole && lo == 0 && (p.by_tile || !whole) && lane == 0) {
+            // the tile's last step lies n - hi steps behind this range's end
+            const int tile = b * p.HR + hr;
+            p.ws_note[p.by_tile ? tile : w] =
+                whole ? make_int4(-1, 0, 0, 0)
+                      : make_int4(tile, w, range.range_of(range.t0 + range.left + (n - hi) - 1), parts > 0 ? 1 : 0);
+            noted = true;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float sum = l[nt][r];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                const int row = nt * 8 + 2 * t + r;
+                if (r0 + row >= p.G) continue;
+                const size_t out_row = (size_t)b * p.Hq + h * p.G + r0 + row;
+                float f = 1.f;
+                if (whole) {
+                    f = sum == 0.f ? 0.f : ex2(mv[nt][r] - kBoost - m[nt][r]) / sum;
+                    if (g == 0 && p.lse != nullptr)
+                        p.lse[out_row] = sum == 0.f ? -INFINITY : (m[nt][r] + log2f(sum)) * kLn2;
+                } else if (g == 0) {
+                    reinterpret_cast<float4 *>(p.ws_ml)[part * p.RP + row] =
+                        make_float4(m[nt][r], sum, mv[nt][r], 0.f);
+                }
+#pragma unroll
+                for (int c = 0; c < VC; ++c) {
+                    // VB consecutive dims of this row: tiles c * 8 .., a pair of dims each
+                    const int d0 = (g + 8 * c) * VB;
+                    float y[VB];
+#pragma unroll
+                    for (int i = 0; i < VB / 2; ++i) {
+                        y[2 * i] = o[c * 8 + i][nt][r] * f;
+                        y[2 * i + 1] = o[c * 8 + i][nt][2 + r] * f;
+                    }
+                    if (!whole || SPLIT) {
+                        float *dst = whole ? static_cast<float *>(p.out) + out_row * D + d0
+                                           : p.ws_o + (part * p.RP + row) * D + d0;
+#pragma unroll
+                        for (int i = 0; i < VB; i += 4)
+                            *reinterpret_cast<float4 *>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                    } else {
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + out_row * D + d0;
+#pragma unroll
+                        for (int i = 0; i < VB; i += 8) {
+                            uint32_t z[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const __nv_bfloat162 two = __floats2bfloat162_rn(y[i + 2 * j], y[i + 2 * j + 1]);
+                                z[j] = *reinterpret_cast<const uint32_t *>(&two);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(z[0], z[1], z[2], z[3]);
+                        }
+                    }
+                }
+            }
+        ++parts;
+    };
+
+    int slot = 0, put = S - 1;
+#pragma unroll 1
+    for (;;) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        __syncwarp();                        // the step is there for every lane, and the one before is used up
+        fetch(put);
+        put = put + 1 == S ? 0 : put + 1;
+        const uint32_t st = ring + slot * PL::STAGE;
+        const uint4 what = lds_16(st + 2 * kStep * D + 16);
+        const uint2 scales = lds_8(st + 2 * kStep * D);
+        const int b = (int)what.x, hr = (int)what.y, step = (int)what.z, len = (int)what.w;
+        if (b != cur_b || hr != cur_hr) {
+            if (cur_b >= 0) finish(cur_b, cur_hr, first_step, first_step + cur_n, steps_of(cur_len));
+            if (b < 0) break;
+            cur_b = b;
+            cur_hr = hr;
+            cur_len = len;
+            cur_n = 0;
+            first_step = step;
+            begin(b, hr);
+        }
+        ++cur_n;
+        const int pos = step * kStep, valid = min(kStep, len - pos);
+        // (an empty sequence's step has no page, and any scale)
+        const float sk = __uint_as_float(scales.x), sv = valid > 0 ? __uint_as_float(scales.y) : 1.f;
+
+        // ---- S^T = K Q^T: slots g and g + 8 of the step, rows 2t and 2t + 1 of the tile ----
+        float c[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[nt][i >> 2][i & 3] = 0.f;
+#pragma unroll
+        for (int h = 0; h < KC; ++h) {
+            const int ch = t + 4 * h, sw = D == 64 ? ch : ch ^ ((g & 1) << 2);
+            const uint4 ka = lds_16(st + g * D + sw * 16), kb = lds_16(st + (g + 8) * D + sw * 16);
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a[4] = {cvt_e4m3x2(wa[j]), cvt_e4m3x2(wb[j]), cvt_e4m3x2(wa[j] >> 16),
+                                       cvt_e4m3x2(wb[j] >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_16816(c[nt][j & 1], a, bq[nt][h * 4 + j][0], bq[nt][h * 4 + j][1]);
+                    if constexpr (SPLIT) mma_16816(c[nt][j & 1], a, bl[nt][h * 4 + j][0], bl[nt][h * 4 + j][1]);
+                }
+            }
+        }
+        // ---- softmax ----
+        // the value scale as 2^ev * fv, fv in [1, 2)
+        int ev = (int)((__float_as_uint(sv) >> 23) & 255u) - 127;
+        ev = ev < -126 ? -126 : (ev > 126 ? 126 : ev);
+        const float fv = sv * __uint_as_float((uint32_t)(127 - ev) << 23);
+        const float evf = (float)ev;
+        const bool in0 = g < valid, in1 = g + 8 < valid;
+        float x[NT][4];                      // log2 units: (slot g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
+        bool rise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float f0 = fq[nt][0] * sk, f1 = fq[nt][1] * sk;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[nt][i] = (c[nt][0][i] + c[nt][1][i]) * (i & 1 ? f1 : f0);
+            if (p.logits != nullptr) {
+                const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8 + nt * 8 + 2 * t;
+                float *dst = p.logits + ((size_t)b * p.Hq + h * p.G + r0) * p.logits_stride + pos + g;
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    if (r0 + r < p.G) {
+                        if (in0) dst[r * p.logits_stride] = x[nt][r];
+                        if (in1) dst[r * p.logits_stride + 8] = x[nt][2 + r];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[nt][i] = (i < 2 ? in0 : in1) ? x[nt][i] * kLog2e : -INFINITY;
+                rise |= x[nt][i] > m[nt][i & 1] + kSlack || x[nt][i] + evf > mv[nt][i & 1] + kSlack;
+            }
+        }
+        if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float y = fmaxf(x[nt][r], x[nt][2 + r]);
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                    const float m1 = fmaxf(m[nt][r], y), v1 = fmaxf(mv[nt][r], y + evf);
+                    l[nt][r] *= ex2(m[nt][r] - m1);
+                    const float f = ex2(mv[nt][r] - v1);
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        o[d][nt][r] *= f;
+                        o[d][nt][2 + r] *= f;
+                    }
+                    m[nt][r] = m1;
+                    mv[nt][r] = v1;
+                }
+        }
+        uint32_t pw[NT][2], pl[SPLIT ? NT : 1][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                l[nt][i & 1] += ex2(x[nt][i] - m[nt][i & 1]);
+                y[i] = ex2(x[nt][i] - mv[nt][i & 1] + (evf + kBoost)) * fv;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t hi = pack_h2(y[2 * i], y[2 * i + 1]);
+                pw[nt][i] = transpose_8x8(hi);
+                if constexpr (SPLIT) {
+                    const float2 z = unpack_h2(hi);
+                    pl[nt][i] = transpose_8x8(pack_h2(y[2 * i] - z.x, y[2 * i + 1] - z.y));
+                }
+            }
+        }
+        // ---- O^T += V^T P^T: slots 2t, 2t + 1, 2t + 8, 2t + 9 of VB dims ----
+        const uint32_t sv_base = st + kStep * D;
+#pragma unroll
+        for (int vc = 0; vc < VC; ++vc) {
+            uint32_t r[4][VB / 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 2 * t + (i & 1) + (i >> 1) * 8;
+                if constexpr (VB == 16) {
+                    const int ch = (g + 8 * vc) ^ (t << 1);
+                    const uint4 y = lds_16(sv_base + row * D + ch * 16);
+                    r[i][0] = y.x; r[i][1] = y.y; r[i][2] = y.z; r[i][3] = y.w;
+                } else {
+                    const int ch = (g >> 1) ^ ((t & 1) << 1);
+                    const uint2 y = lds_8(sv_base + row * D + ch * 16 + (g & 1) * 8);
+                    r[i][0] = y.x; r[i][1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < VB / 4; ++q)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t lo = __byte_perm(r[0][q], r[1][q], u ? 0x7362 : 0x5140);
+                    const uint32_t hi = __byte_perm(r[2][q], r[3][q], u ? 0x7362 : 0x5140);
+                    const uint32_t a[4] = {cvt_e4m3x2(lo), cvt_e4m3x2(lo >> 16), cvt_e4m3x2(hi),
+                                           cvt_e4m3x2(hi >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(o[vc * 8 + q * 2 + u][nt], a, pw[nt][0], pw[nt][1]);
+                        if constexpr (SPLIT) mma_16816(o[vc * 8 + q * 2 + u][nt], a, pl[nt][0], pl[nt][1]);
+                    }
+                }
+        }
+        slot = slot + 1 == S ? 0 : slot + 1;
+    }
+    if (!p.whole && !p.by_tile && !noted && lane == 0) p.ws_note[w] = make_int4(-1, 0, 0, 0);
+}
+
+// Joins the parts of a split row tile, a row a block, 4 columns a thread.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) decode_q8_merge_kernel(const DecodeQ8Params p)
+{
+    constexpr int LPR = D / 4;               // threads of a row
+    __shared__ float2 s_c[128];
+    pdl_trigger();
+    pdl_wait();
+    const int4 note = p.ws_note[blockIdx.x];
+    if (note.x < 0) return;
+    const int b = note.x / p.HR, hr = note.x - b * p.HR, h = hr / p.RT, r0 = (hr - h * p.RT) * p.RP;
+    const int w0 = note.y, nseg = note.z - w0 + 1;
+    const int rows = min(p.RP, p.G - r0);
+    auto part_of = [&](int i) -> size_t { return (size_t)(w0 + i) * 2 + (i == 0 ? note.w : 0); };
+    const int row = blockIdx.y;
+    if (row >= rows) return;
+    // the tile's maxima, then each part's factors, 128 parts at a time
+    const int tid = threadIdx.x, lane = tid & 31;
+    const float4 *ml = reinterpret_cast<const float4 *>(p.ws_ml);
+    float m = kNone, mv = kNone;
+    for (int i = lane; i < nseg; i += 32) {
+        const float4 y = __ldcg(ml + part_of(i) * p.RP + row);
+        m = fmaxf(m, y.x);
+        mv = fmaxf(mv, y.z);
+    }
+    m = warp_max(m);
+    mv = warp_max(mv);
+    constexpr int SETS = 128 / LPR;          // D = 256 takes the row in 64 threads, two sets of parts
+    const int set = tid / LPR, col = tid % LPR * 4;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < nseg; i0 += 128) {
+        __syncthreads();
+        if (i0 + tid < nseg) {
+            const float4 y = __ldcg(ml + part_of(i0 + tid) * p.RP + row);
+            s_c[tid] = make_float2(ex2(y.z - mv), y.y * ex2(y.x - m));
+        }
+        __syncthreads();
+        const int here = min(128, nseg - i0);
+#pragma unroll 4
+        for (int i = set; i < here; i += SETS) {
+            const float2 c = s_c[i];
+            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + (part_of(i0 + i) * p.RP + row) * D + col));
+            l += c.y;
+            o.x = fmaf(c.x, y.x, o.x);
+            o.y = fmaf(c.x, y.y, o.y);
+            o.z = fmaf(c.x, y.z, o.z);
+            o.w = fmaf(c.x, y.w, o.w);
+        }
+    }
+    __shared__ float4 s_o[128];
+    __shared__ float s_l[SETS];
+    s_o[tid] = o;
+    if (tid % LPR == 0) s_l[set] = l;
+    __syncthreads();
+    if (set != 0) return;
+    l = s_l[0];
+#pragma unroll
+    for (int s = 1; s < SETS; ++s) {
+        const float4 y = s_o[s * LPR + tid];
+        l += s_l[s];
+        o.x += y.x;
+        o.y += y.y;
+        o.z += y.z;
+        o.w += y.w;
+    }
+    const size_t out_row = (size_t)b * p.Hq + h * p.G + r0 + row;
+    const float f = l == 0.f ? 0.f : ex2(mv - kBoost - m) / l;
+    if (tid == 0 && p.lse != nullptr) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    T *dst = static_cast<T *>(p.out) + out_row * D + col;
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(dst) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * f, o.y * f), c = __floats2bfloat162_rn(o.z * f, o.w * f);
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+    }
+}
+
+template <int D, int NT, bool SPLIT>
+cudaError_t launch_typed(DecodeQ8Params p, cudaStream_t stream)
+{
+    using PL = Q8Plan<D, NT, SPLIT>;
+    using T = typename std::conditional<SPLIT, float, __nv_bfloat16>::type;
+    static_assert(PL::STAGES >= 3, "two steps in flight at least");
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !configured[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D, NT, SPLIT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, PL::SMEM);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    // no more blocks than the capacity can give work
+    const long long tiles = (long long)p.B * p.HR, most = (p.cap + kStep - 1) / kStep + kEnd;
+    const long long ranges = p.whole ? tiles : tiles * most / p.min_units + 1;
+    const long long blocks = std::min<long long>(p.ranges / PL::WARPS, (ranges + PL::WARPS - 1) / PL::WARPS);
+    // few ranges: one a block, so that they spread over the SMs
+    const int grid = (int)std::max<long long>(1, std::min<long long>(p.ranges / PL::WARPS, std::max(blocks, std::min<long long>(ranges, p.n_sm))));
+    p.ranges = grid * PL::WARPS;
+    cudaError_t e = launch_pdl(decode_q8_kernel<D, NT, SPLIT>, dim3((unsigned)grid), dim3(PL::WARPS * 32), PL::SMEM,
+                               stream, p);
+    if (e != cudaSuccess || p.whole) return e;
+    return launch_pdl(decode_q8_merge_kernel<T, D>, dim3((unsigned)(p.by_tile ? tiles : p.ranges), (unsigned)p.RP),
+                      dim3(128), 0, stream, p);
+}
+
+}  // namespace
+
+// Row tiles of 8 heads, of 16 where a group has more and registers allow it.
+static int tiles_of_8(int G, int D, bool bf16) { return G > 8 && D <= 128 && bf16 ? 2 : 1; }
+
+DecodeQ8Plan decode_q8_plan(int B, int Hkv, int G, int D, bool bf16, int n_sm)
+{
+    DecodeQ8Plan pl{};
+    const int NT = tiles_of_8(G, D, bf16);
+    pl.RT = (G + 8 * NT - 1) / (8 * NT);
+    pl.RP = G < 8 * NT ? G : 8 * NT;
+    const bool two = D <= 128 && NT == 1 && bf16;        // blocks per SM, as Q8Plan says
+    pl.ranges = n_sm * (two ? 2 : 1) * 8;
+    const long long tiles = (long long)B * Hkv * pl.RT;
+    pl.by_tile = tiles <= pl.ranges;
+    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    const size_t states = (size_t)pl.ranges * 2 * pl.RP;
+    pl.off_note = 0;
+    pl.off_ml = up((size_t)pl.ranges * sizeof(int4));
+    pl.off_o = up(pl.off_ml + states * sizeof(float4));
+    pl.bytes = up(pl.off_o + states * D * sizeof(float));
+    return pl;
+}
+
+cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t stream)
+{
+    // Short rows are not split, and then nothing is joined.
+    p.whole = (p.cap + kStep - 1) / kStep <= kWholeSteps;
+    p.min_units = kMinUnits;
+    if (bf16) {
+        const bool wide = tiles_of_8(p.G, D, true) == 2;
+        switch (D) {
+        case 64: return wide ? launch_typed<64, 2, false>(p, stream) : launch_typed<64, 1, false>(p, stream);
+        case 128: return wide ? launch_typed<128, 2, false>(p, stream) : launch_typed<128, 1, false>(p, stream);
+        default: return launch_typed<256, 1, false>(p, stream);
+        }
+    }
+    switch (D) {
+    case 64: return launch_typed<64, 1, true>(p, stream);
+    case 128: return launch_typed<128, 1, true>(p, stream);
+    default: return launch_typed<256, 1, true>(p, stream);
+    }
+}
+
+}  // namespace kvc

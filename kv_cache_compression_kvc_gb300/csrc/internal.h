@@ -370,4 +370,98 @@ cudaError_t launch_latent_expand(const ExpandParams &p, int dtype, cudaStream_t 
 // made.
 cudaError_t launch_latent_expand_tc(const ExpandParams &p, cudaStream_t stream, bool *used);
 
+
+// ------------------------------------------------------------------------------------------
+// Norms and rotation of query and key heads.
+struct QkNormParams {
+    const void *q, *k;           // rows [n_tokens][heads][D], strides in elements
+    int64_t q_st, q_sh, k_st, k_sh;
+    void *q_out, *k_out;
+    int64_t qo_st, qo_sh, ko_st, ko_sh;
+    int32_t n_tokens, Hq, Hkv, rot;
+    const void *w_q, *w_k;       // nullable (no norm)
+    float eps;
+    const float *cos_sin;        // [n_pos][2][rot/2]; rot 0: no rotation
+    const int32_t *pos;          // [n_tokens]
+    int32_t n_pos;
+    int32_t tasks, q_tasks;      // warps per token, those of its queries (set by the launch)
+    int32_t *dev_code;
+};
+cudaError_t launch_qk_norm_rope(const QkNormParams &p, int D, bool bf16, cudaStream_t stream);
+
+// ------------------------------------------------------------------------------------------
+// Pages of e4m3 numbers with a scale for each page and head.
+struct AppendQ8Params {
+    uint8_t *k, *v;              // pool [H][n_pool][bs][D]
+    float *ks, *vs;              // [H][n_pool]
+    int32_t n_pool, H, bs, D, B, max_blocks;
+    int32_t *table, *n_blocks, *len;
+    float *score;
+    int32_t *free_ids, *free_top;
+    int32_t free_cap;
+    const void *k_new, *v_new;   // rows [n_tokens][H][D], strides in elements
+    int64_t new_st, new_sh;
+    const int32_t *cu;           // nullable (one row each); sequence b's rows are cu[b] .. cu[b + 1] - 1
+    int32_t n_tokens;
+    int32_t *appended;           // nullable [B]
+    int4 *jobs;                  // {page, rows held before, first new row, rows}
+    int32_t *n_jobs;
+    int32_t max_jobs;
+    int32_t *dev_code;
+};
+cudaError_t launch_paged_append_q8(const AppendQ8Params &p, bool bf16, cudaStream_t stream);
+
+struct DecodeQ8Params {
+    const void *q;               // [B][Hq][D], bf16 or fp32
+    const uint8_t *k, *v;        // pool [Hkv][n_pool][bs][D]
+    const float *ks, *vs;        // [Hkv][n_pool]
+    const int32_t *table, *len;
+    int32_t n_pool, bs, max_blocks, cap;
+    uint32_t magic;              // ceil(2^32 / (bs / 16)), 0 for pages of 16: a step's page by one product
+    int32_t B, Hq, G;
+    int32_t RT, RP, HR;          // row tiles of a head, rows of one, row tiles of a sequence
+    float scale;
+    void *out;                   // [B][Hq][D], q's type
+    float *logits;               // nullable
+    int64_t logits_stride;
+    float *lse;                  // nullable
+    int32_t ranges, min_units, whole, by_tile, n_sm;
+    int4 *ws_note;               // per row tile (by_tile) or range: {row tile or -1, first range, last, slot}
+    float *ws_ml;                // [ranges][2][RP] {m, l, maximum of the value weights, -}
+    float *ws_o;                 // [ranges][2][RP][D]
+    int32_t *dev_code;
+};
+struct DecodeQ8Plan {
+    int32_t RT, RP, ranges, by_tile;
+    size_t off_note, off_ml, off_o, bytes;
+};
+DecodeQ8Plan decode_q8_plan(int B, int Hkv, int G, int D, bool bf16, int n_sm);
+cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t stream);
+
+
+// ------------------------------------------------------------------------------------------
+// Pages shared between sequences, pools made dense.
+constexpr int kPagesMaxBatch = 8192;         // sequences that pages_reorder_kernel holds in shared memory
+struct PagesParams {
+    char *k, *v;                 // pool [H][n_pool][bs][row_bytes]
+    float *ks, *vs;              // nullable [H][n_pool]
+    int32_t n_pool, H, bs, row_bytes, B, max_blocks;
+    int32_t *table, *n_blocks, *len;
+    float *score;
+    int32_t *free_ids, *free_top;
+    int32_t free_cap;
+    int32_t *shares;             // [n_pool]; compaction: nullable
+    int32_t *pos;                // nullable [n_pool][bs]
+    const int32_t *parent;       // reorder: [B]
+    int32_t *remap;              // compaction: [n_pool]
+    int32_t *ws_n;               // copies, error, the blocks' counts
+    int32_t *ws_ids;             // reorder: [n_pool] freed pages; compaction: [3][n_pool]
+    int4 *ws_copies;             // {from, to, rows, -}: reorder [B], compaction [n_pool / 2]
+    int32_t *ws_table;           // reorder: [B][max_blocks]
+    float *ws_score;
+    int32_t *dev_code;
+};
+cudaError_t launch_pages_reorder(const PagesParams &p, int n_sm, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams &p, int n_sm, cudaStream_t stream);
+
 }  // namespace kvc

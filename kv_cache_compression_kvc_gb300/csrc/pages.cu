@@ -1,0 +1,432 @@
+// pages.cu -- pages held by several sequences, and pools made dense.
+//
+// Full pages are never written again, so sequences may share them: shares[x] counts the sequences
+// that hold page x beyond the first (0 for a page that one sequence holds, and for a free one).  Partly
+// filled pages belong to one sequence each; that is all that appends need to know, so those that pop
+// pages and write rows work on forked sequences as they are.
+//
+// pages_reorder_kernel: sequence b becomes a copy of what sequence parent[b] was, or is freed.  A
+// page that s sequences held is held afterwards by the sum of their children: every table entry adds
+// (children - 1) to its page's count, and a page that ends at -1 is free.  A partly filled page stays
+// with the sequence itself or its first child; the other children get a page of their own, copied by
+// pages_copy_kernel.  Free pages go on the stack in ascending order, copies take theirs from its top in
+// sequence order: results do not depend on timing.
+//
+// pages_compact_kernel: the k-th live page beyond the number of live pages moves to the k-th free page
+// below it; tables, counts and the stack follow.  No page is both read and written.
+//
+// Both tables' kernels are one cluster of 8 blocks with a few barriers (a page table is some 10^5
+// words, which one block would take 8 times as long over, and a launch per step would cost more than the
+// steps); what blocks tell each other goes through the workspace.  Bound by latency.  The copies are bound
+// by HBM: a page's keys and values of a head are one contiguous run each, 64 bytes a thread in flight.
+#include "common.cuh"
+#include "internal.h"
+
+namespace kvc {
+
+namespace {
+
+constexpr int kCl = 8;                       // blocks of the cluster
+constexpr int kThreads = 1024;
+constexpr int kAll = kCl * kThreads;
+constexpr int kCopyThreads_ = 256;
+constexpr int kBadIndex = 3, kBadLength = 5, kBadBlock = 9, kPoolEmpty = 10, kPoolOverflow = 11, kSharedPage = 12;
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// Also orders the cluster's global memory accesses.
+__device__ __forceinline__ void cluster_barrier()
+{
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Threads before this one (in order) whose flag is set, and how many are set in the block.
+__device__ __forceinline__ int block_rank(bool flag, int *s_warp, int *all)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t votes = __ballot_sync(0xffffffffu, flag);
+    __syncthreads();                         // (s_warp is free)
+    if (lane == 0) s_warp[warp] = __popc(votes);
+    __syncthreads();
+    int x = s_warp[lane];
+    const int own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    *all = __shfl_sync(0xffffffffu, x, 31);
+    return __shfl_sync(0xffffffffu, x - own, warp) + __popc(votes & ((1u << lane) - 1u));
+}
+
+// Calls f(b, i) for the entries i < n(b) of every sequence's table, 32 of one sequence a warp.
+template <typename N, typename F>
+__device__ __forceinline__ void each_entry(int B, int max_blocks, int rank, N n, F f)
+{
+    const int lane = threadIdx.x & 31, first = rank * (kThreads / 32) + (threadIdx.x >> 5);
+    const int per = (max_blocks + 31) / 32;
+    int b = first / per, c = first - b * per;
+    constexpr int kStride = kAll / 32;
+    const int db = kStride / per, dc = kStride - db * per;
+    while (b < B) {
+        const int i = c * 32 + lane;
+        if (i < n(b)) f(b, i);
+        b += db;
+        c += dc;
+        if (c >= per) {
+            c -= per;
+            ++b;
+        }
+    }
+}
+
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_reorder_kernel(const PagesParams p)
+{
+    extern __shared__ int s_seq[];           // per sequence: children, keeper, parent, blocks, length, copy
+    __shared__ int s_warp[32];
+    int *s_kids = s_seq, *s_keep = s_kids + p.B, *s_par = s_keep + p.B, *s_nb = s_par + p.B, *s_len = s_nb + p.B,
+        *s_copy = s_len + p.B;
+    const int tid = threadIdx.x, rank = (int)cluster_rank();
+    pdl_trigger();
+    pdl_wait();
+    // ---- the sequences, in every block alike ----
+    int code = 0;
+    const int top = *p.free_top;
+    if (top < 0 || top > p.free_cap) code = kPoolEmpty;
+    if (rank == 0 && tid == 0) {
+        p.ws_n[0] = 0;                       // copies
+        p.ws_n[1] = 0;                       // what is wrong
+    }
+    for (int b = tid; b < p.B; b += kThreads) {
+        const int par = p.parent[b], len = p.len[b], nb = p.n_blocks[b];
+        if (par < -1 || par >= p.B) code = kBadIndex;
+        if (len < 0 || len > p.max_blocks * p.bs || nb != (len + p.bs - 1) / p.bs) code = kBadLength;
+        s_kids[b] = 0;
+        s_keep[b] = 0x7fffffff;
+        s_par[b] = par;
+        s_nb[b] = nb;
+        s_len[b] = len;
+    }
+    const bool bad = __syncthreads_or(code != 0);
+    cluster_barrier();                       // (ws_n is there; no block has left)
+    if (bad) {
+        if (rank == 0 && code != 0) record_code(p.dev_code, code);
+        return;
+    }
+    for (int b = tid; b < p.B; b += kThreads) {
+        const int par = s_par[b];
+        if (par >= 0) {
+            atomicAdd(&s_kids[par], 1);
+            atomicMin(&s_keep[par], b);
+        }
+    }
+    __syncthreads();
+    for (int b = tid; b < p.B; b += kThreads)
+        if (s_par[b] == b) s_keep[b] = b;
+    __syncthreads();
+    int n_copies = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        bool own = false;
+        if (b < p.B) {
+            const int par = s_par[b];
+            own = par >= 0 && s_len[par] % p.bs != 0 && s_keep[par] != b;
+        }
+        int all;
+        const int r = block_rank(own, s_warp, &all);
+        if (b < p.B) s_copy[b] = own ? n_copies + r : -1;
+        n_copies += all;
+    }
+    __syncthreads();
+    auto partial = [&](int b, int i) { return s_len[b] % p.bs != 0 && i == s_nb[b] - 1; };
+    // ---- the tables' ids, of the sequences that change ----
+    auto touched = [&](int b) { return s_kids[b] == 1 && s_par[b] == b ? 0 : s_nb[b]; };
+    each_entry(p.B, p.max_blocks, rank, touched, [&](int b, int i) {
+        const int id = p.table[(size_t)b * p.max_blocks + i];
+        int c = 0;
+        if (id < 0 || id >= p.n_pool) c = kBadBlock;
+        else if (partial(b, i) && p.shares[id] != 0) c = kSharedPage;
+        if (c != 0) atomicCAS(&p.ws_n[1], 0, c);
+    });
+    cluster_barrier();
+    code = __ldcg(&p.ws_n[1]);
+    if (code != 0) {                         // nothing has changed yet
+        if (rank == 0 && tid == 0) record_code(p.dev_code, code);
+        return;
+    }
+    // ---- holders of every page ----
+    auto count = [&](int sign) {
+        each_entry(p.B, p.max_blocks, rank, [&](int b) { return s_kids[b] == 1 ? 0 : s_nb[b]; }, [&](int b, int i) {
+            if (s_kids[b] > 0 && partial(b, i)) return;
+            atomicAdd(&p.shares[p.table[(size_t)b * p.max_blocks + i]], sign * (s_kids[b] - 1));
+        });
+    };
+    count(1);
+    cluster_barrier();
+    const int x0 = (int)((long long)p.n_pool * rank / kCl), x1 = (int)((long long)p.n_pool * (rank + 1) / kCl);
+    int gone = 0;
+    for (int x = x0 + tid; x < x1; x += kThreads) {
+        const int s = __ldcg(&p.shares[x]);
+        gone += s < 0 ? 1 : 0;
+        if (s < -1) atomicCAS(&p.ws_n[1], 0, kBadBlock);       // held by more sequences than it counted
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) gone += __shfl_xor_sync(0xffffffffu, gone, o);
+    __syncthreads();
+    if ((tid & 31) == 0) s_warp[tid >> 5] = gone;
+    __syncthreads();
+    if (tid < 32) {
+        int x = s_warp[tid];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (tid == 0) p.ws_n[2 + rank] = x;
+    }
+    cluster_barrier();
+    int before = 0, n_gone = 0;
+#pragma unroll
+    for (int r = 0; r < kCl; ++r) {
+        const int x = __ldcg(&p.ws_n[2 + r]);
+        if (r < rank) before += x;
+        n_gone += x;
+    }
+    const int new_top = top + n_gone - n_copies;
+    code = __ldcg(&p.ws_n[1]);
+    if (code == 0 && new_top < 0) code = kPoolEmpty;
+    if (code == 0 && new_top > p.free_cap) code = kPoolOverflow;
+    if (code == 0)
+        for (int i = max(new_top, 0) + tid; i < top; i += kThreads) {
+            const int id = p.free_ids[i];
+            if (id < 0 || id >= p.n_pool) code = kBadBlock;
+        }
+    if (__syncthreads_or(code != 0)) {       // (the same in every block) counts as they were
+        if (rank == 0 && code != 0) record_code(p.dev_code, code);
+        count(-1);
+        return;
+    }
+    // ---- freed pages in ascending order; the tables as the children will have them ----
+    for (int c = x0; c < x1; c += kThreads) {
+        const int x = c + tid;
+        const bool free_now = x < x1 && __ldcg(&p.shares[x]) < 0;
+        int all;
+        const int r = before + block_rank(free_now, s_warp, &all);
+        if (free_now) {
+            p.shares[x] = 0;
+            p.ws_ids[r] = x;
+            if (top + r < new_top) p.free_ids[top + r] = x;
+        }
+        before += all;
+    }
+    auto moved = [&](int b) { return s_par[b] < 0 || s_par[b] == b ? 0 : s_nb[s_par[b]]; };
+    each_entry(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
+        const size_t from = (size_t)s_par[b] * p.max_blocks + i, to = (size_t)b * p.max_blocks + i;
+        p.ws_table[to] = p.table[from];
+        p.ws_score[to] = p.score[from];
+    });
+    cluster_barrier();
+    each_entry(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
+        const size_t at = (size_t)b * p.max_blocks + i;
+        int id = __ldcg(&p.ws_table[at]);
+        const int copy = s_copy[b];
+        if (copy >= 0 && i == s_nb[s_par[b]] - 1) {
+            const int place = top + n_gone - 1 - copy;
+            const int to = place >= top ? __ldcg(&p.ws_ids[place - top]) : p.free_ids[place];
+            p.ws_copies[copy] = make_int4(id, to, s_len[s_par[b]] % p.bs, 0);
+            id = to;
+        }
+        p.table[at] = id;
+        p.score[at] = __ldcg(&p.ws_score[at]);
+    });
+    if (rank == 0) {
+        for (int b = tid; b < p.B; b += kThreads) {
+            const int par = s_par[b];
+            if (par == b) continue;
+            p.n_blocks[b] = par < 0 ? 0 : s_nb[par];
+            p.len[b] = par < 0 ? 0 : s_len[par];
+        }
+        if (tid == 0) {
+            p.ws_n[0] = n_copies;
+            *p.free_top = new_top;
+        }
+    }
+}
+
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_compact_kernel(const PagesParams p)
+{
+    __shared__ int s_warp[32];
+    const int tid = threadIdx.x, rank = (int)cluster_rank(), all_tid = rank * kThreads + tid;
+    pdl_trigger();
+    pdl_wait();
+    const int top = *p.free_top;
+    int *mark = p.ws_ids, *holes = p.ws_ids + p.n_pool, *high = p.ws_ids + 2 * (size_t)p.n_pool;
+    if (all_tid == 0) {
+        p.ws_n[0] = 0;                       // moves
+        p.ws_n[1] = 0;                       // what is wrong
+    }
+    for (int x = all_tid; x < p.n_pool; x += kAll) mark[x] = 0;
+    cluster_barrier();
+    const bool bad_top = top < 0 || top > p.free_cap || top > p.n_pool;
+    if (bad_top) {
+        if (all_tid == 0) record_code(p.dev_code, kPoolEmpty);
+        return;
+    }
+    const int n_live = p.n_pool - top;
+    for (int i = all_tid; i < top; i += kAll) {
+        const int id = p.free_ids[i];
+        if (id < 0 || id >= p.n_pool || atomicExch(&mark[id], 1) != 0) atomicCAS(&p.ws_n[1], 0, kBadBlock);
+    }
+    cluster_barrier();
+    auto entries = [&](int b) {
+        const int n = p.n_blocks[b];
+        return n < 0 || n > p.max_blocks ? 0 : n;
+    };
+    each_entry(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
+        const int id = p.table[(size_t)b * p.max_blocks + i];
+        if (id < 0 || id >= p.n_pool || __ldcg(&mark[id]) != 0) atomicCAS(&p.ws_n[1], 0, kBadBlock);
+    });
+    for (int b = all_tid; b < p.B; b += kAll) {
+        const int n = p.n_blocks[b];
+        if (n < 0 || n > p.max_blocks) atomicCAS(&p.ws_n[1], 0, kBadLength);
+    }
+    // ---- free pages below the number of live ones, live pages beyond it: equally many ----
+    const int x0 = (int)((long long)p.n_pool * rank / kCl), x1 = (int)((long long)p.n_pool * (rank + 1) / kCl);
+    int n_hole = 0, n_high = 0;
+    for (int c = x0; c < x1; c += kThreads) {
+        const int x = c + tid;
+        const bool in = x < x1, free_page = in && __ldcg(&mark[x]) != 0;
+        n_hole += __syncthreads_count(free_page && x < n_live);
+        n_high += __syncthreads_count(in && !free_page && x >= n_live);
+    }
+    if (tid == 0) {
+        p.ws_n[2 + 2 * rank] = n_hole;
+        p.ws_n[3 + 2 * rank] = n_high;
+    }
+    cluster_barrier();
+    const int code = __ldcg(&p.ws_n[1]);
+    if (code != 0) {                         // nothing has changed yet
+        if (all_tid == 0) record_code(p.dev_code, code);
+        return;
+    }
+    int hole0 = 0, high0 = 0, moves = 0;
+#pragma unroll
+    for (int r = 0; r < kCl; ++r) {
+        const int a = __ldcg(&p.ws_n[2 + 2 * r]), b = __ldcg(&p.ws_n[3 + 2 * r]);
+        if (r < rank) {
+            hole0 += a;
+            high0 += b;
+        }
+        moves += a;
+    }
+    for (int c = x0; c < x1; c += kThreads) {
+        const int x = c + tid;
+        const bool in = x < x1, free_page = in && __ldcg(&mark[x]) != 0;
+        const bool hole = free_page && x < n_live, up = in && !free_page && x >= n_live;
+        int all;
+        int r = hole0 + block_rank(hole, s_warp, &all);
+        hole0 += all;
+        if (hole) holes[r] = x;
+        r = high0 + block_rank(up, s_warp, &all);
+        high0 += all;
+        if (up) high[r] = x;
+        else if (in) p.remap[x] = free_page ? -1 : x;
+    }
+    cluster_barrier();
+    for (int k = all_tid; k < moves; k += kAll) {
+        const int from = __ldcg(&high[k]), to = __ldcg(&holes[k]);
+        p.ws_copies[k] = make_int4(from, to, p.bs, 0);
+        p.remap[from] = to;
+        if (p.shares != nullptr) {
+            p.shares[to] = p.shares[from];
+            p.shares[from] = 0;
+        }
+    }
+    // the stack hands out the lowest free page first
+    for (int i = all_tid; i < top; i += kAll) p.free_ids[i] = p.n_pool - 1 - i;
+    if (all_tid == 0) p.ws_n[0] = moves;
+    cluster_barrier();
+    each_entry(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
+        int32_t *e = p.table + (size_t)b * p.max_blocks + i;
+        *e = __ldcg(&p.remap[*e]);
+    });
+}
+
+// Job (copy c, head h): rows of keys and values from page to page, with their scales; head 0 takes the
+// tokens' positions along.
+__global__ void __launch_bounds__(kCopyThreads_) pages_copy_kernel(const PagesParams p)
+{
+    pdl_trigger();
+    pdl_wait();
+    const long long jobs = (long long)*p.ws_n * p.H;
+    const size_t page_bytes = (size_t)p.bs * p.row_bytes;
+    for (long long j = blockIdx.x; j < jobs; j += gridDim.x) {
+        const int c = (int)(j / p.H), h = (int)(j - (long long)c * p.H);
+        const int4 what = p.ws_copies[c];
+        const size_t from = (size_t)h * p.n_pool + what.x, to = (size_t)h * p.n_pool + what.y;
+        const int n = what.z * (p.row_bytes / 16);         // vectors of keys, then as many of values
+        constexpr int U = 4;
+        for (int i0 = threadIdx.x; i0 < 2 * n; i0 += kCopyThreads_ * U) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kCopyThreads_;
+                if (i < 2 * n)
+                    x[u] = ld_stream_16((i < n ? p.k : p.v) + from * page_bytes + (size_t)(i < n ? i : i - n) * 16);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * kCopyThreads_;
+                if (i < 2 * n)
+                    *reinterpret_cast<uint4 *>((i < n ? p.k : p.v) + to * page_bytes +
+                                               (size_t)(i < n ? i : i - n) * 16) = x[u];
+            }
+        }
+        if (threadIdx.x == 0 && p.ks != nullptr) {
+            p.ks[to] = p.ks[from];
+            p.vs[to] = p.vs[from];
+        }
+        if (h == 0 && p.pos != nullptr)
+            for (int i = threadIdx.x; i < what.z; i += kCopyThreads_)
+                p.pos[(size_t)what.y * p.bs + i] = p.pos[(size_t)what.x * p.bs + i];
+    }
+}
+
+// `copies`: the most that there can be.
+cudaError_t launch_copies(const PagesParams &p, long long copies, int n_sm, cudaStream_t stream)
+{
+    const long long jobs = copies * p.H, most = (long long)n_sm * 8;
+    const long long blocks = jobs < 1 ? 1 : (jobs < most ? jobs : most);
+    return launch_pdl(pages_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads_), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_reorder(const PagesParams &p, int n_sm, cudaStream_t stream)
+{
+    const size_t smem = (size_t)p.B * 6 * sizeof(int);
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !configured[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            pages_reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagesMaxBatch * 6 * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    const cudaError_t e = launch_pdl(pages_reorder_kernel, dim3(kCl), dim3(kThreads), smem, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_copies(p, p.B, n_sm, stream);
+}
+
+cudaError_t launch_pages_compact(const PagesParams &p, int n_sm, cudaStream_t stream)
+{
+    const cudaError_t e = launch_pdl(pages_compact_kernel, dim3(kCl), dim3(kThreads), 0, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_copies(p, p.n_pool / 2, n_sm, stream);
+}
+
+}  // namespace kvc

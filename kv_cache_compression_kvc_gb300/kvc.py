@@ -18,7 +18,7 @@ import torch
 from . import build as _build
 
 KVC_OK = 0
-KVC_F32, KVC_BF16 = 0, 1
+KVC_F32, KVC_BF16, KVC_E4M3 = 0, 1, 2
 KVC_APPEND_TAIL, KVC_APPEND_RING, KVC_APPEND_FREE_SLOT = 0, 1, 2
 KVC_DECODE_KV_SETTLED = 1
 KVC_DECODE_BALANCE = 2
@@ -91,6 +91,21 @@ class kvc_latent_cache(ctypes.Structure):
                 ("stride_b", ctypes.c_int64), ("stride_slot", ctypes.c_int64)]
 
 
+class kvc_block_pool_q8(ctypes.Structure):
+    _fields_ = [("pages", kvc_block_pool), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class kvc_qk_rows(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("k_out", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32), ("n_heads_q", ctypes.c_int32),
+                ("n_heads_kv", ctypes.c_int32), ("d_head", ctypes.c_int32),
+                ("d_rot", ctypes.c_int32)] + [
+        (f"{x}_stride_{y}", ctypes.c_int64) for x in ("q", "k", "q_out", "k_out")
+        for y in ("token", "head")]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -107,6 +122,8 @@ _FREE_P = ctypes.POINTER(kvc_free_pool)
 _DUO_P = ctypes.POINTER(kvc_duo)
 _DRAFT_P = ctypes.POINTER(kvc_draft)
 _LATENT_P = ctypes.POINTER(kvc_latent_cache)
+_POOL8_P = ctypes.POINTER(kvc_block_pool_q8)
+_ROWS_P = ctypes.POINTER(kvc_qk_rows)
 
 # name -> (restype, argtypes); every symbol declared in include/kvc.h
 SIGNATURES = {
@@ -165,6 +182,16 @@ SIGNATURES = {
                                       _SZ, _P]),
     "kvc_latent_accept": (_I32, [_LATENT_P, _P, _DRAFT_P, _P, _P, _P]),
     "kvc_latent_expand": (_I32, [_LATENT_P, _P, _I32, _P, _P, _CACHE_P, _P]),
+    "kvc_qk_norm_rope": (_I32, [_ROWS_P, _P, _P, _F32, _P, _P, _I32, _P]),
+    "kvc_paged_append_q8_workspace_bytes": (_SZ, [_I32] * 3),
+    "kvc_paged_append_q8": (_I32, [_POOL8_P, _PT_P, _FREE_P, _P, _P, _I32, _I32, _I64, _I64, _P, _P,
+                                   _P, _SZ, _P]),
+    "kvc_decode_attn_paged_q8_workspace_bytes": (_SZ, [_I32] * 5),
+    "kvc_decode_attn_paged_q8": (_I32, [_P, _I32, _I32, _POOL8_P, _PT_P, _F32, _P, _P, _I64, _P, _P,
+                                        _SZ, _P]),
+    "kvc_pages_workspace_bytes": (_SZ, [_I32] * 3),
+    "kvc_pages_reorder": (_I32, [_POOL_P, _P, _P, _PT_P, _FREE_P, _P, _P, _P, _P, _SZ, _P]),
+    "kvc_pages_compact": (_I32, [_POOL_P, _P, _P, _PT_P, _FREE_P, _P, _P, _P, _P, _SZ, _P]),
     "kvc_h2o_prefill_select": (_I32, [_P, _CACHE_P, _I32, _I32, _I32, _F32, _P, _P, _P, _P,
                                       _SZ, _P]),
 }
@@ -1033,3 +1060,239 @@ def kvc_latent_expand(cache: kvc_latent_cache, w_k: torch.Tensor, w_v: torch.Ten
     _need(len, "len", torch.int32, (c.batch,), index)
     _check((_lib or load()).kvc_latent_expand(c, None if len is None else len.data_ptr(), -1 if n_valid is None else n_valid,
                                     w_k.data_ptr(), w_v.data_ptr(), dst, _raw_stream(index, stream)))
+
+
+# ------------------------------------------------------------------------------------------
+# Norms and rotation of queries and keys, pages in 8 bits, pages held by several sequences.
+def _rows_of(t: torch.Tensor, what: str, dtype, n: int, d: int, index: int):
+    """A [n, heads, d] tensor of rows, each contiguous: checked, its address and two strides."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != n or shape[2] != d or stride[2] != 1 or t.dtype is not dtype or \
+            t.get_device() != index:
+        raise ValueError(f"{what} must be a {dtype} tensor [{n}, heads, {d}] with contiguous rows on "
+                         f"cuda:{index}, got {t.dtype} {list(shape)}, strides {list(stride)}, on {t.device}")
+    return t.data_ptr(), stride[0], stride[1]
+
+
+def kvc_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, *, w_q: Optional[torch.Tensor] = None,
+                     w_k: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     cos_sin: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     stream=None):
+    """q [T, Hq, D], k [T, Hkv, D] (rows contiguous, any strides) -> (q_out, k_out): RMS norm of every
+    row by w_q, w_k [D], then the rotation of its first d_rot elements to pos int32 [T], with
+    cos_sin fp32 [n_pos, 2, d_rot/2] (kvc_rope_table).  q_out=q, k_out=k: in place."""
+    dt, index = q.dtype, q.get_device()
+    code = _dtype_code(dt)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, n_heads_q, d_head], got {list(q.shape)}")
+    T, Hq, D = q.shape
+    if index < 0 or index != torch._C._cuda_getDevice():
+        _on_current(index, None, "q")
+    r = kvc_qk_rows()
+    r.q, r.q_stride_token, r.q_stride_head = _rows_of(q, "q", dt, T, D, index)
+    r.k, r.k_stride_token, r.k_stride_head = _rows_of(k, "k", dt, T, D, index)
+    _need(w_q, "w_q", dt, (D,), index)
+    _need(w_k, "w_k", dt, (D,), index)
+    n_pos = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 3 or pos is None:
+            raise ValueError("a rotation needs cos_sin [n_pos, 2, d_rot/2] and pos [T]")
+        n_pos, _, half = cos_sin.shape
+        _need(cos_sin, "cos_sin", torch.float32, (n_pos, 2, half), index)
+        _need(pos, "pos", torch.int32, (T,), index)
+        r.d_rot = 2 * half
+    elif pos is not None:
+        raise ValueError("positions need a table (cos_sin)")
+    with _on(stream, q_out, k_out):
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dt, device=q.device)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError(f"outputs {list(q_out.shape)}, {list(k_out.shape)} for rows {list(q.shape)}, {list(k.shape)}")
+    r.q_out, r.q_out_stride_token, r.q_out_stride_head = _rows_of(q_out, "q_out", dt, T, D, index)
+    r.k_out, r.k_out_stride_token, r.k_out_stride_head = _rows_of(k_out, "k_out", dt, T, D, index)
+    r.dtype, r.n_tokens, r.n_heads_q, r.n_heads_kv, r.d_head = code, T, Hq, k.shape[1], D
+    status = (_lib or load()).kvc_qk_norm_rope(
+        r, None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), eps,
+        None if cos_sin is None else cos_sin.data_ptr(), None if pos is None else pos.data_ptr(), n_pos,
+        _raw_stream(index, stream))
+    if status:
+        _check(status)
+    return q_out, k_out
+
+
+def block_pool_q8_view(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor,
+                       v_scale: torch.Tensor) -> kvc_block_pool_q8:
+    """Describe pages of e4m3 numbers: pools [n_heads_kv, n_blocks, block_size, d_head] (float8_e4m3fn
+    or its bytes as uint8) and scales fp32 [n_heads_kv, n_blocks], all contiguous."""
+    if k_pool.dim() != 4 or k_pool.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("8-bit pools are float8_e4m3fn or uint8 [n_heads_kv, n_blocks, block_size, d_head]")
+    index = k_pool.get_device()
+    _need(k_pool, "k_pool", k_pool.dtype, k_pool.shape, index)
+    _need(v_pool, "v_pool", k_pool.dtype, k_pool.shape, index)
+    _need(k_scale, "k_scale", torch.float32, k_pool.shape[:2], index)
+    _need(v_scale, "v_scale", torch.float32, k_pool.shape[:2], index)
+    c = kvc_block_pool_q8()
+    c.pages.k, c.pages.v = k_pool.data_ptr(), v_pool.data_ptr()
+    c.pages.dtype = KVC_E4M3
+    c.pages.n_heads_kv, c.pages.n_blocks, c.pages.block_size, c.pages.d_head = (int(x) for x in k_pool.shape)
+    c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    c._keep = (k_pool, v_pool, k_scale, v_scale)
+    return c
+
+
+def kvc_paged_append_q8_workspace_bytes(batch, n_tokens, block_size) -> int:
+    return int(load().kvc_paged_append_q8_workspace_bytes(batch, n_tokens, block_size))
+
+
+def append_q8_workspace(batch, n_tokens, block_size, device) -> torch.Tensor:
+    """A workspace for kvc_paged_append_q8 (need not be cleared)."""
+    return torch.empty(kvc_paged_append_q8_workspace_bytes(batch, n_tokens, block_size) + 256,
+                       dtype=torch.uint8, device=device)
+
+
+def kvc_paged_append_q8(pool: kvc_block_pool_q8, pt: kvc_page_table, free_pool: kvc_free_pool,
+                        k_new: torch.Tensor, v_new: torch.Tensor, *,
+                        cu: Optional[torch.Tensor] = None, appended: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Append rows k_new, v_new [n, Hkv, D] (rows contiguous, the same strides): sequence b's are
+    cu[b] .. cu[b + 1] - 1 (int32 [B + 1]), or row b.  appended int32 [B]: rows appended."""
+    pages, B = pool.pages, pt.batch
+    index = k_new.get_device()
+    _on_current(index, pool, "k_new")
+    _beside(index, pt, "k_new")
+    _beside(index, free_pool, "k_new")
+    n, H, D = k_new.shape if k_new.dim() == 3 else (0, 0, 0)
+    if H != pages.n_heads_kv or D != pages.d_head:
+        raise ValueError(f"k_new must be [n, {pages.n_heads_kv}, {pages.d_head}], got {list(k_new.shape)}")
+    code = _dtype_code(k_new.dtype)
+    kp, st, sh = _rows_of(k_new, "k_new", k_new.dtype, n, D, index)
+    vp, vt, vh = _rows_of(v_new, "v_new", k_new.dtype, n, D, index)
+    if v_new.shape[1] != H or (vt, vh) != (st, sh):
+        raise ValueError("v_new must have the shape and the strides of k_new")
+    if cu is None and n != B:
+        raise ValueError(f"{n} rows for {B} sequences: give their offsets (cu)")
+    _need(cu, "cu", torch.int32, (B + 1,), index)
+    _need(appended, "appended", torch.int32, (B,), index)
+    if ws is None:
+        with _on(stream):
+            ws = append_q8_workspace(B, n, pages.block_size, k_new.device)
+    wp, wb = _space(ws, index)
+    status = (_lib or load()).kvc_paged_append_q8(
+        pool, pt, free_pool, kp, vp, code, n, st, sh, None if cu is None else cu.data_ptr(),
+        None if appended is None else appended.data_ptr(), wp, wb, _raw_stream(index, stream))
+    if status:
+        _check(status)
+
+
+def kvc_decode_attn_paged_q8_workspace_bytes(batch, n_heads_q, n_heads_kv, d_head, dtype) -> int:
+    return int(load().kvc_decode_attn_paged_q8_workspace_bytes(batch, n_heads_q, n_heads_kv, d_head,
+                                                               dtype))
+
+
+def decode_q8_workspace(batch, n_heads_q, n_heads_kv, d_head, dtype: torch.dtype, device) -> torch.Tensor:
+    """A workspace for kvc_decode_attn_paged_q8 (need not be cleared); dtype: the queries'."""
+    n = kvc_decode_attn_paged_q8_workspace_bytes(batch, n_heads_q, n_heads_kv, d_head, _dtype_code(dtype))
+    return torch.empty(n + 256, dtype=torch.uint8, device=device)
+
+
+def kvc_decode_attn_paged_q8(q: torch.Tensor, pool: kvc_block_pool_q8, pt: kvc_page_table, *,
+                             scale: float, out: Optional[torch.Tensor] = None,
+                             logits: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                             ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """q [B, Hq, D] -> out [B, Hq, D] (q's type) over each sequence's 8-bit pages.  logits fp32
+    [B, Hq, >= max_blocks * block_size], lse fp32 [B, Hq]."""
+    pages, B, dt = pool.pages, pt.batch, q.dtype
+    code, shape = _dtype_code(dt), q.shape
+    if len(shape) != 3 or shape[0] != B or shape[2] != pages.d_head or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous tensor [{B}, n_heads_q, {pages.d_head}], got {list(shape)}")
+    index = q.get_device()
+    _on_current(index, pool, "q")
+    _beside(index, pt, "q")
+    Hq = shape[1]
+    lstride = 0
+    if logits is not None:
+        _need(logits, "logits", torch.float32, (B, Hq, logits.shape[-1]), index)
+        lstride = logits.shape[-1]
+    _need(lse, "lse", torch.float32, (B, Hq), index)
+    if out is None or ws is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if ws is None:
+                ws = decode_q8_workspace(B, Hq, pages.n_heads_kv, pages.d_head, dt, q.device)
+    _need(out, "out", dt, shape, index)
+    wp, wb = _space(ws, index)
+    status = (_lib or load()).kvc_decode_attn_paged_q8(
+        q.data_ptr(), code, Hq, pool, pt, scale, out.data_ptr(),
+        None if logits is None else logits.data_ptr(), lstride, None if lse is None else lse.data_ptr(),
+        wp, wb, _raw_stream(index, stream))
+    if status:
+        _check(status)
+    return out
+
+
+def kvc_pages_workspace_bytes(batch, max_blocks, n_blocks) -> int:
+    return int(load().kvc_pages_workspace_bytes(batch, max_blocks, n_blocks))
+
+
+def pages_workspace(batch, max_blocks, n_blocks, device) -> torch.Tensor:
+    """A workspace for kvc_pages_reorder and kvc_pages_compact (need not be cleared)."""
+    return torch.empty(kvc_pages_workspace_bytes(batch, max_blocks, n_blocks) + 256, dtype=torch.uint8,
+                       device=device)
+
+
+def _pages_args(pool, pt, free_pool, shares, pos, ws, stream):
+    """The checks shared by the calls on pages; returns (pages, scales, device index, workspace): the
+    caller keeps the workspace until its kernels are launched."""
+    q8 = isinstance(pool, kvc_block_pool_q8)
+    pages = pool.pages if q8 else pool
+    index = pool._keep[0].get_device()
+    _on_current(index, pool, "the pool")
+    _beside(index, pt, "the pool")
+    _beside(index, free_pool, "the pool")
+    _need(shares, "shares", torch.int32, (pages.n_blocks,), index)
+    _need(pos, "pos", torch.int32, (pages.n_blocks, pages.block_size), index)
+    if ws is None:
+        with _on(stream):
+            ws = pages_workspace(pt.batch, pt.max_blocks, pages.n_blocks, pool._keep[0].device)
+    return pages, (pool.k_scale, pool.v_scale) if q8 else (None, None), index, ws
+
+
+def kvc_pages_reorder(pool, pt: kvc_page_table, free_pool: kvc_free_pool, shares: torch.Tensor,
+                      parent: torch.Tensor, *, pos: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Sequence b becomes a copy of sequence parent[b] (int32 [B]; -1: freed), full pages shared.
+    pool: of block_pool_view or block_pool_q8_view; shares int32 [n_blocks]."""
+    if shares is None:
+        raise ValueError("shares is needed: int32 [n_blocks], zero before the first call")
+    pages, scales, index, ws = _pages_args(pool, pt, free_pool, shares, pos, ws, stream)
+    wp, wb = _space(ws, index)
+    _need(parent, "parent", torch.int32, (pt.batch,), index)
+    status = (_lib or load()).kvc_pages_reorder(
+        pages, *scales, pt, free_pool, shares.data_ptr(), None if pos is None else pos.data_ptr(),
+        parent.data_ptr(), wp, wb, _raw_stream(index, stream))
+    if status:
+        _check(status)
+
+
+def kvc_pages_compact(pool, pt: kvc_page_table, free_pool: kvc_free_pool, *,
+                      shares: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                      remap: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Move the live pages to the lowest ids; returns remap int32 [n_blocks] (-1: a free page)."""
+    pages, scales, index, ws = _pages_args(pool, pt, free_pool, shares, pos, ws, stream)
+    wp, wb = _space(ws, index)
+    if remap is None:
+        with _on(stream):
+            remap = torch.empty(pages.n_blocks, dtype=torch.int32, device=pool._keep[0].device)
+    else:
+        _need(remap, "remap", torch.int32, (pages.n_blocks,), index)
+    status = (_lib or load()).kvc_pages_compact(
+        pages, *scales, pt, free_pool, None if shares is None else shares.data_ptr(),
+        None if pos is None else pos.data_ptr(), remap.data_ptr(), wp, wb, _raw_stream(index, stream))
+    if status:
+        _check(status)
+    return remap
