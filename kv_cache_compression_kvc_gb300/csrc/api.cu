@@ -1597,7 +1597,8 @@ kvc_status kvc_qk_norm_rope(const kvc_qk_rows *r, const void *w_q, const void *w
     if ((long long)r->n_tokens * ((long long)r->n_heads_q + r->n_heads_kv) > 0x7fffffffLL)
         return fail(KVC_ERR_SHAPE, "%s: too many rows", name);
     int32_t *code = nullptr;
-    st = device_info(&code, nullptr);
+    int n_sm = 0;
+    st = device_info(&code, &n_sm);
     if (st != KVC_OK) return st;
     kvc::QkNormParams p{};
     p.q = r->q; p.k = r->k; p.q_out = r->q_out; p.k_out = r->k_out;
@@ -1613,7 +1614,7 @@ kvc_status kvc_qk_norm_rope(const kvc_qk_rows *r, const void *w_q, const void *w
     }
     p.dev_code = code;
     const cudaError_t e =
-        kvc::launch_qk_norm_rope(p, r->d_head, r->dtype == KVC_BF16, static_cast<cudaStream_t>(stream));
+        kvc::launch_qk_norm_rope(p, r->d_head, r->dtype == KVC_BF16, n_sm, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
     return ok();
 }
@@ -1750,7 +1751,9 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
     const int G = n_heads_q / Hkv;
     const kvc::DecodeQ8Plan pl =
         kvc::decode_q8_plan(pt->batch, Hkv, G, pool->pages.d_head, dtype == KVC_BF16, n_sm);
-    if ((long long)pt->batch * Hkv * pl.RT > 0x3fffffffLL || (long long)pt->batch * n_heads_q > 0x7fffffffLL)
+    // (a warp counts its steps in 32 bits)
+    if ((long long)pt->batch * Hkv * pl.RT > 0x3fffffffLL || (long long)pt->batch * n_heads_q > 0x7fffffffLL ||
+        (long long)pt->batch * Hkv * pl.RT * (cap / 16 + 3) / pl.blocks > 0x3fffffffLL)
         return fail(KVC_ERR_SHAPE, "%s: batch * heads too large", name);
     st = check_ws(ws, ws_bytes, pl.bytes, name);
     if (st != KVC_OK) return st;
@@ -1767,11 +1770,14 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
     p.RT = pl.RT; p.RP = pl.RP; p.HR = Hkv * pl.RT;
     p.scale = scale;
     p.out = out; p.logits = logits; p.logits_stride = logits_stride; p.lse = lse;
-    p.ranges = pl.ranges; p.by_tile = pl.by_tile; p.n_sm = n_sm;
+    p.blocks = pl.blocks; p.by_tile = pl.by_tile;
     char *w = static_cast<char *>(ws);
-    p.ws_note = reinterpret_cast<int4 *>(w + pl.off_note);
+    p.ws_first = reinterpret_cast<int32_t *>(w + pl.off_first);
+    p.ws_last = reinterpret_cast<int32_t *>(w + pl.off_last);
     p.ws_ml = reinterpret_cast<float *>(w + pl.off_ml);
     p.ws_o = reinterpret_cast<float *>(w + pl.off_o);
+    p.ws_wml = reinterpret_cast<float *>(w + pl.off_wml);
+    p.ws_wo = reinterpret_cast<float *>(w + pl.off_wo);
     p.dev_code = code;
     const cudaError_t e = kvc::launch_decode_q8(p, pool->pages.d_head, dtype == KVC_BF16,
                                                 static_cast<cudaStream_t>(stream));

@@ -6,11 +6,11 @@
 //
 // What bounds it is the stream of the cache: one byte an element, 4 G operations for the G query heads
 // that share it, far below the ridge.  So everything is arranged around bytes in flight:
-//   A warp works alone.  It owns an equal share of the steps (16 slots of one (sequence, KV head,
-//   row tile)) of the whole batch and keeps kStages steps in flight in its own ring in shared memory
-//   (cp.async, 16 bytes a lane; rows behind the length are filled with zeros, whatever the page
-//   holds there).  No barrier between warps, no wait that could fail to end: a warp waits for its own
-//   copies only.
+//   A warp works alone.  The steps (16 slots of one (sequence, KV head, row tile)) of the whole batch are
+//   dealt out evenly, in order, to the blocks and again to a block's warps, and a warp keeps kStages
+//   steps in flight in its own ring in shared memory (cp.async, 16 bytes a lane; rows behind the
+//   length are filled with zeros, whatever the page holds there).  No barrier between warps while they
+//   stream, and no wait that could fail to end: a warp waits for its own copies only.
 //   Both products run on mma.m16n8k16 with the cache as the 16-row operand and the query heads as the 8
 //   columns, so that up to 8 heads waste nothing: S^T = K Q^T, O^T = V^T P^T.  (5th-generation
 //   products want 64 or 128 rows of one operand and, of 8-bit operands, both in 8 bits; the stream
@@ -25,8 +25,9 @@
 //   maximum m are kept beside it.  All sums are fp32.
 //
 // The range of a warp is found on the device (a scan of the lengths), even however ragged the batch
-// is.  A row that crosses ranges leaves partial states (m, l, M, O) in the workspace; decode_q8_merge_kernel
-// joins them in order of the ranges, so results do not depend on timing.
+// is.  A row tile that crosses warps leaves partial states (m, l, M, O): those of a block are joined in
+// shared memory at its end, those of several blocks by decode_q8_merge_kernel, both in order of
+// the slots, so results do not depend on timing.
 #include <algorithm>
 #include <type_traits>
 
@@ -41,8 +42,10 @@ namespace {
 
 constexpr int kStep = 16;                    // slots of a step
 constexpr int kEnd = 2;                      // steps that the end of a row tile counts as
-constexpr int kWholeSteps = 8;               // rows of so many steps are not split
-constexpr int kMinUnits = 4;                 // units that a range is worth at least
+constexpr int kWarps = 8;
+constexpr int kMergeThreads = 256;
+constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block
+constexpr int kMinUnits = 16;                // units that a block is worth at least
 constexpr float kSlack = 8.f;                // a maximum rises when it is passed by 2^8
 constexpr float kBoost = 6.f;                // weights are held times 2^6: at most 2^15, exact down to 2^-20
 constexpr float kNone = -3.402823466e38f;    // a maximum of nothing
@@ -51,7 +54,7 @@ constexpr int kDevBadBlk_ = 9;
 
 template <int D, int NT, bool SPLIT>
 struct Q8Plan {
-    static constexpr int WARPS = 8;
+    static constexpr int WARPS = kWarps;
     static constexpr int BLOCKS = D <= 128 && NT == 1 && !SPLIT ? 2 : 1;    // per SM (registers)
     static constexpr int STAGE = 2 * kStep * D + 32;     // keys, values, the two scales, what they are of
     static constexpr int ROOM = (BLOCKS == 2 ? 112 : 224) * 1024 / WARPS;
@@ -60,11 +63,12 @@ struct Q8Plan {
     static constexpr int SMEM = WARPS * STAGES * STAGE;
 };
 
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two)
+// Four e4m3 numbers to two pairs of fp16.
+__device__ __forceinline__ void cvt_e4m3x4(uint32_t four, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t r;
-    asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}\n" : "=r"(r) : "r"(two));
-    return r;
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 __device__ __forceinline__ void mma_16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
 {
@@ -88,6 +92,10 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
 __device__ __forceinline__ float2 unpack_h2(uint32_t x)
 {
     return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+__device__ __forceinline__ void cp_16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_16(uint32_t dst, const void *src, bool valid)
 {
@@ -124,71 +132,52 @@ __device__ __forceinline__ int steps_of(int len) { return len > 0 ? (len + kStep
 // A warp's share of the units: every row tile counts its steps and kEnd.  Called by a whole warp.
 struct Range {
     int b, hr, off, len;         // the first row tile: sequence, head * RT + tile, first unit in it, slots
-    long long t0, left;          // first unit and number of units
-    long long q;                 // units of a range, one more in the first r
-    long long r;
-    __device__ __forceinline__ int range_of(long long t) const
-    {
-        const long long big = r * (q + 1);
-        return (int)(t < big ? t / (q + 1) : r + (t - big) / q);
-    }
+    int left;                    // units of this warp
 };
-__device__ __forceinline__ Range find_range(const DecodeQ8Params &p, int w, bool check)
+// U: 32 bits where they hold all units (a 64-bit division is a long subroutine).
+template <typename U>
+__device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool check = blockIdx.x == 0 && warp == 0;
     const int per = (p.B + 31) >> 5;
     const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-    long long sum = 0;
+    U sum = 0;
     for (int b = b0; b < b1; ++b) {
         const int n = p.len[b];
         if (check && (n < 0 || n > p.cap)) record_code(p.dev_code, kDevBadLen_);
-        sum += (long long)(steps_of(n < 0 ? 0 : min(n, p.cap)) + kEnd) * p.HR;
+        sum += (U)(steps_of(n < 0 ? 0 : min(n, p.cap)) + kEnd) * (U)p.HR;
     }
-    long long incl = sum;
+    U incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const U y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    const long long T = __shfl_sync(0xffffffffu, incl, 31);
+    const U T = __shfl_sync(0xffffffffu, incl, 31);
+    U blocks = T / kMinUnits;                // a block is worth a few steps
+    blocks = blocks < 1 ? 1 : (blocks > gridDim.x ? gridDim.x : blocks);
+    const U q = T / blocks, r = T - q * blocks, bl = blockIdx.x;
+    const U first = bl * q + (bl < r ? bl : r);
+    const unsigned mine = bl < blocks ? (unsigned)(q + (bl < r ? 1 : 0)) : 0u;
+    const unsigned w0 = (unsigned)((unsigned long long)mine * warp / kWarps);
+    const U t0 = first + w0;
     Range g;
-    if (p.whole) {               // whole row tiles, equally many a range
-        const long long tiles = (long long)p.B * p.HR, i0 = tiles * w / p.ranges, i1 = tiles * (w + 1) / p.ranges;
-        g.b = (int)(i0 / p.HR);
-        g.hr = (int)(i0 - (long long)g.b * p.HR);
-        g.off = 0;
-        g.len = i0 < i1 ? len_of(p, g.b) : 0;
-        g.t0 = g.q = g.r = g.left = 0;
-        for (long long i = i0; i < i1; ++i) g.left += steps_of(len_of(p, (int)(i / p.HR))) + kEnd;
-        return g;
-    }
-    long long ranges = T / p.min_units;      // each is worth a few steps
-    ranges = ranges < 1 ? 1 : (ranges > p.ranges ? p.ranges : ranges);
-    if (T <= 0x7fffffffLL) {     // (a 64-bit division is a long subroutine)
-        const unsigned t = (unsigned)T, c = (unsigned)ranges;
-        g.q = t / c;
-        g.r = t - t / c * c;
-    } else {
-        g.q = T / ranges;
-        g.r = T - g.q * ranges;
-    }
-    g.b = g.hr = g.off = g.len = 0;
-    g.t0 = w * g.q + (w < g.r ? w : g.r);
-    g.left = w < ranges ? g.q + (w < g.r ? 1 : 0) : 0;
-    const long long before = incl - sum;
-    const bool here = g.left > 0 && before <= g.t0 && g.t0 < incl;
+    g.left = (int)((unsigned)((unsigned long long)mine * (warp + 1) / kWarps) - w0);
+    const U before = incl - sum;
+    const bool here = g.left > 0 && before <= t0 && t0 < incl;
     int b = b0, hr = 0, off = 0, len = 0;
     if (here) {
-        long long t = before;
-        long long cost = 0;
+        U t = before;
+        U cost = 0;
         for (;; ++b) {
             len = len_of(p, b);
-            cost = steps_of(len) + kEnd;
-            if (g.t0 < t + cost * p.HR || b == b1 - 1) break;
-            t += cost * p.HR;
+            cost = (U)(steps_of(len) + kEnd);
+            if (t0 < t + cost * (U)p.HR || b == b1 - 1) break;
+            t += cost * (U)p.HR;
         }
-        hr = (int)((g.t0 - t) / cost);
-        off = (int)(g.t0 - t - hr * cost);
+        hr = (int)((t0 - t) / cost);
+        off = (int)(t0 - t - (U)hr * cost);
     }
     const int src = (__ffs(__ballot_sync(0xffffffffu, here)) - 1) & 31;
     g.b = __shfl_sync(0xffffffffu, b, src);
@@ -197,11 +186,47 @@ __device__ __forceinline__ Range find_range(const DecodeQ8Params &p, int w, bool
     g.len = __shfl_sync(0xffffffffu, len, src);
     return g;
 }
+__device__ __noinline__ Range split_range_64(const DecodeQ8Params &p) { return split_range<unsigned long long>(p); }
+
+__device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
+{
+    if (!p.whole) return p.small ? split_range<unsigned>(p) : split_range_64(p);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool check = blockIdx.x == 0 && warp == 0;
+    Range g;
+    g.b = g.hr = g.off = g.len = 0;
+    {                            // whole row tiles, equally many a block
+        if (check)
+            for (int b = lane; b < p.B; b += 32)
+                if (p.len[b] < 0 || p.len[b] > p.cap) record_code(p.dev_code, kDevBadLen_);
+        const unsigned tiles = (unsigned)(p.B * p.HR), n = gridDim.x;
+        const unsigned i0 = (unsigned)((unsigned long long)tiles * blockIdx.x / n);
+        const unsigned i1 = (unsigned)((unsigned long long)tiles * (blockIdx.x + 1) / n);
+        int units = 0;
+        for (unsigned i = i0 + lane; i < i1; i += 32) units += steps_of(len_of(p, (int)(i / p.HR)));
+        units = __reduce_add_sync(0xffffffffu, units);
+        int at = units * warp / kWarps;
+        g.left = units * (warp + 1) / kWarps - at;
+        if (g.left > 0) {
+            unsigned i = i0;
+            for (;; ++i) {
+                g.b = (int)(i / p.HR);
+                g.len = len_of(p, g.b);
+                const int n_i = steps_of(g.len);
+                if (at < n_i) break;
+                at -= n_i;
+            }
+            g.hr = (int)(i - (unsigned)g.b * p.HR);
+            g.off = at;
+        }
+        return g;
+    }
+}
 
 // The steps of a range in order.
 struct Walk {
     int b, hr, step, len, n;     // the step: row tile (b, hr), its number, the tile's slots and steps
-    long long left;              // units of the range left, this step's among them
+    int left;                    // units of the range left, this step's among them
     __device__ __forceinline__ Walk(const DecodeQ8Params &p, const Range &g)
         : b(g.b), hr(g.hr), step(g.off), len(g.len), n(steps_of(g.len)), left(g.left)
     {
@@ -211,7 +236,7 @@ struct Walk {
     __device__ __forceinline__ void settle(const DecodeQ8Params &p)
     {
         while (left > 0 && step >= n) {
-            left -= n + kEnd - step;
+            left -= n + (p.whole ? 0 : kEnd) - step;
             step = 0;
             if (++hr == p.HR) {
                 hr = 0;
@@ -233,6 +258,23 @@ struct Walk {
     }
 };
 
+// 4 columns of an output row from its joined state.
+template <typename T>
+__device__ __forceinline__ void store_row(const DecodeQ8Params &p, size_t row, int D, int col, float m, float l,
+                                          float mv, float4 o)
+{
+    const float f = l == 0.f ? 0.f : ex2(mv - kBoost - m) / l;
+    if (col == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    T *dst = static_cast<T *>(p.out) + row * D + col;
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4 *>(dst) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * f, o.y * f), c = __floats2bfloat162_rn(o.z * f, o.w * f);
+        *reinterpret_cast<uint2 *>(dst) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+    }
+}
+
 template <int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT, SPLIT>::BLOCKS)
     decode_q8_kernel(const DecodeQ8Params p)
@@ -250,18 +292,28 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * (S * PL::STAGE);
-    // neighbouring ranges on different SMs: a small batch is spread over all of them
-    const int w = warp * gridDim.x + blockIdx.x;
+    // parts of row tiles that this block's warps leave: a warp's first one (if others follow) in the
+    // workspace, its last one in its ring: {row tile or -1, first step, behind the last, steps of the tile}
+    __shared__ int4 s_part[2 * kWarps];
+    if (threadIdx.x < 2 * kWarps) s_part[threadIdx.x] = make_int4(-1, 0, 0, 0);
     pdl_trigger();
     pdl_wait();
-    const Range range = find_range(p, w, w == 0);
-    bool noted = false;                      // a row tile begins here and ends in a later range
+    const Range range = find_range(p);
+    __syncthreads();                         // (s_part)
 
     // ---- copies: one step ahead by step into the ring ----
     Walk ld(p, range);
     int page_at = -1, pages = 0;             // the 32 table entries in this warp's lanes: first one's number
     int ld_b = -1;
     const int32_t *tab = p.table;
+    // where this lane's chunk i * 32 + lane of a step's rows goes: chunk c of row r lies at c ^ 4 (r & 1) for
+    // keys and at c ^ 2 (r / 2 & 3) for values (64 dims: c and c ^ 2 (r / 2 & 1)), which keeps the
+    // fragments' reads free of bank conflicts (the values of 64 dims: two ways).  A copy's rows are
+    // 32 / CPR further on than the last one's, which turns the values' swizzle but not the keys'.
+    const int row0 = lane / CPR, c0 = lane % CPR;
+    const uint32_t k_to = row0 * D + (D == 64 ? c0 : c0 ^ ((row0 & 1) << 2)) * 16;
+    const uint32_t v_to = row0 * D + (D == 64 ? c0 ^ ((row0 >> 1 & 1) << 1) : c0 ^ ((row0 >> 1 & 3) << 1)) * 16;
+    auto v_turn = [](int i) -> uint32_t { return D == 64 ? 0u : (uint32_t)(i * (32 / CPR) >> 1 & 3) << 5; };
     auto fetch = [&](int slot) {
         const uint32_t st = ring + slot * PL::STAGE;
         if (ld.more()) {
@@ -280,15 +332,20 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             }
             const size_t page = (size_t)(ld.hr / p.RT) * p.n_pool + id;
             const size_t at = (page * p.bs + (pos - lb * p.bs)) * D;
-            const uint8_t *k = p.k + at, *v = p.v + at;
+            const uint8_t *k = p.k + at + lane * 16, *v = p.v + at + lane * 16;
+            if (valid == kStep) {
 #pragma unroll
-            for (int i = 0; i < CPR / 2; ++i) {
-                const int x = i * 32 + lane, row = x / CPR, c = x % CPR;
-                const bool ok = row < valid;
-                const int ck = D == 64 ? c : c ^ ((row & 1) << 2);
-                const int cv = D == 64 ? c ^ ((row >> 1 & 1) << 1) : c ^ ((row >> 1 & 3) << 1);
-                cp_16(st + row * D + ck * 16, k + x * 16, ok);
-                cp_16(st + kStep * D + row * D + cv * 16, v + x * 16, ok);
+                for (int i = 0; i < CPR / 2; ++i) {
+                    cp_16(st + k_to + i * 512, k + i * 512);
+                    cp_16(st + kStep * D + (v_to ^ v_turn(i)) + i * 512, v + i * 512);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < CPR / 2; ++i) {
+                    const bool ok = (i * 32 + lane) / CPR < valid;
+                    cp_16(st + k_to + i * 512, k + i * 512, ok);
+                    cp_16(st + kStep * D + (v_to ^ v_turn(i)) + i * 512, v + i * 512, ok);
+                }
             }
             if (lane < 2) cp_4(st + 2 * kStep * D + lane * 4, (lane == 0 ? p.ks : p.vs) + page);
             if (lane == 0) {
@@ -313,7 +370,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     float fq[NT][2];                         // row 2t, 2t + 1: the query's power of two times scale
     float o[DT][NT][4];
     float m[NT][2], mv[NT][2], l[NT][2];
-    int cur_b = -1, cur_hr = -1, cur_len = 0, cur_n = 0, first_step = 0, parts = 0;
+    int cur_b = -1, cur_hr = -1, cur_len = 0, cur_n = 0, first_step = 0;
 
     auto begin = [&](int b, int hr) {
         const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8;
@@ -380,18 +437,18 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 for (int r = 0; r < 4; ++r) o[d][nt][r] = 0.f;
         }
     };
-    // Outputs of the row tile, or its partial state.
-    auto finish = [&](int b, int hr, int lo, int hi, int n) {
+    // Outputs of the row tile, or the state of its part.
+    auto finish = [&](int b, int hr, int lo, int hi, int n, bool last) {
         const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8;
         const bool whole = lo == 0 && hi == n;
-        const size_t part = (size_t)w * 2 + (parts > 0 ? 1 : 0);
-        if (!p.whole && lo == 0 && (p.by_tile || !whole) && lane == 0) {
-            // the tile's last step lies n - hi steps behind this range's end
-            const int tile = b * p.HR + hr;
-            p.ws_note[p.by_tile ? tile : w] =
-                whole ? make_int4(-1, 0, 0, 0)
-                      : make_int4(tile, w, range.range_of(range.t0 + range.left + (n - hi) - 1), parts > 0 ? 1 : 0);
-            noted = true;
+        float *po = nullptr, *pm = nullptr;
+        if (!whole) {
+            const size_t at = (size_t)blockIdx.x * kWarps + warp;
+            po = last ? reinterpret_cast<float *>(smem + warp * (S * PL::STAGE)) : p.ws_wo + at * p.RP * D;
+            pm = last ? po + p.RP * D : p.ws_wml + at * p.RP * 4;
+            if (lane == 0) s_part[2 * warp + (last ? 1 : 0)] = make_int4(b * p.HR + hr, lo, hi, n);
+        } else if (p.by_tile && !p.whole && lane == 0) {
+            p.ws_first[b * p.HR + hr] = -1;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -410,8 +467,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                     if (g == 0 && p.lse != nullptr)
                         p.lse[out_row] = sum == 0.f ? -INFINITY : (m[nt][r] + log2f(sum)) * kLn2;
                 } else if (g == 0) {
-                    reinterpret_cast<float4 *>(p.ws_ml)[part * p.RP + row] =
-                        make_float4(m[nt][r], sum, mv[nt][r], 0.f);
+                    reinterpret_cast<float4 *>(pm)[row] = make_float4(m[nt][r], sum, mv[nt][r], 0.f);
                 }
 #pragma unroll
                 for (int c = 0; c < VC; ++c) {
@@ -424,8 +480,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                         y[2 * i + 1] = o[c * 8 + i][nt][2 + r] * f;
                     }
                     if (!whole || SPLIT) {
-                        float *dst = whole ? static_cast<float *>(p.out) + out_row * D + d0
-                                           : p.ws_o + (part * p.RP + row) * D + d0;
+                        float *dst = whole ? static_cast<float *>(p.out) + out_row * D + d0 : po + row * D + d0;
 #pragma unroll
                         for (int i = 0; i < VB; i += 4)
                             *reinterpret_cast<float4 *>(dst + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
@@ -444,7 +499,6 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                     }
                 }
             }
-        ++parts;
     };
 
     int slot = 0, put = S - 1;
@@ -459,7 +513,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         const uint2 scales = lds_8(st + 2 * kStep * D);
         const int b = (int)what.x, hr = (int)what.y, step = (int)what.z, len = (int)what.w;
         if (b != cur_b || hr != cur_hr) {
-            if (cur_b >= 0) finish(cur_b, cur_hr, first_step, first_step + cur_n, steps_of(cur_len));
+            if (cur_b >= 0) finish(cur_b, cur_hr, first_step, first_step + cur_n, steps_of(cur_len), b < 0);
             if (b < 0) break;
             cur_b = b;
             cur_hr = hr;
@@ -486,8 +540,9 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t a[4] = {cvt_e4m3x2(wa[j]), cvt_e4m3x2(wb[j]), cvt_e4m3x2(wa[j] >> 16),
-                                       cvt_e4m3x2(wb[j] >> 16)};
+                uint32_t a[4];
+                cvt_e4m3x4(wa[j], a[0], a[2]);
+                cvt_e4m3x4(wb[j], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     mma_16816(c[nt][j & 1], a, bq[nt][h * 4 + j][0], bq[nt][h * 4 + j][1]);
@@ -501,29 +556,34 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         ev = ev < -126 ? -126 : (ev > 126 ? 126 : ev);
         const float fv = sv * __uint_as_float((uint32_t)(127 - ev) << 23);
         const float evf = (float)ev;
-        const bool in0 = g < valid, in1 = g + 8 < valid;
         float x[NT][4];                      // log2 units: (slot g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
         bool rise = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float f0 = fq[nt][0] * sk, f1 = fq[nt][1] * sk;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[nt][i] = (c[nt][0][i] + c[nt][1][i]) * (i & 1 ? f1 : f0);
+            for (int i = 0; i < 4; ++i) x[nt][i] = c[nt][0][i] + c[nt][1][i];
             if (p.logits != nullptr) {
                 const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8 + nt * 8 + 2 * t;
                 float *dst = p.logits + ((size_t)b * p.Hq + h * p.G + r0) * p.logits_stride + pos + g;
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
                     if (r0 + r < p.G) {
-                        if (in0) dst[r * p.logits_stride] = x[nt][r];
-                        if (in1) dst[r * p.logits_stride + 8] = x[nt][2 + r];
+                        if (g < valid) dst[r * p.logits_stride] = x[nt][r] * (r ? f1 : f0);
+                        if (g + 8 < valid) dst[r * p.logits_stride + 8] = x[nt][2 + r] * (r ? f1 : f0);
                     }
             }
+            const float e0 = f0 * kLog2e, e1 = f1 * kLog2e;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[nt][i] = (i < 2 ? in0 : in1) ? x[nt][i] * kLog2e : -INFINITY;
-                rise |= x[nt][i] > m[nt][i & 1] + kSlack || x[nt][i] + evf > mv[nt][i & 1] + kSlack;
+            for (int i = 0; i < 4; ++i) x[nt][i] *= i & 1 ? e1 : e0;
+            if (valid < kStep) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (g + (i >> 1) * 8 >= valid) x[nt][i] = -INFINITY;
             }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                rise |= fmaxf(x[nt][r], x[nt][2 + r]) > fminf(m[nt][r], mv[nt][r] - evf) + kSlack;
         }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
@@ -550,10 +610,11 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float y[4];
+            const float to[2] = {evf + kBoost - mv[nt][0], evf + kBoost - mv[nt][1]};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 l[nt][i & 1] += ex2(x[nt][i] - m[nt][i & 1]);
-                y[i] = ex2(x[nt][i] - mv[nt][i & 1] + (evf + kBoost)) * fv;
+                y[i] = ex2(x[nt][i] + to[i & 1]) * fv;
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -589,8 +650,9 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 for (int u = 0; u < 2; ++u) {
                     const uint32_t lo = __byte_perm(r[0][q], r[1][q], u ? 0x7362 : 0x5140);
                     const uint32_t hi = __byte_perm(r[2][q], r[3][q], u ? 0x7362 : 0x5140);
-                    const uint32_t a[4] = {cvt_e4m3x2(lo), cvt_e4m3x2(lo >> 16), cvt_e4m3x2(hi),
-                                           cvt_e4m3x2(hi >> 16)};
+                    uint32_t a[4];
+                    cvt_e4m3x4(lo, a[0], a[1]);
+                    cvt_e4m3x4(hi, a[2], a[3]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma_16816(o[vc * 8 + q * 2 + u][nt], a, pw[nt][0], pw[nt][1]);
@@ -600,86 +662,162 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         }
         slot = slot + 1 == S ? 0 : slot + 1;
     }
-    if (!p.whole && !p.by_tile && !noted && lane == 0) p.ws_note[w] = make_int4(-1, 0, 0, 0);
+    // ---- the block's parts, in order: those of one row tile are joined, a row a warp ----
+    __syncthreads();
+    const int4 mine = lane < 2 * kWarps ? s_part[lane] : make_int4(-1, 0, 0, 0);
+    const uint32_t parts = __ballot_sync(0xffffffffu, mine.x >= 0);
+    const uint32_t below = parts & ((1u << lane) - 1u);
+    const int tile_below = __shfl_sync(0xffffffffu, mine.x, below != 0 ? 31 - __clz(below) : 0);
+    uint32_t firsts = __ballot_sync(0xffffffffu, mine.x >= 0 && (below == 0 || tile_below != mine.x));
+    bool begun = false;                      // a row tile begins here and ends in a later block
+    int turn = warp;                         // rows are dealt out to the warps in turn
+#pragma unroll 1
+    while (firsts != 0) {
+        const int i = __ffs(firsts) - 1;
+        firsts &= firsts - 1;
+        const uint32_t members = parts & ~((1u << i) - 1u) & (firsts != 0 ? (1u << (__ffs(firsts) - 1)) - 1u : ~0u);
+        const int tile = __shfl_sync(0xffffffffu, mine.x, i), lo = __shfl_sync(0xffffffffu, mine.y, i);
+        const int n = __shfl_sync(0xffffffffu, mine.w, i), hi = __shfl_sync(0xffffffffu, mine.z, 31 - __clz(members));
+        const bool whole = lo == 0 && hi == n;
+        const int b = tile / p.HR, hr = tile - b * p.HR, h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8;
+        const int rows = min(p.RP, p.G - r0);
+        // part x: odd ones in the ring of warp x / 2, even ones in the workspace
+        const float *ring_o = reinterpret_cast<const float *>(smem);
+        const size_t ws_at = (size_t)blockIdx.x * kWarps * p.RP;
+        constexpr int RING = S * PL::STAGE / 4;
+        int row = turn;
+        for (; row < rows; row += kWarps) {
+            // lane x has part x's state, and then its factor
+            float4 y = make_float4(kNone, 0.f, kNone, 0.f);
+            if (members >> lane & 1u)
+                y = lane & 1 ? reinterpret_cast<const float4 *>(ring_o + (lane >> 1) * RING + p.RP * D)[row]
+                             : reinterpret_cast<const float4 *>(p.ws_wml)[ws_at + (lane >> 1) * p.RP + row];
+            const float m1 = warp_max(y.x), v1 = warp_max(y.z);
+            const float sum = warp_sum(y.y * ex2(y.x - m1)), f = ex2(y.z - v1);
+#pragma unroll
+            for (int c = 0; c < (D + 127) / 128; ++c) {
+                const int col = c * 128 + lane * 4;
+                const bool in = col < D;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int x0 = 0; x0 < 2 * kWarps; x0 += 8) {
+                    float4 z[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int x = x0 + k;
+                        z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (in && (members >> x & 1u))
+                            z[k] = *reinterpret_cast<const float4 *>(
+                                x & 1 ? ring_o + (x >> 1) * RING + row * D + col
+                                      : p.ws_wo + (ws_at + (x >> 1) * p.RP + row) * D + col);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float fx = __shfl_sync(0xffffffffu, f, x0 + k);
+                        acc.x = fmaf(fx, z[k].x, acc.x);
+                        acc.y = fmaf(fx, z[k].y, acc.y);
+                        acc.z = fmaf(fx, z[k].z, acc.z);
+                        acc.w = fmaf(fx, z[k].w, acc.w);
+                    }
+                }
+                if (!in) continue;
+                // (of a row tile that began before this block the state is the block's first)
+                const size_t part = ((size_t)blockIdx.x * 2 + (lo == 0 ? 1 : 0)) * p.RP + row;
+                if (whole) store_row<T>(p, (size_t)b * p.Hq + h * p.G + r0 + row, D, col, m1, sum, v1, acc);
+                else *reinterpret_cast<float4 *>(p.ws_o + part * D + col) = acc;
+                if (!whole && col == 0) reinterpret_cast<float4 *>(p.ws_ml)[part] = make_float4(m1, sum, v1, 0.f);
+            }
+        }
+        turn = row - rows;
+        if (threadIdx.x == 0 && !p.whole) {
+            if (lo == 0 && p.by_tile) p.ws_first[tile] = whole ? -1 : (int)blockIdx.x;
+            if (lo == 0 && !whole && !p.by_tile) p.ws_first[blockIdx.x] = tile;
+            if (lo > 0 && hi == n) p.ws_last[tile] = (int)blockIdx.x;
+        }
+        begun |= lo == 0 && !whole;
+    }
+    if (threadIdx.x == 0 && !p.whole && !p.by_tile && !begun) p.ws_first[blockIdx.x] = -1;
 }
 
-// Joins the parts of a split row tile, a row a block, 4 columns a thread.
+// Joins the parts that several blocks left of a row tile: a row a block, 4 columns a thread, the parts in
+// turn over sets of threads that each keep a state of their own, so that states and outputs are read at
+// once (two trips to memory in all: where the parts are, and the parts).
 template <typename T, int D>
-__global__ void __launch_bounds__(128) decode_q8_merge_kernel(const DecodeQ8Params p)
+__global__ void __launch_bounds__(kMergeThreads) decode_q8_merge_kernel(const DecodeQ8Params p)
 {
     constexpr int LPR = D / 4;               // threads of a row
-    __shared__ float2 s_c[128];
+    constexpr int SETS = kMergeThreads / LPR;
+    __shared__ float4 s_o[kMergeThreads], s_m[SETS];
+    const int row = blockIdx.y, tid = threadIdx.x, set = tid / LPR, col = tid % LPR * 4;
     pdl_trigger();
     pdl_wait();
-    const int4 note = p.ws_note[blockIdx.x];
-    if (note.x < 0) return;
-    const int b = note.x / p.HR, hr = note.x - b * p.HR, h = hr / p.RT, r0 = (hr - h * p.RT) * p.RP;
-    const int w0 = note.y, nseg = note.z - w0 + 1;
-    const int rows = min(p.RP, p.G - r0);
-    auto part_of = [&](int i) -> size_t { return (size_t)(w0 + i) * 2 + (i == 0 ? note.w : 0); };
-    const int row = blockIdx.y;
-    if (row >= rows) return;
-    // the tile's maxima, then each part's factors, 128 parts at a time
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int first = p.ws_first[blockIdx.x], tile = p.by_tile ? (int)blockIdx.x : first;
+    int last = p.by_tile ? p.ws_last[tile] : 0;      // (no matter what where the tile is whole)
+    if (first < 0) return;
+    if (!p.by_tile) last = p.ws_last[tile];
+    const int w0 = p.by_tile ? first : (int)blockIdx.x, nseg = last - w0 + 1;
+    const int b = tile / p.HR, hr = tile - b * p.HR, h = hr / p.RT, r0 = (hr - h * p.RT) * p.RP;
+    if (row >= min(p.RP, p.G - r0)) return;
     const float4 *ml = reinterpret_cast<const float4 *>(p.ws_ml);
-    float m = kNone, mv = kNone;
-    for (int i = lane; i < nseg; i += 32) {
-        const float4 y = __ldcg(ml + part_of(i) * p.RP + row);
-        m = fmaxf(m, y.x);
-        mv = fmaxf(mv, y.z);
-    }
-    m = warp_max(m);
-    mv = warp_max(mv);
-    constexpr int SETS = 128 / LPR;          // D = 256 takes the row in 64 threads, two sets of parts
-    const int set = tid / LPR, col = tid % LPR * 4;
-    float l = 0.f;
+    float m = kNone, mv = kNone, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < nseg; i0 += 128) {
-        __syncthreads();
-        if (i0 + tid < nseg) {
-            const float4 y = __ldcg(ml + part_of(i0 + tid) * p.RP + row);
-            s_c[tid] = make_float2(ex2(y.z - mv), y.y * ex2(y.x - m));
+    constexpr int U = 4;
+    for (int i0 = set; i0 < nseg; i0 += SETS * U) {
+        float4 y[U], z[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * SETS;
+            y[u] = make_float4(kNone, 0.f, kNone, 0.f);
+            z[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < nseg) {
+                const size_t part = ((size_t)(w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.RP + row;
+                y[u] = __ldcg(ml + part);
+                z[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + part * D + col));
+            }
         }
-        __syncthreads();
-        const int here = min(128, nseg - i0);
-#pragma unroll 4
-        for (int i = set; i < here; i += SETS) {
-            const float2 c = s_c[i];
-            const float4 y = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + (part_of(i0 + i) * p.RP + row) * D + col));
-            l += c.y;
-            o.x = fmaf(c.x, y.x, o.x);
-            o.y = fmaf(c.x, y.y, o.y);
-            o.z = fmaf(c.x, y.z, o.z);
-            o.w = fmaf(c.x, y.w, o.w);
+        float m1 = m, v1 = mv;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            m1 = fmaxf(m1, y[u].x);
+            v1 = fmaxf(v1, y[u].z);
         }
+        const float f = ex2(mv - v1);
+        l *= ex2(m - m1);
+        o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float g = ex2(y[u].z - v1);
+            l = fmaf(y[u].y, ex2(y[u].x - m1), l);
+            o.x = fmaf(g, z[u].x, o.x);
+            o.y = fmaf(g, z[u].y, o.y);
+            o.z = fmaf(g, z[u].z, o.z);
+            o.w = fmaf(g, z[u].w, o.w);
+        }
+        m = m1;
+        mv = v1;
     }
-    __shared__ float4 s_o[128];
-    __shared__ float s_l[SETS];
     s_o[tid] = o;
-    if (tid % LPR == 0) s_l[set] = l;
+    if (tid % LPR == 0) s_m[set] = make_float4(m, l, mv, 0.f);
     __syncthreads();
     if (set != 0) return;
-    l = s_l[0];
 #pragma unroll
     for (int s = 1; s < SETS; ++s) {
-        const float4 y = s_o[s * LPR + tid];
-        l += s_l[s];
-        o.x += y.x;
-        o.y += y.y;
-        o.z += y.z;
-        o.w += y.w;
+        m = fmaxf(m, s_m[s].x);
+        mv = fmaxf(mv, s_m[s].z);
     }
-    const size_t out_row = (size_t)b * p.Hq + h * p.G + r0 + row;
-    const float f = l == 0.f ? 0.f : ex2(mv - kBoost - m) / l;
-    if (tid == 0 && p.lse != nullptr) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    T *dst = static_cast<T *>(p.out) + out_row * D + col;
-    if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(dst) = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * f, o.y * f), c = __floats2bfloat162_rn(o.z * f, o.w * f);
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) {
+        const float4 y = s_m[s], z = s_o[s * LPR + tid];
+        const float g = ex2(y.z - mv);
+        l = fmaf(y.y, ex2(y.x - m), l);
+        o.x = fmaf(g, z.x, o.x);
+        o.y = fmaf(g, z.y, o.y);
+        o.z = fmaf(g, z.z, o.z);
+        o.w = fmaf(g, z.w, o.w);
     }
+    store_row<T>(p, (size_t)b * p.Hq + h * p.G + r0 + row, D, col, m, l, mv, o);
 }
 
 template <int D, int NT, bool SPLIT>
@@ -688,6 +826,7 @@ cudaError_t launch_typed(DecodeQ8Params p, cudaStream_t stream)
     using PL = Q8Plan<D, NT, SPLIT>;
     using T = typename std::conditional<SPLIT, float, __nv_bfloat16>::type;
     static_assert(PL::STAGES >= 3, "two steps in flight at least");
+    static_assert(8 * NT * (D + 4) * 4 <= PL::STAGES * PL::STAGE, "a part fits its warp's ring");
     static bool configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -698,17 +837,15 @@ cudaError_t launch_typed(DecodeQ8Params p, cudaStream_t stream)
         configured[dev] = true;
     }
     // no more blocks than the capacity can give work
-    const long long tiles = (long long)p.B * p.HR, most = (p.cap + kStep - 1) / kStep + kEnd;
-    const long long ranges = p.whole ? tiles : tiles * most / p.min_units + 1;
-    const long long blocks = std::min<long long>(p.ranges / PL::WARPS, (ranges + PL::WARPS - 1) / PL::WARPS);
-    // few ranges: one a block, so that they spread over the SMs
-    const int grid = (int)std::max<long long>(1, std::min<long long>(p.ranges / PL::WARPS, std::max(blocks, std::min<long long>(ranges, p.n_sm))));
-    p.ranges = grid * PL::WARPS;
-    cudaError_t e = launch_pdl(decode_q8_kernel<D, NT, SPLIT>, dim3((unsigned)grid), dim3(PL::WARPS * 32), PL::SMEM,
+    const long long tiles = (long long)p.B * p.HR, steps = (p.cap + kStep - 1) / kStep;
+    const long long units = tiles * (steps + kEnd);
+    const int grid = (int)std::min<long long>(p.blocks, p.whole ? tiles : units / kMinUnits + 1);
+    p.small = units <= 0x7fffffffLL;
+    cudaError_t e = launch_pdl(decode_q8_kernel<D, NT, SPLIT>, dim3((unsigned)grid), dim3(kWarps * 32), PL::SMEM,
                                stream, p);
     if (e != cudaSuccess || p.whole) return e;
-    return launch_pdl(decode_q8_merge_kernel<T, D>, dim3((unsigned)(p.by_tile ? tiles : p.ranges), (unsigned)p.RP),
-                      dim3(128), 0, stream, p);
+    return launch_pdl(decode_q8_merge_kernel<T, D>, dim3((unsigned)(p.by_tile ? tiles : grid), (unsigned)p.RP),
+                      dim3(kMergeThreads), 0, stream, p);
 }
 
 }  // namespace
@@ -723,23 +860,26 @@ DecodeQ8Plan decode_q8_plan(int B, int Hkv, int G, int D, bool bf16, int n_sm)
     pl.RT = (G + 8 * NT - 1) / (8 * NT);
     pl.RP = G < 8 * NT ? G : 8 * NT;
     const bool two = D <= 128 && NT == 1 && bf16;        // blocks per SM, as Q8Plan says
-    pl.ranges = n_sm * (two ? 2 : 1) * 8;
+    pl.blocks = n_sm * (two ? 2 : 1);
     const long long tiles = (long long)B * Hkv * pl.RT;
-    pl.by_tile = tiles <= pl.ranges;
+    const int most = pl.blocks;
+    pl.by_tile = tiles <= most;
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    const size_t states = (size_t)pl.ranges * 2 * pl.RP;
-    pl.off_note = 0;
-    pl.off_ml = up((size_t)pl.ranges * sizeof(int4));
-    pl.off_o = up(pl.off_ml + states * sizeof(float4));
-    pl.bytes = up(pl.off_o + states * D * sizeof(float));
+    const size_t rows = (size_t)most * 2 * pl.RP, warp_rows = (size_t)most * kWarps * pl.RP;
+    pl.off_first = 0;
+    pl.off_last = up((size_t)most * sizeof(int32_t));
+    pl.off_ml = up(pl.off_last + (size_t)tiles * sizeof(int32_t));
+    pl.off_o = up(pl.off_ml + rows * sizeof(float4));
+    pl.off_wml = up(pl.off_o + rows * D * sizeof(float));
+    pl.off_wo = up(pl.off_wml + warp_rows * sizeof(float4));
+    pl.bytes = up(pl.off_wo + warp_rows * D * sizeof(float));
     return pl;
 }
 
 cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t stream)
 {
-    // Short rows are not split, and then nothing is joined.
+    // Short row tiles stay in one block, and then no second kernel is needed.
     p.whole = (p.cap + kStep - 1) / kStep <= kWholeSteps;
-    p.min_units = kMinUnits;
     if (bf16) {
         const bool wide = tiles_of_8(p.G, D, true) == 2;
         switch (D) {

@@ -387,7 +387,7 @@ struct QkNormParams {
     int32_t tasks, q_tasks;      // warps per token, those of its queries (set by the launch)
     int32_t *dev_code;
 };
-cudaError_t launch_qk_norm_rope(const QkNormParams &p, int D, bool bf16, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(const QkNormParams &p, int D, bool bf16, int n_sm, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------------------
 // Pages of e4m3 numbers with a scale for each page and head.
@@ -425,15 +425,18 @@ struct DecodeQ8Params {
     float *logits;               // nullable
     int64_t logits_stride;
     float *lse;                  // nullable
-    int32_t ranges, min_units, whole, by_tile, n_sm;
-    int4 *ws_note;               // per row tile (by_tile) or range: {row tile or -1, first range, last, slot}
-    float *ws_ml;                // [ranges][2][RP] {m, l, maximum of the value weights, -}
-    float *ws_o;                 // [ranges][2][RP][D]
+    int32_t blocks, whole, by_tile, small;
+    int32_t *ws_first;           // by_tile: the block that a split row tile begins in, else the row tile that
+                                 // is split at a block's end; -1 for none
+    int32_t *ws_last;            // the block that a split row tile ends in
+    float *ws_ml;                // [blocks][2][RP] {m, l, maximum of the value weights, -}
+    float *ws_o;                 // [blocks][2][RP][D]
+    float *ws_wml, *ws_wo;       // the same of a warp's first part: [blocks][8][RP]
     int32_t *dev_code;
 };
 struct DecodeQ8Plan {
-    int32_t RT, RP, ranges, by_tile;
-    size_t off_note, off_ml, off_o, bytes;
+    int32_t RT, RP, blocks, by_tile;
+    size_t off_first, off_last, off_ml, off_o, off_wml, off_wo, bytes;
 };
 DecodeQ8Plan decode_q8_plan(int B, int Hkv, int G, int D, bool bf16, int n_sm);
 cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t stream);
