@@ -843,9 +843,9 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
  * ones -- for those who keep ids elsewhere (a live page need not be in a table).
  * A stack with a bad or doubled id, a table entry that is no live page (KVC_DEV_BAD_BLOCK), n_blocks
  * outside the table (KVC_DEV_BAD_LENGTH) or a top outside the stack (KVC_DEV_POOL_EMPTY): nothing
- * is moved and remap is not written.
+ * is moved and remap is not written.  n_blocks <= 2^20.
  *
- * Each is two kernels.  Workspace of both: kvc_pages_workspace_bytes(), 256-byte aligned; it need not
+ * Each is one kernel, or two where many bytes may be copied.  Workspace of both: kvc_pages_workspace_bytes(), 256-byte aligned; it need not
  * be cleared, and calls that share one must not overlap on the GPU. */
 size_t kvc_pages_workspace_bytes(int32_t batch, int32_t max_blocks, int32_t n_blocks);
 kvc_status kvc_pages_reorder(const kvc_block_pool *pool, float *k_scale, float *v_scale,

@@ -1692,7 +1692,8 @@ kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_tab
                   kvc_paged_append_q8_workspace_bytes(pt->batch, n_tokens, pool->pages.block_size), name);
     if (st != KVC_OK) return st;
     int32_t *code = nullptr;
-    st = device_info(&code, nullptr);
+    int n_sm = 0;
+    st = device_info(&code, &n_sm);
     if (st != KVC_OK) return st;
     kvc::AppendQ8Params p{};
     p.k = static_cast<uint8_t *>(pool->pages.k); p.v = static_cast<uint8_t *>(pool->pages.v);
@@ -1708,7 +1709,7 @@ kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_tab
     p.max_jobs = (int32_t)jobs;
     p.dev_code = code;
     const cudaError_t e =
-        kvc::launch_paged_append_q8(p, dtype == KVC_BF16, static_cast<cudaStream_t>(stream));
+        kvc::launch_paged_append_q8(p, dtype == KVC_BF16, n_sm, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "8-bit append launch");
     return ok();
 }
@@ -1785,13 +1786,12 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
     return ok();
 }
 
-// The workspace of the two page calls: counts, freed ids (three lists when compacting), copies, and the
-// reordered tables.
+// The workspace of the two page calls: counts, ids, copies, and the reordered tables.
 static size_t pages_layout(int B, int mb, int nb, size_t *ids, size_t *copies, size_t *table, size_t *score)
 {
     const size_t entries = (size_t)B * mb;
     *ids = 256;
-    *copies = *ids + align256((size_t)nb * 3 * sizeof(int32_t));
+    *copies = *ids + align256((size_t)nb * sizeof(int32_t));
     *table = *copies + align256((size_t)std::max(B, nb / 2) * sizeof(int4));
     *score = *table + align256(entries * sizeof(int32_t));
     return *score + align256(entries * sizeof(float));
@@ -1821,6 +1821,8 @@ static kvc_status pages_call(const kvc_block_pool *pool, float *ks, float *vs, c
         return fail(KVC_ERR_ALIGN, "%s: shares, pos, parent and remap must be 4-byte aligned", name);
     if (reorder && pt->batch > kvc::kPagesMaxBatch)
         return fail(KVC_ERR_SHAPE, "%s: batch %d > %d", name, pt->batch, kvc::kPagesMaxBatch);
+    if (!reorder && pool->n_blocks > kvc::kPagesMaxPool)
+        return fail(KVC_ERR_SHAPE, "%s: n_blocks %d > %d", name, pool->n_blocks, kvc::kPagesMaxPool);
     st = check_ws(ws, ws_bytes, kvc_pages_workspace_bytes(pt->batch, pt->max_blocks, pool->n_blocks), name);
     if (st != KVC_OK) return st;
     int32_t *code = nullptr;

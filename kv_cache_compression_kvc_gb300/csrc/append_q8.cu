@@ -14,6 +14,8 @@
 // on timing; it writes one job per page that gets rows.  append_q8_rows_kernel, a warp per (job, head,
 // K or V): the rows stay in registers between the maximum and the rounding.  Bound by HBM (2 or 4
 // bytes in, 1 out an element) for prompts, by the latency of the two kernels for single tokens.
+#include <algorithm>
+
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -25,6 +27,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kRowWarps = 4;
+constexpr int kRowBlocks = 4;                // per SM
+constexpr int kCl = 8;                       // blocks of the cluster that takes a small decode step
+constexpr int kStepTasks = 4096;             // (page, head, K or V) of it
 constexpr int kDevBadLen_ = 5;               // KVC_DEV_BAD_LENGTH
 constexpr int kDevBadBlk_ = 9;               // KVC_DEV_BAD_BLOCK
 constexpr int kDevPoolEmpty_ = 10;           // KVC_DEV_POOL_EMPTY
@@ -74,7 +79,7 @@ __device__ __forceinline__ int find_above(const int *a, int n, int x)
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) append_q8_plan_kernel(const AppendQ8Params p)
+__device__ __forceinline__ void append_plan(const AppendQ8Params &p)
 {
     __shared__ int s_warp[64];
     __shared__ int s_need[kPlanThreads];     // pages to pop (then their inclusive scan)
@@ -83,8 +88,6 @@ __global__ void __launch_bounds__(kPlanThreads) append_q8_plan_kernel(const Appe
     __shared__ int s_n[kPlanThreads];        // rows to append
     __shared__ int s_len[kPlanThreads], s_row[kPlanThreads];
     __shared__ int s_top;
-    pdl_trigger();
-    pdl_wait();
     const int tid = threadIdx.x;
     bool bad = false;
     if (p.cu != nullptr)
@@ -228,7 +231,14 @@ __global__ void __launch_bounds__(kPlanThreads) append_q8_plan_kernel(const Appe
     }
 }
 
-// 8 elements of a row, and their largest size as a float's bits (NaN counts as nothing).
+__global__ void __launch_bounds__(kPlanThreads) append_q8_plan_kernel(const AppendQ8Params p)
+{
+    pdl_trigger();
+    pdl_wait();
+    append_plan(p);
+}
+
+// 8 elements of a row, and the largest size among them and `a` (NaN counts as nothing).
 template <typename T>
 struct Row8;
 template <>
@@ -241,6 +251,18 @@ struct Row8<__nv_bfloat16> {
         f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x); f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);
         f[4] = bf16_lo(w.z); f[5] = bf16_hi(w.z); f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
     }
+    using Max = __nv_bfloat162;              // of the even and of the odd elements
+    static __device__ __forceinline__ Max none() { return __floats2bfloat162_rn(0.f, 0.f); }
+    __device__ __forceinline__ void widen(Max &m) const
+    {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = x[i] & 0x7fff7fffu;
+            m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162 *>(&a));
+        }
+    }
+    static __device__ __forceinline__ float size(Max m) { return fmaxf(__low2float(m), __high2float(m)); }
 };
 template <>
 struct Row8<float> {
@@ -258,6 +280,16 @@ struct Row8<float> {
         f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
         f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
     }
+    using Max = float;
+    static __device__ __forceinline__ Max none() { return 0.f; }
+    __device__ __forceinline__ void widen(Max &m) const
+    {
+        float f[8];
+        get(f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
+    }
+    static __device__ __forceinline__ float size(Max m) { return m; }
 };
 
 // The smallest power of two s >= 2^-120 with amax / s <= 448 = 1.75 * 2^8 (2^119 at most: beyond
@@ -276,22 +308,17 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
     return lo | hi << 16;
 }
 
-// NV: vectors of 8 elements that a lane holds at once.
+// One task: a page's new rows of a head, keys or values, by a warp.  NV: vectors of 8 elements that a lane
+// holds at once.
 template <typename T, int D, int NV>
-__global__ void __launch_bounds__(kRowWarps * 32) append_q8_rows_kernel(const AppendQ8Params p)
+__device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, int rest)
 {
     constexpr int VPR = D / 8;               // vectors per row
     const int lane = threadIdx.x & 31;
-    const long long task = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-    pdl_trigger();
-    pdl_wait();
-    const int job = (int)(task / (2 * p.H)), rest = (int)(task - (long long)job * (2 * p.H));
-    if (job >= *p.n_jobs) return;
-    const int4 j = p.jobs[job];
     const int h = rest >> 1, held = j.y, n_vec = j.w * VPR;
     const bool is_v = rest & 1;
-    const T *src = static_cast<const T *>(is_v ? p.v_new : p.k_new) + h * p.new_sh;
     const int64_t st = p.new_st;
+    const T *src = static_cast<const T *>(is_v ? p.v_new : p.k_new) + h * p.new_sh + j.z * st;
     const size_t page = (size_t)h * p.n_pool + j.x;
     uint8_t *dst = (is_v ? p.v : p.k) + page * p.bs * D;
     float *scale = (is_v ? p.vs : p.ks) + page;
@@ -299,25 +326,28 @@ __global__ void __launch_bounds__(kRowWarps * 32) append_q8_rows_kernel(const Ap
 
     Row8<T> x[NV];
     auto fetch = [&](int v0) {
+        if (n_vec - v0 >= 32 * NV) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = v0 + i * 32 + lane;
+                x[i].load(src + v / VPR * st + v % VPR * 8);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = v0 + i * 32 + lane;
-            if (v < n_vec) x[i].load(src + (int64_t)(j.z + v / VPR) * st + v % VPR * 8);
+            if (v < n_vec) x[i].load(src + v / VPR * st + v % VPR * 8);
             else x[i].zero();
         }
     };
-    float amax = 0.f;
+    typename Row8<T>::Max big = Row8<T>::none();
     for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
         fetch(v0);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float f[8];
-            x[i].get(f);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
-        }
+        for (int i = 0; i < NV; ++i) x[i].widen(big);
     }
-    amax = warp_max(amax);
+    float amax = warp_max(Row8<T>::size(big));
     const bool inf = amax == INFINITY;       // then the largest finite one counts
     if (inf) {
         amax = 0.f;
@@ -357,56 +387,98 @@ __global__ void __launch_bounds__(kRowWarps * 32) append_q8_rows_kernel(const Ap
     const bool power = (__float_as_uint(s) & 0x7fffffu) == 0u;   // then x * inv is x / s
     for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
         if (n_vec > 32 * NV || inf) fetch(v0);
+        uint8_t *to = dst + (size_t)held * D + (size_t)(v0 + lane) * 8;
+        const int in = n_vec - v0 - lane;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = v0 + i * 32 + lane;
             float f[8];
             x[i].get(f);
-            if (inf)
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (fabsf(f[k]) == INFINITY) f[k] = __uint_as_float(0x7fc00000u);
-            if (power)
+            if (power && !inf) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) f[k] *= inv;
-            else
+            } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] = f[k] / s;
-            if (v < n_vec)
-                *reinterpret_cast<uint2 *>(dst + (size_t)held * D + (size_t)v * 8) =
+                for (int k = 0; k < 8; ++k) f[k] = fabsf(f[k]) == INFINITY ? __uint_as_float(0x7fc00000u) : f[k] / s;
+            }
+            if (i * 32 < in)
+                *reinterpret_cast<uint2 *>(to + i * 256) =
                     make_uint2(pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]));
         }
     }
 }
 
+// Tasks (job, head, K or V) w, w + n_w, ... of warp w; the next task's job is read ahead.
+template <typename T, int D, int NV>
+__device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long w, long long n_w)
+{
+    const unsigned per = 2u * (unsigned)p.H;
+    const long long tasks = (long long)__ldcg(p.n_jobs) * per;
+    if (w >= tasks) return;
+    unsigned job = (unsigned)(w / per);
+    int4 j = __ldcg(p.jobs + job);
+    for (; w < tasks; w += n_w) {
+        const int rest = (int)(w - (long long)job * per);
+        const unsigned job1 = (unsigned)((unsigned long long)(w + n_w) / per);
+        int4 j1 = j;
+        if (job1 != job && w + n_w < tasks) j1 = __ldcg(p.jobs + job1);
+        quantise<T, D, NV>(p, j, rest);
+        job = job1;
+        j = j1;
+    }
+}
+
+template <typename T, int D, int NV>
+__global__ void __launch_bounds__(kRowWarps * 32) append_q8_rows_kernel(const AppendQ8Params p)
+{
+    pdl_trigger();
+    pdl_wait();
+    quantise_all<T, D, NV>(p, (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5), (long long)gridDim.x * kRowWarps);
+}
+
+// Both steps in one cluster, for few rows.
 template <typename T, int D>
-cudaError_t rows_typed(const AppendQ8Params &p, cudaStream_t stream)
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) append_q8_step_kernel(const AppendQ8Params p)
+{
+    pdl_trigger();
+    pdl_wait();
+    if (blockIdx.x == 0) append_plan(p);
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // warps of a block take tasks of different jobs: a block's share is no smaller where jobs are few
+    quantise_all<T, D, 1>(p, (long long)(threadIdx.x >> 5) * kCl + blockIdx.x, kCl * (kPlanThreads / 32));
+}
+
+template <typename T, int D>
+cudaError_t append_typed(const AppendQ8Params &p, int n_sm, cudaStream_t stream)
 {
     const long long tasks = (long long)p.max_jobs * 2 * p.H;
-    const dim3 grid((unsigned)(tasks > 0 ? (tasks + kRowWarps - 1) / kRowWarps : 1)), block(kRowWarps * 32);
+    if (p.cu == nullptr && tasks <= kStepTasks)
+        return launch_pdl(append_q8_step_kernel<T, D>, dim3(kCl), dim3(kPlanThreads), 0, stream, p);
+    const cudaError_t e = launch_pdl(append_q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+    if (e != cudaSuccess) return e;
+    const long long blocks = (tasks + kRowWarps - 1) / kRowWarps, most = (long long)n_sm * kRowBlocks;
+    const dim3 grid((unsigned)std::max(1LL, std::min(blocks, most))), block(kRowWarps * 32);
     // a page of 32 rows of 128 elements is 16 vectors a lane, which is what registers hold in bf16
     constexpr int NV = sizeof(T) == 2 ? 16 : 8;
     if (p.cu == nullptr) return launch_pdl(append_q8_rows_kernel<T, D, 1>, grid, block, 0, stream, p);
     return launch_pdl(append_q8_rows_kernel<T, D, NV>, grid, block, 0, stream, p);
 }
 template <typename T>
-cudaError_t rows_dims(const AppendQ8Params &p, cudaStream_t stream)
+cudaError_t append_dims(const AppendQ8Params &p, int n_sm, cudaStream_t stream)
 {
     switch (p.D) {
-    case 64: return rows_typed<T, 64>(p, stream);
-    case 128: return rows_typed<T, 128>(p, stream);
-    default: return rows_typed<T, 256>(p, stream);
+    case 64: return append_typed<T, 64>(p, n_sm, stream);
+    case 128: return append_typed<T, 128>(p, n_sm, stream);
+    default: return append_typed<T, 256>(p, n_sm, stream);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_append_q8(const AppendQ8Params &p, bool bf16, cudaStream_t stream)
+cudaError_t launch_paged_append_q8(const AppendQ8Params &p, bool bf16, int n_sm, cudaStream_t stream)
 {
-    const cudaError_t e =
-        launch_pdl(append_q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
-    if (e != cudaSuccess) return e;
-    return bf16 ? rows_dims<__nv_bfloat16>(p, stream) : rows_dims<float>(p, stream);
+    return bf16 ? append_dims<__nv_bfloat16>(p, n_sm, stream) : append_dims<float>(p, n_sm, stream);
 }
 
 }  // namespace kvc

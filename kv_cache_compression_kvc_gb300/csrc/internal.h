@@ -409,7 +409,7 @@ struct AppendQ8Params {
     int32_t max_jobs;
     int32_t *dev_code;
 };
-cudaError_t launch_paged_append_q8(const AppendQ8Params &p, bool bf16, cudaStream_t stream);
+cudaError_t launch_paged_append_q8(const AppendQ8Params &p, bool bf16, int n_sm, cudaStream_t stream);
 
 struct DecodeQ8Params {
     const void *q;               // [B][Hq][D], bf16 or fp32
@@ -445,6 +445,7 @@ cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t st
 // ------------------------------------------------------------------------------------------
 // Pages shared between sequences, pools made dense.
 constexpr int kPagesMaxBatch = 8192;         // sequences that pages_reorder_kernel holds in shared memory
+constexpr int kPagesMaxPool = 1 << 20;       // pages that pages_compact_kernel holds there, a bit each
 struct PagesParams {
     char *k, *v;                 // pool [H][n_pool][bs][row_bytes]
     float *ks, *vs;              // nullable [H][n_pool]
@@ -458,13 +459,14 @@ struct PagesParams {
     const int32_t *parent;       // reorder: [B]
     int32_t *remap;              // compaction: [n_pool]
     int32_t *ws_n;               // copies, error, the blocks' counts
-    int32_t *ws_ids;             // reorder: [n_pool] freed pages; compaction: [3][n_pool]
+    int32_t *ws_ids;             // [n_pool]: freed pages, or free pages below the number of live ones
     int4 *ws_copies;             // {from, to, rows, -}: reorder [B], compaction [n_pool / 2]
     int32_t *ws_table;           // reorder: [B][max_blocks]
     float *ws_score;
+    int32_t fused;               // the copies follow in the same kernel
     int32_t *dev_code;
 };
-cudaError_t launch_pages_reorder(const PagesParams &p, int n_sm, cudaStream_t stream);
-cudaError_t launch_pages_compact(const PagesParams &p, int n_sm, cudaStream_t stream);
+cudaError_t launch_pages_reorder(PagesParams p, int n_sm, cudaStream_t stream);
+cudaError_t launch_pages_compact(PagesParams p, int n_sm, cudaStream_t stream);
 
 }  // namespace kvc

@@ -30,6 +30,7 @@ constexpr int kCl = 8;                       // blocks of the cluster
 constexpr int kThreads = 1024;
 constexpr int kAll = kCl * kThreads;
 constexpr int kCopyThreads_ = 256;
+constexpr long long kFusedBytes = 1 << 20;
 constexpr int kBadIndex = 3, kBadLength = 5, kBadBlock = 9, kPoolEmpty = 10, kPoolOverflow = 11, kSharedPage = 12;
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -83,6 +84,45 @@ __device__ __forceinline__ void each_entry(int B, int max_blocks, int rank, N n,
             c -= per;
             ++b;
         }
+    }
+}
+
+// Job (copy c, head h): rows of keys and values from page to page, with their scales; head 0 takes the
+// tokens' positions along.  Blocks first, first + stride, ... of THREADS threads each take a job.
+template <int THREADS>
+__device__ __forceinline__ void copy_pages(const PagesParams &p, int n_copies, int first, int stride)
+{
+    const long long jobs = (long long)n_copies * p.H;
+    const size_t page_bytes = (size_t)p.bs * p.row_bytes;
+    for (long long j = first; j < jobs; j += stride) {
+        const int c = (int)(j / p.H), h = (int)(j - (long long)c * p.H);
+        const int4 what = __ldcg(p.ws_copies + c);
+        const size_t from = (size_t)h * p.n_pool + what.x, to = (size_t)h * p.n_pool + what.y;
+        const int n = what.z * (p.row_bytes / 16);         // vectors of keys, then as many of values
+        constexpr int U = 4;
+        for (int i0 = threadIdx.x; i0 < 2 * n; i0 += THREADS * U) {
+            uint4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * THREADS;
+                if (i < 2 * n)
+                    x[u] = ld_stream_16((i < n ? p.k : p.v) + from * page_bytes + (size_t)(i < n ? i : i - n) * 16);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * THREADS;
+                if (i < 2 * n)
+                    *reinterpret_cast<uint4 *>((i < n ? p.k : p.v) + to * page_bytes +
+                                               (size_t)(i < n ? i : i - n) * 16) = x[u];
+            }
+        }
+        if (threadIdx.x == 0 && p.ks != nullptr) {
+            p.ks[to] = p.ks[from];
+            p.vs[to] = p.vs[from];
+        }
+        if (h == 0 && p.pos != nullptr)
+            for (int i = threadIdx.x; i < what.z; i += THREADS)
+                p.pos[(size_t)what.y * p.bs + i] = p.pos[(size_t)what.x * p.bs + i];
     }
 }
 
@@ -254,145 +294,151 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
             *p.free_top = new_top;
         }
     }
+    if (p.fused) {
+        cluster_barrier();
+        copy_pages<kThreads>(p, n_copies, rank, kCl);
+    }
 }
+
+// Free pages as bits of shared memory, which every block of the cluster sets for itself from the whole
+// stack, and how many of them lie below a page: thread t keeps the count before its `per` words in s_before.
+struct FreeBits {
+    const uint32_t *bits;
+    const int *before;
+    int per, n_live;
+    __device__ __forceinline__ bool get(int x) const { return bits[x >> 5] >> (x & 31) & 1u; }
+    __device__ __forceinline__ int below(int x) const
+    {
+        const int word = x >> 5, t = word / per;
+        int n = before[t] + __popc(bits[word] & ((1u << (x & 31)) - 1u));
+        for (int w = t * per; w < word; ++w) n += __popc(bits[w]);
+        return n;
+    }
+    // the number of a live page with an id >= n_live among those
+    __device__ __forceinline__ int rank_high(int x, int holes) const { return x - n_live - (below(x) - holes); }
+};
 
 __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_compact_kernel(const PagesParams p)
 {
-    __shared__ int s_warp[32];
-    const int tid = threadIdx.x, rank = (int)cluster_rank(), all_tid = rank * kThreads + tid;
+    extern __shared__ int s_seq[];           // the bits
+    __shared__ int s_warp[32], s_before[kThreads], s_holes;
+    const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster_rank(), all_tid = rank * kThreads + tid;
+    uint32_t *bits = reinterpret_cast<uint32_t *>(s_seq);
+    const int words = (p.n_pool + 31) / 32, per = (words + kThreads - 1) / kThreads;
+    for (int w = tid; w < words; w += kThreads) bits[w] = 0u;
     pdl_trigger();
     pdl_wait();
     const int top = *p.free_top;
-    int *mark = p.ws_ids, *holes = p.ws_ids + p.n_pool, *high = p.ws_ids + 2 * (size_t)p.n_pool;
-    if (all_tid == 0) {
-        p.ws_n[0] = 0;                       // moves
-        p.ws_n[1] = 0;                       // what is wrong
-    }
-    for (int x = all_tid; x < p.n_pool; x += kAll) mark[x] = 0;
-    cluster_barrier();
-    const bool bad_top = top < 0 || top > p.free_cap || top > p.n_pool;
-    if (bad_top) {
-        if (all_tid == 0) record_code(p.dev_code, kPoolEmpty);
-        return;
-    }
+    int code = top < 0 || top > p.free_cap || top > p.n_pool ? kPoolEmpty : 0;
     const int n_live = p.n_pool - top;
-    for (int i = all_tid; i < top; i += kAll) {
-        const int id = p.free_ids[i];
-        if (id < 0 || id >= p.n_pool || atomicExch(&mark[id], 1) != 0) atomicCAS(&p.ws_n[1], 0, kBadBlock);
+    __syncthreads();
+    if (code == 0) {
+        bool bad = false;
+        for (int i = tid; i < top; i += kThreads) {
+            const int id = p.free_ids[i];
+            const bool in = id >= 0 && id < p.n_pool;
+            bad |= !in || (atomicOr(&bits[in ? id >> 5 : 0], in ? 1u << (id & 31) : 0u) >> (id & 31) & 1u);
+        }
+        if (__syncthreads_or(bad)) code = kBadBlock;
     }
-    cluster_barrier();
+    // ---- the tables, each block its part ----
     auto entries = [&](int b) {
         const int n = p.n_blocks[b];
         return n < 0 || n > p.max_blocks ? 0 : n;
     };
-    each_entry(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
-        const int id = p.table[(size_t)b * p.max_blocks + i];
-        if (id < 0 || id >= p.n_pool || __ldcg(&mark[id]) != 0) atomicCAS(&p.ws_n[1], 0, kBadBlock);
-    });
-    for (int b = all_tid; b < p.B; b += kAll) {
-        const int n = p.n_blocks[b];
-        if (n < 0 || n > p.max_blocks) atomicCAS(&p.ws_n[1], 0, kBadLength);
+    if (code == 0) {
+        int c = 0;
+        each_entry(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
+            const int id = p.table[(size_t)b * p.max_blocks + i];
+            if (id < 0 || id >= p.n_pool || (bits[id >> 5] >> (id & 31) & 1u)) c = max(c, kBadBlock);
+        });
+        for (int b = all_tid; b < p.B; b += kAll) {
+            const int n = p.n_blocks[b];
+            if (n < 0 || n > p.max_blocks) c = max(c, kBadLength);
+        }
+        c = __reduce_max_sync(0xffffffffu, c);
+        __syncthreads();                     // (s_warp is free)
+        if (lane == 0) s_warp[tid >> 5] = c;
+        __syncthreads();
+        code = __reduce_max_sync(0xffffffffu, s_warp[lane]);
+        __syncthreads();
     }
-    // ---- free pages below the number of live ones, live pages beyond it: equally many ----
-    const int x0 = (int)((long long)p.n_pool * rank / kCl), x1 = (int)((long long)p.n_pool * (rank + 1) / kCl);
-    int n_hole = 0, n_high = 0;
-    for (int c = x0; c < x1; c += kThreads) {
-        const int x = c + tid;
-        const bool in = x < x1, free_page = in && __ldcg(&mark[x]) != 0;
-        n_hole += __syncthreads_count(free_page && x < n_live);
-        n_high += __syncthreads_count(in && !free_page && x >= n_live);
+    if (tid == 0) p.ws_n[2 + rank] = code;
+    // ---- free pages before every thread's words, and below the number of live pages: the holes ----
+    int own = 0;
+    for (int w = tid * per; w < min(words, (tid + 1) * per); ++w) own += __popc(bits[w]);
+    int incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
     }
-    if (tid == 0) {
-        p.ws_n[2 + 2 * rank] = n_hole;
-        p.ws_n[3 + 2 * rank] = n_high;
+    if (lane == 31) s_warp[tid >> 5] = incl;
+    __syncthreads();
+    int warps = s_warp[lane];
+    const int mine = warps;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, warps, o);
+        if (lane >= o) warps += y;
+    }
+    const int first = __shfl_sync(0xffffffffu, warps - mine, tid >> 5) + incl - own;
+    s_before[tid] = first;
+    if (tid == 0) s_holes = top;             // (with no page from n_live on: none is free either)
+    __syncthreads();
+    const FreeBits f{bits, s_before, per, n_live};
+    if (tid == 0 && code == 0 && n_live < p.n_pool) s_holes = f.below(n_live);
+    // the holes in order, each block the words of its threads' share
+    if (code == 0 && tid % kCl == rank) {
+        int r = first;
+        for (int w = tid * per; w < min(words, (tid + 1) * per); ++w)
+            for (uint32_t m = bits[w]; m != 0; m &= m - 1) {
+                const int x = w * 32 + __ffs(m) - 1;
+                if (x < n_live) p.ws_ids[r] = x;
+                ++r;
+            }
     }
     cluster_barrier();
-    const int code = __ldcg(&p.ws_n[1]);
-    if (code != 0) {                         // nothing has changed yet
+#pragma unroll
+    for (int r = 0; r < kCl; ++r) code = max(code, __ldcg(&p.ws_n[2 + r]));
+    const int holes = s_holes;
+    if (all_tid == 0) p.ws_n[0] = code == 0 ? holes : 0;       // moves
+    if (code != 0) {                         // nothing has changed
         if (all_tid == 0) record_code(p.dev_code, code);
         return;
     }
-    int hole0 = 0, high0 = 0, moves = 0;
-#pragma unroll
-    for (int r = 0; r < kCl; ++r) {
-        const int a = __ldcg(&p.ws_n[2 + 2 * r]), b = __ldcg(&p.ws_n[3 + 2 * r]);
-        if (r < rank) {
-            hole0 += a;
-            high0 += b;
+    for (int x = all_tid; x < p.n_pool; x += kAll) {
+        const bool free_page = f.get(x);
+        int to = free_page ? -1 : x;
+        if (!free_page && x >= n_live) {
+            const int k = f.rank_high(x, holes);
+            to = __ldcg(&p.ws_ids[k]);
+            p.ws_copies[k] = make_int4(x, to, p.bs, 0);
+            if (p.shares != nullptr) {
+                p.shares[to] = p.shares[x];
+                p.shares[x] = 0;
+            }
         }
-        moves += a;
-    }
-    for (int c = x0; c < x1; c += kThreads) {
-        const int x = c + tid;
-        const bool in = x < x1, free_page = in && __ldcg(&mark[x]) != 0;
-        const bool hole = free_page && x < n_live, up = in && !free_page && x >= n_live;
-        int all;
-        int r = hole0 + block_rank(hole, s_warp, &all);
-        hole0 += all;
-        if (hole) holes[r] = x;
-        r = high0 + block_rank(up, s_warp, &all);
-        high0 += all;
-        if (up) high[r] = x;
-        else if (in) p.remap[x] = free_page ? -1 : x;
-    }
-    cluster_barrier();
-    for (int k = all_tid; k < moves; k += kAll) {
-        const int from = __ldcg(&high[k]), to = __ldcg(&holes[k]);
-        p.ws_copies[k] = make_int4(from, to, p.bs, 0);
-        p.remap[from] = to;
-        if (p.shares != nullptr) {
-            p.shares[to] = p.shares[from];
-            p.shares[from] = 0;
-        }
+        p.remap[x] = to;
     }
     // the stack hands out the lowest free page first
     for (int i = all_tid; i < top; i += kAll) p.free_ids[i] = p.n_pool - 1 - i;
-    if (all_tid == 0) p.ws_n[0] = moves;
-    cluster_barrier();
     each_entry(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
         int32_t *e = p.table + (size_t)b * p.max_blocks + i;
-        *e = __ldcg(&p.remap[*e]);
+        const int x = *e;
+        if (x >= n_live) *e = __ldcg(&p.ws_ids[f.rank_high(x, holes)]);
     });
+    if (p.fused) {
+        cluster_barrier();
+        copy_pages<kThreads>(p, holes, rank, kCl);
+    }
 }
 
-// Job (copy c, head h): rows of keys and values from page to page, with their scales; head 0 takes the
-// tokens' positions along.
 __global__ void __launch_bounds__(kCopyThreads_) pages_copy_kernel(const PagesParams p)
 {
     pdl_trigger();
     pdl_wait();
-    const long long jobs = (long long)*p.ws_n * p.H;
-    const size_t page_bytes = (size_t)p.bs * p.row_bytes;
-    for (long long j = blockIdx.x; j < jobs; j += gridDim.x) {
-        const int c = (int)(j / p.H), h = (int)(j - (long long)c * p.H);
-        const int4 what = p.ws_copies[c];
-        const size_t from = (size_t)h * p.n_pool + what.x, to = (size_t)h * p.n_pool + what.y;
-        const int n = what.z * (p.row_bytes / 16);         // vectors of keys, then as many of values
-        constexpr int U = 4;
-        for (int i0 = threadIdx.x; i0 < 2 * n; i0 += kCopyThreads_ * U) {
-            uint4 x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * kCopyThreads_;
-                if (i < 2 * n)
-                    x[u] = ld_stream_16((i < n ? p.k : p.v) + from * page_bytes + (size_t)(i < n ? i : i - n) * 16);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * kCopyThreads_;
-                if (i < 2 * n)
-                    *reinterpret_cast<uint4 *>((i < n ? p.k : p.v) + to * page_bytes +
-                                               (size_t)(i < n ? i : i - n) * 16) = x[u];
-            }
-        }
-        if (threadIdx.x == 0 && p.ks != nullptr) {
-            p.ks[to] = p.ks[from];
-            p.vs[to] = p.vs[from];
-        }
-        if (h == 0 && p.pos != nullptr)
-            for (int i = threadIdx.x; i < what.z; i += kCopyThreads_)
-                p.pos[(size_t)what.y * p.bs + i] = p.pos[(size_t)what.x * p.bs + i];
-    }
+    copy_pages<kCopyThreads_>(p, *p.ws_n, blockIdx.x, gridDim.x);
 }
 
 // `copies`: the most that there can be.
@@ -402,30 +448,44 @@ cudaError_t launch_copies(const PagesParams &p, long long copies, int n_sm, cuda
     const long long blocks = jobs < 1 ? 1 : (jobs < most ? jobs : most);
     return launch_pdl(pages_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads_), 0, stream, p);
 }
+// Few bytes are copied by the cluster itself, without a second kernel.
+bool copies_fit(const PagesParams &p, long long copies)
+{
+    return copies * p.H * p.bs * p.row_bytes * 2 <= kFusedBytes;
+}
+
+cudaError_t configure(const void *kernel, int bytes, bool *configured)
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || configured[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) configured[dev] = true;
+    return e;
+}
 
 }  // namespace
 
-cudaError_t launch_pages_reorder(const PagesParams &p, int n_sm, cudaStream_t stream)
+cudaError_t launch_pages_reorder(PagesParams p, int n_sm, cudaStream_t stream)
 {
-    const size_t smem = (size_t)p.B * 6 * sizeof(int);
     static bool configured[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !configured[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            pages_reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPagesMaxBatch * 6 * (int)sizeof(int));
-        if (e != cudaSuccess) return e;
-        configured[dev] = true;
-    }
-    const cudaError_t e = launch_pdl(pages_reorder_kernel, dim3(kCl), dim3(kThreads), smem, stream, p);
+    cudaError_t e = configure(reinterpret_cast<const void *>(pages_reorder_kernel),
+                              kPagesMaxBatch * 6 * (int)sizeof(int), configured);
     if (e != cudaSuccess) return e;
+    p.fused = copies_fit(p, p.B);
+    e = launch_pdl(pages_reorder_kernel, dim3(kCl), dim3(kThreads), (size_t)p.B * 6 * sizeof(int), stream, p);
+    if (e != cudaSuccess || p.fused) return e;
     return launch_copies(p, p.B, n_sm, stream);
 }
 
-cudaError_t launch_pages_compact(const PagesParams &p, int n_sm, cudaStream_t stream)
+cudaError_t launch_pages_compact(PagesParams p, int n_sm, cudaStream_t stream)
 {
-    const cudaError_t e = launch_pdl(pages_compact_kernel, dim3(kCl), dim3(kThreads), 0, stream, p);
+    static bool configured[64] = {};
+    cudaError_t e = configure(reinterpret_cast<const void *>(pages_compact_kernel), kPagesMaxPool / 8, configured);
     if (e != cudaSuccess) return e;
+    p.fused = copies_fit(p, p.n_pool / 2);
+    e = launch_pdl(pages_compact_kernel, dim3(kCl), dim3(kThreads), (size_t)((p.n_pool + 31) / 32) * 4, stream, p);
+    if (e != cudaSuccess || p.fused) return e;
     return launch_copies(p, p.n_pool / 2, n_sm, stream);
 }
 

@@ -1083,42 +1083,46 @@ def kvc_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, *, w_q: Optional[torch.Te
     """q [T, Hq, D], k [T, Hkv, D] (rows contiguous, any strides) -> (q_out, k_out): RMS norm of every
     row by w_q, w_k [D], then the rotation of its first d_rot elements to pos int32 [T], with
     cos_sin fp32 [n_pos, 2, d_rot/2] (kvc_rope_table).  q_out=q, k_out=k: in place."""
-    dt, index = q.dtype, q.get_device()
-    code = _dtype_code(dt)
-    if q.dim() != 3:
-        raise ValueError(f"q must be [T, n_heads_q, d_head], got {list(q.shape)}")
-    T, Hq, D = q.shape
-    if index < 0 or index != torch._C._cuda_getDevice():
+    dt, index, shape = q.dtype, q.get_device(), q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [T, n_heads_q, d_head], got {list(shape)}")
+    if index != torch._C._cuda_getDevice():
         _on_current(index, None, "q")
+    T, Hq, D = shape
     r = kvc_qk_rows()
     r.q, r.q_stride_token, r.q_stride_head = _rows_of(q, "q", dt, T, D, index)
     r.k, r.k_stride_token, r.k_stride_head = _rows_of(k, "k", dt, T, D, index)
-    _need(w_q, "w_q", dt, (D,), index)
-    _need(w_k, "w_k", dt, (D,), index)
+    wq = wk = table = at = None
     n_pos = 0
+    if w_q is not None:
+        _need(w_q, "w_q", dt, (D,), index)
+        wq = w_q.data_ptr()
+    if w_k is not None:
+        _need(w_k, "w_k", dt, (D,), index)
+        wk = w_k.data_ptr()
     if cos_sin is not None:
         if cos_sin.dim() != 3 or pos is None:
             raise ValueError("a rotation needs cos_sin [n_pos, 2, d_rot/2] and pos [T]")
         n_pos, _, half = cos_sin.shape
         _need(cos_sin, "cos_sin", torch.float32, (n_pos, 2, half), index)
         _need(pos, "pos", torch.int32, (T,), index)
+        table, at = cos_sin.data_ptr(), pos.data_ptr()
         r.d_rot = 2 * half
     elif pos is not None:
         raise ValueError("positions need a table (cos_sin)")
-    with _on(stream, q_out, k_out):
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=dt, device=q.device)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError(f"outputs {list(q_out.shape)}, {list(k_out.shape)} for rows {list(q.shape)}, {list(k.shape)}")
+    Hkv = k.shape[1]
+    if q_out is None or k_out is None:
+        with _on(stream):
+            if q_out is None:
+                q_out = torch.empty(shape, dtype=dt, device=q.device)
+            if k_out is None:
+                k_out = torch.empty((T, Hkv, D), dtype=dt, device=q.device)
     r.q_out, r.q_out_stride_token, r.q_out_stride_head = _rows_of(q_out, "q_out", dt, T, D, index)
     r.k_out, r.k_out_stride_token, r.k_out_stride_head = _rows_of(k_out, "k_out", dt, T, D, index)
-    r.dtype, r.n_tokens, r.n_heads_q, r.n_heads_kv, r.d_head = code, T, Hq, k.shape[1], D
-    status = (_lib or load()).kvc_qk_norm_rope(
-        r, None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), eps,
-        None if cos_sin is None else cos_sin.data_ptr(), None if pos is None else pos.data_ptr(), n_pos,
-        _raw_stream(index, stream))
+    if q_out.shape[1] != Hq or k_out.shape[1] != Hkv:
+        raise ValueError(f"outputs {list(q_out.shape)}, {list(k_out.shape)} for rows {list(shape)}, {list(k.shape)}")
+    r.dtype, r.n_tokens, r.n_heads_q, r.n_heads_kv, r.d_head = _dtype_code(dt), T, Hq, Hkv, D
+    status = (_lib or load()).kvc_qk_norm_rope(r, wq, wk, eps, table, at, n_pos, _raw_stream(index, stream))
     if status:
         _check(status)
     return q_out, k_out
