@@ -45,6 +45,7 @@ constexpr int kEnd = 2;                      // steps that the end of a row tile
 constexpr int kWarps = 8;
 constexpr int kMergeThreads = 256;
 constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block
+constexpr int kWholeWait = 20;               // and longer ones where the fullest block has so many above the mean
 constexpr int kMinUnits = 16;                // units that a block is worth at least
 constexpr float kSlack = 8.f;                // a maximum rises when it is passed by 2^8
 constexpr float kBoost = 6.f;                // weights are held times 2^6: at most 2^15, exact down to 2^-20
@@ -77,6 +78,15 @@ __device__ __forceinline__ void mma_16816(float *c, const uint32_t *a, uint32_t 
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The same onto zero.
+__device__ __forceinline__ void mma_16816_new(float *c, const uint32_t *a, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x)
 {
@@ -303,8 +313,10 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
 
     // ---- copies: one step ahead by step into the ring ----
     Walk ld(p, range);
+    const Walk first = ld;
     int page_at = -1, pages = 0;             // the 32 table entries in this warp's lanes: first one's number
-    int ld_b = -1;
+    int ld_b = -1, ld_hr = -1;
+    long long head = 0;                      // the loaded row tile's head's first page
     const int32_t *tab = p.table;
     // where this lane's chunk i * 32 + lane of a step's rows goes: chunk c of row r lies at c ^ 4 (r & 1) for
     // keys and at c ^ 2 (r / 2 & 3) for values (64 dims: c and c ^ 2 (r / 2 & 1)), which keeps the
@@ -330,9 +342,13 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 if (valid > 0 && lane == 0) record_code(p.dev_code, kDevBadBlk_);
                 id = 0;
             }
-            const size_t page = (size_t)(ld.hr / p.RT) * p.n_pool + id;
-            const size_t at = (page * p.bs + (pos - lb * p.bs)) * D;
-            const uint8_t *k = p.k + at + lane * 16, *v = p.v + at + lane * 16;
+            if (ld.hr != ld_hr) {            // (a division, once a row tile)
+                ld_hr = ld.hr;
+                head = (long long)(p.RT == 1 ? ld.hr : ld.hr / p.RT) * p.n_pool;
+            }
+            const long long page = head + id;
+            const long long at = (page * p.bs + (pos - lb * p.bs)) * D + lane * 16;
+            const uint8_t *k = p.k + at, *v = p.v + at;
             if (valid == kStep) {
 #pragma unroll
                 for (int i = 0; i < CPR / 2; ++i) {
@@ -501,6 +517,13 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             }
     };
 
+    if (first.more()) {    // (while the first steps are on their way)
+        cur_b = first.b;
+        cur_hr = first.hr;
+        cur_len = first.len;
+        first_step = first.step;
+        begin(cur_b, cur_hr);
+    }
     int slot = 0, put = S - 1;
 #pragma unroll 1
     for (;;) {
@@ -530,10 +553,6 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         // ---- S^T = K Q^T: slots g and g + 8 of the step, rows 2t and 2t + 1 of the tile ----
         float c[NT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c[nt][i >> 2][i & 3] = 0.f;
-#pragma unroll
         for (int h = 0; h < KC; ++h) {
             const int ch = t + 4 * h, sw = D == 64 ? ch : ch ^ ((g & 1) << 2);
             const uint4 ka = lds_16(st + g * D + sw * 16), kb = lds_16(st + (g + 8) * D + sw * 16);
@@ -545,7 +564,8 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 cvt_e4m3x4(wb[j], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_16816(c[nt][j & 1], a, bq[nt][h * 4 + j][0], bq[nt][h * 4 + j][1]);
+                    if (h == 0 && j < 2) mma_16816_new(c[nt][j], a, bq[nt][j][0], bq[nt][j][1]);
+                    else mma_16816(c[nt][j & 1], a, bq[nt][h * 4 + j][0], bq[nt][h * 4 + j][1]);
                     if constexpr (SPLIT) mma_16816(c[nt][j & 1], a, bl[nt][h * 4 + j][0], bl[nt][h * 4 + j][1]);
                 }
             }
@@ -692,33 +712,33 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             if (members >> lane & 1u)
                 y = lane & 1 ? reinterpret_cast<const float4 *>(ring_o + (lane >> 1) * RING + p.RP * D)[row]
                              : reinterpret_cast<const float4 *>(p.ws_wml)[ws_at + (lane >> 1) * p.RP + row];
-            const float m1 = warp_max(y.x), v1 = warp_max(y.z);
-            const float sum = warp_sum(y.y * ex2(y.x - m1)), f = ex2(y.z - v1);
+            float m1 = 0.f, v1 = 0.f, sum = 0.f, f = 0.f;
 #pragma unroll
             for (int c = 0; c < (D + 127) / 128; ++c) {
                 const int col = c * 128 + lane * 4;
                 const bool in = col < D;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), z[2 * kWarps];
 #pragma unroll
-                for (int x0 = 0; x0 < 2 * kWarps; x0 += 8) {
-                    float4 z[8];
+                for (int x = 0; x < 2 * kWarps; ++x) {
+                    z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (in && (members >> x & 1u))
+                        z[x] = *reinterpret_cast<const float4 *>(
+                            x & 1 ? ring_o + (x >> 1) * RING + row * D + col
+                                  : p.ws_wo + (ws_at + (x >> 1) * p.RP + row) * D + col);
+                }
+                if (c == 0) {                // (while those are on their way)
+                    m1 = warp_max(y.x);
+                    v1 = warp_max(y.z);
+                    sum = warp_sum(y.y * ex2(y.x - m1));
+                    f = ex2(y.z - v1);
+                }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int x = x0 + k;
-                        z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (in && (members >> x & 1u))
-                            z[k] = *reinterpret_cast<const float4 *>(
-                                x & 1 ? ring_o + (x >> 1) * RING + row * D + col
-                                      : p.ws_wo + (ws_at + (x >> 1) * p.RP + row) * D + col);
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float fx = __shfl_sync(0xffffffffu, f, x0 + k);
-                        acc.x = fmaf(fx, z[k].x, acc.x);
-                        acc.y = fmaf(fx, z[k].y, acc.y);
-                        acc.z = fmaf(fx, z[k].z, acc.z);
-                        acc.w = fmaf(fx, z[k].w, acc.w);
-                    }
+                for (int x = 0; x < 2 * kWarps; ++x) {
+                    const float fx = __shfl_sync(0xffffffffu, f, x);
+                    acc.x = fmaf(fx, z[x].x, acc.x);
+                    acc.y = fmaf(fx, z[x].y, acc.y);
+                    acc.z = fmaf(fx, z[x].z, acc.z);
+                    acc.w = fmaf(fx, z[x].w, acc.w);
                 }
                 if (!in) continue;
                 // (of a row tile that began before this block the state is the block's first)
@@ -878,8 +898,13 @@ DecodeQ8Plan decode_q8_plan(int B, int Hkv, int G, int D, bool bf16, int n_sm)
 
 cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t stream)
 {
-    // Short row tiles stay in one block, and then no second kernel is needed.
-    p.whole = (p.cap + kStep - 1) / kStep <= kWholeSteps;
+    // Row tiles stay in one block each, and no second kernel is needed, where that leaves the fullest block
+    // little more than the mean: by the capacity (which the host knows), and with few steps a block, since the
+    // lengths behind it may differ.  Measured with 52 steps of 128 dims, whole and split: 512 row tiles on 304
+    // blocks (16 steps above the mean) 24.4 and 26.7 us.
+    const long long tiles = (long long)p.B * p.HR, steps = (p.cap + kStep - 1) / kStep;
+    const long long fullest = (tiles + p.blocks - 1) / p.blocks * steps;
+    p.whole = steps <= kWholeSteps || (fullest * D <= 128 * 128 && (fullest - tiles * steps / p.blocks) * D <= kWholeWait * 128);
     if (bf16) {
         const bool wide = tiles_of_8(p.G, D, true) == 2;
         switch (D) {
