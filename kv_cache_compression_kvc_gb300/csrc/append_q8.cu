@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kRowWarps = 4;
-constexpr int kRowBlocks = 4;                // per SM
+constexpr int kRowBlocks = 5;                // per SM
 constexpr int kCl = 8;                       // blocks of the cluster that takes a small decode step
 constexpr int kStepTasks = 4096;             // (page, head, K or V) of it
 constexpr int kDevBadLen_ = 5;               // KVC_DEV_BAD_LENGTH
@@ -82,7 +82,7 @@ __device__ __forceinline__ int find_above(const int *a, int n, int x)
 __device__ __forceinline__ void append_plan(const AppendQ8Params &p)
 {
     __shared__ int s_warp[64];
-    __shared__ int s_need[kPlanThreads];     // pages to pop (then their inclusive scan)
+    __shared__ int s_need[kPlanThreads];     // pages to pop
     __shared__ int s_jobs[kPlanThreads];     // inclusive scan of the pages that get rows
     __shared__ int s_first[kPlanThreads];    // a sequence's ids are ids[first - 1], ids[first - 2], ...
     __shared__ int s_n[kPlanThreads];        // rows to append
@@ -190,30 +190,28 @@ __device__ __forceinline__ void append_plan(const AppendQ8Params &p)
             s_top = top - all.x;
         }
         __syncthreads();
-        s_need[tid] = incl.x;
         s_jobs[tid] = incl.y;
         s_first[tid] = first;
         s_n[tid] = n;
         s_len[tid] = len;
         s_row[tid] = row;
         __syncthreads();
-        // table entries of the popped pages, then a job for every page that gets rows
-        for (int e = tid; e < all.x; e += kPlanThreads) {
-            const int i = find_above(s_need, kPlanThreads, e);
-            const int j = e - (i > 0 ? s_need[i - 1] : 0);
-            const size_t at = (size_t)(b0 + i) * p.max_blocks + (s_len[i] + p.bs - 1) / p.bs + j;
-            p.table[at] = p.free_ids[s_first[i] - 1 - j];
-            p.score[at] = 0.f;
-        }
+        // a job for every page that gets rows, and a table entry for the popped ones
         for (int e = tid; e < all.y; e += kPlanThreads) {
             const int i = find_above(s_jobs, kPlanThreads, e);
             const int j = e - (i > 0 ? s_jobs[i - 1] : 0);
             const int l = s_len[i], lb = l / p.bs + j, held = j == 0 ? l % p.bs : 0;
             const int at = lb * p.bs + held;                   // the first new row's slot
-            const int id = held > 0 ? p.table[(size_t)(b0 + i) * p.max_blocks + lb]
-                                    : p.free_ids[s_first[i] - 1 - (lb - (l + p.bs - 1) / p.bs)];
-            const int rows = min(p.bs - held, l + s_n[i] - at);
-            p.jobs[jobs0 + e] = make_int4(id, held, s_row[i] + at - l, rows);
+            const size_t entry = (size_t)(b0 + i) * p.max_blocks + lb;
+            int id;
+            if (held > 0) {
+                id = p.table[entry];
+            } else {
+                id = p.free_ids[s_first[i] - 1 - (lb - (l + p.bs - 1) / p.bs)];
+                p.table[entry] = id;
+                p.score[entry] = 0.f;
+            }
+            p.jobs[jobs0 + e] = make_int4(id, held, s_row[i] + at - l, min(p.bs - held, l + s_n[i] - at));
         }
         jobs0 += all.y;
         if (b < p.B) {
@@ -428,7 +426,7 @@ __device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long 
 }
 
 template <typename T, int D, int NV>
-__global__ void __launch_bounds__(kRowWarps * 32) append_q8_rows_kernel(const AppendQ8Params p)
+__global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks) append_q8_rows_kernel(const AppendQ8Params p)
 {
     pdl_trigger();
     pdl_wait();

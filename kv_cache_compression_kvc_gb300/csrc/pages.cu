@@ -19,6 +19,8 @@
 // words, which one block would take 8 times as long over, and a launch per step would cost more than the
 // steps); what blocks tell each other goes through the workspace.  Bound by latency.  The copies are bound
 // by HBM: a page's keys and values of a head are one contiguous run each, 64 bytes a thread in flight.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -29,8 +31,9 @@ namespace {
 constexpr int kCl = 8;                       // blocks of the cluster
 constexpr int kThreads = 1024;
 constexpr int kAll = kCl * kThreads;
-constexpr int kCopyThreads_ = 256;
-constexpr long long kFusedBytes = 1 << 20;
+constexpr int kCopyThreads_ = 256, kCopyBlocks = 8;      // of the copies: threads of a block, blocks per SM
+constexpr long long kFusedBytes = 1 << 17;   // a block
+constexpr int kOneBlock = 64, kOnePool = 16384;          // 32-entry runs of the tables, and pages, that one block takes
 constexpr int kBadIndex = 3, kBadLength = 5, kBadBlock = 9, kPoolEmpty = 10, kPoolOverflow = 11, kSharedPage = 12;
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -40,8 +43,13 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 // Also orders the cluster's global memory accesses.
+template <int CL>
 __device__ __forceinline__ void cluster_barrier()
 {
+    if (CL == 1) {
+        __syncthreads();
+        return;
+    }
     __threadfence();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -67,13 +75,13 @@ __device__ __forceinline__ int block_rank(bool flag, int *s_warp, int *all)
 }
 
 // Calls f(b, i) for the entries i < n(b) of every sequence's table, 32 of one sequence a warp.
-template <typename N, typename F>
+template <int CL, typename N, typename F>
 __device__ __forceinline__ void each_entry(int B, int max_blocks, int rank, N n, F f)
 {
     const int lane = threadIdx.x & 31, first = rank * (kThreads / 32) + (threadIdx.x >> 5);
     const int per = (max_blocks + 31) / 32;
     int b = first / per, c = first - b * per;
-    constexpr int kStride = kAll / 32;
+    constexpr int kStride = CL * kThreads / 32;
     const int db = kStride / per, dc = kStride - db * per;
     while (b < B) {
         const int i = c * 32 + lane;
@@ -87,52 +95,51 @@ __device__ __forceinline__ void each_entry(int B, int max_blocks, int rank, N n,
     }
 }
 
-// Job (copy c, head h): rows of keys and values from page to page, with their scales; head 0 takes the
-// tokens' positions along.  Blocks first, first + stride, ... of THREADS threads each take a job.
-template <int THREADS>
-__device__ __forceinline__ void copy_pages(const PagesParams &p, int n_copies, int first, int stride)
+// Task (copy, head, keys or values), a warp each: the rows of a page of a head are one run, with the page's
+// scale; head 0's keys take the tokens' positions along.  Warps first, first + stride, ... take them in
+// turn and read the next one's copy ahead.
+__device__ __forceinline__ void copy_pages(const PagesParams &p, int n_copies, long long first, long long stride)
 {
-    const long long jobs = (long long)n_copies * p.H;
+    const int lane = threadIdx.x & 31;
+    const unsigned per = 2u * (unsigned)p.H;
+    const long long tasks = (long long)n_copies * per;
+    if (first >= tasks) return;
     const size_t page_bytes = (size_t)p.bs * p.row_bytes;
-    for (long long j = first; j < jobs; j += stride) {
-        const int c = (int)(j / p.H), h = (int)(j - (long long)c * p.H);
-        const int4 what = __ldcg(p.ws_copies + c);
-        const size_t from = (size_t)h * p.n_pool + what.x, to = (size_t)h * p.n_pool + what.y;
-        const int n = what.z * (p.row_bytes / 16);         // vectors of keys, then as many of values
-        constexpr int U = 4;
-        for (int i0 = threadIdx.x; i0 < 2 * n; i0 += THREADS * U) {
+    int4 what = __ldcg(p.ws_copies + (unsigned)(first / per));
+    for (long long j = first; j < tasks; j += stride) {
+        const int rest = (int)(j - j / per * per), h = rest >> 1;
+        const int4 now = what;
+        if (j + stride < tasks) what = __ldcg(p.ws_copies + (unsigned)((j + stride) / per));
+        const size_t from = (size_t)h * p.n_pool + now.x, to = (size_t)h * p.n_pool + now.y;
+        char *pool = rest & 1 ? p.v : p.k;
+        const char *src = pool + from * page_bytes;
+        char *dst = pool + to * page_bytes;
+        const int n = now.z * p.row_bytes;
+        constexpr int U = 8;
+        for (int i0 = lane * 16; i0 < n; i0 += 512 * U) {
             uint4 x[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * THREADS;
-                if (i < 2 * n)
-                    x[u] = ld_stream_16((i < n ? p.k : p.v) + from * page_bytes + (size_t)(i < n ? i : i - n) * 16);
-            }
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * 512 < n) x[u] = ld_stream_16(src + i0 + u * 512);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = i0 + u * THREADS;
-                if (i < 2 * n)
-                    *reinterpret_cast<uint4 *>((i < n ? p.k : p.v) + to * page_bytes +
-                                               (size_t)(i < n ? i : i - n) * 16) = x[u];
-            }
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * 512 < n) *reinterpret_cast<uint4 *>(dst + i0 + u * 512) = x[u];
         }
-        if (threadIdx.x == 0 && p.ks != nullptr) {
-            p.ks[to] = p.ks[from];
-            p.vs[to] = p.vs[from];
-        }
-        if (h == 0 && p.pos != nullptr)
-            for (int i = threadIdx.x; i < what.z; i += THREADS)
-                p.pos[(size_t)what.y * p.bs + i] = p.pos[(size_t)what.x * p.bs + i];
+        float *scale = rest & 1 ? p.vs : p.ks;
+        if (lane == 0 && scale != nullptr) scale[to] = scale[from];
+        if (rest == 0 && p.pos != nullptr)
+            for (int i = lane; i < now.z; i += 32) p.pos[(size_t)now.y * p.bs + i] = p.pos[(size_t)now.x * p.bs + i];
     }
 }
 
-__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_reorder_kernel(const PagesParams p)
+template <int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reorder_kernel(const PagesParams p)
 {
     extern __shared__ int s_seq[];           // per sequence: children, keeper, parent, blocks, length, copy
     __shared__ int s_warp[32];
     int *s_kids = s_seq, *s_keep = s_kids + p.B, *s_par = s_keep + p.B, *s_nb = s_par + p.B, *s_len = s_nb + p.B,
         *s_copy = s_len + p.B;
-    const int tid = threadIdx.x, rank = (int)cluster_rank();
+    const int tid = threadIdx.x, rank = CL == 1 ? 0 : (int)cluster_rank();
     pdl_trigger();
     pdl_wait();
     // ---- the sequences, in every block alike ----
@@ -154,7 +161,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
         s_len[b] = len;
     }
     const bool bad = __syncthreads_or(code != 0);
-    cluster_barrier();                       // (ws_n is there; no block has left)
+    cluster_barrier<CL>();                       // (ws_n is there; no block has left)
     if (bad) {
         if (rank == 0 && code != 0) record_code(p.dev_code, code);
         return;
@@ -187,14 +194,14 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
     auto partial = [&](int b, int i) { return s_len[b] % p.bs != 0 && i == s_nb[b] - 1; };
     // ---- the tables' ids, of the sequences that change ----
     auto touched = [&](int b) { return s_kids[b] == 1 && s_par[b] == b ? 0 : s_nb[b]; };
-    each_entry(p.B, p.max_blocks, rank, touched, [&](int b, int i) {
+    each_entry<CL>(p.B, p.max_blocks, rank, touched, [&](int b, int i) {
         const int id = p.table[(size_t)b * p.max_blocks + i];
         int c = 0;
         if (id < 0 || id >= p.n_pool) c = kBadBlock;
         else if (partial(b, i) && p.shares[id] != 0) c = kSharedPage;
         if (c != 0) atomicCAS(&p.ws_n[1], 0, c);
     });
-    cluster_barrier();
+    cluster_barrier<CL>();
     code = __ldcg(&p.ws_n[1]);
     if (code != 0) {                         // nothing has changed yet
         if (rank == 0 && tid == 0) record_code(p.dev_code, code);
@@ -202,14 +209,14 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
     }
     // ---- holders of every page ----
     auto count = [&](int sign) {
-        each_entry(p.B, p.max_blocks, rank, [&](int b) { return s_kids[b] == 1 ? 0 : s_nb[b]; }, [&](int b, int i) {
+        each_entry<CL>(p.B, p.max_blocks, rank, [&](int b) { return s_kids[b] == 1 ? 0 : s_nb[b]; }, [&](int b, int i) {
             if (s_kids[b] > 0 && partial(b, i)) return;
             atomicAdd(&p.shares[p.table[(size_t)b * p.max_blocks + i]], sign * (s_kids[b] - 1));
         });
     };
     count(1);
-    cluster_barrier();
-    const int x0 = (int)((long long)p.n_pool * rank / kCl), x1 = (int)((long long)p.n_pool * (rank + 1) / kCl);
+    cluster_barrier<CL>();
+    const int x0 = (int)((long long)p.n_pool * rank / CL), x1 = (int)((long long)p.n_pool * (rank + 1) / CL);
     int gone = 0;
     for (int x = x0 + tid; x < x1; x += kThreads) {
         const int s = __ldcg(&p.shares[x]);
@@ -227,10 +234,10 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (tid == 0) p.ws_n[2 + rank] = x;
     }
-    cluster_barrier();
+    cluster_barrier<CL>();
     int before = 0, n_gone = 0;
 #pragma unroll
-    for (int r = 0; r < kCl; ++r) {
+    for (int r = 0; r < CL; ++r) {
         const int x = __ldcg(&p.ws_n[2 + r]);
         if (r < rank) before += x;
         n_gone += x;
@@ -263,13 +270,13 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
         before += all;
     }
     auto moved = [&](int b) { return s_par[b] < 0 || s_par[b] == b ? 0 : s_nb[s_par[b]]; };
-    each_entry(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
+    each_entry<CL>(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
         const size_t from = (size_t)s_par[b] * p.max_blocks + i, to = (size_t)b * p.max_blocks + i;
         p.ws_table[to] = p.table[from];
         p.ws_score[to] = p.score[from];
     });
-    cluster_barrier();
-    each_entry(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
+    cluster_barrier<CL>();
+    each_entry<CL>(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
         const size_t at = (size_t)b * p.max_blocks + i;
         int id = __ldcg(&p.ws_table[at]);
         const int copy = s_copy[b];
@@ -295,8 +302,8 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
         }
     }
     if (p.fused) {
-        cluster_barrier();
-        copy_pages<kThreads>(p, n_copies, rank, kCl);
+        cluster_barrier<CL>();
+        copy_pages(p, n_copies, rank * (kThreads / 32) + (tid >> 5), CL * kThreads / 32);
     }
 }
 
@@ -348,7 +355,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_co
     };
     if (code == 0) {
         int c = 0;
-        each_entry(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
+        each_entry<kCl>(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
             const int id = p.table[(size_t)b * p.max_blocks + i];
             if (id < 0 || id >= p.n_pool || (bits[id >> 5] >> (id & 31) & 1u)) c = max(c, kBadBlock);
         });
@@ -398,7 +405,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_co
                 ++r;
             }
     }
-    cluster_barrier();
+    cluster_barrier<kCl>();
 #pragma unroll
     for (int r = 0; r < kCl; ++r) code = max(code, __ldcg(&p.ws_n[2 + r]));
     const int holes = s_holes;
@@ -423,14 +430,14 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_co
     }
     // the stack hands out the lowest free page first
     for (int i = all_tid; i < top; i += kAll) p.free_ids[i] = p.n_pool - 1 - i;
-    each_entry(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
+    each_entry<kCl>(p.B, p.max_blocks, rank, entries, [&](int b, int i) {
         int32_t *e = p.table + (size_t)b * p.max_blocks + i;
         const int x = *e;
         if (x >= n_live) *e = __ldcg(&p.ws_ids[f.rank_high(x, holes)]);
     });
     if (p.fused) {
-        cluster_barrier();
-        copy_pages<kThreads>(p, holes, rank, kCl);
+        cluster_barrier<kCl>();
+        copy_pages(p, holes, rank * (kThreads / 32) + (tid >> 5), kAll / 32);
     }
 }
 
@@ -438,20 +445,21 @@ __global__ void __launch_bounds__(kCopyThreads_) pages_copy_kernel(const PagesPa
 {
     pdl_trigger();
     pdl_wait();
-    copy_pages<kCopyThreads_>(p, *p.ws_n, blockIdx.x, gridDim.x);
+    constexpr int kWarps = kCopyThreads_ / 32;
+    copy_pages(p, *p.ws_n, (long long)blockIdx.x * kWarps + (threadIdx.x >> 5), (long long)gridDim.x * kWarps);
 }
 
 // `copies`: the most that there can be.
 cudaError_t launch_copies(const PagesParams &p, long long copies, int n_sm, cudaStream_t stream)
 {
-    const long long jobs = copies * p.H, most = (long long)n_sm * 8;
-    const long long blocks = jobs < 1 ? 1 : (jobs < most ? jobs : most);
+    const long long most = (long long)n_sm * kCopyBlocks, need = (copies * p.H * 2 + kCopyThreads_ / 32 - 1) / (kCopyThreads_ / 32);
+    const long long blocks = std::max(1LL, std::min(need, most));
     return launch_pdl(pages_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads_), 0, stream, p);
 }
 // Few bytes are copied by the cluster itself, without a second kernel.
-bool copies_fit(const PagesParams &p, long long copies)
+bool copies_fit(const PagesParams &p, long long copies, int blocks)
 {
-    return copies * p.H * p.bs * p.row_bytes * 2 <= kFusedBytes;
+    return copies * p.H * p.bs * p.row_bytes * 2 <= kFusedBytes * blocks;
 }
 
 cudaError_t configure(const void *kernel, int bytes, bool *configured)
@@ -466,16 +474,25 @@ cudaError_t configure(const void *kernel, int bytes, bool *configured)
 
 }  // namespace
 
-cudaError_t launch_pages_reorder(PagesParams p, int n_sm, cudaStream_t stream)
+template <int CL>
+static cudaError_t reorder_with(PagesParams p, int n_sm, cudaStream_t stream)
 {
     static bool configured[64] = {};
-    cudaError_t e = configure(reinterpret_cast<const void *>(pages_reorder_kernel),
+    cudaError_t e = configure(reinterpret_cast<const void *>(pages_reorder_kernel<CL>),
                               kPagesMaxBatch * 6 * (int)sizeof(int), configured);
     if (e != cudaSuccess) return e;
-    p.fused = copies_fit(p, p.B);
-    e = launch_pdl(pages_reorder_kernel, dim3(kCl), dim3(kThreads), (size_t)p.B * 6 * sizeof(int), stream, p);
+    p.fused = copies_fit(p, p.B, CL);
+    e = launch_pdl(pages_reorder_kernel<CL>, dim3(CL), dim3(kThreads), (size_t)p.B * 6 * sizeof(int), stream, p);
     if (e != cudaSuccess || p.fused) return e;
     return launch_copies(p, p.B, n_sm, stream);
+}
+
+cudaError_t launch_pages_reorder(PagesParams p, int n_sm, cudaStream_t stream)
+{
+    // barriers of a cluster cost more than they save where the tables are small: 4 runs 7.9 us by one block and
+    // 11.7 by the cluster, 128 runs 19.9 and 18.1
+    const bool one = (long long)p.B * ((p.max_blocks + 31) / 32) <= kOneBlock && p.n_pool <= kOnePool;
+    return one ? reorder_with<1>(p, n_sm, stream) : reorder_with<kCl>(p, n_sm, stream);
 }
 
 cudaError_t launch_pages_compact(PagesParams p, int n_sm, cudaStream_t stream)
@@ -483,7 +500,7 @@ cudaError_t launch_pages_compact(PagesParams p, int n_sm, cudaStream_t stream)
     static bool configured[64] = {};
     cudaError_t e = configure(reinterpret_cast<const void *>(pages_compact_kernel), kPagesMaxPool / 8, configured);
     if (e != cudaSuccess) return e;
-    p.fused = copies_fit(p, p.n_pool / 2);
+    p.fused = copies_fit(p, p.n_pool / 2, kCl);
     e = launch_pdl(pages_compact_kernel, dim3(kCl), dim3(kThreads), (size_t)((p.n_pool + 31) / 32) * 4, stream, p);
     if (e != cudaSuccess || p.fused) return e;
     return launch_copies(p, p.n_pool / 2, n_sm, stream);
