@@ -785,12 +785,13 @@ def _on_current(index: int, view, what: str) -> None:
 def _beside(index: int, view, what: str) -> None:
     """The tensors that a descriptor keeps live on that device too (looked at once a descriptor)."""
     kept = getattr(view, "_keep", None)
-    if kept is not None and getattr(view, "_at", None) != index:
+    seen = getattr(view, "_seen", None)
+    if kept is not None and (seen is None or seen[0] is not kept or seen[1] != index):
         for t in kept if type(kept) is tuple else (kept,):
             if t is not None and t.get_device() != index:
                 raise ValueError(f"{what} is on cuda:{index}, a tensor of its {type(view).__name__} "
                                  f"on {t.device}")
-        view._at = index
+        view._seen = (kept, index)
 
 
 def _raw_stream(index: int, stream) -> int:
