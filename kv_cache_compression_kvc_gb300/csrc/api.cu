@@ -1745,6 +1745,8 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
     const int cap = pt->max_blocks * pool->pages.block_size;
     if (logits != nullptr && logits_stride < cap)
         return fail(KVC_ERR_CAPACITY, "%s: logits_stride %lld < %d", name, (long long)logits_stride, cap);
+    st = check_ws(ws, ws_bytes, 0, name);    // (its size depends on the device)
+    if (st != KVC_OK) return st;
     int32_t *code = nullptr;
     int n_sm = 0;
     st = device_info(&code, &n_sm);

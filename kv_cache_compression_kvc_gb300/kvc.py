@@ -1085,10 +1085,10 @@ def kvc_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, *, w_q: Optional[torch.Te
     row by w_q, w_k [D], then the rotation of its first d_rot elements to pos int32 [T], with
     cos_sin fp32 [n_pos, 2, d_rot/2] (kvc_rope_table).  q_out=q, k_out=k: in place."""
     dt, index, shape = q.dtype, q.get_device(), q.shape
+    code = _dtype_code(dt)
     if len(shape) != 3:
         raise ValueError(f"q must be [T, n_heads_q, d_head], got {list(shape)}")
-    if index != torch._C._cuda_getDevice():
-        _on_current(index, None, "q")
+    _on_current(index, None, "q")
     T, Hq, D = shape
     r = kvc_qk_rows()
     r.q, r.q_stride_token, r.q_stride_head = _rows_of(q, "q", dt, T, D, index)
@@ -1122,7 +1122,7 @@ def kvc_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, *, w_q: Optional[torch.Te
     r.k_out, r.k_out_stride_token, r.k_out_stride_head = _rows_of(k_out, "k_out", dt, T, D, index)
     if q_out.shape[1] != Hq or k_out.shape[1] != Hkv:
         raise ValueError(f"outputs {list(q_out.shape)}, {list(k_out.shape)} for rows {list(shape)}, {list(k.shape)}")
-    r.dtype, r.n_tokens, r.n_heads_q, r.n_heads_kv, r.d_head = _dtype_code(dt), T, Hq, Hkv, D
+    r.dtype, r.n_tokens, r.n_heads_q, r.n_heads_kv, r.d_head = code, T, Hq, Hkv, D
     status = (_lib or load()).kvc_qk_norm_rope(r, wq, wk, eps, table, at, n_pos, _raw_stream(index, stream))
     if status:
         _check(status)
