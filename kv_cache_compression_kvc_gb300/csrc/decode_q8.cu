@@ -217,17 +217,21 @@ __device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
         units = __reduce_add_sync(0xffffffffu, units);
         int at = units * warp / kWarps;
         g.left = units * (warp + 1) / kWarps - at;
-        if (g.left > 0) {
-            unsigned i = i0;
-            for (;; ++i) {
-                g.b = (int)(i / p.HR);
+        if (g.left > 0) {                    // (a sequence's row tiles are alike)
+            g.b = (int)(i0 / p.HR);
+            g.hr = (int)(i0 - (unsigned)g.b * p.HR);
+            for (;;) {
                 g.len = len_of(p, g.b);
-                const int n_i = steps_of(g.len);
-                if (at < n_i) break;
-                at -= n_i;
+                const int n = steps_of(g.len), k = at / n;
+                if (k < p.HR - g.hr) {
+                    g.hr += k;
+                    g.off = at - k * n;
+                    break;
+                }
+                at -= (p.HR - g.hr) * n;
+                g.hr = 0;
+                ++g.b;
             }
-            g.hr = (int)(i - (unsigned)g.b * p.HR);
-            g.off = at;
         }
         return g;
     }

@@ -149,6 +149,68 @@ def test_short_rows_in_thousands(kvc):
     c.check(which=list(range(0, 1500, 41)) + [1499])
 
 
+def test_batches_without_any_slots(kvc):
+    for n, mb in ((1, 1), (5, 100), (400, 100)):
+        c = Case(kvc, [0] * n, 8, 2, 128, 16, torch.bfloat16, seed=6, max_blocks=mb)
+        c.call()
+        c.check()
+
+
+def test_row_tiles_of_one_slot_in_thousands(kvc):
+    c = Case(kvc, [1 + b % 3 for b in range(6000)], 1, 1, 64, 16, torch.float32, seed=6)
+    c.call()
+    c.check(which=list(range(0, 6000, 307)) + [5999])
+
+
+def test_pools_beyond_32_bits_of_bytes(kvc):
+    """Pages at the end of a pool of more than 2^32 bytes, in every call that reads or writes them."""
+    H, NB, bs, D, B = 2, 140000, 64, 256, 2
+    assert H * NB * bs * D > 2 ** 32
+    k, v = (torch.zeros((H, NB, bs, D), dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = torch.zeros((H, NB), device=DEV), torch.zeros((H, NB), device=DEV)
+    table = torch.zeros((B, 4), dtype=torch.int32, device=DEV)
+    nb, lens = torch.zeros(B, dtype=torch.int32, device=DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    ids = torch.arange(NB, dtype=torch.int32, device=DEV)       # the last pages are popped first
+    top = torch.tensor([NB], dtype=torch.int32, device=DEV)
+    pool, free = kvc.block_pool_q8_view(k, v, ks, vs), kvc.free_pool_view(ids, top)
+    pt = kvc.page_table_view(table, nb, lens, torch.zeros((B, 4), device=DEV))
+    x = torch.randn((300, H, D), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(torch.bfloat16)
+    cu = torch.tensor([0, 200, 300], dtype=torch.int32, device=DEV)
+    kvc.kvc_paged_append_q8(pool, pt, free, x, -x, cu=cu)
+    assert table[0].tolist() == [NB - 1, NB - 2, NB - 3, NB - 4]
+    q = torch.randn((B, 4, D), generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).to(torch.bfloat16)
+    want = kvc.kvc_decode_attn_paged_q8(q, pool, pt, scale=0.05)
+    for b, n in enumerate([200, 100]):
+        t = table[b, : (n + bs - 1) // bs].long()
+        for h in range(H):
+            kk, vv = ((p[h, t].view(torch.float8_e4m3fn).double() * s[h, t].double()[:, None, None]).flatten(0, 1)[:n]
+                      for p, s in ((k, ks), (v, vs)))
+            # half a step of 4 significant bits, and of the smallest step of a page
+            rows = x[int(cu[b]):int(cu[b]) + n, h].double()
+            assert bool(((kk - rows).abs() <= 2.0 ** -4 * rows.abs() + 2.0 ** -17 * rows.abs().max()).all())
+            assert torch.equal(vv, -kk)
+            ref, _, _, size = attention(q[b, 2 * h:2 * h + 2].double(), kk, vv, 0.05)
+            # bf16 outputs 2^-8, weights 2^-11, and 2^-14 for fp32 logits below 10
+            assert bool(((want[b, 2 * h:2 * h + 2].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.0 ** -14) * size).all())
+    shares = torch.zeros(NB, dtype=torch.int32, device=DEV)
+    kvc.kvc_pages_reorder(pool, pt, free, shares, torch.tensor([1, 1], dtype=torch.int32, device=DEV))
+    out = kvc.kvc_decode_attn_paged_q8(q, pool, pt, scale=0.05)
+    assert torch.equal(out[1], want[1])
+    same = kvc.kvc_decode_attn_paged_q8(q[1:].expand(2, 4, D).contiguous(), pool, pt, scale=0.05)
+    assert torch.equal(same[0], same[1])
+    kvc.kvc_pages_compact(pool, pt, free, shares=shares)
+    assert torch.equal(kvc.kvc_decode_attn_paged_q8(q, pool, pt, scale=0.05), out)
+    assert int(table[:, :2].max()) < 4 and kvc.kvc_device_status() == 0
+
+
+def test_a_workspace_too_small_is_refused(kvc):
+    c = Case(kvc, [40], 4, 2, 64, 16, torch.bfloat16, seed=6)
+    n = kvc.kvc_decode_attn_paged_q8_workspace_bytes(1, 4, 2, 64, kvc.KVC_BF16)
+    c.call(ws=torch.empty(n + 256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(kvc.KvcError):
+        c.call(ws=torch.empty(n - 1, dtype=torch.uint8, device=DEV))
+
+
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_scales_of_any_size(kvc, dt):
     """Pages whose scales are no powers of two and differ by 2^40: keys, then values."""
