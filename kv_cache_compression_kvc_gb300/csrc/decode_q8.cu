@@ -42,7 +42,8 @@ namespace {
 
 constexpr int kStep = 16;                    // slots of a step
 constexpr int kEnd = 2;                      // steps that the end of a row tile counts as
-constexpr int kWarps = 8;
+// Warps of a block: what registers allow (one block an SM with 16 heads or fp32 queries, two otherwise).
+constexpr int warps_of(int D, int NT, bool split) { return D <= 128 && (NT == 2 || split) ? 12 : 8; }
 constexpr int kMergeThreads = 256;
 constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block
 constexpr int kWholeWait = 20;               // and longer ones where the fullest block has so many above the mean
@@ -55,7 +56,7 @@ constexpr int kDevBadBlk_ = 9;
 
 template <int D, int NT, bool SPLIT>
 struct Q8Plan {
-    static constexpr int WARPS = kWarps;
+    static constexpr int WARPS = warps_of(D, NT, SPLIT);
     static constexpr int BLOCKS = D <= 128 && NT == 1 && !SPLIT ? 2 : 1;    // per SM (registers)
     static constexpr int STAGE = 2 * kStep * D + 32;     // keys, values, the two scales, what they are of
     static constexpr int ROOM = (BLOCKS == 2 ? 112 : 224) * 1024 / WARPS;
@@ -145,7 +146,7 @@ struct Range {
     int left;                    // units of this warp
 };
 // U: 32 bits where they hold all units (a 64-bit division is a long subroutine).
-template <typename U>
+template <typename U, int W>
 __device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -170,10 +171,10 @@ __device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
     const U q = T / blocks, r = T - q * blocks, bl = blockIdx.x;
     const U first = bl * q + (bl < r ? bl : r);
     const unsigned mine = bl < blocks ? (unsigned)(q + (bl < r ? 1 : 0)) : 0u;
-    const unsigned w0 = (unsigned)((unsigned long long)mine * warp / kWarps);
+    const unsigned w0 = (unsigned)((unsigned long long)mine * warp / W);
     const U t0 = first + w0;
     Range g;
-    g.left = (int)((unsigned)((unsigned long long)mine * (warp + 1) / kWarps) - w0);
+    g.left = (int)((unsigned)((unsigned long long)mine * (warp + 1) / W) - w0);
     const U before = incl - sum;
     const bool here = g.left > 0 && before <= t0 && t0 < incl;
     int b = b0, hr = 0, off = 0, len = 0;
@@ -196,11 +197,16 @@ __device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
     g.len = __shfl_sync(0xffffffffu, len, src);
     return g;
 }
-__device__ __noinline__ Range split_range_64(const DecodeQ8Params &p) { return split_range<unsigned long long>(p); }
+template <int W>
+__device__ __noinline__ Range split_range_64(const DecodeQ8Params &p)
+{
+    return split_range<unsigned long long, W>(p);
+}
 
+template <int W>
 __device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
 {
-    if (!p.whole) return p.small ? split_range<unsigned>(p) : split_range_64(p);
+    if (!p.whole) return p.small ? split_range<unsigned, W>(p) : split_range_64<W>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool check = blockIdx.x == 0 && warp == 0;
     Range g;
@@ -215,8 +221,8 @@ __device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
         int units = 0;
         for (unsigned i = i0 + lane; i < i1; i += 32) units += steps_of(len_of(p, (int)(i / p.HR)));
         units = __reduce_add_sync(0xffffffffu, units);
-        int at = units * warp / kWarps;
-        g.left = units * (warp + 1) / kWarps - at;
+        int at = units * warp / W;
+        g.left = units * (warp + 1) / W - at;
         if (g.left > 0) {                    // (a sequence's row tiles are alike)
             g.b = (int)(i0 / p.HR);
             g.hr = (int)(i0 - (unsigned)g.b * p.HR);
@@ -301,18 +307,18 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     constexpr int DT = D / 16;               // 16-dim tiles of the output
     constexpr int VB = D == 64 ? 8 : 16;     // bytes of a value row that a lane takes at once
     constexpr int VC = D == 256 ? 2 : 1;     // how often
-    constexpr int S = PL::STAGES;
+    constexpr int S = PL::STAGES, W = PL::WARPS;
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * (S * PL::STAGE);
     // parts of row tiles that this block's warps leave: a warp's first one (if others follow) in the
     // workspace, its last one in its ring: {row tile or -1, first step, behind the last, steps of the tile}
-    __shared__ int4 s_part[2 * kWarps];
-    if (threadIdx.x < 2 * kWarps) s_part[threadIdx.x] = make_int4(-1, 0, 0, 0);
+    __shared__ int4 s_part[2 * W];
+    if (threadIdx.x < 2 * W) s_part[threadIdx.x] = make_int4(-1, 0, 0, 0);
     pdl_trigger();
     pdl_wait();
-    const Range range = find_range(p);
+    const Range range = find_range<W>(p);
     __syncthreads();                         // (s_part)
 
     // ---- copies: one step ahead by step into the ring ----
@@ -463,7 +469,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         const bool whole = lo == 0 && hi == n;
         float *po = nullptr, *pm = nullptr;
         if (!whole) {
-            const size_t at = (size_t)blockIdx.x * kWarps + warp;
+            const size_t at = (size_t)blockIdx.x * W + warp;
             po = last ? reinterpret_cast<float *>(smem + warp * (S * PL::STAGE)) : p.ws_wo + at * p.RP * D;
             pm = last ? po + p.RP * D : p.ws_wml + at * p.RP * 4;
             if (lane == 0) s_part[2 * warp + (last ? 1 : 0)] = make_int4(b * p.HR + hr, lo, hi, n);
@@ -688,7 +694,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     }
     // ---- the block's parts, in order: those of one row tile are joined, a row a warp ----
     __syncthreads();
-    const int4 mine = lane < 2 * kWarps ? s_part[lane] : make_int4(-1, 0, 0, 0);
+    const int4 mine = lane < 2 * W ? s_part[lane] : make_int4(-1, 0, 0, 0);
     const uint32_t parts = __ballot_sync(0xffffffffu, mine.x >= 0);
     const uint32_t below = parts & ((1u << lane) - 1u);
     const int tile_below = __shfl_sync(0xffffffffu, mine.x, below != 0 ? 31 - __clz(below) : 0);
@@ -707,10 +713,10 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         const int rows = min(p.RP, p.G - r0);
         // part x: odd ones in the ring of warp x / 2, even ones in the workspace
         const float *ring_o = reinterpret_cast<const float *>(smem);
-        const size_t ws_at = (size_t)blockIdx.x * kWarps * p.RP;
+        const size_t ws_at = (size_t)blockIdx.x * W * p.RP;
         constexpr int RING = S * PL::STAGE / 4;
         int row = turn;
-        for (; row < rows; row += kWarps) {
+        for (; row < rows; row += W) {
             // lane x has part x's state, and then its factor
             float4 y = make_float4(kNone, 0.f, kNone, 0.f);
             if (members >> lane & 1u)
@@ -721,9 +727,9 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             for (int c = 0; c < (D + 127) / 128; ++c) {
                 const int col = c * 128 + lane * 4;
                 const bool in = col < D;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), z[2 * kWarps];
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), z[2 * W];
 #pragma unroll
-                for (int x = 0; x < 2 * kWarps; ++x) {
+                for (int x = 0; x < 2 * W; ++x) {
                     z[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (in && (members >> x & 1u))
                         z[x] = *reinterpret_cast<const float4 *>(
@@ -737,7 +743,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                     f = ex2(y.z - v1);
                 }
 #pragma unroll
-                for (int x = 0; x < 2 * kWarps; ++x) {
+                for (int x = 0; x < 2 * W; ++x) {
                     const float fx = __shfl_sync(0xffffffffu, f, x);
                     acc.x = fmaf(fx, z[x].x, acc.x);
                     acc.y = fmaf(fx, z[x].y, acc.y);
@@ -865,7 +871,7 @@ cudaError_t launch_typed(DecodeQ8Params p, cudaStream_t stream)
     const long long units = tiles * (steps + kEnd);
     const int grid = (int)std::min<long long>(p.blocks, p.whole ? tiles : units / kMinUnits + 1);
     p.small = units <= 0x7fffffffLL;
-    cudaError_t e = launch_pdl(decode_q8_kernel<D, NT, SPLIT>, dim3((unsigned)grid), dim3(kWarps * 32), PL::SMEM,
+    cudaError_t e = launch_pdl(decode_q8_kernel<D, NT, SPLIT>, dim3((unsigned)grid), dim3(PL::WARPS * 32), PL::SMEM,
                                stream, p);
     if (e != cudaSuccess || p.whole) return e;
     return launch_pdl(decode_q8_merge_kernel<T, D>, dim3((unsigned)(p.by_tile ? tiles : grid), (unsigned)p.RP),
@@ -889,7 +895,7 @@ DecodeQ8Plan decode_q8_plan(int B, int Hkv, int G, int D, bool bf16, int n_sm)
     const int most = pl.blocks;
     pl.by_tile = tiles <= most;
     auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    const size_t rows = (size_t)most * 2 * pl.RP, warp_rows = (size_t)most * kWarps * pl.RP;
+    const size_t rows = (size_t)most * 2 * pl.RP, warp_rows = (size_t)most * warps_of(D, NT, !bf16) * pl.RP;
     pl.off_first = 0;
     pl.off_last = up((size_t)most * sizeof(int32_t));
     pl.off_ml = up(pl.off_last + (size_t)tiles * sizeof(int32_t));

@@ -431,7 +431,7 @@ struct DecodeQ8Params {
     int32_t *ws_last;            // the block that a split row tile ends in
     float *ws_ml;                // [blocks][2][RP] {m, l, maximum of the value weights, -}
     float *ws_o;                 // [blocks][2][RP][D]
-    float *ws_wml, *ws_wo;       // the same of a warp's first part: [blocks][8][RP]
+    float *ws_wml, *ws_wo;       // the same of a warp's first part: [blocks][warps][RP]
     int32_t *dev_code;
 };
 struct DecodeQ8Plan {
