@@ -341,10 +341,17 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_co
     __syncthreads();
     if (code == 0) {
         bool bad = false;
-        for (int i = tid; i < top; i += kThreads) {
-            const int id = p.free_ids[i];
-            const bool in = id >= 0 && id < p.n_pool;
-            bad |= !in || (atomicOr(&bits[in ? id >> 5 : 0], in ? 1u << (id & 31) : 0u) >> (id & 31) & 1u);
+        constexpr int U = 8;                 // ids on their way at once
+        for (int i0 = tid; i0 < top; i0 += kThreads * U) {
+            int id[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) id[u] = i0 + u * kThreads < top ? p.free_ids[i0 + u * kThreads] : 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u * kThreads >= top) break;
+                const bool in = id[u] >= 0 && id[u] < p.n_pool;
+                bad |= !in || (atomicOr(&bits[in ? id[u] >> 5 : 0], in ? 1u << (id[u] & 31) : 0u) >> (id[u] & 31) & 1u);
+            }
         }
         if (__syncthreads_or(bad)) code = kBadBlock;
     }
