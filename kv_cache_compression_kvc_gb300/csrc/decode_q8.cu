@@ -6,11 +6,11 @@
 //
 // What bounds it is the stream of the cache: one byte an element, 4 G operations for the G query heads
 // that share it, far below the ridge.  So everything is arranged around bytes in flight:
-//   A warp works alone.  The steps (16 slots of one (sequence, KV head, row tile)) of the whole batch are
-//   dealt out evenly, in order, to the blocks and again to a block's warps, and a warp keeps kStages
-//   steps in flight in its own ring in shared memory (cp.async, 16 bytes a lane; rows behind the
-//   length are filled with zeros, whatever the page holds there).  No barrier between warps while they
-//   stream, and no wait that could fail to end: a warp waits for its own copies only.
+//   A warp works alone.  The steps (16 slots of one (sequence, KV head, row tile), 32 with 64 dims) of the
+//   whole batch are dealt out evenly, in order, to the blocks and again to a block's warps, and a warp
+//   keeps two to five steps in flight in its own ring in shared memory (cp.async, 16 bytes a lane; rows
+//   behind the length are filled with zeros, whatever the page holds there).  No barrier between warps
+//   while they stream, and no wait that could fail to end: a warp waits for its own copies only.
 //   Both products run on mma.m16n8k16 with the cache as the 16-row operand and the query heads as the 8
 //   columns, so that up to 8 heads waste nothing: S^T = K Q^T, O^T = V^T P^T.  (5th-generation
 //   products want 64 or 128 rows of one operand and, of 8-bit operands, both in 8 bits; the stream
@@ -28,6 +28,14 @@
 // is.  A row tile that crosses warps leaves partial states (m, l, M, O): those of a block are joined in
 // shared memory at its end, those of several blocks by decode_q8_merge_kernel, both in order of
 // the slots, so results do not depend on timing.
+//
+// Measured: 2 x 131072 slots of 8 heads of 128, 4 query heads each (537 MB) 92.5 us, 5.8 TB/s.  Copies
+// alone in this pattern take 78 us.  3 us pass until the first copies leave (lengths, page ids, cold
+// instructions), 3 us after the last (parts), and equal shares take some SMs 61 us and others 85: whole
+// groups of neighbours are slower.  More blocks than fit at once, so that the fast ones take more, 115 us;
+// four blocks of 4 warps an SM 111; 6 warps a block with four stages 94.7; one block of 8 warps with six
+// stages 99.5; two products side by side with 128 dims 93.4; one warp that finds the block's range
+// for all 95.2; L2 prefetch hints no change.  Parts joined per warp instead of per block: 110.
 #include <algorithm>
 #include <type_traits>
 
@@ -40,9 +48,11 @@ namespace kvc {
 
 namespace {
 
-constexpr int kStep = 16;                    // slots of a step
-constexpr int kEnd = 2;                      // steps that the end of a row tile counts as
-// Warps of a block: what registers allow (one block an SM with 16 heads or fp32 queries, two otherwise).
+constexpr int kSub = 16;                     // slots of one product; a step is one or two of them
+constexpr int kEnd = 2;                      // steps that the end of a row tile counts as (0: 34.5 us for the ragged
+                                             // fp32 batch of the table, 1: 33.5, 2 and 4: 32.7)
+// Warps of a block: what registers allow (one block an SM with 16 heads or fp32 queries, two otherwise).  fp32
+// queries over 2 x 32768 slots of 8 heads of 128: 8 warps 34.5 us, 10 34.3, 12 31.5.
 constexpr int warps_of(int D, int NT, bool split) { return D <= 128 && (NT == 2 || split) ? 12 : 8; }
 constexpr int kMergeThreads = 256;
 constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block
@@ -54,11 +64,16 @@ constexpr float kNone = -3.402823466e38f;    // a maximum of nothing
 constexpr int kDevBadLen_ = 5;
 constexpr int kDevBadBlk_ = 9;
 
+// Products of 16 slots that a step takes side by side: with 64 dims one alone is half bookkeeping (8 x 16384
+// slots of 4 heads of 64: one 21.9 us, two 21.2; fp32 queries 24.9 and 23.3).
+constexpr int subs_of(int D) { return D == 64 ? 2 : 1; }
+
 template <int D, int NT, bool SPLIT>
 struct Q8Plan {
+    static constexpr int SUB = subs_of(D), STEP = kSub * SUB;
     static constexpr int WARPS = warps_of(D, NT, SPLIT);
     static constexpr int BLOCKS = D <= 128 && NT == 1 && !SPLIT ? 2 : 1;    // per SM (registers)
-    static constexpr int STAGE = 2 * kStep * D + 32;     // keys, values, the two scales, what they are of
+    static constexpr int STAGE = 2 * STEP * D + 32;      // keys and values, their scales, what they are of
     static constexpr int ROOM = (BLOCKS == 2 ? 112 : 224) * 1024 / WARPS;
     static constexpr int FIT = ROOM / STAGE;
     static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -138,7 +153,11 @@ __device__ __forceinline__ int len_of(const DecodeQ8Params &p, int b)
     const int n = p.len[b];
     return n < 0 ? 0 : (n > p.cap ? p.cap : n);
 }
-__device__ __forceinline__ int steps_of(int len) { return len > 0 ? (len + kStep - 1) / kStep : 1; }
+template <int STEP>
+__device__ __forceinline__ int steps_of(int len)
+{
+    return len > 0 ? (len + STEP - 1) / STEP : 1;
+}
 
 // A warp's share of the units: every row tile counts its steps and kEnd.  Called by a whole warp.
 struct Range {
@@ -146,7 +165,7 @@ struct Range {
     int left;                    // units of this warp
 };
 // U: 32 bits where they hold all units (a 64-bit division is a long subroutine).
-template <typename U, int W>
+template <typename U, int W, int STEP>
 __device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -157,7 +176,7 @@ __device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
     for (int b = b0; b < b1; ++b) {
         const int n = p.len[b];
         if (check && (n < 0 || n > p.cap)) record_code(p.dev_code, kDevBadLen_);
-        sum += (U)(steps_of(n < 0 ? 0 : min(n, p.cap)) + kEnd) * (U)p.HR;
+        sum += (U)(steps_of<STEP>(n < 0 ? 0 : min(n, p.cap)) + kEnd) * (U)p.HR;
     }
     U incl = sum;
 #pragma unroll
@@ -183,7 +202,7 @@ __device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
         U cost = 0;
         for (;; ++b) {
             len = len_of(p, b);
-            cost = (U)(steps_of(len) + kEnd);
+            cost = (U)(steps_of<STEP>(len) + kEnd);
             if (t0 < t + cost * (U)p.HR || b == b1 - 1) break;
             t += cost * (U)p.HR;
         }
@@ -197,16 +216,16 @@ __device__ __forceinline__ Range split_range(const DecodeQ8Params &p)
     g.len = __shfl_sync(0xffffffffu, len, src);
     return g;
 }
-template <int W>
+template <int W, int STEP>
 __device__ __noinline__ Range split_range_64(const DecodeQ8Params &p)
 {
-    return split_range<unsigned long long, W>(p);
+    return split_range<unsigned long long, W, STEP>(p);
 }
 
-template <int W>
+template <int W, int STEP>
 __device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
 {
-    if (!p.whole) return p.small ? split_range<unsigned, W>(p) : split_range_64<W>(p);
+    if (!p.whole) return p.small ? split_range<unsigned, W, STEP>(p) : split_range_64<W, STEP>(p);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool check = blockIdx.x == 0 && warp == 0;
     Range g;
@@ -219,7 +238,7 @@ __device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
         const unsigned i0 = (unsigned)((unsigned long long)tiles * blockIdx.x / n);
         const unsigned i1 = (unsigned)((unsigned long long)tiles * (blockIdx.x + 1) / n);
         int units = 0;
-        for (unsigned i = i0 + lane; i < i1; i += 32) units += steps_of(len_of(p, (int)(i / p.HR)));
+        for (unsigned i = i0 + lane; i < i1; i += 32) units += steps_of<STEP>(len_of(p, (int)(i / p.HR)));
         units = __reduce_add_sync(0xffffffffu, units);
         int at = units * warp / W;
         g.left = units * (warp + 1) / W - at;
@@ -228,7 +247,7 @@ __device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
             g.hr = (int)(i0 - (unsigned)g.b * p.HR);
             for (;;) {
                 g.len = len_of(p, g.b);
-                const int n = steps_of(g.len), k = at / n;
+                const int n = steps_of<STEP>(g.len), k = at / n;
                 if (k < p.HR - g.hr) {
                     g.hr += k;
                     g.off = at - k * n;
@@ -244,11 +263,12 @@ __device__ __forceinline__ Range find_range(const DecodeQ8Params &p)
 }
 
 // The steps of a range in order.
+template <int STEP>
 struct Walk {
     int b, hr, step, len, n;     // the step: row tile (b, hr), its number, the tile's slots and steps
     int left;                    // units of the range left, this step's among them
     __device__ __forceinline__ Walk(const DecodeQ8Params &p, const Range &g)
-        : b(g.b), hr(g.hr), step(g.off), len(g.len), n(steps_of(g.len)), left(g.left)
+        : b(g.b), hr(g.hr), step(g.off), len(g.len), n(steps_of<STEP>(g.len)), left(g.left)
     {
         settle(p);
     }
@@ -265,7 +285,7 @@ struct Walk {
                     return;
                 }
                 len = len_of(p, b);
-                n = steps_of(len);
+                n = steps_of<STEP>(len);
             }
         }
     }
@@ -307,7 +327,8 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     constexpr int DT = D / 16;               // 16-dim tiles of the output
     constexpr int VB = D == 64 ? 8 : 16;     // bytes of a value row that a lane takes at once
     constexpr int VC = D == 256 ? 2 : 1;     // how often
-    constexpr int S = PL::STAGES, W = PL::WARPS;
+    constexpr int S = PL::STAGES, W = PL::WARPS, SUB = PL::SUB, STEP = PL::STEP;
+    constexpr int SCALES = 2 * STEP * D;     // where a stage keeps its scales; 16 bytes on, what it holds
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -318,12 +339,12 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     if (threadIdx.x < 2 * W) s_part[threadIdx.x] = make_int4(-1, 0, 0, 0);
     pdl_trigger();
     pdl_wait();
-    const Range range = find_range<W>(p);
+    const Range range = find_range<W, STEP>(p);
     __syncthreads();                         // (s_part)
 
     // ---- copies: one step ahead by step into the ring ----
-    Walk ld(p, range);
-    const Walk first = ld;
+    Walk<STEP> ld(p, range);
+    const Walk<STEP> first = ld;
     int page_at = -1, pages = 0;             // the 32 table entries in this warp's lanes: first one's number
     int ld_b = -1, ld_hr = -1;
     long long head = 0;                      // the loaded row tile's head's first page
@@ -339,50 +360,55 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     auto fetch = [&](int slot) {
         const uint32_t st = ring + slot * PL::STAGE;
         if (ld.more()) {
-            const int pos = ld.step * kStep, lb = p.magic != 0 ? (int)__umulhi((unsigned)ld.step, p.magic) : ld.step;
-            if (ld.b != ld_b || lb < page_at || lb >= page_at + 32) {
-                ld_b = ld.b;
-                page_at = lb & ~31;
-                tab = p.table + (size_t)ld.b * p.max_blocks;
-                pages = page_at + lane < p.max_blocks ? __ldg(tab + page_at + lane) : 0;
-            }
-            int id = __shfl_sync(0xffffffffu, pages, lb - page_at);
-            const int valid = min(kStep, ld.len - pos);      // 0 of an empty sequence
-            if (id < 0 || id >= p.n_pool) {
-                if (valid > 0 && lane == 0) record_code(p.dev_code, kDevBadBlk_);
-                id = 0;
-            }
             if (ld.hr != ld_hr) {            // (a division, once a row tile)
                 ld_hr = ld.hr;
                 head = (long long)(p.RT == 1 ? ld.hr : ld.hr / p.RT) * p.n_pool;
             }
-            const long long page = head + id;
-            const long long at = (page * p.bs + (pos - lb * p.bs)) * D + lane * 16;
-            const uint8_t *k = p.k + at, *v = p.v + at;
-            if (valid == kStep) {
 #pragma unroll
-                for (int i = 0; i < CPR / 2; ++i) {
-                    cp_16(st + k_to + i * 512, k + i * 512);
-                    cp_16(st + kStep * D + (v_to ^ v_turn(i)) + i * 512, v + i * 512);
+            for (int sub = 0; sub < SUB; ++sub) {
+                const int pos = ld.step * STEP + sub * kSub, n = ld.step * SUB + sub;
+                const int lb = p.magic != 0 ? (int)__umulhi((unsigned)n, p.magic) : n;
+                const int valid = min(kSub, ld.len - pos);   // none behind the last slot, and in an empty sequence
+                if (ld.b != ld_b || lb < page_at || lb >= page_at + 32) {
+                    ld_b = ld.b;
+                    page_at = lb & ~31;
+                    pages = page_at + lane < p.max_blocks
+                                ? __ldg(p.table + (size_t)ld.b * p.max_blocks + page_at + lane) : 0;
                 }
-            } else {
+                int id = __shfl_sync(0xffffffffu, pages, lb - page_at);
+                if (id < 0 || id >= p.n_pool) {
+                    if (valid > 0 && lane == 0) record_code(p.dev_code, kDevBadBlk_);
+                    id = 0;
+                }
+                const long long page = head + id;
+                const long long at = (page * p.bs + (pos - lb * p.bs)) * D + lane * 16;
+                const uint8_t *k = p.k + at, *v = p.v + at;
+                const uint32_t to = st + sub * 2 * kSub * D;
+                if (valid == kSub) {
 #pragma unroll
-                for (int i = 0; i < CPR / 2; ++i) {
-                    const bool ok = (i * 32 + lane) / CPR < valid;
-                    cp_16(st + k_to + i * 512, k + i * 512, ok);
-                    cp_16(st + kStep * D + (v_to ^ v_turn(i)) + i * 512, v + i * 512, ok);
+                    for (int i = 0; i < CPR / 2; ++i) {
+                        cp_16(to + k_to + i * 512, k + i * 512);
+                        cp_16(to + kSub * D + (v_to ^ v_turn(i)) + i * 512, v + i * 512);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < CPR / 2; ++i) {
+                        const bool ok = (i * 32 + lane) / CPR < valid;
+                        cp_16(to + k_to + i * 512, k + i * 512, ok);
+                        cp_16(to + kSub * D + (v_to ^ v_turn(i)) + i * 512, v + i * 512, ok);
+                    }
                 }
+                if (lane < 2) cp_4(st + SCALES + sub * 8 + lane * 4, (lane == 0 ? p.ks : p.vs) + page);
             }
-            if (lane < 2) cp_4(st + 2 * kStep * D + lane * 4, (lane == 0 ? p.ks : p.vs) + page);
             if (lane == 0) {
-                const uint32_t m = st + 2 * kStep * D + 16;
+                const uint32_t m = st + SCALES + 16;
                 asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(m), "r"(ld.b), "r"(ld.hr), "r"(ld.step),
                              "r"(ld.len)
                              : "memory");
             }
             ld.next(p);
         } else if (lane == 0) {
-            const uint32_t m = st + 2 * kStep * D + 16;
+            const uint32_t m = st + SCALES + 16;
             asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(m), "r"(-1), "r"(0), "r"(0), "r"(0)
                          : "memory");
         }
@@ -542,11 +568,10 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         fetch(put);
         put = put + 1 == S ? 0 : put + 1;
         const uint32_t st = ring + slot * PL::STAGE;
-        const uint4 what = lds_16(st + 2 * kStep * D + 16);
-        const uint2 scales = lds_8(st + 2 * kStep * D);
+        const uint4 what = lds_16(st + SCALES + 16);
         const int b = (int)what.x, hr = (int)what.y, step = (int)what.z, len = (int)what.w;
         if (b != cur_b || hr != cur_hr) {
-            if (cur_b >= 0) finish(cur_b, cur_hr, first_step, first_step + cur_n, steps_of(cur_len), b < 0);
+            if (cur_b >= 0) finish(cur_b, cur_hr, first_step, first_step + cur_n, steps_of<STEP>(cur_len), b < 0);
             if (b < 0) break;
             cur_b = b;
             cur_hr = hr;
@@ -556,75 +581,89 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             begin(b, hr);
         }
         ++cur_n;
-        const int pos = step * kStep, valid = min(kStep, len - pos);
-        // (an empty sequence's step has no page, and any scale)
-        const float sk = __uint_as_float(scales.x), sv = valid > 0 ? __uint_as_float(scales.y) : 1.f;
-
-        // ---- S^T = K Q^T: slots g and g + 8 of the step, rows 2t and 2t + 1 of the tile ----
-        float c[NT][2][4];
+        const int pos = step * STEP, valid = len - pos;      // (STEP or more of a full step)
+        // ---- S^T = K Q^T: slots g and g + 8 of a product, rows 2t and 2t + 1 of the tile ----
+        float c[SUB][NT][2][4];
 #pragma unroll
-        for (int h = 0; h < KC; ++h) {
-            const int ch = t + 4 * h, sw = D == 64 ? ch : ch ^ ((g & 1) << 2);
-            const uint4 ka = lds_16(st + g * D + sw * 16), kb = lds_16(st + (g + 8) * D + sw * 16);
-            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        for (int sub = 0; sub < SUB; ++sub) {
+            const uint32_t sk_base = st + sub * 2 * kSub * D;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t a[4];
-                cvt_e4m3x4(wa[j], a[0], a[2]);
-                cvt_e4m3x4(wb[j], a[1], a[3]);
+            for (int h = 0; h < KC; ++h) {
+                const int ch = t + 4 * h, sw = D == 64 ? ch : ch ^ ((g & 1) << 2);
+                const uint4 ka = lds_16(sk_base + g * D + sw * 16), kb = lds_16(sk_base + (g + 8) * D + sw * 16);
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (h == 0 && j < 2) mma_16816_new(c[nt][j], a, bq[nt][j][0], bq[nt][j][1]);
-                    else mma_16816(c[nt][j & 1], a, bq[nt][h * 4 + j][0], bq[nt][h * 4 + j][1]);
-                    if constexpr (SPLIT) mma_16816(c[nt][j & 1], a, bl[nt][h * 4 + j][0], bl[nt][h * 4 + j][1]);
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t a[4];
+                    cvt_e4m3x4(wa[j], a[0], a[2]);
+                    cvt_e4m3x4(wb[j], a[1], a[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float(&cc)[2][4] = c[sub][nt];
+                        if (h == 0 && j < 2) mma_16816_new(cc[j], a, bq[nt][j][0], bq[nt][j][1]);
+                        else mma_16816(cc[j & 1], a, bq[nt][h * 4 + j][0], bq[nt][h * 4 + j][1]);
+                        if constexpr (SPLIT) mma_16816(cc[j & 1], a, bl[nt][h * 4 + j][0], bl[nt][h * 4 + j][1]);
+                    }
                 }
             }
         }
         // ---- softmax ----
-        // the value scale as 2^ev * fv, fv in [1, 2)
-        int ev = (int)((__float_as_uint(sv) >> 23) & 255u) - 127;
-        ev = ev < -126 ? -126 : (ev > 126 ? 126 : ev);
-        const float fv = sv * __uint_as_float((uint32_t)(127 - ev) << 23);
-        const float evf = (float)ev;
-        float x[NT][4];                      // log2 units: (slot g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
+        float evf[SUB], fv[SUB];             // the value scale as 2^ev * fv, fv in [1, 2)
+        float x[SUB][NT][4];                 // log2 units: (slot g, row 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
         bool rise = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float f0 = fq[nt][0] * sk, f1 = fq[nt][1] * sk;
+        for (int sub = 0; sub < SUB; ++sub) {
+            const uint2 scales = lds_8(st + SCALES + sub * 8);
+            // (a product behind the last slot has no page of its own, and any scale)
+            const float sk = __uint_as_float(scales.x), sv = valid > sub * kSub ? __uint_as_float(scales.y) : 1.f;
+            int ev = (int)((__float_as_uint(sv) >> 23) & 255u) - 127;
+            ev = ev < -126 ? -126 : (ev > 126 ? 126 : ev);
+            fv[sub] = sv * __uint_as_float((uint32_t)(127 - ev) << 23);
+            evf[sub] = (float)ev;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[nt][i] = c[nt][0][i] + c[nt][1][i];
-            if (p.logits != nullptr) {
-                const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8 + nt * 8 + 2 * t;
-                float *dst = p.logits + ((size_t)b * p.Hq + h * p.G + r0) * p.logits_stride + pos + g;
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f0 = fq[nt][0] * sk, f1 = fq[nt][1] * sk;
+                float *xs = x[sub][nt];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xs[i] = c[sub][nt][0][i] + c[sub][nt][1][i];
+                if (p.logits != nullptr) {
+                    const int h = hr / p.RT, r0 = (hr - h * p.RT) * NT * 8 + nt * 8 + 2 * t, at = sub * kSub + g;
+                    float *dst = p.logits + ((size_t)b * p.Hq + h * p.G + r0) * p.logits_stride + pos + at;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (r0 + r < p.G) {
+                            if (at < valid) dst[r * p.logits_stride] = xs[r] * (r ? f1 : f0);
+                            if (at + 8 < valid) dst[r * p.logits_stride + 8] = xs[2 + r] * (r ? f1 : f0);
+                        }
+                }
+                const float e0 = f0 * kLog2e, e1 = f1 * kLog2e;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xs[i] *= i & 1 ? e1 : e0;
+                if (valid < (sub + 1) * kSub) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (sub * kSub + g + (i >> 1) * 8 >= valid) xs[i] = -INFINITY;
+                }
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    if (r0 + r < p.G) {
-                        if (g < valid) dst[r * p.logits_stride] = x[nt][r] * (r ? f1 : f0);
-                        if (g + 8 < valid) dst[r * p.logits_stride + 8] = x[nt][2 + r] * (r ? f1 : f0);
-                    }
+                    rise |= fmaxf(xs[r], xs[2 + r]) > fminf(m[nt][r], mv[nt][r] - evf[sub]) + kSlack;
             }
-            const float e0 = f0 * kLog2e, e1 = f1 * kLog2e;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[nt][i] *= i & 1 ? e1 : e0;
-            if (valid < kStep) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (g + (i >> 1) * 8 >= valid) x[nt][i] = -INFINITY;
-            }
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                rise |= fmaxf(x[nt][r], x[nt][2 + r]) > fminf(m[nt][r], mv[nt][r] - evf) + kSlack;
         }
         if (__any_sync(0xffffffffu, rise)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float y = fmaxf(x[nt][r], x[nt][2 + r]);
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                    const float m1 = fmaxf(m[nt][r], y), v1 = fmaxf(mv[nt][r], y + evf);
+                    float m1 = m[nt][r], v1 = mv[nt][r];
+#pragma unroll
+                    for (int sub = 0; sub < SUB; ++sub) {
+                        float y = fmaxf(x[sub][nt][r], x[sub][nt][2 + r]);
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                        m1 = fmaxf(m1, y);
+                        v1 = fmaxf(v1, y + evf[sub]);
+                    }
                     l[nt][r] *= ex2(m[nt][r] - m1);
                     const float f = ex2(mv[nt][r] - v1);
 #pragma unroll
@@ -636,59 +675,62 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                     mv[nt][r] = v1;
                 }
         }
-        uint32_t pw[NT][2], pl[SPLIT ? NT : 1][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float y[4];
-            const float to[2] = {evf + kBoost - mv[nt][0], evf + kBoost - mv[nt][1]};
+        for (int sub = 0; sub < SUB; ++sub) {
+            uint32_t pw[NT][2], pl[SPLIT ? NT : 1][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                l[nt][i & 1] += ex2(x[nt][i] - m[nt][i & 1]);
-                y[i] = ex2(x[nt][i] + to[i & 1]) * fv;
-            }
+            for (int nt = 0; nt < NT; ++nt) {
+                float y[4];
+                const float to[2] = {evf[sub] + kBoost - mv[nt][0], evf[sub] + kBoost - mv[nt][1]};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t hi = pack_h2(y[2 * i], y[2 * i + 1]);
-                pw[nt][i] = transpose_8x8(hi);
-                if constexpr (SPLIT) {
-                    const float2 z = unpack_h2(hi);
-                    pl[nt][i] = transpose_8x8(pack_h2(y[2 * i] - z.x, y[2 * i + 1] - z.y));
+                for (int i = 0; i < 4; ++i) {
+                    l[nt][i & 1] += ex2(x[sub][nt][i] - m[nt][i & 1]);
+                    y[i] = ex2(x[sub][nt][i] + to[i & 1]) * fv[sub];
                 }
-            }
-        }
-        // ---- O^T += V^T P^T: slots 2t, 2t + 1, 2t + 8, 2t + 9 of VB dims ----
-        const uint32_t sv_base = st + kStep * D;
 #pragma unroll
-        for (int vc = 0; vc < VC; ++vc) {
-            uint32_t r[4][VB / 4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 2 * t + (i & 1) + (i >> 1) * 8;
-                if constexpr (VB == 16) {
-                    const int ch = (g + 8 * vc) ^ (t << 1);
-                    const uint4 y = lds_16(sv_base + row * D + ch * 16);
-                    r[i][0] = y.x; r[i][1] = y.y; r[i][2] = y.z; r[i][3] = y.w;
-                } else {
-                    const int ch = (g >> 1) ^ ((t & 1) << 1);
-                    const uint2 y = lds_8(sv_base + row * D + ch * 16 + (g & 1) * 8);
-                    r[i][0] = y.x; r[i][1] = y.y;
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < VB / 4; ++q)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t lo = __byte_perm(r[0][q], r[1][q], u ? 0x7362 : 0x5140);
-                    const uint32_t hi = __byte_perm(r[2][q], r[3][q], u ? 0x7362 : 0x5140);
-                    uint32_t a[4];
-                    cvt_e4m3x4(lo, a[0], a[1]);
-                    cvt_e4m3x4(hi, a[2], a[3]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_16816(o[vc * 8 + q * 2 + u][nt], a, pw[nt][0], pw[nt][1]);
-                        if constexpr (SPLIT) mma_16816(o[vc * 8 + q * 2 + u][nt], a, pl[nt][0], pl[nt][1]);
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t hi = pack_h2(y[2 * i], y[2 * i + 1]);
+                    pw[nt][i] = transpose_8x8(hi);
+                    if constexpr (SPLIT) {
+                        const float2 z = unpack_h2(hi);
+                        pl[nt][i] = transpose_8x8(pack_h2(y[2 * i] - z.x, y[2 * i + 1] - z.y));
                     }
                 }
+            }
+            // ---- O^T += V^T P^T: slots 2t, 2t + 1, 2t + 8, 2t + 9 of VB dims ----
+            const uint32_t sv_base = st + (sub * 2 + 1) * kSub * D;
+#pragma unroll
+            for (int vc = 0; vc < VC; ++vc) {
+                uint32_t r[4][VB / 4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 2 * t + (i & 1) + (i >> 1) * 8;
+                    if constexpr (VB == 16) {
+                        const int ch = (g + 8 * vc) ^ (t << 1);
+                        const uint4 y = lds_16(sv_base + row * D + ch * 16);
+                        r[i][0] = y.x; r[i][1] = y.y; r[i][2] = y.z; r[i][3] = y.w;
+                    } else {
+                        const int ch = (g >> 1) ^ ((t & 1) << 1);
+                        const uint2 y = lds_8(sv_base + row * D + ch * 16 + (g & 1) * 8);
+                        r[i][0] = y.x; r[i][1] = y.y;
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < VB / 4; ++q)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t lo = __byte_perm(r[0][q], r[1][q], u ? 0x7362 : 0x5140);
+                        const uint32_t hi = __byte_perm(r[2][q], r[3][q], u ? 0x7362 : 0x5140);
+                        uint32_t a[4];
+                        cvt_e4m3x4(lo, a[0], a[1]);
+                        cvt_e4m3x4(hi, a[2], a[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_16816(o[vc * 8 + q * 2 + u][nt], a, pw[nt][0], pw[nt][1]);
+                            if constexpr (SPLIT) mma_16816(o[vc * 8 + q * 2 + u][nt], a, pl[nt][0], pl[nt][1]);
+                        }
+                    }
+            }
         }
         slot = slot + 1 == S ? 0 : slot + 1;
     }
@@ -867,7 +909,7 @@ cudaError_t launch_typed(DecodeQ8Params p, cudaStream_t stream)
         configured[dev] = true;
     }
     // no more blocks than the capacity can give work
-    const long long tiles = (long long)p.B * p.HR, steps = (p.cap + kStep - 1) / kStep;
+    const long long tiles = (long long)p.B * p.HR, steps = (p.cap + PL::STEP - 1) / PL::STEP;
     const long long units = tiles * (steps + kEnd);
     const int grid = (int)std::min<long long>(p.blocks, p.whole ? tiles : units / kMinUnits + 1);
     p.small = units <= 0x7fffffffLL;
@@ -912,9 +954,11 @@ cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t st
     // little more than the mean: by the capacity (which the host knows), and with few steps a block, since the
     // lengths behind it may differ.  Measured with 52 steps of 128 dims, whole and split: 512 row tiles on 304
     // blocks (16 steps above the mean) 24.4 and 26.7 us.
-    const long long tiles = (long long)p.B * p.HR, steps = (p.cap + kStep - 1) / kStep;
+    const int step = kSub * subs_of(D);
+    const long long tiles = (long long)p.B * p.HR, steps = (p.cap + step - 1) / step;
     const long long fullest = (tiles + p.blocks - 1) / p.blocks * steps;
-    p.whole = steps <= kWholeSteps || (fullest * D <= 128 * 128 && (fullest - tiles * steps / p.blocks) * D <= kWholeWait * 128);
+    p.whole = steps <= kWholeSteps || (fullest * step * D <= 128 * 16 * 128 &&
+                                       (fullest - tiles * steps / p.blocks) * step * D <= kWholeWait * 16 * 128);
     if (bf16) {
         const bool wide = tiles_of_8(p.G, D, true) == 2;
         switch (D) {
