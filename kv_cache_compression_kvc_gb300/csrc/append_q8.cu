@@ -9,11 +9,13 @@
 // rows quantised at once hold, but for such small values.  A page whose scale is no power of two
 // (written by someone else) is read and continued just as well, with a division.
 //
-// append_q8_plan_kernel, one block: checks every sequence, numbers the pages they need in sequence
-// order (block-wide scans) and takes them from the top of the free stack, so that ids do not depend
-// on timing; it writes one job per page that gets rows.  append_q8_rows_kernel, a warp per (job, head,
-// K or V): the rows stay in registers between the maximum and the rounding.  Bound by HBM (2 or 4
-// bytes in, 1 out an element) for prompts, by the latency of the two kernels for single tokens.
+// append_plan, by one block: checks every sequence, numbers the pages they need in sequence order
+// (block-wide scans) and takes them from the top of the free stack, so that ids do not depend on
+// timing; it writes one job per page that gets rows.  Then a warp per (job, head, K or V): the rows
+// stay in registers between the maximum and the rounding.  Small steps do both in one cluster.
+// Bound by HBM for prompts (2 or 4 bytes in, 1 out an element): 16 prompts of 2048 to 4096 tokens, 32 heads of
+// 128, bf16, 201 us (6.0 TB/s), of which the plan is 8; with a warp per task instead of persistent ones
+// 228 us, with 16 warps an SM instead of 20 204.  Bound by latency for single tokens: 16 x 32 heads 12 us.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -29,7 +31,9 @@ constexpr int kPlanThreads = 1024;
 constexpr int kRowWarps = 4;
 constexpr int kRowBlocks = 5;                // per SM
 constexpr int kCl = 8;                       // blocks of the cluster that takes a small decode step
-constexpr int kStepTasks = 4096;             // (page, head, K or V) of it
+// (page, head, K or V) of it, at most.  64: 8.3 us by the cluster and 10.1 by two kernels, 256: 9.1 and 10.4, 1024:
+// 12.4 and 10.8, but a call from Python, which the host bounds, 16.7 and 19; 2048: 17.2 and 11.4.
+constexpr int kStepTasks = 1024;
 constexpr int kDevBadLen_ = 5;               // KVC_DEV_BAD_LENGTH
 constexpr int kDevBadBlk_ = 9;               // KVC_DEV_BAD_BLOCK
 constexpr int kDevPoolEmpty_ = 10;           // KVC_DEV_POOL_EMPTY
@@ -451,7 +455,7 @@ template <typename T, int D>
 cudaError_t append_typed(const AppendQ8Params &p, int n_sm, cudaStream_t stream)
 {
     const long long tasks = (long long)p.max_jobs * 2 * p.H;
-    if (p.cu == nullptr && tasks <= kStepTasks)
+    if (p.n_tokens <= 4 * p.B && tasks <= kStepTasks)
         return launch_pdl(append_q8_step_kernel<T, D>, dim3(kCl), dim3(kPlanThreads), 0, stream, p);
     const cudaError_t e = launch_pdl(append_q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (e != cudaSuccess) return e;

@@ -15,10 +15,13 @@
 // pages_compact_kernel: the k-th live page beyond the number of live pages moves to the k-th free page
 // below it; tables, counts and the stack follow.  No page is both read and written.
 //
-// Both tables' kernels are one cluster of 8 blocks with a few barriers (a page table is some 10^5
-// words, which one block would take 8 times as long over, and a launch per step would cost more than the
-// steps); what blocks tell each other goes through the workspace.  Bound by latency.  The copies are bound
-// by HBM: a page's keys and values of a head are one contiguous run each, 64 bytes a thread in flight.
+// Both tables' kernels are one block or one cluster of 8 with a few barriers (a launch per step would cost
+// more than the steps); what blocks tell each other goes through the workspace.  Bound by latency: every
+// step is a trip or two to memory.  For compaction each block keeps the free pages as bits in shared
+// memory and works out by itself where everything goes, which left one barrier of the cluster of six (16384
+// pages, tables and copies: 111 -> 105 us).  The copies are bound by HBM: a page's keys or values of a head are
+// one run, which a warp copies with 128 bytes a lane in flight and the next copy's ids read ahead: 515 MB of
+// 4 KB runs, read and written, in 77 us, 6.7 TB/s (a block a page with 64 bytes a thread: 84 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -32,7 +35,10 @@ constexpr int kCl = 8;                       // blocks of the cluster
 constexpr int kThreads = 1024;
 constexpr int kAll = kCl * kThreads;
 constexpr int kCopyThreads_ = 256, kCopyBlocks = 8;      // of the copies: threads of a block, blocks per SM
-constexpr long long kFusedBytes = 1 << 17;   // a block
+// Copies of so many bytes at most are made by the tables' kernel itself.  By one block, 512 KB: 8.6 us and 9.4 with a
+// second kernel, 1 MB: 11.7 and 10.7.  By the cluster, 256 KB: 10.9 and 9.8 on the device, but a call from
+// Python, which the host bounds, 24 and 27.
+constexpr long long kFusedBytes = 1 << 19, kFusedBytesCluster = 1 << 18;
 constexpr int kOneBlock = 64, kOnePool = 16384;          // 32-entry runs of the tables, and pages, that one block takes
 constexpr int kBadIndex = 3, kBadLength = 5, kBadBlock = 9, kPoolEmpty = 10, kPoolOverflow = 11, kSharedPage = 12;
 
@@ -463,10 +469,9 @@ cudaError_t launch_copies(const PagesParams &p, long long copies, int n_sm, cuda
     const long long blocks = std::max(1LL, std::min(need, most));
     return launch_pdl(pages_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads_), 0, stream, p);
 }
-// Few bytes are copied by the cluster itself, without a second kernel.
-bool copies_fit(const PagesParams &p, long long copies, int blocks)
+bool copies_fit(const PagesParams &p, long long copies, long long bytes)
 {
-    return copies * p.H * p.bs * p.row_bytes * 2 <= kFusedBytes * blocks;
+    return copies * p.H * p.bs * p.row_bytes * 2 <= bytes;
 }
 
 cudaError_t configure(const void *kernel, int bytes, bool *configured)
@@ -488,7 +493,7 @@ static cudaError_t reorder_with(PagesParams p, int n_sm, cudaStream_t stream)
     cudaError_t e = configure(reinterpret_cast<const void *>(pages_reorder_kernel<CL>),
                               kPagesMaxBatch * 6 * (int)sizeof(int), configured);
     if (e != cudaSuccess) return e;
-    p.fused = copies_fit(p, p.B, CL);
+    p.fused = copies_fit(p, p.B, CL == 1 ? kFusedBytes : kFusedBytesCluster);
     e = launch_pdl(pages_reorder_kernel<CL>, dim3(CL), dim3(kThreads), (size_t)p.B * 6 * sizeof(int), stream, p);
     if (e != cudaSuccess || p.fused) return e;
     return launch_copies(p, p.B, n_sm, stream);
@@ -497,7 +502,7 @@ static cudaError_t reorder_with(PagesParams p, int n_sm, cudaStream_t stream)
 cudaError_t launch_pages_reorder(PagesParams p, int n_sm, cudaStream_t stream)
 {
     // barriers of a cluster cost more than they save where the tables are small: 4 runs 7.9 us by one block and
-    // 11.7 by the cluster, 128 runs 19.9 and 18.1
+    // 11.7 by the cluster, 64 runs 14.8 and 17.2, 128 runs 19.9 and 18.1
     const bool one = (long long)p.B * ((p.max_blocks + 31) / 32) <= kOneBlock && p.n_pool <= kOnePool;
     return one ? reorder_with<1>(p, n_sm, stream) : reorder_with<kCl>(p, n_sm, stream);
 }
@@ -507,7 +512,7 @@ cudaError_t launch_pages_compact(PagesParams p, int n_sm, cudaStream_t stream)
     static bool configured[64] = {};
     cudaError_t e = configure(reinterpret_cast<const void *>(pages_compact_kernel), kPagesMaxPool / 8, configured);
     if (e != cudaSuccess) return e;
-    p.fused = copies_fit(p, p.n_pool / 2, kCl);
+    p.fused = copies_fit(p, p.n_pool / 2, kFusedBytesCluster);
     e = launch_pdl(pages_compact_kernel, dim3(kCl), dim3(kThreads), (size_t)((p.n_pool + 31) / 32) * 4, stream, p);
     if (e != cudaSuccess || p.fused) return e;
     return launch_copies(p, p.n_pool / 2, n_sm, stream);
