@@ -348,7 +348,6 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     int page_at = -1, pages = 0;             // the 32 table entries in this warp's lanes: first one's number
     int ld_b = -1, ld_hr = -1;
     long long head = 0;                      // the loaded row tile's head's first page
-    const int32_t *tab = p.table;
     // where this lane's chunk i * 32 + lane of a step's rows goes: chunk c of row r lies at c ^ 4 (r & 1) for
     // keys and at c ^ 2 (r / 2 & 3) for values (64 dims: c and c ^ 2 (r / 2 & 1)), which keeps the
     // fragments' reads free of bank conflicts (the values of 64 dims: two ways).  A copy's rows are
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             }
     };
 
-    if (first.more()) {    // (while the first steps are on their way)
+    if (first.more()) {                      // (while the first steps are on their way)
         cur_b = first.b;
         cur_hr = first.hr;
         cur_len = first.len;

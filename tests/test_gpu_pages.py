@@ -279,6 +279,27 @@ def test_a_large_pool(kvc):
             assert torch.equal(x, y)
 
 
+def test_the_largest_pool(kvc):
+    """2^20 pages, one in a thousand live and anywhere."""
+    NB, n = 2 ** 20, 1000
+    g = torch.Generator().manual_seed(1)
+    perm = torch.randperm(NB, generator=g).to(torch.int32)
+    k, v = (torch.zeros((1, NB, 16, 64), dtype=torch.uint8, device=DEV) for _ in range(2))
+    ks, vs = torch.zeros((1, NB), device=DEV), torch.zeros((1, NB), device=DEV)
+    table = perm[:n].view(4, 250).to(DEV)
+    ks[0, table.long()] = torch.arange(n, device=DEV).float().view(4, 250)
+    ids = torch.zeros(NB, dtype=torch.int32)
+    ids[:NB - n] = perm[n:]
+    ids, top = ids.to(DEV), torch.tensor([NB - n], dtype=torch.int32, device=DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    pt = kvc.page_table_view(table, i32([250] * 4), i32([4000] * 4), torch.zeros((4, 250), device=DEV))
+    remap = kvc.kvc_pages_compact(kvc.block_pool_q8_view(k, v, ks, vs), pt, kvc.free_pool_view(ids, top))
+    assert kvc.kvc_device_status() == 0
+    assert sorted(table.flatten().tolist()) == list(range(n)) and int((remap >= 0).sum()) == n
+    assert torch.equal(ks[0, table.long()], torch.arange(n, device=DEV).float().view(4, 250))
+    assert torch.equal(ids[:NB - n], torch.arange(NB - 1, n - 1, -1, dtype=torch.int32, device=DEV))
+
+
 @pytest.mark.parametrize("code,change", [
     (10, lambda c: c.top.fill_(-1)), (10, lambda c: c.top.fill_(10 ** 6)), (9, lambda c: c.ids.__setitem__(0, -1)),
     (9, lambda c: c.ids.__setitem__(0, 10 ** 6)), (9, lambda c: c.ids.__setitem__(0, int(c.ids[1]))),

@@ -123,6 +123,46 @@ def test_beams_over_8_bit_pages(kvc):
     assert int(s["top"]) == 60 and not bool(shares.any()) and kvc.kvc_device_status() == 0
 
 
+def test_a_captured_step_is_an_eager_one(kvc):
+    """Norms, append, attention, eviction and a reorder captured once and replayed, against the same calls."""
+    B, Hq, H, D, bs, mb, NB = 3, 8, 2, 64, 16, 6, 40
+    cs = kvc.kvc_rope_table(256, D).to(DEV)
+    w = rows(1, D)
+    runs = []
+    for captured in (False, True):
+        s = make(kvc, B, H, D, bs, NB, mb)
+        shares = torch.zeros(NB, dtype=torch.int32, device=DEV)
+        par = torch.tensor([2, 1, 0], dtype=torch.int32, device=DEV)
+        qkv, lse = torch.zeros((B, Hq + 2 * H, D), dtype=torch.bfloat16, device=DEV), torch.zeros((B, Hq), device=DEV)
+        logits, out = torch.zeros((B, Hq, mb * bs), device=DEV), torch.zeros((B, Hq, D), dtype=torch.bfloat16, device=DEV)
+        qo, ko = torch.zeros_like(out), torch.zeros((B, H, D), dtype=torch.bfloat16, device=DEV)
+        v = torch.zeros((B, H, D), dtype=torch.bfloat16, device=DEV)
+        spaces = (kvc.append_q8_workspace(B, B, bs, DEV), kvc.decode_q8_workspace(B, Hq, H, D, torch.bfloat16, DEV),
+                  kvc.pages_workspace(B, mb, NB, DEV))
+
+        def step():
+            kvc.kvc_qk_norm_rope(qkv[:, :Hq], qkv[:, Hq:Hq + H], w_q=w, w_k=w, cos_sin=cs, pos=s["len"], q_out=qo, k_out=ko)
+            v.copy_(qkv[:, Hq + H:])
+            kvc.kvc_paged_append_q8(s["pool"], s["pt"], s["free"], ko, v, ws=spaces[0])
+            kvc.kvc_decode_attn_paged_q8(qo, s["pool"], s["pt"], scale=0.125, out=out, logits=logits, lse=lse, ws=spaces[1])
+            kvc.kvc_block_accumulate_evict(logits, lse, s["pt"], s["free"], block_size=bs, budget_blocks=4, recent_blocks=2)
+            kvc.kvc_pages_reorder(s["pool"], s["pt"], s["free"], shares, par, ws=spaces[2])
+
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        outs = []
+        for i in range(90):
+            qkv.copy_(rows(100 + i, B, Hq + 2 * H, D))
+            graph.replay() if captured else step()
+            outs.append(out.clone())
+        assert kvc.kvc_device_status() == 0 and not bool(shares.any())
+        runs.append((torch.stack(outs), s["len"].clone(), s["n_blocks"].clone(), s["score"].clone()))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
 def test_two_streams_with_workspaces_of_their_own(kvc):
     """Two calls at once on different streams, each with a workspace that the binding made."""
     B, H, D, bs = 2, 2, 64, 16
