@@ -15,13 +15,15 @@
 // pages_compact_kernel: the k-th live page beyond the number of live pages moves to the k-th free page
 // below it; tables, counts and the stack follow.  No page is both read and written.
 //
-// Both tables' kernels are one block or one cluster of 8 with a few barriers (a launch per step would cost
-// more than the steps); what blocks tell each other goes through the workspace.  Bound by latency: every
-// step is a trip or two to memory.  For compaction each block keeps the free pages as bits in shared
-// memory and works out by itself where everything goes, which left one barrier of the cluster of six (16384
-// pages, tables and copies: 111 -> 105 us).  The copies are bound by HBM: a page's keys or values of a head are
-// one run, which a warp copies with 128 bytes a lane in flight and the next copy's ids read ahead: 515 MB of
-// 4 KB runs, read and written, in 77 us, 6.7 TB/s (a block a page with 64 bytes a thread: 84 us).
+// The tables' kernels are a cluster of 8 blocks with a few barriers (a launch per step would cost more than the
+// steps); what blocks tell each other goes through the workspace.  Bound by latency: every step is a trip or two
+// to memory.  Reorders whose tables and counts fit the shared memory of one block need two trips and no barrier
+// of the cluster (pages_reorder_one_kernel: 128 sequences of 26 pages with 20 MB of copies 18.1 -> 13.0 us).
+// For compaction each block keeps the free pages as bits in shared memory and works out by itself where
+// everything goes, which left one barrier of the cluster of six (16384 pages, tables and copies: 111 -> 105 us).
+// The copies are bound by HBM: a page's keys or values of a head are one run, which a warp copies with 128
+// bytes a lane in flight and the next copy's ids read ahead: 515 MB of 4 KB runs, read and written, in 77 us,
+// 6.7 TB/s (a block a page with 64 bytes a thread: 84 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -39,7 +41,10 @@ constexpr int kCopyThreads_ = 256, kCopyBlocks = 8;      // of the copies: threa
 // second kernel, 1 MB: 11.7 and 10.7.  By the cluster, 256 KB: 10.9 and 9.8 on the device, but a call from
 // Python, which the host bounds, 24 and 27.
 constexpr long long kFusedBytes = 1 << 19, kFusedBytesCluster = 1 << 18;
-constexpr int kOneBlock = 64, kOnePool = 16384;          // 32-entry runs of the tables, and pages, that one block takes
+// Reorders that one block takes: bytes of shared memory, runs of 32 table entries.  Device times by one block and by
+// the cluster: 4 runs 5.2 and 11.1 us, 128 runs 13.1 and 18.1, 256 runs 11.5 and 15.4, 512 runs 18.9 to 20.2 and
+// 18.0 to 18.6, 1024 runs 27.9 and 22.4; 4 runs and a pool of 32000 pages 10.2 and 12.1.
+constexpr int kOneBytes = 200 * 1024, kOneRuns = 256;
 constexpr int kBadIndex = 3, kBadLength = 5, kBadBlock = 9, kPoolEmpty = 10, kPoolOverflow = 11, kSharedPage = 12;
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -49,13 +54,8 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 // Also orders the cluster's global memory accesses.
-template <int CL>
 __device__ __forceinline__ void cluster_barrier()
 {
-    if (CL == 1) {
-        __syncthreads();
-        return;
-    }
     __threadfence();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -138,14 +138,13 @@ __device__ __forceinline__ void copy_pages(const PagesParams &p, int n_copies, l
     }
 }
 
-template <int CL>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reorder_kernel(const PagesParams p)
+__global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_reorder_kernel(const PagesParams p)
 {
     extern __shared__ int s_seq[];           // per sequence: children, keeper, parent, blocks, length, copy
     __shared__ int s_warp[32];
     int *s_kids = s_seq, *s_keep = s_kids + p.B, *s_par = s_keep + p.B, *s_nb = s_par + p.B, *s_len = s_nb + p.B,
         *s_copy = s_len + p.B;
-    const int tid = threadIdx.x, rank = CL == 1 ? 0 : (int)cluster_rank();
+    const int tid = threadIdx.x, rank = (int)cluster_rank();
     pdl_trigger();
     pdl_wait();
     // ---- the sequences, in every block alike ----
@@ -167,7 +166,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reo
         s_len[b] = len;
     }
     const bool bad = __syncthreads_or(code != 0);
-    cluster_barrier<CL>();                       // (ws_n is there; no block has left)
+    cluster_barrier();                       // (ws_n is there; no block has left)
     if (bad) {
         if (rank == 0 && code != 0) record_code(p.dev_code, code);
         return;
@@ -200,14 +199,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reo
     auto partial = [&](int b, int i) { return s_len[b] % p.bs != 0 && i == s_nb[b] - 1; };
     // ---- the tables' ids, of the sequences that change ----
     auto touched = [&](int b) { return s_kids[b] == 1 && s_par[b] == b ? 0 : s_nb[b]; };
-    each_entry<CL>(p.B, p.max_blocks, rank, touched, [&](int b, int i) {
+    each_entry<kCl>(p.B, p.max_blocks, rank, touched, [&](int b, int i) {
         const int id = p.table[(size_t)b * p.max_blocks + i];
         int c = 0;
         if (id < 0 || id >= p.n_pool) c = kBadBlock;
         else if (partial(b, i) && p.shares[id] != 0) c = kSharedPage;
         if (c != 0) atomicCAS(&p.ws_n[1], 0, c);
     });
-    cluster_barrier<CL>();
+    cluster_barrier();
     code = __ldcg(&p.ws_n[1]);
     if (code != 0) {                         // nothing has changed yet
         if (rank == 0 && tid == 0) record_code(p.dev_code, code);
@@ -215,14 +214,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reo
     }
     // ---- holders of every page ----
     auto count = [&](int sign) {
-        each_entry<CL>(p.B, p.max_blocks, rank, [&](int b) { return s_kids[b] == 1 ? 0 : s_nb[b]; }, [&](int b, int i) {
+        each_entry<kCl>(p.B, p.max_blocks, rank, [&](int b) { return s_kids[b] == 1 ? 0 : s_nb[b]; }, [&](int b, int i) {
             if (s_kids[b] > 0 && partial(b, i)) return;
             atomicAdd(&p.shares[p.table[(size_t)b * p.max_blocks + i]], sign * (s_kids[b] - 1));
         });
     };
     count(1);
-    cluster_barrier<CL>();
-    const int x0 = (int)((long long)p.n_pool * rank / CL), x1 = (int)((long long)p.n_pool * (rank + 1) / CL);
+    cluster_barrier();
+    const int x0 = (int)((long long)p.n_pool * rank / kCl), x1 = (int)((long long)p.n_pool * (rank + 1) / kCl);
     int gone = 0;
     for (int x = x0 + tid; x < x1; x += kThreads) {
         const int s = __ldcg(&p.shares[x]);
@@ -240,10 +239,10 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reo
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (tid == 0) p.ws_n[2 + rank] = x;
     }
-    cluster_barrier<CL>();
+    cluster_barrier();
     int before = 0, n_gone = 0;
 #pragma unroll
-    for (int r = 0; r < CL; ++r) {
+    for (int r = 0; r < kCl; ++r) {
         const int x = __ldcg(&p.ws_n[2 + r]);
         if (r < rank) before += x;
         n_gone += x;
@@ -276,13 +275,13 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reo
         before += all;
     }
     auto moved = [&](int b) { return s_par[b] < 0 || s_par[b] == b ? 0 : s_nb[s_par[b]]; };
-    each_entry<CL>(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
+    each_entry<kCl>(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
         const size_t from = (size_t)s_par[b] * p.max_blocks + i, to = (size_t)b * p.max_blocks + i;
         p.ws_table[to] = p.table[from];
         p.ws_score[to] = p.score[from];
     });
-    cluster_barrier<CL>();
-    each_entry<CL>(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
+    cluster_barrier();
+    each_entry<kCl>(p.B, p.max_blocks, rank, moved, [&](int b, int i) {
         const size_t at = (size_t)b * p.max_blocks + i;
         int id = __ldcg(&p.ws_table[at]);
         const int copy = s_copy[b];
@@ -308,8 +307,167 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads) pages_reo
         }
     }
     if (p.fused) {
-        cluster_barrier<CL>();
-        copy_pages(p, n_copies, rank * (kThreads / 32) + (tid >> 5), CL * kThreads / 32);
+        cluster_barrier();
+        copy_pages(p, n_copies, rank * (kThreads / 32) + (tid >> 5), kAll / 32);
+    }
+}
+
+// The same by one block that holds everything in shared memory: tables, scores, counts and sequences come
+// in one trip to memory, the rest is steps between barriers of the block, and results go out once.
+__host__ __device__ inline size_t one_block_bytes(const PagesParams &p)
+{
+    return ((size_t)p.B * (7 + 2 * (size_t)p.max_blocks) + (size_t)p.n_pool) * 4 + ((size_t)p.n_pool + 1) / 2 * 4;
+}
+__device__ __forceinline__ void take_4(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads) pages_reorder_one_kernel(const PagesParams p)
+{
+    extern __shared__ int s_seq[];           // per sequence as above and an id of the stack; tables, scores, counts, freed
+    __shared__ int s_warp[32];
+    int *s_kids = s_seq, *s_keep = s_kids + p.B, *s_par = s_keep + p.B, *s_nb = s_par + p.B, *s_len = s_nb + p.B,
+        *s_copy = s_len + p.B, *s_stack = s_copy + p.B, *s_table = s_stack + p.B;
+    const int entries = p.B * p.max_blocks;
+    int *s_score = s_table + entries, *s_count = s_score + entries;
+    uint16_t *s_freed = reinterpret_cast<uint16_t *>(s_count + p.n_pool);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
+    pdl_wait();
+    if (tid == 0) p.ws_n[0] = 0;             // copies
+    const int top = *p.free_top;
+    for (int j = tid; j < entries; j += kThreads) {
+        take_4(s_table + j, p.table + j);
+        take_4(s_score + j, p.score + j);
+    }
+    for (int x = tid; x < p.n_pool; x += kThreads) take_4(s_count + x, p.shares + x);
+    int code = top < 0 || top > p.free_cap ? kPoolEmpty : 0;
+    for (int b = tid; b < p.B; b += kThreads) {
+        const int par = p.parent[b], len = p.len[b], nb = p.n_blocks[b];
+        if (par < -1 || par >= p.B) code = kBadIndex;
+        if (len < 0 || len > p.max_blocks * p.bs || nb != (len + p.bs - 1) / p.bs) code = kBadLength;
+        s_kids[b] = 0;
+        s_keep[b] = 0x7fffffff;
+        s_par[b] = par;
+        s_nb[b] = nb;
+        s_len[b] = len;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (__syncthreads_or(code != 0)) {
+        if (code != 0) record_code(p.dev_code, code);
+        return;
+    }
+    for (int b = tid; b < p.B; b += kThreads) {
+        const int par = s_par[b];
+        if (par >= 0) {
+            atomicAdd(&s_kids[par], 1);
+            atomicMin(&s_keep[par], b);
+        }
+    }
+    __syncthreads();
+    int n_copies = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + tid;
+        bool own = false;
+        if (b < p.B) {
+            const int par = s_par[b];
+            own = par >= 0 && par != b && s_len[par] % p.bs != 0 && (s_par[par] == par || s_keep[par] != b);
+        }
+        int all;
+        const int r = block_rank(own, s_warp, &all);
+        if (b < p.B) s_copy[b] = own ? n_copies + r : -1;
+        n_copies += all;
+    }
+    // ids that copies may need, from the top of the stack
+    for (int e = tid; e < min(n_copies, top); e += kThreads) take_4(s_stack + e, p.free_ids + top - 1 - e);
+    auto partial = [&](int b, int i) { return s_len[b] % p.bs != 0 && i == s_nb[b] - 1; };
+    auto stays = [&](int b) { return s_kids[b] == 1 && s_par[b] == b; };
+    // ---- partly filled pages of the sequences that change have one holder ----
+    for (int b = tid; b < p.B; b += kThreads)
+        if (!stays(b) && s_len[b] % p.bs != 0) {
+            const int id = s_table[b * p.max_blocks + s_nb[b] - 1];
+            if (id >= 0 && id < p.n_pool && s_count[id] != 0) code = kSharedPage;
+        }
+    __syncthreads();
+    // ---- holders of every page ----
+    each_entry<1>(p.B, p.max_blocks, 0, [&](int b) { return stays(b) ? 0 : s_nb[b]; }, [&](int b, int i) {
+        const int id = s_table[b * p.max_blocks + i], more = s_kids[b] - 1;
+        if (id < 0 || id >= p.n_pool) code = kBadBlock;
+        else if (more != 0 && !(more > 0 && partial(b, i))) atomicAdd(&s_count[id], more);
+    });
+    if (__syncthreads_or(code != 0)) {
+        if (code != 0) record_code(p.dev_code, code);
+        return;
+    }
+    // a warp looks at `per` runs of 32 pages
+    const int per = (p.n_pool + kThreads - 1) / kThreads, x0 = warp * per * 32 + lane;
+    int gone = 0;
+    for (int r = 0, x = x0; r < per; ++r, x += 32) {
+        const int s = x < p.n_pool ? s_count[x] : 0;
+        gone += __popc(__ballot_sync(0xffffffffu, s < 0));
+        if (s < -1) code = kBadBlock;        // held by more sequences than it counted
+    }
+    if (lane == 0) s_warp[warp] = gone;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    int x = s_warp[lane];
+    const int own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    const int n_gone = __shfl_sync(0xffffffffu, x, 31);
+    int before = __shfl_sync(0xffffffffu, x - own, warp);
+    const int new_top = top + n_gone - n_copies;
+    if (code == 0 && new_top < 0) code = kPoolEmpty;
+    if (code == 0 && new_top > p.free_cap) code = kPoolOverflow;
+    for (int e = tid; e < min(n_copies - n_gone, top); e += kThreads)
+        if (code == 0 && (s_stack[e] < 0 || s_stack[e] >= p.n_pool)) code = kBadBlock;
+    if (__syncthreads_or(code != 0)) {       // nothing has changed
+        if (code != 0) record_code(p.dev_code, code);
+        return;
+    }
+    // ---- freed pages in ascending order; the tables as the children have them ----
+    for (int r = 0, x = x0; r < per; ++r, x += 32) {
+        const int s = x < p.n_pool ? s_count[x] : 0;
+        const uint32_t votes = __ballot_sync(0xffffffffu, s < 0);
+        if (s < 0) {
+            const int k = before + __popc(votes & ((1u << lane) - 1u));
+            s_freed[k] = (uint16_t)x;
+            if (top + k < new_top) p.free_ids[top + k] = x;
+        }
+        if (x < p.n_pool) p.shares[x] = max(s, 0);
+        before += __popc(votes);
+    }
+    __syncthreads();
+    each_entry<1>(p.B, p.max_blocks, 0, [&](int b) { return s_par[b] < 0 || s_par[b] == b ? 0 : s_nb[s_par[b]]; },
+                  [&](int b, int i) {
+        const int par = s_par[b], from = par * p.max_blocks + i, copy = s_copy[b];
+        int id = s_table[from];
+        if (copy >= 0 && i == s_nb[par] - 1) {
+            const int place = n_gone - 1 - copy;
+            const int to = place >= 0 ? s_freed[place] : s_stack[-1 - place];
+            p.ws_copies[copy] = make_int4(id, to, s_len[par] % p.bs, 0);
+            id = to;
+        }
+        p.table[b * p.max_blocks + i] = id;
+        p.score[b * p.max_blocks + i] = __int_as_float(s_score[from]);
+    });
+    for (int b = tid; b < p.B; b += kThreads) {
+        const int par = s_par[b];
+        if (par == b) continue;
+        p.n_blocks[b] = par < 0 ? 0 : s_nb[par];
+        p.len[b] = par < 0 ? 0 : s_len[par];
+    }
+    if (tid == 0) {
+        p.ws_n[0] = n_copies;
+        *p.free_top = new_top;
+    }
+    if (p.fused) {
+        __syncthreads();
+        copy_pages(p, n_copies, warp, kThreads / 32);
     }
 }
 
@@ -418,7 +576,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_co
                 ++r;
             }
     }
-    cluster_barrier<kCl>();
+    cluster_barrier();
 #pragma unroll
     for (int r = 0; r < kCl; ++r) code = max(code, __ldcg(&p.ws_n[2 + r]));
     const int holes = s_holes;
@@ -449,7 +607,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_co
         if (x >= n_live) *e = __ldcg(&p.ws_ids[f.rank_high(x, holes)]);
     });
     if (p.fused) {
-        cluster_barrier<kCl>();
+        cluster_barrier();
         copy_pages(p, holes, rank * (kThreads / 32) + (tid >> 5), kAll / 32);
     }
 }
@@ -486,25 +644,19 @@ cudaError_t configure(const void *kernel, int bytes, bool *configured)
 
 }  // namespace
 
-template <int CL>
-static cudaError_t reorder_with(PagesParams p, int n_sm, cudaStream_t stream)
-{
-    static bool configured[64] = {};
-    cudaError_t e = configure(reinterpret_cast<const void *>(pages_reorder_kernel<CL>),
-                              kPagesMaxBatch * 6 * (int)sizeof(int), configured);
-    if (e != cudaSuccess) return e;
-    p.fused = copies_fit(p, p.B, CL == 1 ? kFusedBytes : kFusedBytesCluster);
-    e = launch_pdl(pages_reorder_kernel<CL>, dim3(CL), dim3(kThreads), (size_t)p.B * 6 * sizeof(int), stream, p);
-    if (e != cudaSuccess || p.fused) return e;
-    return launch_copies(p, p.B, n_sm, stream);
-}
-
 cudaError_t launch_pages_reorder(PagesParams p, int n_sm, cudaStream_t stream)
 {
-    // barriers of a cluster cost more than they save where the tables are small: 4 runs 7.9 us by one block and
-    // 11.7 by the cluster, 64 runs 14.8 and 17.2, 128 runs 19.9 and 18.1
-    const bool one = (long long)p.B * ((p.max_blocks + 31) / 32) <= kOneBlock && p.n_pool <= kOnePool;
-    return one ? reorder_with<1>(p, n_sm, stream) : reorder_with<kCl>(p, n_sm, stream);
+    static bool configured[64] = {}, configured_one[64] = {};
+    const bool one = one_block_bytes(p) <= (size_t)kOneBytes && (long long)p.B * ((p.max_blocks + 31) / 32) <= kOneRuns;
+    auto kernel = one ? pages_reorder_one_kernel : pages_reorder_kernel;
+    cudaError_t e = one ? configure(reinterpret_cast<const void *>(kernel), kOneBytes, configured_one)
+                        : configure(reinterpret_cast<const void *>(kernel), kPagesMaxBatch * 6 * (int)sizeof(int), configured);
+    if (e != cudaSuccess) return e;
+    p.fused = copies_fit(p, p.B, one ? kFusedBytes : kFusedBytesCluster);
+    e = launch_pdl(kernel, dim3(one ? 1 : kCl), dim3(kThreads), one ? one_block_bytes(p) : (size_t)p.B * 6 * sizeof(int),
+                   stream, p);
+    if (e != cudaSuccess || p.fused) return e;
+    return launch_copies(p, p.B, n_sm, stream);
 }
 
 cudaError_t launch_pages_compact(PagesParams p, int n_sm, cudaStream_t stream)

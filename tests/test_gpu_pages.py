@@ -188,6 +188,52 @@ def test_reorder_refusals_change_nothing(kvc, code, change):
     unchanged(c, before)
 
 
+def _far(c, par, code):
+    if code == 10:
+        par[2] = 0
+        c.len[1:], c.n_blocks[1:] = 0, 0
+
+
+@pytest.mark.parametrize("code,change", [
+    (3, lambda c, par: par.__setitem__(1, 4)), (5, lambda c, par: c.len.__setitem__(2, 10 ** 6)),
+    (5, lambda c, par: c.n_blocks.__setitem__(1, 1)), (9, lambda c, par: c.table.__setitem__((0, 1), -1)),
+    (12, lambda c, par: c.shares.__setitem__(int(c.table[0, 1]), 1)), (10, lambda c, par: c.top.fill_(-1)),
+    (10, lambda c, par: c.top.fill_(0)), (9, lambda c, par: c.table.__setitem__((3, 0), int(c.table[2, 0])))])
+@pytest.mark.parametrize("mb", [2048, 2049])
+def test_reorder_refusals_of_large_tables(kvc, mb, code, change):
+    """Tables of 256 and 260 runs of 32 entries, of one block and of a cluster."""
+    c = Cache(kvc, [20, 33, 16, 16], max_blocks=mb)
+    par = torch.tensor([0, 0, -1, -1], dtype=torch.int32, device=DEV)
+    _far(c, par, code)
+    change(c, par)
+    before = state(c)
+    kvc.kvc_pages_reorder(c.pool, c.pt, c.free, c.shares, par, pos=c.pos)
+    assert kvc.kvc_device_status() == code
+    unchanged(c, before)
+
+
+@pytest.mark.parametrize("mb", [12, 2100])
+def test_reorders_in_turn_with_few_free_pages(kvc, mb):
+    """The same reorders over short tables (one block) and long ones (a cluster), the stack almost empty."""
+    rng = random.Random(7)
+    c = Cache(kvc, [rng.randint(0, 40) for _ in range(5)], bs=16, spare=9, max_blocks=mb, kind="e4m3")
+    for step in range(20):
+        c.reorder([rng.choice([-1, 0, 1, 2, 3, 4, b]) for b in range(5)])
+        c.check()
+    assert kvc.kvc_device_status() == 0
+
+
+@pytest.mark.parametrize("NB", [32767, 32768, 33900, 34300])
+def test_reorder_in_a_pool_that_just_fits_shared_memory(kvc, NB):
+    c = Cache(kvc, [40, 17, 0, 90], H=1, D=64, spare=NB - 11)
+    assert c.k.shape[1] == NB
+    c.reorder([3, 0, 0, -1])
+    c.check()
+    c.reorder([2, 1, 1, 0])
+    c.check()
+    assert kvc.kvc_device_status() == 0
+
+
 def test_pages_listed_more_often_than_counted(kvc):
     c = Cache(kvc, [32, 32])
     c.table[1, 0] = c.table[0, 0]
