@@ -37,10 +37,10 @@ constexpr int kCl = 8;                       // blocks of the cluster
 constexpr int kThreads = 1024;
 constexpr int kAll = kCl * kThreads;
 constexpr int kCopyThreads_ = 256, kCopyBlocks = 8;      // of the copies: threads of a block, blocks per SM
-// Copies of so many bytes at most are made by the tables' kernel itself.  By one block, 512 KB: 8.6 us and 9.4 with a
-// second kernel, 1 MB: 11.7 and 10.7.  By the cluster, 256 KB: 10.9 and 9.8 on the device, but a call from
-// Python, which the host bounds, 24 and 27.
-constexpr long long kFusedBytes = 1 << 19, kFusedBytesCluster = 1 << 18;
+// Copies of so many bytes at most are made by the tables' kernel itself.  Reorders, by it and by a second kernel:
+// 64 KB 5.3 and 5.7 us, 256 KB 11.6 and 12.3, 512 KB 8.9 and 7.9.  Compaction, 256 KB: 10.9 and 9.8 on the
+// device, but a call from Python, which the host bounds, 24 and 27.
+constexpr long long kFusedBytes = 1 << 18;
 // Reorders that one block takes: bytes of shared memory, runs of 32 table entries.  Device times by one block and by
 // the cluster: 4 runs 5.2 and 11.1 us, 128 runs 13.1 and 18.1, 256 runs 11.5 and 15.4, 512 runs 18.9 to 20.2 and
 // 18.0 to 18.6, 1024 runs 27.9 and 22.4; 4 runs and a pool of 32000 pages 10.2 and 12.1.
@@ -627,9 +627,9 @@ cudaError_t launch_copies(const PagesParams &p, long long copies, int n_sm, cuda
     const long long blocks = std::max(1LL, std::min(need, most));
     return launch_pdl(pages_copy_kernel, dim3((unsigned)blocks), dim3(kCopyThreads_), 0, stream, p);
 }
-bool copies_fit(const PagesParams &p, long long copies, long long bytes)
+bool copies_fit(const PagesParams &p, long long copies)
 {
-    return copies * p.H * p.bs * p.row_bytes * 2 <= bytes;
+    return copies * p.H * p.bs * p.row_bytes * 2 <= kFusedBytes;
 }
 
 cudaError_t configure(const void *kernel, int bytes, bool *configured)
@@ -652,7 +652,7 @@ cudaError_t launch_pages_reorder(PagesParams p, int n_sm, cudaStream_t stream)
     cudaError_t e = one ? configure(reinterpret_cast<const void *>(kernel), kOneBytes, configured_one)
                         : configure(reinterpret_cast<const void *>(kernel), kPagesMaxBatch * 6 * (int)sizeof(int), configured);
     if (e != cudaSuccess) return e;
-    p.fused = copies_fit(p, p.B, one ? kFusedBytes : kFusedBytesCluster);
+    p.fused = copies_fit(p, p.B);
     e = launch_pdl(kernel, dim3(one ? 1 : kCl), dim3(kThreads), one ? one_block_bytes(p) : (size_t)p.B * 6 * sizeof(int),
                    stream, p);
     if (e != cudaSuccess || p.fused) return e;
@@ -664,7 +664,7 @@ cudaError_t launch_pages_compact(PagesParams p, int n_sm, cudaStream_t stream)
     static bool configured[64] = {};
     cudaError_t e = configure(reinterpret_cast<const void *>(pages_compact_kernel), kPagesMaxPool / 8, configured);
     if (e != cudaSuccess) return e;
-    p.fused = copies_fit(p, p.n_pool / 2, kFusedBytesCluster);
+    p.fused = copies_fit(p, p.n_pool / 2);
     e = launch_pdl(pages_compact_kernel, dim3(kCl), dim3(kThreads), (size_t)((p.n_pool + 31) / 32) * 4, stream, p);
     if (e != cudaSuccess || p.fused) return e;
     return launch_copies(p, p.n_pool / 2, n_sm, stream);
