@@ -384,7 +384,8 @@ struct QkNormParams {
     const float *cos_sin;        // [n_pos][2][rot/2]; rot 0: no rotation
     const int32_t *pos;          // [n_tokens]
     int32_t n_pos;
-    int32_t tasks, q_tasks;      // warps per token, those of its queries (set by the launch)
+    int32_t tasks, q_tasks;      // units of a group of tokens, those of its queries (set by the launch)
+    int32_t ahead;               // the next rows are fetched into L2
     int32_t *dev_code;
 };
 cudaError_t launch_qk_norm_rope(const QkNormParams &p, int D, bool bf16, int n_sm, cudaStream_t stream);

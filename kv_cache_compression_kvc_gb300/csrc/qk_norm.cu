@@ -9,12 +9,17 @@
 // lies in D/8 lanes, and a lane holds 4 elements and their 4 partners, so that the rotation needs no
 // exchange (with 8 neighbours a lane it took 8 shuffles a row: 151 us for 32768 tokens of 32 + 8 heads of
 // 128, bf16); where only a part is rotated, the lanes behind it hold 8 neighbours.  Weights and angles
-// are multiplied once for the rows of a unit (some rows per lane group, of one token and kind), which
-// leaves three products an element:
+// are multiplied once for the rows of a unit (some rows per lane group, of one kind), which leaves three
+// products an element:
 //   out_a = r (a (w_a c) - b (w_b s)),  out_b = r (b (w_b c) + a (w_a s)),  r = rsqrt(mean + eps).
-// Persistent warps take units in order, and a token's angles are read once for them.  Measured on that
-// prompt: 114 us (6.0 TB/s, 89 % of the copy rate) with 24 warps an SM; 116 with 32 (64 registers), 127
-// with the next unit's rows loaded ahead in registers (spills), 159 with a warp per unit.
+// The rows side by side in a warp are neighbouring heads of a token; where that leaves lanes without rows
+// (few heads), those of neighbouring tokens: 100000 tokens of 8 + 1 heads of 64, bf16, 81.6 -> 44.6 us, 20000 of
+// 4 + 1, fp32, 12.7 -> 8.6, but the prompt above 108.8 -> 111.6.
+// Persistent warps take whole tokens in turn, so that all read from one stretch of memory, and share the
+// units of the last ones; a token's angles are read once for its units.  Measured on that prompt: 108.8 us
+// (6.3 TB/s, 93 % of the copy rate) with 24 warps an SM and the next unit on its way into L2; 114 without the
+// latter, 108.2 with a ring in shared memory instead (which costs 2 us of 17 at 5000 tokens), 113.5 with neighbouring
+// tokens a warp, 127 with the next unit's rows in registers (spills), 159 with a warp per unit.
 #include <algorithm>
 
 #include "common.cuh"
@@ -29,6 +34,10 @@ constexpr int kBlocks = 3;                   // per SM
 // Rows per lane group and unit.
 template <typename T>
 constexpr int kIterOf = sizeof(T) == 2 ? 4 : 2;
+// Rows of 16 bits, read and written, from which on the next unit is fetched into L2: 168 MB 31.9 us without and
+// 30.0 with it, 671 MB 114.7 and 108.8; where L2 holds them, 102 MB, 17.4 and 18.3.  fp32 rows, whose loads are twice
+// as wide, lose: 478 MB 76.2 and 81.0.
+constexpr long long kAheadBytes = 128 << 20;
 constexpr int kDevBadPos = 4;                // KVC_DEV_BAD_POSITION
 
 // 4 neighbouring elements as they lie in memory.
@@ -73,6 +82,7 @@ struct Four<float> {
     }
 };
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
 
@@ -80,11 +90,11 @@ __device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y
 struct Turn {
     float4 c, s;
     bool ok;                                 // the position lies in the table
-    __device__ __forceinline__ void load(const QkNormParams &p, int pos, int j)
+    __device__ __forceinline__ void load(const QkNormParams &p, int pos, int j, bool first)
     {
         ok = pos >= 0 && pos < p.n_pos;
         if (!ok) {
-            if ((threadIdx.x & 31) == 0) record_code(p.dev_code, kDevBadPos);
+            if (first) record_code(p.dev_code, kDevBadPos);
             return;
         }
         if (j >= p.rot / 2) return;          // (a lane that rotates nothing)
@@ -94,64 +104,104 @@ struct Turn {
     }
 };
 
-template <typename T, int D>
+// A warp's units: `rounds` whole groups of tokens, n_w apart, then `left` units in a row.
+struct Units {
+    int group, part, rounds, left, group1, part1, n_w, tasks;
+    __device__ __forceinline__ Units(const QkNormParams &p, int tokens)
+        : n_w((int)gridDim.x * kWarps), tasks(p.tasks)
+    {
+        const int n_groups = (p.n_tokens + tokens - 1) / tokens;
+        const int w = (int)blockIdx.x * kWarps + (threadIdx.x >> 5);
+        rounds = n_groups / n_w;
+        const int first = rounds * n_w;
+        const long long units = (long long)(n_groups - first) * tasks, u0 = units * w / n_w;
+        left = (int)(units * (w + 1) / n_w - u0);
+        group1 = first + (int)(u0 / tasks);
+        part1 = (int)(u0 - u0 / tasks * tasks);
+        group = rounds > 0 ? w : group1;
+        part = rounds > 0 ? 0 : part1;
+    }
+    __device__ __forceinline__ bool any() const { return rounds > 0 || left > 0; }
+    __device__ __forceinline__ void next()
+    {
+        if (rounds == 0) --left;
+        if (++part < tasks) return;
+        part = 0;
+        if (rounds == 0) {
+            ++group;
+            return;
+        }
+        group += n_w;
+        if (--rounds == 0) {
+            group = group1;
+            part = part1;
+        }
+    }
+};
+
+// TOKENS: the rows side by side in a warp are those of neighbouring tokens, else of neighbouring heads.
+template <typename T, int D, bool TOKENS>
 __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(const QkNormParams p)
 {
     constexpr int kIter = kIterOf<T>;
     constexpr int LPR = D / 8;               // lanes per row
-    constexpr int RPW = 32 / LPR;            // rows side by side in a warp
-    constexpr int ROWS = RPW * kIter;        // rows of a unit
+    constexpr int TOK = TOKENS ? 32 / LPR : 1;                 // tokens of a group
+    constexpr int SIDE = TOKENS ? 1 : 32 / LPR;                // heads side by side
+    constexpr int HEADS = SIDE * kIter;                        // of a unit
     const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5), n_w = (long long)gridDim.x * kWarps;
-    const long long units = (long long)p.n_tokens * p.tasks;
-    const long long u0 = units * w / n_w;
-    int left = (int)(units * (w + 1) / n_w - u0);
+    Units u(p, TOK);
     pdl_trigger();
     pdl_wait();
-    if (left == 0) return;
+    if (!u.any()) return;
     // this lane's elements: 4 at `at` and 4 at `at2`, its partners or its next ones
-    const int l = lane & (LPR - 1), row0 = lane / LPR;
+    const int l = lane & (LPR - 1), mine = TOKENS ? lane / LPR : 0, row0 = TOKENS ? 0 : lane / LPR;
     const bool turns = l * 8 < p.rot;
     const int at = turns ? l * 4 : l * 8, at2 = at + (turns ? p.rot / 2 : 4);
     const bool part_turns = p.rot < D;       // some lanes do not
 
-    int tok = (int)(u0 / p.tasks), part = (int)(u0 - (long long)tok * p.tasks);
     Turn turn;
     turn.c = make_float4(1.f, 1.f, 1.f, 1.f);
     turn.s = make_float4(0.f, 0.f, 0.f, 0.f);
     turn.ok = true;
-    int pos = p.rot > 0 ? p.pos[tok] : 0;
-    bool fresh = p.rot > 0;                  // a token whose angles are not there yet
+    int tok = u.group * TOK + mine;
+    int pos = p.rot > 0 && (!TOKENS || tok < p.n_tokens) ? p.pos[tok] : 0;
+    constexpr int kLines = D * (int)sizeof(T) / 128;           // of a row
+    bool fresh = p.rot > 0;                  // tokens whose angles are not there yet
 #pragma unroll 1
-    for (;; --left) {
+    for (;;) {
         Four<T> raw[kIter][2];
+        const bool is_k = u.part >= p.q_tasks;
+        const int h0 = (is_k ? u.part - p.q_tasks : u.part) * HEADS + row0;
+        const int all = is_k ? p.Hkv : p.Hq, heads = !TOKENS || tok < p.n_tokens ? all : 0;
         {
-            const bool is_k = part >= p.q_tasks;
-            const int h0 = (is_k ? part - p.q_tasks : part) * ROWS + row0, heads = is_k ? p.Hkv : p.Hq;
             const int64_t sh = is_k ? p.k_sh : p.q_sh;
             const T *src = static_cast<const T *>(is_k ? p.k : p.q) + tok * (is_k ? p.k_st : p.q_st) + h0 * sh;
 #pragma unroll
             for (int i = 0; i < kIter; ++i)
-                if (h0 + i * RPW < heads) {
-                    raw[i][0].load(src + i * RPW * sh + at);
-                    raw[i][1].load(src + i * RPW * sh + at2);
+                if (h0 + i * SIDE < heads) {
+                    raw[i][0].load(src + i * SIDE * sh + at);
+                    raw[i][1].load(src + i * SIDE * sh + at2);
                 } else {
                     raw[i][0].zero();
                     raw[i][1].zero();
                 }
         }
-        if (fresh) {
-            turn.load(p, pos, at);
-            if (tok + 1 < p.n_tokens) pos = p.pos[tok + 1];
+        const int group = u.group;
+        u.next();
+        const bool more = u.any();
+        if (p.ahead && more) {               // the next unit into L2, a line of 128 bytes a lane
+            const bool is_k = u.part >= p.q_tasks;
+            const int t = u.group * TOK + lane / (kLines * HEADS);
+            const int h = (is_k ? u.part - p.q_tasks : u.part) * HEADS + lane / kLines % HEADS;
+            if (lane < kLines * HEADS * TOK && t < p.n_tokens && h < (is_k ? p.Hkv : p.Hq))
+                prefetch_l2(static_cast<const T *>(is_k ? p.k : p.q) + t * (is_k ? p.k_st : p.q_st) +
+                            h * (is_k ? p.k_sh : p.q_sh) + lane % kLines * (128 / (int)sizeof(T)));
         }
-        int tok1 = tok, part1 = part + 1;
-        if (part1 == p.tasks) {
-            part1 = 0;
-            ++tok1;
-        }
-        const bool is_k = part >= p.q_tasks;
-        const int h0 = (is_k ? part - p.q_tasks : part) * ROWS + row0, heads = is_k ? p.Hkv : p.Hq;
+        if (fresh && (!TOKENS || tok < p.n_tokens)) turn.load(p, pos, at, l == 0);
         const int64_t sh = is_k ? p.ko_sh : p.qo_sh;
+        const int next = u.group * TOK + mine;
+        fresh = p.rot > 0 && more && u.group != group;
+        if (fresh && (!TOKENS || next < p.n_tokens)) pos = p.pos[next];
         T *dst = static_cast<T *>(is_k ? p.k_out : p.q_out) + tok * (is_k ? p.ko_st : p.qo_st) + h0 * sh;
         const T *wt = static_cast<const T *>(is_k ? p.w_k : p.w_q);
         // a c, a s, b c, b s of the weights a, b of the two groups of elements
@@ -175,6 +225,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(cons
         }
 #pragma unroll
         for (int i = 0; i < kIter; ++i) {
+            if (h0 - row0 + i * SIDE >= all) break;       // (the same for the whole warp)
             float2 a[2], b[2];
             raw[i][0].get(a);
             raw[i][1].get(b);
@@ -204,32 +255,34 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) qk_norm_rope_kernel(cons
                 ya[k] = mul2(ya[k], rr);
                 yb[k] = mul2(yb[k], rr);
             }
-            if (h0 + i * RPW < heads && turn.ok) {
-                Four<T>::store(dst + i * RPW * sh + at, ya);
-                Four<T>::store(dst + i * RPW * sh + at2, yb);
+            if (h0 + i * SIDE < heads && turn.ok) {
+                Four<T>::store(dst + i * SIDE * sh + at, ya);
+                Four<T>::store(dst + i * SIDE * sh + at2, yb);
             }
         }
-        if (left == 1) return;
-        fresh = p.rot > 0 && part1 == 0;
-        tok = tok1;
-        part = part1;
+        if (!more) return;
+        tok = next;
     }
 }
 
 template <typename T>
 cudaError_t launch_typed(QkNormParams p, int D, int n_sm, cudaStream_t stream)
 {
-    const int rows = 256 / D * kIterOf<T>;   // rows of a unit
-    p.q_tasks = (p.Hq + rows - 1) / rows;
-    p.tasks = p.q_tasks + (p.Hkv + rows - 1) / rows;
-    const long long units = (long long)p.n_tokens * p.tasks, most = (long long)n_sm * kBlocks;
+    // units of `side` tokens with their heads side by side, or with the tokens side by side
+    const int side = 256 / D, n = kIterOf<T>;
+    const auto parts = [](int heads, int per) { return (heads + per - 1) / per; };
+    const bool by_tokens = side > 1 && parts(p.Hq, n) + parts(p.Hkv, n) < side * (parts(p.Hq, side * n) + parts(p.Hkv, side * n));
+    const int tokens = by_tokens ? side : 1, heads = by_tokens ? n : side * n;         // of a unit
+    p.q_tasks = parts(p.Hq, heads);
+    p.tasks = p.q_tasks + parts(p.Hkv, heads);
+    const long long units = ((long long)p.n_tokens + tokens - 1) / tokens * p.tasks, most = (long long)n_sm * kBlocks;
     const long long blocks = std::min((units + kWarps - 1) / kWarps, most);
+    p.ahead = sizeof(T) == 2 && (long long)p.n_tokens * (p.Hq + p.Hkv) * D * 4 > kAheadBytes;
     const dim3 grid((unsigned)blocks), block(kWarps * 32);
-    switch (D) {
-    case 64: return launch_pdl(qk_norm_rope_kernel<T, 64>, grid, block, 0, stream, p);
-    case 128: return launch_pdl(qk_norm_rope_kernel<T, 128>, grid, block, 0, stream, p);
-    default: return launch_pdl(qk_norm_rope_kernel<T, 256>, grid, block, 0, stream, p);
-    }
+    auto kernel = D == 64    ? by_tokens ? qk_norm_rope_kernel<T, 64, true> : qk_norm_rope_kernel<T, 64, false>
+                  : D == 128 ? by_tokens ? qk_norm_rope_kernel<T, 128, true> : qk_norm_rope_kernel<T, 128, false>
+                             : qk_norm_rope_kernel<T, 256, false>;
+    return launch_pdl(kernel, grid, block, 0, stream, p);
 }
 
 }  // namespace

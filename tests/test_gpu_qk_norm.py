@@ -155,3 +155,26 @@ def test_many_tokens(kvc):
     for at in (slice(0, 9), slice(34990, 35011), slice(T - 9, T)):
         check(a[at], q[at], w, 1e-6, cs, pos[at])
         check(b[at], k[at], w, 1e-6, cs, pos[at])
+
+
+@pytest.mark.parametrize("dt,T,Hq,Hkv,D,rot", [
+    (torch.bfloat16, 15001, 8, 1, 64, 64), (torch.bfloat16, 20003, 3, 1, 128, 64), (torch.bfloat16, 8001, 32, 8, 128, 128),
+    (torch.float32, 15005, 4, 1, 64, 16), (torch.float32, 3649, 5, 3, 128, 0), (torch.bfloat16, 3649, 4, 4, 256, 256),
+    (torch.bfloat16, 14591, 1, 1, 64, 64)])
+def test_every_row_of_long_prompts(kvc, dt, T, Hq, Hkv, D, rot):
+    """More tokens than warps: whole rounds of them, then the rest; few heads, whose tokens lie side by side."""
+    q, k = rows(40, dt, T, Hq, D), rows(41, dt, T, Hkv, D)
+    wq, wk = rows(42, dt, D), rows(43, dt, D)
+    cs = kvc.kvc_rope_table(500, rot).to(DEV) if rot else None
+    pos = torch.randint(0, 500, (T,), device=DEV, dtype=torch.int32) if rot else None
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    if rot:
+        bad[[0, 5, T // 2, T - 1]] = True
+        pos[bad] = 500
+    a, b = torch.full_like(q, 7), torch.full_like(k, 7)
+    kvc.kvc_qk_norm_rope(q, k, w_q=wq, w_k=wk, cos_sin=cs, pos=pos, q_out=a, k_out=b)
+    assert kvc.kvc_device_status() == (4 if rot else 0)
+    assert bool((a[bad] == 7).all()) and bool((b[bad] == 7).all())
+    ok = ~bad
+    check(a[ok], q[ok], wq, 1e-6, cs, pos[ok] if rot else None)
+    check(b[ok], k[ok], wk, 1e-6, cs, pos[ok] if rot else None)
