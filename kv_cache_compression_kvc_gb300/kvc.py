@@ -1076,6 +1076,14 @@ def _rows_of(t: torch.Tensor, what: str, dtype, n: int, d: int, index: int):
     return t.data_ptr(), stride[0], stride[1]
 
 
+def _new_rows(like: torch.Tensor, stream) -> torch.Tensor:
+    """A contiguous tensor for the results of these rows."""
+    if stream is None and like.is_contiguous():
+        return torch.empty_like(like)
+    with _on(stream):
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+
+
 def kvc_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, *, w_q: Optional[torch.Tensor] = None,
                      w_k: Optional[torch.Tensor] = None, eps: float = 1e-6,
                      cos_sin: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
@@ -1090,11 +1098,11 @@ def kvc_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, *, w_q: Optional[torch.Te
         raise ValueError(f"q must be [T, n_heads_q, d_head], got {list(shape)}")
     _on_current(index, None, "q")
     T, Hq, D = shape
-    r = kvc_qk_rows()
-    r.q, r.q_stride_token, r.q_stride_head = _rows_of(q, "q", dt, T, D, index)
-    r.k, r.k_stride_token, r.k_stride_head = _rows_of(k, "k", dt, T, D, index)
+    qp, q_st, q_sh = _rows_of(q, "q", dt, T, D, index)
+    kp, k_st, k_sh = _rows_of(k, "k", dt, T, D, index)
+    Hkv = k.shape[1]
     wq = wk = table = at = None
-    n_pos = 0
+    n_pos = d_rot = 0
     if w_q is not None:
         _need(w_q, "w_q", dt, (D,), index)
         wq = w_q.data_ptr()
@@ -1107,22 +1115,22 @@ def kvc_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, *, w_q: Optional[torch.Te
         n_pos, _, half = cos_sin.shape
         _need(cos_sin, "cos_sin", torch.float32, (n_pos, 2, half), index)
         _need(pos, "pos", torch.int32, (T,), index)
-        table, at = cos_sin.data_ptr(), pos.data_ptr()
-        r.d_rot = 2 * half
+        table, at, d_rot = cos_sin.data_ptr(), pos.data_ptr(), 2 * half
     elif pos is not None:
         raise ValueError("positions need a table (cos_sin)")
-    Hkv = k.shape[1]
-    if q_out is None or k_out is None:
-        with _on(stream):
-            if q_out is None:
-                q_out = torch.empty(shape, dtype=dt, device=q.device)
-            if k_out is None:
-                k_out = torch.empty((T, Hkv, D), dtype=dt, device=q.device)
-    r.q_out, r.q_out_stride_token, r.q_out_stride_head = _rows_of(q_out, "q_out", dt, T, D, index)
-    r.k_out, r.k_out_stride_token, r.k_out_stride_head = _rows_of(k_out, "k_out", dt, T, D, index)
+    if q_out is None:
+        q_out = _new_rows(q, stream)
+        qo, qo_st, qo_sh = q_out.data_ptr(), Hq * D, D
+    else:
+        qo, qo_st, qo_sh = _rows_of(q_out, "q_out", dt, T, D, index)
+    if k_out is None:
+        k_out = _new_rows(k, stream)
+        ko, ko_st, ko_sh = k_out.data_ptr(), Hkv * D, D
+    else:
+        ko, ko_st, ko_sh = _rows_of(k_out, "k_out", dt, T, D, index)
     if q_out.shape[1] != Hq or k_out.shape[1] != Hkv:
         raise ValueError(f"outputs {list(q_out.shape)}, {list(k_out.shape)} for rows {list(shape)}, {list(k.shape)}")
-    r.dtype, r.n_tokens, r.n_heads_q, r.n_heads_kv, r.d_head = code, T, Hq, Hkv, D
+    r = kvc_qk_rows(qp, kp, qo, ko, code, T, Hq, Hkv, D, d_rot, q_st, q_sh, k_st, k_sh, qo_st, qo_sh, ko_st, ko_sh)
     status = (_lib or load()).kvc_qk_norm_rope(r, wq, wk, eps, table, at, n_pos, _raw_stream(index, stream))
     if status:
         _check(status)
@@ -1293,7 +1301,8 @@ def kvc_pages_compact(pool, pt: kvc_page_table, free_pool: kvc_free_pool, *,
     wp, wb = _space(ws, index)
     if remap is None:
         with _on(stream):
-            remap = torch.empty(pages.n_blocks, dtype=torch.int32, device=pool._keep[0].device)
+            remap = torch.empty_like(shares) if shares is not None else \
+                torch.empty(pages.n_blocks, dtype=torch.int32, device=pool._keep[0].device)
     else:
         _need(remap, "remap", torch.int32, (pages.n_blocks,), index)
     status = (_lib or load()).kvc_pages_compact(
