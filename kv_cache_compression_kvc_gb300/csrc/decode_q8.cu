@@ -53,7 +53,10 @@ constexpr int kEnd = 2;                      // steps that the end of a row tile
                                              // fp32 batch of the table, 1: 33.5, 2 and 4: 32.7)
 // Warps of a block: what registers allow (one block an SM with 16 heads or fp32 queries, two otherwise).  fp32
 // queries over 2 x 32768 slots of 8 heads of 128: 8 warps 34.5 us, 10 34.3, 12 31.5.
-constexpr int warps_of(int D, int NT, bool split) { return D <= 128 && (NT == 2 || split) ? 12 : 8; }
+constexpr int warps_of(int D, int NT, bool split)
+{
+    return D > 128 || (NT == 2 && split) || (NT == 1 && !split) ? 8 : 12;
+}
 constexpr int kMergeThreads = 256;
 constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block
 constexpr int kWholeWait = 20;               // and longer ones where the fullest block has so many above the mean
@@ -921,8 +924,15 @@ cudaError_t launch_typed(DecodeQ8Params p, cudaStream_t stream)
 
 }  // namespace
 
-// Row tiles of 8 heads, of 16 where a group has more and registers allow it.
-static int tiles_of_8(int G, int D, bool bf16) { return G > 8 && D <= 128 && bf16 ? 2 : 1; }
+// Row tiles of 8 heads, of 16 where a group has more and that pays.  fp32 queries of 128 dims, tiles of 8 and of 16:
+// 28 x 3963 to 6241 slots of 3 heads, groups of 12 47.0 and 41.1 us, 2 x 32768 of 8 heads, groups of 9 51.6 and 44.4, but
+// groups of 24, which are three tiles or two, 36.8 and 37.8.  No gain with 64 dims (groups of 16 31.0 and 30.9 to 35.8),
+// nor with bf16 queries of 256 (groups of 12 59.0 and 61.1).
+static int tiles_of_8(int G, int D, bool bf16)
+{
+    if (bf16) return G > 8 && D <= 128 ? 2 : 1;
+    return D == 128 && (G - 1) % 16 >= 8 ? 2 : 1;
+}
 
 DecodeQ8Plan decode_q8_plan(int B, int Hkv, int G, int D, bool bf16, int n_sm)
 {
@@ -958,8 +968,8 @@ cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t st
     const long long fullest = (tiles + p.blocks - 1) / p.blocks * steps;
     p.whole = steps <= kWholeSteps || (fullest * step * D <= 128 * 16 * 128 &&
                                        (fullest - tiles * steps / p.blocks) * step * D <= kWholeWait * 16 * 128);
+    const bool wide = tiles_of_8(p.G, D, bf16) == 2;
     if (bf16) {
-        const bool wide = tiles_of_8(p.G, D, true) == 2;
         switch (D) {
         case 64: return wide ? launch_typed<64, 2, false>(p, stream) : launch_typed<64, 1, false>(p, stream);
         case 128: return wide ? launch_typed<128, 2, false>(p, stream) : launch_typed<128, 1, false>(p, stream);
@@ -968,7 +978,7 @@ cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t st
     }
     switch (D) {
     case 64: return launch_typed<64, 1, true>(p, stream);
-    case 128: return launch_typed<128, 1, true>(p, stream);
+    case 128: return wide ? launch_typed<128, 2, true>(p, stream) : launch_typed<128, 1, true>(p, stream);
     default: return launch_typed<256, 1, true>(p, stream);
     }
 }

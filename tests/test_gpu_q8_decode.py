@@ -133,6 +133,16 @@ def test_ragged_batches(kvc, D, Hq, H):
     c.check()
 
 
+@pytest.mark.parametrize("lens,Hq,H,bs", [
+    ([4000, 0, 17, 1, 2222, 640, 0, 3], 9, 1, 16), ([1500, 3, 700], 32, 2, 32), ([9001], 31, 1, 64),
+    ([(53 * b) % 401 for b in range(90)], 48, 4, 16)])
+def test_groups_of_nine_to_sixteen_in_fp32(kvc, lens, Hq, H, bs):
+    """Row tiles of 16 heads, whose queries and weights are two terms each."""
+    c = Case(kvc, lens, Hq, H, 128, bs, torch.float32, seed=9)
+    c.call()
+    c.check(which=list(range(0, len(lens), 1 + len(lens) // 30)))
+
+
 def test_more_row_tiles_than_ranges(kvc):
     """Thousands of rows: split ones are noted by the range they begin in."""
     lens = [(37 * b) % 301 for b in range(700)]
