@@ -29,7 +29,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kRowWarps = 4;
-constexpr int kRowBlocks = 5;                // per SM
+// Blocks per SM, as registers allow (the smallest pages: 6 58.7 us, 7 55.5, 8 54.8; twice their size: 6 50.0, 8 51.6).
+template <typename T>
+constexpr int blocks_of(int NV) { return NV * (int)sizeof(T) > 16 ? 5 : NV * (int)sizeof(T) > 8 ? 6 : 8; }
 constexpr int kCl = 8;                       // blocks of the cluster that takes a small decode step
 // (page, head, K or V) of it, at most.  64: 8.3 us by the cluster and 10.1 by two kernels, 256: 9.1 and 10.4, 1024:
 // 12.4 and 10.8, but a call from Python, which the host bounds, 16.7 and 19; 2048: 17.2 and 11.4.
@@ -430,7 +432,7 @@ __device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long 
 }
 
 template <typename T, int D, int NV>
-__global__ void __launch_bounds__(kRowWarps * 32, kRowBlocks) append_q8_rows_kernel(const AppendQ8Params p)
+__global__ void __launch_bounds__(kRowWarps * 32, blocks_of<T>(NV)) append_q8_rows_kernel(const AppendQ8Params p)
 {
     pdl_trigger();
     pdl_wait();
@@ -459,12 +461,19 @@ cudaError_t append_typed(const AppendQ8Params &p, int n_sm, cudaStream_t stream)
         return launch_pdl(append_q8_step_kernel<T, D>, dim3(kCl), dim3(kPlanThreads), 0, stream, p);
     const cudaError_t e = launch_pdl(append_q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (e != cudaSuccess) return e;
-    const long long blocks = (tasks + kRowWarps - 1) / kRowWarps, most = (long long)n_sm * kRowBlocks;
-    const dim3 grid((unsigned)std::max(1LL, std::min(blocks, most))), block(kRowWarps * 32);
-    // a page of 32 rows of 128 elements is 16 vectors a lane, which is what registers hold in bf16
-    constexpr int NV = sizeof(T) == 2 ? 16 : 8;
-    if (p.cu == nullptr) return launch_pdl(append_q8_rows_kernel<T, D, 1>, grid, block, 0, stream, p);
-    return launch_pdl(append_q8_rows_kernel<T, D, NV>, grid, block, 0, stream, p);
+    auto rows = [&](auto kernel, int NV) {
+        const long long blocks = (tasks + kRowWarps - 1) / kRowWarps, most = (long long)n_sm * blocks_of<T>(NV);
+        return launch_pdl(kernel, dim3((unsigned)std::max(1LL, std::min(blocks, most))), dim3(kRowWarps * 32), 0, stream, p);
+    };
+    if (p.cu == nullptr) return rows(append_q8_rows_kernel<T, D, 1>, 1);
+    // A page of 32 rows of 128 elements is 16 vectors a lane, which is what registers hold in bf16.  Smaller pages leave
+    // more warps room: 40 x 1000 rows of 8 heads of 128 in pages of 16, 79.7 us with 16 vectors and 50.7 with 8; of
+    // 16 heads of 64, 126.6 with 16, 71 with 8 and 54.8 with 4; fp32, 8 heads of 64, 51.1 with 8 and 43.6 with 4.
+    constexpr int NV = 32 / (int)sizeof(T);
+    if constexpr (NV == 16)
+        if (p.bs * D <= 32 * 8 * NV / 4) return rows(append_q8_rows_kernel<T, D, NV / 4>, NV / 4);
+    if (p.bs * D <= 32 * 8 * NV / 2) return rows(append_q8_rows_kernel<T, D, NV / 2>, NV / 2);
+    return rows(append_q8_rows_kernel<T, D, NV>, NV);
 }
 template <typename T>
 cudaError_t append_dims(const AppendQ8Params &p, int n_sm, cudaStream_t stream)

@@ -90,6 +90,20 @@ def test_rows_of_ragged_sequences(kvc, dt, H, D, bs, lens, counts):
     assert appended.tolist() == counts and kvc.kvc_device_status() == 0
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,D,bs", [(3, 64, 16), (2, 64, 32), (2, 64, 64), (2, 128, 16), (1, 128, 48), (2, 256, 16)])
+def test_prompts_in_pages_of_every_size(kvc, dt, H, D, bs):
+    """A lane holds 4, 8 or 16 vectors of a page, or takes it in parts; pages begun before, and infinities."""
+    lens, counts = [3, 0, bs, 2 * bs - 1], [5 * bs + 7, 1, 3 * bs, 90]
+    c = Cache(kvc, lens, H, D, bs)
+    n = sum(counts)
+    k, v = rows(50, dt, n, H, D) * 3, rows(51, dt, n, H, D)
+    k[2, 0, 5], v[counts[0], H - 1, D - 1] = float("-inf"), float("inf")
+    c.append(counts, k, v)
+    c.check()
+    assert kvc.kvc_device_status() == 0
+
+
 def test_single_tokens_without_offsets(kvc):
     """Rows that raise a page's scale bring the ones there to it; many steps over page borders."""
     c = Cache(kvc, [0, 7, 16, 30], 2, 128, 16)
