@@ -11,11 +11,12 @@
 //
 // append_plan, by one block: checks every sequence, numbers the pages they need in sequence order
 // (block-wide scans) and takes them from the top of the free stack, so that ids do not depend on
-// timing; it writes one job per page that gets rows.  Then a warp per (job, head, K or V): the rows
-// stay in registers between the maximum and the rounding.  Small steps do both in one cluster.
+// timing; it writes one job per page that gets rows.  Then persistent warps, as many for a (job, head, K or
+// V) as hold its rows in registers between the maximum and the rounding.  Small steps do both in one cluster.
 // Bound by HBM for prompts (2 or 4 bytes in, 1 out an element): 16 prompts of 2048 to 4096 tokens, 32 heads of
-// 128, bf16, 201 us (6.0 TB/s), of which the plan is 8; with a warp per task instead of persistent ones
-// 228 us, with 16 warps an SM instead of 20 204.  Bound by latency for single tokens: 16 x 32 heads 12 us.
+// 128, bf16, 194 us (6.2 TB/s), of which the plan is 8.  Rows fetched into L2 while the plan is made, or one task
+// ahead: 1 us at most.  Bound by latency for single tokens: 16 x 32 heads 12 us, of which ids and pages that the
+// plan would read before it knows them save nothing.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -29,9 +30,14 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kRowWarps = 4;
-// Blocks per SM, as registers allow (the smallest pages: 6 58.7 us, 7 55.5, 8 54.8; twice their size: 6 50.0, 8 51.6).
+// Warps of a block whose TEAM warps share a page, and blocks per SM, as registers allow.  In blocks of 4 warps: the
+// smallest pages 6 58.7 us, 7 55.5, 8 54.8; the prompts above 6 194, 7 197.
+constexpr int warps_of(int team) { return team > 1 ? team : kRowWarps; }
 template <typename T>
-constexpr int blocks_of(int NV) { return NV * (int)sizeof(T) > 16 ? 5 : NV * (int)sizeof(T) > 8 ? 6 : 8; }
+constexpr int blocks_of(int NV, int team)
+{
+    return (NV * (int)sizeof(T) > 16 ? 5 : NV * (int)sizeof(T) > 8 ? 6 : 8) * kRowWarps / warps_of(team);
+}
 constexpr int kCl = 8;                       // blocks of the cluster that takes a small decode step
 // (page, head, K or V) of it, at most.  64: 8.3 us by the cluster and 10.1 by two kernels, 256: 9.1 and 10.4, 1024:
 // 12.4 and 10.8, but a call from Python, which the host bounds, 16.7 and 19; 2048: 17.2 and 11.4.
@@ -312,13 +318,30 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
     return lo | hi << 16;
 }
 
-// One task: a page's new rows of a head, keys or values, by a warp.  NV: vectors of 8 elements that a lane
-// holds at once.
-template <typename T, int D, int NV>
-__device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, int rest)
+// The largest x of a warp, or of the TEAM warps of a block; s_max: two sets of TEAM words, used in turn, so that
+// one barrier a call is enough.
+template <int TEAM>
+__device__ __forceinline__ float team_max(float x, float *s_max, int &turn)
+{
+    x = warp_max(x);
+    if (TEAM == 1) return x;
+    float *s = s_max + turn * TEAM;
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < TEAM; ++w) x = fmaxf(x, s[w]);
+    return x;
+}
+
+// One task: a page's new rows of a head, keys or values, by a warp or by the TEAM warps of a block.  NV:
+// vectors of 8 elements that a lane holds at once.
+template <typename T, int D, int NV, int TEAM>
+__device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, int rest, float *s_max, int &turn)
 {
     constexpr int VPR = D / 8;               // vectors per row
-    const int lane = threadIdx.x & 31;
+    constexpr int LANES = 32 * TEAM;
+    const int lane = TEAM == 1 ? threadIdx.x & 31 : threadIdx.x;
     const int h = rest >> 1, held = j.y, n_vec = j.w * VPR;
     const bool is_v = rest & 1;
     const int64_t st = p.new_st;
@@ -330,32 +353,32 @@ __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, 
 
     Row8<T> x[NV];
     auto fetch = [&](int v0) {
-        if (n_vec - v0 >= 32 * NV) {
+        if (n_vec - v0 >= LANES * NV) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int v = v0 + i * 32 + lane;
+                const int v = v0 + i * LANES + lane;
                 x[i].load(src + v / VPR * st + v % VPR * 8);
             }
             return;
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int v = v0 + i * 32 + lane;
+            const int v = v0 + i * LANES + lane;
             if (v < n_vec) x[i].load(src + v / VPR * st + v % VPR * 8);
             else x[i].zero();
         }
     };
     typename Row8<T>::Max big = Row8<T>::none();
-    for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
+    for (int v0 = 0; v0 < n_vec; v0 += LANES * NV) {
         fetch(v0);
 #pragma unroll
         for (int i = 0; i < NV; ++i) x[i].widen(big);
     }
-    float amax = warp_max(Row8<T>::size(big));
+    float amax = team_max<TEAM>(Row8<T>::size(big), s_max, turn);
     const bool inf = amax == INFINITY;       // then the largest finite one counts
     if (inf) {
         amax = 0.f;
-        for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
+        for (int v0 = 0; v0 < n_vec; v0 += LANES * NV) {
             fetch(v0);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -366,14 +389,14 @@ __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, 
                     if (fabsf(f[k]) < INFINITY) amax = fmaxf(amax, fabsf(f[k]));
             }
         }
-        amax = warp_max(amax);
+        amax = team_max<TEAM>(amax, s_max, turn);
     }
     const float s = fmaxf(s_old, scale_for(amax));
-    __syncwarp();                            // every lane has read the scale
+    if (TEAM == 1) __syncwarp();             // every lane has read the scale
     if (lane == 0 && (held == 0 || s != s_old)) *scale = s;
     if (held > 0 && s != s_old) {            // the rows held before go over to the new scale
         const float ratio = s_old / s;
-        for (int i = lane; i < held * (D / 16); i += 32) {
+        for (int i = lane; i < held * (D / 16); i += LANES) {
             uint4 w = *reinterpret_cast<uint4 *>(dst + i * 16);
             uint32_t *q = &w.x;
 #pragma unroll
@@ -389,8 +412,8 @@ __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, 
     }
     const float inv = 1.f / s;
     const bool power = (__float_as_uint(s) & 0x7fffffu) == 0u;   // then x * inv is x / s
-    for (int v0 = 0; v0 < n_vec; v0 += 32 * NV) {
-        if (n_vec > 32 * NV || inf) fetch(v0);
+    for (int v0 = 0; v0 < n_vec; v0 += LANES * NV) {
+        if (n_vec > LANES * NV || inf) fetch(v0);
         uint8_t *to = dst + (size_t)held * D + (size_t)(v0 + lane) * 8;
         const int in = n_vec - v0 - lane;
 #pragma unroll
@@ -404,17 +427,18 @@ __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, 
 #pragma unroll
                 for (int k = 0; k < 8; ++k) f[k] = fabsf(f[k]) == INFINITY ? __uint_as_float(0x7fc00000u) : f[k] / s;
             }
-            if (i * 32 < in)
-                *reinterpret_cast<uint2 *>(to + i * 256) =
+            if (i * LANES < in)
+                *reinterpret_cast<uint2 *>(to + i * LANES * 8) =
                     make_uint2(pack4(f[0], f[1], f[2], f[3]), pack4(f[4], f[5], f[6], f[7]));
         }
     }
 }
 
-// Tasks (job, head, K or V) w, w + n_w, ... of warp w; the next task's job is read ahead.
-template <typename T, int D, int NV>
-__device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long w, long long n_w)
+// Tasks (job, head, K or V) w, w + n_w, ... of warp or block w; the next task's job is read ahead.
+template <typename T, int D, int NV, int TEAM = 1>
+__device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long w, long long n_w, float *s_max = nullptr)
 {
+    int turn = 0;
     const unsigned per = 2u * (unsigned)p.H;
     const long long tasks = (long long)__ldcg(p.n_jobs) * per;
     if (w >= tasks) return;
@@ -425,18 +449,22 @@ __device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long 
         const unsigned job1 = (unsigned)((unsigned long long)(w + n_w) / per);
         int4 j1 = j;
         if (job1 != job && w + n_w < tasks) j1 = __ldcg(p.jobs + job1);
-        quantise<T, D, NV>(p, j, rest);
+        quantise<T, D, NV, TEAM>(p, j, rest, s_max, turn);
         job = job1;
         j = j1;
     }
 }
 
-template <typename T, int D, int NV>
-__global__ void __launch_bounds__(kRowWarps * 32, blocks_of<T>(NV)) append_q8_rows_kernel(const AppendQ8Params p)
+template <typename T, int D, int NV, int TEAM>
+__global__ void __launch_bounds__(warps_of(TEAM) * 32, blocks_of<T>(NV, TEAM)) append_q8_rows_kernel(const AppendQ8Params p)
 {
+    __shared__ float s_max[2 * TEAM];
     pdl_trigger();
     pdl_wait();
-    quantise_all<T, D, NV>(p, (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5), (long long)gridDim.x * kRowWarps);
+    if constexpr (TEAM > 1)
+        quantise_all<T, D, NV, TEAM>(p, blockIdx.x, gridDim.x, s_max);
+    else
+        quantise_all<T, D, NV>(p, (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5), (long long)gridDim.x * kRowWarps);
 }
 
 // Both steps in one cluster, for few rows.
@@ -461,19 +489,28 @@ cudaError_t append_typed(const AppendQ8Params &p, int n_sm, cudaStream_t stream)
         return launch_pdl(append_q8_step_kernel<T, D>, dim3(kCl), dim3(kPlanThreads), 0, stream, p);
     const cudaError_t e = launch_pdl(append_q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (e != cudaSuccess) return e;
-    auto rows = [&](auto kernel, int NV) {
-        const long long blocks = (tasks + kRowWarps - 1) / kRowWarps, most = (long long)n_sm * blocks_of<T>(NV);
-        return launch_pdl(kernel, dim3((unsigned)std::max(1LL, std::min(blocks, most))), dim3(kRowWarps * 32), 0, stream, p);
+    auto rows = [&](auto kernel, int NV, int team) {
+        const int at_once = team > 1 ? 1 : kRowWarps;          // tasks of a block
+        const long long blocks = (tasks + at_once - 1) / at_once, most = (long long)n_sm * blocks_of<T>(NV, team);
+        return launch_pdl(kernel, dim3((unsigned)std::max(1LL, std::min(blocks, most))), dim3(warps_of(team) * 32), 0,
+                          stream, p);
     };
-    if (p.cu == nullptr) return rows(append_q8_rows_kernel<T, D, 1>, 1);
-    // A page of 32 rows of 128 elements is 16 vectors a lane, which is what registers hold in bf16.  Smaller pages leave
-    // more warps room: 40 x 1000 rows of 8 heads of 128 in pages of 16, 79.7 us with 16 vectors and 50.7 with 8; of
-    // 16 heads of 64, 126.6 with 16, 71 with 8 and 54.8 with 4; fp32, 8 heads of 64, 51.1 with 8 and 43.6 with 4.
-    constexpr int NV = 32 / (int)sizeof(T);
-    if constexpr (NV == 16)
-        if (p.bs * D <= 32 * 8 * NV / 4) return rows(append_q8_rows_kernel<T, D, NV / 4>, NV / 4);
-    if (p.bs * D <= 32 * 8 * NV / 2) return rows(append_q8_rows_kernel<T, D, NV / 2>, NV / 2);
-    return rows(append_q8_rows_kernel<T, D, NV>, NV);
+    if (p.cu == nullptr) return rows(append_q8_rows_kernel<T, D, 1, 1>, 1, 1);
+    // A lane holds NV vectors, 64 bytes of rows in fp32 and 128 in bf16, which leaves 24 warps an SM, and as many warps share
+    // a page as that takes.  Measured (us), 16 prompts of 2048 to 4096 rows of 32 heads of 128, bf16, pages of 32:
+    // one warp with 2 NV 201, two with NV 194, four with NV / 2 211; 41 x 1000 to 2000 rows of 4 heads of 256 in pages
+    // of 32: one warp in two passes 110, four with 2 NV 114, four with NV 69, eight with NV / 2 78; 20 x the same in
+    // pages of 64: one warp 61, four with 2 NV 42, eight with NV 39; 40 x 1000 rows of 8 heads of 128 in pages of
+    // 16: one warp with 2 NV 80, with NV 50; of 16 heads of 64: one warp with 2 NV 127, NV 71, NV / 2 55.
+    constexpr int NV = 16 / (int)sizeof(T);
+    const int page = p.bs * D / 256;         // vectors a lane of one warp
+    if constexpr (NV == 8)                   // (the smallest fp32 page takes more)
+        if (page <= NV / 2) return rows(append_q8_rows_kernel<T, D, NV / 2, 1>, NV / 2, 1);
+    if (page <= NV) return rows(append_q8_rows_kernel<T, D, NV, 1>, NV, 1);
+    if (page <= NV * 2) return rows(append_q8_rows_kernel<T, D, NV, 2>, NV, 2);
+    if (page <= NV * 4) return rows(append_q8_rows_kernel<T, D, NV, 4>, NV, 4);
+    if (page <= NV * 8) return rows(append_q8_rows_kernel<T, D, NV, 8>, NV, 8);
+    return rows(append_q8_rows_kernel<T, D, 2 * NV, 8>, 2 * NV, 8);
 }
 template <typename T>
 cudaError_t append_dims(const AppendQ8Params &p, int n_sm, cudaStream_t stream)

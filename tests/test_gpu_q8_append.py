@@ -91,9 +91,10 @@ def test_rows_of_ragged_sequences(kvc, dt, H, D, bs, lens, counts):
 
 
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("H,D,bs", [(3, 64, 16), (2, 64, 32), (2, 64, 64), (2, 128, 16), (1, 128, 48), (2, 256, 16)])
+@pytest.mark.parametrize("H,D,bs", [(3, 64, 16), (2, 64, 32), (2, 64, 64), (2, 128, 16), (1, 128, 48), (2, 256, 16),
+                                    (1, 256, 32), (1, 256, 128)])
 def test_prompts_in_pages_of_every_size(kvc, dt, H, D, bs):
-    """A lane holds 4, 8 or 16 vectors of a page, or takes it in parts; pages begun before, and infinities."""
+    """One to eight warps hold a page, or take it in parts; pages begun before, and infinities."""
     lens, counts = [3, 0, bs, 2 * bs - 1], [5 * bs + 7, 1, 3 * bs, 90]
     c = Cache(kvc, lens, H, D, bs)
     n = sum(counts)
