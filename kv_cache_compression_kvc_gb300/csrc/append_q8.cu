@@ -14,8 +14,8 @@
 // timing; it writes one job per page that gets rows.  Then persistent warps, as many for a (job, head, K or
 // V) as hold its rows in registers between the maximum and the rounding.  Small steps do both in one cluster.
 // Bound by HBM for prompts (2 or 4 bytes in, 1 out an element): 16 prompts of 2048 to 4096 tokens, 32 heads of
-// 128, bf16, 194 us (6.2 TB/s), of which the plan is 8.  Rows fetched into L2 while the plan is made, or one task
-// ahead: 1 us at most.  Bound by latency for single tokens: 16 x 32 heads 12 us, of which ids and pages that the
+// 128, bf16, 192 us (6.3 TB/s), of which the plan is 7.  Rows fetched into L2 while the plan is made, or one task
+// ahead: 1 us at most.  Bound by latency for single tokens: 16 x 32 heads 11 us, of which ids and pages that the
 // plan would read before it knows them save nothing.
 #include <algorithm>
 
@@ -64,19 +64,18 @@ __device__ __forceinline__ int2 block_scan(int2 x, int *s_warp, int2 *all)
         s_warp[32 + warp] = x.y;
     }
     __syncthreads();
-    int2 before = make_int2(0, 0), total = make_int2(0, 0);
-#pragma unroll 4
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        const int a = s_warp[w], b = s_warp[32 + w];
-        if (w < warp) {
-            before.x += a;
-            before.y += b;
+    const int2 own = make_int2(s_warp[lane], s_warp[32 + lane]);
+    int2 w = own;                            // (kPlanThreads / 32 warps are a warp's lanes)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, w.x, o), b = __shfl_up_sync(0xffffffffu, w.y, o);
+        if (lane >= o) {
+            w.x += a;
+            w.y += b;
         }
-        total.x += a;
-        total.y += b;
     }
-    *all = total;
-    return make_int2(x.x + before.x, x.y + before.y);
+    *all = make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
+    return make_int2(x.x + __shfl_sync(0xffffffffu, w.x - own.x, warp), x.y + __shfl_sync(0xffffffffu, w.y - own.y, warp));
 }
 
 // The first of n ascending numbers above x.
@@ -210,7 +209,7 @@ __device__ __forceinline__ void append_plan(const AppendQ8Params &p)
         __syncthreads();
         // a job for every page that gets rows, and a table entry for the popped ones
         for (int e = tid; e < all.y; e += kPlanThreads) {
-            const int i = find_above(s_jobs, kPlanThreads, e);
+            const int i = find_above(s_jobs, min(kPlanThreads, p.B - b0), e);
             const int j = e - (i > 0 ? s_jobs[i - 1] : 0);
             const int l = s_len[i], lb = l / p.bs + j, held = j == 0 ? l % p.bs : 0;
             const int at = lb * p.bs + held;                   // the first new row's slot
