@@ -15,8 +15,8 @@
 // V) as hold its rows in registers between the maximum and the rounding.  Small steps do both in one cluster.
 // Bound by HBM for prompts (2 or 4 bytes in, 1 out an element): 16 prompts of 2048 to 4096 tokens, 32 heads of
 // 128, bf16, 192 us (6.3 TB/s), of which the plan is 7.  Rows fetched into L2 while the plan is made, or one task
-// ahead: 1 us at most.  Bound by latency for single tokens: 16 x 32 heads 11 us, of which ids and pages that the
-// plan would read before it knows them save nothing.
+// ahead: 1 us at most.  Bound by latency for single tokens, a group of lanes a row: 16 x 32 heads 8.8 us (a warp a
+// row: 11.2); ids and pages that the plan would read before it knows them save nothing.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -39,8 +39,8 @@ constexpr int blocks_of(int NV, int team)
     return (NV * (int)sizeof(T) > 16 ? 5 : NV * (int)sizeof(T) > 8 ? 6 : 8) * kRowWarps / warps_of(team);
 }
 constexpr int kCl = 8;                       // blocks of the cluster that takes a small decode step
-// (page, head, K or V) of it, at most.  64: 8.3 us by the cluster and 10.1 by two kernels, 256: 9.1 and 10.4, 1024:
-// 12.4 and 10.8, but a call from Python, which the host bounds, 16.7 and 19; 2048: 17.2 and 11.4.
+// (page, head, K or V) of it, at most.  256: 7.6 us by the cluster and 7.7 by two kernels, 1024: 8.8 and 8.5, but a
+// call from Python, which the host bounds, 16.4 and 19; 2048: 11.4 and 9.4; 4096: 15.9 and 12.2.
 constexpr int kStepTasks = 1024;
 constexpr int kDevBadLen_ = 5;               // KVC_DEV_BAD_LENGTH
 constexpr int kDevBadBlk_ = 9;               // KVC_DEV_BAD_BLOCK
@@ -317,30 +317,36 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d)
     return lo | hi << 16;
 }
 
-// The largest x of a warp, or of the TEAM warps of a block; s_max: two sets of TEAM words, used in turn, so that
-// one barrier a call is enough.
-template <int TEAM>
+// The lanes of this thread's group of LANES in its warp.
+template <int LANES>
+__device__ __forceinline__ uint32_t group_mask()
+{
+    return LANES >= 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
+}
+// The largest x of LANES threads: some lanes of a warp, a warp, or a block.  s_max: two sets of words, one a warp, used
+// in turn, so that one barrier a call is enough.
+template <int LANES>
 __device__ __forceinline__ float team_max(float x, float *s_max, int &turn)
 {
-    x = warp_max(x);
-    if (TEAM == 1) return x;
-    float *s = s_max + turn * TEAM;
+#pragma unroll
+    for (int o = (LANES < 32 ? LANES : 32) / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(group_mask<LANES>(), x, o));
+    if (LANES <= 32) return x;
+    float *s = s_max + turn * (LANES / 32);
     turn ^= 1;
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < TEAM; ++w) x = fmaxf(x, s[w]);
+    for (int w = 0; w < LANES / 32; ++w) x = fmaxf(x, s[w]);
     return x;
 }
 
-// One task: a page's new rows of a head, keys or values, by a warp or by the TEAM warps of a block.  NV:
-// vectors of 8 elements that a lane holds at once.
-template <typename T, int D, int NV, int TEAM>
+// One task: a page's new rows of a head, keys or values, by LANES threads.  NV: vectors of 8 elements that a
+// lane holds at once.
+template <typename T, int D, int NV, int LANES>
 __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, int rest, float *s_max, int &turn)
 {
     constexpr int VPR = D / 8;               // vectors per row
-    constexpr int LANES = 32 * TEAM;
-    const int lane = TEAM == 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int lane = LANES <= 32 ? threadIdx.x & (LANES - 1) : threadIdx.x;
     const int h = rest >> 1, held = j.y, n_vec = j.w * VPR;
     const bool is_v = rest & 1;
     const int64_t st = p.new_st;
@@ -373,7 +379,7 @@ __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, 
 #pragma unroll
         for (int i = 0; i < NV; ++i) x[i].widen(big);
     }
-    float amax = team_max<TEAM>(Row8<T>::size(big), s_max, turn);
+    float amax = team_max<LANES>(Row8<T>::size(big), s_max, turn);
     const bool inf = amax == INFINITY;       // then the largest finite one counts
     if (inf) {
         amax = 0.f;
@@ -388,10 +394,10 @@ __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, 
                     if (fabsf(f[k]) < INFINITY) amax = fmaxf(amax, fabsf(f[k]));
             }
         }
-        amax = team_max<TEAM>(amax, s_max, turn);
+        amax = team_max<LANES>(amax, s_max, turn);
     }
     const float s = fmaxf(s_old, scale_for(amax));
-    if (TEAM == 1) __syncwarp();             // every lane has read the scale
+    if (LANES <= 32) __syncwarp(group_mask<LANES>());          // every lane has read the scale
     if (lane == 0 && (held == 0 || s != s_old)) *scale = s;
     if (held > 0 && s != s_old) {            // the rows held before go over to the new scale
         const float ratio = s_old / s;
@@ -433,8 +439,8 @@ __device__ __forceinline__ void quantise(const AppendQ8Params &p, const int4 j, 
     }
 }
 
-// Tasks (job, head, K or V) w, w + n_w, ... of warp or block w; the next task's job is read ahead.
-template <typename T, int D, int NV, int TEAM = 1>
+// Tasks (job, head, K or V) w, w + n_w, ... of team w; the next task's job is read ahead.
+template <typename T, int D, int NV, int LANES>
 __device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long w, long long n_w, float *s_max = nullptr)
 {
     int turn = 0;
@@ -448,7 +454,7 @@ __device__ __forceinline__ void quantise_all(const AppendQ8Params &p, long long 
         const unsigned job1 = (unsigned)((unsigned long long)(w + n_w) / per);
         int4 j1 = j;
         if (job1 != job && w + n_w < tasks) j1 = __ldcg(p.jobs + job1);
-        quantise<T, D, NV, TEAM>(p, j, rest, s_max, turn);
+        quantise<T, D, NV, LANES>(p, j, rest, s_max, turn);
         job = job1;
         j = j1;
     }
@@ -460,10 +466,13 @@ __global__ void __launch_bounds__(warps_of(TEAM) * 32, blocks_of<T>(NV, TEAM)) a
     __shared__ float s_max[2 * TEAM];
     pdl_trigger();
     pdl_wait();
-    if constexpr (TEAM > 1)
-        quantise_all<T, D, NV, TEAM>(p, blockIdx.x, gridDim.x, s_max);
-    else
-        quantise_all<T, D, NV>(p, (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5), (long long)gridDim.x * kRowWarps);
+    if constexpr (TEAM > 1) {
+        quantise_all<T, D, NV, 32 * TEAM>(p, blockIdx.x, gridDim.x, s_max);
+    } else {
+        // (a single row is less than a warp's lanes hold)
+        constexpr int LANES = NV == 1 ? D / 8 : 32, TEAMS = kRowWarps * 32 / LANES;
+        quantise_all<T, D, NV, LANES>(p, (long long)blockIdx.x * TEAMS + threadIdx.x / LANES, (long long)gridDim.x * TEAMS);
+    }
 }
 
 // Both steps in one cluster, for few rows.
@@ -476,8 +485,10 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kPlanThreads) appe
     __threadfence();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    // warps of a block take tasks of different jobs: a block's share is no smaller where jobs are few
-    quantise_all<T, D, 1>(p, (long long)(threadIdx.x >> 5) * kCl + blockIdx.x, kCl * (kPlanThreads / 32));
+    // a group of lanes a row; warps of a block take tasks of different jobs: its share is no smaller where jobs are few
+    constexpr int LANES = D / 8, PER = 32 / LANES;
+    quantise_all<T, D, 1, LANES>(p, ((threadIdx.x >> 5) * kCl + blockIdx.x) * PER + (threadIdx.x & 31) / LANES,
+                                 kCl * kPlanThreads / LANES);
 }
 
 template <typename T, int D>
@@ -489,7 +500,7 @@ cudaError_t append_typed(const AppendQ8Params &p, int n_sm, cudaStream_t stream)
     const cudaError_t e = launch_pdl(append_q8_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
     if (e != cudaSuccess) return e;
     auto rows = [&](auto kernel, int NV, int team) {
-        const int at_once = team > 1 ? 1 : kRowWarps;          // tasks of a block
+        const int at_once = team > 1 ? 1 : NV == 1 ? kRowWarps * 256 / D : kRowWarps;          // tasks of a block
         const long long blocks = (tasks + at_once - 1) / at_once, most = (long long)n_sm * blocks_of<T>(NV, team);
         return launch_pdl(kernel, dim3((unsigned)std::max(1LL, std::min(blocks, most))), dim3(warps_of(team) * 32), 0,
                           stream, p);

@@ -105,6 +105,22 @@ def test_prompts_in_pages_of_every_size(kvc, dt, H, D, bs):
     assert kvc.kvc_device_status() == 0
 
 
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,D", [(3, 64), (2, 128), (1, 256)])
+def test_steps_of_uneven_counts(kvc, dt, H, D):
+    """A few rows a sequence, groups of lanes side by side: some with raised scales, infinities, NaN or no rows."""
+    lens, counts = [3, 16, 31, 0, 7, 40], [1, 0, 9, 2, 5, 3]
+    c = Cache(kvc, lens, H, D, 16)
+    n = sum(counts)
+    for step in range(3):
+        k, v = rows(60 + step, dt, n, H, D), rows(70 + step, dt, n, H, D)
+        k[0], v[4, H - 1] = k[0] * 2.0 ** 12, v[4, H - 1] * 2.0 ** 20
+        k[2, 0, 5], k[13, H - 1, 1], v[19, 0, 0] = float("inf"), float("nan"), float("-inf")
+        c.append(counts, k, v)
+        c.check()
+    assert kvc.kvc_device_status() == 0
+
+
 def test_single_tokens_without_offsets(kvc):
     """Rows that raise a page's scale bring the ones there to it; many steps over page borders."""
     c = Cache(kvc, [0, 7, 16, 30], 2, 128, 16)
