@@ -791,10 +791,15 @@ kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_tab
  * length outside [0, max_blocks * block_size] records KVC_DEV_BAD_LENGTH and is clamped, a table
  * entry outside the pool KVC_DEV_BAD_BLOCK and reads page 0.  What a page holds behind the length is
  * never used, whatever it is.
- * fp32 accumulation and softmax statistics.  With bf16 queries the weights are rounded to fp16 once
- * (at most 2^-11 of each, eight times finer than the rounding of out); with fp32 queries, queries
- * and weights enter the products as two fp16 terms (2^-23 of each row's largest element).  Any
- * group size.  Results do not depend on timing.  One kernel or two.  Workspace:
+ * fp32 accumulation and softmax statistics.  fp32 queries enter the products as two fp16 terms (2^-22
+ * of each row's largest element).  Weights (a probability times the scale of its page) enter them as
+ * one fp16 number with bf16 queries, off by 2^-11 of it, eight times finer than the rounding of out,
+ * and as two with fp32 queries, off by 2^-22; beside that by 2^-23 of the largest weight of its own 16
+ * slots (32 with d_head 64), or by 2^-30 of one that is 2^8 times larger and lies among the 256 slots
+ * (512) before them.
+ * A thread's sums are fp32 and cut, not rounded: 2^-23 of the sum for each 16 slots in a row, a few in
+ * rows that many warps share, a thousand or two where every warp walks 16000 slots.  Logits may have any
+ * finite size.  Any group size.  Results do not depend on timing.  One kernel or two.  Workspace:
  * kvc_decode_attn_paged_q8_workspace_bytes(), 256-byte aligned; it need not be cleared, and calls
  * that share one must not overlap on the GPU. */
 size_t kvc_decode_attn_paged_q8_workspace_bytes(int32_t batch, int32_t n_heads_q,

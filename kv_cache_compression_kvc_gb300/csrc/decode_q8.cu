@@ -20,16 +20,18 @@
 //   Queries are brought to [2^14, 2^15) by a power of two per row: bf16 then is exact in fp16 down to
 //   2^-31 of the row's largest element.  fp32 queries become two fp16 terms (22 bits), and so do their
 //   weights; with bf16 queries, whose outputs are rounded to 8 bits, weights are rounded once to 11.
-//   Weights carry the value scale: w_j = 2^(x_j + log2 vs(j) - M) with a running maximum M of its
-//   own, so that pages whose values differ by any factor meet on equal terms; the softmax's sum l and its
-//   maximum m are kept beside it.  All sums are fp32.
+//   Weights carry the value scale: w_j = 2^(x_j - m + log2 vs(j) - ref), with the softmax's running maximum m, whose
+//   sum l is kept beside it, and a whole number ref of its own that follows the weights up and down: pages whose
+//   values differ by any factor meet on equal terms, and the light weights behind a heavy one, fp16 in the products,
+//   are held to as many bits as that one was.  Exponents are formed from the difference x_j - m, which is exact where it
+//   counts however large the logits are.  All sums are fp32.
 //
 // The range of a warp is found on the device (a scan of the lengths), even however ragged the batch
-// is.  A row tile that crosses warps leaves partial states (m, l, M, O): those of a block are joined in
+// is.  A row tile that crosses warps leaves partial states (m, l, ref, O): those of a block are joined in
 // shared memory at its end, those of several blocks by decode_q8_merge_kernel, both in order of
 // the slots, so results do not depend on timing.
 //
-// Measured: 2 x 131072 slots of 8 heads of 128, 4 query heads each (537 MB) 92.5 us, 5.8 TB/s.  Copies
+// Measured: 2 x 131072 slots of 8 heads of 128, 4 query heads each (537 MB) 94.5 us, 5.7 TB/s.  Copies
 // alone in this pattern take 78 us.  3 us pass until the first copies leave (lengths, page ids, cold
 // instructions), 3 us after the last (parts), and equal shares take some SMs 61 us and others 85: whole
 // groups of neighbours are slower.  More blocks than fit at once, so that the fast ones take more, 115 us;
@@ -61,8 +63,13 @@ constexpr int kMergeThreads = 256;
 constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block
 constexpr int kWholeWait = 20;               // and longer ones where the fullest block has so many above the mean
 constexpr int kMinUnits = 16;                // units that a block is worth at least
-constexpr float kSlack = 8.f;                // a maximum rises when it is passed by 2^8
-constexpr float kBoost = 6.f;                // weights are held times 2^6: at most 2^15, exact down to 2^-20
+constexpr float kSlack = 8.f;                // a maximum or reference moves when it is passed by 2^8 either way
+constexpr float kBoost = 6.f;                // weights are held times 2^6: at most 2^15, and the largest of a step
+                                             // that lies low but moves nothing, 2^-2, is 22 bits above the last place.
+                                             // (Slack 4 and boost 10: groups of 12 2 % slower)
+constexpr int kLook = 16;                    // a reference may go down every so many steps (8: groups of 12, fp32, 43.3 us,
+                                             // 16 42.8; a vote on it in every step 50.6)
+constexpr int kTop = 100;                    // and as far as the sums stay below 2^101
 constexpr float kNone = -3.402823466e38f;    // a maximum of nothing
 constexpr int kDevBadLen_ = 5;
 constexpr int kDevBadBlk_ = 9;
@@ -148,6 +155,22 @@ __device__ __forceinline__ uint2 lds_8(uint32_t a)
     uint2 r;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
     return r;
+}
+
+// 2^(ref - kBoost) as two factors, since it may pass the range where the outputs do not.  The second one is 1 for values
+// of ordinary size.
+__device__ __forceinline__ float ex2_near(float ref) { return ex2(fminf(fmaxf(ref - kBoost, -60.f), 60.f)); }
+__device__ __forceinline__ float ex2_far(float ref)
+{
+    return ex2(ref - kBoost - fminf(fmaxf(ref - kBoost, -60.f), 60.f));
+}
+
+// The largest x of a row's lanes.
+__device__ __forceinline__ float row_max(float x)
+{
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
 }
 
 // Slots of sequence b, clamped to the table, and its steps (one for an empty one, which has rows to write).
@@ -304,9 +327,10 @@ struct Walk {
 // 4 columns of an output row from its joined state.
 template <typename T>
 __device__ __forceinline__ void store_row(const DecodeQ8Params &p, size_t row, int D, int col, float m, float l,
-                                          float mv, float4 o)
+                                          float ref, float4 o)
 {
-    const float f = l == 0.f ? 0.f : ex2(mv - kBoost - m) / l;
+    const float f = l == 0.f ? 0.f : ex2_near(ref) / l, f2 = ex2_far(ref);
+    o.x *= f2; o.y *= f2; o.z *= f2; o.w *= f2;
     if (col == 0 && p.lse != nullptr) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     T *dst = static_cast<T *>(p.out) + row * D + col;
     if constexpr (sizeof(T) == 4) {
@@ -331,6 +355,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     constexpr int VB = D == 64 ? 8 : 16;     // bytes of a value row that a lane takes at once
     constexpr int VC = D == 256 ? 2 : 1;     // how often
     constexpr int S = PL::STAGES, W = PL::WARPS, SUB = PL::SUB, STEP = PL::STEP;
+    constexpr bool TWO = SPLIT;              // weights of two terms
     constexpr int SCALES = 2 * STEP * D;     // where a stage keeps its scales; 16 bytes on, what it holds
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -423,7 +448,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     uint32_t bq[NT][KS][2], bl[SPLIT ? NT : 1][SPLIT ? KS : 1][2];
     float fq[NT][2];                         // row 2t, 2t + 1: the query's power of two times scale
     float o[DT][NT][4];
-    float m[NT][2], mv[NT][2], l[NT][2];
+    float m[NT][2], ref[NT][2], l[NT][2];    // of the logits; of the weights, relative to m
     int cur_b = -1, cur_hr = -1, cur_len = 0, cur_n = 0, first_step = 0;
 
     auto begin = [&](int b, int hr) {
@@ -482,8 +507,8 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             fq[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4) * p.scale;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                m[nt][r] = mv[nt][r] = kNone;
-                l[nt][r] = 0.f;
+                m[nt][r] = kNone;
+                ref[nt][r] = l[nt][r] = 0.f;
             }
 #pragma unroll
             for (int d = 0; d < DT; ++d)
@@ -515,13 +540,14 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 const int row = nt * 8 + 2 * t + r;
                 if (r0 + row >= p.G) continue;
                 const size_t out_row = (size_t)b * p.Hq + h * p.G + r0 + row;
-                float f = 1.f;
+                float f = 1.f, f2 = 1.f;
                 if (whole) {
-                    f = sum == 0.f ? 0.f : ex2(mv[nt][r] - kBoost - m[nt][r]) / sum;
+                    f = sum == 0.f ? 0.f : ex2_near(ref[nt][r]) / sum;
+                    f2 = ex2_far(ref[nt][r]);
                     if (g == 0 && p.lse != nullptr)
                         p.lse[out_row] = sum == 0.f ? -INFINITY : (m[nt][r] + log2f(sum)) * kLn2;
                 } else if (g == 0) {
-                    reinterpret_cast<float4 *>(pm)[row] = make_float4(m[nt][r], sum, mv[nt][r], 0.f);
+                    reinterpret_cast<float4 *>(pm)[row] = make_float4(m[nt][r], sum, ref[nt][r], 0.f);
                 }
 #pragma unroll
                 for (int c = 0; c < VC; ++c) {
@@ -530,8 +556,8 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                     float y[VB];
 #pragma unroll
                     for (int i = 0; i < VB / 2; ++i) {
-                        y[2 * i] = o[c * 8 + i][nt][r] * f;
-                        y[2 * i + 1] = o[c * 8 + i][nt][2 + r] * f;
+                        y[2 * i] = o[c * 8 + i][nt][r] * f2 * f;
+                        y[2 * i + 1] = o[c * 8 + i][nt][2 + r] * f2 * f;
                     }
                     if (!whole || SPLIT) {
                         float *dst = whole ? static_cast<float *>(p.out) + out_row * D + d0 : po + row * D + d0;
@@ -648,7 +674,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
-                    rise |= fmaxf(xs[r], xs[2 + r]) > fminf(m[nt][r], mv[nt][r] - evf[sub]) + kSlack;
+                    rise |= fmaxf(xs[r], xs[2 + r]) - m[nt][r] > fminf(0.f, ref[nt][r] - evf[sub]) + kSlack;
             }
         }
         if (__any_sync(0xffffffffu, rise)) {
@@ -656,44 +682,83 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float m1 = m[nt][r], v1 = mv[nt][r];
+                    float y[SUB], xm = -INFINITY, want = -INFINITY;
 #pragma unroll
                     for (int sub = 0; sub < SUB; ++sub) {
-                        float y = fmaxf(x[sub][nt][r], x[sub][nt][2 + r]);
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                        m1 = fmaxf(m1, y);
-                        v1 = fmaxf(v1, y + evf[sub]);
+                        y[sub] = row_max(fmaxf(x[sub][nt][r], x[sub][nt][2 + r]));
+                        xm = fmaxf(xm, y[sub]);
                     }
-                    l[nt][r] *= ex2(m[nt][r] - m1);
-                    const float f = ex2(mv[nt][r] - v1);
+                    const float m1 = xm - m[nt][r] > kSlack ? xm : m[nt][r];
+#pragma unroll
+                    for (int sub = 0; sub < SUB; ++sub) want = fmaxf(want, y[sub] - m1 + evf[sub]);
+                    const float dm = m[nt][r] - m1, now = ref[nt][r] + dm;      // the reference from m1 on
+                    const float r1 = want > now + kSlack ? ceilf(want) : rintf(now);
+                    const float f = ex2(dm + (ref[nt][r] - r1));
+                    l[nt][r] *= ex2(dm);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
                         o[d][nt][r] *= f;
                         o[d][nt][2 + r] *= f;
                     }
                     m[nt][r] = m1;
-                    mv[nt][r] = v1;
+                    ref[nt][r] = r1;
                 }
+        }
+        if (step % kLook == kLook - 1) {     // do all slots of a row lie low?  4 bits of the vote for each t
+            float top[NT][2];
+            uint32_t low = ~(15u << (4 * t));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float y = -INFINITY;
+#pragma unroll
+                    for (int sub = 0; sub < SUB; ++sub)
+                        y = fmaxf(y, fmaxf(x[sub][nt][r], x[sub][nt][2 + r]) - m[nt][r] + evf[sub]);
+                    top[nt][r] = y;
+                    low |= y < ref[nt][r] - kSlack ? 1u << (4 * t + 2 * nt + r) : 0u;
+                }
+            if ((__reduce_and_sync(0xffffffffu, low) & 0xffffu) != 0u) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float want = row_max(top[nt][r]);
+                        float big = 0.f;
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) big = fmaxf(big, fmaxf(fabsf(o[d][nt][r]), fabsf(o[d][nt][2 + r])));
+                        // as far as the sums stay in their range, and not for -inf alone
+                        const int room = kTop + 127 - (int)(__float_as_uint(row_max(big)) >> 23);
+                        float r1 = ref[nt][r];
+                        if (want < r1 - kSlack && want > -INFINITY) r1 = ceilf(fmaxf(want, r1 - (float)max(0, min(126, room))));
+                        const float f = ex2(ref[nt][r] - r1);
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            o[d][nt][r] *= f;
+                            o[d][nt][2 + r] *= f;
+                        }
+                        ref[nt][r] = r1;
+                    }
+            }
         }
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
-            uint32_t pw[NT][2], pl[SPLIT ? NT : 1][2];
+            uint32_t pw[NT][2], pl[TWO ? NT : 1][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float y[4];
-                const float to[2] = {evf[sub] + kBoost - mv[nt][0], evf[sub] + kBoost - mv[nt][1]};
+                const float to[2] = {evf[sub] + kBoost - ref[nt][0], evf[sub] + kBoost - ref[nt][1]};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    l[nt][i & 1] += ex2(x[sub][nt][i] - m[nt][i & 1]);
-                    y[i] = ex2(x[sub][nt][i] + to[i & 1]) * fv[sub];
+                    const float u = x[sub][nt][i] - m[nt][i & 1];
+                    l[nt][i & 1] += ex2(u);
+                    y[i] = ex2(u + to[i & 1]) * fv[sub];
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t hi = pack_h2(y[2 * i], y[2 * i + 1]);
                     pw[nt][i] = transpose_8x8(hi);
-                    if constexpr (SPLIT) {
+                    if constexpr (TWO) {
                         const float2 z = unpack_h2(hi);
                         pl[nt][i] = transpose_8x8(pack_h2(y[2 * i] - z.x, y[2 * i + 1] - z.y));
                     }
@@ -729,7 +794,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_16816(o[vc * 8 + q * 2 + u][nt], a, pw[nt][0], pw[nt][1]);
-                            if constexpr (SPLIT) mma_16816(o[vc * 8 + q * 2 + u][nt], a, pl[nt][0], pl[nt][1]);
+                            if constexpr (TWO) mma_16816(o[vc * 8 + q * 2 + u][nt], a, pl[nt][0], pl[nt][1]);
                         }
                     }
             }
@@ -766,7 +831,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
             if (members >> lane & 1u)
                 y = lane & 1 ? reinterpret_cast<const float4 *>(ring_o + (lane >> 1) * RING + p.RP * D)[row]
                              : reinterpret_cast<const float4 *>(p.ws_wml)[ws_at + (lane >> 1) * p.RP + row];
-            float m1 = 0.f, v1 = 0.f, sum = 0.f, f = 0.f;
+            float m1 = 0.f, r1 = 0.f, sum = 0.f, f = 0.f;
 #pragma unroll
             for (int c = 0; c < (D + 127) / 128; ++c) {
                 const int col = c * 128 + lane * 4;
@@ -782,9 +847,10 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 }
                 if (c == 0) {                // (while those are on their way)
                     m1 = warp_max(y.x);
-                    v1 = warp_max(y.z);
-                    sum = warp_sum(y.y * ex2(y.x - m1));
-                    f = ex2(y.z - v1);
+                    const float dm = y.x - m1;
+                    r1 = ceilf(warp_max(y.z + dm));
+                    sum = warp_sum(y.y * ex2(dm));
+                    f = ex2(dm + (y.z - r1));
                 }
 #pragma unroll
                 for (int x = 0; x < 2 * W; ++x) {
@@ -797,9 +863,9 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 if (!in) continue;
                 // (of a row tile that began before this block the state is the block's first)
                 const size_t part = ((size_t)blockIdx.x * 2 + (lo == 0 ? 1 : 0)) * p.RP + row;
-                if (whole) store_row<T>(p, (size_t)b * p.Hq + h * p.G + r0 + row, D, col, m1, sum, v1, acc);
+                if (whole) store_row<T>(p, (size_t)b * p.Hq + h * p.G + r0 + row, D, col, m1, sum, r1, acc);
                 else *reinterpret_cast<float4 *>(p.ws_o + part * D + col) = acc;
-                if (!whole && col == 0) reinterpret_cast<float4 *>(p.ws_ml)[part] = make_float4(m1, sum, v1, 0.f);
+                if (!whole && col == 0) reinterpret_cast<float4 *>(p.ws_ml)[part] = make_float4(m1, sum, r1, 0.f);
             }
         }
         turn = row - rows;
@@ -833,7 +899,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_q8_merge_kernel(const De
     const int b = tile / p.HR, hr = tile - b * p.HR, h = hr / p.RT, r0 = (hr - h * p.RT) * p.RP;
     if (row >= min(p.RP, p.G - r0)) return;
     const float4 *ml = reinterpret_cast<const float4 *>(p.ws_ml);
-    float m = kNone, mv = kNone, l = 0.f;
+    float m = kNone, ref = 0.f, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 4;
     for (int i0 = set; i0 < nseg; i0 += SETS * U) {
@@ -849,49 +915,52 @@ __global__ void __launch_bounds__(kMergeThreads) decode_q8_merge_kernel(const De
                 z[u] = __ldcg(reinterpret_cast<const float4 *>(p.ws_o + part * D + col));
             }
         }
-        float m1 = m, v1 = mv;
+        float m1 = m;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            m1 = fmaxf(m1, y[u].x);
-            v1 = fmaxf(v1, y[u].z);
-        }
-        const float f = ex2(mv - v1);
-        l *= ex2(m - m1);
+        for (int u = 0; u < U; ++u) m1 = fmaxf(m1, y[u].x);
+        const float dm = m - m1;
+        float r1 = ref + dm;
+#pragma unroll
+        for (int u = 0; u < U; ++u) r1 = fmaxf(r1, y[u].z + (y[u].x - m1));
+        r1 = ceilf(r1);
+        const float f = ex2(dm + (ref - r1));
+        l *= ex2(dm);
         o.x *= f; o.y *= f; o.z *= f; o.w *= f;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float g = ex2(y[u].z - v1);
-            l = fmaf(y[u].y, ex2(y[u].x - m1), l);
+            const float du = y[u].x - m1, g = ex2(du + (y[u].z - r1));
+            l = fmaf(y[u].y, ex2(du), l);
             o.x = fmaf(g, z[u].x, o.x);
             o.y = fmaf(g, z[u].y, o.y);
             o.z = fmaf(g, z[u].z, o.z);
             o.w = fmaf(g, z[u].w, o.w);
         }
         m = m1;
-        mv = v1;
+        ref = r1;
     }
     s_o[tid] = o;
-    if (tid % LPR == 0) s_m[set] = make_float4(m, l, mv, 0.f);
+    if (tid % LPR == 0) s_m[set] = make_float4(m, l, ref, 0.f);
     __syncthreads();
     if (set != 0) return;
 #pragma unroll
-    for (int s = 1; s < SETS; ++s) {
-        m = fmaxf(m, s_m[s].x);
-        mv = fmaxf(mv, s_m[s].z);
-    }
+    for (int s = 1; s < SETS; ++s) m = fmaxf(m, s_m[s].x);
+    ref = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) ref = fmaxf(ref, s_m[s].z + (s_m[s].x - m));
+    ref = ceilf(ref);
     l = 0.f;
     o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int s = 0; s < SETS; ++s) {
         const float4 y = s_m[s], z = s_o[s * LPR + tid];
-        const float g = ex2(y.z - mv);
-        l = fmaf(y.y, ex2(y.x - m), l);
+        const float dm = y.x - m, g = ex2(dm + (y.z - ref));
+        l = fmaf(y.y, ex2(dm), l);
         o.x = fmaf(g, z.x, o.x);
         o.y = fmaf(g, z.y, o.y);
         o.z = fmaf(g, z.z, o.z);
         o.w = fmaf(g, z.w, o.w);
     }
-    store_row<T>(p, (size_t)b * p.Hq + h * p.G + r0 + row, D, col, m, l, mv, o);
+    store_row<T>(p, (size_t)b * p.Hq + h * p.G + r0 + row, D, col, m, l, ref, o);
 }
 
 template <int D, int NT, bool SPLIT>

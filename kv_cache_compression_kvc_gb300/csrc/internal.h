@@ -430,7 +430,7 @@ struct DecodeQ8Params {
     int32_t *ws_first;           // by_tile: the block that a split row tile begins in, else the row tile that
                                  // is split at a block's end; -1 for none
     int32_t *ws_last;            // the block that a split row tile ends in
-    float *ws_ml;                // [blocks][2][RP] {m, l, maximum of the value weights, -}
+    float *ws_ml;                // [blocks][2][RP] {m, l, reference of the value weights, -}
     float *ws_o;                 // [blocks][2][RP][D]
     float *ws_wml, *ws_wo;       // the same of a warp's first part: [blocks][warps][RP]
     int32_t *dev_code;
