@@ -792,11 +792,9 @@ kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_tab
  * entry outside the pool KVC_DEV_BAD_BLOCK and reads page 0.  What a page holds behind the length is
  * never used, whatever it is.
  * fp32 accumulation and softmax statistics.  fp32 queries enter the products as two fp16 terms (2^-22
- * of each row's largest element).  Weights (a probability times the scale of its page) enter them as
- * one fp16 number with bf16 queries, off by 2^-11 of it, eight times finer than the rounding of out,
- * and as two with fp32 queries, off by 2^-22; beside that by 2^-23 of the largest weight of its own 16
- * slots (32 with d_head 64), or by 2^-30 of one that is 2^8 times larger and lies among the 256 slots
- * (512) before them.
+ * of each row's largest element), and so do the weights (a probability times the scale of its page):
+ * off by 2^-22 of each, and by 2^-23 of the largest of its own 16 slots (32 with d_head 64) or 2^-30 of
+ * one that is 2^8 times larger and lies among the 256 slots (512) before them.
  * A thread's sums are fp32 and cut, not rounded: 2^-23 of the sum for each 16 slots in a row, a few in
  * rows that many warps share, a thousand or two where every warp walks 16000 slots.  Logits may have any
  * finite size.  Any group size.  Results do not depend on timing.  One kernel or two.  Workspace:

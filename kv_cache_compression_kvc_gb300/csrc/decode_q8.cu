@@ -18,8 +18,10 @@
 //   the products as they are stored; a fragment's 16 bytes of one row are 4 steps of the
 //   product's inner dimension, which may be dealt out in any order as long as Q is dealt out alike.
 //   Queries are brought to [2^14, 2^15) by a power of two per row: bf16 then is exact in fp16 down to
-//   2^-31 of the row's largest element.  fp32 queries become two fp16 terms (22 bits), and so do their
-//   weights; with bf16 queries, whose outputs are rounded to 8 bits, weights are rounded once to 11.
+//   2^-31 of the row's largest element.  fp32 queries become two fp16 terms (22 bits), and so do the
+//   weights, whatever the queries: bf16 outputs then are those of fp32 weights but for one in some thousands, while
+//   weights of 11 bits would turn the rounding of one in fifty (relative difference 6e-4 for 512 rows of 832
+//   slots, 7e-5 with two terms; 24.6 and 25.3 us, groups of 12 4 to 6 % more, long rows of few heads nothing).
 //   Weights carry the value scale: w_j = 2^(x_j - m + log2 vs(j) - ref), with the softmax's running maximum m, whose
 //   sum l is kept beside it, and a whole number ref of its own that follows the weights up and down: pages whose
 //   values differ by any factor meet on equal terms, and the light weights behind a heavy one, fp16 in the products,
@@ -355,7 +357,6 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
     constexpr int VB = D == 64 ? 8 : 16;     // bytes of a value row that a lane takes at once
     constexpr int VC = D == 256 ? 2 : 1;     // how often
     constexpr int S = PL::STAGES, W = PL::WARPS, SUB = PL::SUB, STEP = PL::STEP;
-    constexpr bool TWO = SPLIT;              // weights of two terms
     constexpr int SCALES = 2 * STEP * D;     // where a stage keeps its scales; 16 bytes on, what it holds
     extern __shared__ __align__(128) unsigned char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
         }
 #pragma unroll
         for (int sub = 0; sub < SUB; ++sub) {
-            uint32_t pw[NT][2], pl[TWO ? NT : 1][2];
+            uint32_t pw[NT][2], pl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float y[4];
@@ -758,10 +759,8 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t hi = pack_h2(y[2 * i], y[2 * i + 1]);
                     pw[nt][i] = transpose_8x8(hi);
-                    if constexpr (TWO) {
-                        const float2 z = unpack_h2(hi);
-                        pl[nt][i] = transpose_8x8(pack_h2(y[2 * i] - z.x, y[2 * i + 1] - z.y));
-                    }
+                    const float2 z = unpack_h2(hi);
+                    pl[nt][i] = transpose_8x8(pack_h2(y[2 * i] - z.x, y[2 * i + 1] - z.y));
                 }
             }
             // ---- O^T += V^T P^T: slots 2t, 2t + 1, 2t + 8, 2t + 9 of VB dims ----
@@ -794,7 +793,7 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             mma_16816(o[vc * 8 + q * 2 + u][nt], a, pw[nt][0], pw[nt][1]);
-                            if constexpr (TWO) mma_16816(o[vc * 8 + q * 2 + u][nt], a, pl[nt][0], pl[nt][1]);
+                            mma_16816(o[vc * 8 + q * 2 + u][nt], a, pl[nt][0], pl[nt][1]);
                         }
                     }
             }

@@ -212,3 +212,25 @@ def test_warps_of_a_thousand_steps(kvc, dt, D, G):
         tol = rel * size + step(dt) * want.abs() * (1 + rel)
         err = (out[i::8].double() - want).abs()
         assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 3), (128, 12), (256, 2)])
+@pytest.mark.parametrize("X", [0.3, 1.9, 4.4])
+def test_sums_that_cancel(kvc, dt, D, G, X):
+    """One heavy slot whose value is the negative of what the others add up to: what is left shows the weights' own
+    rounding, as two terms, whatever the queries' and outputs' type."""
+    n, bs = 1008, 16
+    k, v = torch.zeros((1, 1, n, D), device=DEV), torch.ones((1, 1, n, D), device=DEV)
+    k[:, :, 0], v[:, :, 0], v[:, :, 1:bs] = 1.0, -1.0, 0.0
+    one = torch.ones((1, 1, n // bs), device=DEV)
+    vs = one.clone()
+    vs[..., 0] = (n - bs) * math.exp(-X)
+    c = Cache(kvc, k, v, one, vs, bs)
+    scale = float(torch.tensor(X / D, dtype=torch.float32))
+    out, _ = decode(kvc, c, torch.ones((1, G, D), dtype=dt, device=DEV), scale)
+    want, _, _, size = attention(torch.ones((G, D), dtype=torch.float64, device=DEV), c.k[0, 0], c.v[0, 0], scale)
+    assert bool((want.abs() <= 2.0 ** -20 * size).all())
+    # as in tails(), where every product of 16 slots has weights of one size or two
+    tol = (X * 2.0 ** -22 + 2.0 ** -21 + 2.0 ** -22 + cut_sums(n, 1) * 2.0 ** -23) * size
+    assert bool(((out[0].double() - want).abs() <= tol * (1 + step(dt))).all()), float(((out[0].double() - want).abs() / tol).max())
