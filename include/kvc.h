@@ -834,9 +834,10 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
  * free).
  * All or nothing for the whole call, which leaves everything as it was when it records
  * KVC_DEV_BAD_INDEX (parent outside [-1, batch)), KVC_DEV_BAD_LENGTH (len, n_blocks of any
- * sequence), KVC_DEV_BAD_BLOCK (an id outside the pool, or a page listed by more sequences than
- * shares counts), KVC_DEV_SHARED_PAGE, KVC_DEV_POOL_EMPTY (too few free pages, or a top outside
- * [0, capacity]) or KVC_DEV_POOL_OVERFLOW (more free pages than the stack's capacity).  batch <= 8192.
+ * sequence), KVC_DEV_BAD_BLOCK (an id outside the pool, a page listed more often than shares counts,
+ * by sequences that stay as they are too, or a count below 0), KVC_DEV_SHARED_PAGE,
+ * KVC_DEV_POOL_EMPTY (too few free pages, or a top outside [0, capacity]) or KVC_DEV_POOL_OVERFLOW
+ * (more free pages than the stack's capacity).  batch <= 8192.
  *
  * kvc_pages_compact: the live pages (those not on the free stack) move to the lowest ids 0 ..
  * n_live - 1, so that the rest of the pool can be cut off or used otherwise: the k-th live page with

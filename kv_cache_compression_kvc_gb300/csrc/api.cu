@@ -1794,7 +1794,7 @@ static size_t pages_layout(int B, int mb, int nb, size_t *ids, size_t *copies, s
     const size_t entries = (size_t)B * mb;
     *ids = 256;
     *copies = *ids + align256((size_t)nb * sizeof(int32_t));
-    *table = *copies + align256((size_t)std::max(B, nb / 2) * sizeof(int4));
+    *table = *copies + align256((size_t)std::max(B, (nb + 1) / 2) * sizeof(int4));     // (or two counts a page)
     *score = *table + align256(entries * sizeof(int32_t));
     return *score + align256(entries * sizeof(float));
 }

@@ -461,7 +461,7 @@ struct PagesParams {
     int32_t *remap;              // compaction: [n_pool]
     int32_t *ws_n;               // copies, error, the blocks' counts
     int32_t *ws_ids;             // [n_pool]: freed pages, or free pages below the number of live ones
-    int4 *ws_copies;             // {from, to, rows, -}: reorder [B], compaction [n_pool / 2]
+    int4 *ws_copies;             // {from, to, rows, -}: reorder [B] (before them two counts a page), compaction [n_pool / 2]
     int32_t *ws_table;           // reorder: [B][max_blocks]
     float *ws_score;
     int32_t fused;               // the copies follow in the same kernel

@@ -7,7 +7,8 @@
 //
 // pages_reorder_kernel: sequence b becomes a copy of what sequence parent[b] was, or is freed.  A
 // page that s sequences held is held afterwards by the sum of their children: every table entry adds
-// (children - 1) to its page's count, and a page that ends at -1 is free.  A partly filled page stays
+// (children - 1) to its page's count, and a page that ends at -1 is free.  All entries are counted, those of
+// sequences that stay too: a page listed more often than its count says would be freed under a holder that goes on.  A partly filled page stays
 // with the sequence itself or its first child; the other children get a page of their own, copied by
 // pages_copy_kernel.  Free pages go on the stack in ascending order, copies take theirs from its top in
 // sequence order: results do not depend on timing.
@@ -18,7 +19,7 @@
 // The tables' kernels are a cluster of 8 blocks with a few barriers (a launch per step would cost more than the
 // steps); what blocks tell each other goes through the workspace.  Bound by latency: every step is a trip or two
 // to memory.  Reorders whose tables and counts fit the shared memory of one block need two trips and no barrier
-// of the cluster (pages_reorder_one_kernel: 128 sequences of 26 pages with 20 MB of copies 18.1 -> 13.0 us).
+// of the cluster (pages_reorder_one_kernel: 128 sequences of 26 pages with 20 MB of copies 17.2 -> 14.1 us).
 // For compaction each block keeps the free pages as bits in shared memory and works out by itself where
 // everything goes, which left one barrier of the cluster of six (16384 pages, tables and copies: 111 -> 105 us).
 // The copies are bound by HBM: a page's keys or values of a head are one run, which a warp copies with 128
@@ -42,8 +43,8 @@ constexpr int kCopyThreads_ = 256, kCopyBlocks = 8;      // of the copies: threa
 // device, but a call from Python, which the host bounds, 24 and 27.
 constexpr long long kFusedBytes = 1 << 18;
 // Reorders that one block takes: bytes of shared memory, runs of 32 table entries.  Device times by one block and by
-// the cluster: 4 runs 5.2 and 11.1 us, 128 runs 13.1 and 18.1, 256 runs 11.5 and 15.4, 512 runs 18.9 to 20.2 and
-// 18.0 to 18.6, 1024 runs 27.9 and 22.4; 4 runs and a pool of 32000 pages 10.2 and 12.1.
+// the cluster: 4 runs 5.8 and 10.0 us, 128 runs 14.1 and 17.2, 256 runs 13.1 and 14.5, 512 runs 21.7 to 22.0 and
+// 17.4, 1024 runs 33.0 and 21.0; 4 runs and a pool of 32000 pages 10.3 and 12.5.
 constexpr int kOneBytes = 200 * 1024, kOneRuns = 256;
 constexpr int kBadIndex = 3, kBadLength = 5, kBadBlock = 9, kPoolEmpty = 10, kPoolOverflow = 11, kSharedPage = 12;
 
@@ -155,6 +156,10 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
         p.ws_n[0] = 0;                       // copies
         p.ws_n[1] = 0;                       // what is wrong
     }
+    // of every page: how often the tables list it, and how many holders more (or less) it is to have
+    int32_t *lists = reinterpret_cast<int32_t *>(p.ws_copies), *more = lists + p.n_pool;
+    const int x0 = (int)((long long)p.n_pool * rank / kCl), x1 = (int)((long long)p.n_pool * (rank + 1) / kCl);
+    for (int x = x0 + tid; x < x1; x += kThreads) lists[x] = more[x] = 0;
     for (int b = tid; b < p.B; b += kThreads) {
         const int par = p.parent[b], len = p.len[b], nb = p.n_blocks[b];
         if (par < -1 || par >= p.B) code = kBadIndex;
@@ -166,7 +171,7 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
         s_len[b] = len;
     }
     const bool bad = __syncthreads_or(code != 0);
-    cluster_barrier();                       // (ws_n is there; no block has left)
+    cluster_barrier();                       // (ws_n and the counts are there; no block has left)
     if (bad) {
         if (rank == 0 && code != 0) record_code(p.dev_code, code);
         return;
@@ -197,36 +202,27 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
     }
     __syncthreads();
     auto partial = [&](int b, int i) { return s_len[b] % p.bs != 0 && i == s_nb[b] - 1; };
-    // ---- the tables' ids, of the sequences that change ----
-    auto touched = [&](int b) { return s_kids[b] == 1 && s_par[b] == b ? 0 : s_nb[b]; };
-    each_entry<kCl>(p.B, p.max_blocks, rank, touched, [&](int b, int i) {
-        const int id = p.table[(size_t)b * p.max_blocks + i];
-        int c = 0;
-        if (id < 0 || id >= p.n_pool) c = kBadBlock;
-        else if (partial(b, i) && p.shares[id] != 0) c = kSharedPage;
-        if (c != 0) atomicCAS(&p.ws_n[1], 0, c);
+    // ---- the tables' ids, and what the call makes of their holders ----
+    each_entry<kCl>(p.B, p.max_blocks, rank, [&](int b) { return s_nb[b]; }, [&](int b, int i) {
+        const int id = p.table[(size_t)b * p.max_blocks + i], kids = s_kids[b];
+        if (id < 0 || id >= p.n_pool) {
+            atomicCAS(&p.ws_n[1], 0, kBadBlock);
+            return;
+        }
+        atomicAdd(&lists[id], 1);
+        if (partial(b, i)) {
+            if (p.shares[id] != 0 && !(kids == 1 && s_par[b] == b)) atomicCAS(&p.ws_n[1], 0, kSharedPage);
+            if (kids == 0) atomicAdd(&more[id], -1);
+        } else if (kids != 1) {
+            atomicAdd(&more[id], kids - 1);
+        }
     });
     cluster_barrier();
-    code = __ldcg(&p.ws_n[1]);
-    if (code != 0) {                         // nothing has changed yet
-        if (rank == 0 && tid == 0) record_code(p.dev_code, code);
-        return;
-    }
-    // ---- holders of every page ----
-    auto count = [&](int sign) {
-        each_entry<kCl>(p.B, p.max_blocks, rank, [&](int b) { return s_kids[b] == 1 ? 0 : s_nb[b]; }, [&](int b, int i) {
-            if (s_kids[b] > 0 && partial(b, i)) return;
-            atomicAdd(&p.shares[p.table[(size_t)b * p.max_blocks + i]], sign * (s_kids[b] - 1));
-        });
-    };
-    count(1);
-    cluster_barrier();
-    const int x0 = (int)((long long)p.n_pool * rank / kCl), x1 = (int)((long long)p.n_pool * (rank + 1) / kCl);
     int gone = 0;
     for (int x = x0 + tid; x < x1; x += kThreads) {
-        const int s = __ldcg(&p.shares[x]);
-        gone += s < 0 ? 1 : 0;
-        if (s < -1) atomicCAS(&p.ws_n[1], 0, kBadBlock);       // held by more sequences than it counted
+        const int s = p.shares[x];
+        gone += s + __ldcg(&more[x]) < 0 ? 1 : 0;
+        if (s < 0 || __ldcg(&lists[x]) - 1 > s) atomicCAS(&p.ws_n[1], 0, kBadBlock);   // listed more often than counted
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) gone += __shfl_xor_sync(0xffffffffu, gone, o);
@@ -256,19 +252,19 @@ __global__ void __cluster_dims__(kCl, 1, 1) __launch_bounds__(kThreads) pages_re
             const int id = p.free_ids[i];
             if (id < 0 || id >= p.n_pool) code = kBadBlock;
         }
-    if (__syncthreads_or(code != 0)) {       // (the same in every block) counts as they were
+    if (__syncthreads_or(code != 0)) {       // (the same in every block) nothing has changed
         if (rank == 0 && code != 0) record_code(p.dev_code, code);
-        count(-1);
         return;
     }
     // ---- freed pages in ascending order; the tables as the children will have them ----
     for (int c = x0; c < x1; c += kThreads) {
         const int x = c + tid;
-        const bool free_now = x < x1 && __ldcg(&p.shares[x]) < 0;
+        const int s = x < x1 ? p.shares[x] : 0, add = x < x1 ? __ldcg(&more[x]) : 0;
+        const bool free_now = s + add < 0;
         int all;
         const int r = before + block_rank(free_now, s_warp, &all);
+        if (add != 0) p.shares[x] = max(s + add, 0);
         if (free_now) {
-            p.shares[x] = 0;
             p.ws_ids[r] = x;
             if (top + r < new_top) p.free_ids[top + r] = x;
         }
@@ -354,6 +350,8 @@ __global__ void __launch_bounds__(kThreads) pages_reorder_one_kernel(const Pages
         s_len[b] = len;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    for (int x = tid; x < p.n_pool; x += kThreads)             // (what this thread copied)
+        if (s_count[x] < 0) code = kBadBlock;
     if (__syncthreads_or(code != 0)) {
         if (code != 0) record_code(p.dev_code, code);
         return;
@@ -390,23 +388,26 @@ __global__ void __launch_bounds__(kThreads) pages_reorder_one_kernel(const Pages
             if (id >= 0 && id < p.n_pool && s_count[id] != 0) code = kSharedPage;
         }
     __syncthreads();
-    // ---- holders of every page ----
-    each_entry<1>(p.B, p.max_blocks, 0, [&](int b) { return stays(b) ? 0 : s_nb[b]; }, [&](int b, int i) {
-        const int id = s_table[b * p.max_blocks + i], more = s_kids[b] - 1;
+    // ---- holders of every page: no more listings than counted ones, then what the call makes of them ----
+    each_entry<1>(p.B, p.max_blocks, 0, [&](int b) { return s_nb[b]; }, [&](int b, int i) {
+        const int id = s_table[b * p.max_blocks + i];
         if (id < 0 || id >= p.n_pool) code = kBadBlock;
-        else if (more != 0 && !(more > 0 && partial(b, i))) atomicAdd(&s_count[id], more);
+        else if (atomicSub(&s_count[id], 1) < 0) code = kBadBlock;
     });
     if (__syncthreads_or(code != 0)) {
         if (code != 0) record_code(p.dev_code, code);
         return;
     }
+    each_entry<1>(p.B, p.max_blocks, 0, [&](int b) { return s_kids[b] > 0 ? s_nb[b] : 0; }, [&](int b, int i) {
+        atomicAdd(&s_count[s_table[b * p.max_blocks + i]], partial(b, i) ? 1 : s_kids[b]);
+    });
+    __syncthreads();
     // a warp looks at `per` runs of 32 pages
     const int per = (p.n_pool + kThreads - 1) / kThreads, x0 = warp * per * 32 + lane;
     int gone = 0;
     for (int r = 0, x = x0; r < per; ++r, x += 32) {
         const int s = x < p.n_pool ? s_count[x] : 0;
         gone += __popc(__ballot_sync(0xffffffffu, s < 0));
-        if (s < -1) code = kBadBlock;        // held by more sequences than it counted
     }
     if (lane == 0) s_warp[warp] = gone;
     asm volatile("cp.async.wait_all;" ::: "memory");
