@@ -442,6 +442,19 @@ kvc_status kvc_block_accumulate_evict(const float *logits, int64_t logits_stride
                                       int32_t budget_blocks, int32_t recent_blocks,
                                       int32_t *released, void *stream);
 
+/* The same over pages that several sequences may hold (kvc_pages_reorder): shares is its device
+ * int32[n_blocks], n_blocks the pool's pages.  A released page whose count is above 0 loses one
+ * holder and stays with the others; only one that nobody holds any more goes on the free stack,
+ * where several leave it in one call once.  A released id outside the pool records
+ * KVC_DEV_BAD_BLOCK and leaves the sequence's table as it was (released: -1). */
+kvc_status kvc_block_accumulate_evict_shared(const float *logits, int64_t logits_stride,
+                                             const float *lse, int32_t n_heads_q,
+                                             int32_t block_size, const kvc_page_table *pt,
+                                             const kvc_free_pool *free_pool, int32_t *shares,
+                                             int32_t n_blocks, int32_t budget_blocks,
+                                             int32_t recent_blocks, int32_t *released,
+                                             void *stream);
+
 /* KV bytes under DuoAttention, host: the memory formula of kvc_kv_bytes with seq_len tokens
  * per retrieval head and min(n_sink + window + 1, seq_len) per streaming head.  With 30 % of
  * the heads retrieving at 128k tokens the saving over kvc_kv_bytes is 70 % ([KVC] DuoAttention:
@@ -747,8 +760,8 @@ kvc_status kvc_qk_norm_rope(const kvc_qk_rows *rows, const void *w_q, const void
  * head, for keys and for values: an element stands for its number times the scale of its page.
  * pages.dtype is KVC_E4M3, pages.block_size a multiple of 16 up to 1024; k_scale and v_scale:
  * device fp32[n_heads_kv][n_blocks], positive and at most 2^126.  Page tables and free pools are
- * those of the other paged caches, and kvc_block_accumulate_evict serves these pages too; the other
- * calls over kvc_block_pool refuse KVC_E4M3. */
+ * those of the other paged caches, and kvc_block_accumulate_evict and its _shared form serve these
+ * pages too; the other calls over kvc_block_pool refuse KVC_E4M3. */
 typedef struct {
     kvc_block_pool pages;
     float *k_scale;
@@ -813,11 +826,11 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
 /* Pages held by several sequences (no counterpart on the pages).  Full pages are never written again,
  * so sequences that begin alike may list the same ones.  shares: device int32[n_blocks], the
  * sequences that hold a page beyond the first (0 for a page that one sequence holds and for a free
- * one); zero-filled before the first call, then kept by the two calls below.  A partly filled page
- * belongs to one sequence.  The calls that append (kvc_paged_append, kvc_paged_append_q8,
- * kvc_tree_accept_paged, kvc_block_prompt_select) and those that read work on such sequences as
- * they are.  kvc_block_accumulate_evict knows nothing of shares: give it only sequences whose pages
- * are their own.
+ * one); zero-filled before the first call, then kept by the two calls below and by
+ * kvc_block_accumulate_evict_shared.  A partly filled page belongs to one sequence.  The calls that
+ * append (kvc_paged_append, kvc_paged_append_q8, kvc_tree_accept_paged, kvc_block_prompt_select) and
+ * those that read work on such sequences as they are.  kvc_block_accumulate_evict knows nothing of
+ * shares: it would free pages that others hold.
  * pool: kvc_block_pool of KVC_F32 or KVC_BF16 with k_scale = v_scale = NULL, or the pages of a
  * kvc_block_pool_q8 with its scales.  pos (nullable): device int32[n_blocks][block_size], the
  * positions that kvc_paged_append keeps; they go along with their page.  One page table and one

@@ -718,11 +718,12 @@ kvc_status kvc_block_prompt_select(const float *s, int64_t s_stride, const kvc_c
     return ok();
 }
 
-kvc_status kvc_block_accumulate_evict(const float *logits, int64_t logits_stride,
-                                      const float *lse, int32_t n_heads_q, int32_t block_size,
-                                      const kvc_page_table *pt, const kvc_free_pool *free_pool,
-                                      int32_t budget_blocks, int32_t recent_blocks,
-                                      int32_t *released, void *stream)
+// shares: nullptr, or int32[n_pool].
+static kvc_status block_evict(const float *logits, int64_t logits_stride, const float *lse,
+                              int32_t n_heads_q, int32_t block_size, const kvc_page_table *pt,
+                              const kvc_free_pool *free_pool, int32_t *shares, int32_t n_pool,
+                              int32_t budget_blocks, int32_t recent_blocks, int32_t *released,
+                              void *stream)
 {
     if (pt == nullptr || pt->table == nullptr || pt->n_blocks == nullptr || pt->len == nullptr ||
         pt->score == nullptr || logits == nullptr || lse == nullptr)
@@ -749,11 +750,39 @@ kvc_status kvc_block_accumulate_evict(const float *logits, int64_t logits_stride
     p.free_ids = free_pool->ids; p.free_top = free_pool->top; p.free_cap = free_pool->capacity;
     p.logits = logits; p.logits_stride = logits_stride; p.lse = lse; p.Hq = n_heads_q;
     p.budget_blocks = budget_blocks; p.recent_blocks = recent_blocks; p.released = released;
-    p.n_pool = 0x7fffffff;
+    p.n_pool = n_pool; p.shares = shares;
     p.dev_code = code;
     cudaError_t e = kvc::launch_block_accumulate_evict(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "block accumulate/evict launch");
     return ok();
+}
+
+kvc_status kvc_block_accumulate_evict(const float *logits, int64_t logits_stride,
+                                      const float *lse, int32_t n_heads_q, int32_t block_size,
+                                      const kvc_page_table *pt, const kvc_free_pool *free_pool,
+                                      int32_t budget_blocks, int32_t recent_blocks,
+                                      int32_t *released, void *stream)
+{
+    return block_evict(logits, logits_stride, lse, n_heads_q, block_size, pt, free_pool, nullptr,
+                       0x7fffffff, budget_blocks, recent_blocks, released, stream);
+}
+
+kvc_status kvc_block_accumulate_evict_shared(const float *logits, int64_t logits_stride,
+                                             const float *lse, int32_t n_heads_q,
+                                             int32_t block_size, const kvc_page_table *pt,
+                                             const kvc_free_pool *free_pool, int32_t *shares,
+                                             int32_t n_blocks, int32_t budget_blocks,
+                                             int32_t recent_blocks, int32_t *released,
+                                             void *stream)
+{
+    if (shares == nullptr)
+        return fail(KVC_ERR_INVALID_ARG, "kvc_block_accumulate_evict_shared: null shares");
+    if (reinterpret_cast<uintptr_t>(shares) & 3u)
+        return fail(KVC_ERR_ALIGN, "kvc_block_accumulate_evict_shared: shares must be 4-byte aligned");
+    if (n_blocks <= 0)
+        return fail(KVC_ERR_SHAPE, "kvc_block_accumulate_evict_shared: n_blocks %d", n_blocks);
+    return block_evict(logits, logits_stride, lse, n_heads_q, block_size, pt, free_pool, shares,
+                       n_blocks, budget_blocks, recent_blocks, released, stream);
 }
 
 kvc_status kvc_alibi_slopes(int32_t n_heads, float *out)

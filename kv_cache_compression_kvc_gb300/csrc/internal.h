@@ -235,6 +235,7 @@ struct PagedParams {
     const float *lse;            // [B*Hq]
     int32_t Hq, budget_blocks, recent_blocks;
     int32_t *released;           // nullable [B]
+    int32_t *shares;             // nullable [n_pool]: holders of a page beyond the first
     int32_t *dev_code;
 };
 cudaError_t launch_paged_append(const PagedParams &p, int elem_bytes, cudaStream_t stream);

@@ -195,12 +195,13 @@ __global__ void __launch_bounds__(32) block_release_kernel(const PagedParams p)
             bi = oi;
         }
     }
-    if (lane == 0 && p.released != nullptr) p.released[b] = bi;
-    if (bi < 0) {
-        if (lane == 0) record_code(p.dev_code, kDevNoCandidate);
+    const int phys = bi >= 0 ? row_tab[bi] : -1;
+    const bool bad = bi >= 0 && p.shares != nullptr && (phys < 0 || phys >= p.n_pool);
+    if (lane == 0 && p.released != nullptr) p.released[b] = bad ? -1 : bi;
+    if (bi < 0 || bad) {
+        if (lane == 0) record_code(p.dev_code, bad ? kDevBadBlock : kDevNoCandidate);
         return;
     }
-    const int phys = row_tab[bi];
     // the entries after the victim move down one place, 32 at a time in ascending order (a
     // chunk's reads lie above every index an earlier chunk wrote)
     for (int c = bi; c < nb - 1; c += 32) {
@@ -221,6 +222,11 @@ __global__ void __launch_bounds__(32) block_release_kernel(const PagedParams p)
     if (lane == 0) {
         p.n_blocks[b] = nb - 1;
         p.len[b] = n - p.bs;
+        // a page that others hold loses a holder; of those that leave it in the same call, the last one frees it
+        if (p.shares != nullptr) {
+            if (atomicSub(&p.shares[phys], 1) > 0) return;
+            atomicAdd(&p.shares[phys], 1);
+        }
         const int slot = atomicAdd(p.free_top, 1);
         if (slot < 0 || slot >= p.free_cap) {
             atomicSub(p.free_top, 1);

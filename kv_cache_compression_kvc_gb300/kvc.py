@@ -160,6 +160,8 @@ SIGNATURES = {
                                        _I32, _P, _SZ, _P]),
     "kvc_block_accumulate_evict": (_I32, [_P, _I64, _P, _I32, _I32, _PT_P, _FREE_P, _I32, _I32,
                                           _P, _P]),
+    "kvc_block_accumulate_evict_shared": (_I32, [_P, _I64, _P, _I32, _I32, _PT_P, _FREE_P, _P, _I32,
+                                                 _I32, _I32, _P, _P]),
     "kvc_decode_attn_noalloc": (_I32, [_P, _I32, _CACHE_P, _P, _I32, _ROPE_P, _F32, _P, _P,
                                        _I64, _P, _P]),
     "kvc_h2o_accumulate_evict": (_I32, [_P, _I64, _P, _P, _P, _I64, _P, _I32, _I32, _I32, _P,
@@ -516,9 +518,17 @@ def kvc_block_prompt_select(s: torch.Tensor, k_prompt: torch.Tensor, v_prompt: t
 def kvc_block_accumulate_evict(logits: torch.Tensor, lse: torch.Tensor, pt: kvc_page_table,
                                free_pool: kvc_free_pool, *, block_size: int, budget_blocks: int,
                                recent_blocks: int, released: Optional[torch.Tensor] = None,
-                               stream=None) -> None:
-    """logits [B, Hq, >= max_blocks*block_size], lse [B, Hq]."""
+                               shares: Optional[torch.Tensor] = None, stream=None) -> None:
+    """logits [B, Hq, >= max_blocks*block_size], lse [B, Hq].  shares int32 [n_blocks], needed where
+    sequences hold pages together (kvc_pages_reorder): a page goes on the free stack with its last holder."""
     B, Hq = lse.shape
+    if shares is not None:
+        _need(shares, "shares", torch.int32, (shares.numel(),), logits.get_device())
+        _check(load().kvc_block_accumulate_evict_shared(
+            _ptr(logits), logits.stride(-2), _ptr(lse), Hq, int(block_size), ctypes.byref(pt),
+            ctypes.byref(free_pool), _ptr(shares), shares.numel(), int(budget_blocks), int(recent_blocks),
+            _ptr(released), _stream(stream)))
+        return
     _check(load().kvc_block_accumulate_evict(
         _ptr(logits), logits.stride(-2), _ptr(lse), Hq, int(block_size), ctypes.byref(pt),
         ctypes.byref(free_pool), int(budget_blocks), int(recent_blocks), _ptr(released),
