@@ -1194,6 +1194,10 @@ def kvc_paged_append_q8(pool: kvc_block_pool_q8, pt: kvc_page_table, free_pool: 
     code = _dtype_code(k_new.dtype)
     kp, st, sh = _rows_of(k_new, "k_new", k_new.dtype, n, D, index)
     vp, vt, vh = _rows_of(v_new, "v_new", k_new.dtype, n, D, index)
+    if n <= 1:                               # (the stride of a single row or head means nothing)
+        st = vt = 0
+    if H == 1:
+        sh = vh = 0
     if v_new.shape[1] != H or (vt, vh) != (st, sh):
         raise ValueError("v_new must have the shape and the strides of k_new")
     if cu is None and n != B:
