@@ -834,7 +834,7 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
  * pool: kvc_block_pool of KVC_F32 or KVC_BF16 with k_scale = v_scale = NULL, or the pages of a
  * kvc_block_pool_q8 with its scales.  pos (nullable): device int32[n_blocks][block_size], the
  * positions that kvc_paged_append keeps; they go along with their page.  One page table and one
- * free pool a pool, as everywhere.
+ * free pool a pool, as everywhere.  A page's keys of one head take less than 2^31 - 2^16 bytes.
  *
  * kvc_pages_reorder: every sequence b becomes a copy of what sequence parent[b] was before the call,
  * or is freed (parent[b] = -1: n_blocks = len = 0); parent[b] = b leaves it alone.  Forking a

@@ -1852,6 +1852,8 @@ static kvc_status pages_call(const kvc_block_pool *pool, float *ks, float *vs, c
         return fail(KVC_ERR_ALIGN, "%s: shares, pos, parent and remap must be 4-byte aligned", name);
     if (reorder && pt->batch > kvc::kPagesMaxBatch)
         return fail(KVC_ERR_SHAPE, "%s: batch %d > %d", name, pt->batch, kvc::kPagesMaxBatch);
+    if ((long long)pool->block_size * pool->d_head * (pool->dtype == KVC_E4M3 ? 1 : elem_bytes(pool->dtype)) > 0x7fff0000LL)
+        return fail(KVC_ERR_SHAPE, "%s: pages of 2^31 bytes a head", name);   // (a warp copies one, in 32 bits)
     if (!reorder && pool->n_blocks > kvc::kPagesMaxPool)
         return fail(KVC_ERR_SHAPE, "%s: n_blocks %d > %d", name, pool->n_blocks, kvc::kPagesMaxPool);
     st = check_ws(ws, ws_bytes, kvc_pages_workspace_bytes(pt->batch, pt->max_blocks, pool->n_blocks), name);
