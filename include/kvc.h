@@ -581,17 +581,17 @@ kvc_status kvc_h2o_prefill_select_gqa(const void *q, int32_t n_heads_q, const kv
  * are accepted: no slot and no page is taken by a draft that is then rejected.  Served are
  * caches filled from slot 0 (KVC_APPEND_TAIL, compacted or selected prompts), paged caches and latent
  * caches; not the sink + ring layouts with positions inside the cache, nor DuoAttention's two
- * caches, and acceptance fills neither ring nor freed slots.  No counterpart on the pages (they decode one token at a time); the attention is
- * that of kvc_decode_attn for every drafted token.
+ * caches, and acceptance fills neither ring nor freed slots.  No counterpart on the pages (they decode
+ * one token at a time); the attention is that of kvc_decode_attn for every drafted token.
  * k, v: device [batch][n_draft][n_heads_kv][d_head], cache dtype, contiguous, 16-byte aligned
  * (for a latent cache k is [batch][n_draft][d_latent + d_rope] and v is not read).  k == NULL:
  * the query tokens see the cache only (their keys were appended already).
  * mask: device uint64[batch][n_draft]; bit j of word i set: token i sees token j.  Bits at or
  * above the sequence's token count are ignored.  NULL: a chain, token i sees tokens 0..i.
  * count (nullable): device int32[batch], drafted tokens of each sequence, 0..n_draft (a value
- * outside records KVC_DEV_BAD_LENGTH and is clamped, by the accept calls too).  Outputs of tokens at or beyond it are
- * left as they were, and their keys and values are not used (nor need they be finite).  NULL:
- * n_draft each. */
+ * outside records KVC_DEV_BAD_LENGTH and is clamped, by the accept calls too).  Outputs of tokens at
+ * or beyond it are left as they were, and their keys and values are not used (nor need they be
+ * finite).  NULL: n_draft each. */
 typedef struct {
     const void *k;
     const void *v;
@@ -786,8 +786,8 @@ typedef struct {
  * (KVC_DEV_BAD_BLOCK; bad ids leave the stack), too few free pages (KVC_DEV_POOL_EMPTY).  Offsets cu
  * that do not ascend within 0..n_tokens append nothing at all (KVC_DEV_BAD_LENGTH).
  * appended (nullable): device int32[batch], the rows appended to each sequence.
- * Two kernels.  Workspace: kvc_paged_append_q8_workspace_bytes(), 256-byte aligned; it need not be
- * cleared, and calls that share one must not overlap on the GPU. */
+ * One kernel for small steps, else two.  Workspace: kvc_paged_append_q8_workspace_bytes(), 256-byte
+ * aligned; it need not be cleared, and calls that share one must not overlap on the GPU. */
 size_t kvc_paged_append_q8_workspace_bytes(int32_t batch, int32_t n_tokens, int32_t block_size);
 kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_table *pt,
                                const kvc_free_pool *free_pool, const void *k_new,
@@ -806,13 +806,13 @@ kvc_status kvc_paged_append_q8(const kvc_block_pool_q8 *pool, const kvc_page_tab
  * never used, whatever it is.
  * fp32 accumulation and softmax statistics.  fp32 queries enter the products as two fp16 terms (2^-22
  * of each row's largest element), and so do the weights (a probability times the scale of its page):
- * off by 2^-22 of each, and by 2^-23 of the largest of its own 16 slots (32 with d_head 64) or 2^-30 of
- * one that is 2^8 times larger and lies among the 256 slots (512) before them.
- * A thread's sums are fp32 and cut, not rounded: 2^-23 of the sum for each 16 slots in a row, a few in
- * rows that many warps share, a thousand or two where every warp walks 16000 slots.  Logits may have any
- * finite size.  Any group size.  Results do not depend on timing.  One kernel or two.  Workspace:
- * kvc_decode_attn_paged_q8_workspace_bytes(), 256-byte aligned; it need not be cleared, and calls
- * that share one must not overlap on the GPU. */
+ * off by 2^-22 of each, and by 2^-23 of the largest of its own 16 slots (32 with d_head 64), 2^-30 of
+ * one that is 2^8 times larger and lies among the 256 slots (512) before them, or 2^-90 of the row's
+ * largest.  A warp's sums are fp32 and cut, not rounded: by 2^-23 twice for each 16 slots that it
+ * walks, a few in rows that many warps share, 2000 times where every warp walks 16000 slots.  Logits
+ * may have any size up to 2.3e38.  Any group size.  Results do not depend on timing.  One kernel or
+ * two.  Workspace: kvc_decode_attn_paged_q8_workspace_bytes(), 256-byte aligned; it need not be
+ * cleared, and calls that share one must not overlap on the GPU. */
 size_t kvc_decode_attn_paged_q8_workspace_bytes(int32_t batch, int32_t n_heads_q,
                                                 int32_t n_heads_kv, int32_t d_head,
                                                 int32_t dtype);
@@ -862,8 +862,9 @@ kvc_status kvc_decode_attn_paged_q8(const void *q, int32_t dtype, int32_t n_head
  * outside the table (KVC_DEV_BAD_LENGTH) or a top outside the stack (KVC_DEV_POOL_EMPTY): nothing
  * is moved and remap is not written.  n_blocks <= 2^20.
  *
- * Each is one kernel, or two where many bytes may be copied.  Workspace of both: kvc_pages_workspace_bytes(), 256-byte aligned; it need not
- * be cleared, and calls that share one must not overlap on the GPU. */
+ * Each is one kernel, or two where many bytes may be copied.  Workspace of both:
+ * kvc_pages_workspace_bytes(), 256-byte aligned; it need not be cleared, and calls that share one must
+ * not overlap on the GPU. */
 size_t kvc_pages_workspace_bytes(int32_t batch, int32_t max_blocks, int32_t n_blocks);
 kvc_status kvc_pages_reorder(const kvc_block_pool *pool, float *k_scale, float *v_scale,
                              const kvc_page_table *pt, const kvc_free_pool *free_pool,

@@ -506,12 +506,13 @@ cudaError_t append_typed(const AppendQ8Params &p, int n_sm, cudaStream_t stream)
                           stream, p);
     };
     if (p.cu == nullptr) return rows(append_q8_rows_kernel<T, D, 1, 1>, 1, 1);
-    // A lane holds NV vectors, 64 bytes of rows in fp32 and 128 in bf16, which leaves 24 warps an SM, and as many warps share
+    // A lane holds NV vectors, 128 bytes of rows of either type, which leaves 24 warps an SM, and as many warps share
     // a page as that takes.  Measured (us), 16 prompts of 2048 to 4096 rows of 32 heads of 128, bf16, pages of 32:
     // one warp with 2 NV 201, two with NV 194, four with NV / 2 211; 41 x 1000 to 2000 rows of 4 heads of 256 in pages
     // of 32: one warp in two passes 110, four with 2 NV 114, four with NV 69, eight with NV / 2 78; 20 x the same in
     // pages of 64: one warp 61, four with 2 NV 42, eight with NV 39; 40 x 1000 rows of 8 heads of 128 in pages of
-    // 16: one warp with 2 NV 80, with NV 50; of 16 heads of 64: one warp with 2 NV 127, NV 71, NV / 2 55.
+    // 16: one warp with 2 NV 80, with NV 50; of 16 heads of 64: one warp with 2 NV 127, NV 71, NV / 2 55 (their bytes
+    // at the copy rate: 36; the plan, 7 us or more in which no row is read, is the largest part of the rest).
     constexpr int NV = 16 / (int)sizeof(T);
     const int page = p.bs * D / 256;         // vectors a lane of one warp
     if constexpr (NV == 8)                   // (the smallest fp32 page takes more)

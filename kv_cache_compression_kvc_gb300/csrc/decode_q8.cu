@@ -33,10 +33,10 @@
 // shared memory at its end, those of several blocks by decode_q8_merge_kernel, both in order of
 // the slots, so results do not depend on timing.
 //
-// Measured: 2 x 131072 slots of 8 heads of 128, 4 query heads each (537 MB) 94.5 us, 5.7 TB/s.  Copies
+// Measured: 2 x 131072 slots of 8 heads of 128, 4 query heads each (537 MB) 94.7 us, 5.7 TB/s.  Copies
 // alone in this pattern take 78 us.  3 us pass until the first copies leave (lengths, page ids, cold
 // instructions), 3 us after the last (parts), and equal shares take some SMs 61 us and others 85: whole
-// groups of neighbours are slower.  More blocks than fit at once, so that the fast ones take more, 115 us;
+// groups of neighbours are slower.  Variants, when the weights had one term and this took 92.5: more blocks than fit at once, so that the fast ones take more, 115 us;
 // four blocks of 4 warps an SM 111; 6 warps a block with four stages 94.7; one block of 8 warps with six
 // stages 99.5; two products side by side with 128 dims 93.4; one warp that finds the block's range
 // for all 95.2; L2 prefetch hints no change.  Parts joined per warp instead of per block: 110.
@@ -53,22 +53,24 @@ namespace kvc {
 namespace {
 
 constexpr int kSub = 16;                     // slots of one product; a step is one or two of them
-constexpr int kEnd = 2;                      // steps that the end of a row tile counts as (0: 34.5 us for the ragged
-                                             // fp32 batch of the table, 1: 33.5, 2 and 4: 32.7)
+constexpr int kEnd = 2;                      // steps that the end of a row tile counts as (0: 35.3 us for 8 fp32
+                                             // sequences of 3277 to 13107 slots, 1: 34.3, 2: 33.7, 4: 33.3)
 // Warps of a block: what registers allow (one block an SM with 16 heads or fp32 queries, two otherwise).  fp32
-// queries over 2 x 32768 slots of 8 heads of 128: 8 warps 34.5 us, 10 34.3, 12 31.5.
+// queries over 2 x 32768 slots of 8 heads of 128: 8 warps 36.1 us, 10 35.9, 12 32.1.
 constexpr int warps_of(int D, int NT, bool split)
 {
     return D > 128 || (NT == 2 && split) || (NT == 1 && !split) ? 8 : 12;
 }
 constexpr int kMergeThreads = 256;
-constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block
+constexpr int kWholeSteps = 16;              // row tiles of so many steps stay in one block, however many there are (2000 x
+                                             // 100 to 256 slots of 8 heads: 149 us, split 161; 250 to 256: 192 and 214)
 constexpr int kWholeWait = 20;               // and longer ones where the fullest block has so many above the mean
-constexpr int kMinUnits = 16;                // units that a block is worth at least
+constexpr int kMinUnits = 16;                // units that a block is worth at least (1 x 1000 slots of 8 heads of 128:
+                                             // 8 9.1 us, 16 10.1, 32 12.0)
 constexpr float kSlack = 8.f;                // a maximum or reference moves when it is passed by 2^8 either way
 constexpr float kBoost = 6.f;                // weights are held times 2^6: at most 2^15, and the largest of a step
-                                             // that lies low but moves nothing, 2^-2, is 22 bits above the last place.
-                                             // (Slack 4 and boost 10: groups of 12 2 % slower)
+                                             // that lies low but moves nothing, 2^-2, is 22 bits above the last place
+                                             // (slack 4 and boost 10: groups of 12 2 % slower)
 constexpr int kLook = 16;                    // a reference may go down every so many steps (8: groups of 12, fp32, 43.3 us,
                                              // 16 42.8; a vote on it in every step 50.6)
 constexpr int kTop = 100;                    // and as far as the sums stay below 2^101
@@ -77,7 +79,7 @@ constexpr int kDevBadLen_ = 5;
 constexpr int kDevBadBlk_ = 9;
 
 // Products of 16 slots that a step takes side by side: with 64 dims one alone is half bookkeeping (8 x 16384
-// slots of 4 heads of 64: one 21.9 us, two 21.2; fp32 queries 24.9 and 23.3).
+// slots of 4 heads of 64, 4 query heads each: one 23.9 us, two 22.6; fp32 queries 26.1 and 24.0).
 constexpr int subs_of(int D) { return D == 64 ? 2 : 1; }
 
 template <int D, int NT, bool SPLIT>
@@ -993,9 +995,9 @@ cudaError_t launch_typed(DecodeQ8Params p, cudaStream_t stream)
 }  // namespace
 
 // Row tiles of 8 heads, of 16 where a group has more and that pays.  fp32 queries of 128 dims, tiles of 8 and of 16:
-// 28 x 3963 to 6241 slots of 3 heads, groups of 12 47.0 and 41.1 us, 2 x 32768 of 8 heads, groups of 9 51.6 and 44.4, but
-// groups of 24, which are three tiles or two, 36.8 and 37.8.  No gain with 64 dims (groups of 16 31.0 and 30.9 to 35.8),
-// nor with bf16 queries of 256 (groups of 12 59.0 and 61.1).
+// 28 x 3963 to 6241 slots of 3 heads, groups of 12 47.0 and 42.6 us, 2 x 32768 of 8 heads, groups of 9 51.3 and 46.1, but
+// groups of 24, which are three tiles or two, 36.7 and 39.5.  No gain with 64 dims (groups of 16 32.4 and 32.1), nor with
+// bf16 queries of 256 (groups of 12 61.5 and 67.2).
 static int tiles_of_8(int G, int D, bool bf16)
 {
     if (bf16) return G > 8 && D <= 128 ? 2 : 1;
@@ -1030,7 +1032,8 @@ cudaError_t launch_decode_q8(DecodeQ8Params p, int D, bool bf16, cudaStream_t st
     // Row tiles stay in one block each, and no second kernel is needed, where that leaves the fullest block
     // little more than the mean: by the capacity (which the host knows), and with few steps a block, since the
     // lengths behind it may differ.  Measured with 52 steps of 128 dims, whole and split: 512 row tiles on 304
-    // blocks (16 steps above the mean) 24.4 and 26.7 us.
+    // blocks (16 steps above the mean) 25.4 and 27.6 us.  Lengths well below the capacity lose by it: 400 to 832 slots
+    // 24.4 and 23.3 us, 100 to 832 24.1 and 20.9, 1 to 832 23.9 and 19.7.
     const int step = kSub * subs_of(D);
     const long long tiles = (long long)p.B * p.HR, steps = (p.cap + step - 1) / step;
     const long long fullest = (tiles + p.blocks - 1) / p.blocks * steps;
