@@ -36,10 +36,10 @@
 // Measured: 2 x 131072 slots of 8 heads of 128, 4 query heads each (537 MB) 94.7 us, 5.7 TB/s.  Copies
 // alone in this pattern take 78 us.  3 us pass until the first copies leave (lengths, page ids, cold
 // instructions), 3 us after the last (parts), and equal shares take some SMs 61 us and others 85: whole
-// groups of neighbours are slower.  Variants, when the weights had one term and this took 92.5: more blocks than fit at once, so that the fast ones take more, 115 us;
-// four blocks of 4 warps an SM 111; 6 warps a block with four stages 94.7; one block of 8 warps with six
-// stages 99.5; two products side by side with 128 dims 93.4; one warp that finds the block's range
-// for all 95.2; L2 prefetch hints no change.  Parts joined per warp instead of per block: 110.
+// groups of neighbours are slower.  Variants, when the weights had one term and this took 92.5: more blocks than fit
+// at once, so that the fast ones take more, 115 us; four blocks of 4 warps an SM 111; 6 warps a block with four
+// stages 94.7; one block of 8 warps with six stages 99.5; two products side by side with 128 dims 93.4; one warp that
+// finds the block's range for all 95.2; L2 prefetch hints no change; parts joined per warp instead of per block 110.
 #include <algorithm>
 #include <type_traits>
 
@@ -733,7 +733,8 @@ __global__ void __launch_bounds__(Q8Plan<D, NT, SPLIT>::WARPS * 32, Q8Plan<D, NT
                         // as far as the sums stay in their range, and not for -inf alone
                         const int room = kTop + 127 - (int)(__float_as_uint(row_max(big)) >> 23);
                         float r1 = ref[nt][r];
-                        if (want < r1 - kSlack && want > -INFINITY) r1 = ceilf(fmaxf(want, r1 - (float)max(0, min(126, room))));
+                        if (want < r1 - kSlack && want > -INFINITY)
+                            r1 = ceilf(fmaxf(want, r1 - (float)max(0, min(126, room))));
                         const float f = ex2(ref[nt][r] - r1);
 #pragma unroll
                         for (int d = 0; d < DT; ++d) {

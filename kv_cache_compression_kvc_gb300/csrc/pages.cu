@@ -7,11 +7,11 @@
 //
 // pages_reorder_kernel: sequence b becomes a copy of what sequence parent[b] was, or is freed.  A
 // page that s sequences held is held afterwards by the sum of their children: every table entry adds
-// (children - 1) to its page's count, and a page that ends at -1 is free.  All entries are counted, those of
-// sequences that stay too: a page listed more often than its count says would be freed under a holder that goes on.  A partly filled page stays
-// with the sequence itself or its first child; the other children get a page of their own, copied by
-// pages_copy_kernel.  Free pages go on the stack in ascending order, copies take theirs from its top in
-// sequence order: results do not depend on timing.
+// (children - 1) to its page's count, and a page that ends at -1 is free.  All entries are counted, those
+// of sequences that stay too: a page listed more often than its count says would be freed under a holder
+// that goes on.  A partly filled page stays with the sequence itself or its first child; the other
+// children get a page of their own, copied by pages_copy_kernel.  Free pages go on the stack in ascending
+// order, copies take theirs from its top in sequence order: results do not depend on timing.
 //
 // pages_compact_kernel: the k-th live page beyond the number of live pages moves to the k-th free page
 // below it; tables, counts and the stack follow.  No page is both read and written.
